@@ -37,6 +37,11 @@ FFT_REAL_F64 = 3
 FFT_CONV_COMPLEX = 0
 FFT_CONV_REAL = 1
 
+FFT_ELEM_F32 = 0
+FFT_ELEM_F64 = 1
+FFT_ELEM_BF16 = 2
+FFT_ELEM_F16 = 3
+
 FFT_OPT_PASS_LOG = 1
 FFT_OPT_PASS_SPLIT = 2
 FFT_OPT_NO_TMA = 3
@@ -49,6 +54,17 @@ FFT_OPT_PASS_SHFL = 9
 
 # Every symbol the header declares, with its ctypes signature.
 _VP, _I64, _INT, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+_DBL = ctypes.c_double
+
+
+class DeltaDesc(ctypes.Structure):
+    """fft_delta_desc: sizes, strides (sequence, token, head; in elements),
+    scale and type of a call of the gated delta rule."""
+    _fields_ = ([(n, ctypes.c_int64) for n in ("batch", "tokens", "kheads", "vheads", "dk", "dv")]
+                + [(n + "_stride", ctypes.c_int64 * 3) for n in ("q", "k", "v", "g", "beta")]
+                + [("scale", ctypes.c_double), ("dtype", ctypes.c_int)])
+
+
 SIGNATURES = {
     "fft_plan_create": (_VP, [_I64, _I64, _INT, _INT, _INT]),
     "fft_plan_create_nd": (_VP, [_INT, _VP, _I64, _INT, _INT]),
@@ -67,6 +83,15 @@ SIGNATURES = {
     "fft_convolve_num_kernels": (_INT, [_I64, _I64, _I64, _INT, _INT, _INT]),
     "fft_convolve_host": (_INT, [_VP, _I64, _VP, _I64, _VP, _I64, _INT, _INT, _INT, _VP, _VP,
                                  _I64, _VP]),
+    "fft_layer_norm": (_INT, [_VP, _I64, _VP, _VP, _VP, _I64, _VP, _VP, _I64, _I64, _DBL, _INT,
+                              _INT, _VP]),
+    "fft_layer_norm_workspace_bytes": (_SZ, [_I64, _I64, _INT]),
+    "fft_layer_norm_backward": (_INT, [_VP, _I64, _VP, _I64, _VP, _VP, _VP, _VP, _I64, _VP, _VP,
+                                       _I64, _I64, _INT, _INT, _VP, _SZ, _VP]),
+    "fft_grad_norm_workspace_bytes": (_SZ, [_I64]),
+    "fft_grad_norm": (_INT, [_I64, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "fft_clip_grad_norm": (_INT, [_I64, _VP, _VP, _VP, _VP, _DBL, _DBL, _VP, _VP, _SZ, _VP]),
+    "fft_delta_rule_step": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _VP]),
     "fft_debug_radix2_pass": (_INT, [_VP, _VP, _I64, _I64, _INT, _VP]),
     "fft_device_status": (_INT, [_VP]),
     "fft_debug_wait_timeout": (_INT, [_I64, _VP]),
@@ -198,6 +223,46 @@ def fft_convolve_host(x_host: int, nx: int, h_ptr: int, nh: int, y_host: int, ba
 def fft_convolve_num_kernels(nx: int, nh: int, batch: int, h_per_row: int, kind: int,
                              dtype: int) -> int:
     return int(_lib.fft_convolve_num_kernels(nx, nh, batch, h_per_row, kind, dtype))
+
+
+def fft_layer_norm(x: int, ldx: int, w: int, b: int, y: int, ldy: int, mean: int, rstd: int,
+                   rows: int, dim: int, eps: float, dtype: int, wtype: int, stream: int) -> int:
+    return _lib.fft_layer_norm(x, ldx, w, b, y, ldy, mean, rstd, rows, dim, eps, dtype, wtype,
+                               stream)
+
+
+def fft_layer_norm_workspace_bytes(rows: int, dim: int, dtype: int) -> int:
+    return int(_lib.fft_layer_norm_workspace_bytes(rows, dim, dtype))
+
+
+def fft_layer_norm_backward(dy: int, lddy: int, x: int, ldx: int, w: int, mean: int, rstd: int,
+                            dx: int, lddx: int, dw: int, db: int, rows: int, dim: int, dtype: int,
+                            wtype: int, workspace: int, workspace_bytes: int, stream: int) -> int:
+    return _lib.fft_layer_norm_backward(dy, lddy, x, ldx, w, mean, rstd, dx, lddx, dw, db, rows,
+                                        dim, dtype, wtype, workspace, workspace_bytes, stream)
+
+
+def fft_grad_norm_workspace_bytes(count: int) -> int:
+    return int(_lib.fft_grad_norm_workspace_bytes(count))
+
+
+def fft_grad_norm(count: int, ins, numels, dtypes, norm: int, workspace: int,
+                  workspace_bytes: int, stream: int) -> int:
+    """ins, numels, dtypes: ctypes arrays of `count` pointers, int64, int."""
+    return _lib.fft_grad_norm(count, ins, numels, dtypes, norm, workspace, workspace_bytes, stream)
+
+
+def fft_clip_grad_norm(count: int, ins, outs, numels, dtypes, max_norm: float, eps: float,
+                       norm: int, workspace: int, workspace_bytes: int, stream: int) -> int:
+    """ins, outs, numels, dtypes: ctypes arrays of `count` entries."""
+    return _lib.fft_clip_grad_norm(count, ins, outs, numels, dtypes, max_norm, eps, norm,
+                                   workspace, workspace_bytes, stream)
+
+
+def fft_delta_rule_step(desc: DeltaDesc, q: int, k: int, v: int, g: int, beta: int, state: int,
+                        slots: int, pool: int, o: int, stream: int) -> int:
+    return _lib.fft_delta_rule_step(ctypes.byref(desc), q, k, v, g, beta, state, slots, pool, o,
+                                    stream)
 
 
 def fft_debug_radix2_pass(in_ptr: int, out_ptr: int, n: int, half: int, dtype: int,
@@ -484,3 +549,17 @@ def fftn(x, ndim: int, direction: int = FFT_FORWARD, out=None, stream=None):
         if stream is None:
             _torch().cuda.current_stream().synchronize()
         p.close()
+
+
+# ---- operators of sequence models (tensor helpers in sequence.py) ---------------
+
+_SEQUENCE = ("layer_norm", "layer_norm_backward", "grad_norm", "clip_grad_norm", "delta_rule_step")
+
+
+def __getattr__(name):
+    # Loaded on first use: the module imports torch, this package does not.
+    if name in _SEQUENCE:
+        from . import sequence
+        globals().update({n: getattr(sequence, n) for n in _SEQUENCE})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,461 @@
+// layer_norm.cuh -- layer normalisation of rows, forward and backward.
+//
+//   forward   mu = mean(x), r = (mean((x - mu)^2) + eps)^-1/2,
+//             y = (x - mu) r w + b
+//   backward  xh = (x - mu) r, d = dy w,
+//             dx = r (d - mean(d) - xh mean(d xh)),
+//             dw = sum over rows of dy xh, db = sum over rows of dy
+//
+// Both directions read and write every row once, so HBM bounds them.  A row
+// stays in the registers of the TPR threads that share it (EPT elements
+// each): the variance is taken about the mean in a second pass over
+// registers, not from a difference of two large sums.  Blocks are persistent
+// and walk the rows; a thread keeps the same columns throughout, so w and b
+// are read once per block, and the sums of dw and db over the block's rows
+// stay in registers: one row of partial sums per block goes to HBM, and a
+// second kernel adds those in a fixed order (no atomics, so the result does
+// not depend on timing).  All sums are fp32 (fp64 rows: fp64).
+#pragma once
+
+#include "seq.h"
+
+namespace fftgb {
+
+// Sum over the TPR threads that share a row, returned to all of them.  `red`
+// holds two sets of TPR / 32 values per row group and is used alternately,
+// which saves the barrier between reading one sum and writing the next.
+template <int TPR, typename A>
+__device__ __forceinline__ A row_sum(A v, A *red, int &turn) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (TPR > 32) {
+    constexpr int W = TPR / 32;
+    A *r = red + turn * W;
+    if ((threadIdx.x & 31) == 0) r[(threadIdx.x % TPR) >> 5] = v;
+    __syncthreads();
+    v = r[threadIdx.x & (W - 1)];
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    turn ^= 1;
+  }
+  return v;
+}
+
+// Both sums of the backward pass in one round.
+template <int TPR>
+__device__ __forceinline__ float2 row_sum2(float a, float b, float2 *red, int &turn) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if constexpr (TPR > 32) {
+    constexpr int W = TPR / 32;
+    float2 *r = red + turn * W;
+    if ((threadIdx.x & 31) == 0) r[(threadIdx.x % TPR) >> 5] = make_float2(a, b);
+    __syncthreads();
+    const float2 t = r[threadIdx.x & (W - 1)];
+    a = t.x;
+    b = t.y;
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    turn ^= 1;
+  }
+  return make_float2(a, b);
+}
+
+// Column of a thread's element e: 16-byte vectors (VEC), or single elements
+// at a stride of TPR where the rows are not 16-byte aligned.
+template <typename T, int TPR, bool VEC>
+__device__ __forceinline__ int column(int t, int e) {
+  constexpr int N = Vec16<T>::N;
+  if constexpr (VEC) return ((e / N) * TPR + t) * N + e % N;
+  return e * TPR + t;
+}
+
+template <typename T, int TPR, int EPT, bool VEC>
+struct RowRegs {
+  static constexpr int N = Vec16<T>::N;
+  T v[EPT];
+  __device__ __forceinline__ void load(const T *row, int t, int dim) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int k = 0; k < EPT / N; ++k) {
+        const int c = (k * TPR + t) * N;
+        Vec16<T> x{};
+        if (c < dim) {
+          const uint4 raw = __ldcs(reinterpret_cast<const uint4 *>(row + c));
+          x = *reinterpret_cast<const Vec16<T> *>(&raw);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[k * N + i] = x.v[i];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < EPT; ++e) {
+        const int c = e * TPR + t;
+        v[e] = c < dim ? row[c] : from_acc<T>(0.0f);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T *row, int t, int dim) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int k = 0; k < EPT / N; ++k) {
+        const int c = (k * TPR + t) * N;
+        if (c < dim) {
+          Vec16<T> x;
+#pragma unroll
+          for (int i = 0; i < N; ++i) x.v[i] = v[k * N + i];
+          *reinterpret_cast<uint4 *>(row + c) = *reinterpret_cast<const uint4 *>(&x);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < EPT; ++e) {
+        const int c = e * TPR + t;
+        if (c < dim) row[c] = v[e];
+      }
+    }
+  }
+};
+
+constexpr int kNormThreads = 256;
+
+template <typename T, int TPR, int EPT, bool VEC>
+__global__ void __launch_bounds__(kNormThreads)
+layer_norm_kernel(const LayerNormArgs a) {
+  constexpr int G = kNormThreads / TPR;  // rows in flight per block
+  __shared__ float red[2 * 32];
+  const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  const T *x = static_cast<const T *>(a.x);
+  T *y = static_cast<T *>(a.y);
+  float w[EPT], b[EPT];
+#pragma unroll
+  for (int e = 0; e < EPT; ++e) {
+    const int c = column<T, TPR, VEC>(t, e);
+    w[e] = a.w && c < a.dim ? load_any(a.w, a.wtype, c) : 1.0f;
+    b[e] = a.b && c < a.dim ? load_any(a.b, a.wtype, c) : 0.0f;
+  }
+  const float inv = 1.0f / (float)a.dim;
+  int turn = 0;
+  const long long step = (long long)gridDim.x * G;
+  long long row = (long long)blockIdx.x * G + grp;
+  RowRegs<T, TPR, EPT, VEC> cur, next;
+  if (row < a.rows) cur.load(x + row * a.ldx, t, a.dim);
+  // The row groups of a block share no barrier (a group of several warps is
+  // a whole block), so each may end its loop on its own.
+  for (; row < a.rows; row += step) {
+    if (row + step < a.rows) next.load(x + (row + step) * a.ldx, t, a.dim);
+    float f[EPT], s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) {
+      f[e] = to_acc(cur.v[e]);
+      s += f[e];  // columns beyond dim hold zeros
+    }
+    const float mu = row_sum<TPR>(s, red, turn) * inv;
+    s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) {
+      f[e] -= mu;
+      if (column<T, TPR, VEC>(t, e) < a.dim) s += f[e] * f[e];
+    }
+    const float r = 1.0f / sqrtf(row_sum<TPR>(s, red, turn) * inv + (float)a.eps);
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) cur.v[e] = from_acc<T>(f[e] * r * w[e] + b[e]);
+    cur.store(y + row * a.ldy, t, a.dim);
+    if (t == 0) {
+      if (a.mean) static_cast<float *>(a.mean)[row] = mu;
+      if (a.rstd) static_cast<float *>(a.rstd)[row] = r;
+    }
+    cur = next;
+  }
+}
+
+template <typename T, int TPR, int EPT, bool VEC>
+__global__ void __launch_bounds__(kNormThreads)
+layer_norm_grad_kernel(const LayerNormGradArgs a) {
+  constexpr int G = kNormThreads / TPR;
+  __shared__ float2 red[2 * 32];
+  const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
+  const float *mean = static_cast<const float *>(a.mean);
+  const float *rstd = static_cast<const float *>(a.rstd);
+  T *dx = static_cast<T *>(a.dx);
+  float w[EPT], dw[EPT], db[EPT];
+#pragma unroll
+  for (int e = 0; e < EPT; ++e) {
+    const int c = column<T, TPR, VEC>(t, e);
+    w[e] = a.w && c < a.dim ? load_any(a.w, a.wtype, c) : 1.0f;
+    dw[e] = db[e] = 0.0f;
+  }
+  const float inv = 1.0f / (float)a.dim;
+  int turn = 0;
+  const long long step = (long long)gridDim.x * G;
+  long long row = (long long)blockIdx.x * G + grp;
+  RowRegs<T, TPR, EPT, VEC> xc, dc, xn, dn;
+  float mu = 0.0f, r = 0.0f, mun = 0.0f, rn = 0.0f;
+  if (row < a.rows) {
+    xc.load(x + row * a.ldx, t, a.dim);
+    dc.load(dy + row * a.lddy, t, a.dim);
+    mu = mean[row];
+    r = rstd[row];
+  }
+  for (; row < a.rows; row += step) {
+    if (row + step < a.rows) {
+      xn.load(x + (row + step) * a.ldx, t, a.dim);
+      dn.load(dy + (row + step) * a.lddy, t, a.dim);
+      mun = mean[row + step];
+      rn = rstd[row + step];
+    }
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) {
+      if (column<T, TPR, VEC>(t, e) < a.dim) {
+        const float xh = (to_acc(xc.v[e]) - mu) * r, g = to_acc(dc.v[e]);
+        dw[e] += g * xh;
+        db[e] += g;
+        s1 += g * w[e];
+        s2 += g * w[e] * xh;
+      }
+    }
+    if (dx) {
+      const float2 s = row_sum2<TPR>(s1, s2, red, turn);
+      const float m1 = s.x * inv, m2 = s.y * inv;
+#pragma unroll
+      for (int e = 0; e < EPT; ++e) {
+        const float xh = (to_acc(xc.v[e]) - mu) * r;
+        xc.v[e] = from_acc<T>(r * (to_acc(dc.v[e]) * w[e] - m1 - xh * m2));
+      }
+      xc.store(dx + row * a.lddx, t, a.dim);
+    }
+    xc = xn;
+    dc = dn;
+    mu = mun;
+    r = rn;
+  }
+  if (!a.partial) return;
+  // One row of partial sums per row group: [2][gridDim.x * G][dim].
+  float *pw = static_cast<float *>(a.partial);
+  float *pb = pw + (long long)gridDim.x * G * a.dim;
+  const long long at = ((long long)blockIdx.x * G + grp) * a.dim;
+#pragma unroll
+  for (int e = 0; e < EPT; ++e) {
+    const int c = column<T, TPR, VEC>(t, e);
+    if (c < a.dim) {
+      pw[at + c] = dw[e];
+      pb[at + c] = db[e];
+    }
+  }
+}
+
+// Rows longer than a block's registers, and fp64: three walks over the row,
+// the second and third of them in the caches.
+template <typename T>
+__global__ void __launch_bounds__(1024) layer_norm_long_kernel(const LayerNormArgs a) {
+  using A = typename Acc<T>::type;
+  __shared__ A red[2 * 32];
+  int turn = 0;
+  const A inv = (A)1 / (A)a.dim;
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T *x = static_cast<const T *>(a.x) + row * a.ldx;
+    T *y = static_cast<T *>(a.y) + row * a.ldy;
+    A s = 0;
+    for (int c = threadIdx.x; c < a.dim; c += 1024) s += to_acc(x[c]);
+    const A mu = row_sum<1024>(s, red, turn) * inv;
+    s = 0;
+    for (int c = threadIdx.x; c < a.dim; c += 1024) {
+      const A f = to_acc(x[c]) - mu;
+      s += f * f;
+    }
+    const A r = (A)1 / sqrt(row_sum<1024>(s, red, turn) * inv + (A)a.eps);
+    for (int c = threadIdx.x; c < a.dim; c += 1024) {
+      A w = 1, b = 0;
+      if constexpr (sizeof(T) == 8) {
+        if (a.w) w = static_cast<const double *>(a.w)[c];
+        if (a.b) b = static_cast<const double *>(a.b)[c];
+      } else {
+        if (a.w) w = load_any(a.w, a.wtype, c);
+        if (a.b) b = load_any(a.b, a.wtype, c);
+      }
+      y[c] = from_acc<T>((to_acc(x[c]) - mu) * r * w + b);
+    }
+    if (threadIdx.x == 0) {
+      if (a.mean) static_cast<A *>(a.mean)[row] = mu;
+      if (a.rstd) static_cast<A *>(a.rstd)[row] = r;
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(1024) layer_norm_long_dx_kernel(const LayerNormGradArgs a) {
+  using A = typename Acc<T>::type;
+  __shared__ A red[2 * 32];
+  int turn = 0;
+  const A inv = (A)1 / (A)a.dim;
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T *x = static_cast<const T *>(a.x) + row * a.ldx;
+    const T *dy = static_cast<const T *>(a.dy) + row * a.lddy;
+    T *dx = static_cast<T *>(a.dx) + row * a.lddx;
+    const A mu = static_cast<const A *>(a.mean)[row], r = static_cast<const A *>(a.rstd)[row];
+    auto weight = [&](int c) -> A {
+      if (!a.w) return 1;
+      if constexpr (sizeof(T) == 8) return static_cast<const double *>(a.w)[c];
+      else return load_any(a.w, a.wtype, c);
+    };
+    A s1 = 0, s2 = 0;
+    for (int c = threadIdx.x; c < a.dim; c += 1024) {
+      const A d = to_acc(dy[c]) * weight(c);
+      s1 += d;
+      s2 += d * (to_acc(x[c]) - mu) * r;
+    }
+    const A m1 = row_sum<1024>(s1, red, turn) * inv, m2 = row_sum<1024>(s2, red, turn) * inv;
+    for (int c = threadIdx.x; c < a.dim; c += 1024) {
+      const A xh = (to_acc(x[c]) - mu) * r;
+      dx[c] = from_acc<T>(r * (to_acc(dy[c]) * weight(c) - m1 - xh * m2));
+    }
+  }
+}
+
+// Partial sums of dw and db over the rows blockIdx.y, + gridDim.y, ... of
+// 256 columns.
+template <typename T>
+__global__ void __launch_bounds__(256) layer_norm_long_dw_kernel(const LayerNormGradArgs a) {
+  using A = typename Acc<T>::type;
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= a.dim) return;
+  const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
+  A dw = 0, db = 0;
+  for (long long row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    const A g = to_acc(dy[row * a.lddy + c]);
+    dw += g * (to_acc(x[row * a.ldx + c]) - static_cast<const A *>(a.mean)[row]) *
+          static_cast<const A *>(a.rstd)[row];
+    db += g;
+  }
+  A *pw = static_cast<A *>(a.partial);
+  pw[(long long)blockIdx.y * a.dim + c] = dw;
+  pw[((long long)gridDim.y + blockIdx.y) * a.dim + c] = db;
+}
+
+// dw and db from `parts` rows of partial sums: 32 columns per block, 32
+// threads down each column, added in a fixed order.  blockIdx.y: dw or db.
+template <typename A>
+__global__ void __launch_bounds__(1024)
+layer_norm_sum_kernel(const A *partial, int parts, int dim, void *dw, void *db, int wtype) {
+  __shared__ A tile[32][33];
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  const A *p = partial + (long long)blockIdx.y * parts * dim;
+  A s = 0;
+  if (c < dim)
+    for (int k = threadIdx.y; k < parts; k += 32) s += p[(long long)k * dim + c];
+  tile[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  s = tile[threadIdx.x][threadIdx.y];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int col = blockIdx.x * 32 + threadIdx.y;
+  void *out = blockIdx.y == 0 ? dw : db;
+  if (threadIdx.x == 0 && col < dim && out) store_any(out, wtype, col, s);
+}
+
+// Threads per row and elements per thread by the row's length: warps for
+// rows up to 1024 elements (no barrier), blocks of 256 up to 8192;
+// longer rows and fp64 by the looping kernels.
+constexpr int kNormRegMax = 8192;
+inline int norm_blocks_per_sm(int dim) { return dim > 4096 ? 2 : 4; }
+
+template <typename T, class F>
+cudaError_t norm_dispatch(int dim, bool vec, F f) {
+#define FFTGB_NORM(TPR, EPT)                                      \
+  return vec ? f(std::integral_constant<int, TPR>(), std::integral_constant<int, EPT>(), \
+                 std::true_type())                                \
+             : f(std::integral_constant<int, TPR>(), std::integral_constant<int, EPT>(), \
+                 std::false_type())
+  if (dim <= 256) { FFTGB_NORM(32, 8); }
+  if (dim <= 512) { FFTGB_NORM(32, 16); }
+  if (dim <= 1024) { FFTGB_NORM(32, 32); }
+  if (dim <= 2048) { FFTGB_NORM(256, 8); }
+  if (dim <= 4096) { FFTGB_NORM(256, 16); }
+  FFTGB_NORM(256, 32);
+#undef FFTGB_NORM
+}
+
+inline int norm_groups(int dim) { return dim <= 1024 ? 8 : 1; }  // row groups per block
+
+// Blocks of the persistent kernels.
+inline long long norm_grid(long long rows, int dim) {
+  const long long blocks = (rows + norm_groups(dim) - 1) / norm_groups(dim);
+  const long long most = (long long)sm_count() * norm_blocks_per_sm(dim);
+  return blocks < most ? blocks : most;
+}
+
+template <typename T> bool norm_vec(const void *p, long long ld, int dim) {
+  return ((uintptr_t)p & 15u) == 0 && (ld * (long long)sizeof(T)) % 16 == 0 &&
+         dim % Vec16<T>::N == 0;
+}
+
+template <typename T>
+cudaError_t layer_norm_t(const LayerNormArgs &a, cudaStream_t st) {
+  if constexpr (sizeof(T) < 8) {
+    if (a.dim <= kNormRegMax) {
+      const bool vec = norm_vec<T>(a.x, a.ldx, a.dim) && norm_vec<T>(a.y, a.ldy, a.dim);
+      const int grid = (int)norm_grid(a.rows, a.dim);
+      return norm_dispatch<T>(a.dim, vec, [&](auto tpr, auto ept, auto v) {
+        layer_norm_kernel<T, tpr.value, ept.value, v.value>
+            <<<grid, kNormThreads, 0, st>>>(a);
+        return cudaGetLastError();
+      });
+    }
+  }
+  const long long most = 2LL * sm_count();
+  layer_norm_long_kernel<T><<<(int)(a.rows < most ? a.rows : most), 1024, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+constexpr int kLongParts = 64;  // row ranges of the looping kernel's dw
+
+template <typename T>
+cudaError_t layer_norm_grad_t(const LayerNormGradArgs &a, cudaStream_t st) {
+  using A = typename Acc<T>::type;
+  const int dtype = sizeof(T) == 8 ? FFT_ELEM_F64 : FFT_ELEM_F32;
+  const int parts = layer_norm_partials(dtype, a.rows, a.dim);
+  cudaError_t e = cudaSuccess;
+  bool done = false;
+  if constexpr (sizeof(T) < 8) {
+    if (a.dim <= kNormRegMax) {
+      const bool vec = norm_vec<T>(a.x, a.ldx, a.dim) && norm_vec<T>(a.dy, a.lddy, a.dim) &&
+                       (!a.dx || norm_vec<T>(a.dx, a.lddx, a.dim));
+      const int grid = (int)norm_grid(a.rows, a.dim);
+      e = norm_dispatch<T>(a.dim, vec, [&](auto tpr, auto ept, auto v) {
+        layer_norm_grad_kernel<T, tpr.value, ept.value, v.value>
+            <<<grid, kNormThreads, 0, st>>>(a);
+        return cudaGetLastError();
+      });
+      done = true;
+    }
+  }
+  if (!done) {
+    // dw first: dx may overwrite dy or x.
+    if (a.partial) {
+      const dim3 grid((a.dim + 255) / 256, parts);
+      layer_norm_long_dw_kernel<T><<<grid, 256, 0, st>>>(a);
+      e = cudaGetLastError();
+    }
+    if (e == cudaSuccess && a.dx) {
+      const long long most = 2LL * sm_count();
+      layer_norm_long_dx_kernel<T><<<(int)(a.rows < most ? a.rows : most), 1024, 0, st>>>(a);
+      e = cudaGetLastError();
+    }
+  }
+  if (e == cudaSuccess && a.partial) {
+    layer_norm_sum_kernel<A><<<dim3((a.dim + 31) / 32, 2), dim3(32, 32), 0, st>>>(
+        static_cast<const A *>(a.partial), parts, a.dim, a.dw, a.db, a.wtype);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+}  // namespace fftgb

@@ -1,0 +1,129 @@
+// seq.h -- declarations shared by the sequence-model operators (layer
+// normalisation, gradient clipping, the gated delta rule): element types,
+// conversions, and the kernel launchers behind the C ABI of seq_ops.cu.
+// Not installed.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+
+namespace fftgb {
+
+inline size_t elem_bytes(int dtype) {
+  return dtype == FFT_ELEM_F64 ? 8 : dtype == FFT_ELEM_F32 ? 4 : 2;
+}
+
+// Multiprocessors of the current device (0 if the query fails).
+int sm_count();
+
+// ---- layer normalisation (layer_norm_*.cu) -----------------------------------
+
+struct LayerNormArgs {
+  const void *x, *w, *b;  // w, b may be null (1 and 0)
+  void *y;
+  void *mean, *rstd;  // fp32 (fp64 rows: fp64); may be null
+  long long rows, ldx, ldy;
+  int dim;
+  double eps;
+  int wtype;
+};
+struct LayerNormGradArgs {
+  const void *dy, *x, *w, *mean, *rstd;  // w may be null
+  void *dx, *dw, *db;                    // each may be null
+  long long rows, lddy, ldx, lddx;
+  int dim;
+  int wtype;
+  void *partial;  // 2 x layer_norm_partials() x dim accumulators
+};
+// Rows of partial sums of the weight's gradient that the backward pass leaves.
+int layer_norm_partials(int dtype, long long rows, int dim);
+template <typename T> cudaError_t launch_layer_norm(const LayerNormArgs &a, cudaStream_t st);
+template <typename T> cudaError_t launch_layer_norm_grad(const LayerNormGradArgs &a,
+                                                         cudaStream_t st);
+
+// ---- gradient clipping (clip.cu) ---------------------------------------------
+
+size_t clip_workspace_bytes(long long count);
+cudaError_t launch_clip(long long count, const void *const *in, void *const *out,
+                        const int64_t *numel, const int *dtype, double max_norm, double eps,
+                        float *norm, void *workspace, cudaStream_t st);
+
+// ---- the gated delta rule (delta_*.cu) ------------------------------------------
+
+// Strides in elements: sequence (unused for packed rows), token, head.
+struct DeltaStride {
+  long long seq, tok, head;
+};
+struct DeltaArgs {
+  const void *q, *k, *v;
+  const float *g, *beta;
+  DeltaStride sq, sk, sv, sg, sb;
+  const int *offsets;     // packed rows: batch + 1 first rows; else null
+  const float *state_in;  // may be null (zero)
+  float *state_out;       // may be null
+  void *o;                // contiguous [sequence][token][head][dv]
+  long long batch, tokens;
+  int kheads, vheads, dk, dv;
+  float scale;
+  // Single tokens: the sequence's row of a pool of `pool` states (null: row = sequence).
+  const int *slots;
+  long long pool;
+};
+cudaError_t launch_delta_step(int dtype, const DeltaArgs &a, cudaStream_t st);
+
+// ---- element conversions -----------------------------------------------------
+
+#ifdef __CUDACC__
+__device__ __forceinline__ float to_acc(float v) { return v; }
+__device__ __forceinline__ double to_acc(double v) { return v; }
+__device__ __forceinline__ float to_acc(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_acc(__half v) { return __half2float(v); }
+template <typename T> __device__ __forceinline__ T from_acc(float v);
+template <> __device__ __forceinline__ float from_acc<float>(float v) { return v; }
+template <> __device__ __forceinline__ double from_acc<double>(float v) { return (double)v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_acc<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+template <> __device__ __forceinline__ __half from_acc<__half>(float v) {
+  return __float2half_rn(v);
+}
+template <typename T> __device__ __forceinline__ T from_acc(double v);
+template <> __device__ __forceinline__ double from_acc<double>(double v) { return v; }
+template <> __device__ __forceinline__ float from_acc<float>(double v) { return (float)v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_acc<__nv_bfloat16>(double v) {
+  return __double2bfloat16(v);
+}
+template <> __device__ __forceinline__ __half from_acc<__half>(double v) {
+  return __double2half(v);
+}
+
+// Accumulator type of an element type.
+template <typename T> struct Acc { using type = float; };
+template <> struct Acc<double> { using type = double; };
+
+// Element i of an array whose type is known at run time only (the branch is
+// the same for every thread).
+__device__ __forceinline__ float load_any(const void *p, int dtype, long long i) {
+  if (dtype == FFT_ELEM_F32) return static_cast<const float *>(p)[i];
+  if (dtype == FFT_ELEM_BF16) return to_acc(static_cast<const __nv_bfloat16 *>(p)[i]);
+  if (dtype == FFT_ELEM_F16) return to_acc(static_cast<const __half *>(p)[i]);
+  return (float)static_cast<const double *>(p)[i];
+}
+template <typename A>
+__device__ __forceinline__ void store_any(void *p, int dtype, long long i, A v) {
+  if (dtype == FFT_ELEM_F32) static_cast<float *>(p)[i] = from_acc<float>(v);
+  else if (dtype == FFT_ELEM_BF16) static_cast<__nv_bfloat16 *>(p)[i] = from_acc<__nv_bfloat16>(v);
+  else if (dtype == FFT_ELEM_F16) static_cast<__half *>(p)[i] = from_acc<__half>(v);
+  else static_cast<double *>(p)[i] = from_acc<double>(v);
+}
+
+// 16 bytes of elements.
+template <typename T> struct alignas(16) Vec16 {
+  static constexpr int N = 16 / sizeof(T);
+  T v[N];
+};
+#endif
+
+}  // namespace fftgb

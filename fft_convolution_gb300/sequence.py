@@ -1,0 +1,271 @@
+"""Tensor helpers of the sequence-model operators (``fft_layer_norm``,
+``fft_clip_grad_norm``, ``fft_delta_rule`` and their kin in
+``include/fft_gb300.h``): they check and marshal torch tensors, allocate
+outputs and workspaces, and call the library.  Every call is asynchronous on
+``stream`` (default: torch's current stream); what a call allocates belongs
+to that stream.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from . import (FFT_ELEM_BF16, FFT_ELEM_F16, FFT_ELEM_F32, FFT_ELEM_F64, DeltaDesc, _check, _lib)
+
+_ELEM = {torch.float32: FFT_ELEM_F32, torch.float64: FFT_ELEM_F64,
+         torch.bfloat16: FFT_ELEM_BF16, torch.float16: FFT_ELEM_F16}
+_NULL = contextlib.nullcontext()
+
+
+def _elem(t, what: str) -> int:
+    code = _ELEM.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what}: float32, float64, bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _on(stream):
+    """(context in which the call's allocations are made, stream handle)."""
+    if stream is None:
+        return _NULL, torch.cuda.current_stream().cuda_stream
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _device(first, *others):
+    """Every tensor given lies on one CUDA device."""
+    if not first.is_cuda:
+        raise ValueError("the operators take CUDA tensors")
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+def _workspace(nbytes: int, device):
+    return torch.empty(max(16, nbytes), dtype=torch.uint8, device=device)
+
+
+# ---- layer normalisation -----------------------------------------------------------
+
+def _rows(t):
+    """`t` as rows of its last axis, at one stride: a view where the strides
+    allow it, else a copy."""
+    if t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] == 1) and t.stride(0) >= t.shape[1]:
+        return t
+    t = t.reshape(-1, t.shape[-1])
+    if t.stride(1) != 1 and t.shape[1] != 1 or t.stride(0) < t.shape[1]:
+        t = t.contiguous()
+    return t
+
+
+def _vector(t, dim: int, what: str):
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != dim:
+        raise ValueError(f"{what} must hold {dim} elements")
+    return t.contiguous()
+
+
+def _row_stats(t, rows: int, dtype, what: str):
+    if t.numel() != rows or t.dtype != (torch.float64 if dtype == torch.float64 else torch.float32):
+        raise ValueError(f"{what} must hold one value per row, as layer_norm returned it")
+    return t.contiguous()
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None):
+    """(y, mean, rstd) of the rows along x's last axis (see fft_layer_norm):
+    y = (x - mean) rstd weight + bias.  weight and bias: vectors of x's type,
+    or float32 with 16-bit x.  mean and rstd (float32; float64 for float64
+    x) have x's shape without its last axis."""
+    dim = x.shape[-1]
+    if dim == 0:
+        raise ValueError("rows need at least one element")
+    _device(x, weight, bias, out)
+    code = _elem(x, "x")
+    w, b = _vector(weight, dim, "weight"), _vector(bias, dim, "bias")
+    if w is not None and b is not None and w.dtype != b.dtype:
+        raise TypeError("weight and bias need one type")
+    wcode = code if w is None and b is None else _elem(w if w is not None else b, "weight")
+    context, handle = _on(stream)
+    with context:
+        x2 = _rows(x)
+        rows = x2.shape[0]
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        elif out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous():
+            raise ValueError("out must be contiguous and like x")
+        stats = torch.empty((2,) + tuple(x.shape[:-1]), device=x.device,
+                            dtype=torch.float64 if code == FFT_ELEM_F64 else torch.float32)
+        mean, rstd = stats[0], stats[1]
+        _check(_lib.fft_layer_norm(x2.data_ptr(), max(dim, x2.stride(0)), _ptr(w), _ptr(b),
+                                   out.data_ptr(), dim, mean.data_ptr(), rstd.data_ptr(), rows, dim,
+                                   eps, code, wcode, handle), "fft_layer_norm")
+    return out, mean, rstd
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True, stream=None):
+    """(dx, dweight, dbias) from dy and layer_norm's x, weight, mean and rstd
+    (see fft_layer_norm_backward).  dweight is None without a weight; dbias
+    is None with bias=False.  dweight and dbias have the weight's type (x's
+    without a weight)."""
+    dim = x.shape[-1]
+    if dy.shape != x.shape or dy.dtype != x.dtype or dim == 0:
+        raise ValueError("dy must be like x")
+    _device(x, dy, weight, mean, rstd)
+    code = _elem(x, "x")
+    w = _vector(weight, dim, "weight")
+    wcode = code if w is None else _elem(w, "weight")
+    wtype = x.dtype if w is None else w.dtype
+    context, handle = _on(stream)
+    with context:
+        x2, dy2 = _rows(x), _rows(dy)
+        rows = x2.shape[0]
+        mean, rstd = (_row_stats(t, rows, x.dtype, n) for t, n in ((mean, "mean"), (rstd, "rstd")))
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dw = torch.empty(dim, dtype=wtype, device=x.device) if w is not None else None
+        db = torch.empty(dim, dtype=wtype, device=x.device) if bias else None
+        ws = None
+        nbytes = 0
+        if dw is not None or db is not None:
+            nbytes = _lib.fft_layer_norm_workspace_bytes(rows, dim, code)
+            ws = _workspace(nbytes, x.device)
+        _check(_lib.fft_layer_norm_backward(
+            dy2.data_ptr(), max(dim, dy2.stride(0)), x2.data_ptr(), max(dim, x2.stride(0)), _ptr(w),
+            mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dim, _ptr(dw), _ptr(db), rows, dim,
+            code, wcode, _ptr(ws), nbytes, handle), "fft_layer_norm_backward")
+    return dx, dw, db
+
+
+# ---- gradient clipping ---------------------------------------------------------------
+
+def _table(tensors, what: str):
+    """Host arrays of the tensors' pointers, sizes and types."""
+    n = len(tensors)
+    device = tensors[0].device
+    ptrs, numels, codes = [], [], []
+    for t in tensors:
+        if t.device != device or not t.is_cuda:
+            raise ValueError(f"{what}: CUDA tensors of one device")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: contiguous tensors")
+        ptrs.append(t.data_ptr())
+        numels.append(t.numel())
+        codes.append(_elem(t, what))
+    return ((ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*numels), (ctypes.c_int * n)(*codes))
+
+
+def grad_norm(grads, stream=None):
+    """The 2-norm over all elements of a sequence of contiguous CUDA tensors
+    (types may differ), as a float32 tensor without axes on their device."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grad_norm needs at least one tensor")
+    ptrs, numels, codes = _table(grads, "grads")
+    context, handle = _on(stream)
+    with context:
+        norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
+        nbytes = _lib.fft_grad_norm_workspace_bytes(len(grads))
+        ws = _workspace(nbytes, norm.device)
+        _check(_lib.fft_grad_norm(len(grads), ptrs, numels, codes, norm.data_ptr(), ws.data_ptr(),
+                                  nbytes, handle), "fft_grad_norm")
+    return norm
+
+
+def clip_grad_norm(grads, max_norm: float, out=None, eps: float = 1e-6, stream=None):
+    """Scales every tensor by min(1, max_norm / (norm + eps)), in place or
+    into the tensors of `out` (same shapes and types), and returns the norm
+    before the scaling (see grad_norm, fft_clip_grad_norm)."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("clip_grad_norm needs at least one tensor")
+    ptrs, numels, codes = _table(grads, "grads")
+    outs = ptrs
+    if out is not None:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError("out needs one tensor for each of grads")
+        outs, onumels, ocodes = _table(out, "out")
+        if out[0].device != grads[0].device or list(onumels) != list(numels) or \
+                list(ocodes) != list(codes):
+            raise ValueError("out must be like grads")
+    context, handle = _on(stream)
+    with context:
+        norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
+        nbytes = _lib.fft_grad_norm_workspace_bytes(len(grads))
+        ws = _workspace(nbytes, norm.device)
+        _check(_lib.fft_clip_grad_norm(len(grads), ptrs, outs, numels, codes, max_norm, eps,
+                                       norm.data_ptr(), ws.data_ptr(), nbytes, handle),
+               "fft_clip_grad_norm")
+    return norm
+
+
+# ---- the gated delta rule --------------------------------------------------------------
+
+def _dense(t):
+    return t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
+
+
+def _strides(t, packed: bool):
+    """(sequence, token, head) strides of [batch, tokens, heads, ...], or of
+    packed rows [rows, heads, ...]."""
+    s = t.stride()
+    return (0, s[0], s[1]) if packed else (s[0], s[1], s[2])
+
+
+def _delta_inputs(q, k, v, g, beta, scale, batch, packed: bool):
+    """Checks the five inputs; returns them (elements of a head contiguous)
+    and the descriptor."""
+    lead = 1 if packed else 2
+    if q.dim() != lead + 2 or v.dim() != lead + 2 or q.shape != k.shape or \
+            v.shape[:lead] != q.shape[:lead]:
+        raise ValueError("q, k: [batch, tokens, key heads, dk]; v: [batch, tokens, value heads, dv] "
+                         "(packed rows: without the batch axis)")
+    if g.shape != v.shape[:-1] or beta.shape != g.shape:
+        raise ValueError("g and beta hold one value per token and value head")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k and v need one type")
+    if g.dtype != torch.float32 or beta.dtype != torch.float32:
+        raise TypeError("g and beta are float32")
+    _device(q, k, v, g, beta)
+    q, k, v = _dense(q), _dense(k), _dense(v)
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    desc = DeltaDesc(batch, q.shape[0] if packed else q.shape[1], q.shape[-2], v.shape[-2],
+                     q.shape[-1], v.shape[-1])
+    for name, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta)):
+        setattr(desc, name + "_stride", _strides(t, packed))
+    desc.scale = scale
+    desc.dtype = _elem(q, "q")
+    return q, k, v, desc
+
+
+def delta_rule_step(q, k, v, g, beta, state, slots=None, scale=None, out=None, stream=None):
+    """One or a few tokens per sequence of the gated delta rule (see
+    fft_delta_rule_step): returns o [batch, tokens, value heads, dv] and
+    updates `state` (float32 [pool, value heads, dk, dv], contiguous) in
+    place.  slots: int32 [batch], the state of each sequence (negative: idle,
+    o is 0); by default sequence i has state i."""
+    context, handle = _on(stream)
+    with context:
+        q, k, v, desc = _delta_inputs(q, k, v, g, beta, scale, q.shape[0], False)
+        _device(q, state, slots, out)
+        if state.dtype != torch.float32 or not state.is_contiguous() or state.dim() != 4 or \
+                state.shape[1:] != (v.shape[2], q.shape[3], v.shape[3]):
+            raise ValueError("state must be contiguous float32 [pool, value heads, dk, dv]")
+        if slots is not None and (slots.dtype != torch.int32 or slots.shape != (q.shape[0],)
+                                  or not slots.is_contiguous()):
+            raise ValueError("slots must be contiguous int32 [batch]")
+        if out is None:
+            out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        elif out.shape != v.shape or out.dtype != v.dtype or not out.is_contiguous():
+            raise ValueError("out must be contiguous and like v")
+        _check(_lib.fft_delta_rule_step(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                        g.data_ptr(), beta.data_ptr(), state.data_ptr(), _ptr(slots),
+                                        state.shape[0], out.data_ptr(), handle),
+               "fft_delta_rule_step")
+    return out

@@ -12,7 +12,11 @@
  *   - separable 2D and 3D transforms of any sides (rows, then columns, ...);
  *   - linear convolution of complex or real signals;
  *   - integer polynomial multiplication through fp64 transforms;
- *   - host-buffer forms of these, streamed through the device in chunks.
+ *   - host-buffer forms of these, streamed through the device in chunks;
+ *   - operators of sequence models that stand next to the convolution as a
+ *     mixer of long sequences: the gated delta rule (whole sequences, their
+ *     gradients, single tokens), layer normalisation with its gradients,
+ *     and the clipping of gradients by their global norm.
  *
  * Definitions followed:
  *   forward   X_k = sum_{n<N} x_n e^{-i 2 pi k n / N}
@@ -437,6 +441,123 @@ int fft_debug_cluster_timeout(void *data, int64_t polls, void *stream);
                                      loaded and stored with the TMA's 64-byte swizzle);
                                      0 = shared-memory exchanges */
 int fft_debug_set_option(int option, int64_t value);
+
+/* ---- Operators of sequence models --------------------------------------------
+ *
+ * These take the caller's workspace (device memory, 16-byte aligned, at least
+ * the bytes that the matching *_workspace_bytes call gives; used until the
+ * call's work on `stream` has finished) and otherwise keep to the rules
+ * above: arguments are checked before anything is enqueued, nothing is
+ * allocated or synchronised, every call can be captured into a CUDA graph.
+ * Array pointers are aligned to their elements (else FFT_ERR_MISALIGNED);
+ * 16-byte aligned rows run faster.  Results do not depend on timing (no
+ * atomics): the same call on the same inputs gives the same bits.
+ */
+
+/* Element types of their arrays. */
+#define FFT_ELEM_F32 0  /* float                    */
+#define FFT_ELEM_F64 1  /* double                   */
+#define FFT_ELEM_BF16 2 /* bfloat16, 2 bytes        */
+#define FFT_ELEM_F16 3  /* IEEE half, 2 bytes       */
+
+/*
+ * fft_layer_norm -- y = (x - mean) rstd w + b for every row of x, with mean
+ * and rstd = (variance + eps)^(-1/2) over the row's `dim` elements (the
+ * variance is the mean of (x - mean)^2).
+ *   x, y       rows x dim elements of type dtype; row r starts at element
+ *              r * ldx (r * ldy), ldx, ldy >= dim.  y == x (with ldy == ldx)
+ *              is allowed, other overlaps are not.
+ *   w, b       dim elements of type wtype: dtype, or FFT_ELEM_F32 with 16-bit
+ *              rows.  NULL: 1 and 0.
+ *   mean, rstd per row, float (double with FFT_ELEM_F64); each may be NULL.
+ *   rows       >= 0 (0: nothing is done); dim 1 .. 2^30; eps >= 0.
+ */
+int fft_layer_norm(const void *x, int64_t ldx, const void *w, const void *b, void *y, int64_t ldy,
+                   void *mean, void *rstd, int64_t rows, int64_t dim, double eps, int dtype,
+                   int wtype, void *stream);
+
+/*
+ * fft_layer_norm_backward -- the gradients of fft_layer_norm from dy and the
+ * forward call's x, w, mean and rstd: with xh = (x - mean) rstd, d = dy w,
+ *   dx = rstd (d - mean(d) - xh mean(d xh)),  dw = sum over rows of dy xh,
+ *   db = sum over rows of dy.
+ *   dx         rows x dim of type dtype; NULL: not wanted.  dx == dy or
+ *              dx == x (with equal row strides) is allowed.
+ *   dw, db     dim elements of type wtype, summed in float (double with
+ *              FFT_ELEM_F64) and rounded once; each may be NULL.  rows == 0
+ *              writes zeros.
+ *   workspace  fft_layer_norm_workspace_bytes(rows, dim, dtype) bytes; not
+ *              needed when dw and db are both NULL.
+ */
+size_t fft_layer_norm_workspace_bytes(int64_t rows, int64_t dim, int dtype);
+int fft_layer_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                            const void *w, const void *mean, const void *rstd, void *dx,
+                            int64_t lddx, void *dw, void *db, int64_t rows, int64_t dim,
+                            int dtype, int wtype, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/*
+ * fft_clip_grad_norm -- norm = sqrt(sum of g^2 over all `count` tensors) and
+ * out = g * min(1, max_norm / (norm + eps)) for every tensor.
+ * fft_grad_norm -- the norm alone.
+ *   in, out, numel, dtype  host arrays of `count` entries: device pointers,
+ *              element counts (>= 0) and FFT_ELEM_* types, which may differ
+ *              from tensor to tensor.  out[i] == in[i] (in place) is
+ *              allowed; other overlaps are not.  The arrays are read during
+ *              the call.
+ *   norm       one device float; may be NULL in fft_clip_grad_norm.
+ *   max_norm, eps  >= 0.
+ *   workspace  fft_grad_norm_workspace_bytes(count) bytes.
+ * Squares are summed in fp32 by groups of 16 bytes and those sums in fp64;
+ * squares that overflow or vanish in fp32 are taken in fp64.  An infinite
+ * norm scales by 0, a NaN makes every output NaN.
+ */
+size_t fft_grad_norm_workspace_bytes(int64_t count);
+int fft_grad_norm(int64_t count, const void *const *in, const int64_t *numel, const int *dtype,
+                  float *norm, void *workspace, size_t workspace_bytes, void *stream);
+int fft_clip_grad_norm(int64_t count, const void *const *in, void *const *out,
+                       const int64_t *numel, const int *dtype, double max_norm, double eps,
+                       float *norm, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The gated delta rule.  Per sequence and value head, with a state S of
+ * dk rows and dv columns in float, token t decays the state, corrects what it
+ * holds under the key k_t towards v_t, and reads it with q_t:
+ *   S <- e^{g_t} S
+ *   u  = beta_t (v_t - S^T k_t)
+ *   S <- S + k_t u^T
+ *   o_t = scale S^T q_t
+ * Value head h uses key head h / (vheads / kheads).  Keys are taken as they
+ * are (callers normalise them); g is the logarithm of the decay (0: none;
+ * -infinity: the state is dropped).
+ */
+typedef struct fft_delta_desc {
+  int64_t batch;  /* sequences, >= 0 */
+  int64_t tokens; /* tokens of every sequence; packed: rows of all of them; >= 0 */
+  int64_t kheads; /* heads of q and k */
+  int64_t vheads; /* heads of v, g, beta, o: a multiple of kheads */
+  int64_t dk;     /* 1 .. 128 (fft_delta_rule_step: 1 .. 256) */
+  int64_t dv;     /* 1 .. 65536 */
+  /* Strides in elements: of a sequence (not used for packed rows), a token
+   * and a head.  The elements of one head are contiguous. */
+  int64_t q_stride[3], k_stride[3], v_stride[3], g_stride[3], beta_stride[3];
+  double scale;
+  int dtype; /* of q, k, v and o: FFT_ELEM_F32, _BF16 or _F16; g and beta are float */
+} fft_delta_desc;
+
+/*
+ * fft_delta_rule_step -- the recurrence as it stands, for a few tokens per
+ * sequence (decoding): the states are updated in place.
+ *   state  float [pool][vheads][dk][dv].
+ *   slots  int32 [batch] on the device: the state of each sequence, distinct;
+ *          a sequence whose slot is outside 0 .. pool - 1 is idle: its o is
+ *          0 and no state changes.  NULL: sequence i has state i
+ *          (pool >= batch).
+ *   o      [batch][tokens][vheads][dv], contiguous.
+ */
+int fft_delta_rule_step(const fft_delta_desc *desc, const void *q, const void *k, const void *v,
+                        const float *g, const float *beta, float *state, const int32_t *slots,
+                        int64_t pool, void *o, void *stream);
 
 /* Last status recorded on this host thread by a call that returns a
  * pointer (fft_plan_create). */
