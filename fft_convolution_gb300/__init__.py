@@ -91,6 +91,8 @@ SIGNATURES = {
     "fft_grad_norm_workspace_bytes": (_SZ, [_I64]),
     "fft_grad_norm": (_INT, [_I64, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "fft_clip_grad_norm": (_INT, [_I64, _VP, _VP, _VP, _VP, _DBL, _DBL, _VP, _VP, _SZ, _VP]),
+    "fft_delta_rule_workspace_bytes": (_SZ, [_VP, _INT]),
+    "fft_delta_rule": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "fft_delta_rule_step": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _VP]),
     "fft_debug_radix2_pass": (_INT, [_VP, _VP, _I64, _I64, _INT, _VP]),
     "fft_device_status": (_INT, [_VP]),
@@ -257,6 +259,17 @@ def fft_clip_grad_norm(count: int, ins, outs, numels, dtypes, max_norm: float, e
     """ins, outs, numels, dtypes: ctypes arrays of `count` entries."""
     return _lib.fft_clip_grad_norm(count, ins, outs, numels, dtypes, max_norm, eps, norm,
                                    workspace, workspace_bytes, stream)
+
+
+def fft_delta_rule_workspace_bytes(desc: DeltaDesc, packed: int) -> int:
+    return int(_lib.fft_delta_rule_workspace_bytes(ctypes.byref(desc), packed))
+
+
+def fft_delta_rule(desc: DeltaDesc, q: int, k: int, v: int, g: int, beta: int, offsets: int,
+                   initial_state: int, o: int, final_state: int, workspace: int,
+                   workspace_bytes: int, stream: int) -> int:
+    return _lib.fft_delta_rule(ctypes.byref(desc), q, k, v, g, beta, offsets, initial_state, o,
+                               final_state, workspace, workspace_bytes, stream)
 
 
 def fft_delta_rule_step(desc: DeltaDesc, q: int, k: int, v: int, g: int, beta: int, state: int,
@@ -553,7 +566,8 @@ def fftn(x, ndim: int, direction: int = FFT_FORWARD, out=None, stream=None):
 
 # ---- operators of sequence models (tensor helpers in sequence.py) ---------------
 
-_SEQUENCE = ("layer_norm", "layer_norm_backward", "grad_norm", "clip_grad_norm", "delta_rule_step")
+_SEQUENCE = ("layer_norm", "layer_norm_backward", "grad_norm", "clip_grad_norm", "delta_rule",
+             "delta_rule_step")
 
 
 def __getattr__(name):

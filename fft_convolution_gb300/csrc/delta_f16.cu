@@ -1,0 +1,13 @@
+// delta_f16.cu -- f16 instantiations of the gated delta rule over whole
+// sequences (delta_launch.cuh).
+#include "delta_launch.cuh"
+
+namespace fftgb {
+
+template <>
+cudaError_t launch_delta<__half>(const DeltaArgs &a, void *workspace, cudaStream_t st) {
+  char *ws = static_cast<char *>(workspace);
+  return a.dk <= 64 ? delta_forward_t<__half, 64>(a, ws, st) : delta_forward_t<__half, 128>(a, ws, st);
+}
+
+}  // namespace fftgb

@@ -1,0 +1,67 @@
+// delta_launch.cuh -- the launches of the gated delta rule over whole
+// sequences, for one element type.
+#pragma once
+
+#include "delta_prep.cuh"
+#include "delta_scan.cuh"
+
+namespace fftgb {
+
+// The plan of the chunks, made by a small kernel for packed sequences.
+template <typename T>
+cudaError_t delta_make_plan(const DeltaArgs &a, const DeltaLayout &w, char *ws, DeltaPlan &plan,
+                            cudaStream_t st) {
+  plan.row0 = plan.chunk0 = nullptr;
+  plan.chunks_max = w.chunks;
+  plan.per_seq = (int)((a.tokens + kChunk - 1) / kChunk);
+  if (!a.offsets) return cudaSuccess;
+  int *row0 = reinterpret_cast<int *>(ws + w.row0), *chunk0 = reinterpret_cast<int *>(ws + w.chunk0);
+  plan.row0 = row0;
+  plan.chunk0 = chunk0;
+  return launch_delta_plan(a.offsets, a.batch, a.tokens, row0, chunk0, st);
+}
+
+template <typename T, int DK, bool BACK>
+cudaError_t delta_prep_t(const DeltaArgs &a, const DeltaPlan &plan, char *kq, char *images,
+                         int *status, cudaStream_t st) {
+  static DeviceOnce once;
+  const void *kern = (const void *)delta_prep_kernel<T, DK, BACK>;
+  cudaError_t e = smem_limit_once(kern, prep_smem<T, DK>(), once);
+  if (e != cudaSuccess) return e;
+  const long long blocks = plan.chunks_max * a.kheads;
+  if (blocks == 0) return cudaSuccess;
+  delta_prep_kernel<T, DK, BACK>
+      <<<(unsigned)blocks, kPrepThreads, prep_smem<T, DK>(), st>>>(a, plan, kq, images, status);
+  return cudaGetLastError();
+}
+
+template <typename T, int DK, bool SAVE>
+cudaError_t delta_scan_t(const DeltaArgs &a, const DeltaPlan &plan, const char *kq,
+                         const char *images, float *states, float *rows, int *status,
+                         cudaStream_t st) {
+  constexpr size_t smem = scan_smem(DK, Terms<T>::value);
+  static DeviceOnce once;
+  const void *kern = (const void *)delta_scan_kernel<T, DK, SAVE>;
+  cudaError_t e = smem_limit_once(kern, smem, once);
+  if (e != cudaSuccess) return e;
+  const long long blocks = a.batch * a.vheads * ((a.dv + 127) / 128);
+  delta_scan_kernel<T, DK, SAVE><<<(unsigned)blocks, kScanThreads, smem, st>>>(
+      a, plan, kq, images, states, rows, status);
+  return cudaGetLastError();
+}
+
+template <typename T, int DK>
+cudaError_t delta_forward_t(const DeltaArgs &a, char *ws, cudaStream_t st) {
+  int *status = device_status_word();
+  if (!status) return cudaErrorInvalidDevice;
+  const DeltaLayout w(a, a.offsets != nullptr, false);
+  DeltaPlan plan;
+  cudaError_t e = delta_make_plan<T>(a, w, ws, plan, st);
+  if (e == cudaSuccess) e = delta_prep_t<T, DK, false>(a, plan, ws + w.kq, ws + w.images, status, st);
+  if (e == cudaSuccess)
+    e = delta_scan_t<T, DK, false>(a, plan, ws + w.kq, ws + w.images, nullptr, nullptr, status,
+                                   st);
+  return e;
+}
+
+}  // namespace fftgb

@@ -1,0 +1,295 @@
+// delta_prep.cuh -- what the scans of the gated delta rule need of each
+// chunk (delta.cuh): K and Q as scaled fp16 tiles, the inverse of the unit
+// triangular matrix, M, and the factors of its tokens.
+//
+// One block per chunk and key head.  [K; Q] K^T (128 x 64) is one product on
+// the tensor cores, kept in tensor memory for all value heads that share the
+// key head; each of the 128 threads then owns one row of it.  The inverse is
+// taken in fp32: the four 16 x 16 diagonal blocks by substitution (one warp
+// each, one column per lane), the blocks below them by products, doubling
+// the solved size twice (T_21 = -T_22 L_21 T_11).  Substitution alone would
+// be a chain of 64 dependent steps, and a power series of L would cancel
+// catastrophically for keys that repeat.
+//
+// Everything is written in exactly the layout of the scans' shared memory,
+// so they fetch a chunk with two bulk copies, whatever the inputs' type,
+// strides and alignment.
+//
+// Forward image: (I + A beta)^-1 and M by rows; per token
+//   0: gamma 2^ek   1: Gamma/gamma 2^ek   2: beta   3: gamma 2^(eq - em)
+//   4: scale 2^em   5: 2^et
+// BACK image: (I + beta A)^-T and M^T; per token
+//   0: Gamma/gamma 2^ek   1: scale 2^em   2: 2^et   3: beta
+//   4: gamma beta 2^ek    5: scale gamma 2^eq
+// where 2^-e is the scale of a token's row of K (ek), Q (eq), of the inverse
+// (et) and of M (em).  After the factors: Gamma, the decay of the whole chunk.
+#pragma once
+
+#include "delta.cuh"
+
+namespace fftgb {
+
+constexpr int kPrepThreads = 128;
+constexpr int kPitch = 68;  // floats per row of a 64 x 64 fp32 matrix (rows stay 16-byte aligned)
+
+template <typename T, int DK> constexpr size_t prep_smem() {
+  return 1024 + (size_t)kq_bytes(DK, Terms<T>::value) + 2 * 64 * kPitch * 4;
+}
+
+// 64 x 64 fp32 matrix (or its transpose) to the leading and trailing tile,
+// rows scaled; the inverse scales go to `inv`.
+template <bool TRANS>
+__device__ __forceinline__ void write_image(const float *m, char *dst, float *inv, int tid) {
+#pragma unroll
+  for (int i = tid; i < 64 * 8; i += kPrepThreads) {
+    const int r = i >> 3, c = i & 7;
+    float f[8];
+    if constexpr (TRANS) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = m[(c * 8 + k) * kPitch + r];
+    } else {
+      const float4 x = *reinterpret_cast<const float4 *>(m + r * kPitch + c * 8);
+      const float4 y = *reinterpret_cast<const float4 *>(m + r * kPitch + c * 8 + 4);
+      f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+      f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+    }
+    const float s = row_scale(lane_max<8>(max8(f)));
+    if (c == 0) inv[r] = scale_inverse(s);
+    uint4 hi, lo;
+    split8(f, s, hi, lo);
+    const int at = piece_at(r, c, 0);
+    *reinterpret_cast<uint4 *>(dst + at) = hi;
+    *reinterpret_cast<uint4 *>(dst + kTile + at) = lo;
+  }
+}
+
+// G_i of the 64 tokens, as the sum of two floats: differences of running
+// sums of up to 64 * 128 keep fp32 accuracy.
+__device__ __forceinline__ void running_decay(const float *g, long long step, int n, int tid,
+                                              double *carry, float2 *out) {
+  float x = 0.0f;
+  if (tid < 64 && tid < n) {
+    x = g[tid * step];
+    x = x < kMinLogDecay ? kMinLogDecay : x;  // a NaN stays
+  }
+  double s = x;
+  const int lane = tid & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double t = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += t;
+  }
+  if (tid == 31) *carry = s;
+  __syncthreads();
+  if (tid < 64) {
+    if (tid >= 32) s += *carry;
+    const float h = (float)s;
+    out[tid] = make_float2(h, (float)(s - (double)h));
+  }
+}
+__device__ __forceinline__ float decay_between(float2 i, float2 j) {
+  return expf((i.x - j.x) + (i.y - j.y));
+}
+
+// Rows 0 .. 63 of K or Q into its tiles in shared memory and in the image;
+// inv: the rows' inverse scales.
+template <typename T, int DK>
+__device__ __forceinline__ void load_rows(const T *src, long long stride, int n, int cols, bool vec,
+                                          char *tiles, char *image, float *inv, int tid) {
+  constexpr int P = DK / 8;
+  constexpr int kPlane = 2 * (DK / 64) * kTile;
+#pragma unroll 4
+  for (int i = tid; i < 64 * P; i += kPrepThreads) {
+    const int r = i / P, c = i % P;
+    const int left = r < n ? cols - c * 8 : 0;
+    float f[8];
+    load8(src + (left > 0 ? (long long)r * stride + c * 8 : 0), left, vec, f);
+    const float s = row_scale(lane_max<P>(max8(f)));
+    if (c == 0) inv[r] = scale_inverse(s);
+    uint4 hi, lo;
+    split8(f, s, hi, lo);
+    const int at = piece_at(r, c, 2 * kTile);
+    *reinterpret_cast<uint4 *>(tiles + at) = hi;
+    *reinterpret_cast<uint4 *>(image + at) = hi;
+    if constexpr (Terms<T>::value == 2) {
+      *reinterpret_cast<uint4 *>(tiles + kPlane + at) = lo;
+      *reinterpret_cast<uint4 *>(image + kPlane + at) = lo;
+    }
+  }
+}
+
+template <typename T, int DK, bool BACK>
+__global__ void __launch_bounds__(kPrepThreads)
+delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *images, int *status) {
+  extern __shared__ char smem_raw[];
+  __shared__ uint64_t bar;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int failed;
+  __shared__ double carry;
+  __shared__ float2 G[64];
+  __shared__ float beta_s[64], inv_kq[2 * 64], inv_t[64], inv_m[64];
+  constexpr int NT = Terms<T>::value;
+  constexpr uint32_t kPlane = 2 * (DK / 64) * kTile;  // [K; Q], one term
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hk = blockIdx.x % a.kheads;
+  const long long ci = blockIdx.x / a.kheads;
+  DeltaChunk c;
+  if (!delta_chunk(a, plan, ci, c)) return;
+
+  // Tiles: 128 rows (K above Q) of 64 columns, kTile * 2 bytes each.
+  char *tiles = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  float *L = reinterpret_cast<float *>(tiles + NT * kPlane);
+  float *X = L + 64 * kPitch;
+  const uint32_t t0 = smem_u32(tiles);
+  char *kqi = kq + (ci * a.kheads + hk) * (long long)kq_bytes(DK, NT);
+  load_rows<T, DK>(head_rows<T>(a.k, a.sk, c.b, c.row, hk), a.sk.tok, c.n, a.dk,
+                   vec_rows<T>(a.k, a.sk), tiles, kqi, inv_kq, tid);
+  load_rows<T, DK>(head_rows<T>(a.q, a.sq, c.b, c.row, hk), a.sq.tok, c.n, a.dk,
+                   vec_rows<T>(a.q, a.sq), tiles + kTile, kqi + kTile, inv_kq + 64, tid);
+  __syncwarp();
+  if (warp == 0) tmem_alloc(&tmem_slot, 64);
+  if (tid == 0) {
+    bar_init(&bar, 1);
+    failed = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  fence_smem_to_async();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t acc = tmem_slot;
+  if (tid == 0) {
+    constexpr uint32_t idesc = mma_desc(128, 64, false, false);
+#pragma unroll
+    for (int term = 0; term < (NT == 1 ? 1 : 3); ++term) {
+      // leading x leading, leading x trailing, trailing x leading
+      const uint32_t ta = t0 + (term == 2 ? kPlane : 0), tb = t0 + (term == 1 ? kPlane : 0);
+#pragma unroll
+      for (int k = 0; k < DK / 16; ++k) {
+        const uint32_t at = (k >> 2) * 2 * kTile + (k & 3) * 32;
+        mma_ss(acc, tile_desc(ta + at, 16, 1024), tile_desc(tb + at, 16, 1024), idesc,
+               term > 0 || k > 0);
+      }
+    }
+    mma_commit(&bar);
+  }
+  const bool ok = wait_or_fail(&bar, 0, &failed, status);
+  if (__syncthreads_and(ok)) {
+    tc_fence_after();
+    const int group = a.vheads / a.kheads;
+    for (int hv = hk * group; hv < (hk + 1) * group; ++hv) {
+      char *image = images + (ci * a.vheads + hv) * (long long)kImageBytes;
+      const float *g = a.g + c.b * a.sg.seq + c.row * a.sg.tok + hv * a.sg.head;
+      const float *beta = a.beta + c.b * a.sb.seq + c.row * a.sb.tok + hv * a.sb.head;
+      running_decay(g, a.sg.tok, c.n, tid, &carry, G);
+      if (tid < 64) beta_s[tid] = tid < c.n ? beta[tid * a.sb.tok] : 0.0f;
+      __syncthreads();
+      // Row i of A (threads 0 .. 63, from K K^T) or of M (64 .. 127).  Row i
+      // of the matrix to invert is A_ij beta_j, or beta_i A_ij (BACK).
+      const int i = tid & 63;
+      const float2 gi = G[i];
+      const bool is_m = tid >= 64;
+      const float fi = inv_kq[tid] * (BACK && !is_m ? beta_s[i] : 1.0f);
+      float *row = (is_m ? X : L) + i * kPitch;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t r[32];
+        tmem_ld32(acc + ((uint32_t)(warp * 32) << 16) + half * 32, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int jj = 0; jj < 32; ++jj) {
+          const int j = half * 32 + jj;
+          float x = 0.0f;
+          if (is_m ? j <= i : j < i) {
+            x = decay_between(gi, G[j]) * (__uint_as_float(r[jj]) * fi * inv_kq[j]);
+            if (!BACK && !is_m) x *= beta_s[j];
+          }
+          row[j] = x;
+        }
+      }
+      __syncthreads();
+      write_image<BACK>(X, image + 2 * kTile, inv_m, tid);
+      __syncthreads();
+      // Diagonal blocks: column `col` of the inverse of block `warp`, by
+      // substitution; both halves of the warp do the same columns.
+      {
+        const int col = lane & 15, r0 = warp * 16;
+        float x[16];
+#pragma unroll
+        for (int m = 0; m < 16; ++m) {
+          float s = m == col ? 1.0f : 0.0f;
+#pragma unroll
+          for (int p = 0; p < m; ++p) s = fmaf(-L[(r0 + m) * kPitch + r0 + p], x[p], s);
+          x[m] = s;
+        }
+        if (lane < 16) {
+#pragma unroll
+          for (int m = 0; m < 16; ++m) X[(r0 + m) * kPitch + r0 + col] = x[m];
+        }
+        // zeros above the diagonal blocks
+        for (int e = lane; e < 16 * (48 - r0); e += 32) {
+          const int w = 48 - r0;
+          X[(r0 + e / w) * kPitch + r0 + 16 + e % w] = 0.0f;
+        }
+      }
+      __syncthreads();
+      // Below the diagonal: sizes 16 and 32.  First Z = L_21 T_11 (kept where
+      // T_21 will be), then T_21 = -T_22 Z.
+#pragma unroll
+      for (int size = 16; size <= 32; size *= 2) {
+        const int pairs = 32 / size;              // 2, 1
+        const int per = kPrepThreads / pairs;     // threads of a pair
+        const int pr = tid / per, t = tid % per;
+        const int lo = pr * 2 * size, hi = lo + size;
+        const int outs = size * size / per;       // 4, 8 consecutive rows of one column
+        const int col = t % size, rb = (t / size) * outs;
+        float z[8];
+#pragma unroll
+        for (int o = 0; o < 8; ++o) z[o] = 0.0f;
+        for (int p = 0; p < size; ++p) {
+          const float x = X[(lo + p) * kPitch + lo + col];
+#pragma unroll
+          for (int o = 0; o < 8; ++o)
+            if (o < outs) z[o] = fmaf(L[(hi + rb + o) * kPitch + lo + p], x, z[o]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int o = 0; o < 8; ++o)
+          if (o < outs) X[(hi + rb + o) * kPitch + lo + col] = z[o];
+        __syncthreads();
+#pragma unroll
+        for (int o = 0; o < 8; ++o) z[o] = 0.0f;
+        for (int p = 0; p < size; ++p) {
+          const float x = X[(hi + p) * kPitch + lo + col];
+#pragma unroll
+          for (int o = 0; o < 8; ++o)
+            if (o < outs) z[o] = fmaf(-X[(hi + rb + o) * kPitch + hi + p], x, z[o]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int o = 0; o < 8; ++o)
+          if (o < outs) X[(hi + rb + o) * kPitch + lo + col] = z[o];
+        __syncthreads();
+      }
+      write_image<BACK>(X, image, inv_t, tid);
+      __syncthreads();
+      if (tid < 64) {
+        float *gates = reinterpret_cast<float *>(image + 4 * kTile) + tid;
+        const float ek = inv_kq[tid], eq = inv_kq[64 + tid], em = inv_m[tid], et = inv_t[tid];
+        const float gam = expf(G[tid].x), dec = decay_between(G[63], G[tid]), bt = beta_s[tid];
+        const float ga[kGates] = {gam * ek, dec * ek, bt, gam * (eq / em), a.scale * em, et};
+        const float gb[kGates] = {dec * ek, a.scale * em, et, bt, gam * bt * ek, a.scale * gam * eq};
+#pragma unroll
+        for (int k = 0; k < kGates; ++k) gates[k * 64] = BACK ? gb[k] : ga[k];
+        if (tid == 63) gates[(kGates - 1) * 64 + 1] = gam;  // Gamma, after the last factor
+      }
+      __syncthreads();
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 0) tmem_free(acc, 64);
+}
+
+}  // namespace fftgb

@@ -6,7 +6,10 @@
 //            o = scale S^T q.
 // With S' the decayed state, S^T q = S'^T q + (k . q) u: both products with
 // the state are taken in one walk over it, and one exchange between the
-// threads gives every sum.
+// threads gives every sum.  The state changes by k u + S (e^g - 1), added in
+// one rounding: of a slow decay e^g itself would keep few digits of its
+// distance from 1, an error that thousands of tokens add up; what rounding
+// leaves out of u is carried along for the same reason.
 //
 // Reading and writing the fp32 state is nearly all the traffic (128 KB per
 // head of 128 x 128, against under 1 KB for the token), so HBM bounds the
@@ -83,15 +86,14 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaArg
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) vc[j] = c0 + j < a.dv ? to_acc(v[t * a.sv.tok + c0 + j]) : 0.0f;
-    const float alpha = expf(g[t * a.sg.tok]), bt = beta[t * a.sb.tok];
-    float sum[9];  // S'^T k and S'^T q of the 4 columns, k . q
+    const float decay = expm1f(g[t * a.sg.tok]), bt = beta[t * a.sb.tok];
+    float sum[9];  // S^T k and S^T q of the 4 columns (S before its decay), k . q
 #pragma unroll
     for (int j = 0; j < 9; ++j) sum[j] = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[i][j] *= alpha;
         sum[j] = fmaf(kr[i], s[i][j], sum[j]);
         sum[4 + j] = fmaf(qr[i], s[i][j], sum[4 + j]);
       }
@@ -110,11 +112,17 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaArg
       sum[j] = (rd[0][cg][j] + rd[1][cg][j]) + (rd[2][cg][j] + rd[3][cg][j]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float u = bt * (vc[j] - sum[j]);
+      // u = beta (v - S'^T k) and what its rounding leaves out
+      const float held = fmaf(decay, sum[j], sum[j]), miss = vc[j] - held;
+      const float back = miss - vc[j];
+      const float rest = (vc[j] - (miss - back)) - (held + back);
+      const float u = bt * miss, ur = fmaf(bt, miss, -u) + bt * rest;
 #pragma unroll
-      for (int i = 0; i < R; ++i) s[i][j] = fmaf(kr[i], u, s[i][j]);
+      for (int i = 0; i < R; ++i)
+        s[i][j] += fmaf(kr[i], u, fmaf(kr[i], ur, decay * s[i][j]));
       if (rg == 0 && c0 + j < a.dv)
-        o[t * ostep + c0 + j] = from_acc<T>(a.scale * fmaf(sum[8], u, sum[4 + j]));
+        o[t * ostep + c0 + j] =
+            from_acc<T>(a.scale * fmaf(sum[8], u, fmaf(decay, sum[4 + j], sum[4 + j])));
     }
   }
 

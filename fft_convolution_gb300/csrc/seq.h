@@ -66,12 +66,20 @@ struct DeltaArgs {
   void *o;                // contiguous [sequence][token][head][dv]
   long long batch, tokens;
   int kheads, vheads, dk, dv;
+  int terms;  // fp16 values that hold one element of q and k (2: fp32)
   float scale;
   // Single tokens: the sequence's row of a pool of `pool` states (null: row = sequence).
   const int *slots;
   long long pool;
 };
 cudaError_t launch_delta_step(int dtype, const DeltaArgs &a, cudaStream_t st);
+// Whole sequences, in chunks; `workspace` holds delta_workspace_bytes().
+size_t delta_workspace_bytes(const DeltaArgs &a, bool packed);
+template <typename T>
+cudaError_t launch_delta(const DeltaArgs &a, void *workspace, cudaStream_t st);
+// Fills row0 and chunk0 (batch + 1 entries each) from offsets (delta_plan.cu).
+cudaError_t launch_delta_plan(const int *offsets, long long batch, long long tokens, int *row0,
+                              int *chunk0, cudaStream_t st);
 
 // ---- element conversions -----------------------------------------------------
 

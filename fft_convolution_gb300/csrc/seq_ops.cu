@@ -54,9 +54,10 @@ int clip_check(int64_t count, const void *const *in, const int64_t *numel, const
 
 DeltaStride stride(const int64_t s[3]) { return DeltaStride{s[0], s[1], s[2]}; }
 
-// Sizes, types and pointers that every call of the delta rule has.
-int delta_check(const fft_delta_desc *d, int64_t max_dk, const void *q, const void *k,
-                const void *v, const float *g, const float *beta, DeltaArgs *a) {
+constexpr int64_t kDeltaMaxDk = 128;
+
+// Sizes and types of a call of the delta rule.
+int delta_sizes(const fft_delta_desc *d, int64_t max_dk, DeltaArgs *a) {
   if (!d) return FFT_ERR_INVALID_ARG;
   if (d->batch < 0 || d->tokens < 0 || d->kheads <= 0 || d->vheads <= 0 || d->dk <= 0 ||
       d->dv <= 0 || d->vheads % d->kheads != 0 || !elem_type(d->dtype) || !isfinite(d->scale))
@@ -66,20 +67,11 @@ int delta_check(const fft_delta_desc *d, int64_t max_dk, const void *q, const vo
         d->beta_stride[i] < 0)
       return FFT_ERR_INVALID_ARG;
   if (d->dtype == FFT_ELEM_F64 || d->dk > max_dk || d->dv > 65536 || d->vheads > 65536 ||
-      d->tokens > 0x7fffffff || d->batch > 0x7fffffff / (d->vheads * ((d->dv + 15) / 16)) ||
+      d->tokens > 0x7fffffff || d->batch > ((int64_t)1 << 24) ||
+      d->batch > 0x7fffffff / (d->vheads * ((d->dv + 31) / 32)) ||
       (d->tokens > 0 && d->batch > kMaxElems / (d->tokens * d->vheads)))
     return FFT_ERR_UNSUPPORTED;
-  if (d->batch > 0 && d->tokens > 0 && (!q || !k || !v || !g || !beta))
-    return FFT_ERR_INVALID_ARG;
-  if (off_element(q, d->dtype) || off_element(k, d->dtype) || off_element(v, d->dtype) ||
-      off_element(g, FFT_ELEM_F32) || off_element(beta, FFT_ELEM_F32))
-    return FFT_ERR_MISALIGNED;
   *a = DeltaArgs{};
-  a->q = q;
-  a->k = k;
-  a->v = v;
-  a->g = g;
-  a->beta = beta;
   a->sq = stride(d->q_stride);
   a->sk = stride(d->k_stride);
   a->sv = stride(d->v_stride);
@@ -91,8 +83,33 @@ int delta_check(const fft_delta_desc *d, int64_t max_dk, const void *q, const vo
   a->vheads = (int)d->vheads;
   a->dk = (int)d->dk;
   a->dv = (int)d->dv;
+  a->terms = d->dtype == FFT_ELEM_F32 ? 2 : 1;
   a->scale = (float)d->scale;
   return FFT_OK;
+}
+
+// Those and the inputs.
+int delta_check(const fft_delta_desc *d, int64_t max_dk, const void *q, const void *k,
+                const void *v, const float *g, const float *beta, DeltaArgs *a) {
+  const int rc = delta_sizes(d, max_dk, a);
+  if (rc != FFT_OK) return rc;
+  if (d->batch > 0 && d->tokens > 0 && (!q || !k || !v || !g || !beta))
+    return FFT_ERR_INVALID_ARG;
+  if (off_element(q, d->dtype) || off_element(k, d->dtype) || off_element(v, d->dtype) ||
+      off_element(g, FFT_ELEM_F32) || off_element(beta, FFT_ELEM_F32))
+    return FFT_ERR_MISALIGNED;
+  a->q = q;
+  a->k = k;
+  a->v = v;
+  a->g = g;
+  a->beta = beta;
+  return FFT_OK;
+}
+
+// Grids of the kernels over all chunks.
+int delta_chunks_check(const DeltaArgs &a, bool packed) {
+  const int64_t chunks = packed ? (a.tokens + 63 * a.batch) / 64 : a.batch * ((a.tokens + 63) / 64);
+  return chunks > 0x7fffffff / a.vheads ? FFT_ERR_UNSUPPORTED : FFT_OK;
 }
 
 }  // namespace
@@ -197,6 +214,42 @@ int fft_clip_grad_norm(int64_t count, const void *const *in, void *const *out,
   void *const none[1] = {nullptr};
   return finish(launch_clip(count, in, count > 0 ? out : none, numel, dtype, max_norm, eps, norm,
                             workspace, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fft_delta_rule_workspace_bytes(const fft_delta_desc *desc, int packed) {
+  DeltaArgs a;
+  if (delta_sizes(desc, kDeltaMaxDk, &a) != FFT_OK || delta_chunks_check(a, packed != 0) != FFT_OK)
+    return 0;
+  return delta_workspace_bytes(a, packed != 0);
+}
+
+int fft_delta_rule(const fft_delta_desc *desc, const void *q, const void *k, const void *v,
+                   const float *g, const float *beta, const int32_t *offsets,
+                   const float *initial_state, void *o, float *final_state, void *workspace,
+                   size_t workspace_bytes, void *stream) {
+  DeltaArgs a;
+  int rc = delta_check(desc, kDeltaMaxDk, q, k, v, g, beta, &a);
+  if (rc == FFT_OK) rc = delta_chunks_check(a, offsets != nullptr);
+  if (rc != FFT_OK) return rc;
+  if (a.batch == 0) return FFT_OK;
+  if ((a.tokens > 0 && !o) ||
+      (workspace_bytes < delta_workspace_bytes(a, offsets != nullptr)) ||
+      (!workspace && delta_workspace_bytes(a, offsets != nullptr) > 0))
+    return FFT_ERR_INVALID_ARG;
+  if (misaligned(workspace) || off_element(o, desc->dtype) ||
+      off_element(initial_state, FFT_ELEM_F32) || off_element(final_state, FFT_ELEM_F32) ||
+      off_element(offsets, FFT_ELEM_F32))
+    return FFT_ERR_MISALIGNED;
+  a.offsets = offsets;
+  a.state_in = initial_state;
+  a.state_out = final_state;
+  a.o = o;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  switch (desc->dtype) {
+    case FFT_ELEM_F32: return finish(launch_delta<float>(a, workspace, st));
+    case FFT_ELEM_BF16: return finish(launch_delta<__nv_bfloat16>(a, workspace, st));
+    default: return finish(launch_delta<__half>(a, workspace, st));
+  }
 }
 
 int fft_delta_rule_step(const fft_delta_desc *desc, const void *q, const void *k, const void *v,

@@ -244,6 +244,54 @@ def _delta_inputs(q, k, v, g, beta, scale, batch, packed: bool):
     return q, k, v, desc
 
 
+def _packing(q, offsets):
+    """(number of sequences, packed) of the inputs' leading axes."""
+    if offsets is None:
+        return q.shape[0], False
+    if offsets.dim() != 1 or offsets.shape[0] < 1 or offsets.dtype not in (torch.int32, torch.int64):
+        raise ValueError("offsets must be int32 or int64 [sequences + 1]")
+    return offsets.shape[0] - 1, True
+
+
+def _states(t, shape, what: str):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or tuple(t.shape) != shape:
+        raise ValueError(f"{what} must be float32 {list(shape)}")
+    return t.contiguous()
+
+
+def delta_rule(q, k, v, g, beta, scale=None, initial_state=None, offsets=None, out=None,
+               stream=None):
+    """(o, final state) of the gated delta rule over whole sequences (see
+    fft_delta_rule).  q, k: [batch, tokens, key heads, dk]; v: [batch, tokens,
+    value heads, dv]; g (log decay) and beta: float32 [batch, tokens, value
+    heads].  With offsets (int32 [sequences + 1] on the device) the rows of
+    all sequences are packed and the arrays have no batch axis.  scale:
+    dk ** -0.5 by default.  States: float32 [sequences, value heads, dk, dv]."""
+    batch, packed = _packing(q, offsets)
+    context, handle = _on(stream)
+    with context:
+        q, k, v, desc = _delta_inputs(q, k, v, g, beta, scale, batch, packed)
+        _device(q, initial_state, offsets, out)
+        if packed:
+            offsets = offsets.to(torch.int32).contiguous()
+        shape = (batch, desc.vheads, desc.dk, desc.dv)
+        initial_state = _states(initial_state, shape, "initial_state")
+        if out is None:
+            out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        elif out.shape != v.shape or out.dtype != v.dtype or not out.is_contiguous():
+            raise ValueError("out must be contiguous and like v")
+        final = torch.empty(shape, dtype=torch.float32, device=v.device)
+        nbytes = _lib.fft_delta_rule_workspace_bytes(ctypes.byref(desc), packed)
+        ws = _workspace(nbytes, v.device)
+        _check(_lib.fft_delta_rule(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                   g.data_ptr(), beta.data_ptr(), _ptr(offsets),
+                                   _ptr(initial_state), out.data_ptr(), final.data_ptr(),
+                                   ws.data_ptr(), nbytes, handle), "fft_delta_rule")
+    return out, final
+
+
 def delta_rule_step(q, k, v, g, beta, state, slots=None, scale=None, out=None, stream=None):
     """One or a few tokens per sequence of the gated delta rule (see
     fft_delta_rule_step): returns o [batch, tokens, value heads, dv] and

@@ -546,6 +546,31 @@ typedef struct fft_delta_desc {
 } fft_delta_desc;
 
 /*
+ * fft_delta_rule -- whole sequences, in chunks of 64 tokens.
+ *   offsets        NULL: `batch` sequences of `tokens` tokens.  Else int32
+ *                  [batch + 1] on the device: sequence i has the rows
+ *                  offsets[i] .. offsets[i + 1] - 1 of the packed arrays of
+ *                  `tokens` rows (ascending, from 0 to tokens; empty
+ *                  sequences are fine).  Offsets that descend or leave the
+ *                  rows are cut to the nearest that do not; rows of no
+ *                  sequence are left unwritten.
+ *   initial_state  float [batch][vheads][dk][dv]; NULL: zero.
+ *   final_state    the same, written; may be NULL; may be initial_state.
+ *   o              [batch][tokens][vheads][dv], or [tokens][vheads][dv] with
+ *                  offsets; contiguous.
+ *   workspace      fft_delta_rule_workspace_bytes(desc, offsets != NULL) bytes.
+ * The state and every sum are float; q, k, v and the state enter products
+ * with 16 or more significand bits.  A value that is not finite spoils the
+ * outputs of its chunk of 64 tokens and all later ones of its sequence and
+ * head.
+ */
+size_t fft_delta_rule_workspace_bytes(const fft_delta_desc *desc, int packed);
+int fft_delta_rule(const fft_delta_desc *desc, const void *q, const void *k, const void *v,
+                   const float *g, const float *beta, const int32_t *offsets,
+                   const float *initial_state, void *o, float *final_state, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/*
  * fft_delta_rule_step -- the recurrence as it stands, for a few tokens per
  * sequence (decoding): the states are updated in place.
  *   state  float [pool][vheads][dk][dv].
