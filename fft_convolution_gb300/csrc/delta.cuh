@@ -174,10 +174,10 @@ template <int W> __device__ __forceinline__ float lane_max(float m) {
 }
 
 __device__ __forceinline__ void split8(const float (&f)[8], float s, uint4 &hi, uint4 &lo) {
-  split2(f[0], f[1], s, hi.x, lo.x);
-  split2(f[2], f[3], s, hi.y, lo.y);
-  split2(f[4], f[5], s, hi.z, lo.z);
-  split2(f[6], f[7], s, hi.w, lo.w);
+  split2(make_float2(f[0], f[1]), s, hi.x, lo.x);
+  split2(make_float2(f[2], f[3]), s, hi.y, lo.y);
+  split2(make_float2(f[4], f[5]), s, hi.z, lo.z);
+  split2(make_float2(f[6], f[7]), s, hi.w, lo.w);
 }
 // Byte offset of the 16-byte piece c (8 columns) of row r in a row of tiles
 // `tile` bytes apart.
@@ -196,17 +196,10 @@ __host__ __device__ __forceinline__ bool vec_rows(const void *p, const DeltaStri
 // in shared memory, `status` the device status word.
 __device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, volatile int *failed,
                                              int *status) {
+  if (bar_poll(bar, parity)) return true;
   const long long t0 = clock64();
   for (uint32_t it = 0; it < (1u << 24); ++it) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (done) return true;
+    if (bar_poll(bar, parity)) return true;
     if (*failed || clock64() - t0 > 8000000000ll) break;  // about 4 s
   }
   *failed = 1;

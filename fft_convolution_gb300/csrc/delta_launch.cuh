@@ -35,19 +35,33 @@ cudaError_t delta_prep_t(const DeltaArgs &a, const DeltaPlan &plan, char *kq, ch
   return cudaGetLastError();
 }
 
-template <typename T, int DK, bool SAVE>
+// Whether rows of 128 columns (fewer at the end) can go by bulk copies.
+template <typename T> bool delta_staged(const DeltaArgs &a, const void *in, const DeltaStride &s,
+                                        const void *out) {
+  return sizeof(T) == 2 && a.dv % 8 == 0 && vec_rows<T>(in, s) && ((uintptr_t)out & 15u) == 0;
+}
+
+template <typename T, int DK, bool SAVE, bool STAGED>
 cudaError_t delta_scan_t(const DeltaArgs &a, const DeltaPlan &plan, const char *kq,
                          const char *images, float *states, float *rows, int *status,
                          cudaStream_t st) {
-  constexpr size_t smem = scan_smem(DK, Terms<T>::value);
+  constexpr size_t smem = scan_smem(DK, Terms<T>::value, STAGED);
   static DeviceOnce once;
-  const void *kern = (const void *)delta_scan_kernel<T, DK, SAVE>;
-  cudaError_t e = smem_limit_once(kern, smem, once);
+  auto kern = delta_scan_kernel<T, DK, SAVE, STAGED>;
+  cudaError_t e = smem_limit_once((const void *)kern, smem, once);
   if (e != cudaSuccess) return e;
   const long long blocks = a.batch * a.vheads * ((a.dv + 127) / 128);
-  delta_scan_kernel<T, DK, SAVE><<<(unsigned)blocks, kScanThreads, smem, st>>>(
-      a, plan, kq, images, states, rows, status);
+  kern<<<(unsigned)blocks, kScanThreads, smem, st>>>(a, plan, kq, images, states, rows, status);
   return cudaGetLastError();
+}
+template <typename T, int DK, bool SAVE>
+cudaError_t delta_scan(const DeltaArgs &a, const DeltaPlan &plan, const char *kq,
+                       const char *images, float *states, float *rows, int *status,
+                       cudaStream_t st) {
+  if constexpr (sizeof(T) == 2)
+    if (delta_staged<T>(a, a.v, a.sv, a.o))
+      return delta_scan_t<T, DK, SAVE, true>(a, plan, kq, images, states, rows, status, st);
+  return delta_scan_t<T, DK, SAVE, false>(a, plan, kq, images, states, rows, status, st);
 }
 
 template <typename T, int DK>
@@ -59,8 +73,7 @@ cudaError_t delta_forward_t(const DeltaArgs &a, char *ws, cudaStream_t st) {
   cudaError_t e = delta_make_plan<T>(a, w, ws, plan, st);
   if (e == cudaSuccess) e = delta_prep_t<T, DK, false>(a, plan, ws + w.kq, ws + w.images, status, st);
   if (e == cudaSuccess)
-    e = delta_scan_t<T, DK, false>(a, plan, ws + w.kq, ws + w.images, nullptr, nullptr, status,
-                                   st);
+    e = delta_scan<T, DK, false>(a, plan, ws + w.kq, ws + w.images, nullptr, nullptr, status, st);
   return e;
 }
 

@@ -16,8 +16,8 @@
 // strides and alignment.
 //
 // Forward image: (I + A beta)^-1 and M by rows; per token
-//   0: gamma 2^ek   1: Gamma/gamma 2^ek   2: beta   3: gamma 2^(eq - em)
-//   4: scale 2^em   5: 2^et
+//   0: -gamma 2^ek   1: Gamma/gamma 2^ek   2: beta 2^et   3: gamma 2^(eq - em)
+//   4: scale 2^em    5: 2^et
 // BACK image: (I + beta A)^-T and M^T; per token
 //   0: Gamma/gamma 2^ek   1: scale 2^em   2: 2^et   3: beta
 //   4: gamma beta 2^ek    5: scale gamma 2^eq
@@ -168,7 +168,7 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
 #pragma unroll
       for (int k = 0; k < DK / 16; ++k) {
         const uint32_t at = (k >> 2) * 2 * kTile + (k & 3) * 32;
-        mma_ss(acc, tile_desc(ta + at, 16, 1024), tile_desc(tb + at, 16, 1024), idesc,
+        mma_ss(acc, tile_desc(ta + at, 16), tile_desc(tb + at, 16), idesc,
                term > 0 || k > 0);
       }
     }
@@ -278,7 +278,7 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
         float *gates = reinterpret_cast<float *>(image + 4 * kTile) + tid;
         const float ek = inv_kq[tid], eq = inv_kq[64 + tid], em = inv_m[tid], et = inv_t[tid];
         const float gam = expf(G[tid].x), dec = decay_between(G[63], G[tid]), bt = beta_s[tid];
-        const float ga[kGates] = {gam * ek, dec * ek, bt, gam * (eq / em), a.scale * em, et};
+        const float ga[kGates] = {-gam * ek, dec * ek, bt * et, gam * (eq / em), a.scale * em, et};
         const float gb[kGates] = {dec * ek, a.scale * em, et, bt, gam * bt * ek, a.scale * gam * eq};
 #pragma unroll
         for (int k = 0; k < kGates; ++k) gates[k * 64] = BACK ? gb[k] : ga[k];

@@ -28,22 +28,28 @@
 
 namespace fftgb {
 
-constexpr int kScanThreads = 10 * 32;
+constexpr int kScanThreads = 11 * 32;
 constexpr int kScanMath = 256;
+constexpr int kScanStages = 2;
 
-__host__ __device__ constexpr int scan_stages(int terms) { return terms == 1 ? 3 : 2; }
-// Stage: the tiles of K and Q, then the head's image, 1024-byte aligned.
-__host__ __device__ constexpr int scan_stage_bytes(int dk, int terms) {
-  return kq_bytes(dk, terms) + ((kImageBytes + 1023) & ~1023);
+// 64 tokens x 128 columns of a 16-bit type.
+constexpr int kRows16 = 64 * 128 * 2;
+// Stage: the tiles of K and Q, the head's image, and (STAGED) the rows of V
+// (backwards: of dO); 1024-byte aligned.
+__host__ __device__ constexpr int scan_stage_bytes(int dk, int terms, bool staged) {
+  return kq_bytes(dk, terms) + ((kImageBytes + 1023) & ~1023) + (staged ? kRows16 : 0);
 }
-__host__ __device__ constexpr size_t scan_smem(int dk, int terms) {
-  return 1024 + (size_t)scan_stages(terms) * scan_stage_bytes(dk, terms);
+// Two stages, and (STAGED) the rows of O (of dV) on their way out.
+__host__ __device__ constexpr size_t scan_smem(int dk, int terms, bool staged) {
+  return 1024 + (size_t)kScanStages * scan_stage_bytes(dk, terms, staged) +
+         (staged ? kRows16 : 0);
 }
 
 struct ScanBars {
-  uint64_t full[3], empty[3];
+  uint64_t full[kScanStages], empty[kScanStages];
   uint64_t p, n, e, s, o;       // products done: P, N, E, W K, O
   uint64_t y, u, ns, sb, of;    // operands ready: Y, U and W, N scaled, S; O read
+  uint64_t put, got;            // STAGED: rows of O in shared memory; copied out
   uint64_t done;                // every product
 };
 
@@ -76,31 +82,75 @@ __device__ __forceinline__ long long out_row(const DeltaArgs &a, long long b, lo
   return ((packed ? row : b * a.tokens + row) * a.vheads + h) * a.dv;
 }
 
-// The loading thread: the chunks' images into the stages.
-template <int DK, int NT>
+// The loading warp: the chunks' images into the stages and, STAGED, the rows
+// x of v's type (128 columns from column c0; where the chunk has fewer than 64
+// tokens its last row again: its values meet factors of 0, which only
+// finite ones leave 0).
+template <typename T, int DK, bool STAGED>
 __device__ __forceinline__ void scan_load(const DeltaArgs &a, const ScanSpan &sp, int h,
                                           bool backwards, const char *kq, const char *images,
-                                          char *stages, ScanBars *bars, volatile int *failed,
-                                          int *status) {
-  constexpr int ST = scan_stages(NT);
+                                          const T *x, long long step, int c0, char *stages,
+                                          ScanBars *bars, volatile int *failed, int *status,
+                                          int lane) {
+  constexpr int NT = Terms<T>::value, ST = kScanStages;
+  constexpr int kStage = scan_stage_bytes(DK, NT, STAGED);
   const int hk = h / (a.vheads / a.kheads);
+  const int cols = a.dv - c0 < 128 ? a.dv - c0 : 128;
   int issued = 0;
   for (int it = 0; it < sp.chunks; ++it) {
-    const long long c = sp.chunk0 + (backwards ? sp.chunks - 1 - it : it);
+    const int ci = backwards ? sp.chunks - 1 - it : it;
+    const long long c = sp.chunk0 + ci;
     const int s = it % ST;
-    if (it >= ST && !wait_or_fail(&bars->empty[s], (it / ST - 1) & 1, failed, status)) break;
-    char *stage = stages + s * scan_stage_bytes(DK, NT);
-    bar_arrive_tx(&bars->full[s], kq_bytes(DK, NT) + kImageBytes);
-    bulk_load(stage, kq + (c * a.kheads + hk) * (long long)kq_bytes(DK, NT), kq_bytes(DK, NT),
-              &bars->full[s]);
-    bulk_load(stage + kq_bytes(DK, NT), images + (c * a.vheads + h) * (long long)kImageBytes,
-              kImageBytes, &bars->full[s]);
+    bool ok = it < ST || wait_or_fail(&bars->empty[s], (it / ST - 1) & 1, failed, status);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    char *stage = stages + s * kStage;
+    if (lane == 0) {
+      bar_arrive_tx(&bars->full[s], kq_bytes(DK, NT) + kImageBytes +
+                                        (STAGED ? 64 * cols * (int)sizeof(T) : 0));
+      bulk_load(stage, kq + (c * a.kheads + hk) * (long long)kq_bytes(DK, NT), kq_bytes(DK, NT),
+                &bars->full[s]);
+      bulk_load(stage + kq_bytes(DK, NT), images + (c * a.vheads + h) * (long long)kImageBytes,
+                kImageBytes, &bars->full[s]);
+    }
+    if constexpr (STAGED) {
+      __syncwarp();
+      const long long r0 = (long long)ci * kChunk;
+      const int last = (int)(sp.rows - r0 < kChunk ? sp.rows - r0 : kChunk) - 1;
+      char *dst = stage + kStage - kRows16;
+      for (int r = lane; r < kChunk; r += 32)
+        bulk_load(dst + r * 256, x + (r0 + (r < last ? r : last)) * step, cols * (int)sizeof(T),
+                  &bars->full[s]);
+    }
     issued = it + 1;
   }
   // Given up: no copy may land after the block has gone.
   if (*failed)
     for (int it = issued > ST ? issued - ST : 0; it < issued; ++it)
       bar_wait(&bars->full[it % ST], (it / ST) & 1);
+}
+
+// The storing warp, STAGED: the chunks' rows from shared memory to the
+// contiguous array [sequence][token][head][dv].
+template <typename T>
+__device__ __forceinline__ void scan_store(const DeltaArgs &a, const ScanSpan &sp, bool packed,
+                                           int h, bool backwards, void *out, int c0,
+                                           const char *rows, ScanBars *bars,
+                                           volatile int *failed, int *status, int lane) {
+  const int cols = a.dv - c0 < 128 ? a.dv - c0 : 128;
+  for (int it = 0; it < sp.chunks; ++it) {
+    const int ci = backwards ? sp.chunks - 1 - it : it;
+    const bool ok = wait_or_fail(&bars->put, it & 1, failed, status);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    const long long r0 = (long long)ci * kChunk;
+    const int n = (int)(sp.rows - r0 < kChunk ? sp.rows - r0 : kChunk);
+    T *dst = static_cast<T *>(out) + out_row(a, sp.b, sp.row0 + r0, packed, h) + c0;
+    for (int r = lane; r < n; r += 32)
+      bulk_put(dst + r * (long long)a.vheads * a.dv, rows + r * 256, cols * (int)sizeof(T));
+    bulk_put_read();
+    __syncwarp();
+    if (lane == 0) bar_arrive(&bars->got);
+  }
+  bulk_put_done();
 }
 
 constexpr uint32_t idesc_tokens = mma_desc(128, 64, false, false);
@@ -115,7 +165,7 @@ __device__ __forceinline__ void mma_state(uint32_t d, uint32_t hi, uint32_t lo, 
     const uint32_t ta = term == 1 ? lo : hi, tb = x + (term == 2 ? kPlane : 0);
 #pragma unroll
     for (int k = 0; k < DK / 16; ++k)
-      mma_ts(d, ta + 8 * k, tile_desc(tb + (k >> 2) * 2 * kTile + (k & 3) * 32, 16, 1024),
+      mma_ts(d, ta + 8 * k, tile_desc(tb + (k >> 2) * 2 * kTile + (k & 3) * 32, 16),
              idesc_tokens, term > 0 || k > 0);
   }
 }
@@ -128,7 +178,7 @@ __device__ __forceinline__ void mma_inner(uint32_t d, uint32_t hi, uint32_t lo, 
     const uint32_t ta = term == 1 ? lo : hi, tb = m + (term == 2 ? kTile : 0);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      mma_ts(d, ta + 8 * k, tile_desc(tb + k * 32, 16, 1024), idesc_tokens,
+      mma_ts(d, ta + 8 * k, tile_desc(tb + k * 32, 16), idesc_tokens,
              accumulate || term > 0 || k > 0);
   }
 }
@@ -143,25 +193,31 @@ __device__ __forceinline__ void mma_update(uint32_t d, uint32_t hi, uint32_t lo,
     const uint32_t ta = term == 1 ? lo : hi, tb = x + (term == 2 ? kPlane : 0);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      mma_ts(d, ta + 8 * k, tile_desc(tb + k * 2048, 2 * kTile, 1024), idesc,
+      mma_ts(d, ta + 8 * k, tile_desc(tb + k * 2048, 2 * kTile), idesc,
              accumulate || term > 0 || k > 0);
   }
 }
 
 // 32 values times s to the two parts of a left operand (16 packed columns each).
-__device__ __forceinline__ void put_split(uint32_t hi_at, uint32_t lo_at, const float (&f)[32],
+__device__ __forceinline__ void put_split(uint32_t hi_at, uint32_t lo_at, const float2 (&f)[16],
                                           float s) {
   uint32_t hi[16], lo[16];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) split2(f[2 * j], f[2 * j + 1], s, hi[j], lo[j]);
+  for (int j = 0; j < 16; ++j) split2(f[j], s, hi[j], lo[j]);
   tmem_st16(hi_at, hi);
   tmem_st16(lo_at, lo);
 }
-__device__ __forceinline__ float max32(const float (&f)[32]) {
-  float m = 0.0f;
+__device__ __forceinline__ float max32(float m, const float2 (&f)[16]) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(f[j]));
+  for (int j = 0; j < 16; ++j) m = fmaxf(m, fmaxf(fabsf(f[j].x), fabsf(f[j].y)));
   return m;
+}
+__device__ __forceinline__ float2 pair(const uint32_t (&r)[32], int j) {
+  return make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+}
+// Factors of tokens 2j, 2j + 1 of a thread's half.
+__device__ __forceinline__ float2 gate(const float *g, int j) {
+  return *reinterpret_cast<const float2 *>(g + 2 * j);
 }
 
 // One arrival per warp, after every lane's accesses to tensor memory.
@@ -194,12 +250,12 @@ __device__ __forceinline__ uint32_t scan_begin(ScanBars &bars, uint32_t *slot, v
                                                int tid, int warp) {
   if (warp == 8) tmem_alloc(slot, 512);
   if (tid == 0) {
-    for (int s = 0; s < 3; ++s) {
+    for (int s = 0; s < kScanStages; ++s) {
       bar_init(&bars.full[s], 1);
       bar_init(&bars.empty[s], 1 + kScanMath / 32);
     }
-    for (uint64_t *b : {&bars.p, &bars.n, &bars.e, &bars.s, &bars.o, &bars.done}) bar_init(b, 1);
-    for (uint64_t *b : {&bars.y, &bars.u, &bars.ns, &bars.sb, &bars.of})
+    for (uint64_t *b : {&bars.p, &bars.n, &bars.e, &bars.s, &bars.o, &bars.got, &bars.done}) bar_init(b, 1);
+    for (uint64_t *b : {&bars.y, &bars.u, &bars.ns, &bars.sb, &bars.of, &bars.put})
       bar_init(b, kScanMath / 32);
     *failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -212,7 +268,9 @@ __device__ __forceinline__ uint32_t scan_begin(ScanBars &bars, uint32_t *slot, v
 
 // SAVE leaves for the gradients, per chunk, head and 128 columns of v, the
 // state that entered the chunk (fp32 [DK][128]) and E (fp32 [64][128]).
-template <typename T, int DK, bool SAVE>
+// STAGED: V comes and O goes through shared memory by bulk copies of rows
+// (16-bit types on 16-byte boundaries); else straight from and to HBM.
+template <typename T, int DK, bool SAVE, bool STAGED>
 __global__ void __launch_bounds__(kScanThreads, 1)
 delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const char *images,
                   float *states, float *rows, int *status) {
@@ -221,11 +279,12 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int failed;
   __shared__ float box[2][2][128];
-  constexpr int NT = Terms<T>::value, ST = scan_stages(NT);
+  constexpr int NT = Terms<T>::value, ST = kScanStages;
+  constexpr int kStage = scan_stage_bytes(DK, NT, STAGED);
   // bf16 outputs: their rounding (2^-9) hides what the leading fp16 parts of
   // S, U and M leave out (2^-12) in the products that only the output sees.
   constexpr bool LEAD = std::is_same<T, __nv_bfloat16>::value;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int blocks_v = (a.dv + 127) / 128;
   const int vb = blockIdx.x % blocks_v;
   const int h = (blockIdx.x / blocks_v) % a.vheads;
@@ -234,16 +293,21 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
   const uint32_t tm = scan_begin(bars, &tmem_slot, &failed, tid, warp);
   auto wait = [&](uint64_t *b, uint32_t parity) { return wait_or_fail(b, parity, &failed, status); };
 
-  if (warp == 9) {
-    if (lane == 0)
-      scan_load<DK, NT>(a, sp, h, false, kq, images, stages, &bars, &failed, status);
-    __syncwarp();
+  if (warp == 10) {
+    if constexpr (STAGED)
+      if (a.o)
+        scan_store<T>(a, sp, plan.chunk0 != nullptr, h, false, a.o, vb * 128, stages + ST * kStage,
+                      &bars, &failed, status, lane);
+  } else if (warp == 9) {
+    scan_load<T, DK, STAGED>(a, sp, h, false, kq, images,
+                             head_rows<T>(a.v, a.sv, sp.b, sp.row0, h) + vb * 128, a.sv.tok,
+                             vb * 128, stages, &bars, &failed, status, lane);
   } else if (warp == 8) {
     if (lane == 0) {
       for (int it = 0; it < sp.chunks; ++it) {
         const int s = it % ST;
         const uint32_t ph = it & 1;
-        const uint32_t k = smem_u32(stages + s * scan_stage_bytes(DK, NT));
+        const uint32_t k = smem_u32(stages + s * kStage);
         const uint32_t q = k + kTile, image = k + kq_bytes(DK, NT);
         if (!wait(&bars.full[s], (it / ST) & 1) || !wait(&bars.sb, ph)) break;
         tc_fence_after();
@@ -277,31 +341,41 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
     const uint32_t lb = tm + ((uint32_t)((warp & 3) * 32) << 16);
     const int dvr = vb * 128 + row;
     const bool live = dvr < a.dv;
-    constexpr int SC = DK / 2;               // state columns of a thread
+    constexpr int SC = DK / 2, SP = SC / 32;  // state columns of a thread, in parts of 32
     const long long sat = ((sp.b * a.vheads + h) * a.dk) * (long long)a.dv + dvr;
     RowAgree agree{box, row, half, warp & 3, 0};
     auto saved = [&](long long c) { return ((sp.chunk0 + c) * a.vheads + h) * blocks_v + vb; };
     auto gates_of = [&](int s) {
-      return reinterpret_cast<const float *>(stages + s * scan_stage_bytes(DK, NT) +
-                                             kq_bytes(DK, NT) + 4 * kTile);
+      return reinterpret_cast<const float *>(stages + s * kStage + kq_bytes(DK, NT) + 4 * kTile);
     };
-    float vr[32];
+    // V of a chunk, fetched while the chunk before is worked on: every load is
+    // unconditional (of the last row and column where there is none) and its
+    // value not looked at before it is needed, so all 32 are under way at once.
+    T vr[STAGED ? 1 : 32];
+    const T *vcol = head_rows<T>(a.v, a.sv, sp.b, sp.row0, h) + (live ? dvr : a.dv - 1);
     auto fetch_v = [&](int c) {
-      const long long r0 = sp.row0 + (long long)c * kChunk + half * 32;
-      const long long left = sp.rows - (long long)c * kChunk - half * 32;
-      const T *v = head_rows<T>(a.v, a.sv, sp.b, r0, h) + dvr;
+      if constexpr (!STAGED) {
+        const long long r0 = (long long)c * kChunk;
+        const int last = (int)(sp.rows - r0 < kChunk ? sp.rows - r0 : kChunk) - 1;
+        const T *v = vcol + r0 * a.sv.tok;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) vr[j] = live && j < left ? to_acc(v[j * a.sv.tok]) : 0.0f;
+        for (int j = 0; j < 32; ++j) {
+          const int t = half * 32 + j < last ? half * 32 + j : last;
+          vr[j] = v[(long long)t * a.sv.tok];
+        }
+      }
     };
-    float S[SC / 32][32], inv_s = 1.0f;
+    float2 S[SP][16];
+    float inv_s = 1.0f;
     // The state as the left operand of chunk c's products.
     auto put_state = [&](long long c) {
-      float m = max32(S[0]);
-      if constexpr (SC > 32) m = fmaxf(m, max32(S[SC / 32 - 1]));
+      float m = 0.0f;
+#pragma unroll
+      for (int p = 0; p < SP; ++p) m = max32(m, S[p]);
       const float s = agree.scale(m);
       inv_s = scale_inverse(s);
 #pragma unroll
-      for (int p = 0; p < SC / 32; ++p) {
+      for (int p = 0; p < SP; ++p) {
         const int col = half * SC + p * 32;
         put_split(lb + kColSh + col / 2, lb + kColSl + col / 2, S[p], s);
       }
@@ -310,17 +384,23 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       if constexpr (SAVE) {
         float *dst = states + saved(c) * (DK * 128) + row;
 #pragma unroll
-        for (int p = 0; p < SC / 32; ++p)
+        for (int p = 0; p < SP; ++p)
 #pragma unroll
-          for (int j = 0; j < 32; ++j) dst[(half * SC + p * 32 + j) * 128] = S[p][j];
+          for (int j = 0; j < 16; ++j) {
+            dst[(half * SC + p * 32 + 2 * j) * 128] = S[p][j].x;
+            dst[(half * SC + p * 32 + 2 * j + 1) * 128] = S[p][j].y;
+          }
       }
     };
+    auto initial = [&](int col) {
+      return a.state_in && live && col < a.dk ? a.state_in[sat + (long long)col * a.dv] : 0.0f;
+    };
 #pragma unroll
-    for (int p = 0; p < SC / 32; ++p)
+    for (int p = 0; p < SP; ++p)
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const int col = half * SC + p * 32 + j;
-        S[p][j] = a.state_in && live && col < a.dk ? a.state_in[sat + (long long)col * a.dv] : 0.0f;
+      for (int j = 0; j < 16; ++j) {
+        const int col = half * SC + p * 32 + 2 * j;
+        S[p][j] = make_float2(initial(col), initial(col + 1));
       }
     bool ok = true;
     if (sp.chunks > 0) {
@@ -332,15 +412,22 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       const uint32_t ph = it & 1;
       const float *gates = gates_of(s) + half * 32;
       uint32_t r[32];
-      float f[32];
+      float2 f[16];
       // Y = V^T - P gamma
       if (!(ok = wait(&bars.full[s], (it / ST) & 1) && wait(&bars.p, ph))) break;
       tc_fence_after();
       tmem_ld32(lb + kColP + half * 32, r);
       tmem_wait_ld();
+      const T *vs = reinterpret_cast<const T *>(stages + s * kStage + kStage - kRows16) +
+                    half * 32 * 128 + row;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) f[j] = vr[j] - gates[j] * inv_s * __uint_as_float(r[j]);
-      const float ys = agree.scale(max32(f));
+      for (int j = 0; j < 16; ++j) {
+        const float2 v = STAGED ? make_float2(to_acc(vs[2 * j * 128]), to_acc(vs[(2 * j + 1) * 128]))
+                                : make_float2(to_acc(vr[STAGED ? 0 : 2 * j]),
+                                              to_acc(vr[STAGED ? 0 : 2 * j + 1]));
+        f[j] = fma2(mul2(gate(gates, j), both(inv_s)), pair(r, j), v);
+      }
+      const float ys = agree.scale(max32(0.0f, f));
       put_split(lb + kColYh + half * 16, lb + kColYl + half * 16, f, ys);
       tmem_wait_st();
       warp_arrive(&bars.y, lane);
@@ -350,24 +437,21 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       tmem_ld32(lb + kColP + half * 32, r);
       tmem_wait_ld();
       const float inv_y = scale_inverse(ys);
-#pragma unroll
-      for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(r[j]) * (gates[5 * 64 + j] * inv_y);
       if constexpr (SAVE) {
         float *dst = rows + saved(it) * (64 * 128) + half * 32 * 128 + row;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) dst[j * 128] = f[j];
+        for (int j = 0; j < 32; ++j)
+          dst[j * 128] = __uint_as_float(r[j]) * (gates[5 * 64 + j] * inv_y);
       }
-      float um = 0.0f;
+      float2 w[16];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        f[j] *= gates[2 * 64 + j];
-        um = fmaxf(um, fmaxf(fabsf(f[j]), fabsf(f[j] * gates[64 + j])));
+      for (int j = 0; j < 16; ++j) {
+        f[j] = mul2(pair(r, j), mul2(gate(gates + 2 * 64, j), both(inv_y)));
+        w[j] = mul2(f[j], gate(gates + 64, j));
       }
-      const float us = agree.scale(um), inv_u = scale_inverse(us);
+      const float us = agree.scale(max32(max32(0.0f, f), w)), inv_u = scale_inverse(us);
       put_split(lb + kColYh + half * 16, lb + kColYl + half * 16, f, us);
-#pragma unroll
-      for (int j = 0; j < 32; ++j) f[j] *= gates[64 + j];
-      put_split(lb + kColWh + half * 16, lb + kColWl + half * 16, f, us);
+      put_split(lb + kColWh + half * 16, lb + kColWl + half * 16, w, us);
       tmem_wait_st();
       warp_arrive(&bars.u, lane);
       // N in units of U M^T, the start of O
@@ -377,8 +461,11 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       tmem_wait_ld();
       const float ratio = inv_s * us;
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        r[j] = __float_as_uint(__uint_as_float(r[j]) * (gates[3 * 64 + j] * ratio));
+      for (int j = 0; j < 16; ++j) {
+        const float2 n = mul2(pair(r, j), mul2(gate(gates + 3 * 64, j), both(ratio)));
+        r[2 * j] = __float_as_uint(n.x);
+        r[2 * j + 1] = __float_as_uint(n.y);
+      }
       tmem_st32(lb + kColN + half * 32, r);
       tmem_wait_st();
       warp_arrive(&bars.ns, lane);
@@ -389,20 +476,31 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       if (!(ok = wait(&bars.s, ph))) break;
       tc_fence_after();
 #pragma unroll
-      for (int p = 0; p < SC / 32; ++p) {
+      for (int p = 0; p < SP; ++p) {
         tmem_ld32(lb + kColD + half * SC + p * 32, r);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) S[p][j] = fmaf(S[p][j], Gamma, __uint_as_float(r[j]) * inv_u);
+        for (int j = 0; j < 16; ++j)
+          S[p][j] = fma2(S[p][j], both(Gamma), mul2(pair(r, j), both(inv_u)));
       }
       if (more) put_state(it + 1);
       // The output
       if (!(ok = wait(&bars.o, ph))) break;
+      if (STAGED && a.o && it > 0 && !(ok = wait(&bars.got, ph ^ 1))) break;
       tc_fence_after();
       tmem_ld32(lb + kColN + half * 32, r);
       tmem_wait_ld();
       warp_arrive(&bars.of, lane);
-      if (a.o && live) {
+      if (STAGED && a.o) {
+        T *os = reinterpret_cast<T *>(stages + ST * kStage) + half * 32 * 128 + row;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float2 o = mul2(pair(r, j), mul2(gate(gates + 4 * 64, j), both(inv_u)));
+          os[2 * j * 128] = from_acc<T>(o.x);
+          os[(2 * j + 1) * 128] = from_acc<T>(o.y);
+        }
+        fence_smem_to_async();
+      } else if (a.o && live) {
         const long long r0 = sp.row0 + (long long)it * kChunk + half * 32;
         const long long left = sp.rows - (long long)it * kChunk - half * 32;
         T *o = static_cast<T *>(a.o) + out_row(a, sp.b, r0, plan.chunk0 != nullptr, h) + dvr;
@@ -413,15 +511,19 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
             o[j * step] = from_acc<T>(__uint_as_float(r[j]) * (gates[4 * 64 + j] * inv_u));
       }
       __syncwarp();
-      if (lane == 0) bar_arrive(&bars.empty[s]);  // the gates were read
+      if (lane == 0) {
+        bar_arrive(&bars.empty[s]);  // the gates and V were read
+        if (STAGED) bar_arrive(&bars.put);
+      }
     }
     if (ok && a.state_out && live) {
 #pragma unroll
-      for (int p = 0; p < SC / 32; ++p)
+      for (int p = 0; p < SP; ++p)
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const int col = half * SC + p * 32 + j;
-          if (col < a.dk) a.state_out[sat + (long long)col * a.dv] = S[p][j];
+        for (int j = 0; j < 16; ++j) {
+          const int col = half * SC + p * 32 + 2 * j;
+          if (col < a.dk) a.state_out[sat + (long long)col * a.dv] = S[p][j].x;
+          if (col + 1 < a.dk) a.state_out[sat + (long long)(col + 1) * a.dv] = S[p][j].y;
         }
     }
   }

@@ -32,34 +32,27 @@ __device__ __forceinline__ void bar_arrive_tx(uint64_t *bar, uint32_t bytes) {
                "r"(bytes)
                : "memory");
 }
-// Bounded wait for the phase of the given parity: false if it did not
-// complete within the polls.
+// Whether the phase of the given parity has completed (may wait a little).
+__device__ __forceinline__ bool bar_poll(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// Bounded wait: false if the phase did not complete within the polls.
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
-  for (uint32_t it = 0; it < (1u << 22); ++it) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (done) return true;
-  }
+  for (uint32_t it = 0; it < (1u << 22); ++it)
+    if (bar_poll(bar, parity)) return true;
   return false;
 }
 
 // ---- copies into shared memory -------------------------------------------------
 
-// 16 bytes global -> shared; `bytes` < 16 fills the rest with zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 // Contiguous bulk copy global -> shared (16-byte aligned, whole 16 bytes),
 // counted by the barrier.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes,
@@ -70,7 +63,23 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
       "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
-// Makes this thread's writes to shared memory visible to the tensor cores.
+// Contiguous bulk copy shared -> global, in the thread's current bulk group.
+__device__ __forceinline__ void bulk_put(void *dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                   reinterpret_cast<uint64_t>(dst)),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+// Ends the group and waits until its copies have read shared memory, or are
+// complete.
+__device__ __forceinline__ void bulk_put_read() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_put_done() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+}
+// Makes this thread's writes to shared memory visible to the tensor cores
+// and to bulk copies.
 __device__ __forceinline__ void fence_smem_to_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -139,36 +148,38 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
 
 // ---- products --------------------------------------------------------------------
 
-// Descriptor of a swizzled operand tile at shared address `addr`.
-// K-major (rows along the product's outer index): `group` = bytes between
-// groups of 8 rows; `block` is not used.  MN-major (rows along the summed
-// index): `group` = bytes between groups of 8 rows, `block` = bytes between
-// tiles of 64 outer indexes.
-__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t block, uint32_t group) {
-  return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(block >> 4) << 16) |
-         ((uint64_t)(group >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Swizzled operand tile at shared address `addr`, as the low word of its
+// descriptor.  K-major (rows along the product's outer index): `block` is
+// not used.  MN-major (rows along the summed index): `block` = bytes between
+// tiles of 64 outer indexes.  Groups of 8 rows are 1024 bytes apart.
+__device__ __forceinline__ uint32_t tile_desc(uint32_t addr, uint32_t block) {
+  return (addr >> 4) | ((block >> 4) << 16);
 }
+// The high word: 1024 bytes between groups of 8 rows, 128-byte swizzle.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 // Instruction descriptor: fp16 x fp16 -> fp32, M x N, A and B K-major or MN-major.
 __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool a_mn, bool b_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) |
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 // D (TMEM) (+)= A (TMEM, packed pairs) B (shared), 16 summed indexes.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "n"(kDescHigh)
       : "memory");
 }
 // D (TMEM) (+)= A (shared) B (shared).
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "n"(kDescHigh)
       : "memory");
 }
 // The barrier gets one arrival when every product issued so far by this
@@ -190,14 +201,32 @@ __device__ __forceinline__ float row_scale(float m) {
 __device__ __forceinline__ float scale_inverse(float s) {
   return __uint_as_float(0x7f000000u - __float_as_uint(s));
 }
+// Two fp32 operations per instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // x s = hi + lo, two values packed per register, the first in the low half.
 // With the row's largest |x s| in [1, 2) the sum is exact to 2^-23 of each
 // value or 2^-25 of the largest, whichever is more.
-__device__ __forceinline__ void split2(float x0, float x1, float s, uint32_t &hi, uint32_t &lo) {
-  const float a = x0 * s, b = x1 * s;
-  const __half2 h = __floats2half2_rn(a, b);
-  const float2 f = __half22float2(h);
-  const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+__device__ __forceinline__ void split2(float2 x, float s, uint32_t &hi, uint32_t &lo) {
+  const float2 a = mul2(x, both(s));
+  const __half2 h = __float22half2_rn(a);
+  const __half2 l = __float22half2_rn(fma2(__half22float2(h), both(-1.0f), a));
   hi = *reinterpret_cast<const uint32_t *>(&h);
   lo = *reinterpret_cast<const uint32_t *>(&l);
 }
