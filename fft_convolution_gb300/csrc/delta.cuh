@@ -52,10 +52,11 @@ constexpr int kTile = 64 * 128;
 // inputs: first all leading, then all trailing parts.
 __host__ __device__ constexpr int kq_bytes(int dk, int terms) { return terms * 2 * (dk / 64) * kTile; }
 // Per value head two 64 x 64 matrices (leading and trailing tile of each),
-// rows scaled, six factors per token, and the chunk's decay Gamma.
+// rows scaled, six factors per token, and eight numbers of the chunk: its decay
+// Gamma and bounds (delta_prep.cuh).
 constexpr int kGates = 6;
-constexpr int kGammaAt = kGates * 64;  // in floats, after the tiles
-constexpr int kImageBytes = 4 * kTile + kGates * 64 * 4 + 16;
+constexpr int kChunkAt = kGates * 64;  // in floats, after the tiles
+constexpr int kImageBytes = 4 * kTile + kGates * 64 * 4 + 32;
 
 // Where the chunks of packed sequences lie (device arrays of batch + 1
 // entries, both null for sequences of one length).
@@ -174,10 +175,10 @@ template <int W> __device__ __forceinline__ float lane_max(float m) {
 }
 
 __device__ __forceinline__ void split8(const float (&f)[8], float s, uint4 &hi, uint4 &lo) {
-  split2(make_float2(f[0], f[1]), s, hi.x, lo.x);
-  split2(make_float2(f[2], f[3]), s, hi.y, lo.y);
-  split2(make_float2(f[4], f[5]), s, hi.z, lo.z);
-  split2(make_float2(f[6], f[7]), s, hi.w, lo.w);
+  split2(mul2(make_float2(f[0], f[1]), both(s)), hi.x, lo.x);
+  split2(mul2(make_float2(f[2], f[3]), both(s)), hi.y, lo.y);
+  split2(mul2(make_float2(f[4], f[5]), both(s)), hi.z, lo.z);
+  split2(mul2(make_float2(f[6], f[7]), both(s)), hi.w, lo.w);
 }
 // Byte offset of the 16-byte piece c (8 columns) of row r in a row of tiles
 // `tile` bytes apart.

@@ -20,9 +20,21 @@
 //   4: scale 2^em    5: 2^et
 // BACK image: (I + beta A)^-T and M^T; per token
 //   0: Gamma/gamma 2^ek   1: scale 2^em   2: 2^et   3: beta
-//   4: gamma beta 2^ek    5: scale gamma 2^eq
+//   4: -gamma beta 2^ek   5: scale gamma 2^eq
 // where 2^-e is the scale of a token's row of K (ek), Q (eq), of the inverse
-// (et) and of M (em).  After the factors: Gamma, the decay of the whole chunk.
+// (et) and of M (em).
+//
+// Of the chunk: 0: Gamma, then bounds from which the scans choose the scales
+// of what they compute without looking at it first.  With |S| the largest
+// value of the state in a column of v, and K's scaled rows below 2:
+//   forward  |Y| <= |V| + b1 |S|,  |U| <= b2 |Y|,  |W| <= b3 |Y|
+//            b1 = 2 DK max gamma 2^ek,  b2 = max beta r,
+//            b3 = max Gamma/gamma 2^ek beta r,  r = row sums of |inverse|
+//   BACK     |dU| <= b1 |dS| + b2 |dO|,  |F| <= b3 |dU|,  |gamma beta F 2^ek| <= b4 |F|,
+//            |scale gamma dO 2^eq| <= b5 |dO|
+//            b1 = 2 DK max Gamma/gamma 2^ek,  b2 = max scale (row sums of |M^T|),
+//            b3 = max r,  b4 = max gamma beta 2^ek,  b5 = max scale gamma 2^eq
+// Rounding in fp32 would leave errors of 2^-24 of these same bounds.
 #pragma once
 
 #include "delta.cuh"
@@ -32,29 +44,43 @@ namespace fftgb {
 constexpr int kPrepThreads = 128;
 constexpr int kPitch = 68;  // floats per row of a 64 x 64 fp32 matrix (rows stay 16-byte aligned)
 
+// The tiles, and in their place (after the product) the two fp32 matrices.
 template <typename T, int DK> constexpr size_t prep_smem() {
-  return 1024 + (size_t)kq_bytes(DK, Terms<T>::value) + 2 * 64 * kPitch * 4;
+  constexpr int tiles = kq_bytes(DK, Terms<T>::value), fp32 = 2 * 64 * kPitch * 4;
+  return 1024 + (size_t)(tiles > fp32 ? tiles : fp32);
 }
 
-// 64 x 64 fp32 matrix (or its transpose) to the leading and trailing tile,
-// rows scaled; the inverse scales go to `inv`.
+// 64 x 64 lower triangular fp32 matrix (what lies above its diagonal is not
+// read), or its transpose, to the leading and trailing tile, rows scaled; the
+// rows' inverse scales go to `inv`, the sums of their absolute values to `sum`.
 template <bool TRANS>
-__device__ __forceinline__ void write_image(const float *m, char *dst, float *inv, int tid) {
+__device__ __forceinline__ void write_image(const float *m, char *dst, float *inv, float *sum,
+                                            int tid) {
 #pragma unroll
   for (int i = tid; i < 64 * 8; i += kPrepThreads) {
     const int r = i >> 3, c = i & 7;
     float f[8];
     if constexpr (TRANS) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = m[(c * 8 + k) * kPitch + r];
+      for (int k = 0; k < 8; ++k) f[k] = c * 8 + k >= r ? m[(c * 8 + k) * kPitch + r] : 0.0f;
     } else {
       const float4 x = *reinterpret_cast<const float4 *>(m + r * kPitch + c * 8);
       const float4 y = *reinterpret_cast<const float4 *>(m + r * kPitch + c * 8 + 4);
       f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
       f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = c * 8 + k <= r ? f[k] : 0.0f;
     }
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t += fabsf(f[k]);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     const float s = row_scale(lane_max<8>(max8(f)));
-    if (c == 0) inv[r] = scale_inverse(s);
+    if (c == 0) {
+      inv[r] = scale_inverse(s);
+      sum[r] = t;
+    }
     uint4 hi, lo;
     split8(f, s, hi, lo);
     const int at = piece_at(r, c, 0);
@@ -63,8 +89,8 @@ __device__ __forceinline__ void write_image(const float *m, char *dst, float *in
   }
 }
 
-// G_i of the 64 tokens, as the sum of two floats: differences of running
-// sums of up to 64 * 128 keep fp32 accuracy.
+// G_i of the 64 tokens times log2(e), as the sum of two floats: differences of
+// running sums of up to 64 * 128 keep fp32 accuracy.
 __device__ __forceinline__ void running_decay(const float *g, long long step, int n, int tid,
                                               double *carry, float2 *out) {
   float x = 0.0f;
@@ -83,12 +109,13 @@ __device__ __forceinline__ void running_decay(const float *g, long long step, in
   __syncthreads();
   if (tid < 64) {
     if (tid >= 32) s += *carry;
+    s *= 1.4426950408889634;
     const float h = (float)s;
     out[tid] = make_float2(h, (float)(s - (double)h));
   }
 }
 __device__ __forceinline__ float decay_between(float2 i, float2 j) {
-  return expf((i.x - j.x) + (i.y - j.y));
+  return exp2f((i.x - j.x) + (i.y - j.y));
 }
 
 // Rows 0 .. 63 of K or Q into its tiles in shared memory and in the image;
@@ -118,8 +145,46 @@ __device__ __forceinline__ void load_rows(const T *src, long long stride, int n,
   }
 }
 
+// Z = P X for the lower triangular X at (lo, lo), or -P X with X at (hi, lo):
+// `ROWS` rows from `row` of column `col`, SIZE summed indexes, P at (pr, pc).
+template <int SIZE, int ROWS>
+__device__ __forceinline__ void block_product(const float *p, const float *x, float (&z)[ROWS]) {
+#pragma unroll
+  for (int o = 0; o < ROWS; ++o) z[o] = 0.0f;
+#pragma unroll 2
+  for (int k = 0; k < SIZE; k += 4) {
+    float xs[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) xs[e] = x[(k + e) * kPitch];
+#pragma unroll
+    for (int o = 0; o < ROWS; ++o) {
+      const float4 l = *reinterpret_cast<const float4 *>(p + o * kPitch + k);
+      z[o] = fmaf(l.x, xs[0], fmaf(l.y, xs[1], fmaf(l.z, xs[2], fmaf(l.w, xs[3], z[o]))));
+    }
+  }
+}
+// T_21 = -T_22 (L_21 T_11) for the pairs of SIZE x SIZE diagonal blocks.
+template <int SIZE> __device__ __forceinline__ void join_blocks(const float *L, float *X, int tid) {
+  constexpr int PAIRS = 32 / SIZE, PER = kPrepThreads / PAIRS, ROWS = SIZE * SIZE / PER;
+  const int pr = tid / PER, t = tid % PER;
+  const int lo = pr * 2 * SIZE, hi = lo + SIZE;
+  const int col = t % SIZE, rb = (t / SIZE) * ROWS;
+  float z[ROWS];
+  block_product<SIZE, ROWS>(L + (hi + rb) * kPitch + lo, X + lo * kPitch + lo + col, z);
+  __syncthreads();
+  float *out = X + (hi + rb) * kPitch + lo + col;
+#pragma unroll
+  for (int o = 0; o < ROWS; ++o) out[o * kPitch] = z[o];
+  __syncthreads();
+  block_product<SIZE, ROWS>(X + (hi + rb) * kPitch + hi, X + hi * kPitch + lo + col, z);
+  __syncthreads();
+#pragma unroll
+  for (int o = 0; o < ROWS; ++o) out[o * kPitch] = -z[o];
+  __syncthreads();
+}
+
 template <typename T, int DK, bool BACK>
-__global__ void __launch_bounds__(kPrepThreads)
+__global__ void __launch_bounds__(kPrepThreads, 5)
 delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *images, int *status) {
   extern __shared__ char smem_raw[];
   __shared__ uint64_t bar;
@@ -127,7 +192,8 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
   __shared__ volatile int failed;
   __shared__ double carry;
   __shared__ float2 G[64];
-  __shared__ float beta_s[64], inv_kq[2 * 64], inv_t[64], inv_m[64];
+  __shared__ float beta_s[64], inv_kq[2 * 64], inv_t[64], inv_m[64], sum_t[64], sum_m[64];
+  __shared__ float most[2][5];
   constexpr int NT = Terms<T>::value;
   constexpr uint32_t kPlane = 2 * (DK / 64) * kTile;  // [K; Q], one term
 
@@ -139,7 +205,7 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
 
   // Tiles: 128 rows (K above Q) of 64 columns, kTile * 2 bytes each.
   char *tiles = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  float *L = reinterpret_cast<float *>(tiles + NT * kPlane);
+  float *L = reinterpret_cast<float *>(tiles);
   float *X = L + 64 * kPitch;
   const uint32_t t0 = smem_u32(tiles);
   char *kqi = kq + (ci * a.kheads + hk) * (long long)kq_bytes(DK, NT);
@@ -158,8 +224,8 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t acc = tmem_slot;
-  if (tid == 0) {
+  const uint32_t acc = __shfl_sync(0xffffffffu, tmem_slot, 0);
+  if (warp == 0 && elect_one()) {
     constexpr uint32_t idesc = mma_desc(128, 64, false, false);
 #pragma unroll
     for (int term = 0; term < (NT == 1 ? 1 : 3); ++term) {
@@ -168,12 +234,12 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
 #pragma unroll
       for (int k = 0; k < DK / 16; ++k) {
         const uint32_t at = (k >> 2) * 2 * kTile + (k & 3) * 32;
-        mma_ss(acc, tile_desc(ta + at, 16), tile_desc(tb + at, 16), idesc,
-               term > 0 || k > 0);
+        mma_ss(acc, tile_desc(ta + at, 16), tile_desc(tb + at, 16), idesc, term > 0 || k > 0);
       }
     }
     mma_commit(&bar);
   }
+  __syncwarp();
   const bool ok = wait_or_fail(&bar, 0, &failed, status);
   if (__syncthreads_and(ok)) {
     tc_fence_after();
@@ -185,8 +251,9 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
       running_decay(g, a.sg.tok, c.n, tid, &carry, G);
       if (tid < 64) beta_s[tid] = tid < c.n ? beta[tid * a.sb.tok] : 0.0f;
       __syncthreads();
-      // Row i of A (threads 0 .. 63, from K K^T) or of M (64 .. 127).  Row i
-      // of the matrix to invert is A_ij beta_j, or beta_i A_ij (BACK).
+      // Row i of A (threads 0 .. 63, from K K^T) or of M (64 .. 127), up to
+      // its diagonal.  Row i of the matrix to invert is A_ij beta_j, or beta_i
+      // A_ij (BACK).
       const int i = tid & 63;
       const float2 gi = G[i];
       const bool is_m = tid >= 64;
@@ -194,97 +261,83 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
       float *row = (is_m ? X : L) + i * kPitch;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
+        if (half == 1 && (warp & 1) == 0) break;  // rows 0 .. 31 end before column 32
         uint32_t r[32];
-        tmem_ld32(acc + ((uint32_t)(warp * 32) << 16) + half * 32, r);
+        tmem_ld(acc + ((uint32_t)(warp * 32) << 16) + half * 32, r);
         tmem_wait_ld();
 #pragma unroll
         for (int jj = 0; jj < 32; ++jj) {
           const int j = half * 32 + jj;
-          float x = 0.0f;
-          if (is_m ? j <= i : j < i) {
-            x = decay_between(gi, G[j]) * (__uint_as_float(r[jj]) * fi * inv_kq[j]);
-            if (!BACK && !is_m) x *= beta_s[j];
-          }
+          float f = fi * inv_kq[j];
+          if (!BACK && !is_m) f *= beta_s[j];
+          // (above the diagonal the exponent would be positive)
+          const float x = decay_between(gi, j <= i ? G[j] : gi) * (__uint_as_float(r[jj]) * f);
           row[j] = x;
         }
       }
       __syncthreads();
-      write_image<BACK>(X, image + 2 * kTile, inv_m, tid);
+      write_image<BACK>(X, image + 2 * kTile, inv_m, sum_m, tid);
       __syncthreads();
       // Diagonal blocks: column `col` of the inverse of block `warp`, by
       // substitution; both halves of the warp do the same columns.
       {
         const int col = lane & 15, r0 = warp * 16;
+        const float *l = L + r0 * kPitch + r0;
         float x[16];
 #pragma unroll
         for (int m = 0; m < 16; ++m) {
           float s = m == col ? 1.0f : 0.0f;
 #pragma unroll
-          for (int p = 0; p < m; ++p) s = fmaf(-L[(r0 + m) * kPitch + r0 + p], x[p], s);
+          for (int p = 0; p < m; p += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(l + m * kPitch + p);
+            s = fmaf(-v.x, x[p], s);
+            if (p + 1 < m) s = fmaf(-v.y, x[p + 1], s);
+            if (p + 2 < m) s = fmaf(-v.z, x[p + 2], s);
+            if (p + 3 < m) s = fmaf(-v.w, x[p + 3], s);
+          }
           x[m] = s;
         }
-        if (lane < 16) {
 #pragma unroll
-          for (int m = 0; m < 16; ++m) X[(r0 + m) * kPitch + r0 + col] = x[m];
-        }
-        // zeros above the diagonal blocks
-        for (int e = lane; e < 16 * (48 - r0); e += 32) {
-          const int w = 48 - r0;
-          X[(r0 + e / w) * kPitch + r0 + 16 + e % w] = 0.0f;
+        for (int m = 0; m < 16; ++m) {
+          // the other half of the warp: zeros right of the first of two blocks
+          if (lane < 16) X[(r0 + m) * kPitch + r0 + col] = x[m];
+          else if ((warp & 1) == 0) X[(r0 + m) * kPitch + r0 + 16 + col] = 0.0f;
         }
       }
       __syncthreads();
-      // Below the diagonal: sizes 16 and 32.  First Z = L_21 T_11 (kept where
-      // T_21 will be), then T_21 = -T_22 Z.
-#pragma unroll
-      for (int size = 16; size <= 32; size *= 2) {
-        const int pairs = 32 / size;              // 2, 1
-        const int per = kPrepThreads / pairs;     // threads of a pair
-        const int pr = tid / per, t = tid % per;
-        const int lo = pr * 2 * size, hi = lo + size;
-        const int outs = size * size / per;       // 4, 8 consecutive rows of one column
-        const int col = t % size, rb = (t / size) * outs;
-        float z[8];
-#pragma unroll
-        for (int o = 0; o < 8; ++o) z[o] = 0.0f;
-        for (int p = 0; p < size; ++p) {
-          const float x = X[(lo + p) * kPitch + lo + col];
-#pragma unroll
-          for (int o = 0; o < 8; ++o)
-            if (o < outs) z[o] = fmaf(L[(hi + rb + o) * kPitch + lo + p], x, z[o]);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int o = 0; o < 8; ++o)
-          if (o < outs) X[(hi + rb + o) * kPitch + lo + col] = z[o];
-        __syncthreads();
-#pragma unroll
-        for (int o = 0; o < 8; ++o) z[o] = 0.0f;
-        for (int p = 0; p < size; ++p) {
-          const float x = X[(hi + p) * kPitch + lo + col];
-#pragma unroll
-          for (int o = 0; o < 8; ++o)
-            if (o < outs) z[o] = fmaf(-X[(hi + rb + o) * kPitch + hi + p], x, z[o]);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int o = 0; o < 8; ++o)
-          if (o < outs) X[(hi + rb + o) * kPitch + lo + col] = z[o];
-        __syncthreads();
-      }
-      write_image<BACK>(X, image, inv_t, tid);
+      join_blocks<16>(L, X, tid);
+      join_blocks<32>(L, X, tid);
+      write_image<BACK>(X, image, inv_t, sum_t, tid);
       __syncthreads();
       if (tid < 64) {
-        float *gates = reinterpret_cast<float *>(image + 4 * kTile) + tid;
+        float *gates = reinterpret_cast<float *>(image + 4 * kTile);
         const float ek = inv_kq[tid], eq = inv_kq[64 + tid], em = inv_m[tid], et = inv_t[tid];
-        const float gam = expf(G[tid].x), dec = decay_between(G[63], G[tid]), bt = beta_s[tid];
+        const float2 zero = make_float2(0.0f, 0.0f);
+        const float gam = decay_between(G[tid], zero), dec = decay_between(G[63], G[tid]);
+        const float bt = beta_s[tid];
         const float ga[kGates] = {-gam * ek, dec * ek, bt * et, gam * (eq / em), a.scale * em, et};
-        const float gb[kGates] = {dec * ek, a.scale * em, et, bt, gam * bt * ek, a.scale * gam * eq};
+        const float gb[kGates] = {dec * ek, a.scale * em, et, bt, -gam * bt * ek,
+                                  a.scale * gam * eq};
+        const float ba = fabsf(bt) * sum_t[tid], sc = fabsf(a.scale);
+        float b[5];
+        b[0] = 2.0f * DK * (BACK ? dec : gam) * ek;
+        b[1] = BACK ? sc * sum_m[tid] : ba;
+        b[2] = BACK ? sum_t[tid] : ba * dec * ek;
+        b[3] = gam * fabsf(bt) * ek;
+        b[4] = sc * gam * eq;
 #pragma unroll
-        for (int k = 0; k < kGates; ++k) gates[k * 64] = BACK ? gb[k] : ga[k];
-        if (tid == 63) gates[(kGates - 1) * 64 + 1] = gam;  // Gamma, after the last factor
+        for (int k = 0; k < kGates; ++k) gates[k * 64 + tid] = BACK ? gb[k] : ga[k];
+#pragma unroll
+        for (int k = 0; k < 5; ++k) {
+          b[k] = lane_max<32>(b[k]);
+          if (lane == 0) most[warp][k] = b[k];
+        }
+        if (tid == 63) gates[kChunkAt] = gam;
       }
       __syncthreads();
+      if (tid < 5)
+        reinterpret_cast<float *>(image + 4 * kTile)[kChunkAt + 1 + tid] =
+            fmaxf(most[0][tid], most[1][tid]);
     }
     tc_fence_before();
   }

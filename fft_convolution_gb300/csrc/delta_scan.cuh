@@ -7,15 +7,20 @@
 //   P = S^T K^T, N = S^T Q^T;  Y = V^T - P gamma;  E = Y T^T (T the inverse);
 //   U = E beta;  W = U Gamma / gamma;  S^T <- S^T Gamma + W K;
 //   O^T = scale (N gamma + U M^T).
-// Two threads own a column of v, each with half of the tokens and half of
+// Four threads own a column of v, each with a quarter of the tokens and of
 // the state's columns: the state itself stays in their registers in fp32,
-// and what they hand to the tensor cores (S, Y, U, W) is scaled by the power
-// of two of the column's largest value, which they agree on through shared
-// memory, and split into two fp16 values.  Only P -> Y -> E -> U -> S is a
-// chain; N, U M^T, the output and all loads run beside it.
+// and what they hand to the tensor cores (S, Y, U, W) is scaled by a power of
+// two and split into two fp16 values.  Only P -> Y -> E -> U -> S is a chain;
+// N, U M^T, the output and all loads run beside it.  So the scales do not come
+// from the values (finding the largest of a column takes the four threads a
+// barrier at each step of the chain) but from bounds on them: from the largest
+// values of V and of the state, which are found beside the chain, and the
+// chunk's bounds.  The scale brings the bound to 2^14; values down to 2^-16
+// of the bound keep all their digits.
 //
-// Roles: 8 warps of arithmetic, one thread that issues the products, one
-// that fetches the chunks' images ahead (bulk copies, 3 or 2 stages).
+// Roles: 16 warps of arithmetic (two per scheduler left its issue slots 60%
+// empty), one thread that issues the products, a warp that fetches the chunks'
+// images ahead and one that stores (bulk copies).
 //
 // Tensor memory (512 columns):
 //   W K (fp32)       0 .. DK - 1
@@ -28,8 +33,10 @@
 
 namespace fftgb {
 
-constexpr int kScanThreads = 11 * 32;
-constexpr int kScanMath = 256;
+constexpr int kScanWarps = 16;                       // of arithmetic
+constexpr int kScanGroups = kScanWarps / 4;          // threads that share a column of v
+constexpr int kScanTok = 64 / kScanGroups;           // tokens of each
+constexpr int kScanThreads = (kScanWarps + 3) * 32;
 constexpr int kScanStages = 2;
 
 // 64 tokens x 128 columns of a 16-bit type.
@@ -198,24 +205,23 @@ __device__ __forceinline__ void mma_update(uint32_t d, uint32_t hi, uint32_t lo,
   }
 }
 
-// 32 values times s to the two parts of a left operand (16 packed columns each).
-__device__ __forceinline__ void put_split(uint32_t hi_at, uint32_t lo_at, const float2 (&f)[16],
-                                          float s) {
-  uint32_t hi[16], lo[16];
+// 16 scaled values to the two parts of a left operand (8 packed columns each).
+__device__ __forceinline__ void put_split(uint32_t hi_at, uint32_t lo_at, const float2 (&f)[8]) {
+  uint32_t hi[8], lo[8];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) split2(f[j], s, hi[j], lo[j]);
-  tmem_st16(hi_at, hi);
-  tmem_st16(lo_at, lo);
+  for (int j = 0; j < 8; ++j) split2(f[j], hi[j], lo[j]);
+  tmem_st(hi_at, hi);
+  tmem_st(lo_at, lo);
 }
-__device__ __forceinline__ float max32(float m, const float2 (&f)[16]) {
+__device__ __forceinline__ float max16(float m, const float2 (&f)[8]) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) m = fmaxf(m, fmaxf(fabsf(f[j].x), fabsf(f[j].y)));
+  for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(f[j].x), fabsf(f[j].y)));
   return m;
 }
-__device__ __forceinline__ float2 pair(const uint32_t (&r)[32], int j) {
+__device__ __forceinline__ float2 pair(const uint32_t (&r)[16], int j) {
   return make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
 }
-// Factors of tokens 2j, 2j + 1 of a thread's half.
+// Factors of tokens 2j, 2j + 1 of a thread's.
 __device__ __forceinline__ float2 gate(const float *g, int j) {
   return *reinterpret_cast<const float2 *>(g + 2 * j);
 }
@@ -227,18 +233,23 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
   if (lane == 0) bar_arrive(bar);
 }
 
-// The scale that the two threads of a column of v agree on: each brings the
-// largest value of its half.  The two warps meet at a barrier of their own,
-// the two halves of `box` alternate, so one barrier per agreement is enough.
+// The largest of what the four threads of a column of v bring, twice.  Their
+// four warps meet at a barrier of their own; the two halves of `box` alternate,
+// so one barrier per agreement is enough.
 struct RowAgree {
-  float (*box)[2][128];
-  int row, half, pair, turn;
-  __device__ __forceinline__ float scale(float m) {
-    box[turn][half][row] = m;
-    asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
-    m = fmaxf(m, box[turn][half ^ 1][row]);
+  float2 (*box)[kScanGroups][128];
+  int row, group, quarter, turn;
+  __device__ __forceinline__ float2 largest(float a, float b) {
+    box[turn][group][row] = make_float2(a, b);
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(kScanGroups * 32) : "memory");
+#pragma unroll
+    for (int g = 0; g < kScanGroups; ++g) {
+      const float2 o = box[turn][g][row];
+      a = fmaxf(a, o.x);
+      b = fmaxf(b, o.y);
+    }
     turn ^= 1;
-    return row_scale(m);
+    return make_float2(a, b);
   }
 };
 
@@ -248,22 +259,22 @@ constexpr uint32_t kColD = 0, kColSh = 128, kColSl = 192, kColP = 256, kColYh = 
 // Barriers and tensor memory of a scan: returns the base column.
 __device__ __forceinline__ uint32_t scan_begin(ScanBars &bars, uint32_t *slot, volatile int *failed,
                                                int tid, int warp) {
-  if (warp == 8) tmem_alloc(slot, 512);
+  if (warp == kScanWarps) tmem_alloc(slot, 512);
   if (tid == 0) {
     for (int s = 0; s < kScanStages; ++s) {
       bar_init(&bars.full[s], 1);
-      bar_init(&bars.empty[s], 1 + kScanMath / 32);
+      bar_init(&bars.empty[s], 1 + kScanWarps);
     }
     for (uint64_t *b : {&bars.p, &bars.n, &bars.e, &bars.s, &bars.o, &bars.got, &bars.done}) bar_init(b, 1);
     for (uint64_t *b : {&bars.y, &bars.u, &bars.ns, &bars.sb, &bars.of, &bars.put})
-      bar_init(b, kScanMath / 32);
+      bar_init(b, kScanWarps);
     *failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  return *slot;
+  return __shfl_sync(0xffffffffu, *slot, 0);
 }
 
 // SAVE leaves for the gradients, per chunk, head and 128 columns of v, the
@@ -278,7 +289,7 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
   __shared__ ScanBars bars;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int failed;
-  __shared__ float box[2][2][128];
+  __shared__ float2 box[2][kScanGroups][128];
   constexpr int NT = Terms<T>::value, ST = kScanStages;
   constexpr int kStage = scan_stage_bytes(DK, NT, STAGED);
   // bf16 outputs: their rounding (2^-9) hides what the leading fp16 parts of
@@ -293,65 +304,81 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
   const uint32_t tm = scan_begin(bars, &tmem_slot, &failed, tid, warp);
   auto wait = [&](uint64_t *b, uint32_t parity) { return wait_or_fail(b, parity, &failed, status); };
 
-  if (warp == 10) {
+  if (warp == kScanWarps + 2) {
     if constexpr (STAGED)
       if (a.o)
         scan_store<T>(a, sp, plan.chunk0 != nullptr, h, false, a.o, vb * 128, stages + ST * kStage,
                       &bars, &failed, status, lane);
-  } else if (warp == 9) {
+  } else if (warp == kScanWarps + 1) {
     scan_load<T, DK, STAGED>(a, sp, h, false, kq, images,
                              head_rows<T>(a.v, a.sv, sp.b, sp.row0, h) + vb * 128, a.sv.tok,
                              vb * 128, stages, &bars, &failed, status, lane);
-  } else if (warp == 8) {
-    if (lane == 0) {
-      for (int it = 0; it < sp.chunks; ++it) {
-        const int s = it % ST;
-        const uint32_t ph = it & 1;
-        const uint32_t k = smem_u32(stages + s * kStage);
-        const uint32_t q = k + kTile, image = k + kq_bytes(DK, NT);
-        if (!wait(&bars.full[s], (it / ST) & 1) || !wait(&bars.sb, ph)) break;
-        tc_fence_after();
+  } else if (warp == kScanWarps) {
+    // The whole warp walks along, one lane issues.
+    for (int it = 0; it < sp.chunks; ++it) {
+      const int s = it % ST;
+      const uint32_t ph = it & 1;
+      const uint32_t k = smem_u32(stages) + s * kStage;
+      const uint32_t q = k + kTile, image = k + kq_bytes(DK, NT);
+      if (!wait(&bars.full[s], (it / ST) & 1) || !wait(&bars.sb, ph)) break;
+      tc_fence_after();
+      if (elect_one()) {
         mma_state<DK, NT, false>(tm + kColP, tm + kColSh, tm + kColSl, k);
         mma_commit(&bars.p);
-        if (it > 0 && !wait(&bars.of, ph ^ 1)) break;
-        tc_fence_after();
+      }
+      __syncwarp();
+      if (it > 0 && !wait(&bars.of, ph ^ 1)) break;
+      tc_fence_after();
+      if (elect_one()) {
         mma_state<DK, NT, LEAD>(tm + kColN, tm + kColSh, tm + kColSl, q);
         mma_commit(&bars.n);
-        if (!wait(&bars.y, ph)) break;
-        tc_fence_after();
+      }
+      __syncwarp();
+      if (!wait(&bars.y, ph)) break;
+      tc_fence_after();
+      if (elect_one()) {
         mma_inner<false>(tm + kColP, tm + kColYh, tm + kColYl, image, false);
         mma_commit(&bars.e);
-        if (!wait(&bars.u, ph)) break;
-        tc_fence_after();
+      }
+      __syncwarp();
+      if (!wait(&bars.u, ph)) break;
+      tc_fence_after();
+      if (elect_one()) {
         mma_update<DK, NT>(tm + kColD, tm + kColWh, tm + kColWl, k, false);
         mma_commit(&bars.s);
-        if (!wait(&bars.ns, ph)) break;
-        tc_fence_after();
+      }
+      __syncwarp();
+      if (!wait(&bars.ns, ph)) break;
+      tc_fence_after();
+      if (elect_one()) {
         mma_inner<LEAD>(tm + kColN, tm + kColYh, tm + kColYl, image + 2 * kTile, true);
         mma_commit(&bars.o);
         mma_commit(&bars.empty[s]);
       }
+      __syncwarp();
+    }
+    if (elect_one()) {
       mma_commit(&bars.done);
       bar_wait(&bars.done, 0);
     }
     __syncwarp();
   } else {
-    const int half = warp >> 2;              // tokens and state columns of this group
+    const int group = warp >> 2;             // its tokens and state columns
     const int row = (warp & 3) * 32 + lane;  // column of v within the block
     const uint32_t lb = tm + ((uint32_t)((warp & 3) * 32) << 16);
     const int dvr = vb * 128 + row;
     const bool live = dvr < a.dv;
-    constexpr int SC = DK / 2, SP = SC / 32;  // state columns of a thread, in parts of 32
+    constexpr int TK = kScanTok, SC = DK / kScanGroups, SP = SC / 16;  // state columns in parts of 16
     const long long sat = ((sp.b * a.vheads + h) * a.dk) * (long long)a.dv + dvr;
-    RowAgree agree{box, row, half, warp & 3, 0};
+    RowAgree agree{box, row, group, warp & 3, 0};
     auto saved = [&](long long c) { return ((sp.chunk0 + c) * a.vheads + h) * blocks_v + vb; };
     auto gates_of = [&](int s) {
       return reinterpret_cast<const float *>(stages + s * kStage + kq_bytes(DK, NT) + 4 * kTile);
     };
     // V of a chunk, fetched while the chunk before is worked on: every load is
     // unconditional (of the last row and column where there is none) and its
-    // value not looked at before it is needed, so all 32 are under way at once.
-    T vr[STAGED ? 1 : 32];
+    // value not looked at before it is needed, so all are under way at once.
+    T vr[STAGED ? 1 : TK];
     const T *vcol = head_rows<T>(a.v, a.sv, sp.b, sp.row0, h) + (live ? dvr : a.dv - 1);
     auto fetch_v = [&](int c) {
       if constexpr (!STAGED) {
@@ -359,25 +386,23 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
         const int last = (int)(sp.rows - r0 < kChunk ? sp.rows - r0 : kChunk) - 1;
         const T *v = vcol + r0 * a.sv.tok;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const int t = half * 32 + j < last ? half * 32 + j : last;
+        for (int j = 0; j < TK; ++j) {
+          const int t = group * TK + j < last ? group * TK + j : last;
           vr[j] = v[(long long)t * a.sv.tok];
         }
       }
     };
-    float2 S[SP][16];
-    float inv_s = 1.0f;
+    float2 S[SP][8];
+    float ss = 1.0f;  // scale of the state as an operand
     // The state as the left operand of chunk c's products.
     auto put_state = [&](long long c) {
-      float m = 0.0f;
-#pragma unroll
-      for (int p = 0; p < SP; ++p) m = max32(m, S[p]);
-      const float s = agree.scale(m);
-      inv_s = scale_inverse(s);
 #pragma unroll
       for (int p = 0; p < SP; ++p) {
-        const int col = half * SC + p * 32;
-        put_split(lb + kColSh + col / 2, lb + kColSl + col / 2, S[p], s);
+        const int col = group * SC + p * 16;
+        float2 f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = mul2(S[p][j], both(ss));
+        put_split(lb + kColSh + col / 2, lb + kColSl + col / 2, f);
       }
       tmem_wait_st();
       warp_arrive(&bars.sb, lane);
@@ -386,11 +411,17 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
 #pragma unroll
         for (int p = 0; p < SP; ++p)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            dst[(half * SC + p * 32 + 2 * j) * 128] = S[p][j].x;
-            dst[(half * SC + p * 32 + 2 * j + 1) * 128] = S[p][j].y;
+          for (int j = 0; j < 8; ++j) {
+            dst[(group * SC + p * 16 + 2 * j) * 128] = S[p][j].x;
+            dst[(group * SC + p * 16 + 2 * j + 1) * 128] = S[p][j].y;
           }
       }
+    };
+    auto state_max = [&]() {
+      float m = 0.0f;
+#pragma unroll
+      for (int p = 0; p < SP; ++p) m = max16(m, S[p]);
+      return m;
     };
     auto initial = [&](int col) {
       return a.state_in && live && col < a.dk ? a.state_in[sat + (long long)col * a.dv] : 0.0f;
@@ -398,78 +429,94 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
 #pragma unroll
     for (int p = 0; p < SP; ++p)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int col = half * SC + p * 32 + 2 * j;
+      for (int j = 0; j < 8; ++j) {
+        const int col = group * SC + p * 16 + 2 * j;
         S[p][j] = make_float2(initial(col), initial(col + 1));
       }
     bool ok = true;
     if (sp.chunks > 0) {
       fetch_v(0);
+      ss = bound_scale(agree.largest(state_max(), 0.0f).x);
       put_state(0);
     }
     for (int it = 0; it < sp.chunks && ok; ++it) {
       const int s = it % ST;
       const uint32_t ph = it & 1;
-      const float *gates = gates_of(s) + half * 32;
-      uint32_t r[32];
-      float2 f[16];
-      // Y = V^T - P gamma
-      if (!(ok = wait(&bars.full[s], (it / ST) & 1) && wait(&bars.p, ph))) break;
-      tc_fence_after();
-      tmem_ld32(lb + kColP + half * 32, r);
-      tmem_wait_ld();
+      const float *gates = gates_of(s) + group * TK;
+      uint32_t r[16];
+      float2 f[8];
+      // While P is computed: V, and the scales.
+      if (!(ok = wait(&bars.full[s], (it / ST) & 1))) break;
       const T *vs = reinterpret_cast<const T *>(stages + s * kStage + kStage - kRows16) +
-                    half * 32 * 128 + row;
+                    group * TK * 128 + row;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float2 v = STAGED ? make_float2(to_acc(vs[2 * j * 128]), to_acc(vs[(2 * j + 1) * 128]))
-                                : make_float2(to_acc(vr[STAGED ? 0 : 2 * j]),
-                                              to_acc(vr[STAGED ? 0 : 2 * j + 1]));
-        f[j] = fma2(mul2(gate(gates, j), both(inv_s)), pair(r, j), v);
-      }
-      const float ys = agree.scale(max32(0.0f, f));
-      put_split(lb + kColYh + half * 16, lb + kColYl + half * 16, f, ys);
+      for (int j = 0; j < 8; ++j)
+        f[j] = STAGED ? make_float2(to_acc(vs[2 * j * 128]), to_acc(vs[(2 * j + 1) * 128]))
+                      : make_float2(to_acc(vr[STAGED ? 0 : 2 * j]),
+                                    to_acc(vr[STAGED ? 0 : 2 * j + 1]));
+      const float2 most = agree.largest(state_max(), max16(0.0f, f));
+      const float *chunk = gates_of(s) + kChunkAt;
+      const float Gamma = chunk[0];
+      const float by = most.y + chunk[1] * most.x, bw = by * chunk[3];
+      const float ys = bound_scale(by), us = bound_scale(by * chunk[2]), wsc = bound_scale(bw);
+      const float inv_s = scale_inverse(ss), inv_y = scale_inverse(ys), inv_u = scale_inverse(us);
+      ss = bound_scale(fmaf(Gamma, most.x, 128.0f * bw));  // of the next state
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = mul2(f[j], both(ys));
+      // Y = V^T - P gamma
+      if (!(ok = wait(&bars.p, ph))) break;
+      tc_fence_after();
+      tmem_ld(lb + kColP + group * TK, r);
+      float2 gf[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) gf[j] = mul2(gate(gates, j), both(inv_s * ys));
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = fma2(gf[j], pair(r, j), f[j]);
+      put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, f);
       tmem_wait_st();
       warp_arrive(&bars.y, lane);
       // U = E beta, W = U Gamma / gamma
+      float2 gw[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 b = mul2(gate(gates + 2 * 64, j), both(inv_y));
+        gf[j] = mul2(b, both(us));
+        gw[j] = mul2(mul2(b, gate(gates + 64, j)), both(wsc));
+      }
       if (!(ok = wait(&bars.e, ph))) break;
       tc_fence_after();
-      tmem_ld32(lb + kColP + half * 32, r);
+      tmem_ld(lb + kColP + group * TK, r);
       tmem_wait_ld();
-      const float inv_y = scale_inverse(ys);
-      if constexpr (SAVE) {
-        float *dst = rows + saved(it) * (64 * 128) + half * 32 * 128 + row;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          dst[j * 128] = __uint_as_float(r[j]) * (gates[5 * 64 + j] * inv_y);
-      }
-      float2 w[16];
+      for (int j = 0; j < 8; ++j) f[j] = mul2(pair(r, j), gw[j]);
+      put_split(lb + kColWh + group * 8, lb + kColWl + group * 8, f);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        f[j] = mul2(pair(r, j), mul2(gate(gates + 2 * 64, j), both(inv_y)));
-        w[j] = mul2(f[j], gate(gates + 64, j));
-      }
-      const float us = agree.scale(max32(max32(0.0f, f), w)), inv_u = scale_inverse(us);
-      put_split(lb + kColYh + half * 16, lb + kColYl + half * 16, f, us);
-      put_split(lb + kColWh + half * 16, lb + kColWl + half * 16, w, us);
+      for (int j = 0; j < 8; ++j) f[j] = mul2(pair(r, j), gf[j]);
+      put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, f);
       tmem_wait_st();
       warp_arrive(&bars.u, lane);
+      if constexpr (SAVE) {
+        float *dst = rows + saved(it) * (64 * 128) + group * TK * 128 + row;
+#pragma unroll
+        for (int j = 0; j < TK; ++j)
+          dst[j * 128] = __uint_as_float(r[j]) * (gates[5 * 64 + j] * inv_y);
+      }
       // N in units of U M^T, the start of O
       if (!(ok = wait(&bars.n, ph))) break;
       tc_fence_after();
-      tmem_ld32(lb + kColN + half * 32, r);
+      tmem_ld(lb + kColN + group * TK, r);
       tmem_wait_ld();
       const float ratio = inv_s * us;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < 8; ++j) {
         const float2 n = mul2(pair(r, j), mul2(gate(gates + 3 * 64, j), both(ratio)));
         r[2 * j] = __float_as_uint(n.x);
         r[2 * j + 1] = __float_as_uint(n.y);
       }
-      tmem_st32(lb + kColN + half * 32, r);
+      tmem_st(lb + kColN + group * TK, r);
       tmem_wait_st();
       warp_arrive(&bars.ns, lane);
-      const float Gamma = gates_of(s)[kGammaAt];
       const bool more = it + 1 < sp.chunks;
       if (more) fetch_v(it + 1);
       // The new state
@@ -477,36 +524,36 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       tc_fence_after();
 #pragma unroll
       for (int p = 0; p < SP; ++p) {
-        tmem_ld32(lb + kColD + half * SC + p * 32, r);
+        tmem_ld(lb + kColD + group * SC + p * 16, r);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          S[p][j] = fma2(S[p][j], both(Gamma), mul2(pair(r, j), both(inv_u)));
+        for (int j = 0; j < 8; ++j)
+          S[p][j] = fma2(S[p][j], both(Gamma), mul2(pair(r, j), both(scale_inverse(wsc))));
       }
       if (more) put_state(it + 1);
       // The output
       if (!(ok = wait(&bars.o, ph))) break;
       if (STAGED && a.o && it > 0 && !(ok = wait(&bars.got, ph ^ 1))) break;
       tc_fence_after();
-      tmem_ld32(lb + kColN + half * 32, r);
+      tmem_ld(lb + kColN + group * TK, r);
       tmem_wait_ld();
       warp_arrive(&bars.of, lane);
       if (STAGED && a.o) {
-        T *os = reinterpret_cast<T *>(stages + ST * kStage) + half * 32 * 128 + row;
+        T *os = reinterpret_cast<T *>(stages + ST * kStage) + group * TK * 128 + row;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < 8; ++j) {
           const float2 o = mul2(pair(r, j), mul2(gate(gates + 4 * 64, j), both(inv_u)));
           os[2 * j * 128] = from_acc<T>(o.x);
           os[(2 * j + 1) * 128] = from_acc<T>(o.y);
         }
         fence_smem_to_async();
       } else if (a.o && live) {
-        const long long r0 = sp.row0 + (long long)it * kChunk + half * 32;
-        const long long left = sp.rows - (long long)it * kChunk - half * 32;
+        const long long r0 = sp.row0 + (long long)it * kChunk + group * TK;
+        const long long left = sp.rows - (long long)it * kChunk - group * TK;
         T *o = static_cast<T *>(a.o) + out_row(a, sp.b, r0, plan.chunk0 != nullptr, h) + dvr;
         const long long step = (long long)a.vheads * a.dv;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < TK; ++j)
           if (j < left)
             o[j * step] = from_acc<T>(__uint_as_float(r[j]) * (gates[4 * 64 + j] * inv_u));
       }
@@ -520,8 +567,8 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
 #pragma unroll
       for (int p = 0; p < SP; ++p)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int col = half * SC + p * 32 + 2 * j;
+        for (int j = 0; j < 8; ++j) {
+          const int col = group * SC + p * 16 + 2 * j;
           if (col < a.dk) a.state_out[sat + (long long)col * a.dv] = S[p][j].x;
           if (col + 1 < a.dk) a.state_out[sat + (long long)(col + 1) * a.dv] = S[p][j].y;
         }
@@ -529,7 +576,7 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_free(tm, 512);
+  if (warp == kScanWarps) tmem_free(tm, 512);
 }
 
 }  // namespace fftgb
