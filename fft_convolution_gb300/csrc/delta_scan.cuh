@@ -41,21 +41,24 @@ constexpr int kScanStages = 2;
 
 // 64 tokens x 128 columns of a 16-bit type.
 constexpr int kRows16 = 64 * 128 * 2;
-// Stage: the tiles of K and Q, the head's image, and (STAGED) the rows of V
-// (backwards: of dO); 1024-byte aligned.
+// Stage: the tiles of K and Q, the head's image up to its factors, and
+// (STAGED) the rows of V (backwards: of dO); 1024-byte aligned.
 __host__ __device__ constexpr int scan_stage_bytes(int dk, int terms, bool staged) {
-  return kq_bytes(dk, terms) + ((kImageBytes + 1023) & ~1023) + (staged ? kRows16 : 0);
+  return kq_bytes(dk, terms) + 4 * kTile + (staged ? kRows16 : 0);
 }
-// Two stages, and (STAGED) the rows of O (of dV) on their way out.
+// Two stages, (STAGED) the rows of O (of dV) on their way out, and the factors
+// of four chunks: a chunk's output is still scaled while the stage of its
+// tiles is being filled again.
+constexpr int kGateBytes = kImageBytes - 4 * kTile, kGateRing = 4;
 __host__ __device__ constexpr size_t scan_smem(int dk, int terms, bool staged) {
   return 1024 + (size_t)kScanStages * scan_stage_bytes(dk, terms, staged) +
-         (staged ? kRows16 : 0);
+         (staged ? kRows16 : 0) + kGateRing * kGateBytes;
 }
 
 struct ScanBars {
   uint64_t full[kScanStages], empty[kScanStages];
   uint64_t p, n, e, s, o;       // products done: P, N, E, W K, O
-  uint64_t y, u, ns, sb, of;    // operands ready: Y, U and W, N scaled, S; O read
+  uint64_t y, w, u, sb, of;     // operands ready: Y, W, U and N scaled, S; O read
   uint64_t put, got;            // STAGED: rows of O in shared memory; copied out
   uint64_t done;                // every product
 };
@@ -92,48 +95,55 @@ __device__ __forceinline__ long long out_row(const DeltaArgs &a, long long b, lo
 // The loading warp: the chunks' images into the stages and, STAGED, the rows
 // x of v's type (128 columns from column c0; where the chunk has fewer than 64
 // tokens its last row again: its values meet factors of 0, which only
-// finite ones leave 0).
+// finite ones leave 0).  The rows go by 16-byte copies: as one bulk copy per
+// row of 256 bytes they took longer than the rest of the chunk's work.
 template <typename T, int DK, bool STAGED>
 __device__ __forceinline__ void scan_load(const DeltaArgs &a, const ScanSpan &sp, int h,
                                           bool backwards, const char *kq, const char *images,
                                           const T *x, long long step, int c0, char *stages,
-                                          ScanBars *bars, volatile int *failed, int *status,
-                                          int lane) {
+                                          char *ring, ScanBars *bars, volatile int *failed,
+                                          int *status, int lane) {
   constexpr int NT = Terms<T>::value, ST = kScanStages;
   constexpr int kStage = scan_stage_bytes(DK, NT, STAGED);
   const int hk = h / (a.vheads / a.kheads);
-  const int cols = a.dv - c0 < 128 ? a.dv - c0 : 128;
+  const int pieces = (a.dv - c0 < 128 ? a.dv - c0 : 128) / 8;
   int issued = 0;
   for (int it = 0; it < sp.chunks; ++it) {
     const int ci = backwards ? sp.chunks - 1 - it : it;
     const long long c = sp.chunk0 + ci;
     const int s = it % ST;
-    bool ok = it < ST || wait_or_fail(&bars->empty[s], (it / ST - 1) & 1, failed, status);
+    const bool ok = it < ST || wait_or_fail(&bars->empty[s], (it / ST - 1) & 1, failed, status);
     if (!__all_sync(0xffffffffu, ok)) break;
     char *stage = stages + s * kStage;
     if (lane == 0) {
-      bar_arrive_tx(&bars->full[s], kq_bytes(DK, NT) + kImageBytes +
-                                        (STAGED ? 64 * cols * (int)sizeof(T) : 0));
+      const char *image = images + (c * a.vheads + h) * (long long)kImageBytes;
+      bar_arrive_tx(&bars->full[s], kq_bytes(DK, NT) + kImageBytes);
       bulk_load(stage, kq + (c * a.kheads + hk) * (long long)kq_bytes(DK, NT), kq_bytes(DK, NT),
                 &bars->full[s]);
-      bulk_load(stage + kq_bytes(DK, NT), images + (c * a.vheads + h) * (long long)kImageBytes,
-                kImageBytes, &bars->full[s]);
+      bulk_load(stage + kq_bytes(DK, NT), image, 4 * kTile, &bars->full[s]);
+      bulk_load(ring + (it % kGateRing) * kGateBytes, image + 4 * kTile, kGateBytes,
+                &bars->full[s]);
     }
     if constexpr (STAGED) {
-      __syncwarp();
       const long long r0 = (long long)ci * kChunk;
       const int last = (int)(sp.rows - r0 < kChunk ? sp.rows - r0 : kChunk) - 1;
-      char *dst = stage + kStage - kRows16;
-      for (int r = lane; r < kChunk; r += 32)
-        bulk_load(dst + r * 256, x + (r0 + (r < last ? r : last)) * step, cols * (int)sizeof(T),
-                  &bars->full[s]);
+      const uint32_t dst = smem_u32(stage + kStage - kRows16) + (lane & 15) * 16;
+      const T *src = x + r0 * step + (lane & 15) * 8;
+      if ((lane & 15) < pieces) {
+#pragma unroll 8
+        for (int r = lane >> 4; r < kChunk; r += 2)
+          copy16(dst + r * 256, src + (r < last ? r : last) * step);
+      }
+      copy_arrive(&bars->full[s]);
     }
     issued = it + 1;
   }
   // Given up: no copy may land after the block has gone.
-  if (*failed)
+  if (*failed) {
+    copy_wait_all();
     for (int it = issued > ST ? issued - ST : 0; it < issued; ++it)
       bar_wait(&bars->full[it % ST], (it / ST) & 1);
+  }
 }
 
 // The storing warp, STAGED: the chunks' rows from shared memory to the
@@ -143,21 +153,25 @@ __device__ __forceinline__ void scan_store(const DeltaArgs &a, const ScanSpan &s
                                            int h, bool backwards, void *out, int c0,
                                            const char *rows, ScanBars *bars,
                                            volatile int *failed, int *status, int lane) {
-  const int cols = a.dv - c0 < 128 ? a.dv - c0 : 128;
+  const int pieces = (a.dv - c0 < 128 ? a.dv - c0 : 128) / 8;
+  const long long step = (long long)a.vheads * a.dv;
   for (int it = 0; it < sp.chunks; ++it) {
     const int ci = backwards ? sp.chunks - 1 - it : it;
     const bool ok = wait_or_fail(&bars->put, it & 1, failed, status);
     if (!__all_sync(0xffffffffu, ok)) break;
     const long long r0 = (long long)ci * kChunk;
     const int n = (int)(sp.rows - r0 < kChunk ? sp.rows - r0 : kChunk);
-    T *dst = static_cast<T *>(out) + out_row(a, sp.b, sp.row0 + r0, packed, h) + c0;
-    for (int r = lane; r < n; r += 32)
-      bulk_put(dst + r * (long long)a.vheads * a.dv, rows + r * 256, cols * (int)sizeof(T));
-    bulk_put_read();
+    T *dst = static_cast<T *>(out) + out_row(a, sp.b, sp.row0 + r0, packed, h) + c0 +
+             (lane & 15) * 8;
+    const char *src = rows + (lane & 15) * 16;
+    if ((lane & 15) < pieces) {
+#pragma unroll 4
+      for (int r = lane >> 4; r < n; r += 2)
+        *reinterpret_cast<uint4 *>(dst + r * step) = *reinterpret_cast<const uint4 *>(src + r * 256);
+    }
     __syncwarp();
     if (lane == 0) bar_arrive(&bars->got);
   }
-  bulk_put_done();
 }
 
 constexpr uint32_t idesc_tokens = mma_desc(128, 64, false, false);
@@ -258,15 +272,15 @@ constexpr uint32_t kColD = 0, kColSh = 128, kColSl = 192, kColP = 256, kColYh = 
 
 // Barriers and tensor memory of a scan: returns the base column.
 __device__ __forceinline__ uint32_t scan_begin(ScanBars &bars, uint32_t *slot, volatile int *failed,
-                                               int tid, int warp) {
+                                               bool staged, int tid, int warp) {
   if (warp == kScanWarps) tmem_alloc(slot, 512);
   if (tid == 0) {
     for (int s = 0; s < kScanStages; ++s) {
-      bar_init(&bars.full[s], 1);
+      bar_init(&bars.full[s], staged ? 33 : 1);
       bar_init(&bars.empty[s], 1 + kScanWarps);
     }
     for (uint64_t *b : {&bars.p, &bars.n, &bars.e, &bars.s, &bars.o, &bars.got, &bars.done}) bar_init(b, 1);
-    for (uint64_t *b : {&bars.y, &bars.u, &bars.ns, &bars.sb, &bars.of, &bars.put})
+    for (uint64_t *b : {&bars.y, &bars.w, &bars.u, &bars.sb, &bars.of, &bars.put})
       bar_init(b, kScanWarps);
     *failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -301,7 +315,8 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
   const int h = (blockIdx.x / blocks_v) % a.vheads;
   const ScanSpan sp = scan_span(a, plan, blockIdx.x / blocks_v / a.vheads);
   char *stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  const uint32_t tm = scan_begin(bars, &tmem_slot, &failed, tid, warp);
+  const uint32_t tm = scan_begin(bars, &tmem_slot, &failed, STAGED, tid, warp);
+  char *ring = stages + ST * kStage + (STAGED ? kRows16 : 0);
   auto wait = [&](uint64_t *b, uint32_t parity) { return wait_or_fail(b, parity, &failed, status); };
 
   if (warp == kScanWarps + 2) {
@@ -312,7 +327,7 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
   } else if (warp == kScanWarps + 1) {
     scan_load<T, DK, STAGED>(a, sp, h, false, kq, images,
                              head_rows<T>(a.v, a.sv, sp.b, sp.row0, h) + vb * 128, a.sv.tok,
-                             vb * 128, stages, &bars, &failed, status, lane);
+                             vb * 128, stages, ring, &bars, &failed, status, lane);
   } else if (warp == kScanWarps) {
     // The whole warp walks along, one lane issues.
     for (int it = 0; it < sp.chunks; ++it) {
@@ -327,13 +342,6 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
         mma_commit(&bars.p);
       }
       __syncwarp();
-      if (it > 0 && !wait(&bars.of, ph ^ 1)) break;
-      tc_fence_after();
-      if (elect_one()) {
-        mma_state<DK, NT, LEAD>(tm + kColN, tm + kColSh, tm + kColSl, q);
-        mma_commit(&bars.n);
-      }
-      __syncwarp();
       if (!wait(&bars.y, ph)) break;
       tc_fence_after();
       if (elect_one()) {
@@ -341,14 +349,21 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
         mma_commit(&bars.e);
       }
       __syncwarp();
-      if (!wait(&bars.u, ph)) break;
+      if (it > 0 && !wait(&bars.of, ph ^ 1)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_state<DK, NT, LEAD>(tm + kColN, tm + kColSh, tm + kColSl, q);
+        mma_commit(&bars.n);
+      }
+      __syncwarp();
+      if (!wait(&bars.w, ph)) break;
       tc_fence_after();
       if (elect_one()) {
         mma_update<DK, NT>(tm + kColD, tm + kColWh, tm + kColWl, k, false);
         mma_commit(&bars.s);
       }
       __syncwarp();
-      if (!wait(&bars.ns, ph)) break;
+      if (!wait(&bars.u, ph)) break;
       tc_fence_after();
       if (elect_one()) {
         mma_inner<LEAD>(tm + kColN, tm + kColYh, tm + kColYl, image + 2 * kTile, true);
@@ -372,8 +387,8 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
     const long long sat = ((sp.b * a.vheads + h) * a.dk) * (long long)a.dv + dvr;
     RowAgree agree{box, row, group, warp & 3, 0};
     auto saved = [&](long long c) { return ((sp.chunk0 + c) * a.vheads + h) * blocks_v + vb; };
-    auto gates_of = [&](int s) {
-      return reinterpret_cast<const float *>(stages + s * kStage + kq_bytes(DK, NT) + 4 * kTile);
+    auto gates_of = [&](int it) {
+      return reinterpret_cast<const float *>(ring + (it % kGateRing) * kGateBytes);
     };
     // V of a chunk, fetched while the chunk before is worked on: every load is
     // unconditional (of the last row and column where there is none) and its
@@ -392,28 +407,27 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
         }
       }
     };
+    // The state times ss, its scale as an operand: ss changes from chunk to
+    // chunk, the values' rounding does not.
     float2 S[SP][8];
-    float ss = 1.0f;  // scale of the state as an operand
-    // The state as the left operand of chunk c's products.
+    float ss = 1.0f;
     auto put_state = [&](long long c) {
 #pragma unroll
       for (int p = 0; p < SP; ++p) {
         const int col = group * SC + p * 16;
-        float2 f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = mul2(S[p][j], both(ss));
-        put_split(lb + kColSh + col / 2, lb + kColSl + col / 2, f);
+        put_split(lb + kColSh + col / 2, lb + kColSl + col / 2, S[p]);
       }
       tmem_wait_st();
       warp_arrive(&bars.sb, lane);
       if constexpr (SAVE) {
+        const float inv = scale_inverse(ss);
         float *dst = states + saved(c) * (DK * 128) + row;
 #pragma unroll
         for (int p = 0; p < SP; ++p)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            dst[(group * SC + p * 16 + 2 * j) * 128] = S[p][j].x;
-            dst[(group * SC + p * 16 + 2 * j + 1) * 128] = S[p][j].y;
+            dst[(group * SC + p * 16 + 2 * j) * 128] = S[p][j].x * inv;
+            dst[(group * SC + p * 16 + 2 * j + 1) * 128] = S[p][j].y * inv;
           }
       }
     };
@@ -433,20 +447,12 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
         const int col = group * SC + p * 16 + 2 * j;
         S[p][j] = make_float2(initial(col), initial(col + 1));
       }
-    bool ok = true;
-    if (sp.chunks > 0) {
-      fetch_v(0);
-      ss = bound_scale(agree.largest(state_max(), 0.0f).x);
-      put_state(0);
-    }
-    for (int it = 0; it < sp.chunks && ok; ++it) {
-      const int s = it % ST;
-      const uint32_t ph = it & 1;
-      const float *gates = gates_of(s) + group * TK;
-      uint32_t r[16];
-      float2 f[8];
-      // While P is computed: V, and the scales.
-      if (!(ok = wait(&bars.full[s], (it / ST) & 1))) break;
+    // V of chunk c into f, and the largest of it.
+    float2 f[8];
+    float vmax = 0.0f;
+    auto take_v = [&](int c) {
+      const int s = c % ST;
+      if (!wait(&bars.full[s], (c / ST) & 1)) return false;
       const T *vs = reinterpret_cast<const T *>(stages + s * kStage + kStage - kRows16) +
                     group * TK * 128 + row;
 #pragma unroll
@@ -454,48 +460,106 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
         f[j] = STAGED ? make_float2(to_acc(vs[2 * j * 128]), to_acc(vs[(2 * j + 1) * 128]))
                       : make_float2(to_acc(vr[STAGED ? 0 : 2 * j]),
                                     to_acc(vr[STAGED ? 0 : 2 * j + 1]));
-      const float2 most = agree.largest(state_max(), max16(0.0f, f));
-      const float *chunk = gates_of(s) + kChunkAt;
-      const float Gamma = chunk[0];
-      const float by = most.y + chunk[1] * most.x, bw = by * chunk[3];
-      const float ys = bound_scale(by), us = bound_scale(by * chunk[2]), wsc = bound_scale(bw);
-      const float inv_s = scale_inverse(ss), inv_y = scale_inverse(ys), inv_u = scale_inverse(us);
-      ss = bound_scale(fmaf(Gamma, most.x, 128.0f * bw));  // of the next state
+      vmax = max16(0.0f, f);
+      __syncwarp();
+      if (lane == 0) bar_arrive(&bars.empty[s]);
+      return true;
+    };
+    // The output of chunk c, whose U was scaled by us.
+    auto put_output = [&](int c, float us) {
+      const uint32_t ph = c & 1;
+      const float inv_u = scale_inverse(us);
+      const float *gates = gates_of(c) + group * TK;
+      if (!wait(&bars.o, ph)) return false;
+      if (STAGED && a.o && c > 0 && !wait(&bars.got, ph ^ 1)) return false;
+      tc_fence_after();
+      uint32_t r[16];
+      tmem_ld(lb + kColN + group * TK, r);
+      tmem_wait_ld();
+      warp_arrive(&bars.of, lane);
+      if (STAGED && a.o) {
+        T *os = reinterpret_cast<T *>(stages + ST * kStage) + group * TK * 128 + row;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = mul2(f[j], both(ys));
+        for (int j = 0; j < 8; ++j) {
+          const float2 o = mul2(pair(r, j), mul2(gate(gates + 4 * 64, j), both(inv_u)));
+          os[2 * j * 128] = from_acc<T>(o.x);
+          os[(2 * j + 1) * 128] = from_acc<T>(o.y);
+        }
+      } else if (a.o && live) {
+        const long long r0 = sp.row0 + (long long)c * kChunk + group * TK;
+        const long long left = sp.rows - (long long)c * kChunk - group * TK;
+        T *o = static_cast<T *>(a.o) + out_row(a, sp.b, r0, plan.chunk0 != nullptr, h) + dvr;
+        const long long step = (long long)a.vheads * a.dv;
+#pragma unroll
+        for (int j = 0; j < TK; ++j)
+          if (j < left)
+            o[j * step] = from_acc<T>(__uint_as_float(r[j]) * (gates[4 * 64 + j] * inv_u));
+      }
+      __syncwarp();
+      if (STAGED && lane == 0) bar_arrive(&bars.put);
+      return true;
+    };
+    bool ok = true;
+    if (sp.chunks > 0) {
+      fetch_v(0);
+      ss = bound_scale(agree.largest(state_max(), 0.0f).x);
+#pragma unroll
+      for (int p = 0; p < SP; ++p)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) S[p][j] = mul2(S[p][j], both(ss));
+      put_state(0);
+      ok = take_v(0);
+    }
+    float us_before = 1.0f;
+    for (int it = 0; it < sp.chunks && ok; ++it) {
+      const uint32_t ph = it & 1;
+      const float *gates = gates_of(it) + group * TK;
+      uint32_t r[16];
+      // While P is computed: the scales.
+      const float2 most = agree.largest(state_max(), vmax);
+      const float *chunk = gates_of(it) + kChunkAt;
+      const float Gamma = chunk[0], inv_s = scale_inverse(ss), smax = most.x * inv_s;
+      const float by = most.y + chunk[1] * smax, bw = by * chunk[3];
+      const float ys = bound_scale(by), us = bound_scale(by * chunk[2]), wsc = bound_scale(bw);
+      const float inv_y = scale_inverse(ys);
+      const float next_ss = bound_scale(fmaf(Gamma, smax, 128.0f * bw));
+      float2 gf[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        f[j] = mul2(f[j], both(ys));
+        gf[j] = mul2(gate(gates, j), both(inv_s * ys));
+      }
       // Y = V^T - P gamma
       if (!(ok = wait(&bars.p, ph))) break;
       tc_fence_after();
       tmem_ld(lb + kColP + group * TK, r);
-      float2 gf[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) gf[j] = mul2(gate(gates, j), both(inv_s * ys));
       tmem_wait_ld();
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = fma2(gf[j], pair(r, j), f[j]);
       put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, f);
       tmem_wait_st();
       warp_arrive(&bars.y, lane);
-      // U = E beta, W = U Gamma / gamma
-      float2 gw[8];
+      // While E is computed: the output of the chunk before.
+      if (it > 0 && !(ok = put_output(it - 1, us_before))) break;
+      us_before = us;
+      // W = E beta Gamma / gamma, on which the new state waits, then U = E beta
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 b = mul2(gate(gates + 2 * 64, j), both(inv_y));
-        gf[j] = mul2(b, both(us));
-        gw[j] = mul2(mul2(b, gate(gates + 64, j)), both(wsc));
-      }
+      for (int j = 0; j < 8; ++j)
+        gf[j] = mul2(mul2(mul2(gate(gates + 2 * 64, j), both(inv_y)), gate(gates + 64, j)),
+                     both(wsc));
       if (!(ok = wait(&bars.e, ph))) break;
       tc_fence_after();
       tmem_ld(lb + kColP + group * TK, r);
       tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = mul2(pair(r, j), gw[j]);
-      put_split(lb + kColWh + group * 8, lb + kColWl + group * 8, f);
-#pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = mul2(pair(r, j), gf[j]);
-      put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, f);
+      put_split(lb + kColWh + group * 8, lb + kColWl + group * 8, f);
       tmem_wait_st();
-      warp_arrive(&bars.u, lane);
+      warp_arrive(&bars.w, lane);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        f[j] = mul2(pair(r, j), mul2(gate(gates + 2 * 64, j), both(inv_y * us)));
+      put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, f);
       if constexpr (SAVE) {
         float *dst = rows + saved(it) * (64 * 128) + group * TK * 128 + row;
 #pragma unroll
@@ -516,10 +580,14 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       }
       tmem_st(lb + kColN + group * TK, r);
       tmem_wait_st();
-      warp_arrive(&bars.ns, lane);
+      warp_arrive(&bars.u, lane);
       const bool more = it + 1 < sp.chunks;
-      if (more) fetch_v(it + 1);
+      if (more) {
+        fetch_v(it + 1);
+        if (!(ok = take_v(it + 1))) break;
+      }
       // The new state
+      const float keep = Gamma * inv_s * next_ss, add = scale_inverse(wsc) * next_ss;
       if (!(ok = wait(&bars.s, ph))) break;
       tc_fence_after();
 #pragma unroll
@@ -528,49 +596,21 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
         tmem_wait_ld();
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          S[p][j] = fma2(S[p][j], both(Gamma), mul2(pair(r, j), both(scale_inverse(wsc))));
+          S[p][j] = fma2(S[p][j], both(keep), mul2(pair(r, j), both(add)));
       }
+      ss = next_ss;
       if (more) put_state(it + 1);
-      // The output
-      if (!(ok = wait(&bars.o, ph))) break;
-      if (STAGED && a.o && it > 0 && !(ok = wait(&bars.got, ph ^ 1))) break;
-      tc_fence_after();
-      tmem_ld(lb + kColN + group * TK, r);
-      tmem_wait_ld();
-      warp_arrive(&bars.of, lane);
-      if (STAGED && a.o) {
-        T *os = reinterpret_cast<T *>(stages + ST * kStage) + group * TK * 128 + row;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 o = mul2(pair(r, j), mul2(gate(gates + 4 * 64, j), both(inv_u)));
-          os[2 * j * 128] = from_acc<T>(o.x);
-          os[(2 * j + 1) * 128] = from_acc<T>(o.y);
-        }
-        fence_smem_to_async();
-      } else if (a.o && live) {
-        const long long r0 = sp.row0 + (long long)it * kChunk + group * TK;
-        const long long left = sp.rows - (long long)it * kChunk - group * TK;
-        T *o = static_cast<T *>(a.o) + out_row(a, sp.b, r0, plan.chunk0 != nullptr, h) + dvr;
-        const long long step = (long long)a.vheads * a.dv;
-#pragma unroll
-        for (int j = 0; j < TK; ++j)
-          if (j < left)
-            o[j * step] = from_acc<T>(__uint_as_float(r[j]) * (gates[4 * 64 + j] * inv_u));
-      }
-      __syncwarp();
-      if (lane == 0) {
-        bar_arrive(&bars.empty[s]);  // the gates and V were read
-        if (STAGED) bar_arrive(&bars.put);
-      }
     }
+    if (ok && sp.chunks > 0) ok = put_output(sp.chunks - 1, us_before);
     if (ok && a.state_out && live) {
 #pragma unroll
       for (int p = 0; p < SP; ++p)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int col = group * SC + p * 16 + 2 * j;
-          if (col < a.dk) a.state_out[sat + (long long)col * a.dv] = S[p][j].x;
-          if (col + 1 < a.dk) a.state_out[sat + (long long)(col + 1) * a.dv] = S[p][j].y;
+          const float inv = scale_inverse(ss);
+          if (col < a.dk) a.state_out[sat + (long long)col * a.dv] = S[p][j].x * inv;
+          if (col + 1 < a.dk) a.state_out[sat + (long long)(col + 1) * a.dv] = S[p][j].y * inv;
         }
     }
   }
