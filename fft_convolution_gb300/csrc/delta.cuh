@@ -141,25 +141,29 @@ template <typename T> struct Terms { static constexpr int value = 1; };
 template <> struct Terms<float> { static constexpr int value = 2; };
 
 // Eight elements of a row; zero from `left` elements on.
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, int left, bool vec, float (&f)[8]) {
-  if (vec && left >= 8) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 x = *reinterpret_cast<const float4 *>(p);
-      const float4 y = *reinterpret_cast<const float4 *>(p + 4);
-      f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
-      f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+template <typename T> struct Row8 {
+  static constexpr int N = sizeof(T) / 2;  // 16-byte words
+  uint4 raw[N];
+  __device__ __forceinline__ void load(const T *p, int left, bool vec) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+    if (left <= 0) return;
+    if (vec && left >= 8) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) raw[i] = reinterpret_cast<const uint4 *>(p)[i];
     } else {
-      const uint4 raw = *reinterpret_cast<const uint4 *>(p);
-      const Vec16<T> x = *reinterpret_cast<const Vec16<T> *>(&raw);
+      T *t = reinterpret_cast<T *>(raw);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = to_acc(x.v[i]);
+      for (int i = 0; i < 8; ++i)
+        if (i < left) t[i] = p[i];
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = i < left ? to_acc(p[i]) : 0.0f;
   }
-}
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const T *t = reinterpret_cast<const T *>(raw);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = to_acc(t[i]);
+  }
+};
 
 __device__ __forceinline__ float max8(const float (&f)[8]) {
   float m = fabsf(f[0]);

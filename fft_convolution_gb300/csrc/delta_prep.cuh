@@ -119,28 +119,37 @@ __device__ __forceinline__ float decay_between(float2 i, float2 j) {
 }
 
 // Rows 0 .. 63 of K or Q into its tiles in shared memory and in the image;
-// inv: the rows' inverse scales.
+// inv: the rows' inverse scales.  All loads of a thread are issued before any
+// value is looked at (half of them with fp32).
 template <typename T, int DK>
 __device__ __forceinline__ void load_rows(const T *src, long long stride, int n, int cols, bool vec,
                                           char *tiles, char *image, float *inv, int tid) {
-  constexpr int P = DK / 8;
+  constexpr int P = DK / 8, PER = 64 * P / kPrepThreads, B = sizeof(T) == 2 ? PER : PER / 2;
   constexpr int kPlane = 2 * (DK / 64) * kTile;
-#pragma unroll 4
-  for (int i = tid; i < 64 * P; i += kPrepThreads) {
-    const int r = i / P, c = i % P;
-    const int left = r < n ? cols - c * 8 : 0;
-    float f[8];
-    load8(src + (left > 0 ? (long long)r * stride + c * 8 : 0), left, vec, f);
-    const float s = row_scale(lane_max<P>(max8(f)));
-    if (c == 0) inv[r] = scale_inverse(s);
-    uint4 hi, lo;
-    split8(f, s, hi, lo);
-    const int at = piece_at(r, c, 2 * kTile);
-    *reinterpret_cast<uint4 *>(tiles + at) = hi;
-    *reinterpret_cast<uint4 *>(image + at) = hi;
-    if constexpr (Terms<T>::value == 2) {
-      *reinterpret_cast<uint4 *>(tiles + kPlane + at) = lo;
-      *reinterpret_cast<uint4 *>(image + kPlane + at) = lo;
+#pragma unroll 1
+  for (int k0 = 0; k0 < PER; k0 += B) {
+    Row8<T> x[B];
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      const int i = (k0 + k) * kPrepThreads + tid, r = i / P, c = i % P;
+      x[k].load(src + (r < n ? r : 0) * stride + c * 8, r < n ? cols - c * 8 : 0, vec);
+    }
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      const int i = (k0 + k) * kPrepThreads + tid, r = i / P, c = i % P;
+      float f[8];
+      x[k].get(f);
+      const float s = row_scale(lane_max<P>(max8(f)));
+      if (c == 0) inv[r] = scale_inverse(s);
+      uint4 hi, lo;
+      split8(f, s, hi, lo);
+      const int at = piece_at(r, c, 2 * kTile);
+      *reinterpret_cast<uint4 *>(tiles + at) = hi;
+      *reinterpret_cast<uint4 *>(image + at) = hi;
+      if constexpr (Terms<T>::value == 2) {
+        *reinterpret_cast<uint4 *>(tiles + kPlane + at) = lo;
+        *reinterpret_cast<uint4 *>(image + kPlane + at) = lo;
+      }
     }
   }
 }
