@@ -93,6 +93,8 @@ SIGNATURES = {
     "fft_clip_grad_norm": (_INT, [_I64, _VP, _VP, _VP, _VP, _DBL, _DBL, _VP, _VP, _SZ, _VP]),
     "fft_delta_rule_workspace_bytes": (_SZ, [_VP, _INT]),
     "fft_delta_rule": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "fft_delta_rule_backward_workspace_bytes": (_SZ, [_VP, _INT]),
+    "fft_delta_rule_backward": (_INT, [_VP] * 17 + [_SZ, _VP]),
     "fft_delta_rule_step": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _VP]),
     "fft_debug_radix2_pass": (_INT, [_VP, _VP, _I64, _I64, _INT, _VP]),
     "fft_device_status": (_INT, [_VP]),
@@ -270,6 +272,19 @@ def fft_delta_rule(desc: DeltaDesc, q: int, k: int, v: int, g: int, beta: int, o
                    workspace_bytes: int, stream: int) -> int:
     return _lib.fft_delta_rule(ctypes.byref(desc), q, k, v, g, beta, offsets, initial_state, o,
                                final_state, workspace, workspace_bytes, stream)
+
+
+def fft_delta_rule_backward_workspace_bytes(desc: DeltaDesc, packed: int) -> int:
+    return int(_lib.fft_delta_rule_backward_workspace_bytes(ctypes.byref(desc), packed))
+
+
+def fft_delta_rule_backward(desc: DeltaDesc, dout: int, q: int, k: int, v: int, g: int, beta: int,
+                            offsets: int, initial_state: int, dfinal_state: int, dq: int, dk: int,
+                            dv: int, dg: int, dbeta: int, dinitial_state: int, workspace: int,
+                            workspace_bytes: int, stream: int) -> int:
+    return _lib.fft_delta_rule_backward(ctypes.byref(desc), dout, q, k, v, g, beta, offsets,
+                                        initial_state, dfinal_state, dq, dk, dv, dg, dbeta,
+                                        dinitial_state, workspace, workspace_bytes, stream)
 
 
 def fft_delta_rule_step(desc: DeltaDesc, q: int, k: int, v: int, g: int, beta: int, state: int,
@@ -567,7 +582,7 @@ def fftn(x, ndim: int, direction: int = FFT_FORWARD, out=None, stream=None):
 # ---- operators of sequence models (tensor helpers in sequence.py) ---------------
 
 _SEQUENCE = ("layer_norm", "layer_norm_backward", "grad_norm", "clip_grad_norm", "delta_rule",
-             "delta_rule_step")
+             "delta_rule_backward", "delta_rule_step")
 
 
 def __getattr__(name):

@@ -52,9 +52,9 @@ constexpr int kTile = 64 * 128;
 // inputs: first all leading, then all trailing parts.
 __host__ __device__ constexpr int kq_bytes(int dk, int terms) { return terms * 2 * (dk / 64) * kTile; }
 // Per value head two 64 x 64 matrices (leading and trailing tile of each),
-// rows scaled, six factors per token, and eight numbers of the chunk: its decay
+// rows scaled, eight factors per token, and eight numbers of the chunk: its decay
 // Gamma and bounds (delta_prep.cuh).
-constexpr int kGates = 6;
+constexpr int kGates = 8;
 constexpr int kChunkAt = kGates * 64;  // in floats, after the tiles
 constexpr int kImageBytes = 4 * kTile + kGates * 64 * 4 + 32;
 

@@ -1,0 +1,318 @@
+// delta_back.cuh -- the gated delta rule's gradients from chunk to chunk, last
+// chunk first (delta.cuh): the mirror image of delta_scan.cuh.
+//
+// The state is dS^T, the gradient of the state that leaves the chunk (columns
+// of v along the lanes, dk along the columns).  Per chunk
+//   P = dS^T K^T, X = dO^T M;  dU = P Gamma/gamma + scale X;
+//   F = dU T (T = (I + beta A)^-1);  dV = beta F;
+//   dS^T <- dS^T Gamma - (gamma beta F) K + (scale gamma dO) Q.
+// The chain is P -> dU -> F -> dS; X, the outputs and all loads run beside it.
+// Roles, scales and bounds as there.  Left for the kernel that follows: dS of
+// every chunk and F.
+//
+// Tensor memory (512 columns):
+//   D (fp32)         0 .. DK - 1
+//   dS (two fp16)    128, 192        P, then F           256 .. 319
+//   dU               320, 352        dO, then gamma beta F   384, 416
+//   X, then (two fp16) scale gamma dO   448 .. 511
+#pragma once
+
+#include "delta_scan.cuh"
+
+namespace fftgb {
+
+template <typename T, int DK, bool STAGED>
+__global__ void __launch_bounds__(kScanThreads, 1)
+delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan plan, const char *kq,
+                  const char *images, float *dstates, float *rows, int *status) {
+  extern __shared__ char smem_raw[];
+  __shared__ ScanBars bars;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int failed;
+  __shared__ float2 box[2][kScanGroups][128];
+  constexpr int NT = Terms<T>::value, ST = kScanStages;
+  constexpr int kStage = scan_stage_bytes(DK, NT, STAGED);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int blocks_v = (a.dv + 127) / 128;
+  const int vb = blockIdx.x % blocks_v;
+  const int h = (blockIdx.x / blocks_v) % a.vheads;
+  const ScanSpan sp = scan_span(a, plan, blockIdx.x / blocks_v / a.vheads);
+  const bool packed = plan.chunk0 != nullptr;
+  char *stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t tm = scan_begin(bars, &tmem_slot, &failed, STAGED, tid, warp);
+  char *ring = stages + ST * kStage + (STAGED ? kRows16 : 0);
+  auto wait = [&](uint64_t *b, uint32_t parity) { return wait_or_fail(b, parity, &failed, status); };
+  const T *dout = static_cast<const T *>(ga.dout) + out_row(a, sp.b, sp.row0, packed, h);
+  const long long ostep = (long long)a.vheads * a.dv;
+
+  if (warp == kScanWarps + 2) {
+    if constexpr (STAGED)
+      scan_store<T>(a, sp, packed, h, true, ga.dv, vb * 128, stages + ST * kStage, &bars, &failed,
+                    status, lane);
+  } else if (warp == kScanWarps + 1) {
+    scan_load<T, DK, STAGED>(a, sp, h, true, kq, images, dout + vb * 128, ostep, vb * 128, stages,
+                             ring, &bars, &failed, status, lane);
+  } else if (warp == kScanWarps) {
+    for (int it = 0; it < sp.chunks; ++it) {
+      const int s = it % ST;
+      const uint32_t ph = it & 1;
+      const uint32_t k = smem_u32(stages) + s * kStage;
+      const uint32_t q = k + kTile, image = k + kq_bytes(DK, NT);
+      if (!wait(&bars.full[s], (it / ST) & 1) || !wait(&bars.sb, ph)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_state<DK, NT, false>(tm + kColP, tm + kColSh, tm + kColSl, k);
+        mma_commit(&bars.p);
+      }
+      __syncwarp();
+      if (!wait(&bars.of, ph)) break;  // dO is there
+      tc_fence_after();
+      if (elect_one()) {
+        mma_inner<false, NT == 1>(tm + kColN, tm + kColWh, tm + kColWl, image + 2 * kTile, false);
+        mma_commit(&bars.n);
+      }
+      __syncwarp();
+      if (!wait(&bars.y, ph)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_inner<false>(tm + kColP, tm + kColYh, tm + kColYl, image, false);
+        mma_commit(&bars.e);
+      }
+      __syncwarp();
+      if (!wait(&bars.u, ph)) break;
+      tc_fence_after();
+      if (elect_one())
+        mma_update<DK, NT>(tm + kColD, tm + kColN, tm + kColN + 32, q, false);
+      __syncwarp();
+      if (!wait(&bars.w, ph)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_update<DK, NT>(tm + kColD, tm + kColWh, tm + kColWl, k, true);
+        mma_commit(&bars.s);
+        mma_commit(&bars.empty[s]);
+      }
+      __syncwarp();
+    }
+    if (elect_one()) {
+      mma_commit(&bars.done);
+      bar_wait(&bars.done, 0);
+    }
+    __syncwarp();
+  } else {
+    const int group = warp >> 2;             // its tokens and state columns
+    const int row = (warp & 3) * 32 + lane;  // column of v within the block
+    const uint32_t lb = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    const int dvr = vb * 128 + row;
+    const bool live = dvr < a.dv;
+    constexpr int TK = kScanTok, SC = DK / kScanGroups, SP = SC / 16;
+    const long long sat = ((sp.b * a.vheads + h) * a.dk) * (long long)a.dv + dvr;
+    RowAgree agree{box, row, group, warp & 3, 0};
+    auto chunk_of = [&](int it) { return sp.chunks - 1 - it; };
+    auto saved = [&](long long c) { return ((sp.chunk0 + c) * a.vheads + h) * blocks_v + vb; };
+    auto gates_of = [&](int it) {
+      return reinterpret_cast<const float *>(ring + (it % kGateRing) * kGateBytes);
+    };
+    T vr[STAGED ? 1 : TK];
+    const T *col = dout + (live ? dvr : a.dv - 1);
+    auto fetch = [&](int it) {
+      if constexpr (!STAGED) {
+        const long long r0 = (long long)chunk_of(it) * kChunk;
+        const int last = (int)(sp.rows - r0 < kChunk ? sp.rows - r0 : kChunk) - 1;
+#pragma unroll
+        for (int j = 0; j < TK; ++j) {
+          const int t = group * TK + j < last ? group * TK + j : last;
+          vr[j] = col[(r0 + t) * ostep];
+        }
+      }
+    };
+    float2 S[SP][8];
+    float ss = 1.0f;
+    auto put_state = [&](long long c) {
+#pragma unroll
+      for (int p = 0; p < SP; ++p) {
+        const int at = group * SC + p * 16;
+        put_split(lb + kColSh + at / 2, lb + kColSl + at / 2, S[p]);
+      }
+      tmem_wait_st();
+      warp_arrive(&bars.sb, lane);
+      const float inv = scale_inverse(ss);
+      float *dst = dstates + saved(c) * (DK * 128) + row;
+#pragma unroll
+      for (int p = 0; p < SP; ++p)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          dst[(group * SC + p * 16 + 2 * j) * 128] = S[p][j].x * inv;
+          dst[(group * SC + p * 16 + 2 * j + 1) * 128] = S[p][j].y * inv;
+        }
+    };
+    auto state_max = [&]() {
+      float m = 0.0f;
+#pragma unroll
+      for (int p = 0; p < SP; ++p) m = max16(m, S[p]);
+      return m;
+    };
+    auto initial = [&](int c) {
+      return ga.dfinal && live && c < a.dk ? ga.dfinal[sat + (long long)c * a.dv] : 0.0f;
+    };
+#pragma unroll
+    for (int p = 0; p < SP; ++p)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = group * SC + p * 16 + 2 * j;
+        S[p][j] = make_float2(initial(c), initial(c + 1));
+      }
+    // dO of the chunk of step `it` into f, and the largest of it.
+    float2 f[8];
+    float omax = 0.0f;
+    auto take = [&](int it) {
+      const int s = it % ST;
+      if (!wait(&bars.full[s], (it / ST) & 1)) return false;
+      const T *xs = reinterpret_cast<const T *>(stages + s * kStage + kStage - kRows16) +
+                    group * TK * 128 + row;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        f[j] = STAGED ? make_float2(to_acc(xs[2 * j * 128]), to_acc(xs[(2 * j + 1) * 128]))
+                      : make_float2(to_acc(vr[STAGED ? 0 : 2 * j]),
+                                    to_acc(vr[STAGED ? 0 : 2 * j + 1]));
+      omax = max16(0.0f, f);
+      __syncwarp();
+      if (lane == 0) bar_arrive(&bars.empty[s]);
+      return true;
+    };
+    bool ok = true;
+    if (sp.chunks > 0) {
+      fetch(0);
+      ss = bound_scale(agree.largest(state_max(), 0.0f).x);
+#pragma unroll
+      for (int p = 0; p < SP; ++p)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) S[p][j] = mul2(S[p][j], both(ss));
+      put_state(chunk_of(0));
+      ok = take(0);
+    }
+    for (int it = 0; it < sp.chunks && ok; ++it) {
+      const uint32_t ph = it & 1;
+      const int c = chunk_of(it);
+      const float *gates = gates_of(it) + group * TK;
+      const float *chunk = gates_of(it) + kChunkAt;
+      uint32_t r[16];
+      float2 x[8];
+      // While P is computed: the scales, and dO as an operand.
+      const float2 most = agree.largest(state_max(), omax);
+      const float Gamma = chunk[0], inv_s = scale_inverse(ss), smax = most.x * inv_s;
+      const float os = bound_scale(most.y);
+      const float by = chunk[1] * smax + chunk[2] * most.y;
+      const float bw = fmaxf(by * chunk[3] * chunk[4], chunk[5] * most.y);
+      const float ys = bound_scale(by), ws = bound_scale(bw);
+      const float inv_y = scale_inverse(ys);
+      const float next_ss = bound_scale(fmaf(Gamma, smax, 256.0f * bw));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = mul2(f[j], both(os));
+      put_split(lb + kColWh + group * 8, lb + kColWl + group * 8, x);
+      tmem_wait_st();
+      warp_arrive(&bars.of, lane);
+      // dU
+      if (!(ok = wait(&bars.p, ph) && wait(&bars.n, ph))) break;
+      tc_fence_after();
+      tmem_ld(lb + kColN + group * TK, r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        x[j] = mul2(pair(r, j), mul2(gate(gates + 64, j), both(scale_inverse(os) * ys)));
+      tmem_ld(lb + kColP + group * TK, r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        x[j] = fma2(mul2(gate(gates, j), both(inv_s * ys)), pair(r, j), x[j]);
+      put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, x);
+      tmem_wait_st();
+      warp_arrive(&bars.y, lane);
+      // scale gamma dO, where X was (every warp has read its part of X: they
+      // met when dU was ready)
+      if (!(ok = wait(&bars.e, ph))) break;
+      tc_fence_after();
+      tmem_ld(lb + kColP + group * TK, r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = mul2(f[j], mul2(gate(gates + 5 * 64, j), both(ws)));
+      put_split(lb + kColN + group * 8, lb + kColN + 32 + group * 8, f);
+      tmem_wait_st();
+      warp_arrive(&bars.u, lane);
+      // gamma beta F
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 b = mul2(gate(gates + 2 * 64, j), both(inv_y));
+        x[j] = mul2(pair(r, j), mul2(mul2(b, gate(gates + 4 * 64, j)), both(ws)));
+      }
+      put_split(lb + kColWh + group * 8, lb + kColWl + group * 8, x);
+      tmem_wait_st();
+      warp_arrive(&bars.w, lane);
+      // F itself, and dV = beta F
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        x[j] = mul2(pair(r, j), mul2(gate(gates + 2 * 64, j), both(inv_y)));
+      float *dst = rows + saved(c) * (64 * 128) + group * TK * 128 + row;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dst[2 * j * 128] = x[j].x;
+        dst[(2 * j + 1) * 128] = x[j].y;
+        x[j] = mul2(x[j], gate(gates + 3 * 64, j));
+      }
+      if (STAGED) {
+        if (it > 0 && !(ok = wait(&bars.got, ph ^ 1))) break;
+        T *out = reinterpret_cast<T *>(stages + ST * kStage) + group * TK * 128 + row;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          out[2 * j * 128] = from_acc<T>(x[j].x);
+          out[(2 * j + 1) * 128] = from_acc<T>(x[j].y);
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bars.put);
+      } else if (live) {
+        const long long r0 = (long long)c * kChunk + group * TK;
+        const long long left = sp.rows - r0;
+        T *out = static_cast<T *>(ga.dv) + out_row(a, sp.b, sp.row0 + r0, packed, h) + dvr;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (2 * j < left) out[2 * j * ostep] = from_acc<T>(x[j].x);
+          if (2 * j + 1 < left) out[(2 * j + 1) * ostep] = from_acc<T>(x[j].y);
+        }
+      }
+      const bool more = it + 1 < sp.chunks;
+      if (more) {
+        fetch(it + 1);
+        if (!(ok = take(it + 1))) break;
+      }
+      // The gradient of the state before
+      const float keep = Gamma * inv_s * next_ss, add = scale_inverse(ws) * next_ss;
+      if (!(ok = wait(&bars.s, ph))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int p = 0; p < SP; ++p) {
+        tmem_ld(lb + kColD + group * SC + p * 16, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          S[p][j] = fma2(S[p][j], both(keep), mul2(pair(r, j), both(add)));
+      }
+      ss = next_ss;
+      if (more) put_state(c - 1);
+    }
+    if (ok && ga.dinitial && live) {
+      const float inv = scale_inverse(ss);
+#pragma unroll
+      for (int p = 0; p < SP; ++p)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int c = group * SC + p * 16 + 2 * j;
+          if (c < a.dk) ga.dinitial[sat + (long long)c * a.dv] = S[p][j].x * inv;
+          if (c + 1 < a.dk) ga.dinitial[sat + (long long)(c + 1) * a.dv] = S[p][j].y * inv;
+        }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kScanWarps) tmem_free(tm, 512);
+}
+
+}  // namespace fftgb

@@ -10,4 +10,12 @@ cudaError_t launch_delta<__half>(const DeltaArgs &a, void *workspace, cudaStream
   return a.dk <= 64 ? delta_forward_t<__half, 64>(a, ws, st) : delta_forward_t<__half, 128>(a, ws, st);
 }
 
+template <>
+cudaError_t launch_delta_grad<__half>(const DeltaArgs &a, const DeltaGradArgs &g, void *workspace,
+                                cudaStream_t st) {
+  char *ws = static_cast<char *>(workspace);
+  return a.dk <= 64 ? delta_backward_t<__half, 64>(a, g, ws, st)
+                    : delta_backward_t<__half, 128>(a, g, ws, st);
+}
+
 }  // namespace fftgb

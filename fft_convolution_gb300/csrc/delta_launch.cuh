@@ -2,8 +2,8 @@
 // sequences, for one element type.
 #pragma once
 
-#include "delta_prep.cuh"
-#include "delta_scan.cuh"
+#include "delta_back.cuh"
+#include "delta_grad.cuh"
 
 namespace fftgb {
 
@@ -75,6 +75,72 @@ cudaError_t delta_forward_t(const DeltaArgs &a, char *ws, cudaStream_t st) {
   if (e == cudaSuccess)
     e = delta_scan<T, DK, false>(a, plan, ws + w.kq, ws + w.images, nullptr, nullptr, status, st);
   return e;
+}
+
+template <typename T, int DK, bool STAGED>
+cudaError_t delta_back_t(const DeltaArgs &a, const DeltaGradArgs &g, const DeltaPlan &plan,
+                         const char *kq, const char *images, float *dstates, float *rows,
+                         int *status, cudaStream_t st) {
+  constexpr size_t smem = scan_smem(DK, Terms<T>::value, STAGED);
+  static DeviceOnce once;
+  auto kern = delta_back_kernel<T, DK, STAGED>;
+  cudaError_t e = smem_limit_once((const void *)kern, smem, once);
+  if (e != cudaSuccess) return e;
+  const long long blocks = a.batch * a.vheads * ((a.dv + 127) / 128);
+  kern<<<(unsigned)blocks, kScanThreads, smem, st>>>(a, g, plan, kq, images, dstates, rows, status);
+  return cudaGetLastError();
+}
+template <typename T, int DK>
+cudaError_t delta_back(const DeltaArgs &a, const DeltaGradArgs &g, const DeltaPlan &plan,
+                       const char *kq, const char *images, float *dstates, float *rows,
+                       int *status, cudaStream_t st) {
+  if constexpr (sizeof(T) == 2)
+    if (a.dv % 8 == 0 && (((uintptr_t)g.dout | (uintptr_t)g.dv) & 15u) == 0)
+      return delta_back_t<T, DK, true>(a, g, plan, kq, images, dstates, rows, status, st);
+  return delta_back_t<T, DK, false>(a, g, plan, kq, images, dstates, rows, status, st);
+}
+
+template <typename T, int DK, bool PARTIAL>
+cudaError_t delta_grad_t(const DeltaArgs &a, const DeltaGradArgs &g, const DeltaPlan &plan,
+                         const char *kq, const char *back, const float *states,
+                         const float *dstates, float *es, float *fs, int *status,
+                         cudaStream_t st) {
+  static DeviceOnce once;
+  auto kern = delta_grad_kernel<T, DK, PARTIAL>;
+  cudaError_t e = smem_limit_once((const void *)kern, grad_smem(), once);
+  const long long chunks = plan.chunks_max;
+  if (e != cudaSuccess || chunks == 0) return e;
+  kern<<<(unsigned)(chunks * a.vheads), kGradThreads, grad_smem(), st>>>(
+      a, g, plan, kq, back, states, dstates, es, fs, status);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !PARTIAL) return e;
+  delta_grad_sum_kernel<T, DK>
+      <<<dim3((unsigned)(chunks * a.kheads), 2), 256, 0, st>>>(a, g, plan, es, fs);
+  return cudaGetLastError();
+}
+
+template <typename T, int DK>
+cudaError_t delta_backward_t(const DeltaArgs &a, const DeltaGradArgs &g, char *ws,
+                             cudaStream_t st) {
+  int *status = device_status_word();
+  if (!status) return cudaErrorInvalidDevice;
+  const DeltaLayout w(a, a.offsets != nullptr, true);
+  auto floats = [&](size_t at) { return reinterpret_cast<float *>(ws + at); };
+  char *kq = ws + w.kq, *images = ws + w.images, *back = ws + w.back;
+  DeltaPlan plan;
+  cudaError_t e = delta_make_plan<T>(a, w, ws, plan, st);
+  if (e == cudaSuccess) e = delta_prep_t<T, DK, false>(a, plan, kq, images, status, st);
+  if (e == cudaSuccess) e = delta_prep_t<T, DK, true>(a, plan, kq, back, status, st);
+  if (e == cudaSuccess)
+    e = delta_scan<T, DK, true>(a, plan, kq, images, floats(w.state), floats(w.e), status, st);
+  if (e == cudaSuccess)
+    e = delta_back<T, DK>(a, g, plan, kq, back, floats(w.dstate), floats(w.f), status, st);
+  if (e != cudaSuccess) return e;
+  return a.vheads == a.kheads
+             ? delta_grad_t<T, DK, false>(a, g, plan, kq, back, floats(w.state), floats(w.dstate),
+                                          floats(w.e), floats(w.f), status, st)
+             : delta_grad_t<T, DK, true>(a, g, plan, kq, back, floats(w.state), floats(w.dstate),
+                                         floats(w.e), floats(w.f), status, st);
 }
 
 }  // namespace fftgb

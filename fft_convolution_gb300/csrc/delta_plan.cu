@@ -64,8 +64,10 @@ cudaError_t launch_delta_plan(const int *offsets, long long batch, long long tok
 }
 
 size_t delta_workspace_bytes(const DeltaArgs &a, bool packed) {
-  const DeltaLayout w(a, packed, false);
-  return w.bytes;
+  return DeltaLayout(a, packed, false).bytes;
+}
+size_t delta_grad_workspace_bytes(const DeltaArgs &a, bool packed) {
+  return DeltaLayout(a, packed, true).bytes;
 }
 
 }  // namespace fftgb

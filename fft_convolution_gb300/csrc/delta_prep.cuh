@@ -21,6 +21,7 @@
 // BACK image: (I + beta A)^-T and M^T; per token
 //   0: Gamma/gamma 2^ek   1: scale 2^em   2: 2^et   3: beta
 //   4: -gamma beta 2^ek   5: scale gamma 2^eq
+// and in both 6: 2^ek, 7: 2^eq,
 // where 2^-e is the scale of a token's row of K (ek), Q (eq), of the inverse
 // (et) and of M (em).
 //
@@ -324,9 +325,10 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
         const float2 zero = make_float2(0.0f, 0.0f);
         const float gam = decay_between(G[tid], zero), dec = decay_between(G[63], G[tid]);
         const float bt = beta_s[tid];
-        const float ga[kGates] = {-gam * ek, dec * ek, bt * et, gam * (eq / em), a.scale * em, et};
-        const float gb[kGates] = {dec * ek, a.scale * em, et, bt, -gam * bt * ek,
-                                  a.scale * gam * eq};
+        const float ga[kGates] = {-gam * ek, dec * ek, bt * et, gam * (eq / em),
+                                  a.scale * em, et, ek, eq};
+        const float gb[kGates] = {dec * ek, a.scale * em, et, bt,
+                                  -gam * bt * ek, a.scale * gam * eq, ek, eq};
         const float ba = fabsf(bt) * sum_t[tid], sc = fabsf(a.scale);
         float b[5];
         b[0] = 2.0f * DK * (BACK ? dec : gam) * ek;

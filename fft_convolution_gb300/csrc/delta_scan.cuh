@@ -190,12 +190,14 @@ __device__ __forceinline__ void mma_state(uint32_t d, uint32_t hi, uint32_t lo, 
              idesc_tokens, term > 0 || k > 0);
   }
 }
-// A B^T for 64-token A (two parts) and a 64 x 64 matrix of the image.
-template <bool LEAD>
+// A B^T for 64-token A (two parts; ONE: the leading one is all of it) and a
+// 64 x 64 matrix of the image.
+template <bool LEAD, bool ONE = false>
 __device__ __forceinline__ void mma_inner(uint32_t d, uint32_t hi, uint32_t lo, uint32_t m,
                                           bool accumulate) {
 #pragma unroll
   for (int term = 0; term < (LEAD ? 1 : 3); ++term) {
+    if (ONE && term == 1) continue;
     const uint32_t ta = term == 1 ? lo : hi, tb = m + (term == 2 ? kTile : 0);
 #pragma unroll
     for (int k = 0; k < 4; ++k)

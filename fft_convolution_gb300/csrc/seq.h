@@ -72,11 +72,23 @@ struct DeltaArgs {
   const int *slots;
   long long pool;
 };
+// The gradients' own arrays: contiguous, laid out like the inputs without
+// strides ([sequence][token][head][..], packed: [row][head][..]).
+struct DeltaGradArgs {
+  const void *dout;
+  const float *dfinal;  // may be null (zero)
+  void *dq, *dk, *dv;
+  float *dg, *dbeta, *dinitial;  // dinitial may be null
+};
 cudaError_t launch_delta_step(int dtype, const DeltaArgs &a, cudaStream_t st);
 // Whole sequences, in chunks; `workspace` holds delta_workspace_bytes().
 size_t delta_workspace_bytes(const DeltaArgs &a, bool packed);
 template <typename T>
 cudaError_t launch_delta(const DeltaArgs &a, void *workspace, cudaStream_t st);
+size_t delta_grad_workspace_bytes(const DeltaArgs &a, bool packed);
+template <typename T>
+cudaError_t launch_delta_grad(const DeltaArgs &a, const DeltaGradArgs &g, void *workspace,
+                              cudaStream_t st);
 // Fills row0 and chunk0 (batch + 1 entries each) from offsets (delta_plan.cu).
 cudaError_t launch_delta_plan(const int *offsets, long long batch, long long tokens, int *row0,
                               int *chunk0, cudaStream_t st);

@@ -252,6 +252,45 @@ int fft_delta_rule(const fft_delta_desc *desc, const void *q, const void *k, con
   }
 }
 
+size_t fft_delta_rule_backward_workspace_bytes(const fft_delta_desc *desc, int packed) {
+  DeltaArgs a;
+  if (delta_sizes(desc, kDeltaMaxDk, &a) != FFT_OK || delta_chunks_check(a, packed != 0) != FFT_OK)
+    return 0;
+  return delta_grad_workspace_bytes(a, packed != 0);
+}
+
+int fft_delta_rule_backward(const fft_delta_desc *desc, const void *dout, const void *q,
+                            const void *k, const void *v, const float *g, const float *beta,
+                            const int32_t *offsets, const float *initial_state,
+                            const float *dfinal_state, void *dq, void *dk, void *dv, float *dg,
+                            float *dbeta, float *dinitial_state, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+  DeltaArgs a;
+  int rc = delta_check(desc, kDeltaMaxDk, q, k, v, g, beta, &a);
+  if (rc == FFT_OK) rc = delta_chunks_check(a, offsets != nullptr);
+  if (rc != FFT_OK) return rc;
+  if (a.batch == 0) return FFT_OK;
+  const size_t need = delta_grad_workspace_bytes(a, offsets != nullptr);
+  if ((a.tokens > 0 && (!dout || !dq || !dk || !dv || !dg || !dbeta)) || workspace_bytes < need ||
+      (!workspace && need > 0))
+    return FFT_ERR_INVALID_ARG;
+  for (const void *p : {dout, (const void *)dq, (const void *)dk, (const void *)dv})
+    if (off_element(p, desc->dtype)) return FFT_ERR_MISALIGNED;
+  for (const void *p : {(const void *)initial_state, (const void *)dfinal_state, (const void *)dg,
+                        (const void *)dbeta, (const void *)dinitial_state, (const void *)offsets})
+    if (off_element(p, FFT_ELEM_F32)) return FFT_ERR_MISALIGNED;
+  if (misaligned(workspace)) return FFT_ERR_MISALIGNED;
+  a.offsets = offsets;
+  a.state_in = initial_state;
+  const DeltaGradArgs ga{dout, dfinal_state, dq, dk, dv, dg, dbeta, dinitial_state};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  switch (desc->dtype) {
+    case FFT_ELEM_F32: return finish(launch_delta_grad<float>(a, ga, workspace, st));
+    case FFT_ELEM_BF16: return finish(launch_delta_grad<__nv_bfloat16>(a, ga, workspace, st));
+    default: return finish(launch_delta_grad<__half>(a, ga, workspace, st));
+  }
+}
+
 int fft_delta_rule_step(const fft_delta_desc *desc, const void *q, const void *k, const void *v,
                         const float *g, const float *beta, float *state, const int32_t *slots,
                         int64_t pool, void *o, void *stream) {

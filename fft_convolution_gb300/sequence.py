@@ -292,6 +292,38 @@ def delta_rule(q, k, v, g, beta, scale=None, initial_state=None, offsets=None, o
     return out, final
 
 
+def delta_rule_backward(do, q, k, v, g, beta, scale=None, initial_state=None, offsets=None,
+                        dfinal_state=None, stream=None):
+    """(dq, dk, dv, dg, dbeta, dinitial_state) of delta_rule, from the gradient
+    of o (like v) and of the final state (None: zero); the other arguments
+    as in the forward call (see fft_delta_rule_backward)."""
+    batch, packed = _packing(q, offsets)
+    context, handle = _on(stream)
+    with context:
+        q, k, v, desc = _delta_inputs(q, k, v, g, beta, scale, batch, packed)
+        _device(q, do, initial_state, dfinal_state, offsets)
+        if do.shape != v.shape or do.dtype != v.dtype:
+            raise ValueError("do must be like v")
+        do = do.contiguous()
+        if packed:
+            offsets = offsets.to(torch.int32).contiguous()
+        shape = (batch, desc.vheads, desc.dk, desc.dv)
+        initial_state = _states(initial_state, shape, "initial_state")
+        dfinal_state = _states(dfinal_state, shape, "dfinal_state")
+        new = lambda like, dtype: torch.empty(like.shape, dtype=dtype, device=v.device)  # noqa: E731
+        dq, dk, dv = new(q, q.dtype), new(k, q.dtype), new(v, q.dtype)
+        dg, dbeta = new(g, torch.float32), new(g, torch.float32)
+        dinitial = torch.empty(shape, dtype=torch.float32, device=v.device)
+        nbytes = _lib.fft_delta_rule_backward_workspace_bytes(ctypes.byref(desc), packed)
+        ws = _workspace(nbytes, v.device)
+        _check(_lib.fft_delta_rule_backward(
+            ctypes.byref(desc), do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            g.data_ptr(), beta.data_ptr(), _ptr(offsets), _ptr(initial_state), _ptr(dfinal_state),
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(),
+            dinitial.data_ptr(), ws.data_ptr(), nbytes, handle), "fft_delta_rule_backward")
+    return dq, dk, dv, dg, dbeta, dinitial
+
+
 def delta_rule_step(q, k, v, g, beta, state, slots=None, scale=None, out=None, stream=None):
     """One or a few tokens per sequence of the gated delta rule (see
     fft_delta_rule_step): returns o [batch, tokens, value heads, dv] and

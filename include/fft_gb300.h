@@ -571,6 +571,29 @@ int fft_delta_rule(const fft_delta_desc *desc, const void *q, const void *k, con
                    size_t workspace_bytes, void *stream);
 
 /*
+ * fft_delta_rule_backward -- the gradients of fft_delta_rule, from the
+ * gradient of o and (NULL: zero) that of the final state.  Nothing of the
+ * forward call is needed but its inputs: the states are computed again.
+ *   dout, dv       like o;  dq, dk: [batch][tokens][kheads][dk] ([tokens]..
+ *                  with offsets), of the same type, contiguous: summed in
+ *                  float over the value heads that share a key head.
+ *   dg, dbeta      float [batch][tokens][vheads] ([tokens]..), contiguous.
+ *   dfinal_state, dinitial_state  float [batch][vheads][dk][dv]; dinitial_state
+ *                  may be NULL, and may be dfinal_state.
+ *   workspace      fft_delta_rule_backward_workspace_bytes(desc, offsets !=
+ *                  NULL) bytes: about 130 KB per 64 tokens and value head of
+ *                  128 x 128 for the states, twice that with their gradients
+ *                  and the rest.
+ */
+size_t fft_delta_rule_backward_workspace_bytes(const fft_delta_desc *desc, int packed);
+int fft_delta_rule_backward(const fft_delta_desc *desc, const void *dout, const void *q,
+                            const void *k, const void *v, const float *g, const float *beta,
+                            const int32_t *offsets, const float *initial_state,
+                            const float *dfinal_state, void *dq, void *dk, void *dv, float *dg,
+                            float *dbeta, float *dinitial_state, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/*
  * fft_delta_rule_step -- the recurrence as it stands, for a few tokens per
  * sequence (decoding): the states are updated in place.
  *   state  float [pool][vheads][dk][dv].

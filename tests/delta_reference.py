@@ -69,6 +69,8 @@ def backward(do, q, k, v, g, beta, scale=None, state=None, dfinal=None):
         d = d - ke[t][:, :, None] * dy[:, None, :]
         dg[t] = (d * before).sum((-1, -2))
         d = d * g[t].exp()[:, None, None]
+
     def shared(t):
-        return t.reshape(t.shape[0], -1, group, t.shape[2]).sum(2)
+        return t.reshape(t.shape[0], heads // group, group, t.shape[2]).sum(2)
+
     return shared(dq), shared(dk), dv, dg, dbeta, d
