@@ -99,14 +99,14 @@ __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t a, uint32_t ablock
                                          bool accumulate) {
   constexpr uint32_t idesc = mma_desc(128, 64, false, false);
 #pragma unroll
-  for (int term = 0; term < 3; ++term) {
+  for (int term = 2; term >= 0; --term) {  // trailing parts first (delta_scan.cuh)
     if (term == 2 && b_exact) continue;
     const uint32_t ta = a + (term == 1 ? alo : 0), tb = b + (term == 2 ? blo : 0);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       mma_ss(d, tile_desc(ta + (k >> 2) * ablock + (k & 3) * 32, 16),
              tile_desc(tb + (k >> 2) * bblock + (k & 3) * 32, 16), idesc,
-             accumulate || term > 0 || k > 0);
+             accumulate || term < (b_exact ? 1 : 2) || k > 0);
   }
 }
 // K^T or Q^T (MN-major, 64 tokens) times a 64 x 64 matrix in two parts,
@@ -117,12 +117,12 @@ __device__ __forceinline__ void mma_tokens(uint32_t d, uint32_t a, uint32_t b, b
   constexpr uint32_t kPlane = 2 * (DK / 64) * kTile;
   constexpr uint32_t block = DK == 128 ? 2 * kTile : 0;  // DK = 64: lanes 64 .. 127 repeat
 #pragma unroll
-  for (int term = 0; term < (NT == 1 ? 2 : 3); ++term) {
+  for (int term = NT == 1 ? 1 : 2; term >= 0; --term) {
     const uint32_t ta = a + (term == 2 ? kPlane : 0), tb = b + (term == 1 ? kTile : 0);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       mma_ss(d, tile_desc(ta + k * 2048, block), tile_desc(tb + (B_MN ? k * 2048 : k * 32), 16),
-             idesc, accumulate || term > 0 || k > 0);
+             idesc, accumulate || term < (NT == 1 ? 1 : 2) || k > 0);
   }
 }
 

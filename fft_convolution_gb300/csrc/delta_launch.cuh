@@ -21,17 +21,18 @@ cudaError_t delta_make_plan(const DeltaArgs &a, const DeltaLayout &w, char *ws, 
   return launch_delta_plan(a.offsets, a.batch, a.tokens, row0, chunk0, st);
 }
 
-template <typename T, int DK, bool BACK>
+template <typename T, int DK, bool GRAD>
 cudaError_t delta_prep_t(const DeltaArgs &a, const DeltaPlan &plan, char *kq, char *images,
-                         int *status, cudaStream_t st) {
+                         char *back, int *status, cudaStream_t st) {
   static DeviceOnce once;
-  const void *kern = (const void *)delta_prep_kernel<T, DK, BACK>;
+  const void *kern = (const void *)delta_prep_kernel<T, DK, GRAD>;
   cudaError_t e = smem_limit_once(kern, prep_smem<T, DK>(), once);
   if (e != cudaSuccess) return e;
   const long long blocks = plan.chunks_max * a.kheads;
   if (blocks == 0) return cudaSuccess;
-  delta_prep_kernel<T, DK, BACK>
-      <<<(unsigned)blocks, kPrepThreads, prep_smem<T, DK>(), st>>>(a, plan, kq, images, status);
+  delta_prep_kernel<T, DK, GRAD>
+      <<<(unsigned)blocks, kPrepThreads, prep_smem<T, DK>(), st>>>(a, plan, kq, images, back,
+                                                                       status);
   return cudaGetLastError();
 }
 
@@ -71,7 +72,7 @@ cudaError_t delta_forward_t(const DeltaArgs &a, char *ws, cudaStream_t st) {
   const DeltaLayout w(a, a.offsets != nullptr, false);
   DeltaPlan plan;
   cudaError_t e = delta_make_plan<T>(a, w, ws, plan, st);
-  if (e == cudaSuccess) e = delta_prep_t<T, DK, false>(a, plan, ws + w.kq, ws + w.images, status, st);
+  if (e == cudaSuccess) e = delta_prep_t<T, DK, false>(a, plan, ws + w.kq, ws + w.images, nullptr, status, st);
   if (e == cudaSuccess)
     e = delta_scan<T, DK, false>(a, plan, ws + w.kq, ws + w.images, nullptr, nullptr, status, st);
   return e;
@@ -129,8 +130,7 @@ cudaError_t delta_backward_t(const DeltaArgs &a, const DeltaGradArgs &g, char *w
   char *kq = ws + w.kq, *images = ws + w.images, *back = ws + w.back;
   DeltaPlan plan;
   cudaError_t e = delta_make_plan<T>(a, w, ws, plan, st);
-  if (e == cudaSuccess) e = delta_prep_t<T, DK, false>(a, plan, kq, images, status, st);
-  if (e == cudaSuccess) e = delta_prep_t<T, DK, true>(a, plan, kq, back, status, st);
+  if (e == cudaSuccess) e = delta_prep_t<T, DK, true>(a, plan, kq, images, back, status, st);
   if (e == cudaSuccess)
     e = delta_scan<T, DK, true>(a, plan, kq, images, floats(w.state), floats(w.e), status, st);
   if (e == cudaSuccess)

@@ -4,12 +4,15 @@
 //
 // One block per chunk and key head.  [K; Q] K^T (128 x 64) is one product on
 // the tensor cores, kept in tensor memory for all value heads that share the
-// key head; each of the 128 threads then owns one row of it.  The inverse is
-// taken in fp32: the four 16 x 16 diagonal blocks by substitution (one warp
-// each, one column per lane), the blocks below them by products, doubling
-// the solved size twice (T_21 = -T_22 L_21 T_11).  Substitution alone would
-// be a chain of 64 dependent steps, and a power series of L would cancel
-// catastrophically for keys that repeat.
+// key head; each of the 128 threads then owns one row of it.  With A the
+// strictly lower triangular matrix of delta.cuh and R = (I + A beta)^-1 A,
+//   (I + A beta)^-1 = I - R beta  and  (I + beta A)^-1 = I - beta R,
+// so one R serves both scans.  It is taken in fp32: the four 16 x 16 diagonal
+// blocks by substitution (one warp each, one column per lane), the blocks
+// below them by products, doubling the solved size twice:
+//   R_21 = (I - R_22 beta_2) A_21 (I - beta_1 R_11).
+// Substitution alone would be a chain of 64 dependent steps, and a power
+// series of A would cancel catastrophically for keys that repeat.
 //
 // Everything is written in exactly the layout of the scans' shared memory,
 // so they fetch a chunk with two bulk copies, whatever the inputs' type,
@@ -51,30 +54,41 @@ template <typename T, int DK> constexpr size_t prep_smem() {
   return 1024 + (size_t)(tiles > fp32 ? tiles : fp32);
 }
 
-// 64 x 64 lower triangular fp32 matrix (what lies above its diagonal is not
-// read), or its transpose, to the leading and trailing tile, rows scaled; the
-// rows' inverse scales go to `inv`, the sums of their absolute values to `sum`.
-template <bool TRANS>
-__device__ __forceinline__ void write_image(const float *m, char *dst, float *inv, float *sum,
-                                            int tid) {
+// A 64 x 64 lower triangular fp32 matrix m (what lies above its diagonal is
+// not read), or its transpose (TRANS), to the leading and trailing tile, rows
+// scaled; the rows' inverse scales go to `inv`, the sums of their absolute
+// values to `sum`.  INV: of m = R the inverse, I - R beta, or (TRANS) the
+// transpose of I - beta R.
+template <bool TRANS, bool INV>
+__device__ __forceinline__ void write_image(const float *m, const float *beta, char *dst,
+                                            float *inv, float *sum, int tid) {
 #pragma unroll
   for (int i = tid; i < 64 * 8; i += kPrepThreads) {
     const int r = i >> 3, c = i & 7;
     float f[8];
     if constexpr (TRANS) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = c * 8 + k >= r ? m[(c * 8 + k) * kPitch + r] : 0.0f;
+      for (int k = 0; k < 8; ++k) f[k] = m[(c * 8 + k) * kPitch + r];
     } else {
       const float4 x = *reinterpret_cast<const float4 *>(m + r * kPitch + c * 8);
       const float4 y = *reinterpret_cast<const float4 *>(m + r * kPitch + c * 8 + 4);
       f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
       f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = c * 8 + k <= r ? f[k] : 0.0f;
     }
+    if constexpr (INV) {
+      const float4 x = *reinterpret_cast<const float4 *>(beta + c * 8);
+      const float4 y = *reinterpret_cast<const float4 *>(beta + c * 8 + 4);
+      f[0] *= -x.x; f[1] *= -x.y; f[2] *= -x.z; f[3] *= -x.w;
+      f[4] *= -y.x; f[5] *= -y.y; f[6] *= -y.z; f[7] *= -y.w;
+    }
+    const int d = r - c * 8;  // the diagonal's place among the eight
     float t = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) t += fabsf(f[k]);
+    for (int k = 0; k < 8; ++k) {
+      if (TRANS ? k < d : k > d) f[k] = 0.0f;
+      if (INV && k == d) f[k] = 1.0f;
+      t += fabsf(f[k]);
+    }
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     const float s = row_scale(lane_max<8>(max8(f)));
@@ -116,7 +130,9 @@ __device__ __forceinline__ void running_decay(const float *g, long long step, in
   }
 }
 __device__ __forceinline__ float decay_between(float2 i, float2 j) {
-  return exp2f((i.x - j.x) + (i.y - j.y));
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"((i.x - j.x) + (i.y - j.y)));
+  return e;
 }
 
 // Rows 0 .. 63 of K or Q into its tiles in shared memory and in the image;
@@ -155,55 +171,62 @@ __device__ __forceinline__ void load_rows(const T *src, long long stride, int n,
   }
 }
 
-// Z = P X for the lower triangular X at (lo, lo), or -P X with X at (hi, lo):
-// `ROWS` rows from `row` of column `col`, SIZE summed indexes, P at (pr, pc).
+// z -= P (beta X): ROWS rows of one column, SIZE summed indexes; p points at
+// the first of the rows, x at the column, beta at the first summed index.
 template <int SIZE, int ROWS>
-__device__ __forceinline__ void block_product(const float *p, const float *x, float (&z)[ROWS]) {
-#pragma unroll
-  for (int o = 0; o < ROWS; ++o) z[o] = 0.0f;
+__device__ __forceinline__ void block_product(const float *p, const float *x, const float *beta,
+                                              float (&z)[ROWS]) {
 #pragma unroll 2
   for (int k = 0; k < SIZE; k += 4) {
-    float xs[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) xs[e] = x[(k + e) * kPitch];
+    const float4 b = *reinterpret_cast<const float4 *>(beta + k);
+    const float x0 = b.x * x[k * kPitch], x1 = b.y * x[(k + 1) * kPitch];
+    const float x2 = b.z * x[(k + 2) * kPitch], x3 = b.w * x[(k + 3) * kPitch];
 #pragma unroll
     for (int o = 0; o < ROWS; ++o) {
       const float4 l = *reinterpret_cast<const float4 *>(p + o * kPitch + k);
-      z[o] = fmaf(l.x, xs[0], fmaf(l.y, xs[1], fmaf(l.z, xs[2], fmaf(l.w, xs[3], z[o]))));
+      z[o] = fmaf(-l.x, x0, fmaf(-l.y, x1, fmaf(-l.z, x2, fmaf(-l.w, x3, z[o]))));
     }
   }
 }
-// T_21 = -T_22 (L_21 T_11) for the pairs of SIZE x SIZE diagonal blocks.
-template <int SIZE> __device__ __forceinline__ void join_blocks(const float *L, float *X, int tid) {
+// R_21 for the pairs of SIZE x SIZE diagonal blocks: Z = A_21 (I - beta_1 R_11),
+// R_21 = Z - R_22 beta_2 Z.
+template <int SIZE>
+__device__ __forceinline__ void join_blocks(const float *A, float *R, const float *beta, int tid) {
   constexpr int PAIRS = 32 / SIZE, PER = kPrepThreads / PAIRS, ROWS = SIZE * SIZE / PER;
   const int pr = tid / PER, t = tid % PER;
   const int lo = pr * 2 * SIZE, hi = lo + SIZE;
   const int col = t % SIZE, rb = (t / SIZE) * ROWS;
   float z[ROWS];
-  block_product<SIZE, ROWS>(L + (hi + rb) * kPitch + lo, X + lo * kPitch + lo + col, z);
-  __syncthreads();
-  float *out = X + (hi + rb) * kPitch + lo + col;
+  const float *a21 = A + (hi + rb) * kPitch + lo;
+#pragma unroll
+  for (int o = 0; o < ROWS; ++o) z[o] = a21[o * kPitch + col];
+  block_product<SIZE, ROWS>(a21, R + lo * kPitch + lo + col, beta + lo, z);
+  float *out = R + (hi + rb) * kPitch + lo + col;
 #pragma unroll
   for (int o = 0; o < ROWS; ++o) out[o * kPitch] = z[o];
   __syncthreads();
-  block_product<SIZE, ROWS>(X + (hi + rb) * kPitch + hi, X + hi * kPitch + lo + col, z);
+  block_product<SIZE, ROWS>(R + (hi + rb) * kPitch + hi, R + hi * kPitch + lo + col, beta + hi, z);
   __syncthreads();
 #pragma unroll
-  for (int o = 0; o < ROWS; ++o) out[o * kPitch] = -z[o];
+  for (int o = 0; o < ROWS; ++o) out[o * kPitch] = z[o];
   __syncthreads();
 }
 
-template <typename T, int DK, bool BACK>
+// GRAD: the images of both scans.
+template <typename T, int DK, bool GRAD>
 __global__ void __launch_bounds__(kPrepThreads, 5)
-delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *images, int *status) {
+delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *images, char *back,
+                  int *status) {
   extern __shared__ char smem_raw[];
   __shared__ uint64_t bar;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int failed;
   __shared__ double carry;
   __shared__ float2 G[64];
-  __shared__ float beta_s[64], inv_kq[2 * 64], inv_t[64], inv_m[64], sum_t[64], sum_m[64];
-  __shared__ float most[2][5];
+  __shared__ float4 Gk[64];  // G, the scale of K's row
+  __shared__ __align__(16) float beta_s[64];
+  __shared__ float inv_kq[2 * 64], inv[4][64], sum[4][64];
+  __shared__ float most[2][8];
   constexpr int NT = Terms<T>::value;
   constexpr uint32_t kPlane = 2 * (DK / 64) * kTile;  // [K; Q], one term
 
@@ -238,13 +261,14 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
   if (warp == 0 && elect_one()) {
     constexpr uint32_t idesc = mma_desc(128, 64, false, false);
 #pragma unroll
-    for (int term = 0; term < (NT == 1 ? 1 : 3); ++term) {
-      // leading x leading, leading x trailing, trailing x leading
+    for (int term = NT == 1 ? 0 : 2; term >= 0; --term) {
+      // trailing x leading, leading x trailing, leading x leading
       const uint32_t ta = t0 + (term == 2 ? kPlane : 0), tb = t0 + (term == 1 ? kPlane : 0);
 #pragma unroll
       for (int k = 0; k < DK / 16; ++k) {
         const uint32_t at = (k >> 2) * 2 * kTile + (k & 3) * 32;
-        mma_ss(acc, tile_desc(ta + at, 16), tile_desc(tb + at, 16), idesc, term > 0 || k > 0);
+        mma_ss(acc, tile_desc(ta + at, 16), tile_desc(tb + at, 16), idesc,
+               term < (NT == 1 ? 0 : 2) || k > 0);
       }
     }
     mma_commit(&bar);
@@ -259,16 +283,17 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
       const float *g = a.g + c.b * a.sg.seq + c.row * a.sg.tok + hv * a.sg.head;
       const float *beta = a.beta + c.b * a.sb.seq + c.row * a.sb.tok + hv * a.sb.head;
       running_decay(g, a.sg.tok, c.n, tid, &carry, G);
-      if (tid < 64) beta_s[tid] = tid < c.n ? beta[tid * a.sb.tok] : 0.0f;
+      if (tid < 64) {
+        beta_s[tid] = tid < c.n ? beta[tid * a.sb.tok] : 0.0f;
+        Gk[tid] = make_float4(G[tid].x, G[tid].y, inv_kq[tid], 0.0f);
+      }
       __syncthreads();
       // Row i of A (threads 0 .. 63, from K K^T) or of M (64 .. 127), up to
-      // its diagonal.  Row i of the matrix to invert is A_ij beta_j, or beta_i
-      // A_ij (BACK).
+      // its diagonal (what lies above is arbitrary).
       const int i = tid & 63;
       const float2 gi = G[i];
-      const bool is_m = tid >= 64;
-      const float fi = inv_kq[tid] * (BACK && !is_m ? beta_s[i] : 1.0f);
-      float *row = (is_m ? X : L) + i * kPitch;
+      const float fi = inv_kq[tid];
+      float *row = (tid >= 64 ? X : L) + i * kPitch;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         if (half == 1 && (warp & 1) == 0) break;  // rows 0 .. 31 end before column 32
@@ -276,27 +301,31 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
         tmem_ld(acc + ((uint32_t)(warp * 32) << 16) + half * 32, r);
         tmem_wait_ld();
 #pragma unroll
-        for (int jj = 0; jj < 32; ++jj) {
-          const int j = half * 32 + jj;
-          float f = fi * inv_kq[j];
-          if (!BACK && !is_m) f *= beta_s[j];
-          // (above the diagonal the exponent would be positive)
-          const float x = decay_between(gi, j <= i ? G[j] : gi) * (__uint_as_float(r[jj]) * f);
-          row[j] = x;
+        for (int jj = 0; jj < 32; jj += 4) {
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 gj = Gk[half * 32 + jj + e];
+            x[e] = decay_between(gi, make_float2(gj.x, gj.y)) *
+                   (__uint_as_float(r[jj + e]) * (fi * gj.z));
+          }
+          *reinterpret_cast<float4 *>(row + half * 32 + jj) = make_float4(x[0], x[1], x[2], x[3]);
         }
       }
       __syncthreads();
-      write_image<BACK>(X, image + 2 * kTile, inv_m, sum_m, tid);
+      char *imageb = back + (ci * a.vheads + hv) * (long long)kImageBytes;
+      write_image<false, false>(X, beta_s, image + 2 * kTile, inv[1], sum[1], tid);
+      if constexpr (GRAD) write_image<true, false>(X, beta_s, imageb + 2 * kTile, inv[3], sum[3], tid);
       __syncthreads();
-      // Diagonal blocks: column `col` of the inverse of block `warp`, by
-      // substitution; both halves of the warp do the same columns.
+      // Diagonal blocks of R: column `col` of block `warp`, R_m = A_m - sum_p
+      // A_mp beta_p R_p; both halves of the warp do the same columns.
       {
         const int col = lane & 15, r0 = warp * 16;
         const float *l = L + r0 * kPitch + r0;
-        float x[16];
+        float x[16];  // beta R
 #pragma unroll
         for (int m = 0; m < 16; ++m) {
-          float s = m == col ? 1.0f : 0.0f;
+          float s = m > col ? l[m * kPitch + col] : 0.0f;
 #pragma unroll
           for (int p = 0; p < m; p += 4) {
             const float4 v = *reinterpret_cast<const float4 *>(l + m * kPitch + p);
@@ -305,50 +334,56 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
             if (p + 2 < m) s = fmaf(-v.z, x[p + 2], s);
             if (p + 3 < m) s = fmaf(-v.w, x[p + 3], s);
           }
-          x[m] = s;
-        }
-#pragma unroll
-        for (int m = 0; m < 16; ++m) {
+          x[m] = s * beta_s[r0 + m];
           // the other half of the warp: zeros right of the first of two blocks
-          if (lane < 16) X[(r0 + m) * kPitch + r0 + col] = x[m];
+          if (lane < 16) X[(r0 + m) * kPitch + r0 + col] = s;
           else if ((warp & 1) == 0) X[(r0 + m) * kPitch + r0 + 16 + col] = 0.0f;
         }
       }
       __syncthreads();
-      join_blocks<16>(L, X, tid);
-      join_blocks<32>(L, X, tid);
-      write_image<BACK>(X, image, inv_t, sum_t, tid);
+      join_blocks<16>(L, X, beta_s, tid);
+      join_blocks<32>(L, X, beta_s, tid);
+      write_image<false, true>(X, beta_s, image, inv[0], sum[0], tid);
+      if constexpr (GRAD) write_image<true, true>(X, beta_s, imageb, inv[2], sum[2], tid);
       __syncthreads();
       if (tid < 64) {
-        float *gates = reinterpret_cast<float *>(image + 4 * kTile);
-        const float ek = inv_kq[tid], eq = inv_kq[64 + tid], em = inv_m[tid], et = inv_t[tid];
-        const float2 zero = make_float2(0.0f, 0.0f);
-        const float gam = decay_between(G[tid], zero), dec = decay_between(G[63], G[tid]);
-        const float bt = beta_s[tid];
+        float *gates = reinterpret_cast<float *>(image + 4 * kTile) + tid;
+        const float ek = inv_kq[tid], eq = inv_kq[64 + tid], em = inv[1][tid], et = inv[0][tid];
+        const float gam = decay_between(G[tid], make_float2(0.0f, 0.0f));
+        const float dec = decay_between(G[63], G[tid]), bt = beta_s[tid];
         const float ga[kGates] = {-gam * ek, dec * ek, bt * et, gam * (eq / em),
                                   a.scale * em, et, ek, eq};
-        const float gb[kGates] = {dec * ek, a.scale * em, et, bt,
-                                  -gam * bt * ek, a.scale * gam * eq, ek, eq};
-        const float ba = fabsf(bt) * sum_t[tid], sc = fabsf(a.scale);
-        float b[5];
-        b[0] = 2.0f * DK * (BACK ? dec : gam) * ek;
-        b[1] = BACK ? sc * sum_m[tid] : ba;
-        b[2] = BACK ? sum_t[tid] : ba * dec * ek;
-        b[3] = gam * fabsf(bt) * ek;
-        b[4] = sc * gam * eq;
+        const float ba = fabsf(bt) * sum[0][tid], sc = fabsf(a.scale);
+        float b[8];
+        b[0] = 2.0f * DK * gam * ek;
+        b[1] = ba;
+        b[2] = ba * dec * ek;
 #pragma unroll
-        for (int k = 0; k < kGates; ++k) gates[k * 64 + tid] = BACK ? gb[k] : ga[k];
+        for (int k = 0; k < kGates; ++k) gates[k * 64] = ga[k];
+        if (tid == 63) gates[kChunkAt - 63] = gam;
+        if constexpr (GRAD) {
+          gates = reinterpret_cast<float *>(imageb + 4 * kTile) + tid;
+          const float gb[kGates] = {dec * ek, a.scale * inv[3][tid], inv[2][tid], bt,
+                                    -gam * bt * ek, a.scale * gam * eq, ek, eq};
 #pragma unroll
-        for (int k = 0; k < 5; ++k) {
+          for (int k = 0; k < kGates; ++k) gates[k * 64] = gb[k];
+          if (tid == 63) gates[kChunkAt - 63] = gam;
+          b[3] = 2.0f * DK * dec * ek;
+          b[4] = sc * sum[3][tid];
+          b[5] = sum[2][tid];
+          b[6] = gam * fabsf(bt) * ek;
+          b[7] = sc * gam * eq;
+        }
+#pragma unroll
+        for (int k = 0; k < (GRAD ? 8 : 3); ++k) {
           b[k] = lane_max<32>(b[k]);
           if (lane == 0) most[warp][k] = b[k];
         }
-        if (tid == 63) gates[kChunkAt] = gam;
       }
       __syncthreads();
-      if (tid < 5)
-        reinterpret_cast<float *>(image + 4 * kTile)[kChunkAt + 1 + tid] =
-            fmaxf(most[0][tid], most[1][tid]);
+      if (tid < (GRAD ? 8 : 3))
+        reinterpret_cast<float *>((tid < 3 ? image : imageb) + 4 * kTile)
+            [kChunkAt + (tid < 3 ? 1 + tid : tid - 2)] = fmaxf(most[0][tid], most[1][tid]);
     }
     tc_fence_before();
   }

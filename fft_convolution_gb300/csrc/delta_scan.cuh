@@ -176,18 +176,22 @@ __device__ __forceinline__ void scan_store(const DeltaArgs &a, const ScanSpan &s
 
 constexpr uint32_t idesc_tokens = mma_desc(128, 64, false, false);
 
+// Products of trailing parts come first: the accumulator cuts off below its
+// last bit at every step, which costs little while it is small (dbeta of 16384
+// tokens: 7.7e-7 off, with the leading parts first 1.9e-6).
+
 // S^T X^T into `d` (64 columns): left operand the state's two parts, right
 // one the chunk's X (K or Q).  LEAD: leading parts only.
 template <int DK, int NT, bool LEAD>
 __device__ __forceinline__ void mma_state(uint32_t d, uint32_t hi, uint32_t lo, uint32_t x) {
   constexpr uint32_t kPlane = 2 * (DK / 64) * kTile;
 #pragma unroll
-  for (int term = 0; term < (LEAD ? 1 : NT == 1 ? 2 : 3); ++term) {
+  for (int term = LEAD ? 0 : NT == 1 ? 1 : 2; term >= 0; --term) {
     const uint32_t ta = term == 1 ? lo : hi, tb = x + (term == 2 ? kPlane : 0);
 #pragma unroll
     for (int k = 0; k < DK / 16; ++k)
       mma_ts(d, ta + 8 * k, tile_desc(tb + (k >> 2) * 2 * kTile + (k & 3) * 32, 16),
-             idesc_tokens, term > 0 || k > 0);
+             idesc_tokens, term < (LEAD ? 0 : NT == 1 ? 1 : 2) || k > 0);
   }
 }
 // A B^T for 64-token A (two parts; ONE: the leading one is all of it) and a
@@ -196,13 +200,13 @@ template <bool LEAD, bool ONE = false>
 __device__ __forceinline__ void mma_inner(uint32_t d, uint32_t hi, uint32_t lo, uint32_t m,
                                           bool accumulate) {
 #pragma unroll
-  for (int term = 0; term < (LEAD ? 1 : 3); ++term) {
+  for (int term = LEAD ? 0 : 2; term >= 0; --term) {
     if (ONE && term == 1) continue;
     const uint32_t ta = term == 1 ? lo : hi, tb = m + (term == 2 ? kTile : 0);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       mma_ts(d, ta + 8 * k, tile_desc(tb + k * 32, 16), idesc_tokens,
-             accumulate || term > 0 || k > 0);
+             accumulate || term < (LEAD ? 0 : 2) || k > 0);
   }
 }
 // A X for 64-token A and the chunk's X (K or Q) as 64 tokens x DK.
@@ -212,12 +216,12 @@ __device__ __forceinline__ void mma_update(uint32_t d, uint32_t hi, uint32_t lo,
   constexpr uint32_t idesc = mma_desc(128, DK, false, true);
   constexpr uint32_t kPlane = 2 * (DK / 64) * kTile;
 #pragma unroll
-  for (int term = 0; term < (NT == 1 ? 2 : 3); ++term) {
+  for (int term = NT == 1 ? 1 : 2; term >= 0; --term) {
     const uint32_t ta = term == 1 ? lo : hi, tb = x + (term == 2 ? kPlane : 0);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       mma_ts(d, ta + 8 * k, tile_desc(tb + k * 2048, 2 * kTile), idesc,
-             accumulate || term > 0 || k > 0);
+             accumulate || term < (NT == 1 ? 1 : 2) || k > 0);
   }
 }
 
