@@ -235,6 +235,9 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
   const long long ci = blockIdx.x / a.kheads;
   DeltaChunk c;
   if (!delta_chunk(a, plan, ci, c)) return;
+  // First of all: the next block of this kernel starts on the multiprocessor
+  // only when this one has given back the right to allocate.
+  if (warp == 0) tmem_alloc(&tmem_slot, 64);
 
   // Tiles: 128 rows (K above Q) of 64 columns, kTile * 2 bytes each.
   char *tiles = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -246,8 +249,6 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
                    vec_rows<T>(a.k, a.sk), tiles, kqi, inv_kq, tid);
   load_rows<T, DK>(head_rows<T>(a.q, a.sq, c.b, c.row, hk), a.sq.tok, c.n, a.dk,
                    vec_rows<T>(a.q, a.sq), tiles + kTile, kqi + kTile, inv_kq + 64, tid);
-  __syncwarp();
-  if (warp == 0) tmem_alloc(&tmem_slot, 64);
   if (tid == 0) {
     bar_init(&bar, 1);
     failed = 0;
