@@ -17,9 +17,13 @@ namespace fftgb {
 
 constexpr int kClipThreads = 256;
 constexpr int kClipBlocksPerSm = 3;
-// Values per work item: enough that finding an item's tensor costs nothing,
-// few enough that items spread evenly over the blocks.
-constexpr long long kClipItem = 16384;
+// A work item is 32 KB of one tensor: each thread loads its eight 16-byte
+// vectors of it before it uses any.
+constexpr int kClipVectors = 8;
+constexpr long long kClipItemBytes = 16ll * kClipVectors * kClipThreads;
+__host__ __device__ __forceinline__ int clip_size(int dtype) {
+  return dtype == FFT_ELEM_F64 ? 8 : dtype == FFT_ELEM_F32 ? 4 : 2;
+}
 
 template <int N> struct ClipTable {
   const void *in[N];
@@ -32,23 +36,6 @@ template <int N> struct ClipTable {
 constexpr int kClipSmall = 72, kClipLarge = 960;  // 2.5 KB and 31.7 KB of kernel arguments
 static_assert(sizeof(ClipTable<kClipLarge>) + 64 <= 32764, "kernel arguments");
 
-// Sum of the squares of N values.  Their fp32 sum is exact enough (N is
-// small) unless it overflows or is so small that squares were lost: then,
-// which no ordinary gradient reaches, the squares are taken in fp64.
-template <int N> __device__ __forceinline__ double squares(const float (&v)[N]) {
-  float s = 0.0f, m = 0.0f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    s = fmaf(v[i], v[i], s);
-    m = fmaxf(m, fabsf(v[i]));
-  }
-  if (s < 1e37f && (s > 1e-24f || m == 0.0f)) return (double)s;
-  double d = 0.0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) d += (double)v[i] * (double)v[i];
-  return d;
-}
-
 template <int N> struct ClipItem {
   int t;
   long long begin, end;
@@ -60,77 +47,148 @@ template <int N> struct ClipItem {
       else hi = mid - 1;
     }
     t = lo;
-    begin = (item - tab.first[t]) * kClipItem;
-    end = begin + kClipItem;
+    const long long each = kClipItemBytes / clip_size(tab.dtype[t]);
+    begin = (item - tab.first[t]) * each;
+    end = begin + each;
     if (end > tab.numel[t]) end = tab.numel[t];
   }
 };
 
 // Calls f(vector of 16 bytes, index) on the aligned vectors of [begin, end)
 // and g(value, index) on what is left at both ends.
-template <typename T, int UNROLL, class F, class G>
+template <typename T, class F, class G>
 __device__ __forceinline__ void walk(const T *p, long long begin, long long end, F f, G g) {
   constexpr int V = Vec16<T>::N;
   const long long skew = ((16 - ((uintptr_t)(p + begin) & 15u)) & 15u) / sizeof(T);
   long long vb = begin + skew;
   if (vb > end) vb = end;
-  const long long nv = (end - vb) / V;
+  const int nv = (int)((end - vb) / V);
+  const uint4 *q = reinterpret_cast<const uint4 *>(p + vb) + threadIdx.x;
+  uint4 raw[kClipVectors];
   for (long long i = begin + threadIdx.x; i < vb; i += kClipThreads) g(p[i], i);
-  for (long long i = vb + nv * V + threadIdx.x; i < end; i += kClipThreads) g(p[i], i);
-  const uint4 *q = reinterpret_cast<const uint4 *>(p + vb);
-  for (long long k = threadIdx.x; k < nv; k += (long long)UNROLL * kClipThreads) {
-    uint4 raw[UNROLL];
+  for (long long i = vb + (long long)nv * V + threadIdx.x; i < end; i += kClipThreads) g(p[i], i);
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
-      if (k + u * kClipThreads < nv) raw[u] = q[k + u * kClipThreads];
+  for (int u = 0; u < kClipVectors; ++u)
+    raw[u] = (int)threadIdx.x + u * kClipThreads < nv ? q[u * kClipThreads]
+                                                      : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
-      if (k + u * kClipThreads < nv)
-        f(*reinterpret_cast<const Vec16<T> *>(&raw[u]), vb + (k + u * kClipThreads) * V);
-  }
+  for (int u = 0; u < kClipVectors; ++u)
+    if ((int)threadIdx.x + u * kClipThreads < nv)
+      f(raw[u], vb + (long long)(threadIdx.x + u * kClipThreads) * V);
 }
 
+// The squares of the same elements in fp64.
+template <typename T>
+__device__ __noinline__ double item_squares_fp64(const T *p, long long begin, long long end) {
+  constexpr int V = Vec16<T>::N;
+  double d = 0.0;
+  walk<T>(
+      p, begin, end,
+      [&](uint4 w, long long) {
+        typename Acc<T>::type f[V];
+        unpack<T>(w, f);
+        for (int i = 0; i < V; ++i) d += (double)f[i] * (double)f[i];
+      },
+      [&](T x, long long) {
+        const double f = (double)to_acc(x);
+        d += f * f;
+      });
+  return d;
+}
+
+// A thread's squares of an item: up to 64 of them in fp32, which is exact
+// enough unless the sum overflows or is so small that squares were lost.
+// Then, which no ordinary gradient reaches, they are taken again in fp64.
+// (Adding to fp64 once per vector instead made the kernel wait for the few
+// fp64 units.)
 template <typename T>
 __device__ __forceinline__ double item_squares(const T *p, long long begin, long long end) {
   constexpr int V = Vec16<T>::N;
-  double s = 0.0;
-  walk<T, 4>(
-      p, begin, end,
-      [&](const Vec16<T> &x, long long) {
-        if constexpr (sizeof(T) == 8) {
-          for (int i = 0; i < V; ++i) s += x.v[i] * x.v[i];
-        } else {
+  if constexpr (sizeof(T) < 8) {
+    float s[2] = {0.0f, 0.0f};
+    unsigned any = 0;
+    walk<T>(
+        p, begin, end,
+        [&](uint4 w, long long) {
+          any |= w.x | w.y | w.z | w.w;
           float f[V];
+          unpack<T>(w, f);
 #pragma unroll
-          for (int i = 0; i < V; ++i) f[i] = to_acc(x.v[i]);
-          s += squares(f);
-        }
-      },
-      [&](T x, long long) {
-        const double d = (double)to_acc(x);
-        s += d * d;
-      });
-  return s;
+          for (int i = 0; i < V; ++i) s[i & 1] = fmaf(f[i], f[i], s[i & 1]);
+        },
+        [&](T x, long long) {
+          const float f = to_acc(x);
+          any |= __float_as_uint(f);
+          s[0] = fmaf(f, f, s[0]);
+        });
+    const float sum = s[0] + s[1];
+    if (sum < 1e37f && (sum > 1e-24f || any == 0)) return (double)sum;
+  }
+  return item_squares_fp64(p, begin, end);
 }
 
+// The 16 bytes that start `skew` bytes (a multiple of 2) into eight words.
+__device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int skew) {
+  unsigned w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (skew & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (skew & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  if (skew & 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Elements begin .. end of a tensor of n, times c.  Output vectors are
+// aligned; where the input lies differently within its 16 bytes, a vector is
+// cut from the two aligned ones it lies in (both inside the tensor).
 template <typename T>
 __device__ __forceinline__ void item_scale(const T *p, T *o, long long begin, long long end,
-                                           typename Acc<T>::type c) {
+                                           long long n, typename Acc<T>::type c) {
   constexpr int V = Vec16<T>::N;
-  const bool same = (((uintptr_t)p ^ (uintptr_t)o) & 15u) == 0;
-  walk<T, 4>(
-      p, begin, end,
-      [&](Vec16<T> x, long long i) {
+  const int skew = (int)(((uintptr_t)p - (uintptr_t)o) & 15u);
+  long long vb = begin + (long long)(((16 - ((uintptr_t)(o + begin) & 15u)) & 15u) / sizeof(T));
+  if (skew != 0 && vb * (long long)sizeof(T) < skew) vb += V;
+  if (vb > end) vb = end;
+  int nv = (int)((end - vb) / V);
+  // the vector after the last one ends at or before the tensor's end
+  const int room = (int)((n - vb) * (long long)sizeof(T) / 16) - 1;
+  if (skew != 0 && nv > room) nv = room > 0 ? room : 0;
+  for (long long i = begin + threadIdx.x; i < vb; i += kClipThreads)
+    o[i] = from_acc<T>(to_acc(p[i]) * c);
+  for (long long i = vb + (long long)nv * V + threadIdx.x; i < end; i += kClipThreads)
+    o[i] = from_acc<T>(to_acc(p[i]) * c);
+  const char *base = reinterpret_cast<const char *>(p + vb) - skew;
+  const uint4 *q = reinterpret_cast<const uint4 *>(base) + threadIdx.x;
+  uint4 *out = reinterpret_cast<uint4 *>(o + vb) + threadIdx.x;
+  uint4 raw[kClipVectors];
 #pragma unroll
-        for (int k = 0; k < V; ++k) x.v[k] = from_acc<T>(to_acc(x.v[k]) * c);
-        if (same) {
-          *reinterpret_cast<uint4 *>(o + i) = *reinterpret_cast<const uint4 *>(&x);
-        } else {
+  for (int u = 0; u < kClipVectors; ++u)
+    raw[u] = (int)threadIdx.x + u * kClipThreads < nv ? q[u * kClipThreads] : make_uint4(0, 0, 0, 0);
+  if (skew != 0) {
+    uint4 next[kClipVectors];  // the neighbour's: in the cache
 #pragma unroll
-          for (int k = 0; k < V; ++k) o[i + k] = x.v[k];
-        }
-      },
-      [&](T x, long long i) { o[i] = from_acc<T>(to_acc(x) * c); });
+    for (int u = 0; u < kClipVectors; ++u)
+      next[u] = (int)threadIdx.x + u * kClipThreads < nv ? q[u * kClipThreads + 1]
+                                                         : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < kClipVectors; ++u) raw[u] = shifted(raw[u], next[u], skew);
+  }
+#pragma unroll
+  for (int u = 0; u < kClipVectors; ++u)
+    if ((int)threadIdx.x + u * kClipThreads < nv) {
+      typename Acc<T>::type f[V];
+      unpack<T>(raw[u], f);
+#pragma unroll
+      for (int k = 0; k < V; ++k) f[k] *= c;
+      out[u * kClipThreads] = pack<T>(f);
+    }
 }
 
 // Sum over the block in a fixed order, returned to every thread.
@@ -188,17 +246,21 @@ clip_scale_kernel(const __grid_constant__ ClipTable<N> tab, const double *partia
     if (c == 1.0 && p == o) continue;  // in place and nothing to change
     switch (tab.dtype[w.t]) {
       case FFT_ELEM_F32:
-        item_scale(static_cast<const float *>(p), static_cast<float *>(o), w.begin, w.end, cf);
+        item_scale(static_cast<const float *>(p), static_cast<float *>(o), w.begin, w.end,
+                   tab.numel[w.t], cf);
         break;
       case FFT_ELEM_F64:
-        item_scale(static_cast<const double *>(p), static_cast<double *>(o), w.begin, w.end, c);
+        item_scale(static_cast<const double *>(p), static_cast<double *>(o), w.begin, w.end,
+                   tab.numel[w.t], c);
         break;
       case FFT_ELEM_BF16:
         item_scale(static_cast<const __nv_bfloat16 *>(p), static_cast<__nv_bfloat16 *>(o),
-                   w.begin, w.end, cf);
+                   w.begin, w.end,
+                   tab.numel[w.t], cf);
         break;
       default:
-        item_scale(static_cast<const __half *>(p), static_cast<__half *>(o), w.begin, w.end, cf);
+        item_scale(static_cast<const __half *>(p), static_cast<__half *>(o), w.begin, w.end,
+                   tab.numel[w.t], cf);
     }
   }
 }
@@ -224,7 +286,8 @@ static void fill_table(ClipTable<N> &tab, long long begin, long long end, const 
     tab.numel[k] = numel[begin + k];
     tab.dtype[k] = (signed char)dtype[begin + k];
     tab.first[k] = items;
-    items += (tab.numel[k] + kClipItem - 1) / kClipItem;
+    const long long each = kClipItemBytes / clip_size(tab.dtype[k]);
+    items += (tab.numel[k] + each - 1) / each;
   }
   tab.first[tab.count] = items;
 }

@@ -22,8 +22,8 @@
 namespace fftgb {
 
 // Sum over the TPR threads that share a row, returned to all of them.  `red`
-// holds two sets of TPR / 32 values per row group and is used alternately,
-// which saves the barrier between reading one sum and writing the next.
+// holds two sets of TPR / 32 values and is used alternately, which saves the
+// barrier between reading one sum and writing the next.
 template <int TPR, typename A>
 __device__ __forceinline__ A row_sum(A v, A *red, int &turn) {
 #pragma unroll
@@ -41,6 +41,46 @@ __device__ __forceinline__ A row_sum(A v, A *red, int &turn) {
   return v;
 }
 
+// Mean of a row and the sum of squares about it with one barrier: a warp takes
+// both of its own elements (the squares about its own mean, from registers),
+// and the warps' are joined by M = sum over warps of M_w + n_w (mean_w - mean)^2.
+// n: this warp's elements; elements beyond the row hold 0.
+template <int TPR, int EPT, class Inside>
+__device__ __forceinline__ float2 row_moments(const float (&f)[EPT], float n, float inv_dim,
+                                              float4 *red, int &turn, Inside inside) {
+  float s = 0.0f, m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < EPT; ++e) s += f[e];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const float mean_w = n > 0.0f ? s / n : 0.0f;
+#pragma unroll
+  for (int e = 0; e < EPT; ++e) {
+    const float d = f[e] - mean_w;
+    if (inside(e)) m = fmaf(d, d, m);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+  if constexpr (TPR == 32) {
+    return make_float2(mean_w, m);
+  } else {
+    constexpr int W = TPR / 32;
+    float4 *r = red + turn * W;
+    if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = make_float4(s, m, mean_w, n);
+    __syncthreads();
+    turn ^= 1;
+    const float4 w = r[threadIdx.x & (W - 1)];
+    s = w.x;
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float mean = s * inv_dim, d = w.z - mean;
+    m = fmaf(w.w * d, d, w.y);
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+    return make_float2(mean, m);
+  }
+}
+
 // Both sums of the backward pass in one round.
 template <int TPR>
 __device__ __forceinline__ float2 row_sum2(float a, float b, float2 *red, int &turn) {
@@ -52,7 +92,7 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float2 *red, int &t
   if constexpr (TPR > 32) {
     constexpr int W = TPR / 32;
     float2 *r = red + turn * W;
-    if ((threadIdx.x & 31) == 0) r[(threadIdx.x % TPR) >> 5] = make_float2(a, b);
+    if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = make_float2(a, b);
     __syncthreads();
     const float2 t = r[threadIdx.x & (W - 1)];
     a = t.x;
@@ -76,109 +116,127 @@ __device__ __forceinline__ int column(int t, int e) {
   return e * TPR + t;
 }
 
-template <typename T, int TPR, int EPT, bool VEC>
-struct RowRegs {
+// A thread's part of a row as loaded: whole 16-byte words where the rows allow
+// it (16-bit elements then stay two to a register).
+template <typename T, int TPR, int EPT, bool VEC> struct RowRegs;
+template <typename T, int TPR, int EPT> struct RowRegs<T, TPR, EPT, true> {
   static constexpr int N = Vec16<T>::N;
-  T v[EPT];
+  uint4 raw[EPT / N];
   __device__ __forceinline__ void load(const T *row, int t, int dim) {
-    if constexpr (VEC) {
 #pragma unroll
-      for (int k = 0; k < EPT / N; ++k) {
-        const int c = (k * TPR + t) * N;
-        Vec16<T> x{};
-        if (c < dim) {
-          const uint4 raw = __ldcs(reinterpret_cast<const uint4 *>(row + c));
-          x = *reinterpret_cast<const Vec16<T> *>(&raw);
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[k * N + i] = x.v[i];
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < EPT; ++e) {
-        const int c = e * TPR + t;
-        v[e] = c < dim ? row[c] : from_acc<T>(0.0f);
-      }
+    for (int k = 0; k < EPT / N; ++k) {
+      const int c = (k * TPR + t) * N;
+      raw[k] = c < dim ? __ldcs(reinterpret_cast<const uint4 *>(row + c)) : make_uint4(0, 0, 0, 0);
     }
   }
-  __device__ __forceinline__ void store(T *row, int t, int dim) const {
-    if constexpr (VEC) {
+  __device__ __forceinline__ void get(float (&f)[EPT]) const {
 #pragma unroll
-      for (int k = 0; k < EPT / N; ++k) {
-        const int c = (k * TPR + t) * N;
-        if (c < dim) {
-          Vec16<T> x;
+    for (int k = 0; k < EPT / N; ++k) {
+      float g[N];
+      unpack<T>(raw[k], g);
 #pragma unroll
-          for (int i = 0; i < N; ++i) x.v[i] = v[k * N + i];
-          *reinterpret_cast<uint4 *>(row + c) = *reinterpret_cast<const uint4 *>(&x);
-        }
-      }
-    } else {
+      for (int i = 0; i < N; ++i) f[k * N + i] = g[i];
+    }
+  }
+  static __device__ __forceinline__ void store(T *row, const float (&f)[EPT], int t, int dim) {
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) {
-        const int c = e * TPR + t;
-        if (c < dim) row[c] = v[e];
-      }
+    for (int k = 0; k < EPT / N; ++k) {
+      const int c = (k * TPR + t) * N;
+      float g[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) g[i] = f[k * N + i];
+      if (c < dim) *reinterpret_cast<uint4 *>(row + c) = pack<T>(g);
     }
   }
 };
+template <typename T, int TPR, int EPT> struct RowRegs<T, TPR, EPT, false> {
+  T v[EPT];
+  __device__ __forceinline__ void load(const T *row, int t, int dim) {
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) {
+      const int c = e * TPR + t;
+      v[e] = c < dim ? row[c] : from_acc<T>(0.0f);
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[EPT]) const {
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) f[e] = to_acc(v[e]);
+  }
+  static __device__ __forceinline__ void store(T *row, const float (&f)[EPT], int t, int dim) {
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) {
+      const int c = e * TPR + t;
+      if (c < dim) row[c] = from_acc<T>(f[e]);
+    }
+  }
+};
+// Rows under way per thread: each is loaded that many rounds before it is
+// used, into registers of its own (moving a row would wait for it).
+template <typename T, bool VEC, int MOST> constexpr int kNormDepth = VEC && sizeof(T) == 2 ? MOST : 1;
 
-constexpr int kNormThreads = 256;
+// Rows of one warp share blocks of eight; other rows have a block each.
+template <int TPR> struct NormBlock {
+  static constexpr int THREADS = TPR == 32 ? 256 : TPR;
+  static constexpr int GROUPS = THREADS / TPR;
+  // Blocks per multiprocessor: 1024 threads, which leaves them 64 registers;
+  // half of that for rows of one warp, which hold more and wait for no one.
+  static constexpr int BLOCKS = TPR == 32 ? 2 : THREADS >= 1024 ? 1 : 1024 / THREADS;
+};
 
 template <typename T, int TPR, int EPT, bool VEC>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(NormBlock<TPR>::THREADS, NormBlock<TPR>::BLOCKS)
 layer_norm_kernel(const LayerNormArgs a) {
-  constexpr int G = kNormThreads / TPR;  // rows in flight per block
-  __shared__ float red[2 * 32];
+  constexpr int G = NormBlock<TPR>::GROUPS;
+  __shared__ float4 red[2 * 32];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const T *x = static_cast<const T *>(a.x);
   T *y = static_cast<T *>(a.y);
-  float w[EPT], b[EPT];
+  float w[EPT], b[EPT], n = 0.0f;
 #pragma unroll
   for (int e = 0; e < EPT; ++e) {
     const int c = column<T, TPR, VEC>(t, e);
     w[e] = a.w && c < a.dim ? load_any(a.w, a.wtype, c) : 1.0f;
     b[e] = a.b && c < a.dim ? load_any(a.b, a.wtype, c) : 0.0f;
+    if (c < a.dim) n += 1.0f;
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   const float inv = 1.0f / (float)a.dim;
   int turn = 0;
   const long long step = (long long)gridDim.x * G;
   long long row = (long long)blockIdx.x * G + grp;
-  RowRegs<T, TPR, EPT, VEC> cur, next;
-  if (row < a.rows) cur.load(x + row * a.ldx, t, a.dim);
+  constexpr int DEPTH = kNormDepth<T, VEC, 3>;
+  RowRegs<T, TPR, EPT, VEC> buf[DEPTH];
+#pragma unroll
+  for (int k = 0; k < DEPTH; ++k)
+    if (row + k * step < a.rows) buf[k].load(x + (row + k * step) * a.ldx, t, a.dim);
   // The row groups of a block share no barrier (a group of several warps is
   // a whole block), so each may end its loop on its own.
-  for (; row < a.rows; row += step) {
-    if (row + step < a.rows) next.load(x + (row + step) * a.ldx, t, a.dim);
-    float f[EPT], s = 0.0f;
+  while (row < a.rows) {
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) {
-      f[e] = to_acc(cur.v[e]);
-      s += f[e];  // columns beyond dim hold zeros
-    }
-    const float mu = row_sum<TPR>(s, red, turn) * inv;
-    s = 0.0f;
+    for (int k = 0; k < DEPTH; ++k, row += step) {
+      if (row >= a.rows) break;
+      float f[EPT];
+      buf[k].get(f);
+      if (row + DEPTH * step < a.rows) buf[k].load(x + (row + DEPTH * step) * a.ldx, t, a.dim);
+      const float2 m = row_moments<TPR, EPT>(
+          f, n, inv, red, turn, [&](int e) { return column<T, TPR, VEC>(t, e) < a.dim; });
+      const float mu = m.x, r = 1.0f / sqrtf(m.y * inv + (float)a.eps);
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) {
-      f[e] -= mu;
-      if (column<T, TPR, VEC>(t, e) < a.dim) s += f[e] * f[e];
+      for (int e = 0; e < EPT; ++e) f[e] = (f[e] - mu) * r * w[e] + b[e];
+      RowRegs<T, TPR, EPT, VEC>::store(y + row * a.ldy, f, t, a.dim);
+      if (t == 0) {
+        if (a.mean) static_cast<float *>(a.mean)[row] = mu;
+        if (a.rstd) static_cast<float *>(a.rstd)[row] = r;
+      }
     }
-    const float r = 1.0f / sqrtf(row_sum<TPR>(s, red, turn) * inv + (float)a.eps);
-#pragma unroll
-    for (int e = 0; e < EPT; ++e) cur.v[e] = from_acc<T>(f[e] * r * w[e] + b[e]);
-    cur.store(y + row * a.ldy, t, a.dim);
-    if (t == 0) {
-      if (a.mean) static_cast<float *>(a.mean)[row] = mu;
-      if (a.rstd) static_cast<float *>(a.rstd)[row] = r;
-    }
-    cur = next;
   }
 }
 
 template <typename T, int TPR, int EPT, bool VEC>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(NormBlock<TPR>::THREADS, NormBlock<TPR>::BLOCKS)
 layer_norm_grad_kernel(const LayerNormGradArgs a) {
-  constexpr int G = kNormThreads / TPR;
+  constexpr int G = NormBlock<TPR>::GROUPS;
   __shared__ float2 red[2 * 32];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
@@ -196,46 +254,46 @@ layer_norm_grad_kernel(const LayerNormGradArgs a) {
   int turn = 0;
   const long long step = (long long)gridDim.x * G;
   long long row = (long long)blockIdx.x * G + grp;
-  RowRegs<T, TPR, EPT, VEC> xc, dc, xn, dn;
-  float mu = 0.0f, r = 0.0f, mun = 0.0f, rn = 0.0f;
-  if (row < a.rows) {
-    xc.load(x + row * a.ldx, t, a.dim);
-    dc.load(dy + row * a.lddy, t, a.dim);
-    mu = mean[row];
-    r = rstd[row];
-  }
-  for (; row < a.rows; row += step) {
-    if (row + step < a.rows) {
-      xn.load(x + (row + step) * a.ldx, t, a.dim);
-      dn.load(dy + (row + step) * a.lddy, t, a.dim);
-      mun = mean[row + step];
-      rn = rstd[row + step];
-    }
-    float s1 = 0.0f, s2 = 0.0f;
+  constexpr int DEPTH = kNormDepth<T, VEC, 2>;
+  RowRegs<T, TPR, EPT, VEC> xb[DEPTH], db_[DEPTH];
+  float mub[DEPTH], rb[DEPTH];
+  auto load = [&](int k, long long at) {
+    xb[k].load(x + at * a.ldx, t, a.dim);
+    db_[k].load(dy + at * a.lddy, t, a.dim);
+    mub[k] = mean[at];
+    rb[k] = rstd[at];
+  };
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) {
-      if (column<T, TPR, VEC>(t, e) < a.dim) {
-        const float xh = (to_acc(xc.v[e]) - mu) * r, g = to_acc(dc.v[e]);
-        dw[e] += g * xh;
-        db[e] += g;
-        s1 += g * w[e];
-        s2 += g * w[e] * xh;
-      }
-    }
-    if (dx) {
-      const float2 s = row_sum2<TPR>(s1, s2, red, turn);
-      const float m1 = s.x * inv, m2 = s.y * inv;
+  for (int k = 0; k < DEPTH; ++k)
+    if (row + k * step < a.rows) load(k, row + k * step);
+  while (row < a.rows) {
+#pragma unroll
+    for (int k = 0; k < DEPTH; ++k, row += step) {
+      if (row >= a.rows) break;
+      const float mu = mub[k], r = rb[k];
+      float xh[EPT], g[EPT], s1 = 0.0f, s2 = 0.0f;
+      xb[k].get(xh);
+      db_[k].get(g);
 #pragma unroll
       for (int e = 0; e < EPT; ++e) {
-        const float xh = (to_acc(xc.v[e]) - mu) * r;
-        xc.v[e] = from_acc<T>(r * (to_acc(dc.v[e]) * w[e] - m1 - xh * m2));
+        xh[e] = (xh[e] - mu) * r;
+        if (column<T, TPR, VEC>(t, e) < a.dim) {
+          dw[e] = fmaf(g[e], xh[e], dw[e]);
+          db[e] += g[e];
+          g[e] *= w[e];
+          s1 += g[e];
+          s2 = fmaf(g[e], xh[e], s2);
+        }
       }
-      xc.store(dx + row * a.lddx, t, a.dim);
+      if (row + DEPTH * step < a.rows) load(k, row + DEPTH * step);
+      if (dx) {
+        const float2 s = row_sum2<TPR>(s1, s2, red, turn);
+        const float m1 = s.x * inv, m2 = s.y * inv;
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) g[e] = r * (g[e] - m1 - xh[e] * m2);
+        RowRegs<T, TPR, EPT, VEC>::store(dx + row * a.lddx, g, t, a.dim);
+      }
     }
-    xc = xn;
-    dc = dn;
-    mu = mun;
-    r = rn;
   }
   if (!a.partial) return;
   // One row of partial sums per row group: [2][gridDim.x * G][dim].
@@ -361,11 +419,15 @@ layer_norm_sum_kernel(const A *partial, int parts, int dim, void *dw, void *db, 
   if (threadIdx.x == 0 && col < dim && out) store_any(out, wtype, col, s);
 }
 
-// Threads per row and elements per thread by the row's length: warps for
-// rows up to 1024 elements (no barrier), blocks of 256 up to 8192;
-// longer rows and fp64 by the looping kernels.
+// Threads per row and elements per thread by the row's length: a warp for rows
+// up to 512 elements (no barrier), blocks of 128 to 1024 threads with 8
+// elements each up to 8192; longer rows and fp64 by the looping kernels.  Few
+// elements per thread leave room for many warps, which hide the barrier of a
+// row's reduction (16 per thread, 256 threads: 90 us for 16384 x 4096 bf16).
 constexpr int kNormRegMax = 8192;
-inline int norm_blocks_per_sm(int dim) { return dim > 4096 ? 2 : 4; }
+inline int norm_tpr(int dim) {
+  return dim <= 512 ? 32 : dim <= 1024 ? 128 : dim <= 2048 ? 256 : dim <= 4096 ? 512 : 1024;
+}
 
 template <typename T, class F>
 cudaError_t norm_dispatch(int dim, bool vec, F f) {
@@ -376,19 +438,20 @@ cudaError_t norm_dispatch(int dim, bool vec, F f) {
                  std::false_type())
   if (dim <= 256) { FFTGB_NORM(32, 8); }
   if (dim <= 512) { FFTGB_NORM(32, 16); }
-  if (dim <= 1024) { FFTGB_NORM(32, 32); }
+  if (dim <= 1024) { FFTGB_NORM(128, 8); }
   if (dim <= 2048) { FFTGB_NORM(256, 8); }
-  if (dim <= 4096) { FFTGB_NORM(256, 16); }
-  FFTGB_NORM(256, 32);
+  if (dim <= 4096) { FFTGB_NORM(512, 8); }
+  FFTGB_NORM(1024, 8);
 #undef FFTGB_NORM
 }
 
-inline int norm_groups(int dim) { return dim <= 1024 ? 8 : 1; }  // row groups per block
+inline int norm_groups(int dim) { return dim <= 512 ? 8 : 1; }  // row groups per block
 
 // Blocks of the persistent kernels.
 inline long long norm_grid(long long rows, int dim) {
+  const int tpr = norm_tpr(dim);
   const long long blocks = (rows + norm_groups(dim) - 1) / norm_groups(dim);
-  const long long most = (long long)sm_count() * norm_blocks_per_sm(dim);
+  const long long most = (long long)sm_count() * (tpr == 32 ? 2 : tpr >= 1024 ? 1 : 1024 / tpr);
   return blocks < most ? blocks : most;
 }
 
@@ -405,7 +468,7 @@ cudaError_t layer_norm_t(const LayerNormArgs &a, cudaStream_t st) {
       const int grid = (int)norm_grid(a.rows, a.dim);
       return norm_dispatch<T>(a.dim, vec, [&](auto tpr, auto ept, auto v) {
         layer_norm_kernel<T, tpr.value, ept.value, v.value>
-            <<<grid, kNormThreads, 0, st>>>(a);
+            <<<grid, NormBlock<tpr.value>::THREADS, 0, st>>>(a);
         return cudaGetLastError();
       });
     }
@@ -431,7 +494,7 @@ cudaError_t layer_norm_grad_t(const LayerNormGradArgs &a, cudaStream_t st) {
       const int grid = (int)norm_grid(a.rows, a.dim);
       e = norm_dispatch<T>(a.dim, vec, [&](auto tpr, auto ept, auto v) {
         layer_norm_grad_kernel<T, tpr.value, ept.value, v.value>
-            <<<grid, kNormThreads, 0, st>>>(a);
+            <<<grid, NormBlock<tpr.value>::THREADS, 0, st>>>(a);
         return cudaGetLastError();
       });
       done = true;

@@ -4,6 +4,8 @@
 // Not installed.
 #pragma once
 
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -144,6 +146,54 @@ template <typename T> struct alignas(16) Vec16 {
   static constexpr int N = 16 / sizeof(T);
   T v[N];
 };
+// The elements of 16 bytes, and back.
+template <typename T> __device__ __forceinline__ void unpack(uint4 w, float (&f)[4]) {
+  f[0] = __uint_as_float(w.x);
+  f[1] = __uint_as_float(w.y);
+  f[2] = __uint_as_float(w.z);
+  f[3] = __uint_as_float(w.w);
+}
+template <typename T> __device__ __forceinline__ void unpack(uint4 w, float (&f)[8]) {
+  const unsigned r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 x;
+    if constexpr (std::is_same<T, __half>::value) {
+      x = __half22float2(*reinterpret_cast<const __half2 *>(&r[i]));
+    } else {
+      x.x = __uint_as_float(r[i] << 16);
+      x.y = __uint_as_float(r[i] & 0xffff0000u);
+    }
+    f[2 * i] = x.x;
+    f[2 * i + 1] = x.y;
+  }
+}
+template <typename T> __device__ __forceinline__ void unpack(uint4 w, double (&f)[2]) {
+  f[0] = __hiloint2double((int)w.y, (int)w.x);
+  f[1] = __hiloint2double((int)w.w, (int)w.z);
+}
+template <typename T> __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                    __float_as_uint(f[3]));
+}
+template <typename T> __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+  unsigned r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same<T, __half>::value) {
+      const __half2 x = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      r[i] = *reinterpret_cast<const unsigned *>(&x);
+    } else {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      r[i] = *reinterpret_cast<const unsigned *>(&x);
+    }
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+template <typename T> __device__ __forceinline__ uint4 pack(const double (&f)[2]) {
+  return make_uint4((unsigned)__double2loint(f[0]), (unsigned)__double2hiint(f[0]),
+                    (unsigned)__double2loint(f[1]), (unsigned)__double2hiint(f[1]));
+}
 #endif
 
 }  // namespace fftgb

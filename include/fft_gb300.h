@@ -508,8 +508,8 @@ int fft_layer_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t
  *   norm       one device float; may be NULL in fft_clip_grad_norm.
  *   max_norm, eps  >= 0.
  *   workspace  fft_grad_norm_workspace_bytes(count) bytes.
- * Squares are summed in fp32 by groups of 16 bytes and those sums in fp64;
- * squares that overflow or vanish in fp32 are taken in fp64.  An infinite
+ * Squares are summed in fp32 by groups of at most 64 and those sums in
+ * fp64; squares that overflow or vanish in fp32 are taken in fp64.  An infinite
  * norm scales by 0, a NaN makes every output NaN.
  */
 size_t fft_grad_norm_workspace_bytes(int64_t count);
