@@ -18,6 +18,7 @@
 #pragma once
 
 #include "seq.h"
+#include "tcgen05.cuh"
 
 namespace fftgb {
 
@@ -81,7 +82,7 @@ __device__ __forceinline__ float2 row_moments(const float (&f)[EPT], float n, fl
   }
 }
 
-// Both sums of the backward pass in one round.
+// Both sums of a row of the backward pass in one round.
 template <int TPR>
 __device__ __forceinline__ float2 row_sum2(float a, float b, float2 *red, int &turn) {
 #pragma unroll
@@ -106,6 +107,30 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float2 *red, int &t
   }
   return make_float2(a, b);
 }
+// The same of two rows.
+template <int TPR>
+__device__ __forceinline__ float4 row_sum4(float4 v, float4 *red, int &turn) {
+  auto add = [](float4 a, int o) {
+    a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+    a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+    a.z += __shfl_xor_sync(0xffffffffu, a.z, o);
+    a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
+    return a;
+  };
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = add(v, o);
+  if constexpr (TPR > 32) {
+    constexpr int W = TPR / 32;
+    float4 *r = red + turn * W;
+    if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = r[threadIdx.x & (W - 1)];
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) v = add(v, o);
+    turn ^= 1;
+  }
+  return v;
+}
 
 // Column of a thread's element e: 16-byte vectors (VEC), or single elements
 // at a stride of TPR where the rows are not 16-byte aligned.
@@ -122,6 +147,10 @@ template <typename T, int TPR, int EPT, bool VEC> struct RowRegs;
 template <typename T, int TPR, int EPT> struct RowRegs<T, TPR, EPT, true> {
   static constexpr int N = Vec16<T>::N;
   uint4 raw[EPT / N];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int k = 0; k < EPT / N; ++k) raw[k] = make_uint4(0, 0, 0, 0);
+  }
   __device__ __forceinline__ void load(const T *row, int t, int dim) {
 #pragma unroll
     for (int k = 0; k < EPT / N; ++k) {
@@ -151,6 +180,10 @@ template <typename T, int TPR, int EPT> struct RowRegs<T, TPR, EPT, true> {
 };
 template <typename T, int TPR, int EPT> struct RowRegs<T, TPR, EPT, false> {
   T v[EPT];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) v[e] = from_acc<T>(0.0f);
+  }
   __device__ __forceinline__ void load(const T *row, int t, int dim) {
 #pragma unroll
     for (int e = 0; e < EPT; ++e) {
@@ -233,11 +266,109 @@ layer_norm_kernel(const LayerNormArgs a) {
   }
 }
 
+// Rows that a warp holds whole (NV 16-byte words
+// per lane): no barrier at all, and with 16 warps per multiprocessor 128 KB of
+// rows under way.  w and b lie in shared memory in fp32.  (A block per row
+// waits for its barrier most of the time: 70 us against 49 for 16384 x 4096
+// bf16.)
+template <typename T, int NV>
+__global__ void __launch_bounds__(256, 2) layer_norm_warp_kernel(const LayerNormArgs a) {
+  extern __shared__ float wb[];  // w, then b
+  constexpr int N = Vec16<T>::N;
+  const int lane = threadIdx.x & 31;
+  float *ws = wb, *bs = wb + a.dim;
+  for (int c = threadIdx.x; c < a.dim; c += 256) {
+    ws[c] = a.w ? load_any(a.w, a.wtype, c) : 1.0f;
+    bs[c] = a.b ? load_any(a.b, a.wtype, c) : 0.0f;
+  }
+  __syncthreads();
+  const float inv = 1.0f / (float)a.dim;
+  const long long step = (long long)gridDim.x * 8;
+  for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < a.rows; row += step) {
+    const T *x = static_cast<const T *>(a.x) + row * a.ldx;
+    T *y = static_cast<T *>(a.y) + row * a.ldy;
+    uint4 raw[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (k * 32 + lane) * N;
+      raw[k] = c < a.dim ? __ldcs(reinterpret_cast<const uint4 *>(x + c)) : make_uint4(0, 0, 0, 0);
+    }
+    // Three walks over the registers, two values per instruction.
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float f[N];
+      unpack<T>(raw[k], f);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) s = fma2(make_float2(f[i], f[i + 1]), both(1.0f), s);
+    }
+    s.x += s.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+    const float mu = s.x * inv;
+    s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float f[N];
+      unpack<T>(raw[k], f);
+      if ((k * 32 + lane) * N < a.dim) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          const float2 d = fma2(both(-mu), both(1.0f), make_float2(f[i], f[i + 1]));
+          s = fma2(d, d, s);
+        }
+      }
+    }
+    s.x += s.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+    const float r = 1.0f / sqrtf(s.x * inv + (float)a.eps);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (k * 32 + lane) * N;
+      if (c < a.dim) {
+        float f[N];
+        unpack<T>(raw[k], f);
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+          const float4 w = *reinterpret_cast<const float4 *>(ws + c + i);
+          const float4 b = *reinterpret_cast<const float4 *>(bs + c + i);
+#pragma unroll
+          for (int h = 0; h < 4; h += 2) {
+            const float2 d = mul2(fma2(both(-mu), both(1.0f), make_float2(f[i + h], f[i + h + 1])),
+                                  both(r));
+            const float2 o = fma2(d, h ? make_float2(w.z, w.w) : make_float2(w.x, w.y),
+                                  h ? make_float2(b.z, b.w) : make_float2(b.x, b.y));
+            f[i + h] = o.x;
+            f[i + h + 1] = o.y;
+          }
+        }
+        *reinterpret_cast<uint4 *>(y + c) = pack<T>(f);
+      }
+    }
+    if (lane == 0) {
+      if (a.mean) static_cast<float *>(a.mean)[row] = mu;
+      if (a.rstd) static_cast<float *>(a.rstd)[row] = r;
+    }
+  }
+}
+template <typename T, int NV = 1>
+cudaError_t layer_norm_warp(const LayerNormArgs &a, cudaStream_t st) {
+  if constexpr (NV < 16)
+    if (a.dim > NV * 32 * Vec16<T>::N) return layer_norm_warp<T, 2 * NV>(a, st);
+  const long long blocks = (a.rows + 7) / 8, most = 2ll * sm_count();
+  layer_norm_warp_kernel<T, NV>
+      <<<(int)(blocks < most ? blocks : most), 256, 2 * a.dim * sizeof(float), st>>>(a);
+  return cudaGetLastError();
+}
+
+// 16-bit rows: two per round share one barrier (fp32 rows would not fit the
+// registers).
 template <typename T, int TPR, int EPT, bool VEC>
 __global__ void __launch_bounds__(NormBlock<TPR>::THREADS, NormBlock<TPR>::BLOCKS)
 layer_norm_grad_kernel(const LayerNormGradArgs a) {
   constexpr int G = NormBlock<TPR>::GROUPS;
-  __shared__ float2 red[2 * 32];
+  __shared__ float4 red[2 * 32];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
   const float *mean = static_cast<const float *>(a.mean);
@@ -250,49 +381,74 @@ layer_norm_grad_kernel(const LayerNormGradArgs a) {
     w[e] = a.w && c < a.dim ? load_any(a.w, a.wtype, c) : 1.0f;
     dw[e] = db[e] = 0.0f;
   }
+  constexpr int ROWS = VEC && sizeof(T) == 2 ? 2 : 1;
   const float inv = 1.0f / (float)a.dim;
   int turn = 0;
   const long long step = (long long)gridDim.x * G;
   long long row = (long long)blockIdx.x * G + grp;
-  constexpr int DEPTH = kNormDepth<T, VEC, 2>;
-  RowRegs<T, TPR, EPT, VEC> xb[DEPTH], db_[DEPTH];
-  float mub[DEPTH], rb[DEPTH];
+  RowRegs<T, TPR, EPT, VEC> xb[ROWS], gb[ROWS];
+  float mu[ROWS], r[ROWS];
   auto load = [&](int k, long long at) {
-    xb[k].load(x + at * a.ldx, t, a.dim);
-    db_[k].load(dy + at * a.lddy, t, a.dim);
-    mub[k] = mean[at];
-    rb[k] = rstd[at];
+    if (at < a.rows) {
+      xb[k].load(x + at * a.ldx, t, a.dim);
+      gb[k].load(dy + at * a.lddy, t, a.dim);
+      mu[k] = mean[at];
+      r[k] = rstd[at];
+    } else {
+      xb[k].zero();
+      gb[k].zero();
+      mu[k] = r[k] = 0.0f;  // a row that adds nothing
+    }
   };
+  if (row < a.rows) {
 #pragma unroll
-  for (int k = 0; k < DEPTH; ++k)
-    if (row + k * step < a.rows) load(k, row + k * step);
-  while (row < a.rows) {
+    for (int k = 0; k < ROWS; ++k) load(k, row + k * step);
+  }
+  for (; row < a.rows; row += ROWS * step) {
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int k = 0; k < DEPTH; ++k, row += step) {
-      if (row >= a.rows) break;
-      const float mu = mub[k], r = rb[k];
-      float xh[EPT], g[EPT], s1 = 0.0f, s2 = 0.0f;
+    for (int k = 0; k < ROWS; ++k) {
+      float xh[EPT], g[EPT];
       xb[k].get(xh);
-      db_[k].get(g);
+      gb[k].get(g);
 #pragma unroll
       for (int e = 0; e < EPT; ++e) {
-        xh[e] = (xh[e] - mu) * r;
-        if (column<T, TPR, VEC>(t, e) < a.dim) {
-          dw[e] = fmaf(g[e], xh[e], dw[e]);
-          db[e] += g[e];
-          g[e] *= w[e];
-          s1 += g[e];
-          s2 = fmaf(g[e], xh[e], s2);
-        }
+        const float h = (xh[e] - mu[k]) * r[k];  // (g is 0 beyond the row)
+        dw[e] = fmaf(g[e], h, dw[e]);
+        db[e] += g[e];
+        s[2 * k] = fmaf(g[e], w[e], s[2 * k]);
+        s[2 * k + 1] = fmaf(g[e] * w[e], h, s[2 * k + 1]);
       }
-      if (row + DEPTH * step < a.rows) load(k, row + DEPTH * step);
-      if (dx) {
-        const float2 s = row_sum2<TPR>(s1, s2, red, turn);
-        const float m1 = s.x * inv, m2 = s.y * inv;
+    }
+    if (dx) {
+      float m1[2], m2[2];
+      if constexpr (ROWS == 2) {
+        const float4 m = row_sum4<TPR>(make_float4(s[0], s[1], s[2], s[3]), red, turn);
+        m1[0] = m.x * inv;
+        m2[0] = m.y * inv;
+        m1[1] = m.z * inv;
+        m2[1] = m.w * inv;
+      } else {
+        const float2 m = row_sum2<TPR>(s[0], s[1], reinterpret_cast<float2 *>(red), turn);
+        m1[0] = m.x * inv;
+        m2[0] = m.y * inv;
+      }
 #pragma unroll
-        for (int e = 0; e < EPT; ++e) g[e] = r * (g[e] - m1 - xh[e] * m2);
-        RowRegs<T, TPR, EPT, VEC>::store(dx + row * a.lddx, g, t, a.dim);
+      for (int k = 0; k < ROWS; ++k) {
+        if (row + k * step < a.rows) {
+          float xh[EPT], g[EPT];
+          xb[k].get(xh);
+          gb[k].get(g);
+#pragma unroll
+          for (int e = 0; e < EPT; ++e)
+            g[e] = r[k] * (g[e] * w[e] - m1[k] - (xh[e] - mu[k]) * r[k] * m2[k]);
+          RowRegs<T, TPR, EPT, VEC>::store(dx + (row + k * step) * a.lddx, g, t, a.dim);
+        }
+        load(k, row + (k + ROWS) * step);
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) load(k, row + (k + ROWS) * step);
     }
   }
   if (!a.partial) return;
@@ -465,6 +621,10 @@ cudaError_t layer_norm_t(const LayerNormArgs &a, cudaStream_t st) {
   if constexpr (sizeof(T) < 8) {
     if (a.dim <= kNormRegMax) {
       const bool vec = norm_vec<T>(a.x, a.ldx, a.dim) && norm_vec<T>(a.y, a.ldy, a.dim);
+      // Few long rows do not fill the multiprocessors with a warp each.
+      if (vec && a.dim <= 16 * 32 * Vec16<T>::N &&
+          (a.dim <= 512 || a.rows >= 8ll * sm_count()))
+        return layer_norm_warp<T>(a, st);
       const int grid = (int)norm_grid(a.rows, a.dim);
       return norm_dispatch<T>(a.dim, vec, [&](auto tpr, auto ept, auto v) {
         layer_norm_kernel<T, tpr.value, ept.value, v.value>
