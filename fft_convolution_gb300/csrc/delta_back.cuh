@@ -12,9 +12,9 @@
 //
 // Tensor memory (512 columns):
 //   D (fp32)         0 .. DK - 1
-//   dS (two fp16)    128, 192        P, then F           256 .. 319
-//   dU               320, 352        dO, then gamma beta F   384, 416
-//   X, then (two fp16) scale gamma dO   448 .. 511
+//   dS (two fp16)             128, 192        P, then F   256 .. 319
+//   dU, then gamma beta F     320, 352        X           448 .. 511
+//   dO, then scale gamma dO   384, 416
 #pragma once
 
 #include "delta_scan.cuh"
@@ -82,12 +82,12 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
       if (!wait(&bars.u, ph)) break;
       tc_fence_after();
       if (elect_one())
-        mma_update<DK, NT>(tm + kColD, tm + kColN, tm + kColN + 32, q, false);
+        mma_update<DK, NT>(tm + kColD, tm + kColWh, tm + kColWl, q, false);
       __syncwarp();
       if (!wait(&bars.w, ph)) break;
       tc_fence_after();
       if (elect_one()) {
-        mma_update<DK, NT>(tm + kColD, tm + kColWh, tm + kColWl, k, true);
+        mma_update<DK, NT>(tm + kColD, tm + kColYh, tm + kColYl, k, true);
         mma_commit(&bars.s);
         mma_commit(&bars.empty[s]);
       }
@@ -179,6 +179,26 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
       if (lane == 0) bar_arrive(&bars.empty[s]);
       return true;
     };
+    // dV of the chunk of step `it`.
+    T dv[TK];
+    auto put_dv = [&](int it) {
+      if (STAGED) {
+        if (it > 0 && !wait(&bars.got, (it & 1) ^ 1)) return false;
+        T *out = reinterpret_cast<T *>(stages + ST * kStage) + group * TK * 128 + row;
+#pragma unroll
+        for (int j = 0; j < TK; ++j) out[j * 128] = dv[j];
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bars.put);
+      } else if (live) {
+        const long long r0 = (long long)chunk_of(it) * kChunk + group * TK;
+        const long long left = sp.rows - r0;
+        T *out = static_cast<T *>(ga.dv) + out_row(a, sp.b, sp.row0 + r0, packed, h) + dvr;
+#pragma unroll
+        for (int j = 0; j < TK; ++j)
+          if (j < left) out[j * ostep] = dv[j];
+      }
+      return true;
+    };
     bool ok = true;
     if (sp.chunks > 0) {
       fetch(0);
@@ -227,24 +247,26 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
       put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, x);
       tmem_wait_st();
       warp_arrive(&bars.y, lane);
-      // scale gamma dO, where X was (every warp has read its part of X: they
-      // met when dU was ready)
+      // While F is computed: scale gamma dO, where dO was, and the chunk
+      // before's dV.
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = mul2(f[j], mul2(gate(gates + 5 * 64, j), both(ws)));
+      put_split(lb + kColWh + group * 8, lb + kColWl + group * 8, f);
+      tmem_wait_st();
+      warp_arrive(&bars.u, lane);
+      if (it > 0 && !(ok = put_dv(it - 1))) break;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        f[j] = mul2(mul2(mul2(gate(gates + 2 * 64, j), both(inv_y)), gate(gates + 4 * 64, j)),
+                    both(ws));
+      // gamma beta F, where dU was
       if (!(ok = wait(&bars.e, ph))) break;
       tc_fence_after();
       tmem_ld(lb + kColP + group * TK, r);
       tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = mul2(f[j], mul2(gate(gates + 5 * 64, j), both(ws)));
-      put_split(lb + kColN + group * 8, lb + kColN + 32 + group * 8, f);
-      tmem_wait_st();
-      warp_arrive(&bars.u, lane);
-      // gamma beta F
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 b = mul2(gate(gates + 2 * 64, j), both(inv_y));
-        x[j] = mul2(pair(r, j), mul2(mul2(b, gate(gates + 4 * 64, j)), both(ws)));
-      }
-      put_split(lb + kColWh + group * 8, lb + kColWl + group * 8, x);
+      for (int j = 0; j < 8; ++j) x[j] = mul2(pair(r, j), f[j]);
+      put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, x);
       tmem_wait_st();
       warp_arrive(&bars.w, lane);
       // F itself, and dV = beta F
@@ -257,26 +279,8 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
         dst[2 * j * 128] = x[j].x;
         dst[(2 * j + 1) * 128] = x[j].y;
         x[j] = mul2(x[j], gate(gates + 3 * 64, j));
-      }
-      if (STAGED) {
-        if (it > 0 && !(ok = wait(&bars.got, ph ^ 1))) break;
-        T *out = reinterpret_cast<T *>(stages + ST * kStage) + group * TK * 128 + row;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          out[2 * j * 128] = from_acc<T>(x[j].x);
-          out[(2 * j + 1) * 128] = from_acc<T>(x[j].y);
-        }
-        __syncwarp();
-        if (lane == 0) bar_arrive(&bars.put);
-      } else if (live) {
-        const long long r0 = (long long)c * kChunk + group * TK;
-        const long long left = sp.rows - r0;
-        T *out = static_cast<T *>(ga.dv) + out_row(a, sp.b, sp.row0 + r0, packed, h) + dvr;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (2 * j < left) out[2 * j * ostep] = from_acc<T>(x[j].x);
-          if (2 * j + 1 < left) out[(2 * j + 1) * ostep] = from_acc<T>(x[j].y);
-        }
+        dv[2 * j] = from_acc<T>(x[j].x);
+        dv[2 * j + 1] = from_acc<T>(x[j].y);
       }
       const bool more = it + 1 < sp.chunks;
       if (more) {
@@ -298,6 +302,7 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
       ss = next_ss;
       if (more) put_state(c - 1);
     }
+    if (ok && sp.chunks > 0) ok = put_dv(sp.chunks - 1);
     if (ok && ga.dinitial && live) {
       const float inv = scale_inverse(ss);
 #pragma unroll

@@ -233,6 +233,16 @@ __device__ __forceinline__ void put_split(uint32_t hi_at, uint32_t lo_at, const 
   tmem_st(hi_at, hi);
   tmem_st(lo_at, lo);
 }
+// The leading part alone.
+__device__ __forceinline__ void put_lead(uint32_t at, const float2 (&f)[8]) {
+  uint32_t hi[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const __half2 h = __float22half2_rn(f[j]);
+    hi[j] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  tmem_st(at, hi);
+}
 __device__ __forceinline__ float max16(float m, const float2 (&f)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(f[j].x), fabsf(f[j].y)));
@@ -348,18 +358,18 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
         mma_commit(&bars.p);
       }
       __syncwarp();
-      if (!wait(&bars.y, ph)) break;
-      tc_fence_after();
-      if (elect_one()) {
-        mma_inner<false>(tm + kColP, tm + kColYh, tm + kColYl, image, false);
-        mma_commit(&bars.e);
-      }
-      __syncwarp();
       if (it > 0 && !wait(&bars.of, ph ^ 1)) break;
       tc_fence_after();
       if (elect_one()) {
         mma_state<DK, NT, LEAD>(tm + kColN, tm + kColSh, tm + kColSl, q);
         mma_commit(&bars.n);
+      }
+      __syncwarp();
+      if (!wait(&bars.y, ph)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_inner<false>(tm + kColP, tm + kColYh, tm + kColYl, image, false);
+        mma_commit(&bars.e);
       }
       __syncwarp();
       if (!wait(&bars.w, ph)) break;
@@ -471,26 +481,33 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       if (lane == 0) bar_arrive(&bars.empty[s]);
       return true;
     };
-    // The output of chunk c, whose U was scaled by us.
-    auto put_output = [&](int c, float us) {
-      const uint32_t ph = c & 1;
+    // The output of chunk c, whose U was scaled by us, in two parts that fit
+    // where the thread would wait otherwise: taken from tensor memory, and
+    // stored.
+    T out[TK];
+    auto take_output = [&](int c, float us) {
       const float inv_u = scale_inverse(us);
       const float *gates = gates_of(c) + group * TK;
-      if (!wait(&bars.o, ph)) return false;
-      if (STAGED && a.o && c > 0 && !wait(&bars.got, ph ^ 1)) return false;
+      if (!wait(&bars.o, c & 1)) return false;
       tc_fence_after();
       uint32_t r[16];
       tmem_ld(lb + kColN + group * TK, r);
       tmem_wait_ld();
       warp_arrive(&bars.of, lane);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 o = mul2(pair(r, j), mul2(gate(gates + 4 * 64, j), both(inv_u)));
+        out[2 * j] = from_acc<T>(o.x);
+        out[2 * j + 1] = from_acc<T>(o.y);
+      }
+      return true;
+    };
+    auto put_output = [&](int c) {
       if (STAGED && a.o) {
+        if (c > 0 && !wait(&bars.got, (c & 1) ^ 1)) return false;
         T *os = reinterpret_cast<T *>(stages + ST * kStage) + group * TK * 128 + row;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 o = mul2(pair(r, j), mul2(gate(gates + 4 * 64, j), both(inv_u)));
-          os[2 * j * 128] = from_acc<T>(o.x);
-          os[(2 * j + 1) * 128] = from_acc<T>(o.y);
-        }
+        for (int j = 0; j < TK; ++j) os[j * 128] = out[j];
       } else if (a.o && live) {
         const long long r0 = sp.row0 + (long long)c * kChunk + group * TK;
         const long long left = sp.rows - (long long)c * kChunk - group * TK;
@@ -498,8 +515,7 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
         const long long step = (long long)a.vheads * a.dv;
 #pragma unroll
         for (int j = 0; j < TK; ++j)
-          if (j < left)
-            o[j * step] = from_acc<T>(__uint_as_float(r[j]) * (gates[4 * 64 + j] * inv_u));
+          if (j < left) o[j * step] = out[j];
       }
       __syncwarp();
       if (STAGED && lane == 0) bar_arrive(&bars.put);
@@ -529,6 +545,8 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       const float ys = bound_scale(by), us = bound_scale(by * chunk[2]), wsc = bound_scale(bw);
       const float inv_y = scale_inverse(ys);
       const float next_ss = bound_scale(fmaf(Gamma, smax, 128.0f * bw));
+      if (it > 0 && !(ok = take_output(it - 1, us_before))) break;
+      us_before = us;
       float2 gf[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -545,9 +563,21 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, f);
       tmem_wait_st();
       warp_arrive(&bars.y, lane);
-      // While E is computed: the output of the chunk before.
-      if (it > 0 && !(ok = put_output(it - 1, us_before))) break;
-      us_before = us;
+      // While E is computed: N in units of U M^T, the start of O, and the
+      // output of the chunk before.
+      if (!(ok = wait(&bars.n, ph))) break;
+      tc_fence_after();
+      tmem_ld(lb + kColN + group * TK, r);
+      tmem_wait_ld();
+      const float ratio = inv_s * us;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 n = mul2(pair(r, j), mul2(gate(gates + 3 * 64, j), both(ratio)));
+        r[2 * j] = __float_as_uint(n.x);
+        r[2 * j + 1] = __float_as_uint(n.y);
+      }
+      tmem_st(lb + kColN + group * TK, r);
+      if (it > 0 && !(ok = put_output(it - 1))) break;
       // W = E beta Gamma / gamma, on which the new state waits, then U = E beta
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -565,28 +595,16 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         f[j] = mul2(pair(r, j), mul2(gate(gates + 2 * 64, j), both(inv_y * us)));
-      put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, f);
+      if constexpr (LEAD) put_lead(lb + kColYh + group * 8, f);
+      else put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, f);
+      tmem_wait_st();
+      warp_arrive(&bars.u, lane);
       if constexpr (SAVE) {
         float *dst = rows + saved(it) * (64 * 128) + group * TK * 128 + row;
 #pragma unroll
         for (int j = 0; j < TK; ++j)
           dst[j * 128] = __uint_as_float(r[j]) * (gates[5 * 64 + j] * inv_y);
       }
-      // N in units of U M^T, the start of O
-      if (!(ok = wait(&bars.n, ph))) break;
-      tc_fence_after();
-      tmem_ld(lb + kColN + group * TK, r);
-      tmem_wait_ld();
-      const float ratio = inv_s * us;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 n = mul2(pair(r, j), mul2(gate(gates + 3 * 64, j), both(ratio)));
-        r[2 * j] = __float_as_uint(n.x);
-        r[2 * j + 1] = __float_as_uint(n.y);
-      }
-      tmem_st(lb + kColN + group * TK, r);
-      tmem_wait_st();
-      warp_arrive(&bars.u, lane);
       const bool more = it + 1 < sp.chunks;
       if (more) {
         fetch_v(it + 1);
@@ -607,7 +625,8 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       ss = next_ss;
       if (more) put_state(it + 1);
     }
-    if (ok && sp.chunks > 0) ok = put_output(sp.chunks - 1, us_before);
+    if (ok && sp.chunks > 0)
+      ok = take_output(sp.chunks - 1, us_before) && put_output(sp.chunks - 1);
     if (ok && a.state_out && live) {
 #pragma unroll
       for (int p = 0; p < SP; ++p)
