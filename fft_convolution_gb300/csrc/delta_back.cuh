@@ -45,10 +45,10 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
   const T *dout = static_cast<const T *>(ga.dout) + out_row(a, sp.b, sp.row0, packed, h);
   const long long ostep = (long long)a.vheads * a.dv;
 
-  if (warp == kScanWarps + 2) {
+  if (warp >= kScanWarps + 2) {
     if constexpr (STAGED)
       scan_store<T>(a, sp, packed, h, true, ga.dv, vb * 128, stages + ST * kStage, &bars, &failed,
-                    status, lane);
+                    status, warp - kScanWarps - 2, lane);
   } else if (warp == kScanWarps + 1) {
     scan_load<T, DK, STAGED>(a, sp, h, true, kq, images, dout + vb * 128, ostep, vb * 128, stages,
                              ring, &bars, &failed, status, lane);
@@ -161,43 +161,15 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
         const int c = group * SC + p * 16 + 2 * j;
         S[p][j] = make_float2(initial(c), initial(c + 1));
       }
-    // dO of the chunk of step `it` into f, and the largest of it.
-    float2 f[8];
-    float omax = 0.0f;
-    auto take = [&](int it) {
-      const int s = it % ST;
-      if (!wait(&bars.full[s], (it / ST) & 1)) return false;
-      const T *xs = reinterpret_cast<const T *>(stages + s * kStage + kStage - kRows16) +
+    // dO of the chunk of step `it`.
+    auto take = [&](int it, float2 (&f)[8]) {
+      const T *xs = reinterpret_cast<const T *>(stages + (it % ST) * kStage + kStage - kRows16) +
                     group * TK * 128 + row;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         f[j] = STAGED ? make_float2(to_acc(xs[2 * j * 128]), to_acc(xs[(2 * j + 1) * 128]))
                       : make_float2(to_acc(vr[STAGED ? 0 : 2 * j]),
                                     to_acc(vr[STAGED ? 0 : 2 * j + 1]));
-      omax = max16(0.0f, f);
-      __syncwarp();
-      if (lane == 0) bar_arrive(&bars.empty[s]);
-      return true;
-    };
-    // dV of the chunk of step `it`.
-    T dv[TK];
-    auto put_dv = [&](int it) {
-      if (STAGED) {
-        if (it > 0 && !wait(&bars.got, (it & 1) ^ 1)) return false;
-        T *out = reinterpret_cast<T *>(stages + ST * kStage) + group * TK * 128 + row;
-#pragma unroll
-        for (int j = 0; j < TK; ++j) out[j * 128] = dv[j];
-        __syncwarp();
-        if (lane == 0) bar_arrive(&bars.put);
-      } else if (live) {
-        const long long r0 = (long long)chunk_of(it) * kChunk + group * TK;
-        const long long left = sp.rows - r0;
-        T *out = static_cast<T *>(ga.dv) + out_row(a, sp.b, sp.row0 + r0, packed, h) + dvr;
-#pragma unroll
-        for (int j = 0; j < TK; ++j)
-          if (j < left) out[j * ostep] = dv[j];
-      }
-      return true;
     };
     bool ok = true;
     if (sp.chunks > 0) {
@@ -208,7 +180,6 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
 #pragma unroll
         for (int j = 0; j < 8; ++j) S[p][j] = mul2(S[p][j], both(ss));
       put_state(chunk_of(0));
-      ok = take(0);
     }
     for (int it = 0; it < sp.chunks && ok; ++it) {
       const uint32_t ph = it & 1;
@@ -218,7 +189,9 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
       uint32_t r[16];
       float2 x[8];
       // While P is computed: the scales, and dO as an operand.
-      const float2 most = agree.largest(state_max(), omax);
+      if (!(ok = wait(&bars.full[it % ST], (it / ST) & 1))) break;
+      take(it, x);
+      const float2 most = agree.largest(state_max(), max16(0.0f, x));
       const float Gamma = chunk[0], inv_s = scale_inverse(ss), smax = most.x * inv_s;
       const float os = bound_scale(most.y);
       const float by = chunk[1] * smax + chunk[2] * most.y;
@@ -227,8 +200,9 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
       const float inv_y = scale_inverse(ys);
       const float next_ss = bound_scale(fmaf(Gamma, smax, 256.0f * bw));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = mul2(f[j], both(os));
-      put_split(lb + kColWh + group * 8, lb + kColWl + group * 8, x);
+      for (int j = 0; j < 8; ++j) x[j] = mul2(x[j], both(os));
+      if constexpr (NT == 1) put_lead(lb + kColWh + group * 8, x);
+      else put_split(lb + kColWh + group * 8, lb + kColWl + group * 8, x);
       tmem_wait_st();
       warp_arrive(&bars.of, lane);
       // dU
@@ -247,46 +221,53 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
       put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, x);
       tmem_wait_st();
       warp_arrive(&bars.y, lane);
-      // While F is computed: scale gamma dO, where dO was, and the chunk
-      // before's dV.
+      // While F is computed: scale gamma dO, where dO was.
+      take(it, x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = mul2(f[j], mul2(gate(gates + 5 * 64, j), both(ws)));
-      put_split(lb + kColWh + group * 8, lb + kColWl + group * 8, f);
+      for (int j = 0; j < 8; ++j) x[j] = mul2(x[j], mul2(gate(gates + 5 * 64, j), both(ws)));
+      put_split(lb + kColWh + group * 8, lb + kColWl + group * 8, x);
       tmem_wait_st();
       warp_arrive(&bars.u, lane);
-      if (it > 0 && !(ok = put_dv(it - 1))) break;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        f[j] = mul2(mul2(mul2(gate(gates + 2 * 64, j), both(inv_y)), gate(gates + 4 * 64, j)),
-                    both(ws));
+      if (lane == 0) bar_arrive(&bars.empty[it % ST]);
       // gamma beta F, where dU was
       if (!(ok = wait(&bars.e, ph))) break;
       tc_fence_after();
       tmem_ld(lb + kColP + group * TK, r);
       tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = mul2(pair(r, j), f[j]);
+      for (int j = 0; j < 8; ++j)
+        x[j] = mul2(pair(r, j), mul2(gate(gates + 4 * 64, j), both(inv_y * ws)));
       put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, x);
       tmem_wait_st();
       warp_arrive(&bars.w, lane);
-      // F itself, and dV = beta F
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        x[j] = mul2(pair(r, j), mul2(gate(gates + 2 * 64, j), both(inv_y)));
+      // While the new dS is computed: F itself (taken from tensor memory once
+      // more, which saves registers), and dV = beta F
+      tmem_ld(lb + kColP + group * TK, r);
+      tmem_wait_ld();
       float *dst = rows + saved(c) * (64 * 128) + group * TK * 128 + row;
+      TokenValues<T> dv;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        dst[2 * j * 128] = x[j].x;
-        dst[(2 * j + 1) * 128] = x[j].y;
-        x[j] = mul2(x[j], gate(gates + 3 * 64, j));
-        dv[2 * j] = from_acc<T>(x[j].x);
-        dv[2 * j + 1] = from_acc<T>(x[j].y);
+        const float2 y = mul2(pair(r, j), mul2(gate(gates + 2 * 64, j), both(inv_y)));
+        dst[2 * j * 128] = y.x;
+        dst[(2 * j + 1) * 128] = y.y;
+        dv.set(j, mul2(y, gate(gates + 3 * 64, j)));
+      }
+      if (STAGED) {
+        if (it > 0 && !(ok = wait(&bars.got, ph ^ 1))) break;
+        dv.put(stages + ST * kStage, group * TK, row, lane);
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bars.put);
+      } else if (live) {
+        const long long r0 = (long long)c * kChunk + group * TK;
+        const long long left = sp.rows - r0;
+        T *out = static_cast<T *>(ga.dv) + out_row(a, sp.b, sp.row0 + r0, packed, h) + dvr;
+#pragma unroll
+        for (int j = 0; j < TK; ++j)
+          if (j < left) out[j * ostep] = dv.get(j);
       }
       const bool more = it + 1 < sp.chunks;
-      if (more) {
-        fetch(it + 1);
-        if (!(ok = take(it + 1))) break;
-      }
+      if (more) fetch(it + 1);
       // The gradient of the state before
       const float keep = Gamma * inv_s * next_ss, add = scale_inverse(ws) * next_ss;
       if (!(ok = wait(&bars.s, ph))) break;
@@ -302,7 +283,6 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
       ss = next_ss;
       if (more) put_state(c - 1);
     }
-    if (ok && sp.chunks > 0) ok = put_dv(sp.chunks - 1);
     if (ok && ga.dinitial && live) {
       const float inv = scale_inverse(ss);
 #pragma unroll

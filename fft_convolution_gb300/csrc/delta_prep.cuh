@@ -19,11 +19,11 @@
 // strides and alignment.
 //
 // Forward image: (I + A beta)^-1 and M by rows; per token
-//   0: -gamma 2^ek   1: Gamma/gamma 2^ek   2: beta 2^et   3: gamma 2^(eq - em)
+//   0: -gamma 2^ek   1: Gamma/gamma beta 2^(ek + et)   2: beta 2^et   3: gamma 2^(eq - em)
 //   4: scale 2^em    5: 2^et
 // BACK image: (I + beta A)^-T and M^T; per token
 //   0: Gamma/gamma 2^ek   1: scale 2^em   2: 2^et   3: beta
-//   4: -gamma beta 2^ek   5: scale gamma 2^eq
+//   4: -gamma beta 2^(ek + et)   5: scale gamma 2^eq
 // and in both 6: 2^ek, 7: 2^eq,
 // where 2^-e is the scale of a token's row of K (ek), Q (eq), of the inverse
 // (et) and of M (em).
@@ -352,7 +352,7 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
         const float ek = inv_kq[tid], eq = inv_kq[64 + tid], em = inv[1][tid], et = inv[0][tid];
         const float gam = decay_between(G[tid], make_float2(0.0f, 0.0f));
         const float dec = decay_between(G[63], G[tid]), bt = beta_s[tid];
-        const float ga[kGates] = {-gam * ek, dec * ek, bt * et, gam * (eq / em),
+        const float ga[kGates] = {-gam * ek, dec * bt * ek * et, bt * et, gam * (eq / em),
                                   a.scale * em, et, ek, eq};
         const float ba = fabsf(bt) * sum[0][tid], sc = fabsf(a.scale);
         float b[8];
@@ -365,7 +365,7 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
         if constexpr (GRAD) {
           gates = reinterpret_cast<float *>(imageb + 4 * kTile) + tid;
           const float gb[kGates] = {dec * ek, a.scale * inv[3][tid], inv[2][tid], bt,
-                                    -gam * bt * ek, a.scale * gam * eq, ek, eq};
+                                    -gam * bt * ek * inv[2][tid], a.scale * gam * eq, ek, eq};
 #pragma unroll
           for (int k = 0; k < kGates; ++k) gates[k * 64] = gb[k];
           if (tid == 63) gates[kChunkAt - 63] = gam;

@@ -20,7 +20,7 @@
 //
 // Roles: 16 warps of arithmetic (two per scheduler left its issue slots 60%
 // empty), one thread that issues the products, a warp that fetches the chunks'
-// images ahead and one that stores (bulk copies).
+// images ahead (bulk copies) and two that store.
 //
 // Tensor memory (512 columns):
 //   W K (fp32)       0 .. DK - 1
@@ -36,7 +36,7 @@ namespace fftgb {
 constexpr int kScanWarps = 16;                       // of arithmetic
 constexpr int kScanGroups = kScanWarps / 4;          // threads that share a column of v
 constexpr int kScanTok = 64 / kScanGroups;           // tokens of each
-constexpr int kScanThreads = (kScanWarps + 3) * 32;
+constexpr int kScanThreads = (kScanWarps + 4) * 32;
 constexpr int kScanStages = 2;
 
 // 64 tokens x 128 columns of a 16-bit type.
@@ -130,7 +130,7 @@ __device__ __forceinline__ void scan_load(const DeltaArgs &a, const ScanSpan &sp
       const uint32_t dst = smem_u32(stage + kStage - kRows16) + (lane & 15) * 16;
       const T *src = x + r0 * step + (lane & 15) * 8;
       if ((lane & 15) < pieces) {
-#pragma unroll 8
+#pragma unroll 16
         for (int r = lane >> 4; r < kChunk; r += 2)
           copy16(dst + r * 256, src + (r < last ? r : last) * step);
       }
@@ -146,28 +146,81 @@ __device__ __forceinline__ void scan_load(const DeltaArgs &a, const ScanSpan &sp
   }
 }
 
-// The storing warp, STAGED: the chunks' rows from shared memory to the
-// contiguous array [sequence][token][head][dv].
+// A thread's values of one column of v, 16 tokens.  Into the rows in shared
+// memory two lanes put their columns' values of a token in one word each, one
+// lane the even tokens, the other the odd ones (stores of two bytes took four
+// times as long); odd rows have their 64-byte halves exchanged, so that the
+// two lanes' words lie in different banks.
+template <typename T> struct TokenValues {
+  T v[kScanTok];
+  __device__ __forceinline__ void set(int j, float2 x) {
+    v[2 * j] = from_acc<T>(x.x);
+    v[2 * j + 1] = from_acc<T>(x.y);
+  }
+  __device__ __forceinline__ T get(int j) const { return v[j]; }
+  __device__ __forceinline__ void put(char *, int, int, int) const {}  // not staged
+};
+template <typename T> struct TokenPairs {
+  uint32_t w[kScanTok / 2];
+  __device__ __forceinline__ T get(int j) const {
+    const uint16_t x = (uint16_t)(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
+    return *reinterpret_cast<const T *>(&x);
+  }
+  __device__ __forceinline__ void put(char *rows, int tok, int col, int lane) const {
+    const int odd = lane & 1;
+    char *at = rows + (tok + odd) * 256 + (((col & ~1) * 2) ^ (odd << 6));
+#pragma unroll
+    for (int j = 0; j < kScanTok / 2; ++j) {
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, w[j], 1);
+      const uint32_t x = odd ? __byte_perm(o, w[j], 0x7632) : __byte_perm(w[j], o, 0x5410);
+      *reinterpret_cast<uint32_t *>(at + j * 512) = x;
+    }
+  }
+};
+template <> struct TokenValues<__nv_bfloat16> : TokenPairs<__nv_bfloat16> {
+  __device__ __forceinline__ void set(int j, float2 x) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(x.x, x.y);
+    w[j] = *reinterpret_cast<const uint32_t *>(&p);
+  }
+};
+template <> struct TokenValues<__half> : TokenPairs<__half> {
+  __device__ __forceinline__ void set(int j, float2 x) {
+    const __half2 p = __floats2half2_rn(x.x, x.y);
+    w[j] = *reinterpret_cast<const uint32_t *>(&p);
+  }
+};
+
+// The two storing warps, STAGED: the chunks' rows from shared memory to the
+// contiguous array [sequence][token][head][dv].  `which`: half of the rows.
 template <typename T>
 __device__ __forceinline__ void scan_store(const DeltaArgs &a, const ScanSpan &sp, bool packed,
                                            int h, bool backwards, void *out, int c0,
                                            const char *rows, ScanBars *bars,
-                                           volatile int *failed, int *status, int lane) {
+                                           volatile int *failed, int *status, int which,
+                                           int lane) {
   const int pieces = (a.dv - c0 < 128 ? a.dv - c0 : 128) / 8;
   const long long step = (long long)a.vheads * a.dv;
   for (int it = 0; it < sp.chunks; ++it) {
     const int ci = backwards ? sp.chunks - 1 - it : it;
     const bool ok = wait_or_fail(&bars->put, it & 1, failed, status);
     if (!__all_sync(0xffffffffu, ok)) break;
-    const long long r0 = (long long)ci * kChunk;
-    const int n = (int)(sp.rows - r0 < kChunk ? sp.rows - r0 : kChunk);
-    T *dst = static_cast<T *>(out) + out_row(a, sp.b, sp.row0 + r0, packed, h) + c0 +
+    const long long row = (long long)ci * kChunk;
+    const int n = (int)(sp.rows - row < kChunk ? sp.rows - row : kChunk);
+    T *dst = static_cast<T *>(out) + out_row(a, sp.b, sp.row0 + row, packed, h) + c0 +
              (lane & 15) * 8;
-    const char *src = rows + (lane & 15) * 16;
+    const char *src = rows + (((lane & 15) * 16) ^ ((lane >> 4) << 6));
     if ((lane & 15) < pieces) {
-#pragma unroll 4
-      for (int r = lane >> 4; r < n; r += 2)
-        *reinterpret_cast<uint4 *>(dst + r * step) = *reinterpret_cast<const uint4 *>(src + r * 256);
+      const int r0 = which * 32 + (lane >> 4);
+#pragma unroll
+      for (int b = 0; b < 32; b += 16) {
+        uint4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          x[k] = *reinterpret_cast<const uint4 *>(src + (r0 + b + 2 * k) * 256);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (r0 + b + 2 * k < n) *reinterpret_cast<uint4 *>(dst + (r0 + b + 2 * k) * step) = x[k];
+      }
     }
     __syncwarp();
     if (lane == 0) bar_arrive(&bars->got);
@@ -295,7 +348,8 @@ __device__ __forceinline__ uint32_t scan_begin(ScanBars &bars, uint32_t *slot, v
       bar_init(&bars.full[s], staged ? 33 : 1);
       bar_init(&bars.empty[s], 1 + kScanWarps);
     }
-    for (uint64_t *b : {&bars.p, &bars.n, &bars.e, &bars.s, &bars.o, &bars.got, &bars.done}) bar_init(b, 1);
+    for (uint64_t *b : {&bars.p, &bars.n, &bars.e, &bars.s, &bars.o, &bars.done}) bar_init(b, 1);
+    bar_init(&bars.got, 2);
     for (uint64_t *b : {&bars.y, &bars.w, &bars.u, &bars.sb, &bars.of, &bars.put})
       bar_init(b, kScanWarps);
     *failed = 0;
@@ -335,11 +389,11 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
   char *ring = stages + ST * kStage + (STAGED ? kRows16 : 0);
   auto wait = [&](uint64_t *b, uint32_t parity) { return wait_or_fail(b, parity, &failed, status); };
 
-  if (warp == kScanWarps + 2) {
+  if (warp >= kScanWarps + 2) {
     if constexpr (STAGED)
       if (a.o)
         scan_store<T>(a, sp, plan.chunk0 != nullptr, h, false, a.o, vb * 128, stages + ST * kStage,
-                      &bars, &failed, status, lane);
+                      &bars, &failed, status, warp - kScanWarps - 2, lane);
   } else if (warp == kScanWarps + 1) {
     scan_load<T, DK, STAGED>(a, sp, h, false, kq, images,
                              head_rows<T>(a.v, a.sv, sp.b, sp.row0, h) + vb * 128, a.sv.tok,
@@ -358,18 +412,18 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
         mma_commit(&bars.p);
       }
       __syncwarp();
-      if (it > 0 && !wait(&bars.of, ph ^ 1)) break;
-      tc_fence_after();
-      if (elect_one()) {
-        mma_state<DK, NT, LEAD>(tm + kColN, tm + kColSh, tm + kColSl, q);
-        mma_commit(&bars.n);
-      }
-      __syncwarp();
       if (!wait(&bars.y, ph)) break;
       tc_fence_after();
       if (elect_one()) {
         mma_inner<false>(tm + kColP, tm + kColYh, tm + kColYl, image, false);
         mma_commit(&bars.e);
+      }
+      __syncwarp();
+      if (it > 0 && !wait(&bars.of, ph ^ 1)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_state<DK, NT, LEAD>(tm + kColN, tm + kColSh, tm + kColSl, q);
+        mma_commit(&bars.n);
       }
       __syncwarp();
       if (!wait(&bars.w, ph)) break;
@@ -464,9 +518,8 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
         S[p][j] = make_float2(initial(col), initial(col + 1));
       }
     // V of chunk c into f, and the largest of it.
-    float2 f[8];
     float vmax = 0.0f;
-    auto take_v = [&](int c) {
+    auto take_v = [&](int c, float2 (&f)[8]) {
       const int s = c % ST;
       if (!wait(&bars.full[s], (c / ST) & 1)) return false;
       const T *vs = reinterpret_cast<const T *>(stages + s * kStage + kStage - kRows16) +
@@ -481,33 +534,23 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       if (lane == 0) bar_arrive(&bars.empty[s]);
       return true;
     };
-    // The output of chunk c, whose U was scaled by us, in two parts that fit
-    // where the thread would wait otherwise: taken from tensor memory, and
-    // stored.
-    T out[TK];
-    auto take_output = [&](int c, float us) {
+    // The output of chunk c, whose U was scaled by us.
+    auto put_output = [&](int c, float us) {
       const float inv_u = scale_inverse(us);
       const float *gates = gates_of(c) + group * TK;
       if (!wait(&bars.o, c & 1)) return false;
+      if (STAGED && a.o && c > 0 && !wait(&bars.got, (c & 1) ^ 1)) return false;
       tc_fence_after();
       uint32_t r[16];
       tmem_ld(lb + kColN + group * TK, r);
       tmem_wait_ld();
       warp_arrive(&bars.of, lane);
+      TokenValues<T> out;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 o = mul2(pair(r, j), mul2(gate(gates + 4 * 64, j), both(inv_u)));
-        out[2 * j] = from_acc<T>(o.x);
-        out[2 * j + 1] = from_acc<T>(o.y);
-      }
-      return true;
-    };
-    auto put_output = [&](int c) {
+      for (int j = 0; j < 8; ++j)
+        out.set(j, mul2(pair(r, j), mul2(gate(gates + 4 * 64, j), both(inv_u))));
       if (STAGED && a.o) {
-        if (c > 0 && !wait(&bars.got, (c & 1) ^ 1)) return false;
-        T *os = reinterpret_cast<T *>(stages + ST * kStage) + group * TK * 128 + row;
-#pragma unroll
-        for (int j = 0; j < TK; ++j) os[j * 128] = out[j];
+        out.put(stages + ST * kStage, group * TK, row, lane);
       } else if (a.o && live) {
         const long long r0 = sp.row0 + (long long)c * kChunk + group * TK;
         const long long left = sp.rows - (long long)c * kChunk - group * TK;
@@ -515,7 +558,7 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
         const long long step = (long long)a.vheads * a.dv;
 #pragma unroll
         for (int j = 0; j < TK; ++j)
-          if (j < left) o[j * step] = out[j];
+          if (j < left) o[j * step] = out.get(j);
       }
       __syncwarp();
       if (STAGED && lane == 0) bar_arrive(&bars.put);
@@ -530,14 +573,15 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
 #pragma unroll
         for (int j = 0; j < 8; ++j) S[p][j] = mul2(S[p][j], both(ss));
       put_state(0);
-      ok = take_v(0);
     }
     float us_before = 1.0f;
     for (int it = 0; it < sp.chunks && ok; ++it) {
       const uint32_t ph = it & 1;
       const float *gates = gates_of(it) + group * TK;
       uint32_t r[16];
-      // While P is computed: the scales.
+      // While P is computed: V, and the scales.
+      float2 f[8];
+      if (!(ok = take_v(it, f))) break;
       const float2 most = agree.largest(state_max(), vmax);
       const float *chunk = gates_of(it) + kChunkAt;
       const float Gamma = chunk[0], inv_s = scale_inverse(ss), smax = most.x * inv_s;
@@ -545,26 +589,48 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       const float ys = bound_scale(by), us = bound_scale(by * chunk[2]), wsc = bound_scale(bw);
       const float inv_y = scale_inverse(ys);
       const float next_ss = bound_scale(fmaf(Gamma, smax, 128.0f * bw));
-      if (it > 0 && !(ok = take_output(it - 1, us_before))) break;
-      us_before = us;
-      float2 gf[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        f[j] = mul2(f[j], both(ys));
-        gf[j] = mul2(gate(gates, j), both(inv_s * ys));
-      }
+      for (int j = 0; j < 8; ++j) f[j] = mul2(f[j], both(ys));
       // Y = V^T - P gamma
       if (!(ok = wait(&bars.p, ph))) break;
       tc_fence_after();
       tmem_ld(lb + kColP + group * TK, r);
       tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = fma2(gf[j], pair(r, j), f[j]);
+      for (int j = 0; j < 8; ++j)
+        f[j] = fma2(mul2(gate(gates, j), both(inv_s * ys)), pair(r, j), f[j]);
       put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, f);
       tmem_wait_st();
       warp_arrive(&bars.y, lane);
-      // While E is computed: N in units of U M^T, the start of O, and the
-      // output of the chunk before.
+      // While E is computed: the output of the chunk before.
+      if (it > 0 && !(ok = put_output(it - 1, us_before))) break;
+      us_before = us;
+      // W = E beta Gamma / gamma, on which the new state waits, then U = E beta
+      // (E taken from tensor memory once more, which saves registers).
+      if (!(ok = wait(&bars.e, ph))) break;
+      tc_fence_after();
+      tmem_ld(lb + kColP + group * TK, r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        f[j] = mul2(pair(r, j), mul2(gate(gates + 64, j), both(inv_y * wsc)));
+      put_split(lb + kColWh + group * 8, lb + kColWl + group * 8, f);
+      tmem_wait_st();
+      warp_arrive(&bars.w, lane);
+      tmem_ld(lb + kColP + group * TK, r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        f[j] = mul2(pair(r, j), mul2(gate(gates + 2 * 64, j), both(inv_y * us)));
+      if constexpr (LEAD) put_lead(lb + kColYh + group * 8, f);
+      else put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, f);
+      if constexpr (SAVE) {
+        float *dst = rows + saved(it) * (64 * 128) + group * TK * 128 + row;
+#pragma unroll
+        for (int j = 0; j < TK; ++j)
+          dst[j * 128] = __uint_as_float(r[j]) * (gates[5 * 64 + j] * inv_y);
+      }
+      // While the new state is computed: N in units of U M^T, the start of O
       if (!(ok = wait(&bars.n, ph))) break;
       tc_fence_after();
       tmem_ld(lb + kColN + group * TK, r);
@@ -577,39 +643,10 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
         r[2 * j + 1] = __float_as_uint(n.y);
       }
       tmem_st(lb + kColN + group * TK, r);
-      if (it > 0 && !(ok = put_output(it - 1))) break;
-      // W = E beta Gamma / gamma, on which the new state waits, then U = E beta
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        gf[j] = mul2(mul2(mul2(gate(gates + 2 * 64, j), both(inv_y)), gate(gates + 64, j)),
-                     both(wsc));
-      if (!(ok = wait(&bars.e, ph))) break;
-      tc_fence_after();
-      tmem_ld(lb + kColP + group * TK, r);
-      tmem_wait_ld();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = mul2(pair(r, j), gf[j]);
-      put_split(lb + kColWh + group * 8, lb + kColWl + group * 8, f);
-      tmem_wait_st();
-      warp_arrive(&bars.w, lane);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        f[j] = mul2(pair(r, j), mul2(gate(gates + 2 * 64, j), both(inv_y * us)));
-      if constexpr (LEAD) put_lead(lb + kColYh + group * 8, f);
-      else put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, f);
       tmem_wait_st();
       warp_arrive(&bars.u, lane);
-      if constexpr (SAVE) {
-        float *dst = rows + saved(it) * (64 * 128) + group * TK * 128 + row;
-#pragma unroll
-        for (int j = 0; j < TK; ++j)
-          dst[j * 128] = __uint_as_float(r[j]) * (gates[5 * 64 + j] * inv_y);
-      }
       const bool more = it + 1 < sp.chunks;
-      if (more) {
-        fetch_v(it + 1);
-        if (!(ok = take_v(it + 1))) break;
-      }
+      if (more) fetch_v(it + 1);
       // The new state
       const float keep = Gamma * inv_s * next_ss, add = scale_inverse(wsc) * next_ss;
       if (!(ok = wait(&bars.s, ph))) break;
@@ -625,8 +662,7 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       ss = next_ss;
       if (more) put_state(it + 1);
     }
-    if (ok && sp.chunks > 0)
-      ok = take_output(sp.chunks - 1, us_before) && put_output(sp.chunks - 1);
+    if (ok && sp.chunks > 0) ok = put_output(sp.chunks - 1, us_before);
     if (ok && a.state_out && live) {
 #pragma unroll
       for (int p = 0; p < SP; ++p)

@@ -240,10 +240,14 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 // value or 2^-25, whichever is more; a larger scale (below fp16's 2^16)
 // extends the former downwards.
 __device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
-  const __half2 h = __float22half2_rn(x);
-  const __half2 l = __float22half2_rn(fma2(__half22float2(h), both(-1.0f), x));
-  hi = *reinterpret_cast<const uint32_t *>(&h);
-  lo = *reinterpret_cast<const uint32_t *>(&l);
+  asm("{\n\t.reg .b16 h0, h1;\n\t.reg .f32 l0, l1;\n\t"
+      "cvt.rn.f16x2.f32 %0, %3, %2;\n\t"
+      "mov.b32 {h0, h1}, %0;\n\t"
+      "sub.rn.f32.f16 l0, h0, %2;\n\tsub.rn.f32.f16 l1, h1, %3;\n\t"
+      "neg.f32 l0, l0;\n\tneg.f32 l1, l1;\n\t"
+      "cvt.rn.f16x2.f32 %1, l1, l0;\n\t}"
+      : "=&r"(hi), "=r"(lo)
+      : "f"(x.x), "f"(x.y));
 }
 
 }  // namespace fftgb
