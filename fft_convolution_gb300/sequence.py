@@ -7,16 +7,19 @@ to that stream.
 """
 from __future__ import annotations
 
+import array
 import contextlib
-import ctypes
+import struct
 
 import torch
 
-from . import (FFT_ELEM_BF16, FFT_ELEM_F16, FFT_ELEM_F32, FFT_ELEM_F64, DeltaDesc, _check, _lib)
+from . import FFT_ELEM_BF16, FFT_ELEM_F16, FFT_ELEM_F32, FFT_ELEM_F64, _check, _lib
 
 _ELEM = {torch.float32: FFT_ELEM_F32, torch.float64: FFT_ELEM_F64,
          torch.bfloat16: FFT_ELEM_BF16, torch.float16: FFT_ELEM_F16}
 _NULL = contextlib.nullcontext()
+# fft_delta_desc: sizes, five strides of three, scale, type (and its padding).
+_DESC = struct.Struct("=6q15qdi4x")
 
 
 def _elem(t, what: str) -> int:
@@ -38,12 +41,14 @@ def _ptr(t):
 
 
 def _device(first, *others):
-    """Every tensor given lies on one CUDA device."""
+    """Every tensor given lies on one CUDA device, which it returns."""
     if not first.is_cuda:
         raise ValueError("the operators take CUDA tensors")
+    device = first.device
     for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}")
+    return device
 
 
 def _workspace(nbytes: int, device):
@@ -55,6 +60,8 @@ def _workspace(nbytes: int, device):
 def _rows(t):
     """`t` as rows of its last axis, at one stride: a view where the strides
     allow it, else a copy."""
+    if t.is_contiguous():
+        return t if t.dim() == 2 else t.view(-1, t.shape[-1])
     if t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] == 1) and t.stride(0) >= t.shape[1]:
         return t
     t = t.reshape(-1, t.shape[-1])
@@ -68,7 +75,7 @@ def _vector(t, dim: int, what: str):
         return None
     if t.dim() != 1 or t.shape[0] != dim:
         raise ValueError(f"{what} must hold {dim} elements")
-    return t.contiguous()
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _row_stats(t, rows: int, dtype, what: str):
@@ -85,7 +92,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
     dim = x.shape[-1]
     if dim == 0:
         raise ValueError("rows need at least one element")
-    _device(x, weight, bias, out)
+    device = _device(x, weight, bias, out)
     code = _elem(x, "x")
     w, b = _vector(weight, dim, "weight"), _vector(bias, dim, "bias")
     if w is not None and b is not None and w.dtype != b.dtype:
@@ -96,15 +103,17 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
         x2 = _rows(x)
         rows = x2.shape[0]
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            out = torch.empty(x.shape, dtype=x.dtype, device=device)
         elif out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous():
             raise ValueError("out must be contiguous and like x")
-        stats = torch.empty((2,) + tuple(x.shape[:-1]), device=x.device,
-                            dtype=torch.float64 if code == FFT_ELEM_F64 else torch.float32)
-        mean, rstd = stats[0], stats[1]
-        _check(_lib.fft_layer_norm(x2.data_ptr(), max(dim, x2.stride(0)), _ptr(w), _ptr(b),
-                                   out.data_ptr(), dim, mean.data_ptr(), rstd.data_ptr(), rows, dim,
-                                   eps, code, wcode, handle), "fft_layer_norm")
+        kind = torch.float64 if code == FFT_ELEM_F64 else torch.float32
+        mean = torch.empty(x.shape[:-1], dtype=kind, device=device)
+        rstd = torch.empty(x.shape[:-1], dtype=kind, device=device)
+        rc = _lib.fft_layer_norm(x2.data_ptr(), max(dim, x2.stride(0)), _ptr(w), _ptr(b),
+                                 out.data_ptr(), dim, mean.data_ptr(), rstd.data_ptr(), rows, dim,
+                                 eps, code, wcode, handle)
+    if rc:
+        _check(rc, "fft_layer_norm")
     return out, mean, rstd
 
 
@@ -144,19 +153,22 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True, stream=Non
 # ---- gradient clipping ---------------------------------------------------------------
 
 def _table(tensors, what: str):
-    """Host arrays of the tensors' pointers, sizes and types."""
-    n = len(tensors)
+    """Host arrays of the tensors' pointers, sizes and types, and their device."""
     device = tensors[0].device
-    ptrs, numels, codes = [], [], []
-    for t in tensors:
-        if t.device != device or not t.is_cuda:
-            raise ValueError(f"{what}: CUDA tensors of one device")
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: contiguous tensors")
-        ptrs.append(t.data_ptr())
-        numels.append(t.numel())
-        codes.append(_elem(t, what))
-    return ((ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*numels), (ctypes.c_int * n)(*codes))
+    if device.type != "cuda" or any(t.device != device for t in tensors):
+        raise ValueError(f"{what}: CUDA tensors of one device")
+    if not all([t.is_contiguous() for t in tensors]):
+        raise ValueError(f"{what}: contiguous tensors")
+    try:
+        codes = array.array("i", [_ELEM[t.dtype] for t in tensors])
+    except KeyError:
+        raise TypeError(f"{what}: float32, float64, bfloat16 or float16") from None
+    return (array.array("Q", [t.data_ptr() for t in tensors]),
+            array.array("q", [t.numel() for t in tensors]), codes, device)
+
+
+def _address(a) -> int:
+    return a.buffer_info()[0]
 
 
 def grad_norm(grads, stream=None):
@@ -165,14 +177,14 @@ def grad_norm(grads, stream=None):
     grads = list(grads)
     if not grads:
         raise ValueError("grad_norm needs at least one tensor")
-    ptrs, numels, codes = _table(grads, "grads")
+    ptrs, numels, codes, device = _table(grads, "grads")
     context, handle = _on(stream)
     with context:
-        norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
+        norm = torch.empty((), dtype=torch.float32, device=device)
         nbytes = _lib.fft_grad_norm_workspace_bytes(len(grads))
-        ws = _workspace(nbytes, norm.device)
-        _check(_lib.fft_grad_norm(len(grads), ptrs, numels, codes, norm.data_ptr(), ws.data_ptr(),
-                                  nbytes, handle), "fft_grad_norm")
+        ws = _workspace(nbytes, device)
+        _check(_lib.fft_grad_norm(len(grads), _address(ptrs), _address(numels), _address(codes),
+                                  norm.data_ptr(), ws.data_ptr(), nbytes, handle), "fft_grad_norm")
     return norm
 
 
@@ -183,22 +195,22 @@ def clip_grad_norm(grads, max_norm: float, out=None, eps: float = 1e-6, stream=N
     grads = list(grads)
     if not grads:
         raise ValueError("clip_grad_norm needs at least one tensor")
-    ptrs, numels, codes = _table(grads, "grads")
+    ptrs, numels, codes, device = _table(grads, "grads")
     outs = ptrs
     if out is not None:
         out = list(out)
         if len(out) != len(grads):
             raise ValueError("out needs one tensor for each of grads")
-        outs, onumels, ocodes = _table(out, "out")
-        if out[0].device != grads[0].device or list(onumels) != list(numels) or \
-                list(ocodes) != list(codes):
+        outs, onumels, ocodes, odevice = _table(out, "out")
+        if odevice != device or onumels != numels or ocodes != codes:
             raise ValueError("out must be like grads")
     context, handle = _on(stream)
     with context:
-        norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
+        norm = torch.empty((), dtype=torch.float32, device=device)
         nbytes = _lib.fft_grad_norm_workspace_bytes(len(grads))
-        ws = _workspace(nbytes, norm.device)
-        _check(_lib.fft_clip_grad_norm(len(grads), ptrs, outs, numels, codes, max_norm, eps,
+        ws = _workspace(nbytes, device)
+        _check(_lib.fft_clip_grad_norm(len(grads), _address(ptrs), _address(outs),
+                                       _address(numels), _address(codes), max_norm, eps,
                                        norm.data_ptr(), ws.data_ptr(), nbytes, handle),
                "fft_clip_grad_norm")
     return norm
@@ -210,38 +222,29 @@ def _dense(t):
     return t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
 
 
-def _strides(t, packed: bool):
-    """(sequence, token, head) strides of [batch, tokens, heads, ...], or of
-    packed rows [rows, heads, ...]."""
-    s = t.stride()
-    return (0, s[0], s[1]) if packed else (s[0], s[1], s[2])
-
-
 def _delta_inputs(q, k, v, g, beta, scale, batch, packed: bool):
-    """Checks the five inputs; returns them (elements of a head contiguous)
-    and the descriptor."""
+    """Checks the five inputs; returns q, k, v (elements of a head contiguous),
+    fft_delta_desc, its head sizes and the device."""
+    qs, vs, kind = q.shape, v.shape, q.dtype
     lead = 1 if packed else 2
-    if q.dim() != lead + 2 or v.dim() != lead + 2 or q.shape != k.shape or \
-            v.shape[:lead] != q.shape[:lead]:
+    if len(qs) != lead + 2 or len(vs) != lead + 2 or k.shape != qs or vs[:lead] != qs[:lead]:
         raise ValueError("q, k: [batch, tokens, key heads, dk]; v: [batch, tokens, value heads, dv] "
                          "(packed rows: without the batch axis)")
-    if g.shape != v.shape[:-1] or beta.shape != g.shape:
+    if g.shape != vs[:-1] or beta.shape != g.shape:
         raise ValueError("g and beta hold one value per token and value head")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    if k.dtype != kind or v.dtype != kind:
         raise TypeError("q, k and v need one type")
     if g.dtype != torch.float32 or beta.dtype != torch.float32:
         raise TypeError("g and beta are float32")
-    _device(q, k, v, g, beta)
+    device = _device(q, k, v, g, beta)
     q, k, v = _dense(q), _dense(k), _dense(v)
     if scale is None:
-        scale = q.shape[-1] ** -0.5
-    desc = DeltaDesc(batch, q.shape[0] if packed else q.shape[1], q.shape[-2], v.shape[-2],
-                     q.shape[-1], v.shape[-1])
-    for name, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta)):
-        setattr(desc, name + "_stride", _strides(t, packed))
-    desc.scale = scale
-    desc.dtype = _elem(q, "q")
-    return q, k, v, desc
+        scale = qs[-1] ** -0.5
+    first = (0,) if packed else ()  # packed rows have no stride between sequences
+    strides = [first + t.stride()[:lead + 1] for t in (q, k, v, g, beta)]
+    desc = _DESC.pack(batch, qs[lead - 1], qs[-2], vs[-2], qs[-1], vs[-1], *strides[0], *strides[1],
+                      *strides[2], *strides[3], *strides[4], scale, _elem(q, "q"))
+    return q, k, v, desc, (vs[-2], qs[-1], vs[-1]), device
 
 
 def _packing(q, offsets):
@@ -272,20 +275,20 @@ def delta_rule(q, k, v, g, beta, scale=None, initial_state=None, offsets=None, o
     batch, packed = _packing(q, offsets)
     context, handle = _on(stream)
     with context:
-        q, k, v, desc = _delta_inputs(q, k, v, g, beta, scale, batch, packed)
+        q, k, v, desc, sizes, device = _delta_inputs(q, k, v, g, beta, scale, batch, packed)
         _device(q, initial_state, offsets, out)
         if packed:
             offsets = offsets.to(torch.int32).contiguous()
-        shape = (batch, desc.vheads, desc.dk, desc.dv)
+        shape = (batch,) + sizes
         initial_state = _states(initial_state, shape, "initial_state")
         if out is None:
-            out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+            out = torch.empty(v.shape, dtype=v.dtype, device=device)
         elif out.shape != v.shape or out.dtype != v.dtype or not out.is_contiguous():
             raise ValueError("out must be contiguous and like v")
-        final = torch.empty(shape, dtype=torch.float32, device=v.device)
-        nbytes = _lib.fft_delta_rule_workspace_bytes(ctypes.byref(desc), packed)
-        ws = _workspace(nbytes, v.device)
-        _check(_lib.fft_delta_rule(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        final = torch.empty(shape, dtype=torch.float32, device=device)
+        nbytes = _lib.fft_delta_rule_workspace_bytes(desc, packed)
+        ws = _workspace(nbytes, device)
+        _check(_lib.fft_delta_rule(desc, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                    g.data_ptr(), beta.data_ptr(), _ptr(offsets),
                                    _ptr(initial_state), out.data_ptr(), final.data_ptr(),
                                    ws.data_ptr(), nbytes, handle), "fft_delta_rule")
@@ -300,24 +303,24 @@ def delta_rule_backward(do, q, k, v, g, beta, scale=None, initial_state=None, of
     batch, packed = _packing(q, offsets)
     context, handle = _on(stream)
     with context:
-        q, k, v, desc = _delta_inputs(q, k, v, g, beta, scale, batch, packed)
+        q, k, v, desc, sizes, device = _delta_inputs(q, k, v, g, beta, scale, batch, packed)
         _device(q, do, initial_state, dfinal_state, offsets)
         if do.shape != v.shape or do.dtype != v.dtype:
             raise ValueError("do must be like v")
         do = do.contiguous()
         if packed:
             offsets = offsets.to(torch.int32).contiguous()
-        shape = (batch, desc.vheads, desc.dk, desc.dv)
+        shape = (batch,) + sizes
         initial_state = _states(initial_state, shape, "initial_state")
         dfinal_state = _states(dfinal_state, shape, "dfinal_state")
-        new = lambda like, dtype: torch.empty(like.shape, dtype=dtype, device=v.device)  # noqa: E731
+        new = lambda like, dtype: torch.empty(like.shape, dtype=dtype, device=device)  # noqa: E731
         dq, dk, dv = new(q, q.dtype), new(k, q.dtype), new(v, q.dtype)
         dg, dbeta = new(g, torch.float32), new(g, torch.float32)
-        dinitial = torch.empty(shape, dtype=torch.float32, device=v.device)
-        nbytes = _lib.fft_delta_rule_backward_workspace_bytes(ctypes.byref(desc), packed)
-        ws = _workspace(nbytes, v.device)
+        dinitial = torch.empty(shape, dtype=torch.float32, device=device)
+        nbytes = _lib.fft_delta_rule_backward_workspace_bytes(desc, packed)
+        ws = _workspace(nbytes, device)
         _check(_lib.fft_delta_rule_backward(
-            ctypes.byref(desc), do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            desc, do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
             g.data_ptr(), beta.data_ptr(), _ptr(offsets), _ptr(initial_state), _ptr(dfinal_state),
             dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(),
             dinitial.data_ptr(), ws.data_ptr(), nbytes, handle), "fft_delta_rule_backward")
@@ -332,19 +335,19 @@ def delta_rule_step(q, k, v, g, beta, state, slots=None, scale=None, out=None, s
     o is 0); by default sequence i has state i."""
     context, handle = _on(stream)
     with context:
-        q, k, v, desc = _delta_inputs(q, k, v, g, beta, scale, q.shape[0], False)
+        q, k, v, desc, sizes, device = _delta_inputs(q, k, v, g, beta, scale, q.shape[0], False)
         _device(q, state, slots, out)
         if state.dtype != torch.float32 or not state.is_contiguous() or state.dim() != 4 or \
-                state.shape[1:] != (v.shape[2], q.shape[3], v.shape[3]):
+                state.shape[1:] != sizes:
             raise ValueError("state must be contiguous float32 [pool, value heads, dk, dv]")
         if slots is not None and (slots.dtype != torch.int32 or slots.shape != (q.shape[0],)
                                   or not slots.is_contiguous()):
             raise ValueError("slots must be contiguous int32 [batch]")
         if out is None:
-            out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+            out = torch.empty(v.shape, dtype=v.dtype, device=device)
         elif out.shape != v.shape or out.dtype != v.dtype or not out.is_contiguous():
             raise ValueError("out must be contiguous and like v")
-        _check(_lib.fft_delta_rule_step(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        _check(_lib.fft_delta_rule_step(desc, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                         g.data_ptr(), beta.data_ptr(), state.data_ptr(), _ptr(slots),
                                         state.shape[0], out.data_ptr(), handle),
                "fft_delta_rule_step")
