@@ -29,10 +29,16 @@ def _elem(t, what: str) -> int:
     return code
 
 
-def _on(stream):
+# Handle of torch's current stream on a device: without building a Stream
+# object, where torch offers that (it costs as much as a kernel launch).
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on(stream, device):
     """(context in which the call's allocations are made, stream handle)."""
     if stream is None:
-        return _NULL, torch.cuda.current_stream().cuda_stream
+        return _NULL, _current(device.index)
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
@@ -98,7 +104,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
     if w is not None and b is not None and w.dtype != b.dtype:
         raise TypeError("weight and bias need one type")
     wcode = code if w is None and b is None else _elem(w if w is not None else b, "weight")
-    context, handle = _on(stream)
+    context, handle = _on(stream, device)
     with context:
         x2 = _rows(x)
         rows = x2.shape[0]
@@ -125,24 +131,24 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True, stream=Non
     dim = x.shape[-1]
     if dy.shape != x.shape or dy.dtype != x.dtype or dim == 0:
         raise ValueError("dy must be like x")
-    _device(x, dy, weight, mean, rstd)
+    device = _device(x, dy, weight, mean, rstd)
     code = _elem(x, "x")
     w = _vector(weight, dim, "weight")
     wcode = code if w is None else _elem(w, "weight")
     wtype = x.dtype if w is None else w.dtype
-    context, handle = _on(stream)
+    context, handle = _on(stream, device)
     with context:
         x2, dy2 = _rows(x), _rows(dy)
         rows = x2.shape[0]
         mean, rstd = (_row_stats(t, rows, x.dtype, n) for t, n in ((mean, "mean"), (rstd, "rstd")))
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dw = torch.empty(dim, dtype=wtype, device=x.device) if w is not None else None
-        db = torch.empty(dim, dtype=wtype, device=x.device) if bias else None
+        dx = torch.empty(x.shape, dtype=x.dtype, device=device)
+        dw = torch.empty(dim, dtype=wtype, device=device) if w is not None else None
+        db = torch.empty(dim, dtype=wtype, device=device) if bias else None
         ws = None
         nbytes = 0
         if dw is not None or db is not None:
             nbytes = _lib.fft_layer_norm_workspace_bytes(rows, dim, code)
-            ws = _workspace(nbytes, x.device)
+            ws = _workspace(nbytes, device)
         _check(_lib.fft_layer_norm_backward(
             dy2.data_ptr(), max(dim, dy2.stride(0)), x2.data_ptr(), max(dim, x2.stride(0)), _ptr(w),
             mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dim, _ptr(dw), _ptr(db), rows, dim,
@@ -178,7 +184,7 @@ def grad_norm(grads, stream=None):
     if not grads:
         raise ValueError("grad_norm needs at least one tensor")
     ptrs, numels, codes, device = _table(grads, "grads")
-    context, handle = _on(stream)
+    context, handle = _on(stream, device)
     with context:
         norm = torch.empty((), dtype=torch.float32, device=device)
         nbytes = _lib.fft_grad_norm_workspace_bytes(len(grads))
@@ -204,7 +210,7 @@ def clip_grad_norm(grads, max_norm: float, out=None, eps: float = 1e-6, stream=N
         outs, onumels, ocodes, odevice = _table(out, "out")
         if odevice != device or onumels != numels or ocodes != codes:
             raise ValueError("out must be like grads")
-    context, handle = _on(stream)
+    context, handle = _on(stream, device)
     with context:
         norm = torch.empty((), dtype=torch.float32, device=device)
         nbytes = _lib.fft_grad_norm_workspace_bytes(len(grads))
@@ -273,7 +279,7 @@ def delta_rule(q, k, v, g, beta, scale=None, initial_state=None, offsets=None, o
     all sequences are packed and the arrays have no batch axis.  scale:
     dk ** -0.5 by default.  States: float32 [sequences, value heads, dk, dv]."""
     batch, packed = _packing(q, offsets)
-    context, handle = _on(stream)
+    context, handle = _on(stream, _device(q))
     with context:
         q, k, v, desc, sizes, device = _delta_inputs(q, k, v, g, beta, scale, batch, packed)
         _device(q, initial_state, offsets, out)
@@ -301,7 +307,7 @@ def delta_rule_backward(do, q, k, v, g, beta, scale=None, initial_state=None, of
     of o (like v) and of the final state (None: zero); the other arguments
     as in the forward call (see fft_delta_rule_backward)."""
     batch, packed = _packing(q, offsets)
-    context, handle = _on(stream)
+    context, handle = _on(stream, _device(q))
     with context:
         q, k, v, desc, sizes, device = _delta_inputs(q, k, v, g, beta, scale, batch, packed)
         _device(q, do, initial_state, dfinal_state, offsets)
@@ -333,7 +339,7 @@ def delta_rule_step(q, k, v, g, beta, state, slots=None, scale=None, out=None, s
     updates `state` (float32 [pool, value heads, dk, dv], contiguous) in
     place.  slots: int32 [batch], the state of each sequence (negative: idle,
     o is 0); by default sequence i has state i."""
-    context, handle = _on(stream)
+    context, handle = _on(stream, _device(q))
     with context:
         q, k, v, desc, sizes, device = _delta_inputs(q, k, v, g, beta, scale, q.shape[0], False)
         _device(q, state, slots, out)
