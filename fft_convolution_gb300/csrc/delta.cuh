@@ -58,6 +58,17 @@ constexpr int kGates = 8;
 constexpr int kChunkAt = kGates * 64;  // in floats, after the tiles
 constexpr int kImageBytes = 4 * kTile + kGates * 64 * 4 + 32;
 
+// What the gradients' kernel takes from the scans, per chunk, value head and
+// 128 columns of v: the states S0 and dS (DK rows), E, F and dO (64 rows) as
+// left and right operands of products over v.  A slab is 16 columns of v, one
+// step of the tensor cores: [leading, trailing part][rows / 8][16 columns][8
+// rows] of fp16, so a thread of a scan, which owns a column, stores 16 bytes
+// and neighbouring lanes neighbouring ones.  One power of two scales a whole
+// matrix (products over v admit no scale per column); the inverses are kept.
+constexpr int kSlab = 16, kSlabs = 128 / kSlab;
+__host__ __device__ constexpr int slab_part(int rows) { return rows * kSlab * 2; }
+enum { kScaleS, kScaleE, kScaleD, kScaleF, kScaleO, kScales = 8 };
+
 // Where the chunks of packed sequences lie (device arrays of batch + 1
 // entries, both null for sequences of one length).
 struct DeltaPlan {
@@ -102,7 +113,7 @@ struct DeltaLayout {
   long long chunks;        // at most
   size_t row0, chunk0;     // packed: the sequences' first rows and chunks
   size_t kq, images;       // chunks x kheads, chunks x vheads
-  size_t back, state, dstate, e, f;  // gradients only
+  size_t back, state, dstate, e, f, o, scales;  // gradients only
   size_t bytes;
   DeltaLayout(const DeltaArgs &a, bool packed, bool grad) {
     chunks = packed ? (a.tokens + (kChunk - 1) * a.batch) / kChunk
@@ -124,6 +135,8 @@ struct DeltaLayout {
     dstate = take(grad ? chv * 128 * dk * 4 : 0);
     e = take(grad ? chv * 64 * 128 * 4 : 0);
     f = take(grad ? chv * 64 * 128 * 4 : 0);
+    o = take(grad ? chv * 64 * 128 * 2 * a.terms : 0);
+    scales = take(grad ? chv * kScales * 4 : 0);
     bytes = at;
   }
 };

@@ -24,12 +24,14 @@ namespace fftgb {
 template <typename T, int DK, bool STAGED>
 __global__ void __launch_bounds__(kScanThreads, 1)
 delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan plan, const char *kq,
-                  const char *images, float *dstates, float *rows, int *status) {
+                  const char *images, char *dstates, char *fs, char *os_, float *scales,
+                  int *status) {
   extern __shared__ char smem_raw[];
   __shared__ ScanBars bars;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int failed;
   __shared__ float2 box[2][kScanGroups][128];
+  __shared__ BlockBounds bounds;
   constexpr int NT = Terms<T>::value, ST = kScanStages;
   constexpr int kStage = scan_stage_bytes(DK, NT, STAGED);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -39,6 +41,7 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
   const ScanSpan sp = scan_span(a, plan, blockIdx.x / blocks_v / a.vheads);
   const bool packed = plan.chunk0 != nullptr;
   char *stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  if (tid < 4 * kTops) bounds.top[tid / kTops][tid % kTops] = 0;
   const uint32_t tm = scan_begin(bars, &tmem_slot, &failed, STAGED, tid, warp);
   char *ring = stages + ST * kStage + (STAGED ? kRows16 : 0);
   auto wait = [&](uint64_t *b, uint32_t parity) { return wait_or_fail(b, parity, &failed, status); };
@@ -127,7 +130,8 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
     };
     float2 S[SP][8];
     float ss = 1.0f;
-    auto put_state = [&](long long c) {
+    auto put_state = [&](int it) {
+      const long long c = chunk_of(it);
 #pragma unroll
       for (int p = 0; p < SP; ++p) {
         const int at = group * SC + p * 16;
@@ -135,15 +139,15 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
       }
       tmem_wait_st();
       warp_arrive(&bars.sb, lane);
-      const float inv = scale_inverse(ss);
-      float *dst = dstates + saved(c) * (DK * 128) + row;
+      const float xs = bounds.scale(it - 1, 1), by = scale_inverse(ss) * xs;
 #pragma unroll
-      for (int p = 0; p < SP; ++p)
+      for (int p = 0; p < SP; ++p) {
+        float2 f[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          dst[(group * SC + p * 16 + 2 * j) * 128] = S[p][j].x * inv;
-          dst[(group * SC + p * 16 + 2 * j + 1) * 128] = S[p][j].y * inv;
-        }
+        for (int j = 0; j < 8; ++j) f[j] = mul2(S[p][j], both(by));
+        put_slab<true>(dstates + saved(c) * (512 * DK), DK, 2, group * SC + p * 16, row, f, live);
+      }
+      if (tid == 0) scales[saved(c) * kScales + kScaleD] = scale_inverse(xs);
     };
     auto state_max = [&]() {
       float m = 0.0f;
@@ -174,12 +178,15 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
     bool ok = true;
     if (sp.chunks > 0) {
       fetch(0);
-      ss = bound_scale(agree.largest(state_max(), 0.0f).x);
+      const float smax = agree.largest(state_max(), 0.0f).x;
+      ss = bound_scale(smax);
+      bounds.enter(-1, 1, live ? smax : 0.0f, lane);
+      asm volatile("bar.sync 5, %0;" ::"n"(kScanWarps * 32) : "memory");
 #pragma unroll
       for (int p = 0; p < SP; ++p)
 #pragma unroll
         for (int j = 0; j < 8; ++j) S[p][j] = mul2(S[p][j], both(ss));
-      put_state(chunk_of(0));
+      put_state(0);
     }
     for (int it = 0; it < sp.chunks && ok; ++it) {
       const uint32_t ph = it & 1;
@@ -198,7 +205,10 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
       const float bw = fmaxf(by * chunk[3] * chunk[4], chunk[5] * most.y);
       const float ys = bound_scale(by), ws = bound_scale(bw);
       const float inv_y = scale_inverse(ys);
-      const float next_ss = bound_scale(fmaf(Gamma, smax, 256.0f * bw));
+      const float bs = fmaf(Gamma, smax, 256.0f * bw), next_ss = bound_scale(bs);
+      bounds.enter(it, 0, live ? by * chunk[3] : 0.0f, lane);
+      bounds.enter(it, 1, live ? bs : 0.0f, lane);
+      bounds.enter(it, 2, live ? most.y : 0.0f, lane);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = mul2(x[j], both(os));
       if constexpr (NT == 1) put_lead(lb + kColWh + group * 8, x);
@@ -223,6 +233,13 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
       warp_arrive(&bars.y, lane);
       // While F is computed: scale gamma dO, where dO was.
       take(it, x);
+      const float fscale = bounds.scale(it, 0), oscale = bounds.scale(it, 2);
+      {
+        float2 f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = mul2(x[j], both(oscale));
+        put_slab<NT == 2>(os_ + saved(c) * (64 * 128 * 2 * NT), 64, NT, group * TK, row, f, live);
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = mul2(x[j], mul2(gate(gates + 5 * 64, j), both(ws)));
       put_split(lb + kColWh + group * 8, lb + kColWl + group * 8, x);
@@ -244,14 +261,19 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
       // more, which saves registers), and dV = beta F
       tmem_ld(lb + kColP + group * TK, r);
       tmem_wait_ld();
-      float *dst = rows + saved(c) * (64 * 128) + group * TK * 128 + row;
       TokenValues<T> dv;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float2 y = mul2(pair(r, j), mul2(gate(gates + 2 * 64, j), both(inv_y)));
-        dst[2 * j * 128] = y.x;
-        dst[(2 * j + 1) * 128] = y.y;
         dv.set(j, mul2(y, gate(gates + 3 * 64, j)));
+        x[j] = mul2(y, both(fscale));
+      }
+      put_slab<true>(fs + saved(c) * (64 * 128 * 4), 64, 2, group * TK, row, x, live);
+      if (tid == 0) {
+        float *to = scales + saved(c) * kScales;
+        to[kScaleF] = scale_inverse(fscale);
+        to[kScaleO] = scale_inverse(oscale);
+        bounds.clear(it);
       }
       if (STAGED) {
         if (it > 0 && !(ok = wait(&bars.got, ph ^ 1))) break;
@@ -281,7 +303,7 @@ delta_back_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
           S[p][j] = fma2(S[p][j], both(keep), mul2(pair(r, j), both(add)));
       }
       ss = next_ss;
-      if (more) put_state(c - 1);
+      if (more) put_state(it + 1);
     }
     if (ok && ga.dinitial && live) {
       const float inv = scale_inverse(ss);

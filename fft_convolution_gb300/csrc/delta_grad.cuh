@@ -14,13 +14,22 @@
 // where k is written under its e^{-G_i}); <S1, dS> = Gamma <S0, dS> +
 // sum_j k_j . (Gamma/gamma beta dS E)_j.
 //
-// One block per chunk and value head, products transposed (dk along the lanes
-// of tensor memory, tokens along the columns): S0 and dS are left operands,
-// dO, F and E right ones, [dO; F] E^T one product of 128 rows; then K and Q
-// (MN-major) on the left, X and Z on the right.  Heads that share a key head
+// The products run transposed (dk along the lanes of tensor memory, tokens along
+// the columns).  S0, dS, E, F and dO come as the scans left them, slabs of 16
+// columns of v that are operands as they are: over a ring of slabs go
+//   S0 [dO; F]^T (128 columns: dQ's and dKr's first parts), dS E^T, [dO; F] E^T,
+// leading parts and trailing ones into accumulators of their own (the
+// accumulator cuts off below its last bit at every step: with both in one,
+// dbeta was 2.5 times as far off).  X and Z, from the last of them, become
+// right operands of the products with K and Q.  Heads that share a key head
 // leave fp32 partial sums, added by a small kernel in a fixed order.
 //
-// Reading S0, dS, E and F (192 KB for 128 x 128 heads) bounds it.
+// One block per SM walks over chunks and value heads: 16 warps turn
+// accumulators into X, Z and the results; one thread issues the products; a
+// warp copies slabs ahead, so that the next chunk's arrive while this one's
+// results are written; two take <S0, dS> from the slabs.
+//
+// Reading S0, dS, E, F and dO (208 KB for 128 x 128 heads of 16 bits) bounds it.
 #pragma once
 
 #include "delta_prep.cuh"
@@ -28,86 +37,60 @@
 
 namespace fftgb {
 
-constexpr int kGradThreads = 512;
-// S0 / dS (two parts), later X and Z; [dO; F] (two parts), later K and Q; E.
-constexpr int kGradA = 4 * 128 * 128, kGradB = 8 * kTile, kGradC = 4 * kTile;
-constexpr size_t grad_smem() { return 1024 + kGradA + kGradB + kGradC; }
+constexpr int kGradWarps = 16, kGradThreads = (kGradWarps + 4) * 32;
+// A slab: S0, dS and E (two parts each), [dO; F] leading, [dO; F] trailing.
+__host__ __device__ constexpr int slab_e(int dk) { return 4 * slab_part(dk); }
+__host__ __device__ constexpr int slab_of(int dk) { return slab_e(dk) + 2 * slab_part(64); }
+__host__ __device__ constexpr int slab_bytes(int dk) { return slab_of(dk) + 2 * slab_part(128); }
+__host__ __device__ constexpr int grad_slabs(int terms) { return terms == 1 ? 4 : 3; }
+// K and Q; X and Z (two tiles of two parts each); the ring.
+__host__ __device__ constexpr size_t grad_smem(int dk, int terms) {
+  return 1024 + kq_bytes(dk, terms) + 8 * kTile + (size_t)grad_slabs(terms) * slab_bytes(dk);
+}
 
+struct GradTokens {
+  float2 G[64];
+  float beta[64], gam[64], dec[64], ek[64], eq[64];
+  unsigned most[3];  // largest X1, Z1, and X2 or Z2
+};
 struct GradShared {
-  uint64_t mma, kq;
+  uint64_t full[4], empty[4];       // slabs
+  uint64_t kq, kq_free;             // K and Q there; read
+  uint64_t first, tiles, second;    // products over v done; X and Z there; their products done
+  uint64_t read;                    // accumulators read
+  uint64_t inner, done;
   uint32_t tmem_slot;
   int failed;
-  float2 G[64];
-  double carry;
-  float beta[64], gam[64], dec[64], ek[64], eq[64];
-  // inverse scales of the rows of S0, dS, [dO; F] and E
-  float s0[128], ds[128], of[128], e[64];
-  unsigned most[4];       // largest X1, Z1, and X2 or Z2
+  GradTokens tok[2];                // of this chunk and the next
+  float inner_part[2][2];           // <S0, dS>
   float dots[4][64];
-  float part[2][16];
+  float k_w[kGradWarps];
 };
 
-// Rows of 128 columns, four per lane: the largest value of a row, over all
-// blocks of columns when there are several.
-__device__ __forceinline__ float4 load4(const float *p, int col, int dv, bool there) {
-  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (there) x = *reinterpret_cast<const float4 *>(p);
-  if (col + 3 >= dv) {
-    if (col >= dv) x.x = 0.0f;
-    if (col + 1 >= dv) x.y = 0.0f;
-    if (col + 2 >= dv) x.z = 0.0f;
-    x.w = 0.0f;
-  }
-  return x;
-}
-template <typename T>
-__device__ __forceinline__ float4 load4(const T *p, int left, bool vec, bool there) {
-  float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (there) {
-    if (vec && left >= 4) {
-      T t[4];
-      if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(t) = *reinterpret_cast<const uint4 *>(p);
-      else *reinterpret_cast<uint2 *>(t) = *reinterpret_cast<const uint2 *>(p);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = to_acc(t[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < left) f[i] = to_acc(p[i]);
-    }
-  }
-  return make_float4(f[0], f[1], f[2], f[3]);
-}
-__device__ __forceinline__ float max4(float4 x) {
-  return fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
-}
-// A lane's four values of row r to the two parts of the tiles.
-__device__ __forceinline__ void put4(char *hi_tiles, int lo_at, int tile, int r, int lane, float4 x,
-                                     float s) {
-  uint2 hi, lo;
-  split2(mul2(make_float2(x.x, x.y), both(s)), hi.x, lo.x);
-  split2(mul2(make_float2(x.z, x.w), both(s)), hi.y, lo.y);
-  const int at = piece_at(r, lane >> 1, tile) + (lane & 1) * 8;
-  *reinterpret_cast<uint2 *>(hi_tiles + at) = hi;
-  *reinterpret_cast<uint2 *>(hi_tiles + lo_at + at) = lo;
+// A barrier of the 16 warps: whether `p` holds in all of their threads.
+__device__ __forceinline__ bool grad_all(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)p), "n"(kGradWarps * 32)
+      : "memory");
+  return r != 0;
 }
 
-// A (shared, 128 rows, `ablock` bytes between tiles of 64 columns, trailing
-// parts `alo` bytes on) times B (64 rows) over 128 columns.
-__device__ __forceinline__ void mma_cols(uint32_t d, uint32_t a, uint32_t ablock, uint32_t alo,
-                                         uint32_t b, uint32_t bblock, uint32_t blo, bool b_exact,
-                                         bool accumulate) {
-  constexpr uint32_t idesc = mma_desc(128, 64, false, false);
-#pragma unroll
-  for (int term = 2; term >= 0; --term) {  // trailing parts first (delta_scan.cuh)
-    if (term == 2 && b_exact) continue;
-    const uint32_t ta = a + (term == 1 ? alo : 0), tb = b + (term == 2 ? blo : 0);
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      mma_ss(d, tile_desc(ta + (k >> 2) * ablock + (k & 3) * 32, 16),
-             tile_desc(tb + (k >> 2) * bblock + (k & 3) * 32, 16), idesc,
-             accumulate || term < (b_exact ? 1 : 2) || k > 0);
-  }
+// Between a warp's reads of shared memory and the arrival that lets a bulk copy
+// overwrite it: without the fence the arrival overtook loads under way (<S0, dS>
+// then summed values of the next slab, in 1 to 100% of calls).
+__device__ __forceinline__ void read_before_copy() {
+  __threadfence_block();
+  fence_smem_to_async();
+}
+
+// D (128 lanes x N) (+)= A B^T over one slab.
+template <int N>
+__device__ __forceinline__ void mma_slab(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
+  mma_ss_plain(d, a, b, mma_desc(128, N, true, true), accumulate);
 }
 // K^T or Q^T (MN-major, 64 tokens) times a 64 x 64 matrix in two parts,
 // K-major (rows = columns of the result) or MN-major (B_MN).
@@ -126,8 +109,10 @@ __device__ __forceinline__ void mma_tokens(uint32_t d, uint32_t a, uint32_t b, b
   }
 }
 
-constexpr uint32_t kColQ1 = 0, kColR1 = 64, kColW1 = 128, kColG = 192, kColQ2 = 256, kColR2 = 320,
-                   kColW2 = 384;
+// Columns of tensor memory: leading and trailing accumulators of S0 [dO; F]^T,
+// dS E^T and [dO; F] E^T; later, in place of the last two, the products with K
+// and Q.
+constexpr uint32_t kAccQ = 0, kAccQt = 128, kAccW = 256, kAccWt = 320, kAccG = 384, kAccGt = 448;
 
 // Sums of 16 values per lane over the warp: lane l gets that of value l >> 1.
 __device__ __forceinline__ float warp_sums(float (&v)[16], int lane) {
@@ -144,392 +129,394 @@ __device__ __forceinline__ float warp_sums(float (&v)[16], int lane) {
 }
 
 // PARTIAL: dq and dk of this value head go to `partial` (fp32 [2][64][DK] in
-// place of the block's E and F), else to their arrays.
+// place of the chunk's E and F, which only this block reads), else to their arrays.
 template <typename T, int DK, bool PARTIAL>
 __global__ void __launch_bounds__(kGradThreads, 1)
 delta_grad_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan plan, const char *kq,
-                  const char *back, const float *states, const float *dstates, float *es,
-                  float *fs, int *status) {
+                  const char *back, const char *states, const char *dstates, char *es, char *fs,
+                  const char *os, const float *scales, int *status) {
   extern __shared__ char smem_raw[];
   __shared__ GradShared sh;
-  constexpr int NT = Terms<T>::value;
+  constexpr int NT = Terms<T>::value, R = grad_slabs(NT), kSlabBytes = slab_bytes(DK);
+  constexpr int kE = slab_e(DK), kOF = slab_of(DK), kPart = slab_part(64);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int h = blockIdx.x % a.vheads, hk = h / (a.vheads / a.kheads);
-  const long long ci = blockIdx.x / a.vheads;
-  DeltaChunk c;
-  if (!delta_chunk(a, plan, ci, c)) return;
   char *ra = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  char *rb = ra + kGradA, *rc = rb + kGradB;
+  char *rb = ra + 8 * kTile, *ring = rb + kq_bytes(DK, NT);
   const int blocks_v = (a.dv + 127) / 128;
-  const long long slot = (ci * a.vheads + h) * blocks_v;
   const bool packed = plan.chunk0 != nullptr;
+  const long long items = (packed ? (long long)plan.chunk0[a.batch] : plan.chunks_max) * a.vheads;
   volatile int *failed = &sh.failed;
+  auto wait = [&](uint64_t *b, uint32_t parity) { return wait_or_fail(b, parity, failed, status); };
 
-  if (warp == 0) tmem_alloc(&sh.tmem_slot, 512);
+  if (warp == kGradWarps) tmem_alloc(&sh.tmem_slot, 512);
   if (tid == 0) {
-    bar_init(&sh.mma, 1);
-    bar_init(&sh.kq, 1);
+    for (int s = 0; s < R; ++s) {
+      bar_init(&sh.full[s], 1);
+      bar_init(&sh.empty[s], 3);
+    }
+    for (uint64_t *b : {&sh.kq, &sh.first, &sh.second, &sh.done}) bar_init(b, 1);
+    for (uint64_t *b : {&sh.kq_free, &sh.tiles, &sh.read}) bar_init(b, kGradWarps);
+    bar_init(&sh.inner, 2);
     sh.failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (tid < 4) sh.most[tid] = 0;
-  if (tid < 128) sh.s0[tid] = sh.ds[tid] = sh.of[tid] = 0.0f;
-  if (tid < 64) sh.e[tid] = 0.0f;
-  {
-    const float *gates = reinterpret_cast<const float *>(
-        back + (ci * a.vheads + h) * (long long)kImageBytes + 4 * kTile);
-    if (tid < 64) {
-      sh.beta[tid] = gates[3 * 64 + tid];
-      sh.ek[tid] = gates[6 * 64 + tid];
-      sh.eq[tid] = gates[7 * 64 + tid];
-    }
+  if (NT == 1) {  // one value holds dO: its trailing part stays 0
+    for (int i = tid; i < R * (kPart / 16); i += kGradThreads)
+      *reinterpret_cast<uint4 *>(ring + (i / (kPart / 16)) * kSlabBytes + kOF + 2 * kPart +
+                                 (i % (kPart / 16)) * 16) = make_uint4(0, 0, 0, 0);
+    fence_smem_to_async();
   }
-  running_decay(a.g + c.b * a.sg.seq + c.row * a.sg.tok + h * a.sg.head, a.sg.tok, c.n, tid,
-                &sh.carry, sh.G);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = __shfl_sync(0xffffffffu, sh.tmem_slot, 0);
-  if (tid < 64) {
-    sh.gam[tid] = decay_between(sh.G[tid], make_float2(0.0f, 0.0f));
-    sh.dec[tid] = decay_between(sh.G[63], sh.G[tid]);
-  }
-  const long long orow = out_row(a, c.b, c.row, packed, h), ostep = (long long)a.vheads * a.dv;
-  const bool ovec = a.dv % 4 == 0 && ((uintptr_t)ga.dout & 15u) == 0;
-  const int col = lane * 4;
-  // A warp takes whole rows: its lanes' four values of the row.
-  auto row_s = [&](const float *p, int vb, int r) {
-    return load4(p + (slot + vb) * (DK * 128) + r * 128 + col, vb * 128 + col, a.dv, true);
-  };
-  auto row_e = [&](const float *p, int vb, int r) {
-    return load4(p + (slot + vb) * (64 * 128) + r * 128 + col, vb * 128 + col, a.dv, r < c.n);
-  };
-  auto row_o = [&](int vb, int r) {
-    const int left = a.dv - vb * 128 - col;
-    return load4<T>(static_cast<const T *>(ga.dout) + orow + r * ostep + vb * 128 + col, left, ovec,
-                    r < c.n && left > 0);
-  };
-  // Several blocks of columns: the rows' largest values over all of them first.
-  if (blocks_v > 1) {
-    for (int vb = 0; vb < blocks_v; ++vb) {
-      for (int r = warp; r < DK; r += 16) {
-        const float m = lane_max<32>(max4(row_s(states, vb, r)));
-        const float n = lane_max<32>(max4(row_s(dstates, vb, r)));
-        if (lane == 0) {
-          sh.s0[r] = fmaxf(sh.s0[r], m);
-          sh.ds[r] = fmaxf(sh.ds[r], n);
+
+  if (warp == kGradWarps + 1) {
+    // Copies: K and Q after the first slabs, since they wait for the chunk before.
+    if (elect_one()) {
+      long long n = 0, kqs = 0;
+      bool ok = true;
+      for (long long i = blockIdx.x; i < items && ok; i += gridDim.x) {
+        const long long ci = i / a.vheads;
+        const int h = (int)(i % a.vheads), hk = h / (a.vheads / a.kheads);
+        for (int k = 0; k < blocks_v * kSlabs && ok; ++k, ++n) {
+          if (k == R) {
+            if (!(ok = kqs == 0 || wait(&sh.kq_free, (kqs - 1) & 1))) break;
+            bar_arrive_tx(&sh.kq, kq_bytes(DK, NT));
+            bulk_load(rb, kq + (ci * a.kheads + hk) * (long long)kq_bytes(DK, NT),
+                      kq_bytes(DK, NT), &sh.kq);
+            ++kqs;
+          }
+          const int s = (int)(n % R);
+          if (!(ok = n < R || wait(&sh.empty[s], (n / R - 1) & 1))) break;
+          const long long slot = i * blocks_v + (k >> 3);
+          const int sl = k & 7;
+          char *dst = ring + s * kSlabBytes;
+          uint64_t *bar = &sh.full[s];
+          bar_arrive_tx(bar, 4 * slab_part(DK) + 4 * kPart + NT * kPart);
+          bulk_load(dst, states + slot * (512 * DK) + sl * 2 * slab_part(DK), 2 * slab_part(DK), bar);
+          bulk_load(dst + 2 * slab_part(DK), dstates + slot * (512 * DK) + sl * 2 * slab_part(DK),
+                    2 * slab_part(DK), bar);
+          bulk_load(dst + kE, es + slot * (kSlabs * 2 * kPart) + sl * 2 * kPart, 2 * kPart, bar);
+          const char *f = fs + slot * (kSlabs * 2 * kPart) + sl * 2 * kPart;
+          const char *o = os + (slot * kSlabs + sl) * (NT * kPart);
+          bulk_load(dst + kOF, o, kPart, bar);
+          bulk_load(dst + kOF + kPart, f, kPart, bar);
+          if (NT == 2) bulk_load(dst + kOF + 2 * kPart, o + kPart, kPart, bar);
+          bulk_load(dst + kOF + 3 * kPart, f + kPart, kPart, bar);
         }
       }
-      for (int r = warp; r < 64; r += 16) {
-        const float m = lane_max<32>(max4(row_o(vb, r))), n = lane_max<32>(max4(row_e(fs, vb, r)));
-        const float e = lane_max<32>(max4(row_e(es, vb, r)));
-        if (lane == 0) {
-          sh.of[r] = fmaxf(sh.of[r], m);
-          sh.of[64 + r] = fmaxf(sh.of[64 + r], n);
-          sh.e[r] = fmaxf(sh.e[r], e);
+      if (*failed) {  // given up: no copy may land after the block has gone
+        for (long long k = n > R ? n - R : 0; k < n; ++k) bar_wait(&sh.full[k % R], (k / R) & 1);
+        if (kqs > 0) bar_wait(&sh.kq, (kqs - 1) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kGradWarps) {
+    long long n = 0, phases = 0;
+    uint32_t item = 0;
+    bool ok = true;
+    const uint32_t sa = smem_u32(ra), sb = smem_u32(rb), slabs = smem_u32(ring);
+    for (long long i = blockIdx.x; i < items && ok; i += gridDim.x, ++item) {
+      for (int vb = 0; vb < blocks_v && ok; ++vb, ++phases) {
+        if (!(ok = phases == 0 || wait(&sh.read, (phases - 1) & 1))) break;
+        for (int k = 0; k < kSlabs; ++k, ++n) {
+          const int s = (int)(n % R);
+          if (!(ok = wait(&sh.full[s], (n / R) & 1))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t S = slabs + s * kSlabBytes, D = S + 2 * slab_part(DK), E = S + kE,
+                           OF = S + kOF;
+            mma_slab<128>(tm + kAccQt, S + slab_part(DK), OF, k > 0);
+            if (NT == 2) mma_slab<128>(tm + kAccQt, S, OF + 2 * kPart, true);
+            else mma_slab<64>(tm + kAccQt + 64, S, OF + 3 * kPart, true);
+            mma_slab<128>(tm + kAccQ, S, OF, k > 0);
+            mma_slab<64>(tm + kAccWt, D + slab_part(DK), E, k > 0);
+            mma_slab<64>(tm + kAccWt, D, E + kPart, true);
+            mma_slab<64>(tm + kAccW, D, E, k > 0);
+            mma_slab<64>(tm + kAccGt, OF + 2 * kPart, E, k > 0);
+            mma_slab<64>(tm + kAccGt, OF, E + kPart, true);
+            mma_slab<64>(tm + kAccG, OF, E, k > 0);
+            mma_commit(&sh.empty[s]);
+            if (k == kSlabs - 1) mma_commit(&sh.first);
+          }
+          __syncwarp();
         }
       }
-    }
-    __syncthreads();
-    if (tid < 128) {
-      sh.s0[tid] = scale_inverse(row_scale(sh.s0[tid]));
-      sh.ds[tid] = scale_inverse(row_scale(sh.ds[tid]));
-      sh.of[tid] = scale_inverse(row_scale(sh.of[tid]));
-    }
-    if (tid < 64) sh.e[tid] = scale_inverse(row_scale(sh.e[tid]));
-    __syncthreads();
-  }
-  auto scale_of = [&](float4 x, float *inv) {
-    if (blocks_v > 1) return scale_inverse(*inv);
-    const float s = row_scale(lane_max<32>(max4(x)));
-    __syncwarp();
-    if (lane == 0) *inv = scale_inverse(s);
-    return s;
-  };
-  const uint32_t sa = smem_u32(ra), sb = smem_u32(rb), sc = smem_u32(rc);
-  uint32_t ph = 0;
-  bool ok = true;
-  float inner = 0.0f;  // <S0, dS>
-  for (int vb = 0; vb < blocks_v && ok; ++vb) {
-    constexpr int RS = DK / 16, RT = 4;  // rows of a warp
-    {
-      float4 x[RS];
-#pragma unroll
-      for (int k = 0; k < RS; ++k) x[k] = row_s(states, vb, warp + 16 * k);
-#pragma unroll
-      for (int k = 0; k < RS; ++k) {
-        const int r = warp + 16 * k;
-        put4(ra, 2 * 128 * 128, 128 * 128, r, lane, x[k], scale_of(x[k], &sh.s0[r]));
+      ok = ok && wait(&sh.tiles, item & 1) && wait(&sh.kq, item & 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_tokens<DK, NT, false>(tm + kAccG, sb, sa, false);
+        mma_tokens<DK, NT, false>(tm + kAccGt, sb, sa + 4 * kTile, false);
+        mma_tokens<DK, NT, true>(tm + kAccW, sb + kTile, sa + 2 * kTile, false);
+        mma_tokens<DK, NT, true>(tm + kAccW, sb, sa + 6 * kTile, true);
+        mma_commit(&sh.second);
       }
+      __syncwarp();
     }
-    {
-      float4 x[RT], y[RT], z[RT];
-#pragma unroll
-      for (int k = 0; k < RT; ++k) {
-        const int r = warp + 16 * k;
-        x[k] = row_o(vb, r);
-        y[k] = row_e(fs, vb, r);
-        z[k] = row_e(es, vb, r);
-      }
-#pragma unroll
-      for (int k = 0; k < RT; ++k) {
-        const int r = warp + 16 * k;
-        put4(rb, 4 * kTile, 2 * kTile, r, lane, x[k], scale_of(x[k], &sh.of[r]));
-        put4(rb, 4 * kTile, 2 * kTile, 64 + r, lane, y[k], scale_of(y[k], &sh.of[64 + r]));
-        put4(rc, 2 * kTile, kTile, r, lane, z[k], scale_of(z[k], &sh.e[r]));
-      }
-    }
-    fence_smem_to_async();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 0 && elect_one()) {
-      constexpr uint32_t lo_a = 2 * 128 * 128, lo_b = 4 * kTile;
-      mma_cols(tm + kColQ1, sa, 128 * 128, lo_a, sb, 2 * kTile, lo_b, NT == 1, vb > 0);
-      mma_cols(tm + kColR1, sa, 128 * 128, lo_a, sb + kTile, 2 * kTile, lo_b, false, vb > 0);
-      mma_cols(tm + kColG, sb, 2 * kTile, lo_b, sc, kTile, 2 * kTile, false, vb > 0);
-      mma_commit(&sh.mma);
+    if (elect_one()) {
+      mma_commit(&sh.done);
+      bar_wait(&sh.done, 0);
     }
     __syncwarp();
-    {
-      float4 x[RS];
+  } else if (warp > kGradWarps) {
+    // <S0, dS>, half of every slab's pieces of eight values each
+    const int which = warp - kGradWarps - 2, piece = which * 32 + lane;
+    long long n = 0;
+    uint32_t item = 0;
+    bool ok = true;
+    for (long long i = blockIdx.x; i < items && ok; i += gridDim.x, ++item) {
+      float inner = 0.0f;
+      for (int vb = 0; vb < blocks_v && ok; ++vb) {
+        const float *sc = scales + (i * blocks_v + vb) * kScales;
+        const float is = sc[kScaleS], ids = sc[kScaleD];
+        float sum = 0.0f;
+        for (int k = 0; k < kSlabs; ++k, ++n) {
+          const int s = (int)(n % R);
+          if (!(ok = wait(&sh.full[s], (n / R) & 1))) break;
+          const char *S = ring + s * kSlabBytes + piece * 16, *D = S + 2 * slab_part(DK);
 #pragma unroll
-      for (int k = 0; k < RS; ++k) x[k] = row_s(dstates, vb, warp + 16 * k);
-      ok = wait_or_fail(&sh.mma, ph, failed, status);
-      ph ^= 1;
+          for (int j = 0; j < slab_part(DK) / (64 * 16); ++j) {
+            const uint4 sh4 = *reinterpret_cast<const uint4 *>(S + j * 1024);
+            const uint4 sl4 = *reinterpret_cast<const uint4 *>(S + j * 1024 + slab_part(DK));
+            const uint4 dh4 = *reinterpret_cast<const uint4 *>(D + j * 1024);
+            const uint4 dl4 = *reinterpret_cast<const uint4 *>(D + j * 1024 + slab_part(DK));
+            auto both_parts = [](uint32_t h, uint32_t l) {
+              const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+              const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&l));
+              return make_float2(x.x + y.x, x.y + y.y);
+            };
+            auto add = [&](uint32_t h, uint32_t l, uint32_t dh, uint32_t dl) {
+              const float2 x = both_parts(h, l), y = both_parts(dh, dl);
+              sum = fmaf(x.x, y.x, fmaf(x.y, y.y, sum));
+            };
+            add(sh4.x, sl4.x, dh4.x, dl4.x);
+            add(sh4.y, sl4.y, dh4.y, dl4.y);
+            add(sh4.z, sl4.z, dh4.z, dl4.z);
+            add(sh4.w, sl4.w, dh4.w, dl4.w);
+          }
+          read_before_copy();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&sh.empty[s]);
+        }
+        inner = fmaf(sum * is, ids, inner);
+      }
 #pragma unroll
-      for (int k = 0; k < RS; ++k) {
-        // <S0, dS>: S0 from its two parts, before they are overwritten
-        const int r = warp + 16 * k;
-        const int at = piece_at(r, lane >> 1, 128 * 128) + (lane & 1) * 8;
-        const uint2 hi = *reinterpret_cast<const uint2 *>(ra + at);
-        const uint2 lo = *reinterpret_cast<const uint2 *>(ra + 2 * 128 * 128 + at);
-        auto two = [](uint32_t x) { return __half22float2(*reinterpret_cast<const __half2 *>(&x)); };
-        const float2 h0 = two(hi.x), h1 = two(hi.y), l0 = two(lo.x), l1 = two(lo.y);
-        inner += sh.s0[r] * ((h0.x + l0.x) * x[k].x + (h0.y + l0.y) * x[k].y +
-                             (h1.x + l1.x) * x[k].z + (h1.y + l1.y) * x[k].w);
-        put4(ra, 2 * 128 * 128, 128 * 128, r, lane, x[k], scale_of(x[k], &sh.ds[r]));
+      for (int o = 16; o > 0; o >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, o);
+      if (lane == 0) {
+        sh.inner_part[item & 1][which] = inner;
+        bar_arrive(&sh.inner);
       }
     }
-    fence_smem_to_async();
-    tc_fence_before();
-    ok = __syncthreads_and(ok);
-    tc_fence_after();
-    if (ok && warp == 0 && elect_one()) {
-      mma_cols(tm + kColW1, sa, 128 * 128, 2 * 128 * 128, sc, kTile, 2 * kTile, false, vb > 0);
-      mma_commit(&sh.mma);
-    }
-    // K and Q, where [dO; F] was
-    if ((vb + 1 == blocks_v || !ok) && warp == 0 && elect_one()) {
-      bar_arrive_tx(&sh.kq, kq_bytes(DK, NT));
-      bulk_load(rb, kq + (ci * a.kheads + hk) * (long long)kq_bytes(DK, NT), kq_bytes(DK, NT),
-                &sh.kq);
-    }
-    __syncwarp();
-    ok = ok && wait_or_fail(&sh.mma, ph, failed, status);
-    ph ^= 1;
-    ok = __syncthreads_and(ok);
-  }
-  if (!ok && tid == 0) bar_wait(&sh.kq, 0);  // given up: no copy may land after the block has gone
-  const int quarter = warp & 3, group = warp >> 2, lrow = quarter * 32 + lane;
-  const uint32_t lb = tm + ((uint32_t)(quarter * 32) << 16) + group * 16;
-  if (ok) {
-    tc_fence_after();
-    // X (rows 0 .. 63) and Z (64 .. 127) of [dO; F] E^T: this thread's row and 16
-    // columns, each twice: times 2^ek_j for the products summed over j, times
-    // 2^eq_i or 2^ek_i for those summed over i.
-    const int i = lrow & 63;
-    const bool is_z = lrow >= 64;
-    uint32_t r[16];
-    tmem_ld(lb + kColG, r);
-    tmem_wait_ld();
-    float x1[16], x2[16], m1 = 0.0f, m2 = 0.0f;
-    const float inv = sh.of[lrow], bi = sh.beta[i], over = is_z ? sh.ek[i] : sh.eq[i];
-    const float2 gi = sh.G[i];
+  } else {
+    const int quarter = warp & 3, group = warp >> 2, lrow = quarter * 32 + lane;
+    const uint32_t lb = tm + ((uint32_t)(quarter * 32) << 16) + group * 16;
+    const int i = lrow & 63;         // of [dO; F] E^T: token
+    const bool is_z = lrow >= 64, live = lrow < a.dk;
+    uint32_t item = 0, phases = 0;
+    bool ok = true;
+    for (long long it = blockIdx.x; it < items; it += gridDim.x, ++item) {
+      const long long ci = it / a.vheads, slot = it * blocks_v;
+      const int h = (int)(it % a.vheads), hk = h / (a.vheads / a.kheads);
+      DeltaChunk c;
+      delta_chunk(a, plan, ci, c);
+      GradTokens &tk = sh.tok[item & 1];
+      if (warp == 0) {
+        running_decay_warp(a.g + c.b * a.sg.seq + c.row * a.sg.tok + h * a.sg.head, a.sg.tok, c.n,
+                           lane, tk.G);
+        __syncwarp();
+        const float2 end = tk.G[63];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int j = group * 16 + k;
-      const float g = __uint_as_float(r[k]) * inv * sh.e[j];
-      if (is_z && j == i && i < c.n)
-        ga.dbeta[(packed ? c.row + i : c.b * a.tokens + c.row + i) * a.vheads + h] = g;
-      float x = 0.0f;
-      if (is_z ? j < i : j <= i)
-        x = decay_between(gi, sh.G[j]) * sh.beta[j] * g * (is_z ? -bi : a.scale);
-      x1[k] = x * sh.ek[j];
-      x2[k] = x * over;
-      m1 = fmaxf(m1, fabsf(x1[k]));
-      m2 = fmaxf(m2, fabsf(x2[k]));
-    }
-    m1 = lane_max<32>(m1);
-    m2 = lane_max<32>(m2);
-    if (lane == 0) {  // (of values that are not negative the bits are in order)
-      atomicMax(&sh.most[is_z ? 1 : 0], __float_as_uint(m1));
-      atomicMax(&sh.most[2], __float_as_uint(m2));
-    }
-    __syncthreads();
-    const float s1 = bound_scale(__uint_as_float(sh.most[is_z ? 1 : 0]));
-    const float s2 = bound_scale(__uint_as_float(sh.most[2]));
-    // Tiles in place of dS: X1, X2, Z1, Z2, two parts each.
-    char *tiles = ra + (is_z ? 4 * kTile : 0);
+        for (int t = lane; t < 64; t += 32) {
+          tk.gam[t] = decay_between(tk.G[t], make_float2(0.0f, 0.0f));
+          tk.dec[t] = decay_between(end, tk.G[t]);
+        }
+      } else if (warp == 1) {
+        const float *gates = reinterpret_cast<const float *>(
+            back + (ci * a.vheads + h) * (long long)kImageBytes + 4 * kTile);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      float f[8], g[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        f[k] = x1[8 * p + k];
-        g[k] = x2[8 * p + k];
+        for (int t = lane; t < 64; t += 32) {
+          tk.beta[t] = gates[3 * 64 + t];
+          tk.ek[t] = gates[6 * 64 + t];
+          tk.eq[t] = gates[7 * 64 + t];
+        }
+        if (lane < 3) tk.most[lane] = 0;
       }
-      uint4 hi, lo;
-      const int at = piece_at(i, group * 2 + p, 0);
-      split8(f, s1, hi, lo);
-      *reinterpret_cast<uint4 *>(tiles + at) = hi;
-      *reinterpret_cast<uint4 *>(tiles + kTile + at) = lo;
-      split8(g, s2, hi, lo);
-      *reinterpret_cast<uint4 *>(tiles + 2 * kTile + at) = hi;
-      *reinterpret_cast<uint4 *>(tiles + 3 * kTile + at) = lo;
-    }
-    fence_smem_to_async();
-    ok = wait_or_fail(&sh.kq, 0, failed, status);
-    tc_fence_before();
-    ok = __syncthreads_and(ok);
-    tc_fence_after();
-  }
-  if (ok) {
-    if (warp == 0 && elect_one()) {
-      mma_tokens<DK, NT, false>(tm + kColQ2, sb, sa, false);
-      mma_tokens<DK, NT, false>(tm + kColR2, sb, sa + 4 * kTile, false);
-      mma_tokens<DK, NT, true>(tm + kColW2, sb + kTile, sa + 2 * kTile, false);
-      mma_tokens<DK, NT, true>(tm + kColW2, sb, sa + 6 * kTile, true);
-      mma_commit(&sh.mma);
-    }
-    __syncwarp();
-    ok = wait_or_fail(&sh.mma, ph, failed, status);
-  }
-  if (__syncthreads_and(ok)) {
-    tc_fence_after();
-    const float ix = scale_inverse(bound_scale(__uint_as_float(sh.most[0])));
-    const float iz = scale_inverse(bound_scale(__uint_as_float(sh.most[1])));
-    const float iw = scale_inverse(bound_scale(__uint_as_float(sh.most[2])));
-    // Row lrow of dk (columns of K), 16 tokens.
-    const bool live = lrow < a.dk;
-    const float is = lrow < DK ? sh.s0[lrow] : 0.0f, ids = lrow < DK ? sh.ds[lrow] : 0.0f;
-    uint32_t r[16];
-    float dot[16], w[16], out[16];
-    float k_w = 0.0f;  // sum_j k_j . (Gamma/gamma beta dS E)_j
-    auto element = [&](int tok, int which) {  // of K (0) or Q (1)
-      const char *p = rb + which * kTile + (lrow >> 6) * 2 * kTile + tok * 128 +
-                      ((((lrow >> 3) & 7) ^ (tok & 7)) << 4) + (lrow & 7) * 2;
-      float x = __half2float(*reinterpret_cast<const __half *>(p));
-      if constexpr (NT == 2)
-        x += __half2float(*reinterpret_cast<const __half *>(p + 2 * (DK / 64) * kTile));
-      return live ? x * (which ? sh.eq[tok] : sh.ek[tok]) : 0.0f;
-    };
-    auto put = [&](void *dst, int which, const float (&v)[16]) {
-      if (!live) return;
-      if constexpr (PARTIAL) {
-        float *p = (which ? fs : es) + slot * (64 * 128) + lrow;
+      // The products over v
+      float q1[16], r1[16], w1[16], gx[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) p[(group * 16 + k) * DK] = v[k];
-      } else {
-        const long long row = packed ? c.row : c.b * a.tokens + c.row;
-        T *p = static_cast<T *>(dst) + (row * a.kheads + hk) * a.dk + lrow;
+      for (int k = 0; k < 16; ++k) q1[k] = r1[k] = w1[k] = gx[k] = 0.0f;
+      for (int vb = 0; vb < blocks_v; ++vb, ++phases) {
+        const float *sc = scales + (slot + vb) * kScales;
+        const float is = sc[kScaleS], ie = sc[kScaleE], ids = sc[kScaleD], jf = sc[kScaleF],
+                    jo = sc[kScaleO];
+        ok = ok && wait(&sh.first, phases & 1);
+        tc_fence_after();
+        uint32_t r[16], t[16];
+        auto take = [&](uint32_t lead, uint32_t trail, float x, float y, float (&to)[16]) {
+          tmem_ld(lb + lead, r);
+          tmem_ld(lb + trail, t);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            to[k] = fmaf((__uint_as_float(r[k]) + __uint_as_float(t[k])) * x, y, to[k]);
+        };
+        take(kAccG, kAccGt, is_z ? jf : jo, ie, gx);
+        take(kAccQ, kAccQt, is, jo, q1);
+        take(kAccQ + 64, kAccQt + 64, is, jf, r1);
+        take(kAccW, kAccWt, ids, ie, w1);
+        if (vb + 1 < blocks_v) warp_arrive(&sh.read, lane);
+      }
+      ok = grad_all(ok);
+      if (!ok) break;
+      // X (rows 0 .. 63) and Z (64 .. 127) of [dO; F] E^T: this thread's row and 16
+      // columns, each twice: times 2^ek_j for the products summed over j, times
+      // 2^eq_i or 2^ek_i for those summed over i.
+      {
+        float m1 = 0.0f, m2 = 0.0f;
+        const float bi = is_z ? -tk.beta[i] : a.scale, over = is_z ? tk.ek[i] : tk.eq[i];
+        const float2 gi = tk.G[i];
+        const int last = i < c.n ? is_z ? i - 1 : i : -1;
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const int t = group * 16 + k;
-          if (t < c.n) p[(long long)t * a.kheads * a.dk] = from_acc<T>(v[k]);
+          const int j = group * 16 + k;
+          if (is_z && j == i && i < c.n)
+            ga.dbeta[(packed ? c.row + i : c.b * a.tokens + c.row + i) * a.vheads + h] = gx[k];
+          gx[k] = j <= last ? decay_between(gi, tk.G[j]) * tk.beta[j] * gx[k] * bi : 0.0f;
+          m1 = fmaxf(m1, fabsf(gx[k] * tk.ek[j]));
+          m2 = fmaxf(m2, fabsf(gx[k]));
         }
+        m1 = lane_max<32>(m1);
+        m2 = lane_max<32>(m2 * over);
+        if (lane == 0) {  // (of values that are not negative the bits are in order)
+          atomicMax(&tk.most[is_z ? 1 : 0], __float_as_uint(m1));
+          atomicMax(&tk.most[2], __float_as_uint(m2));
+        }
+        grad_all(true);
+        const float s1 = bound_scale(__uint_as_float(tk.most[is_z ? 1 : 0]));
+        const float s2 = bound_scale(__uint_as_float(tk.most[2])) * over;
+        char *tiles = ra + (is_z ? 4 * kTile : 0);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          float f[8], g[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            g[k] = gx[8 * p + k];
+            f[k] = g[k] * tk.ek[group * 16 + 8 * p + k];
+          }
+          uint4 hi, lo;
+          const int at = piece_at(i, group * 2 + p, 0);
+          split8(f, s1, hi, lo);
+          *reinterpret_cast<uint4 *>(tiles + at) = hi;
+          *reinterpret_cast<uint4 *>(tiles + kTile + at) = lo;
+          split8(g, s2, hi, lo);
+          *reinterpret_cast<uint4 *>(tiles + 2 * kTile + at) = hi;
+          *reinterpret_cast<uint4 *>(tiles + 3 * kTile + at) = lo;
+        }
+        fence_smem_to_async();
+        warp_arrive(&sh.tiles, lane);
       }
-    };
-    // dQ
-    tmem_ld(lb + kColQ1, r);
-    tmem_wait_ld();
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int t = group * 16 + k;
-      out[k] = __uint_as_float(r[k]) * (is * sh.of[t] * sh.gam[t] * a.scale);
-    }
-    tmem_ld(lb + kColQ2, r);
-    tmem_wait_ld();
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      out[k] = fmaf(__uint_as_float(r[k]), ix, out[k]);
-      dot[k] = element(group * 16 + k, 1) * out[k];
-    }
-    put(ga.dq, 0, out);
-    // dKw
-    tmem_ld(lb + kColW1, r);
-    tmem_wait_ld();
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int t = group * 16 + k;
-      w[k] = __uint_as_float(r[k]) * (ids * sh.e[t] * sh.dec[t] * sh.beta[t]);
-      k_w = fmaf(element(t, 0), w[k], k_w);
-    }
-    tmem_ld(lb + kColW2, r);
-    tmem_wait_ld();
-#pragma unroll
-    for (int k = 0; k < 16; ++k) w[k] = fmaf(__uint_as_float(r[k]), iw, w[k]);
-    // dKr
-    tmem_ld(lb + kColR1, r);
-    tmem_wait_ld();
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int t = group * 16 + k;
-      out[k] = __uint_as_float(r[k]) * (-is * sh.of[64 + t] * sh.gam[t] * sh.beta[t]);
-    }
-    tmem_ld(lb + kColR2, r);
-    tmem_wait_ld();
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      out[k] = fmaf(__uint_as_float(r[k]), iz, out[k]);
-      dot[k] = fmaf(element(group * 16 + k, 0), out[k] - w[k], dot[k]);
-      out[k] += w[k];
-      if (!live) dot[k] = 0.0f;
-    }
-    put(ga.dk, 1, out);
-    if (!live) k_w = 0.0f;
-    // Sums over dk, and of <S0, dS> and k_w over the block.
-    const float d = warp_sums(dot, lane);
-    if ((lane & 1) == 0) sh.dots[quarter][group * 16 + (lane >> 1)] = d;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      inner += __shfl_xor_sync(0xffffffffu, inner, o);
-      k_w += __shfl_xor_sync(0xffffffffu, k_w, o);
-    }
-    if (lane == 0) {
-      sh.part[0][warp] = inner;
-      sh.part[1][warp] = k_w;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      float end = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) end += sh.part[1][k];
-      float s = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) s += sh.part[0][k];
-      end = fmaf(sh.gam[63], s, end);
-      // sums from each token to the last: two tokens per lane
-      auto dg = [&](int t) {
-        return (sh.dots[0][t] + sh.dots[1][t]) + (sh.dots[2][t] + sh.dots[3][t]);
+      ok = wait(&sh.kq, item & 1);
+      float k_w = 0.0f;  // sum_j k_j . (Gamma/gamma beta dS E)_j
+      auto element = [&](int tok, int which) {  // of K (0) or Q (1), row lrow of dk
+        const char *p = rb + which * kTile + (lrow >> 6) * 2 * kTile + tok * 128 +
+                        ((((lrow >> 3) & 7) ^ (tok & 7)) << 4) + (lrow & 7) * 2;
+        float x = __half2float(*reinterpret_cast<const __half *>(p));
+        if constexpr (NT == 2)
+          x += __half2float(*reinterpret_cast<const __half *>(p + 2 * (DK / 64) * kTile));
+        return x * (which ? tk.eq[tok] : tk.ek[tok]);
       };
-      const float hi = dg(2 * lane + 1), lo = dg(2 * lane);
-      float sum = hi + lo;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float t = __shfl_down_sync(0xffffffffu, sum, o);
-        if (lane + o < 32) sum += t;
+      for (int k = 0; k < 16; ++k) {
+        const int t = group * 16 + k;
+        const float gam = tk.gam[t], bt = tk.beta[t];
+        q1[k] *= gam * a.scale;
+        r1[k] *= -gam * bt;
+        w1[k] *= tk.dec[t] * bt;
+        if (live && t < c.n) k_w = fmaf(element(t, 0), w1[k], k_w);
       }
-      const float after = sum - (hi + lo);
-      const long long row = packed ? c.row : c.b * a.tokens + c.row;
-      float *p = ga.dg + row * a.vheads + h;
-      if (2 * lane < c.n) p[2ll * lane * a.vheads] = sum + end;
-      if (2 * lane + 1 < c.n) p[(2ll * lane + 1) * a.vheads] = after + hi + end;
+      // The products over tokens
+      ok = ok && wait(&sh.second, item & 1);
+      tc_fence_after();
+      {
+        uint32_t r[16];
+        auto take = [&](uint32_t col, int which, float (&to)[16]) {
+          const float x = scale_inverse(bound_scale(__uint_as_float(tk.most[which])));
+          tmem_ld(lb + col, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) to[k] = fmaf(__uint_as_float(r[k]), x, to[k]);
+        };
+        take(kAccG, 0, q1);
+        take(kAccGt, 1, r1);
+        take(kAccW, 2, w1);
+      }
+      ok = ok && wait(&sh.inner, item & 1);
+      warp_arrive(&sh.read, lane);
+      float dot[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int t = group * 16 + k;
+        dot[k] = live && t < c.n
+                     ? fmaf(element(t, 0), r1[k] - w1[k], element(t, 1) * q1[k]) : 0.0f;
+        r1[k] += w1[k];
+      }
+      const float d = warp_sums(dot, lane);
+      read_before_copy();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh.kq_free);
+      if ((lane & 1) == 0) sh.dots[quarter][group * 16 + (lane >> 1)] = d;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) k_w += __shfl_xor_sync(0xffffffffu, k_w, o);
+      if (lane == 0) sh.k_w[warp] = k_w;
+      auto put = [&](void *dst, char *partial, const float (&v)[16]) {
+        if (!live) return;
+        if constexpr (PARTIAL) {
+          float *p = reinterpret_cast<float *>(partial) + slot * (64 * 128) + group * 16 * DK + lrow;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) p[k * DK] = v[k];
+        } else {
+          const long long row = packed ? c.row : c.b * a.tokens + c.row;
+          T *p = static_cast<T *>(dst) + (row * a.kheads + hk) * a.dk + lrow;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int t = group * 16 + k;
+            if (t < c.n) p[(long long)t * a.kheads * a.dk] = from_acc<T>(v[k]);
+          }
+        }
+      };
+      put(ga.dq, es, q1);
+      put(ga.dk, fs, r1);
+      ok = grad_all(ok);
+      if (!ok) break;
+      if (warp == 0) {
+        float end = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kGradWarps; ++k) end += sh.k_w[k];
+        end = fmaf(tk.gam[63], sh.inner_part[item & 1][0] + sh.inner_part[item & 1][1], end);
+        // sums from each token to the last: two tokens per lane
+        auto dg = [&](int t) {
+          return (sh.dots[0][t] + sh.dots[1][t]) + (sh.dots[2][t] + sh.dots[3][t]);
+        };
+        const float hi = dg(2 * lane + 1), lo = dg(2 * lane);
+        float sum = hi + lo;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float t = __shfl_down_sync(0xffffffffu, sum, o);
+          if (lane + o < 32) sum += t;
+        }
+        const float after = sum - (hi + lo);
+        const long long row = packed ? c.row : c.b * a.tokens + c.row;
+        float *p = ga.dg + row * a.vheads + h;
+        if (2 * lane < c.n) p[2ll * lane * a.vheads] = sum + end;
+        if (2 * lane + 1 < c.n) p[(2ll * lane + 1) * a.vheads] = after + hi + end;
+      }
     }
-    tc_fence_before();
   }
+  tc_fence_before();
   __syncthreads();
-  if (warp == 0) tmem_free(tm, 512);
+  if (warp == kGradWarps) tmem_free(tm, 512);
 }
 
 // dq and dk of the key heads from their value heads' partial sums.

@@ -44,25 +44,26 @@ template <typename T> bool delta_staged(const DeltaArgs &a, const void *in, cons
 
 template <typename T, int DK, bool SAVE, bool STAGED>
 cudaError_t delta_scan_t(const DeltaArgs &a, const DeltaPlan &plan, const char *kq,
-                         const char *images, float *states, float *rows, int *status,
-                         cudaStream_t st) {
+                         const char *images, char *states, char *es, float *scales,
+                         int *status, cudaStream_t st) {
   constexpr size_t smem = scan_smem(DK, Terms<T>::value, STAGED);
   static DeviceOnce once;
   auto kern = delta_scan_kernel<T, DK, SAVE, STAGED>;
   cudaError_t e = smem_limit_once((const void *)kern, smem, once);
   if (e != cudaSuccess) return e;
   const long long blocks = a.batch * a.vheads * ((a.dv + 127) / 128);
-  kern<<<(unsigned)blocks, kScanThreads, smem, st>>>(a, plan, kq, images, states, rows, status);
+  kern<<<(unsigned)blocks, kScanThreads, smem, st>>>(a, plan, kq, images, states, es, scales, status);
   return cudaGetLastError();
 }
 template <typename T, int DK, bool SAVE>
 cudaError_t delta_scan(const DeltaArgs &a, const DeltaPlan &plan, const char *kq,
-                       const char *images, float *states, float *rows, int *status,
-                       cudaStream_t st) {
+                       const char *images, char *states, char *es, float *scales,
+                       int *status, cudaStream_t st) {
   if constexpr (sizeof(T) == 2)
     if (delta_staged<T>(a, a.v, a.sv, a.o))
-      return delta_scan_t<T, DK, SAVE, true>(a, plan, kq, images, states, rows, status, st);
-  return delta_scan_t<T, DK, SAVE, false>(a, plan, kq, images, states, rows, status, st);
+      return delta_scan_t<T, DK, SAVE, true>(a, plan, kq, images, states, es, scales, status,
+                                             st);
+  return delta_scan_t<T, DK, SAVE, false>(a, plan, kq, images, states, es, scales, status, st);
 }
 
 template <typename T, int DK>
@@ -74,49 +75,54 @@ cudaError_t delta_forward_t(const DeltaArgs &a, char *ws, cudaStream_t st) {
   cudaError_t e = delta_make_plan<T>(a, w, ws, plan, st);
   if (e == cudaSuccess) e = delta_prep_t<T, DK, false>(a, plan, ws + w.kq, ws + w.images, nullptr, status, st);
   if (e == cudaSuccess)
-    e = delta_scan<T, DK, false>(a, plan, ws + w.kq, ws + w.images, nullptr, nullptr, status, st);
+    e = delta_scan<T, DK, false>(a, plan, ws + w.kq, ws + w.images, nullptr, nullptr, nullptr, status,
+                                st);
   return e;
 }
 
 template <typename T, int DK, bool STAGED>
 cudaError_t delta_back_t(const DeltaArgs &a, const DeltaGradArgs &g, const DeltaPlan &plan,
-                         const char *kq, const char *images, float *dstates, float *rows,
-                         int *status, cudaStream_t st) {
+                         const char *kq, const char *images, char *dstates, char *fs, char *os,
+                         float *scales, int *status, cudaStream_t st) {
   constexpr size_t smem = scan_smem(DK, Terms<T>::value, STAGED);
   static DeviceOnce once;
   auto kern = delta_back_kernel<T, DK, STAGED>;
   cudaError_t e = smem_limit_once((const void *)kern, smem, once);
   if (e != cudaSuccess) return e;
   const long long blocks = a.batch * a.vheads * ((a.dv + 127) / 128);
-  kern<<<(unsigned)blocks, kScanThreads, smem, st>>>(a, g, plan, kq, images, dstates, rows, status);
+  kern<<<(unsigned)blocks, kScanThreads, smem, st>>>(a, g, plan, kq, images, dstates, fs, os, scales,
+                                                       status);
   return cudaGetLastError();
 }
 template <typename T, int DK>
 cudaError_t delta_back(const DeltaArgs &a, const DeltaGradArgs &g, const DeltaPlan &plan,
-                       const char *kq, const char *images, float *dstates, float *rows,
-                       int *status, cudaStream_t st) {
+                       const char *kq, const char *images, char *dstates, char *fs, char *os,
+                       float *scales, int *status, cudaStream_t st) {
   if constexpr (sizeof(T) == 2)
     if (a.dv % 8 == 0 && (((uintptr_t)g.dout | (uintptr_t)g.dv) & 15u) == 0)
-      return delta_back_t<T, DK, true>(a, g, plan, kq, images, dstates, rows, status, st);
-  return delta_back_t<T, DK, false>(a, g, plan, kq, images, dstates, rows, status, st);
+      return delta_back_t<T, DK, true>(a, g, plan, kq, images, dstates, fs, os, scales, status, st);
+  return delta_back_t<T, DK, false>(a, g, plan, kq, images, dstates, fs, os, scales, status, st);
 }
 
 template <typename T, int DK, bool PARTIAL>
 cudaError_t delta_grad_t(const DeltaArgs &a, const DeltaGradArgs &g, const DeltaPlan &plan,
-                         const char *kq, const char *back, const float *states,
-                         const float *dstates, float *es, float *fs, int *status,
-                         cudaStream_t st) {
+                         const char *kq, const char *back, const char *states,
+                         const char *dstates, char *es, char *fs, const char *os,
+                         const float *scales, int *status, cudaStream_t st) {
   static DeviceOnce once;
   auto kern = delta_grad_kernel<T, DK, PARTIAL>;
-  cudaError_t e = smem_limit_once((const void *)kern, grad_smem(), once);
+  cudaError_t e = smem_limit_once((const void *)kern, grad_smem(DK, Terms<T>::value), once);
   const long long chunks = plan.chunks_max;
   if (e != cudaSuccess || chunks == 0) return e;
-  kern<<<(unsigned)(chunks * a.vheads), kGradThreads, grad_smem(), st>>>(
-      a, g, plan, kq, back, states, dstates, es, fs, status);
+  const long long items = chunks * a.vheads;
+  const int blocks = (int)(items < sm_count() ? items : sm_count());
+  kern<<<blocks, kGradThreads, grad_smem(DK, Terms<T>::value), st>>>(
+      a, g, plan, kq, back, states, dstates, es, fs, os, scales, status);
   e = cudaGetLastError();
   if (e != cudaSuccess || !PARTIAL) return e;
   delta_grad_sum_kernel<T, DK>
-      <<<dim3((unsigned)(chunks * a.kheads), 2), 256, 0, st>>>(a, g, plan, es, fs);
+      <<<dim3((unsigned)(chunks * a.kheads), 2), 256, 0, st>>>(
+      a, g, plan, reinterpret_cast<const float *>(es), reinterpret_cast<const float *>(fs));
   return cudaGetLastError();
 }
 
@@ -126,21 +132,19 @@ cudaError_t delta_backward_t(const DeltaArgs &a, const DeltaGradArgs &g, char *w
   int *status = device_status_word();
   if (!status) return cudaErrorInvalidDevice;
   const DeltaLayout w(a, a.offsets != nullptr, true);
-  auto floats = [&](size_t at) { return reinterpret_cast<float *>(ws + at); };
   char *kq = ws + w.kq, *images = ws + w.images, *back = ws + w.back;
+  char *states = ws + w.state, *dstates = ws + w.dstate, *es = ws + w.e, *fs = ws + w.f, *os = ws + w.o;
+  float *scales = reinterpret_cast<float *>(ws + w.scales);
   DeltaPlan plan;
   cudaError_t e = delta_make_plan<T>(a, w, ws, plan, st);
   if (e == cudaSuccess) e = delta_prep_t<T, DK, true>(a, plan, kq, images, back, status, st);
   if (e == cudaSuccess)
-    e = delta_scan<T, DK, true>(a, plan, kq, images, floats(w.state), floats(w.e), status, st);
+    e = delta_scan<T, DK, true>(a, plan, kq, images, states, es, scales, status, st);
   if (e == cudaSuccess)
-    e = delta_back<T, DK>(a, g, plan, kq, back, floats(w.dstate), floats(w.f), status, st);
+    e = delta_back<T, DK>(a, g, plan, kq, back, dstates, fs, os, scales, status, st);
   if (e != cudaSuccess) return e;
-  return a.vheads == a.kheads
-             ? delta_grad_t<T, DK, false>(a, g, plan, kq, back, floats(w.state), floats(w.dstate),
-                                          floats(w.e), floats(w.f), status, st)
-             : delta_grad_t<T, DK, true>(a, g, plan, kq, back, floats(w.state), floats(w.dstate),
-                                         floats(w.e), floats(w.f), status, st);
+  auto grad = a.vheads == a.kheads ? delta_grad_t<T, DK, false> : delta_grad_t<T, DK, true>;
+  return grad(a, g, plan, kq, back, states, dstates, es, fs, os, scales, status, st);
 }
 
 }  // namespace fftgb

@@ -33,7 +33,7 @@
 // value of the state in a column of v, and K's scaled rows below 2:
 //   forward  |Y| <= |V| + b1 |S|,  |U| <= b2 |Y|,  |W| <= b3 |Y|
 //            b1 = 2 DK max gamma 2^ek,  b2 = max beta r,
-//            b3 = max Gamma/gamma 2^ek beta r,  r = row sums of |inverse|
+//            b3 = max Gamma/gamma 2^ek beta r,  r = row sums of |inverse|,  b4 = max r
 //   BACK     |dU| <= b1 |dS| + b2 |dO|,  |F| <= b3 |dU|,  |gamma beta F 2^ek| <= b4 |F|,
 //            |scale gamma dO 2^eq| <= b5 |dO|
 //            b1 = 2 DK max Gamma/gamma 2^ek,  b2 = max scale (row sums of |M^T|),
@@ -127,6 +127,30 @@ __device__ __forceinline__ void running_decay(const float *g, long long step, in
     s *= 1.4426950408889634;
     const float h = (float)s;
     out[tid] = make_float2(h, (float)(s - (double)h));
+  }
+}
+// The same by one warp, two tokens per lane.
+__device__ __forceinline__ void running_decay_warp(const float *g, long long step, int n, int lane,
+                                                   float2 *out) {
+  double x[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int t = 2 * lane + k;
+    float v = t < n ? g[t * step] : 0.0f;
+    v = v < kMinLogDecay ? kMinLogDecay : v;
+    x[k] = v;
+  }
+  double s = x[0] + x[1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double t = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += t;
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const double e = (k ? s : s - x[1]) * 1.4426950408889634;
+    const float h = (float)e;
+    out[2 * lane + k] = make_float2(h, (float)(e - (double)h));
   }
 }
 __device__ __forceinline__ float decay_between(float2 i, float2 j) {
@@ -226,7 +250,7 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
   __shared__ float4 Gk[64];  // G, the scale of K's row
   __shared__ __align__(16) float beta_s[64];
   __shared__ float inv_kq[2 * 64], inv[4][64], sum[4][64];
-  __shared__ float most[2][8];
+  __shared__ float most[2][9];
   constexpr int NT = Terms<T>::value;
   constexpr uint32_t kPlane = 2 * (DK / 64) * kTile;  // [K; Q], one term
 
@@ -355,7 +379,7 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
         const float ga[kGates] = {-gam * ek, dec * bt * ek * et, bt * et, gam * (eq / em),
                                   a.scale * em, et, ek, eq};
         const float ba = fabsf(bt) * sum[0][tid], sc = fabsf(a.scale);
-        float b[8];
+        float b[9];
         b[0] = 2.0f * DK * gam * ek;
         b[1] = ba;
         b[2] = ba * dec * ek;
@@ -374,17 +398,19 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
           b[5] = sum[2][tid];
           b[6] = gam * fabsf(bt) * ek;
           b[7] = sc * gam * eq;
+          b[8] = sum[0][tid];
         }
 #pragma unroll
-        for (int k = 0; k < (GRAD ? 8 : 3); ++k) {
+        for (int k = 0; k < (GRAD ? 9 : 3); ++k) {
           b[k] = lane_max<32>(b[k]);
           if (lane == 0) most[warp][k] = b[k];
         }
       }
       __syncthreads();
-      if (tid < (GRAD ? 8 : 3))
-        reinterpret_cast<float *>((tid < 3 ? image : imageb) + 4 * kTile)
-            [kChunkAt + (tid < 3 ? 1 + tid : tid - 2)] = fmaxf(most[0][tid], most[1][tid]);
+      if (tid < (GRAD ? 9 : 3))
+        reinterpret_cast<float *>((tid < 3 || tid == 8 ? image : imageb) + 4 * kTile)
+            [kChunkAt + (tid < 3 ? 1 + tid : tid == 8 ? 4 : tid - 2)] =
+                fmaxf(most[0][tid], most[1][tid]);
     }
     tc_fence_before();
   }

@@ -316,6 +316,47 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
   if (lane == 0) bar_arrive(bar);
 }
 
+// 16 scaled values of a thread's column, rows m .. m + 15, to the slabs of a
+// matrix of `rows` rows; TWO: both parts, else the leading one.
+template <bool TWO>
+__device__ __forceinline__ void put_slab(char *matrix, int rows, int parts, int m, int col,
+                                         const float2 (&f)[8], bool live) {
+  char *at = matrix + (col >> 4) * (parts * slab_part(rows)) + (m >> 3) * 256 + (col & 15) * 16;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      split2(f[4 * p + j], hi[j], lo[j]);
+      if (!live) hi[j] = lo[j] = 0;
+    }
+    *reinterpret_cast<uint4 *>(at + p * 256) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if constexpr (TWO)
+      *reinterpret_cast<uint4 *>(at + p * 256 + slab_part(rows)) =
+          make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+}
+
+// Bounds over all 128 columns of v, for the scales of what is kept for the
+// gradients: every warp enters its own before it hands over an operand, and
+// reads the block's once the product that waited for all of them is there.
+// Four chunks' entries; those of the chunk after next are cleared.
+constexpr int kTops = 3;
+struct BlockBounds {
+  unsigned top[4][kTops];
+  __device__ __forceinline__ void enter(int it, int which, float b, int lane) {
+    // (of values that are not negative the bits are in order)
+    const unsigned m = __reduce_max_sync(0xffffffffu, __float_as_uint(b));
+    if (lane == 0) atomicMax(&top[it & 3][which], m);
+  }
+  __device__ __forceinline__ float scale(int it, int which) const {
+    return bound_scale(__uint_as_float(*(volatile const unsigned *)&top[it & 3][which]));
+  }
+  __device__ __forceinline__ void clear(int it) {
+    for (int k = 0; k < kTops; ++k) top[(it + 2) & 3][k] = 0;
+  }
+};
+
 // The largest of what the four threads of a column of v bring, twice.  Their
 // four warps meet at a barrier of their own; the two halves of `box` alternate,
 // so one barrier per agreement is enough.
@@ -361,19 +402,20 @@ __device__ __forceinline__ uint32_t scan_begin(ScanBars &bars, uint32_t *slot, v
   return __shfl_sync(0xffffffffu, *slot, 0);
 }
 
-// SAVE leaves for the gradients, per chunk, head and 128 columns of v, the
-// state that entered the chunk (fp32 [DK][128]) and E (fp32 [64][128]).
+// SAVE leaves for the gradients the state that entered each chunk and E, as
+// slabs (delta.cuh).
 // STAGED: V comes and O goes through shared memory by bulk copies of rows
 // (16-bit types on 16-byte boundaries); else straight from and to HBM.
 template <typename T, int DK, bool SAVE, bool STAGED>
 __global__ void __launch_bounds__(kScanThreads, 1)
 delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const char *images,
-                  float *states, float *rows, int *status) {
+                  char *states, char *es, float *scales, int *status) {
   extern __shared__ char smem_raw[];
   __shared__ ScanBars bars;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int failed;
   __shared__ float2 box[2][kScanGroups][128];
+  __shared__ BlockBounds bounds;
   constexpr int NT = Terms<T>::value, ST = kScanStages;
   constexpr int kStage = scan_stage_bytes(DK, NT, STAGED);
   // bf16 outputs: their rounding (2^-9) hides what the leading fp16 parts of
@@ -385,6 +427,7 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
   const int h = (blockIdx.x / blocks_v) % a.vheads;
   const ScanSpan sp = scan_span(a, plan, blockIdx.x / blocks_v / a.vheads);
   char *stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  if (SAVE && tid < 4 * kTops) bounds.top[tid / kTops][tid % kTops] = 0;
   const uint32_t tm = scan_begin(bars, &tmem_slot, &failed, STAGED, tid, warp);
   char *ring = stages + ST * kStage + (STAGED ? kRows16 : 0);
   auto wait = [&](uint64_t *b, uint32_t parity) { return wait_or_fail(b, parity, &failed, status); };
@@ -490,15 +533,15 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       tmem_wait_st();
       warp_arrive(&bars.sb, lane);
       if constexpr (SAVE) {
-        const float inv = scale_inverse(ss);
-        float *dst = states + saved(c) * (DK * 128) + row;
+        const float xs = bounds.scale(c - 1, 1), by = scale_inverse(ss) * xs;
 #pragma unroll
-        for (int p = 0; p < SP; ++p)
+        for (int p = 0; p < SP; ++p) {
+          float2 f[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            dst[(group * SC + p * 16 + 2 * j) * 128] = S[p][j].x * inv;
-            dst[(group * SC + p * 16 + 2 * j + 1) * 128] = S[p][j].y * inv;
-          }
+          for (int j = 0; j < 8; ++j) f[j] = mul2(S[p][j], both(by));
+          put_slab<true>(states + saved(c) * (512 * DK), DK, 2, group * SC + p * 16, row, f, live);
+        }
+        if (tid == 0) scales[saved(c) * kScales + kScaleS] = scale_inverse(xs);
       }
     };
     auto state_max = [&]() {
@@ -530,8 +573,6 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
                       : make_float2(to_acc(vr[STAGED ? 0 : 2 * j]),
                                     to_acc(vr[STAGED ? 0 : 2 * j + 1]));
       vmax = max16(0.0f, f);
-      __syncwarp();
-      if (lane == 0) bar_arrive(&bars.empty[s]);
       return true;
     };
     // The output of chunk c, whose U was scaled by us.
@@ -567,7 +608,12 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
     bool ok = true;
     if (sp.chunks > 0) {
       fetch_v(0);
-      ss = bound_scale(agree.largest(state_max(), 0.0f).x);
+      const float smax = agree.largest(state_max(), 0.0f).x;
+      ss = bound_scale(smax);
+      if constexpr (SAVE) {
+        bounds.enter(-1, 1, live ? smax : 0.0f, lane);
+        asm volatile("bar.sync 5, %0;" ::"n"(kScanWarps * 32) : "memory");
+      }
 #pragma unroll
       for (int p = 0; p < SP; ++p)
 #pragma unroll
@@ -588,7 +634,11 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       const float by = most.y + chunk[1] * smax, bw = by * chunk[3];
       const float ys = bound_scale(by), us = bound_scale(by * chunk[2]), wsc = bound_scale(bw);
       const float inv_y = scale_inverse(ys);
-      const float next_ss = bound_scale(fmaf(Gamma, smax, 128.0f * bw));
+      const float bs = fmaf(Gamma, smax, 128.0f * bw), next_ss = bound_scale(bs);
+      if constexpr (SAVE) {
+        bounds.enter(it, 0, live ? by * chunk[4] : 0.0f, lane);
+        bounds.enter(it, 1, live ? bs : 0.0f, lane);
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = mul2(f[j], both(ys));
       // Y = V^T - P gamma
@@ -602,6 +652,7 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, f);
       tmem_wait_st();
       warp_arrive(&bars.y, lane);
+      if (lane == 0) bar_arrive(&bars.empty[it % ST]);  // V has been used
       // While E is computed: the output of the chunk before.
       if (it > 0 && !(ok = put_output(it - 1, us_before))) break;
       us_before = us;
@@ -625,10 +676,15 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
       if constexpr (LEAD) put_lead(lb + kColYh + group * 8, f);
       else put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, f);
       if constexpr (SAVE) {
-        float *dst = rows + saved(it) * (64 * 128) + group * TK * 128 + row;
+        const float es_scale = bounds.scale(it, 0);
 #pragma unroll
-        for (int j = 0; j < TK; ++j)
-          dst[j * 128] = __uint_as_float(r[j]) * (gates[5 * 64 + j] * inv_y);
+        for (int j = 0; j < 8; ++j)
+          f[j] = mul2(pair(r, j), mul2(gate(gates + 5 * 64, j), both(inv_y * es_scale)));
+        put_slab<true>(es + saved(it) * (64 * 128 * 4), 64, 2, group * TK, row, f, live);
+        if (tid == 0) {
+          scales[saved(it) * kScales + kScaleE] = scale_inverse(es_scale);
+          bounds.clear(it);
+        }
       }
       // While the new state is computed: N in units of U M^T, the start of O
       if (!(ok = wait(&bars.n, ph))) break;

@@ -191,6 +191,19 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint3
       "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "n"(kDescHigh)
       : "memory");
 }
+// D (TMEM) (+)= A (shared) B (shared), both MN-major without swizzle: blocks of 8
+// summed x 8 outer indexes are 128 contiguous bytes, along the summed index
+// 128 bytes apart, along the outer one 256.
+__device__ __forceinline__ void mma_ss_plain(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                             bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(tile_desc(a, 128)), "r"(tile_desc(b, 128)), "r"(idesc), "r"((uint32_t)accumulate),
+      "n"((256u >> 4) | (1u << 14))
+      : "memory");
+}
 // The barrier gets one arrival when every product issued so far by this
 // thread has completed.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
