@@ -48,11 +48,18 @@ __host__ __device__ constexpr size_t grad_smem(int dk, int terms) {
   return 1024 + kq_bytes(dk, terms) + 8 * kTile + (size_t)grad_slabs(terms) * slab_bytes(dk);
 }
 
-struct GradTokens {
+struct alignas(16) GradTokens {
   float2 G[64];
-  float beta[64], gam[64], dec[64], ek[64], eq[64];
+  float beta[64], ek[64], eq[64];
+  float fq[64], fr[64], fw[64];  // scale gamma, -gamma beta, Gamma/gamma beta; 0 past the chunk's end
+  float Gamma;
   unsigned most[3];  // largest X1, Z1, and X2 or Z2
 };
+// Four tokens' factors.
+__device__ __forceinline__ void four(const float *p, float (&f)[4]) {
+  const float4 x = *reinterpret_cast<const float4 *>(p);
+  f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+}
 struct GradShared {
   uint64_t full[4], empty[4];       // slabs
   uint64_t kq, kq_free;             // K and Q there; read
@@ -128,13 +135,47 @@ __device__ __forceinline__ float warp_sums(float (&v)[16], int lane) {
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-// PARTIAL: dq and dk of this value head go to `partial` (fp32 [2][64][DK] in
-// place of the chunk's E and F, which only this block reads), else to their arrays.
-template <typename T, int DK, bool PARTIAL>
+// A thread's column of dk of 16 tokens, `step` apart.  Two lanes exchange every
+// other token, so that each stores two columns at once (PAIRS).
+template <typename T, bool PAIRS>
+__device__ __forceinline__ void put_tokens(T *p, long long step, int tokens, bool live, int lane,
+                                           const float (&v)[16]) {
+  if constexpr (PAIRS) {
+    const int odd = lane & 1;
+    uint32_t *w = reinterpret_cast<uint32_t *>(p - odd + odd * step);
+    float x[16];
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+      const float o = __shfl_xor_sync(0xffffffffu, odd ? v[k] : v[k + 1], 1);
+      x[k] = odd ? o : v[k];
+      x[k + 1] = odd ? v[k + 1] : o;
+    }
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+      T pair[2] = {from_acc<T>(x[k]), from_acc<T>(x[k + 1])};
+      if (live && k + odd < tokens) *w = *reinterpret_cast<const uint32_t *>(pair);
+      w = reinterpret_cast<uint32_t *>(reinterpret_cast<T *>(w) + 2 * step);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (live && k < tokens) *p = from_acc<T>(v[k]);
+      p += step;
+    }
+  }
+}
+
+// partial: dq and dk of this value head go to fp32 arrays [64][DK] in place of
+// the chunk's E and F, which only this block reads, else to their arrays.
+// MULTI: more than 128 columns of v, whose sums are kept in registers; with one
+// block of columns they stay in tensor memory until X and Z are done (what was
+// spilled instead cost 280 us of 424: the memory left beside the ring is no
+// cache).
+template <typename T, int DK, bool MULTI>
 __global__ void __launch_bounds__(kGradThreads, 1)
 delta_grad_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan plan, const char *kq,
                   const char *back, const char *states, const char *dstates, char *es, char *fs,
-                  const char *os, const float *scales, int *status) {
+                  const char *os, const float *scales, bool partial, int *status) {
   extern __shared__ char smem_raw[];
   __shared__ GradShared sh;
   constexpr int NT = Terms<T>::value, R = grad_slabs(NT), kSlabBytes = slab_bytes(DK);
@@ -142,7 +183,7 @@ delta_grad_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   char *ra = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   char *rb = ra + 8 * kTile, *ring = rb + kq_bytes(DK, NT);
-  const int blocks_v = (a.dv + 127) / 128;
+  const int blocks_v = MULTI ? (a.dv + 127) / 128 : 1;
   const bool packed = plan.chunk0 != nullptr;
   const long long items = (packed ? (long long)plan.chunk0[a.batch] : plan.chunks_max) * a.vheads;
   volatile int *failed = &sh.failed;
@@ -325,13 +366,6 @@ delta_grad_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
       if (warp == 0) {
         running_decay_warp(a.g + c.b * a.sg.seq + c.row * a.sg.tok + h * a.sg.head, a.sg.tok, c.n,
                            lane, tk.G);
-        __syncwarp();
-        const float2 end = tk.G[63];
-#pragma unroll
-        for (int t = lane; t < 64; t += 32) {
-          tk.gam[t] = decay_between(tk.G[t], make_float2(0.0f, 0.0f));
-          tk.dec[t] = decay_between(end, tk.G[t]);
-        }
       } else if (warp == 1) {
         const float *gates = reinterpret_cast<const float *>(
             back + (ci * a.vheads + h) * (long long)kImageBytes + 4 * kTile);
@@ -347,29 +381,43 @@ delta_grad_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
       float q1[16], r1[16], w1[16], gx[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) q1[k] = r1[k] = w1[k] = gx[k] = 0.0f;
+      auto take = [&](uint32_t lead, uint32_t trail, float x, float y, float (&to)[16]) {
+        uint32_t r[16], t[16];
+        tmem_ld(lb + lead, r);
+        tmem_ld(lb + trail, t);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          to[k] = fmaf((__uint_as_float(r[k]) + __uint_as_float(t[k])) * x, y, to[k]);
+      };
+      float is = 0.0f, jf = 0.0f, jo = 0.0f;
       for (int vb = 0; vb < blocks_v; ++vb, ++phases) {
         const float *sc = scales + (slot + vb) * kScales;
-        const float is = sc[kScaleS], ie = sc[kScaleE], ids = sc[kScaleD], jf = sc[kScaleF],
-                    jo = sc[kScaleO];
+        const float ie = sc[kScaleE], ids = sc[kScaleD];
+        is = sc[kScaleS];
+        jf = sc[kScaleF];
+        jo = sc[kScaleO];
         ok = ok && wait(&sh.first, phases & 1);
         tc_fence_after();
-        uint32_t r[16], t[16];
-        auto take = [&](uint32_t lead, uint32_t trail, float x, float y, float (&to)[16]) {
-          tmem_ld(lb + lead, r);
-          tmem_ld(lb + trail, t);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            to[k] = fmaf((__uint_as_float(r[k]) + __uint_as_float(t[k])) * x, y, to[k]);
-        };
         take(kAccG, kAccGt, is_z ? jf : jo, ie, gx);
-        take(kAccQ, kAccQt, is, jo, q1);
-        take(kAccQ + 64, kAccQt + 64, is, jf, r1);
         take(kAccW, kAccWt, ids, ie, w1);
-        if (vb + 1 < blocks_v) warp_arrive(&sh.read, lane);
+        if (MULTI) {
+          take(kAccQ, kAccQt, is, jo, q1);
+          take(kAccQ + 64, kAccQt + 64, is, jf, r1);
+          if (vb + 1 < blocks_v) warp_arrive(&sh.read, lane);
+        }
       }
       ok = grad_all(ok);
       if (!ok) break;
+      if (warp < 2) {
+        const int t = tid;
+        const float gam = decay_between(tk.G[t], make_float2(0.0f, 0.0f)), bt = tk.beta[t];
+        const bool there = t < c.n;
+        tk.fq[t] = there ? gam * a.scale : 0.0f;
+        tk.fr[t] = there ? -gam * bt : 0.0f;
+        tk.fw[t] = there ? decay_between(tk.G[63], tk.G[t]) * bt : 0.0f;
+        if (t == 63) tk.Gamma = gam;
+      }
       // X (rows 0 .. 63) and Z (64 .. 127) of [dO; F] E^T: this thread's row and 16
       // columns, each twice: times 2^ek_j for the products summed over j, times
       // 2^eq_i or 2^ek_i for those summed over i.
@@ -377,15 +425,22 @@ delta_grad_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
         float m1 = 0.0f, m2 = 0.0f;
         const float bi = is_z ? -tk.beta[i] : a.scale, over = is_z ? tk.ek[i] : tk.eq[i];
         const float2 gi = tk.G[i];
-        const int last = i < c.n ? is_z ? i - 1 : i : -1;
+        const int last = (i < c.n ? is_z ? i - 1 : i : -1) - group * 16;
+        const int diagonal = is_z && i < c.n ? i - group * 16 : -1;
+        float *db = ga.dbeta + (packed ? c.row + i : c.b * a.tokens + c.row + i) * a.vheads + h;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int j = group * 16 + k;
-          if (is_z && j == i && i < c.n)
-            ga.dbeta[(packed ? c.row + i : c.b * a.tokens + c.row + i) * a.vheads + h] = gx[k];
-          gx[k] = j <= last ? decay_between(gi, tk.G[j]) * tk.beta[j] * gx[k] * bi : 0.0f;
-          m1 = fmaxf(m1, fabsf(gx[k] * tk.ek[j]));
-          m2 = fmaxf(m2, fabsf(gx[k]));
+        for (int k0 = 0; k0 < 16; k0 += 4) {
+          float bj[4], ej[4];
+          four(tk.beta + group * 16 + k0, bj);
+          four(tk.ek + group * 16 + k0, ej);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = k0 + e;
+            if (k == diagonal) *db = gx[k];
+            gx[k] = k <= last ? decay_between(gi, tk.G[group * 16 + k]) * bj[e] * gx[k] * bi : 0.0f;
+            m1 = fmaxf(m1, fabsf(gx[k] * ej[e]));
+            m2 = fmaxf(m2, fabsf(gx[k]));
+          }
         }
         m1 = lane_max<32>(m1);
         m2 = lane_max<32>(m2 * over);
@@ -401,9 +456,14 @@ delta_grad_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
         for (int p = 0; p < 2; ++p) {
           float f[8], g[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            g[k] = gx[8 * p + k];
-            f[k] = g[k] * tk.ek[group * 16 + 8 * p + k];
+          for (int k = 0; k < 8; k += 4) {
+            float ej[4];
+            four(tk.ek + group * 16 + 8 * p + k, ej);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              g[k + e] = gx[8 * p + k + e];
+              f[k + e] = g[k + e] * ej[e];
+            }
           }
           uint4 hi, lo;
           const int at = piece_at(i, group * 2 + p, 0);
@@ -417,51 +477,70 @@ delta_grad_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
         fence_smem_to_async();
         warp_arrive(&sh.tiles, lane);
       }
+      if (!MULTI) {
+        take(kAccQ, kAccQt, is, jo, q1);
+        take(kAccQ + 64, kAccQt + 64, is, jf, r1);
+      }
       ok = wait(&sh.kq, item & 1);
-      float k_w = 0.0f;  // sum_j k_j . (Gamma/gamma beta dS E)_j
-      auto element = [&](int tok, int which) {  // of K (0) or Q (1), row lrow of dk
+      // Row lrow of dk of K (0) or Q (1), a token's value without its scale
+      auto element = [&](int tok, int which) {
         const char *p = rb + which * kTile + (lrow >> 6) * 2 * kTile + tok * 128 +
                         ((((lrow >> 3) & 7) ^ (tok & 7)) << 4) + (lrow & 7) * 2;
         float x = __half2float(*reinterpret_cast<const __half *>(p));
         if constexpr (NT == 2)
           x += __half2float(*reinterpret_cast<const __half *>(p + 2 * (DK / 64) * kTile));
-        return x * (which ? tk.eq[tok] : tk.ek[tok]);
+        return x;
       };
+      float k_w = 0.0f, dot[16];  // k_w: sum_j k_j . (Gamma/gamma beta dS E)_j
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int t = group * 16 + k;
-        const float gam = tk.gam[t], bt = tk.beta[t];
-        q1[k] *= gam * a.scale;
-        r1[k] *= -gam * bt;
-        w1[k] *= tk.dec[t] * bt;
-        if (live && t < c.n) k_w = fmaf(element(t, 0), w1[k], k_w);
+      for (int k0 = 0; k0 < 16; k0 += 4) {
+        float fq[4], fr[4], fw[4], ek[4];
+        four(tk.fq + group * 16 + k0, fq);
+        four(tk.fr + group * 16 + k0, fr);
+        four(tk.fw + group * 16 + k0, fw);
+        four(tk.ek + group * 16 + k0, ek);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int k = k0 + e;
+          q1[k] *= fq[e];
+          r1[k] *= fr[e];
+          w1[k] *= fw[e];
+          dot[k] = element(group * 16 + k, 0) * ek[e];
+          k_w = fmaf(dot[k], w1[k], k_w);
+        }
       }
       // The products over tokens
       ok = ok && wait(&sh.second, item & 1);
       tc_fence_after();
       {
-        uint32_t r[16];
-        auto take = [&](uint32_t col, int which, float (&to)[16]) {
+        auto add = [&](uint32_t col, int which, float (&to)[16]) {
           const float x = scale_inverse(bound_scale(__uint_as_float(tk.most[which])));
+          uint32_t r[16];
           tmem_ld(lb + col, r);
           tmem_wait_ld();
 #pragma unroll
           for (int k = 0; k < 16; ++k) to[k] = fmaf(__uint_as_float(r[k]), x, to[k]);
         };
-        take(kAccG, 0, q1);
-        take(kAccGt, 1, r1);
-        take(kAccW, 2, w1);
+        add(kAccG, 0, q1);
+        add(kAccGt, 1, r1);
+        add(kAccW, 2, w1);
       }
       ok = ok && wait(&sh.inner, item & 1);
       warp_arrive(&sh.read, lane);
-      float dot[16];
+      const int tokens = c.n - group * 16;  // of these 16
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int t = group * 16 + k;
-        dot[k] = live && t < c.n
-                     ? fmaf(element(t, 0), r1[k] - w1[k], element(t, 1) * q1[k]) : 0.0f;
-        r1[k] += w1[k];
+      for (int k0 = 0; k0 < 16; k0 += 4) {
+        float eq[4];
+        four(tk.eq + group * 16 + k0, eq);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int k = k0 + e;
+          dot[k] = fmaf(dot[k], r1[k] - w1[k], element(group * 16 + k, 1) * eq[e] * q1[k]);
+          if (!live || k >= tokens) dot[k] = 0.0f;
+          r1[k] += w1[k];
+        }
       }
+      if (!live) k_w = 0.0f;
       const float d = warp_sums(dot, lane);
       read_before_copy();
       __syncwarp();
@@ -470,31 +549,30 @@ delta_grad_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) k_w += __shfl_xor_sync(0xffffffffu, k_w, o);
       if (lane == 0) sh.k_w[warp] = k_w;
-      auto put = [&](void *dst, char *partial, const float (&v)[16]) {
-        if (!live) return;
-        if constexpr (PARTIAL) {
-          float *p = reinterpret_cast<float *>(partial) + slot * (64 * 128) + group * 16 * DK + lrow;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) p[k * DK] = v[k];
+      if (partial) {
+        const long long at = slot * (64 * 128) + group * 16 * DK + lrow;
+        put_tokens<float, false>(reinterpret_cast<float *>(es) + at, DK, 16, lrow < DK, lane, q1);
+        put_tokens<float, false>(reinterpret_cast<float *>(fs) + at, DK, 16, lrow < DK, lane, r1);
+      } else {
+        const long long step = (long long)a.kheads * a.dk;
+        const long long row = (packed ? c.row : c.b * a.tokens + c.row) + group * 16;
+        T *dq = static_cast<T *>(ga.dq) + row * step + hk * a.dk + lrow;
+        T *dk = static_cast<T *>(ga.dk) + row * step + hk * a.dk + lrow;
+        if (sizeof(T) == 2 && a.dk % 2 == 0 && (((uintptr_t)ga.dq | (uintptr_t)ga.dk) & 3u) == 0) {
+          put_tokens<T, sizeof(T) == 2>(dq, step, tokens, live, lane, q1);
+          put_tokens<T, sizeof(T) == 2>(dk, step, tokens, live, lane, r1);
         } else {
-          const long long row = packed ? c.row : c.b * a.tokens + c.row;
-          T *p = static_cast<T *>(dst) + (row * a.kheads + hk) * a.dk + lrow;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int t = group * 16 + k;
-            if (t < c.n) p[(long long)t * a.kheads * a.dk] = from_acc<T>(v[k]);
-          }
+          put_tokens<T, false>(dq, step, tokens, live, lane, q1);
+          put_tokens<T, false>(dk, step, tokens, live, lane, r1);
         }
-      };
-      put(ga.dq, es, q1);
-      put(ga.dk, fs, r1);
+      }
       ok = grad_all(ok);
       if (!ok) break;
       if (warp == 0) {
         float end = 0.0f;
 #pragma unroll
         for (int k = 0; k < kGradWarps; ++k) end += sh.k_w[k];
-        end = fmaf(tk.gam[63], sh.inner_part[item & 1][0] + sh.inner_part[item & 1][1], end);
+        end = fmaf(tk.Gamma, sh.inner_part[item & 1][0] + sh.inner_part[item & 1][1], end);
         // sums from each token to the last: two tokens per lane
         auto dg = [&](int t) {
           return (sh.dots[0][t] + sh.dots[1][t]) + (sh.dots[2][t] + sh.dots[3][t]);

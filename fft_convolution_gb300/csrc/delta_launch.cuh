@@ -104,24 +104,25 @@ cudaError_t delta_back(const DeltaArgs &a, const DeltaGradArgs &g, const DeltaPl
   return delta_back_t<T, DK, false>(a, g, plan, kq, images, dstates, fs, os, scales, status, st);
 }
 
-template <typename T, int DK, bool PARTIAL>
+template <typename T, int DK, bool MULTI>
 cudaError_t delta_grad_t(const DeltaArgs &a, const DeltaGradArgs &g, const DeltaPlan &plan,
                          const char *kq, const char *back, const char *states,
                          const char *dstates, char *es, char *fs, const char *os,
                          const float *scales, int *status, cudaStream_t st) {
+  constexpr size_t smem = grad_smem(DK, Terms<T>::value);
   static DeviceOnce once;
-  auto kern = delta_grad_kernel<T, DK, PARTIAL>;
-  cudaError_t e = smem_limit_once((const void *)kern, grad_smem(DK, Terms<T>::value), once);
+  auto kern = delta_grad_kernel<T, DK, MULTI>;
+  cudaError_t e = smem_limit_once((const void *)kern, smem, once);
   const long long chunks = plan.chunks_max;
   if (e != cudaSuccess || chunks == 0) return e;
   const long long items = chunks * a.vheads;
   const int blocks = (int)(items < sm_count() ? items : sm_count());
-  kern<<<blocks, kGradThreads, grad_smem(DK, Terms<T>::value), st>>>(
-      a, g, plan, kq, back, states, dstates, es, fs, os, scales, status);
+  const bool partial = a.vheads > a.kheads;
+  kern<<<blocks, kGradThreads, smem, st>>>(a, g, plan, kq, back, states, dstates, es, fs, os,
+                                           scales, partial, status);
   e = cudaGetLastError();
-  if (e != cudaSuccess || !PARTIAL) return e;
-  delta_grad_sum_kernel<T, DK>
-      <<<dim3((unsigned)(chunks * a.kheads), 2), 256, 0, st>>>(
+  if (e != cudaSuccess || !partial) return e;
+  delta_grad_sum_kernel<T, DK><<<dim3((unsigned)(chunks * a.kheads), 2), 256, 0, st>>>(
       a, g, plan, reinterpret_cast<const float *>(es), reinterpret_cast<const float *>(fs));
   return cudaGetLastError();
 }
@@ -143,7 +144,7 @@ cudaError_t delta_backward_t(const DeltaArgs &a, const DeltaGradArgs &g, char *w
   if (e == cudaSuccess)
     e = delta_back<T, DK>(a, g, plan, kq, back, dstates, fs, os, scales, status, st);
   if (e != cudaSuccess) return e;
-  auto grad = a.vheads == a.kheads ? delta_grad_t<T, DK, false> : delta_grad_t<T, DK, true>;
+  auto grad = a.dv <= 128 ? delta_grad_t<T, DK, false> : delta_grad_t<T, DK, true>;
   return grad(a, g, plan, kq, back, states, dstates, es, fs, os, scales, status, st);
 }
 
