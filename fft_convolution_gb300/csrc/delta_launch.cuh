@@ -42,28 +42,17 @@ template <typename T> bool delta_staged(const DeltaArgs &a, const void *in, cons
   return sizeof(T) == 2 && a.dv % 8 == 0 && vec_rows<T>(in, s) && ((uintptr_t)out & 15u) == 0;
 }
 
-template <typename T, int DK, bool SAVE, bool STAGED>
+template <typename T, int DK, bool STAGED>
 cudaError_t delta_scan_t(const DeltaArgs &a, const DeltaPlan &plan, const char *kq,
-                         const char *images, char *states, char *es, float *scales,
-                         int *status, cudaStream_t st) {
+                         const char *images, int *status, cudaStream_t st) {
   constexpr size_t smem = scan_smem(DK, Terms<T>::value, STAGED);
   static DeviceOnce once;
-  auto kern = delta_scan_kernel<T, DK, SAVE, STAGED>;
+  auto kern = delta_scan_kernel<T, DK, STAGED>;
   cudaError_t e = smem_limit_once((const void *)kern, smem, once);
   if (e != cudaSuccess) return e;
   const long long blocks = a.batch * a.vheads * ((a.dv + 127) / 128);
-  kern<<<(unsigned)blocks, kScanThreads, smem, st>>>(a, plan, kq, images, states, es, scales, status);
+  kern<<<(unsigned)blocks, kScanThreads, smem, st>>>(a, plan, kq, images, status);
   return cudaGetLastError();
-}
-template <typename T, int DK, bool SAVE>
-cudaError_t delta_scan(const DeltaArgs &a, const DeltaPlan &plan, const char *kq,
-                       const char *images, char *states, char *es, float *scales,
-                       int *status, cudaStream_t st) {
-  if constexpr (sizeof(T) == 2)
-    if (delta_staged<T>(a, a.v, a.sv, a.o))
-      return delta_scan_t<T, DK, SAVE, true>(a, plan, kq, images, states, es, scales, status,
-                                             st);
-  return delta_scan_t<T, DK, SAVE, false>(a, plan, kq, images, states, es, scales, status, st);
 }
 
 template <typename T, int DK>
@@ -74,34 +63,31 @@ cudaError_t delta_forward_t(const DeltaArgs &a, char *ws, cudaStream_t st) {
   DeltaPlan plan;
   cudaError_t e = delta_make_plan<T>(a, w, ws, plan, st);
   if (e == cudaSuccess) e = delta_prep_t<T, DK, false>(a, plan, ws + w.kq, ws + w.images, nullptr, status, st);
-  if (e == cudaSuccess)
-    e = delta_scan<T, DK, false>(a, plan, ws + w.kq, ws + w.images, nullptr, nullptr, nullptr, status,
-                                st);
-  return e;
+  if (e != cudaSuccess) return e;
+  if constexpr (sizeof(T) == 2)
+    if (delta_staged<T>(a, a.v, a.sv, a.o))
+      return delta_scan_t<T, DK, true>(a, plan, ws + w.kq, ws + w.images, status, st);
+  return delta_scan_t<T, DK, false>(a, plan, ws + w.kq, ws + w.images, status, st);
 }
 
 template <typename T, int DK, bool STAGED>
-cudaError_t delta_back_t(const DeltaArgs &a, const DeltaGradArgs &g, const DeltaPlan &plan,
-                         const char *kq, const char *images, char *dstates, char *fs, char *os,
-                         float *scales, int *status, cudaStream_t st) {
+cudaError_t delta_scans_t(const DeltaArgs &a, const DeltaGradArgs &g, const DeltaPlan &plan,
+                          const char *kq, const char *images, const char *back, char *states,
+                          char *dstates, char *es, char *fs, char *os, float *scales, int *status,
+                          cudaStream_t st) {
   constexpr size_t smem = scan_smem(DK, Terms<T>::value, STAGED);
   static DeviceOnce once;
-  auto kern = delta_back_kernel<T, DK, STAGED>;
+  auto kern = delta_scans_kernel<T, DK, STAGED>;
   cudaError_t e = smem_limit_once((const void *)kern, smem, once);
   if (e != cudaSuccess) return e;
-  const long long blocks = a.batch * a.vheads * ((a.dv + 127) / 128);
-  kern<<<(unsigned)blocks, kScanThreads, smem, st>>>(a, g, plan, kq, images, dstates, fs, os, scales,
-                                                       status);
+  const long long blocks = 2 * a.batch * a.vheads * ((a.dv + 127) / 128);
+  kern<<<(unsigned)blocks, kScanThreads, smem, st>>>(a, g, plan, kq, images, back, states, dstates,
+                                                     es, fs, os, scales, status);
   return cudaGetLastError();
 }
-template <typename T, int DK>
-cudaError_t delta_back(const DeltaArgs &a, const DeltaGradArgs &g, const DeltaPlan &plan,
-                       const char *kq, const char *images, char *dstates, char *fs, char *os,
-                       float *scales, int *status, cudaStream_t st) {
-  if constexpr (sizeof(T) == 2)
-    if (a.dv % 8 == 0 && (((uintptr_t)g.dout | (uintptr_t)g.dv) & 15u) == 0)
-      return delta_back_t<T, DK, true>(a, g, plan, kq, images, dstates, fs, os, scales, status, st);
-  return delta_back_t<T, DK, false>(a, g, plan, kq, images, dstates, fs, os, scales, status, st);
+template <typename T> bool delta_scans_staged(const DeltaArgs &a, const DeltaGradArgs &g) {
+  return delta_staged<T>(a, a.v, a.sv, a.o) &&
+         (((uintptr_t)g.dout | (uintptr_t)g.dv) & 15u) == 0;
 }
 
 template <typename T, int DK, bool MULTI>
@@ -139,10 +125,11 @@ cudaError_t delta_backward_t(const DeltaArgs &a, const DeltaGradArgs &g, char *w
   DeltaPlan plan;
   cudaError_t e = delta_make_plan<T>(a, w, ws, plan, st);
   if (e == cudaSuccess) e = delta_prep_t<T, DK, true>(a, plan, kq, images, back, status, st);
-  if (e == cudaSuccess)
-    e = delta_scan<T, DK, true>(a, plan, kq, images, states, es, scales, status, st);
-  if (e == cudaSuccess)
-    e = delta_back<T, DK>(a, g, plan, kq, back, dstates, fs, os, scales, status, st);
+  if (e != cudaSuccess) return e;
+  auto scans = delta_scans_t<T, DK, false>;
+  if constexpr (sizeof(T) == 2)
+    if (delta_scans_staged<T>(a, g)) scans = delta_scans_t<T, DK, true>;
+  e = scans(a, g, plan, kq, images, back, states, dstates, es, fs, os, scales, status, st);
   if (e != cudaSuccess) return e;
   auto grad = a.dv <= 128 ? delta_grad_t<T, DK, false> : delta_grad_t<T, DK, true>;
   return grad(a, g, plan, kq, back, states, dstates, es, fs, os, scales, status, st);

@@ -407,9 +407,9 @@ __device__ __forceinline__ uint32_t scan_begin(ScanBars &bars, uint32_t *slot, v
 // STAGED: V comes and O goes through shared memory by bulk copies of rows
 // (16-bit types on 16-byte boundaries); else straight from and to HBM.
 template <typename T, int DK, bool SAVE, bool STAGED>
-__global__ void __launch_bounds__(kScanThreads, 1)
-delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const char *images,
-                  char *states, char *es, float *scales, int *status) {
+__device__ __forceinline__ void delta_scan(const DeltaArgs &a, const DeltaPlan &plan, unsigned block,
+                                           const char *kq, const char *images, char *states,
+                                           char *es, float *scales, int *status) {
   extern __shared__ char smem_raw[];
   __shared__ ScanBars bars;
   __shared__ uint32_t tmem_slot;
@@ -423,9 +423,9 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
   constexpr bool LEAD = std::is_same<T, __nv_bfloat16>::value;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int blocks_v = (a.dv + 127) / 128;
-  const int vb = blockIdx.x % blocks_v;
-  const int h = (blockIdx.x / blocks_v) % a.vheads;
-  const ScanSpan sp = scan_span(a, plan, blockIdx.x / blocks_v / a.vheads);
+  const int vb = block % blocks_v;
+  const int h = (block / blocks_v) % a.vheads;
+  const ScanSpan sp = scan_span(a, plan, block / blocks_v / a.vheads);
   char *stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   if (SAVE && tid < 4 * kTops) bounds.top[tid / kTops][tid % kTops] = 0;
   const uint32_t tm = scan_begin(bars, &tmem_slot, &failed, STAGED, tid, warp);
@@ -734,6 +734,14 @@ delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const
   tc_fence_before();
   __syncthreads();
   if (warp == kScanWarps) tmem_free(tm, 512);
+}
+
+template <typename T, int DK, bool STAGED>
+__global__ void __launch_bounds__(kScanThreads, 1)
+delta_scan_kernel(const DeltaArgs a, const DeltaPlan plan, const char *kq, const char *images,
+                  int *status) {
+  delta_scan<T, DK, false, STAGED>(a, plan, blockIdx.x, kq, images, nullptr, nullptr, nullptr,
+                                   status);
 }
 
 }  // namespace fftgb

@@ -106,10 +106,10 @@ int delta_check(const fft_delta_desc *d, int64_t max_dk, const void *q, const vo
   return FFT_OK;
 }
 
-// Grids of the kernels over all chunks.
+// Grids of the kernels over all chunks, and of the gradients' two scans.
 int delta_chunks_check(const DeltaArgs &a, bool packed) {
   const int64_t chunks = packed ? (a.tokens + 63 * a.batch) / 64 : a.batch * ((a.tokens + 63) / 64);
-  return chunks > 0x7fffffff / a.vheads ? FFT_ERR_UNSUPPORTED : FFT_OK;
+  return chunks > 0x3fffffff / a.vheads ? FFT_ERR_UNSUPPORTED : FFT_OK;
 }
 
 }  // namespace
