@@ -581,9 +581,10 @@ int fft_delta_rule(const fft_delta_desc *desc, const void *q, const void *k, con
  *   dfinal_state, dinitial_state  float [batch][vheads][dk][dv]; dinitial_state
  *                  may be NULL, and may be dfinal_state.
  *   workspace      fft_delta_rule_backward_workspace_bytes(desc, offsets !=
- *                  NULL) bytes: about 130 KB per 64 tokens and value head of
- *                  128 x 128 for the states, twice that with their gradients
- *                  and the rest.
+ *                  NULL) bytes: about 310 KB per 64 tokens and value head of
+ *                  128 x 128 (330 KB in float), of which 208 are the states,
+ *                  their gradients and what else the last pass reads.
+ * No output overlaps an input or another output except as said.
  */
 size_t fft_delta_rule_backward_workspace_bytes(const fft_delta_desc *desc, int packed);
 int fft_delta_rule_backward(const fft_delta_desc *desc, const void *dout, const void *q,

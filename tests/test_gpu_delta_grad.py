@@ -194,3 +194,24 @@ def test_refusals(fg):
         fg.delta_rule_backward(v, q, k, v, g, beta, dfinal_state=torch.zeros(1, 4, 16, 15, device="cuda"))
     with pytest.raises(fg.FFTError):
         fg.delta_rule_backward(v[:, :, :3], q, k, v[:, :, :3], g[:, :, :3], beta[:, :, :3])
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_columns_of_different_size(fg, kind):
+    # one scale holds all columns of a head's state: what is small beside the
+    # largest is small in every sum over columns too
+    q, k, v, g, beta = ref.inputs(31, 1, 200, 1, 2, 64, 96, torch.float32)
+    v = v * 2.0 ** -(torch.arange(96) % 13).float()
+    check(fg, (q.to(TYPES[kind]), k.to(TYPES[kind]), v.to(TYPES[kind]), g, beta), 32)
+
+
+@pytest.mark.parametrize("kind,tokens,heads,dv", [("f32", 150, 2, 256), ("f32", 3000, 4, 128), ("bf16", 6000, 4, 128),
+                                                  ("bf16", 700, 2, 520)])
+def test_same_bits_again(fg, kind, tokens, heads, dv):
+    args = cuda(ref.inputs(33, 1, tokens, heads, heads, 128, dv, TYPES[kind]))
+    do = normal(34, 1, tokens, heads, dv).to(TYPES[kind]).cuda()
+    first = fg.delta_rule_backward(do, *args)
+    for _ in range(30):
+        for a, b in zip(fg.delta_rule_backward(do, *args), first):
+            assert torch.equal(a, b)
+    assert fg.fft_device_status(None) == fg.FFT_OK
