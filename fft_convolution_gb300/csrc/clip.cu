@@ -9,6 +9,10 @@
 // read twice unless they fit the L2: the second kernel walks the tensors
 // from their end, where the first one has just been.
 //
+// HBM bounds both: 600 million bf16 values in 291 tensors take 175 us to square
+// (6.9 TB/s) and 465 to scale (5.2 TB/s); 61 small tensors are two launches of
+// 5 us behind the host's 18.
+//
 // The tensors' addresses and sizes travel in the kernels' arguments: no
 // table has to be copied to the device, and the calls can be captured.
 #include "seq.h"

@@ -20,8 +20,8 @@
 //
 // Kernels: delta_prep (all chunks in parallel: the triangular inverse and M),
 // delta_scan (one block per sequence, head and 128 columns of v walks the
-// chunks with the state in tensor memory), and for gradients the same scan
-// backwards and one more kernel over all chunks.
+// chunks, the state in registers), and for gradients the same scan backwards in
+// the same launch and one more kernel over all chunks.
 //
 // Precision: products run on the tensor cores in fp16 with fp32
 // accumulators.  A row of an operand is first scaled by a power of two that
@@ -31,8 +31,9 @@
 // sum of two fp16 values, of which the products leading x leading, leading x
 // trailing and trailing x leading are taken.  22 significand bits count that
 // way, at two to three times the products: results in fp32 are as good as
-// fp32 arithmetic's (the error of a test of 256 tokens is 3e-7; with pairs of
-// bf16, which need no scaling, it was 6e-6, with single bf16 values 2e-3).
+// fp32 arithmetic's (8192 tokens: the final state 2.3e-7 off, the gradients of
+// 16384 tokens 3e-7 to 8e-7; with pairs of bf16, which need no scaling, a test
+// of 256 tokens was 6e-6 off, with single bf16 values 2e-3).
 #pragma once
 
 #include "seq.h"

@@ -36,7 +36,7 @@ template <int N, typename T> __device__ __forceinline__ void load_whole(const T 
 }
 
 // VEC: the state goes by 16 bytes.  FULL: so do k, q and v, and all 16 R rows
-// are there.  (One token of 64 sequences with 32 heads of 128 x 128: with
+// are there.  (One token of 128 sequences with 32 heads of 128 x 128: with
 // elements of k and q loaded one by one 134 us, FULL 84: 95% of the copy rate;
 // 5, 6 or 7 blocks per SM make 87, 84 and 84 us.)
 template <typename T, int R, bool VEC, bool FULL>

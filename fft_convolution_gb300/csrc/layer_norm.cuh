@@ -266,16 +266,18 @@ layer_norm_kernel(const LayerNormArgs a) {
   }
 }
 
-// Rows that a warp holds whole (NV 16-byte words
-// per lane): no barrier at all, and with 16 warps per multiprocessor 128 KB of
-// rows under way.  w and b lie in shared memory in fp32.  (A block per row
-// waits for its barrier most of the time: 70 us against 49 for 16384 x 4096
-// bf16.)
-template <typename T, int NV>
+// Rows that W = 1 or 2 warps hold whole (NV 16-byte words per lane): no barrier
+// at all, or one between two warps; with 16 warps per multiprocessor up to 128
+// KB of rows under way.  w and b lie in shared memory in fp32.  16384 x 4096
+// bf16: two warps per row 51 us, 78% of the copy rate; one warp with 16 words
+// per lane spills, 60; a block per row waits for its barrier most of the time,
+// 70; rows copied ahead to shared memory change nothing.
+template <typename T, int NV, int W>
 __global__ void __launch_bounds__(256, 2) layer_norm_warp_kernel(const LayerNormArgs a) {
   extern __shared__ float wb[];  // w, then b
+  __shared__ float2 red[2][8];
   constexpr int N = Vec16<T>::N;
-  const int lane = threadIdx.x & 31;
+  const int t = threadIdx.x % (32 * W), warp = threadIdx.x >> 5;
   float *ws = wb, *bs = wb + a.dim;
   for (int c = threadIdx.x; c < a.dim; c += 256) {
     ws[c] = a.w ? load_any(a.w, a.wtype, c) : 1.0f;
@@ -283,14 +285,21 @@ __global__ void __launch_bounds__(256, 2) layer_norm_warp_kernel(const LayerNorm
   }
   __syncthreads();
   const float inv = 1.0f / (float)a.dim;
-  const long long step = (long long)gridDim.x * 8;
-  for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < a.rows; row += step) {
+  // elements of a row that this warp has
+  float mine = (float)a.dim;
+  if constexpr (W > 1) {
+    const int words = (int)(a.dim / N), rounds = words / (32 * W), rest = words % (32 * W) - (t & ~31);
+    mine = (float)((rounds * 32 + (rest < 0 ? 0 : rest > 32 ? 32 : rest)) * N);
+  }
+  int turn = 0;
+  const long long step = (long long)gridDim.x * (8 / W);
+  for (long long row = (long long)blockIdx.x * (8 / W) + warp / W; row < a.rows; row += step) {
     const T *x = static_cast<const T *>(a.x) + row * a.ldx;
     T *y = static_cast<T *>(a.y) + row * a.ldy;
     uint4 raw[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (k * 32 + lane) * N;
+      const int c = (k * 32 * W + t) * N;
       raw[k] = c < a.dim ? __ldcs(reinterpret_cast<const uint4 *>(x + c)) : make_uint4(0, 0, 0, 0);
     }
     // Three walks over the registers, two values per instruction.
@@ -305,13 +314,13 @@ __global__ void __launch_bounds__(256, 2) layer_norm_warp_kernel(const LayerNorm
     s.x += s.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
-    const float mu = s.x * inv;
+    float mu = W == 1 ? s.x * inv : mine > 0.0f ? s.x / mine : 0.0f;
     s = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       float f[N];
       unpack<T>(raw[k], f);
-      if ((k * 32 + lane) * N < a.dim) {
+      if ((k * 32 * W + t) * N < a.dim) {
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
           const float2 d = fma2(both(-mu), both(1.0f), make_float2(f[i], f[i + 1]));
@@ -322,10 +331,21 @@ __global__ void __launch_bounds__(256, 2) layer_norm_warp_kernel(const LayerNorm
     s.x += s.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+    if constexpr (W > 1) {
+      // both warps' squares about their own means, joined (row_moments)
+      const float own = mu, n = mine, m = (float)a.dim - mine;
+      if ((t & 31) == 0) red[turn][warp] = make_float2(own, s.x);
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + warp / 2) : "memory");
+      const float2 o = red[turn][warp ^ 1];
+      turn ^= 1;
+      mu = (own * n + o.x * m) * inv;
+      const float d = own - mu, e = o.x - mu;
+      s.x = (s.x + o.y) + (n * d * d + m * e * e);
+    }
     const float r = 1.0f / sqrtf(s.x * inv + (float)a.eps);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (k * 32 + lane) * N;
+      const int c = (k * 32 * W + t) * N;
       if (c < a.dim) {
         float f[N];
         unpack<T>(raw[k], f);
@@ -346,18 +366,21 @@ __global__ void __launch_bounds__(256, 2) layer_norm_warp_kernel(const LayerNorm
         *reinterpret_cast<uint4 *>(y + c) = pack<T>(f);
       }
     }
-    if (lane == 0) {
+    if (t == 0) {
       if (a.mean) static_cast<float *>(a.mean)[row] = mu;
       if (a.rstd) static_cast<float *>(a.rstd)[row] = r;
     }
   }
 }
-template <typename T, int NV = 1>
+template <typename T, int NV = 1, int W = 1>
 cudaError_t layer_norm_warp(const LayerNormArgs &a, cudaStream_t st) {
-  if constexpr (NV < 16)
-    if (a.dim > NV * 32 * Vec16<T>::N) return layer_norm_warp<T, 2 * NV>(a, st);
-  const long long blocks = (a.rows + 7) / 8, most = 2ll * sm_count();
-  layer_norm_warp_kernel<T, NV>
+  if constexpr (NV < 8) {
+    if (a.dim > NV * 32 * Vec16<T>::N) return layer_norm_warp<T, 2 * NV, 1>(a, st);
+  } else if constexpr (W == 1) {
+    if (a.dim > NV * 32 * Vec16<T>::N) return layer_norm_warp<T, NV, 2>(a, st);
+  }
+  const long long blocks = (a.rows * W + 7) / 8, most = 2ll * sm_count();
+  layer_norm_warp_kernel<T, NV, W>
       <<<(int)(blocks < most ? blocks : most), 256, 2 * a.dim * sizeof(float), st>>>(a);
   return cudaGetLastError();
 }
@@ -374,12 +397,15 @@ layer_norm_grad_kernel(const LayerNormGradArgs a) {
   const float *mean = static_cast<const float *>(a.mean);
   const float *rstd = static_cast<const float *>(a.rstd);
   T *dx = static_cast<T *>(a.dx);
-  float w[EPT], dw[EPT], db[EPT];
+  // Two elements per instruction: the fp32 rows of 3001 elements, without vector
+  // loads, went from 42 to 39 us.
+  constexpr int PAIRS = EPT / 2;
+  float2 w[PAIRS], dw[PAIRS], db[PAIRS];
 #pragma unroll
-  for (int e = 0; e < EPT; ++e) {
-    const int c = column<T, TPR, VEC>(t, e);
-    w[e] = a.w && c < a.dim ? load_any(a.w, a.wtype, c) : 1.0f;
-    dw[e] = db[e] = 0.0f;
+  for (int e = 0; e < PAIRS; ++e) {
+    auto weight = [&](int c) { return a.w && c < a.dim ? load_any(a.w, a.wtype, c) : 1.0f; };
+    w[e] = make_float2(weight(column<T, TPR, VEC>(t, 2 * e)), weight(column<T, TPR, VEC>(t, 2 * e + 1)));
+    dw[e] = db[e] = make_float2(0.0f, 0.0f);
   }
   constexpr int ROWS = VEC && sizeof(T) == 2 ? 2 : 1;
   const float inv = 1.0f / (float)a.dim;
@@ -405,20 +431,25 @@ layer_norm_grad_kernel(const LayerNormGradArgs a) {
     for (int k = 0; k < ROWS; ++k) load(k, row + k * step);
   }
   for (; row < a.rows; row += ROWS * step) {
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float s[4];
+    const float2 one = both(1.0f);
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
       float xh[EPT], g[EPT];
       xb[k].get(xh);
       gb[k].get(g);
+      float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) {
-        const float h = (xh[e] - mu[k]) * r[k];  // (g is 0 beyond the row)
-        dw[e] = fmaf(g[e], h, dw[e]);
-        db[e] += g[e];
-        s[2 * k] = fmaf(g[e], w[e], s[2 * k]);
-        s[2 * k + 1] = fmaf(g[e] * w[e], h, s[2 * k + 1]);
+      for (int e = 0; e < PAIRS; ++e) {
+        const float2 d = make_float2(g[2 * e], g[2 * e + 1]);  // (0 beyond the row)
+        const float2 h = mul2(fma2(both(-mu[k]), one, make_float2(xh[2 * e], xh[2 * e + 1])), both(r[k]));
+        dw[e] = fma2(d, h, dw[e]);
+        db[e] = fma2(d, one, db[e]);
+        s1 = fma2(d, w[e], s1);
+        s2 = fma2(mul2(d, w[e]), h, s2);
       }
+      s[2 * k] = s1.x + s1.y;
+      s[2 * k + 1] = s2.x + s2.y;
     }
     if (dx) {
       float m1[2], m2[2];
@@ -440,8 +471,13 @@ layer_norm_grad_kernel(const LayerNormGradArgs a) {
           xb[k].get(xh);
           gb[k].get(g);
 #pragma unroll
-          for (int e = 0; e < EPT; ++e)
-            g[e] = r[k] * (g[e] * w[e] - m1[k] - (xh[e] - mu[k]) * r[k] * m2[k]);
+          for (int e = 0; e < PAIRS; ++e) {
+            const float2 d = make_float2(g[2 * e], g[2 * e + 1]);
+            const float2 h = mul2(fma2(both(-mu[k]), one, make_float2(xh[2 * e], xh[2 * e + 1])), both(r[k]));
+            const float2 o = mul2(fma2(h, both(-m2[k]), fma2(d, w[e], both(-m1[k]))), both(r[k]));
+            g[2 * e] = o.x;
+            g[2 * e + 1] = o.y;
+          }
           RowRegs<T, TPR, EPT, VEC>::store(dx + (row + k * step) * a.lddx, g, t, a.dim);
         }
         load(k, row + (k + ROWS) * step);
@@ -460,8 +496,8 @@ layer_norm_grad_kernel(const LayerNormGradArgs a) {
   for (int e = 0; e < EPT; ++e) {
     const int c = column<T, TPR, VEC>(t, e);
     if (c < a.dim) {
-      pw[at + c] = dw[e];
-      pb[at + c] = db[e];
+      pw[at + c] = e & 1 ? dw[e / 2].y : dw[e / 2].x;
+      pb[at + c] = e & 1 ? db[e / 2].y : db[e / 2].x;
     }
   }
 }
@@ -579,7 +615,10 @@ layer_norm_sum_kernel(const A *partial, int parts, int dim, void *dw, void *db, 
 // up to 512 elements (no barrier), blocks of 128 to 1024 threads with 8
 // elements each up to 8192; longer rows and fp64 by the looping kernels.  Few
 // elements per thread leave room for many warps, which hide the barrier of a
-// row's reduction (16 per thread, 256 threads: 90 us for 16384 x 4096 bf16).
+// row's reduction (16 per thread, 256 threads: 90 us for 16384 x 4096 bf16
+// forwards).  The gradients of that size take 102 us, 58% of the copy rate, the
+// sum of the partial rows 7: the two blocks of an SM wait at their barriers
+// (one per two rows) and for the rows behind them, issuing half of the time.
 constexpr int kNormRegMax = 8192;
 inline int norm_tpr(int dim) {
   return dim <= 512 ? 32 : dim <= 1024 ? 128 : dim <= 2048 ? 256 : dim <= 4096 ? 512 : 1024;
