@@ -107,28 +107,39 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float2 *red, int &t
   }
   return make_float2(a, b);
 }
-// The same of two rows.
+// The same of two rows.  Lanes halve the values they carry at each step (one of
+// four is left after two), then each sums one of them over the warps.
 template <int TPR>
 __device__ __forceinline__ float4 row_sum4(float4 v, float4 *red, int &turn) {
-  auto add = [](float4 a, int o) {
-    a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
-    a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
-    a.z += __shfl_xor_sync(0xffffffffu, a.z, o);
-    a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
-    return a;
+  const int lane = threadIdx.x & 31;
+  const bool b4 = lane & 16, b3 = lane & 8;
+  auto trade = [](float keep, float give, int o) {
+    return keep + __shfl_xor_sync(0xffffffffu, give, o);
   };
+  const float x = trade(b4 ? v.z : v.x, b4 ? v.x : v.z, 16);
+  const float y = trade(b4 ? v.w : v.y, b4 ? v.y : v.w, 16);
+  float s = trade(b3 ? y : x, b3 ? x : y, 8);  // value 2 b4 + b3
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = add(v, o);
+  for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  int from = 8;  // lanes from one value to the next
   if constexpr (TPR > 32) {
     constexpr int W = TPR / 32;
-    float4 *r = red + turn * W;
-    if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
+    float *r = reinterpret_cast<float *>(red + turn * W);
+    if ((lane & 7) == 0) r[(threadIdx.x >> 5) * 4 + (lane >> 3)] = s;
     __syncthreads();
-    v = r[threadIdx.x & (W - 1)];
+    s = 0.0f;
 #pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) v = add(v, o);
+    for (int k = 0; k < 4 * W; k += 32)
+      if (k + lane < 4 * W) s += r[k + lane];
+#pragma unroll
+    for (int o = 4; o < (4 * W < 32 ? 4 * W : 32); o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     turn ^= 1;
+    from = 1;
   }
+  v.x = __shfl_sync(0xffffffffu, s, 0);
+  v.y = __shfl_sync(0xffffffffu, s, from);
+  v.z = __shfl_sync(0xffffffffu, s, 2 * from);
+  v.w = __shfl_sync(0xffffffffu, s, 3 * from);
   return v;
 }
 
@@ -267,11 +278,11 @@ layer_norm_kernel(const LayerNormArgs a) {
 }
 
 // Rows that W = 1 or 2 warps hold whole (NV 16-byte words per lane): no barrier
-// at all, or one between two warps; with 16 warps per multiprocessor up to 128
-// KB of rows under way.  w and b lie in shared memory in fp32.  16384 x 4096
-// bf16: two warps per row 51 us, 78% of the copy rate; one warp with 16 words
-// per lane spills, 60; a block per row waits for its barrier most of the time,
-// 70; rows copied ahead to shared memory change nothing.
+// at all, or one between two warps.  While a row is worked on, each lane copies
+// its words of the next one to shared memory, where nobody else reads them.  w
+// and b lie there in fp32.  16384 x 4096 bf16: two warps per row 46 us, 87% of
+// the copy rate (51 without the copies ahead); one warp with 16 words per lane
+// spills, 60; a block per row waits for its barrier most of the time, 70.
 template <typename T, int NV, int W>
 __global__ void __launch_bounds__(256, 2) layer_norm_warp_kernel(const LayerNormArgs a) {
   extern __shared__ float wb[];  // w, then b
@@ -293,15 +304,23 @@ __global__ void __launch_bounds__(256, 2) layer_norm_warp_kernel(const LayerNorm
   }
   int turn = 0;
   const long long step = (long long)gridDim.x * (8 / W);
-  for (long long row = (long long)blockIdx.x * (8 / W) + warp / W; row < a.rows; row += step) {
-    const T *x = static_cast<const T *>(a.x) + row * a.ldx;
+  // The next row's words, each lane its own.
+  uint4 *mine_words = reinterpret_cast<uint4 *>(wb + 2 * a.dim) + threadIdx.x;
+  auto fetch = [&](long long row) {
+    const T *x = static_cast<const T *>(a.x) + row * a.ldx + t * N;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if ((k * 32 * W + t) * N < a.dim) copy16(smem_u32(mine_words + k * 256), x + k * 32 * W * N);
+  };
+  long long row = (long long)blockIdx.x * (8 / W) + warp / W;
+  if (row < a.rows) fetch(row);
+  for (; row < a.rows; row += step) {
     T *y = static_cast<T *>(a.y) + row * a.ldy;
     uint4 raw[NV];
+    copy_wait_all();
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = (k * 32 * W + t) * N;
-      raw[k] = c < a.dim ? __ldcs(reinterpret_cast<const uint4 *>(x + c)) : make_uint4(0, 0, 0, 0);
-    }
+    for (int k = 0; k < NV; ++k)
+      raw[k] = (k * 32 * W + t) * N < a.dim ? mine_words[k * 256] : make_uint4(0, 0, 0, 0);
     // Three walks over the registers, two values per instruction.
     float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -315,6 +334,7 @@ __global__ void __launch_bounds__(256, 2) layer_norm_warp_kernel(const LayerNorm
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
     float mu = W == 1 ? s.x * inv : mine > 0.0f ? s.x / mine : 0.0f;
+    if (row + step < a.rows) fetch(row + step);  // (every word has been used)
     s = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -380,9 +400,25 @@ cudaError_t layer_norm_warp(const LayerNormArgs &a, cudaStream_t st) {
     if (a.dim > NV * 32 * Vec16<T>::N) return layer_norm_warp<T, NV, 2>(a, st);
   }
   const long long blocks = (a.rows * W + 7) / 8, most = 2ll * sm_count();
-  layer_norm_warp_kernel<T, NV, W>
-      <<<(int)(blocks < most ? blocks : most), 256, 2 * a.dim * sizeof(float), st>>>(a);
+  constexpr size_t words = 256 * NV * 16;
+  static DeviceOnce once;
+  const cudaError_t e = smem_limit_once((const void *)layer_norm_warp_kernel<T, NV, W>,
+                                        words + 2 * W * NV * 32 * Vec16<T>::N * sizeof(float), once);
+  if (e != cudaSuccess) return e;
+  layer_norm_warp_kernel<T, NV, W><<<(int)(blocks < most ? blocks : most), 256,
+                                     words + 2 * a.dim * sizeof(float), st>>>(a);
   return cudaGetLastError();
+}
+
+// Rows shared by several warps, on 16-byte boundaries, are copied to shared
+// memory ahead: 64 bytes per thread and round, three rounds, 192 KB per SM
+// (16384 x 4096 bf16, loaded into registers for the next round only: 112 us; copied
+// 106; 16-bit rows read from there again for dx, which spares the registers that
+// spilled, 97; fewer shuffles in the rows' sums, 91).
+constexpr int kNormStages = 3, kNormRoundBytes = 64;
+template <int TPR, bool VEC> __host__ __device__ constexpr bool norm_ring() { return VEC && TPR > 32; }
+template <int TPR, bool VEC> constexpr size_t norm_grad_smem() {
+  return norm_ring<TPR, VEC>() ? (size_t)kNormStages * kNormRoundBytes * NormBlock<TPR>::THREADS : 0;
 }
 
 // 16-bit rows: two per round share one barrier (fp32 rows would not fit the
@@ -408,6 +444,7 @@ layer_norm_grad_kernel(const LayerNormGradArgs a) {
     dw[e] = db[e] = make_float2(0.0f, 0.0f);
   }
   constexpr int ROWS = VEC && sizeof(T) == 2 ? 2 : 1;
+  constexpr bool RING = norm_ring<TPR, VEC>();
   const float inv = 1.0f / (float)a.dim;
   int turn = 0;
   const long long step = (long long)gridDim.x * G;
@@ -426,11 +463,65 @@ layer_norm_grad_kernel(const LayerNormGradArgs a) {
       mu[k] = r[k] = 0.0f;  // a row that adds nothing
     }
   };
-  if (row < a.rows) {
+  // RING: a thread's words of the rows ahead, nobody else reads them.
+  constexpr int WORDS = VEC ? EPT / Vec16<T>::N : 1;
+  extern __shared__ uint4 norm_ring_words[];
+  uint4 *mine = norm_ring_words + threadIdx.x;
+  auto word = [&](int stage, int k, int which, int j) {
+    return mine + (((stage * ROWS + k) * 2 + which) * WORDS + j) * NormBlock<TPR>::THREADS;
+  };
+  auto fetch = [&](int stage, long long first) {
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const long long at = first + k * step;
+      if (at < a.rows)
+#pragma unroll
+        for (int j = 0; j < WORDS; ++j) {
+          const int c = (j * TPR + t) * Vec16<T>::N;
+          if (c < a.dim) {
+            copy16(smem_u32(word(stage, k, 0, j)), x + at * a.ldx + c);
+            copy16(smem_u32(word(stage, k, 1, j)), dy + at * a.lddy + c);
+          }
+        }
+    }
+    copy_group();
+  };
+  float next_mu[ROWS], next_r[ROWS];
+  auto moments = [&](int k, long long at) {
+    next_mu[k] = at < a.rows ? mean[at] : 0.0f;
+    next_r[k] = at < a.rows ? rstd[at] : 0.0f;
+  };
+  int stage = 0;
+  auto take = [&](int k) {
+    if constexpr (RING) {
+#pragma unroll
+      for (int j = 0; j < WORDS; ++j) {
+        const bool there = row + k * step < a.rows && (j * TPR + t) * Vec16<T>::N < a.dim;
+        xb[k].raw[j] = there ? *word(stage, k, 0, j) : make_uint4(0, 0, 0, 0);
+        gb[k].raw[j] = there ? *word(stage, k, 1, j) : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  if constexpr (RING) {
+#pragma unroll
+    for (int i = 0; i < kNormStages; ++i) fetch(i, row + i * ROWS * step);
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) moments(k, row + k * step);
+  } else if (row < a.rows) {
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) load(k, row + k * step);
   }
   for (; row < a.rows; row += ROWS * step) {
+    if constexpr (RING) {
+      copy_wait<kNormStages - 1>();
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) {
+        mu[k] = next_mu[k];
+        r[k] = next_r[k];
+        moments(k, row + (k + ROWS) * step);
+        take(k);
+      }
+    }
     float s[4];
     const float2 one = both(1.0f);
 #pragma unroll
@@ -468,6 +559,7 @@ layer_norm_grad_kernel(const LayerNormGradArgs a) {
       for (int k = 0; k < ROWS; ++k) {
         if (row + k * step < a.rows) {
           float xh[EPT], g[EPT];
+          if constexpr (ROWS == 2) take(k);  // (once more: kept over the barrier they spill)
           xb[k].get(xh);
           gb[k].get(g);
 #pragma unroll
@@ -480,13 +572,18 @@ layer_norm_grad_kernel(const LayerNormGradArgs a) {
           }
           RowRegs<T, TPR, EPT, VEC>::store(dx + (row + k * step) * a.lddx, g, t, a.dim);
         }
-        load(k, row + (k + ROWS) * step);
+        if constexpr (!RING) load(k, row + (k + ROWS) * step);
       }
-    } else {
+    } else if constexpr (!RING) {
 #pragma unroll
       for (int k = 0; k < ROWS; ++k) load(k, row + (k + ROWS) * step);
     }
+    if constexpr (RING) {
+      fetch(stage, row + kNormStages * ROWS * step);  // (every word has been used)
+      stage = stage + 1 < kNormStages ? stage + 1 : 0;
+    }
   }
+  if constexpr (RING) copy_wait_all();
   if (!a.partial) return;
   // One row of partial sums per row group: [2][gridDim.x * G][dim].
   float *pw = static_cast<float *>(a.partial);
@@ -616,9 +713,9 @@ layer_norm_sum_kernel(const A *partial, int parts, int dim, void *dw, void *db, 
 // elements each up to 8192; longer rows and fp64 by the looping kernels.  Few
 // elements per thread leave room for many warps, which hide the barrier of a
 // row's reduction (16 per thread, 256 threads: 90 us for 16384 x 4096 bf16
-// forwards).  The gradients of that size take 102 us, 58% of the copy rate, the
-// sum of the partial rows 7: the two blocks of an SM wait at their barriers
-// (one per two rows) and for the rows behind them, issuing half of the time.
+// forwards).  The gradients of that size take 83 us, 72% of the copy rate, and
+// the sum of the partial rows 7: 16-bit rows are bound by their arithmetic (twice
+// the elements per byte; fp32 rows reach 81%).
 constexpr int kNormRegMax = 8192;
 inline int norm_tpr(int dim) {
   return dim <= 512 ? 32 : dim <= 1024 ? 128 : dim <= 2048 ? 256 : dim <= 4096 ? 512 : 1024;
@@ -692,8 +789,14 @@ cudaError_t layer_norm_grad_t(const LayerNormGradArgs &a, cudaStream_t st) {
                        (!a.dx || norm_vec<T>(a.dx, a.lddx, a.dim));
       const int grid = (int)norm_grid(a.rows, a.dim);
       e = norm_dispatch<T>(a.dim, vec, [&](auto tpr, auto ept, auto v) {
-        layer_norm_grad_kernel<T, tpr.value, ept.value, v.value>
-            <<<grid, NormBlock<tpr.value>::THREADS, 0, st>>>(a);
+        constexpr size_t smem = norm_grad_smem<tpr.value, v.value>();
+        auto kern = layer_norm_grad_kernel<T, tpr.value, ept.value, v.value>;
+        if constexpr (smem > 0) {
+          static DeviceOnce once;
+          const cudaError_t limit = smem_limit_once((const void *)kern, smem, once);
+          if (limit != cudaSuccess) return limit;
+        }
+        kern<<<grid, NormBlock<tpr.value>::THREADS, smem, st>>>(a);
         return cudaGetLastError();
       });
       done = true;

@@ -82,6 +82,11 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
 __device__ __forceinline__ void copy_arrive(uint64_t *bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// This thread's copies so far as a group; waits until at most N groups are under way.
+__device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Makes this thread's writes to shared memory visible to the tensor cores.
 __device__ __forceinline__ void fence_smem_to_async() {
