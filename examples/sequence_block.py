@@ -2,7 +2,7 @@
 causal convolution along time, the gated delta rule; trained with clipped
 gradients, then run one token at a time from its states.
 
-    python examples/sequence_block.py [--steps 120] [--tokens 128]
+    python examples/sequence_block.py [--steps 120] [--tokens 64]
 
 The task is recall: a sequence of (key, value) token pairs, then keys whose
 values have to be answered.  Prints the loss on the way and how far the
@@ -124,7 +124,7 @@ def recall_batch(gen, batch, pairs, symbols):
     return torch.cat([torch.stack([keys, values], -1).flatten(1), again], 1).cuda(), 2 * pairs
 
 
-def train(steps: int = 120, tokens: int = 128, batch: int = 16, width: int = 128, heads: int = 2,
+def train(steps: int = 120, tokens: int = 64, batch: int = 16, width: int = 128, heads: int = 2,
           lr: float = 0.01, report=print):
     gen = torch.Generator().manual_seed(1)
     pairs, symbols = tokens // 4, 128
@@ -164,7 +164,7 @@ def decode_error(block, tokens: int = 96, batch: int = 3):
 if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--steps", type=int, default=120)
-    ap.add_argument("--tokens", type=int, default=128)
+    ap.add_argument("--tokens", type=int, default=64)
     args = ap.parse_args()
     trained, _ = train(args.steps, args.tokens)
     print(f"one token at a time: logits off by {decode_error(trained):.1e}")
