@@ -64,21 +64,21 @@ __device__ __forceinline__ void delta_back(const DeltaArgs &a, const DeltaGradAr
       if (!wait(&bars.full[s], (it / ST) & 1) || !wait(&bars.sb, ph)) break;
       tc_fence_after();
       if (elect_one()) {
-        mma_state<DK, NT, false>(tm + kColP, tm + kColSh, tm + kColSl, k);
+        mma_state<DK, NT>(tm + kColP, tm + kColSh, tm + kColSl, k);
         mma_commit(&bars.p);
       }
       __syncwarp();
       if (!wait(&bars.of, ph)) break;  // dO is there
       tc_fence_after();
       if (elect_one()) {
-        mma_inner<false, NT == 1>(tm + kColN, tm + kColWh, tm + kColWl, image + 2 * kTile, false);
+        mma_inner<NT == 1>(tm + kColN, tm + kColWh, tm + kColWl, image + 2 * kTile, false);
         mma_commit(&bars.n);
       }
       __syncwarp();
       if (!wait(&bars.y, ph)) break;
       tc_fence_after();
       if (elect_one()) {
-        mma_inner<false>(tm + kColP, tm + kColYh, tm + kColYl, image, false);
+        mma_inner<>(tm + kColP, tm + kColYh, tm + kColYl, image, false);
         mma_commit(&bars.e);
       }
       __syncwarp();

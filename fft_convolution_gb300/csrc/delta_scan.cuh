@@ -239,32 +239,32 @@ constexpr uint32_t idesc_tokens = mma_desc(128, 64, false, false);
 // tokens: 7.7e-7 off, with the leading parts first 1.9e-6).
 
 // S^T X^T into `d` (64 columns): left operand the state's two parts, right
-// one the chunk's X (K or Q).  LEAD: leading parts only.
-template <int DK, int NT, bool LEAD>
+// one the chunk's X (K or Q).
+template <int DK, int NT>
 __device__ __forceinline__ void mma_state(uint32_t d, uint32_t hi, uint32_t lo, uint32_t x) {
   constexpr uint32_t kPlane = 2 * (DK / 64) * kTile;
 #pragma unroll
-  for (int term = LEAD ? 0 : NT == 1 ? 1 : 2; term >= 0; --term) {
+  for (int term = NT == 1 ? 1 : 2; term >= 0; --term) {
     const uint32_t ta = term == 1 ? lo : hi, tb = x + (term == 2 ? kPlane : 0);
 #pragma unroll
     for (int k = 0; k < DK / 16; ++k)
       mma_ts(d, ta + 8 * k, tile_desc(tb + (k >> 2) * 2 * kTile + (k & 3) * 32, 16),
-             idesc_tokens, term < (LEAD ? 0 : NT == 1 ? 1 : 2) || k > 0);
+             idesc_tokens, term < (NT == 1 ? 1 : 2) || k > 0);
   }
 }
 // A B^T for 64-token A (two parts; ONE: the leading one is all of it) and a
 // 64 x 64 matrix of the image.
-template <bool LEAD, bool ONE = false>
+template <bool ONE = false>
 __device__ __forceinline__ void mma_inner(uint32_t d, uint32_t hi, uint32_t lo, uint32_t m,
                                           bool accumulate) {
 #pragma unroll
-  for (int term = LEAD ? 0 : 2; term >= 0; --term) {
+  for (int term = 2; term >= 0; --term) {
     if (ONE && term == 1) continue;
     const uint32_t ta = term == 1 ? lo : hi, tb = m + (term == 2 ? kTile : 0);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       mma_ts(d, ta + 8 * k, tile_desc(tb + k * 32, 16), idesc_tokens,
-             accumulate || term < (LEAD ? 0 : 2) || k > 0);
+             accumulate || term < 2 || k > 0);
   }
 }
 // A X for 64-token A and the chunk's X (K or Q) as 64 tokens x DK.
@@ -423,9 +423,6 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs &a, const DeltaPlan &
   __shared__ BlockBounds bounds;
   constexpr int NT = Terms<T>::value, ST = kScanStages;
   constexpr int kStage = scan_stage_bytes(DK, NT, STAGED);
-  // bf16 outputs: their rounding (2^-9) hides what the leading fp16 parts of
-  // S, U and M leave out (2^-12) in the products that only the output sees.
-  constexpr bool LEAD = std::is_same<T, __nv_bfloat16>::value;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int blocks_v = (a.dv + 127) / 128;
   const int vb = block % blocks_v;
@@ -456,21 +453,21 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs &a, const DeltaPlan &
       if (!wait(&bars.full[s], (it / ST) & 1) || !wait(&bars.sb, ph)) break;
       tc_fence_after();
       if (elect_one()) {
-        mma_state<DK, NT, false>(tm + kColP, tm + kColSh, tm + kColSl, k);
+        mma_state<DK, NT>(tm + kColP, tm + kColSh, tm + kColSl, k);
         mma_commit(&bars.p);
       }
       __syncwarp();
       if (!wait(&bars.y, ph)) break;
       tc_fence_after();
       if (elect_one()) {
-        mma_inner<false>(tm + kColP, tm + kColYh, tm + kColYl, image, false);
+        mma_inner<>(tm + kColP, tm + kColYh, tm + kColYl, image, false);
         mma_commit(&bars.e);
       }
       __syncwarp();
       if (it > 0 && !wait(&bars.of, ph ^ 1)) break;
       tc_fence_after();
       if (elect_one()) {
-        mma_state<DK, NT, LEAD>(tm + kColN, tm + kColSh, tm + kColSl, q);
+        mma_state<DK, NT>(tm + kColN, tm + kColSh, tm + kColSl, q);
         mma_commit(&bars.n);
       }
       __syncwarp();
@@ -484,7 +481,7 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs &a, const DeltaPlan &
       if (!wait(&bars.u, ph)) break;
       tc_fence_after();
       if (elect_one()) {
-        mma_inner<LEAD>(tm + kColN, tm + kColYh, tm + kColYl, image + 2 * kTile, true);
+        mma_inner<>(tm + kColN, tm + kColYh, tm + kColYl, image + 2 * kTile, true);
         mma_commit(&bars.o);
         mma_commit(&bars.empty[s]);
       }
@@ -678,8 +675,7 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs &a, const DeltaPlan &
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         f[j] = mul2(pair(r, j), mul2(gate(gates + 2 * 64, j), both(inv_y * us)));
-      if constexpr (LEAD) put_lead(lb + kColYh + group * 8, f);
-      else put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, f);
+      put_split(lb + kColYh + group * 8, lb + kColYl + group * 8, f);
       if constexpr (SAVE) {
         const float es_scale = bounds.scale(it, 0);
 #pragma unroll

@@ -1,0 +1,90 @@
+"""The gated delta rule where operands differ much in size, against the
+token-by-token recurrence in 64 bits.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+import delta_reference as ref  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+HALF_ULP = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+
+
+@pytest.fixture(scope="module")
+def fg(fg_lib):
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return fg_lib
+
+
+def cuda(ts):
+    return [None if t is None else t.cuda() for t in ts]
+
+
+def normal(seed, *shape):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed))
+
+
+# ---- what an output keeps of a sum whose terms are larger than it ------------------------
+#
+# Every factor of a product keeps 22 significand bits or is exact (2^-23 of rounding), and the tensor
+# cores cut each of up to 24 partial sums below the last fp32 bit (2^-23): 32 * 2^-23 of the sum of
+# the terms' absolute values, on each output, beside the output's own rounding.
+KEPT = 32 * 2.0 ** -23
+
+
+def outputs_and_terms(q, k, v, g, beta, state):
+    """o of one sequence [tokens, heads, dv] in 64 bits, and for each value the sum of the absolute
+    values that make it up: |S0|^T |q| as it decays, and |u_j| |k_j . q_t| of the tokens since."""
+    q, k, v, g, beta, s = (t.double() for t in (q, k, v, g, beta, state))
+    group = v.shape[1] // q.shape[1]
+    q, k = q.repeat_interleave(group, 1), k.repeat_interleave(group, 1)
+    scale = q.shape[-1] ** -0.5
+    first, decay, us, outs, sizes = s.abs(), torch.zeros_like(g[0]), [], [], []
+    for t in range(q.shape[0]):
+        s = s * g[t].exp()[:, None, None]
+        u = beta[t][:, None] * (v[t] - torch.einsum("hkv,hk->hv", s, k[t]))
+        s = s + k[t][:, :, None] * u[:, None, :]
+        decay = decay + g[t]
+        us.append((u, k[t], decay))
+        outs.append(scale * torch.einsum("hkv,hk->hv", s, q[t]))
+        size = decay.exp()[:, None] * torch.einsum("hkv,hk->hv", first, q[t].abs())
+        for uj, kj, dj in us:
+            size = size + ((decay - dj).exp() * (kj * q[t]).sum(-1).abs())[:, None] * uj.abs()
+        sizes.append(scale * size)
+    return torch.stack(outs), torch.stack(sizes)
+
+
+def check_terms(fg, args, state):
+    o, _ = fg.delta_rule(*cuda([t[None] for t in args]), initial_state=state[None].cuda())
+    want, size = outputs_and_terms(*args, state)
+    bound = HALF_ULP[o.dtype] * want.abs() + KEPT * size
+    off = ((o[0].double().cpu() - want).abs() / bound).max()
+    assert off <= 1, float(off)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("dk", [64, 128])
+def test_a_small_value_overwrites_a_large_one(fg, kind, dk):
+    # q = k, beta = 1: o = scale v (if |k| = 1), where S0^T k is a thousand times as large
+    q, k, v, g, beta = (t[0] for t in ref.inputs(51, 1, 100, 1, 1, dk, 64, TYPES[kind]))
+    state = 1024 * normal(52, 1, dk, 64)
+    check_terms(fg, (k, k, v, torch.zeros_like(g), torch.ones_like(beta)), state)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_one_value_among_larger_ones(fg, kind):
+    # 64 orthonormal keys (Hadamard's, exact in every type); of the values stored under them one is
+    # a thousand times smaller, and that one is read
+    h = torch.ones(1, 1)
+    while h.shape[0] < 64:
+        h = torch.cat([torch.cat([h, h], 1), torch.cat([h, -h], 1)])
+    keys, values = h / 8, 1000 * normal(53, 64, 64)
+    values[5] /= 1000
+    state = torch.einsum("jk,jv->kv", keys, values)[None]
+    q = keys[5].expand(100, 1, 64).to(TYPES[kind]).contiguous()
+    _, k, v, g, beta = (t[0] for t in ref.inputs(54, 1, 100, 1, 1, 64, 64, TYPES[kind]))
+    k = torch.where(torch.arange(64) < 32, k, torch.zeros_like(k))
+    check_terms(fg, (q, k, v, 0.01 * g, 0.1 * beta), state)
