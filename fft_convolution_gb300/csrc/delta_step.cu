@@ -6,10 +6,13 @@
 //            o = scale S^T q.
 // With S' the decayed state, S^T q = S'^T q + (k . q) u: both products with
 // the state are taken in one walk over it, and one exchange between the
-// threads gives every sum.  The state changes by k u + S (e^g - 1), added in
-// one rounding: of a slow decay e^g itself would keep few digits of its
+// threads gives every sum.  In a slow decay the state changes by k u +
+// S (e^g - 1), added in one rounding: e^g itself would keep few digits of its
 // distance from 1, an error that thousands of tokens add up; what rounding
-// leaves out of u is carried along for the same reason.
+// leaves out of u is carried along for the same reason.  In a quick one (g
+// below kQuick, where less than half of S is left) it is k u + S e^g, each
+// rounded at its own size: of S - S (1 - e^g) would only remain what the
+// rounding of S leaves (g = -16: 20% of the state off).
 //
 // Reading and writing the fp32 state is nearly all the traffic (128 KB per
 // head of 128 x 128, against under 1 KB for the token), so HBM bounds the
@@ -23,6 +26,7 @@
 namespace fftgb {
 
 constexpr int kStepThreads = 128, kStepCols = 32;
+constexpr float kQuick = -0.6875f;  // -log 2, a little above
 
 // N elements on a boundary of N elements (of 16 bytes, if that is less).
 template <int N, typename T> __device__ __forceinline__ void load_whole(const T *p, float (&f)[N]) {
@@ -109,7 +113,10 @@ __global__ void __launch_bounds__(kStepThreads, 6) delta_step_kernel(const Delta
 #pragma unroll
       for (int j = 0; j < 4; ++j) vc[j] = c0 + j < a.dv ? to_acc(v[t * a.sv.tok + c0 + j]) : 0.0f;
     }
-    const float decay = expm1f(g[t * a.sg.tok]), bt = beta[t * a.sb.tok];
+    // S e^g = S decay + S whole
+    const float gt = g[t * a.sg.tok], bt = beta[t * a.sb.tok];
+    const bool slow = gt > kQuick;
+    const float decay = slow ? expm1f(gt) : expf(gt), whole = slow ? 1.0f : 0.0f;
     // S^T k and S^T q of the 4 columns (S before its decay), k . q
     float2 sk[2], sq[2];
     sk[0] = sk[1] = sq[0] = sq[1] = make_float2(0.0f, 0.0f);
@@ -147,14 +154,14 @@ __global__ void __launch_bounds__(kStepThreads, 6) delta_step_kernel(const Delta
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       // u = beta (v - S'^T k) and what its rounding leaves out
-      const float held = fmaf(decay, sum[j], sum[j]), miss = vc[j] - held;
+      const float held = fmaf(decay, sum[j], whole * sum[j]), miss = vc[j] - held;
       const float back = miss - vc[j];
       const float rest = (vc[j] - (miss - back)) - (held + back);
       u[j] = bt * miss;
       ur[j] = fmaf(bt, miss, -u[j]) + bt * rest;
       if (rg == 0 && c0 + j < a.dv)
         o[t * ostep + c0 + j] =
-            from_acc<T>(a.scale * fmaf(sum[8], u[j], fmaf(decay, sum[4 + j], sum[4 + j])));
+            from_acc<T>(a.scale * fmaf(sum[8], u[j], fmaf(decay, sum[4 + j], whole * sum[4 + j])));
     }
 #pragma unroll
     for (int i = 0; i < R; ++i)
@@ -163,7 +170,7 @@ __global__ void __launch_bounds__(kStepThreads, 6) delta_step_kernel(const Delta
         const float2 ku = make_float2(u[2 * j], u[2 * j + 1]), kur = make_float2(ur[2 * j], ur[2 * j + 1]);
         const float2 change =
             fma2(both(kr[i]), ku, fma2(both(kr[i]), kur, mul2(both(decay), s[i][j])));
-        s[i][j] = fma2(change, both(1.0f), s[i][j]);
+        s[i][j] = fma2(s[i][j], both(whole), change);
       }
   }
 

@@ -88,3 +88,39 @@ def test_one_value_among_larger_ones(fg, kind):
     _, k, v, g, beta = (t[0] for t in ref.inputs(54, 1, 100, 1, 1, 64, 64, TYPES[kind]))
     k = torch.where(torch.arange(64) < 32, k, torch.zeros_like(k))
     check_terms(fg, (q, k, v, 0.01 * g, 0.1 * beta), state)
+
+
+# ---- one token after a strong decay ----------------------------------------------------------
+
+# The new state is e^g S + k u in fp32, u = beta (v - e^g S^T k): a sum over dk, rounded a few
+# times (64 * 2^-24, as for any single token), at the size of the two terms of each result.
+TOKEN = 64 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [1.0, 1000.0])
+@pytest.mark.parametrize("strength", [0.0, 0.01, 0.5])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (50, 77), (200, 64)])
+def test_step_after_a_strong_decay(fg, kind, size, strength, dk, dv):
+    decays = torch.tensor([0.0, -0.1, -0.69, -0.7, -1.0, -5.0, -10.0, -16.0, -60.0, -float("inf")])
+    heads = len(decays)
+    q, k, v, g, beta = ref.inputs(61, 2, 1, heads, heads, dk, dv, TYPES[kind])
+    g, beta = decays.expand(2, 1, heads).contiguous(), torch.full_like(beta, strength)
+    state = size * normal(62, 2, heads, dk, dv)
+    pool = state.cuda()
+    o = fg.delta_rule_step(*cuda((q, k, v, g, beta)), pool)
+    scale = dk ** -0.5
+    for i in range(2):
+        o64, s64 = ref.forward(*(t[i] for t in (q, k, v, g, beta)), state=state[i])
+        for h in range(heads):
+            e, kh, qh = float(decays[h].double().exp()), k[i, 0, h].double(), q[i, 0, h].double()
+            held = e * state[i, h].double()
+            u = strength * (v[i, 0, h].double() - held.t() @ kh)
+            # S: the errors of u enter along k, those of e^g S stay where they are
+            size_u = strength * (v[i, 0, h].double().norm() + (held.t() @ kh).norm())
+            bound = TOKEN * (held.norm() + size_u * kh.norm())
+            assert float((pool[i, h].double().cpu() - s64[h]).norm()) <= float(bound), (i, h)
+            bound = HALF_ULP[TYPES[kind]] * o64[0, h].norm() + TOKEN * scale * (
+                (held.t() @ qh).norm() + (kh @ qh).abs() * size_u)
+            assert float((o[i, 0, h].double().cpu() - o64[0, h]).norm()) <= float(bound), (i, h)
+            assert u.isfinite().all()
