@@ -203,7 +203,10 @@ __device__ __forceinline__ void delta_back(const DeltaArgs &a, const DeltaGradAr
       const float os = bound_scale(most.y);
       const float by = chunk[1] * smax + chunk[2] * most.y;
       const float bw = fmaxf(by * chunk[3] * chunk[4], chunk[5] * most.y);
-      const float ys = bound_scale(by), ws = bound_scale(bw);
+      const float yb = fmaxf(by, fmaxf(smax, most.y) * kApart);
+      const float ys = bound_scale(yb);
+      const float ws =
+          bound_scale(fmaxf(bw, fmaxf(yb * fmaxf(1.0f, chunk[4]), chunk[5]) * kApart));
       const float inv_y = scale_inverse(ys);
       const float bs = fmaf(Gamma, smax, 256.0f * bw), next_ss = bound_scale(bs);
       bounds.enter(it, 0, live ? by * chunk[3] : 0.0f, lane);

@@ -453,7 +453,7 @@ delta_grad_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
         }
         grad_all(true);
         const float s1 = bound_scale(__uint_as_float(tk.most[is_z ? 1 : 0]));
-        const float s2 = bound_scale(__uint_as_float(tk.most[2])) * over;
+        const float s2 = bound_scale(__uint_as_float(tk.most[2]));
         char *tiles = ra + (is_z ? 4 * kTile : 0);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
@@ -464,8 +464,8 @@ delta_grad_kernel(const DeltaArgs a, const DeltaGradArgs ga, const DeltaPlan pla
             four(tk.ek + group * 16 + 8 * p + k, ej);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              g[k + e] = gx[8 * p + k + e];
-              f[k + e] = g[k + e] * ej[e];
+              f[k + e] = gx[8 * p + k + e] * ej[e];
+              g[k + e] = gx[8 * p + k + e] * over;
             }
           }
           uint4 hi, lo;

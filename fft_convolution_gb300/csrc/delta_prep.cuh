@@ -24,7 +24,7 @@
 // strides and alignment.
 //
 // Forward image: (I + A beta)^-1 and M by rows; per token
-//   0: -gamma 2^ek   1: Gamma/gamma beta 2^(ek + et)   2: beta 2^et   3: gamma 2^(eq - em)
+//   0: -gamma 2^ek   1: Gamma/gamma beta 2^(ek + et)   2: beta 2^et   3: scale gamma 2^eq
 //   4: scale 2^em    5: 2^et
 // BACK image: (I + beta A)^-T and M^T; per token
 //   0: Gamma/gamma 2^ek   1: scale 2^em   2: 2^et   3: beta
@@ -381,7 +381,7 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
         const float ek = inv_kq[tid], eq = inv_kq[64 + tid], em = inv[1][tid], et = inv[0][tid];
         const float gam = decay_between(G[tid], make_float2(0.0f, 0.0f));
         const float dec = decay_between(G[63], G[tid]), bt = beta_s[tid];
-        const float ga[kGates] = {-gam * ek, dec * bt * ek * et, bt * et, gam * (eq / em),
+        const float ga[kGates] = {-gam * ek, dec * bt * ek * et, bt * et, a.scale * gam * eq,
                                   a.scale * em, et, ek, eq};
         const float ba = fabsf(bt) * sum[0][tid], sc = fabsf(a.scale);
         float b[9];

@@ -11,12 +11,15 @@
 // the state's columns: the state itself stays in their registers in fp32,
 // and what they hand to the tensor cores (S, Y, U, W) is scaled by a power of
 // two and split into two fp16 values.  Only P -> Y -> E -> U -> S is a chain;
-// N, U M^T, the output and all loads run beside it.  So the scales do not come
+// N, U M^T, the output (their sum, in fp32: each has its own scale, and one of
+// them may be far below the other) and all loads run beside it.  So the scales do not come
 // from the values (finding the largest of a column takes the four threads a
 // barrier at each step of the chain) but from bounds on them: from the largest
 // values of V and of the state, which are found beside the chain, and the
 // chunk's bounds.  The scale brings the bound to 2^14; values down to 2^-16
-// of the bound keep all their digits.
+// of the bound keep all their digits.  A bound counts as kApart of what it is
+// computed from at least: the quotient of two scales stays finite then (a chunk
+// that writes nothing has a bound of 0 on U and W, however large the state).
 //
 // The chain bounds it: a chunk takes 4800 clocks, of which the tensor cores work
 // 1100; the rest are four trips from them through registers and back, with 61%
@@ -30,8 +33,8 @@
 // Tensor memory (512 columns):
 //   W K (fp32)       0 .. DK - 1
 //   S (two fp16)     128, 192        P, then E     256 .. 319
-//   Y, then U        320, 352        W             384, 416
-//   N, then O        448 .. 511
+//   Y, then U        320, 352        W, then U M^T  384, 416
+//   N                448 .. 511
 #pragma once
 
 #include "delta.cuh"
@@ -43,6 +46,7 @@ constexpr int kScanGroups = kScanWarps / 4;          // threads that share a col
 constexpr int kScanTok = 64 / kScanGroups;           // tokens of each
 constexpr int kScanThreads = (kScanWarps + 4) * 32;
 constexpr int kScanStages = 2;
+constexpr float kApart = 0x1p-86f;
 
 // 64 tokens x 128 columns of a 16-bit type.
 constexpr int kRows16 = 64 * 128 * 2;
@@ -62,8 +66,8 @@ __host__ __device__ constexpr size_t scan_smem(int dk, int terms, bool staged) {
 
 struct ScanBars {
   uint64_t full[kScanStages], empty[kScanStages];
-  uint64_t p, n, e, s, o;       // products done: P, N, E, W K, O
-  uint64_t y, w, u, sb, of;     // operands ready: Y, W, U and N scaled, S; O read
+  uint64_t p, n, e, s, o;       // products done: P, X (backwards), E, W K, N and U M^T
+  uint64_t y, w, u, sb, of;     // operands ready: Y, W, U, S; N and U M^T read
   uint64_t put, got;            // STAGED: rows of O in shared memory; copied out
   uint64_t done;                // every product
 };
@@ -306,7 +310,7 @@ __device__ __forceinline__ float max16(float m, const float2 (&f)[8]) {
   for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(f[j].x), fabsf(f[j].y)));
   return m;
 }
-__device__ __forceinline__ float2 pair(const uint32_t (&r)[16], int j) {
+template <int N> __device__ __forceinline__ float2 pair(const uint32_t (&r)[N], int j) {
   return make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
 }
 // Factors of tokens 2j, 2j + 1 of a thread's.
@@ -383,7 +387,7 @@ struct RowAgree {
 };
 
 constexpr uint32_t kColD = 0, kColSh = 128, kColSl = 192, kColP = 256, kColYh = 320, kColYl = 352,
-                   kColWh = 384, kColWl = 416, kColN = 448;
+                   kColWh = 384, kColWl = 416, kColN = 448, kColUM = kColWh;
 
 // Barriers and tensor memory of a scan: returns the base column.
 __device__ __forceinline__ uint32_t scan_begin(ScanBars &bars, uint32_t *slot, volatile int *failed,
@@ -459,14 +463,13 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs &a, const DeltaPlan &
       __syncwarp();
       if (!wait(&bars.y, ph)) break;
       tc_fence_after();
-      if (elect_one()) {
-        mma_inner<>(tm + kColP, tm + kColYh, tm + kColYl, image, false);
-        mma_commit(&bars.e);
-      }
+      if (elect_one()) mma_inner<>(tm + kColP, tm + kColYh, tm + kColYl, image, false);
       __syncwarp();
+      // E is told of when U M^T has been read too: W will lie there.
       if (it > 0 && !wait(&bars.of, ph ^ 1)) break;
       tc_fence_after();
       if (elect_one()) {
+        mma_commit(&bars.e);
         mma_state<DK, NT>(tm + kColN, tm + kColSh, tm + kColSl, q);
         mma_commit(&bars.n);
       }
@@ -478,10 +481,10 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs &a, const DeltaPlan &
         mma_commit(&bars.s);
       }
       __syncwarp();
-      if (!wait(&bars.u, ph)) break;
+      if (!wait(&bars.u, ph) || !wait(&bars.s, ph)) break;  // (W has been used)
       tc_fence_after();
       if (elect_one()) {
-        mma_inner<>(tm + kColN, tm + kColYh, tm + kColYl, image + 2 * kTile, true);
+        mma_inner<>(tm + kColUM, tm + kColYh, tm + kColYl, image + 2 * kTile, false);
         mma_commit(&bars.o);
         mma_commit(&bars.empty[s]);
       }
@@ -577,21 +580,26 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs &a, const DeltaPlan &
       vmax = max16(0.0f, f);
       return true;
     };
-    // The output of chunk c, whose U was scaled by us.
-    auto put_output = [&](int c, float us) {
-      const float inv_u = scale_inverse(us);
+    // The output of chunk c, whose U had this scale.
+    auto put_output = [&](int c, float inv_u) {
       const float *gates = gates_of(c) + group * TK;
       if (!wait(&bars.o, c & 1)) return false;
       if (STAGED && a.o && c > 0 && !wait(&bars.got, (c & 1) ^ 1)) return false;
       tc_fence_after();
-      uint32_t r[16];
-      tmem_ld(lb + kColN + group * TK, r);
-      tmem_wait_ld();
-      warp_arrive(&bars.of, lane);
+      tmem_wait_st();  // (N)
       TokenValues<T> out;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        out.set(j, mul2(pair(r, j), mul2(gate(gates + 4 * 64, j), both(inv_u))));
+      for (int p = 0; p < 2; ++p) {  // (all 16 tokens' at once spill)
+        uint32_t r[8], n[8];
+        tmem_ld(lb + kColUM + group * TK + 8 * p, r);
+        tmem_ld(lb + kColN + group * TK + 8 * p, n);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          out.set(4 * p + j, fma2(pair(r, j), mul2(gate(gates + 4 * 64, 4 * p + j), both(inv_u)),
+                                  pair(n, j)));
+      }
+      warp_arrive(&bars.of, lane);
       if (STAGED && a.o) {
         out.put(stages + ST * kStage, group * TK, row, lane);
       } else if (a.o && live) {
@@ -622,7 +630,7 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs &a, const DeltaPlan &
         for (int j = 0; j < 8; ++j) S[p][j] = mul2(S[p][j], both(ss));
       put_state(0);
     }
-    float us_before = 1.0f;
+    float inv_u = 1.0f;  // of the chunk before
     for (int it = 0; it < sp.chunks && ok; ++it) {
       const uint32_t ph = it & 1;
       const float *gates = gates_of(it) + group * TK;
@@ -634,11 +642,14 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs &a, const DeltaPlan &
       const float *chunk = gates_of(it) + kChunkAt;
       const float Gamma = chunk[0], inv_s = scale_inverse(ss), smax = most.x * inv_s;
       const float by = most.y + chunk[1] * smax, bw = by * chunk[3];
-      const float ys = bound_scale(by), us = bound_scale(by * chunk[2]), wsc = bound_scale(bw);
+      const float yb = fmaxf(by, smax * kApart), least = yb * kApart;
+      const float ys = bound_scale(yb);
+      const float us = bound_scale(fmaxf(by * chunk[2], least * fmaxf(1.0f, chunk[2])));
+      const float wsc = bound_scale(fmaxf(bw, least * fmaxf(1.0f, chunk[3])));
       const float inv_y = scale_inverse(ys);
       const float bs = fmaf(Gamma, smax, 128.0f * bw), next_ss = bound_scale(bs);
       if constexpr (SAVE) {
-        bounds.enter(it, 0, live ? by * chunk[4] : 0.0f, lane);
+        bounds.enter(it, 0, live ? yb * chunk[4] : 0.0f, lane);
         bounds.enter(it, 1, live ? bs : 0.0f, lane);
       }
 #pragma unroll
@@ -656,8 +667,8 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs &a, const DeltaPlan &
       warp_arrive(&bars.y, lane);
       if (lane == 0) bar_arrive(&bars.empty[it % ST]);  // V has been used
       // While E is computed: the output of the chunk before.
-      if (it > 0 && !(ok = put_output(it - 1, us_before))) break;
-      us_before = us;
+      if (it > 0 && !(ok = put_output(it - 1, inv_u))) break;
+      inv_u = scale_inverse(us);
       // W = E beta Gamma / gamma, on which the new state waits, then U = E beta
       // (E taken from tensor memory once more, which saves registers).
       if (!(ok = wait(&bars.e, ph))) break;
@@ -687,21 +698,20 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs &a, const DeltaPlan &
           bounds.clear(it);
         }
       }
-      // While the new state is computed: N in units of U M^T, the start of O
+      tmem_wait_st();
+      warp_arrive(&bars.u, lane);
+      // While the new state is computed: N in the output's units.
       if (!(ok = wait(&bars.n, ph))) break;
       tc_fence_after();
       tmem_ld(lb + kColN + group * TK, r);
       tmem_wait_ld();
-      const float ratio = inv_s * us;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float2 n = mul2(pair(r, j), mul2(gate(gates + 3 * 64, j), both(ratio)));
+        const float2 n = mul2(pair(r, j), mul2(gate(gates + 3 * 64, j), both(inv_s)));
         r[2 * j] = __float_as_uint(n.x);
         r[2 * j + 1] = __float_as_uint(n.y);
       }
       tmem_st(lb + kColN + group * TK, r);
-      tmem_wait_st();
-      warp_arrive(&bars.u, lane);
       const bool more = it + 1 < sp.chunks;
       if (more) fetch_v(it + 1);
       // The new state
@@ -719,7 +729,7 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs &a, const DeltaPlan &
       ss = next_ss;
       if (more) put_state(it + 1);
     }
-    if (ok && sp.chunks > 0) ok = put_output(sp.chunks - 1, us_before);
+    if (ok && sp.chunks > 0) ok = put_output(sp.chunks - 1, inv_u);
     if (ok && a.state_out && live) {
 #pragma unroll
       for (int p = 0; p < SP; ++p)

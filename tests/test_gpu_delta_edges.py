@@ -124,3 +124,89 @@ def test_step_after_a_strong_decay(fg, kind, size, strength, dk, dv):
                 (held.t() @ qh).norm() + (kh @ qh).abs() * size_u)
             assert float((o[i, 0, h].double().cpu() - o64[0, h]).norm()) <= float(bound), (i, h)
             assert u.isfinite().all()
+
+
+# ---- chunks that write nothing, and sizes far apart -----------------------------------------
+
+FP = 5 * 2.0 ** -18          # whole sequences, forward: five products one after the other
+FP_GRAD = 12 * 2.0 ** -20    # gradients: twelve
+NAMES = ("dq", "dk", "dv", "dg", "dbeta", "dinitial")
+
+
+def rel(a, b):
+    a, b = a.double().cpu(), b.double().cpu()
+    n = b.norm()
+    return float((a - b).norm() / n) if n > 0 else float((a - b).norm())
+
+
+def check_by_chunk(fg, args, state):
+    """Outputs chunk by chunk and the final state, of one sequence."""
+    o, s = fg.delta_rule(*cuda(args), initial_state=state.cuda())
+    o64, s64 = ref.forward(*(t[0] for t in args), state=state[0])
+    for c in range(0, o.shape[1], 64):
+        got = o[0, c:c + 64]
+        assert got.isfinite().all(), c
+        assert rel(got, o64[c:c + 64]) <= HALF_ULP[o.dtype] + FP, c
+    assert s.isfinite().all() and rel(s[0], s64) <= FP
+
+
+def check_gradients(fg, args, do, state, dfinal):
+    grads = fg.delta_rule_backward(do.cuda(), *cuda(args), initial_state=state.cuda(),
+                                   dfinal_state=None if dfinal is None else dfinal.cuda())
+    want = ref.backward(do[0], *(t[0] for t in args), state=state[0], dfinal=None if dfinal is None else dfinal[0])
+    for name, got, w in zip(NAMES, grads, want):
+        assert got.isfinite().all(), name
+        tol = HALF_ULP[got.dtype] + (4 if name == "dg" else 1) * FP_GRAD
+        assert rel(got[0], w) <= tol, (name, rel(got[0], w))
+
+
+def still_chunk(kind, how):
+    """Three chunks, the second of them without a write."""
+    q, k, v, g, beta = ref.inputs(71, 1, 192, 1, 1, 64, 64, torch.float32)
+    beta[:, 64:128] = 0.0
+    if how == "small keys":
+        k[:, 64:128] *= 2.0 ** (-20 if kind == "f16" else -30)
+    elif how == "orthogonal":  # but for a rounding
+        q[:, 64:128, :, 32:] = 0.0
+        k[:, 64:128, :, :32] = 0.0
+        k[:, 64:128, :, 0] = 2.0 ** -24
+    return [t.to(TYPES[kind]) for t in (q, k, v)] + [0.01 * g, beta]
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("how", ["small keys", "orthogonal", "plain"])
+def test_a_chunk_that_writes_nothing(fg, kind, how):
+    args = still_chunk(kind, how)
+    state = 2.0 ** (11 if kind == "f16" else 14) * normal(72, 1, 1, 64, 64)  # (gradients within fp16's range)
+    check_by_chunk(fg, args, state)
+    check_gradients(fg, args, normal(73, *args[2].shape).to(TYPES[kind]), state, normal(74, 1, 1, 64, 64))
+
+
+@pytest.mark.parametrize("how", ["small keys", "orthogonal", "plain", "dropped"])
+def test_a_chunk_that_writes_nothing_to_a_very_large_state(fg, how):
+    # what the outputs and the states are scaled by lies far apart
+    args = still_chunk("f32", how)
+    if how == "dropped":  # and nothing to store either
+        args[2][:, 64:128] = 0.0
+        args[3][:, 64] = -float("inf")
+    check_by_chunk(fg, args, 2.0 ** 45 * normal(75, 1, 1, 64, 64))
+
+
+@pytest.mark.parametrize("how", ["no keys", "no queries", "no gradient", "large queries"])
+def test_gradients_of_sizes_far_apart(fg, how):
+    args = still_chunk("f32", "plain")
+    do, state, dfinal = normal(76, 1, 192, 1, 64), normal(77, 1, 1, 64, 64), None
+    if how == "no keys":
+        args[1][:, 64:] = 0.0
+        do *= 2.0 ** 45
+    elif how == "no queries":
+        args[0][:, 64:] = 0.0
+        do *= 2.0 ** 45
+    elif how == "no gradient":
+        do[:, 64:] = 0.0
+        args[0][:, 64:] *= 2.0 ** 40
+        dfinal = normal(78, 1, 1, 64, 64)
+    else:
+        args[0][:] *= 2.0 ** 40
+        args[4][:] = 0.0
+    check_gradients(fg, args, do, state, dfinal)
