@@ -36,9 +36,13 @@ _current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 
 def _on(stream, device):
-    """(context in which the call's allocations are made, stream handle)."""
+    """(context in which the call allocates and launches, stream handle).  The
+    library works on the current device, so inside it that is the tensors'."""
     if stream is None:
-        return _NULL, _current(device.index)
+        here = device.index == torch.cuda.current_device()
+        return _NULL if here else torch.cuda.device(device), _current(device.index)
+    if stream.device != device:
+        raise ValueError(f"tensors on {device}, a stream of {stream.device}")
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
