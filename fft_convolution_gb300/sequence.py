@@ -104,12 +104,12 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
         raise ValueError("rows need at least one element")
     device = _device(x, weight, bias, out)
     code = _elem(x, "x")
-    w, b = _vector(weight, dim, "weight"), _vector(bias, dim, "bias")
-    if w is not None and b is not None and w.dtype != b.dtype:
-        raise TypeError("weight and bias need one type")
-    wcode = code if w is None and b is None else _elem(w if w is not None else b, "weight")
     context, handle = _on(stream, device)
     with context:
+        w, b = _vector(weight, dim, "weight"), _vector(bias, dim, "bias")
+        if w is not None and b is not None and w.dtype != b.dtype:
+            raise TypeError("weight and bias need one type")
+        wcode = code if w is None and b is None else _elem(w if w is not None else b, "weight")
         x2 = _rows(x)
         rows = x2.shape[0]
         if out is None:
@@ -137,11 +137,11 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True, stream=Non
         raise ValueError("dy must be like x")
     device = _device(x, dy, weight, mean, rstd)
     code = _elem(x, "x")
-    w = _vector(weight, dim, "weight")
-    wcode = code if w is None else _elem(w, "weight")
-    wtype = x.dtype if w is None else w.dtype
     context, handle = _on(stream, device)
     with context:
+        w = _vector(weight, dim, "weight")
+        wcode = code if w is None else _elem(w, "weight")
+        wtype = x.dtype if w is None else w.dtype
         x2, dy2 = _rows(x), _rows(dy)
         rows = x2.shape[0]
         mean, rstd = (_row_stats(t, rows, x.dtype, n) for t, n in ((mean, "mean"), (rstd, "rstd")))

@@ -85,3 +85,16 @@ def test_the_tensors_device_is_current_in_every_call(seq, recorder):
         call()
         assert name in recorder.calls and not recorder.outside, name
         assert recorder.inside == 0
+
+
+def test_copies_belong_to_the_calls_stream(seq, recorder, monkeypatch):
+    contiguous, outside = torch.Tensor.contiguous, []
+
+    def watched(t, *args, **kwargs):
+        if not recorder.inside:
+            outside.append(tuple(t.shape))
+        return contiguous(t, *args, **kwargs)
+    monkeypatch.setattr(torch.Tensor, "contiguous", watched)
+    for name, call in calls(seq):
+        call()
+        assert not outside, name
