@@ -39,12 +39,19 @@ template <int N, typename T> __device__ __forceinline__ void load_whole(const T 
   for (int i = 0; i < N; ++i) f[i] = to_acc(reinterpret_cast<const T *>(w)[i]);
 }
 
+// Blocks per SM: what the registers of R rows allow.  (64 sequences with 16
+// heads of 256 x 256: at 6 blocks, spilling 350 to 560 bytes, 113 us, at 3
+// none, 90; of 192 x 192 78 and 67.  256 sequences with 32 heads of 96 x 96: 5
+// blocks 143 us, 6 124, although a form or two spills 8 bytes.)
+constexpr int step_blocks(int rows) { return rows > 8 ? 3 : 6; }
+
 // VEC: the state goes by 16 bytes.  FULL: so do k, q and v, and all 16 R rows
 // are there.  (One token of 128 sequences with 32 heads of 128 x 128: with
 // elements of k and q loaded one by one 134 us, FULL 84: 95% of the copy rate;
 // 5, 6 or 7 blocks per SM make 87, 84 and 84 us.)
 template <typename T, int R, bool VEC, bool FULL>
-__global__ void __launch_bounds__(kStepThreads, 6) delta_step_kernel(const DeltaArgs a) {
+__global__ void __launch_bounds__(kStepThreads, step_blocks(R))
+delta_step_kernel(const DeltaArgs a) {
   __shared__ float4 red[2][4][8][3];
   const int tiles = (a.dv + kStepCols - 1) / kStepCols;
   const int tile = blockIdx.x % tiles;
