@@ -59,10 +59,10 @@ _DBL = ctypes.c_double
 
 class DeltaDesc(ctypes.Structure):
     """fft_delta_desc: sizes, strides (sequence, token, head; in elements),
-    scale and type of a call of the gated delta rule."""
+    scale, type and treatment of padding of a call of the gated delta rule."""
     _fields_ = ([(n, ctypes.c_int64) for n in ("batch", "tokens", "kheads", "vheads", "dk", "dv")]
                 + [(n + "_stride", ctypes.c_int64 * 3) for n in ("q", "k", "v", "g", "beta")]
-                + [("scale", ctypes.c_double), ("dtype", ctypes.c_int)])
+                + [("scale", ctypes.c_double), ("dtype", ctypes.c_int), ("clear_rows", ctypes.c_int)])
 
 
 SIGNATURES = {

@@ -9,8 +9,8 @@ namespace fftgb {
 
 // The plan of the chunks, made by a small kernel for packed sequences.
 template <typename T>
-cudaError_t delta_make_plan(const DeltaArgs &a, const DeltaLayout &w, char *ws, DeltaPlan &plan,
-                            cudaStream_t st) {
+cudaError_t delta_make_plan(const DeltaArgs &a, const DeltaGradArgs *g, const DeltaLayout &w,
+                            char *ws, DeltaPlan &plan, cudaStream_t st) {
   plan.row0 = plan.chunk0 = nullptr;
   plan.chunks_max = w.chunks;
   plan.per_seq = (int)((a.tokens + kChunk - 1) / kChunk);
@@ -18,7 +18,8 @@ cudaError_t delta_make_plan(const DeltaArgs &a, const DeltaLayout &w, char *ws, 
   int *row0 = reinterpret_cast<int *>(ws + w.row0), *chunk0 = reinterpret_cast<int *>(ws + w.chunk0);
   plan.row0 = row0;
   plan.chunk0 = chunk0;
-  return launch_delta_plan(a.offsets, a.batch, a.tokens, row0, chunk0, st);
+  return launch_delta_plan(a.offsets, a.batch, a.tokens, row0, chunk0, delta_clear(a, g, sizeof(T)),
+                           st);
 }
 
 template <typename T, int DK, bool GRAD>
@@ -61,7 +62,7 @@ cudaError_t delta_forward_t(const DeltaArgs &a, char *ws, cudaStream_t st) {
   if (!status) return cudaErrorInvalidDevice;
   const DeltaLayout w(a, a.offsets != nullptr, false);
   DeltaPlan plan;
-  cudaError_t e = delta_make_plan<T>(a, w, ws, plan, st);
+  cudaError_t e = delta_make_plan<T>(a, nullptr, w, ws, plan, st);
   if (e == cudaSuccess) e = delta_prep_t<T, DK, false>(a, plan, ws + w.kq, ws + w.images, nullptr, status, st);
   if (e != cudaSuccess) return e;
   if constexpr (sizeof(T) == 2)
@@ -123,7 +124,7 @@ cudaError_t delta_backward_t(const DeltaArgs &a, const DeltaGradArgs &g, char *w
   char *states = ws + w.state, *dstates = ws + w.dstate, *es = ws + w.e, *fs = ws + w.f, *os = ws + w.o;
   float *scales = reinterpret_cast<float *>(ws + w.scales);
   DeltaPlan plan;
-  cudaError_t e = delta_make_plan<T>(a, w, ws, plan, st);
+  cudaError_t e = delta_make_plan<T>(a, &g, w, ws, plan, st);
   if (e == cudaSuccess) e = delta_prep_t<T, DK, true>(a, plan, kq, images, back, status, st);
   if (e != cudaSuccess) return e;
   auto scans = delta_scans_t<T, DK, false>;

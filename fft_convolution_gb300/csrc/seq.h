@@ -70,6 +70,7 @@ struct DeltaArgs {
   int kheads, vheads, dk, dv;
   int terms;  // fp16 values that hold one element of q and k (2: fp32)
   float scale;
+  bool clear;  // packed rows that belong to no sequence: results of 0
   // Single tokens: the sequence's row of a pool of `pool` states (null: row = sequence).
   const int *slots;
   long long pool;
@@ -91,9 +92,18 @@ size_t delta_grad_workspace_bytes(const DeltaArgs &a, bool packed);
 template <typename T>
 cudaError_t launch_delta_grad(const DeltaArgs &a, const DeltaGradArgs &g, void *workspace,
                               cudaStream_t st);
-// Fills row0 and chunk0 (batch + 1 entries each) from offsets (delta_plan.cu).
+// Packed arrays whose rows of no sequence are to be 0.
+struct DeltaClear {
+  void *p[5];
+  long long row_bytes[5];
+  int count;
+};
+// The results of a call (g: of the gradients); none unless a.clear.
+DeltaClear delta_clear(const DeltaArgs &a, const DeltaGradArgs *g, size_t elem);
+// Fills row0 and chunk0 (batch + 1 entries each; null: not wanted) from offsets
+// and clears rows (delta_plan.cu).
 cudaError_t launch_delta_plan(const int *offsets, long long batch, long long tokens, int *row0,
-                              int *chunk0, cudaStream_t st);
+                              int *chunk0, const DeltaClear &clear, cudaStream_t st);
 
 // ---- element conversions -----------------------------------------------------
 

@@ -85,6 +85,7 @@ int delta_sizes(const fft_delta_desc *d, int64_t max_dk, DeltaArgs *a) {
   a->dv = (int)d->dv;
   a->terms = d->dtype == FFT_ELEM_F32 ? 2 : 1;
   a->scale = (float)d->scale;
+  a->clear = d->clear_rows != 0;
   return FFT_OK;
 }
 
@@ -231,7 +232,8 @@ int fft_delta_rule(const fft_delta_desc *desc, const void *q, const void *k, con
   int rc = delta_check(desc, kDeltaMaxDk, q, k, v, g, beta, &a);
   if (rc == FFT_OK) rc = delta_chunks_check(a, offsets != nullptr);
   if (rc != FFT_OK) return rc;
-  if (a.batch == 0) return FFT_OK;
+  a.clear = a.clear && offsets && a.tokens > 0;
+  if (a.batch == 0 && !a.clear) return FFT_OK;
   if ((a.tokens > 0 && !o) ||
       (workspace_bytes < delta_workspace_bytes(a, offsets != nullptr)) ||
       (!workspace && delta_workspace_bytes(a, offsets != nullptr) > 0))
@@ -245,6 +247,9 @@ int fft_delta_rule(const fft_delta_desc *desc, const void *q, const void *k, con
   a.state_out = final_state;
   a.o = o;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (a.batch == 0)
+    return finish(launch_delta_plan(offsets, 0, a.tokens, nullptr, nullptr,
+                                    delta_clear(a, nullptr, elem_bytes(desc->dtype)), st));
   switch (desc->dtype) {
     case FFT_ELEM_F32: return finish(launch_delta<float>(a, workspace, st));
     case FFT_ELEM_BF16: return finish(launch_delta<__nv_bfloat16>(a, workspace, st));
@@ -269,7 +274,8 @@ int fft_delta_rule_backward(const fft_delta_desc *desc, const void *dout, const 
   int rc = delta_check(desc, kDeltaMaxDk, q, k, v, g, beta, &a);
   if (rc == FFT_OK) rc = delta_chunks_check(a, offsets != nullptr);
   if (rc != FFT_OK) return rc;
-  if (a.batch == 0) return FFT_OK;
+  a.clear = a.clear && offsets && a.tokens > 0;
+  if (a.batch == 0 && !a.clear) return FFT_OK;
   const size_t need = delta_grad_workspace_bytes(a, offsets != nullptr);
   if ((a.tokens > 0 && (!dout || !dq || !dk || !dv || !dg || !dbeta)) || workspace_bytes < need ||
       (!workspace && need > 0))
@@ -284,6 +290,9 @@ int fft_delta_rule_backward(const fft_delta_desc *desc, const void *dout, const 
   a.state_in = initial_state;
   const DeltaGradArgs ga{dout, dfinal_state, dq, dk, dv, dg, dbeta, dinitial_state};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (a.batch == 0)
+    return finish(launch_delta_plan(offsets, 0, a.tokens, nullptr, nullptr,
+                                    delta_clear(a, &ga, elem_bytes(desc->dtype)), st));
   switch (desc->dtype) {
     case FFT_ELEM_F32: return finish(launch_delta_grad<float>(a, ga, workspace, st));
     case FFT_ELEM_BF16: return finish(launch_delta_grad<__nv_bfloat16>(a, ga, workspace, st));

@@ -18,8 +18,8 @@ from . import FFT_ELEM_BF16, FFT_ELEM_F16, FFT_ELEM_F32, FFT_ELEM_F64, _check, _
 _ELEM = {torch.float32: FFT_ELEM_F32, torch.float64: FFT_ELEM_F64,
          torch.bfloat16: FFT_ELEM_BF16, torch.float16: FFT_ELEM_F16}
 _NULL = contextlib.nullcontext()
-# fft_delta_desc: sizes, five strides of three, scale, type (and its padding).
-_DESC = struct.Struct("=6q15qdi4x")
+# fft_delta_desc: sizes, five strides of three, scale, type, whether to clear rows.
+_DESC = struct.Struct("=6q15qd2i")
 
 
 def _elem(t, what: str) -> int:
@@ -233,7 +233,7 @@ def _dense(t):
     return t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
 
 
-def _delta_inputs(q, k, v, g, beta, scale, batch, packed: bool):
+def _delta_inputs(q, k, v, g, beta, scale, batch, packed: bool, clear: bool = False):
     """Checks the five inputs; returns q, k, v (elements of a head contiguous),
     fft_delta_desc, its head sizes and the device."""
     qs, vs, kind = q.shape, v.shape, q.dtype
@@ -254,7 +254,7 @@ def _delta_inputs(q, k, v, g, beta, scale, batch, packed: bool):
     first = (0,) if packed else ()  # packed rows have no stride between sequences
     strides = [first + t.stride()[:lead + 1] for t in (q, k, v, g, beta)]
     desc = _DESC.pack(batch, qs[lead - 1], qs[-2], vs[-2], qs[-1], vs[-1], *strides[0], *strides[1],
-                      *strides[2], *strides[3], *strides[4], scale, _elem(q, "q"))
+                      *strides[2], *strides[3], *strides[4], scale, _elem(q, "q"), clear)
     return q, k, v, desc, (vs[-2], qs[-1], vs[-1]), device
 
 
@@ -281,12 +281,14 @@ def delta_rule(q, k, v, g, beta, scale=None, initial_state=None, offsets=None, o
     fft_delta_rule).  q, k: [batch, tokens, key heads, dk]; v: [batch, tokens,
     value heads, dv]; g (log decay) and beta: float32 [batch, tokens, value
     heads].  With offsets (int32 [sequences + 1] on the device) the rows of
-    all sequences are packed and the arrays have no batch axis.  scale:
+    all sequences are packed and the arrays have no batch axis; rows of no
+    sequence are 0 in o (in `out`, if it is given, as they were).  scale:
     dk ** -0.5 by default.  States: float32 [sequences, value heads, dk, dv]."""
     batch, packed = _packing(q, offsets)
     context, handle = _on(stream, _device(q))
     with context:
-        q, k, v, desc, sizes, device = _delta_inputs(q, k, v, g, beta, scale, batch, packed)
+        q, k, v, desc, sizes, device = _delta_inputs(q, k, v, g, beta, scale, batch, packed,
+                                                     packed and out is None)
         _device(q, initial_state, offsets, out)
         if packed:
             offsets = offsets.to(torch.int32).contiguous()
@@ -310,11 +312,12 @@ def delta_rule_backward(do, q, k, v, g, beta, scale=None, initial_state=None, of
                         dfinal_state=None, stream=None):
     """(dq, dk, dv, dg, dbeta, dinitial_state) of delta_rule, from the gradient
     of o (like v) and of the final state (None: zero); the other arguments
-    as in the forward call (see fft_delta_rule_backward)."""
+    as in the forward call (see fft_delta_rule_backward).  Packed rows of no
+    sequence have gradients of 0."""
     batch, packed = _packing(q, offsets)
     context, handle = _on(stream, _device(q))
     with context:
-        q, k, v, desc, sizes, device = _delta_inputs(q, k, v, g, beta, scale, batch, packed)
+        q, k, v, desc, sizes, device = _delta_inputs(q, k, v, g, beta, scale, batch, packed, packed)
         _device(q, do, initial_state, dfinal_state, offsets)
         if do.shape != v.shape or do.dtype != v.dtype:
             raise ValueError("do must be like v")

@@ -543,6 +543,8 @@ typedef struct fft_delta_desc {
   int64_t q_stride[3], k_stride[3], v_stride[3], g_stride[3], beta_stride[3];
   double scale;
   int dtype; /* of q, k, v and o: FFT_ELEM_F32, _BF16 or _F16; g and beta are float */
+  int clear_rows; /* packed rows of no sequence, in o or the gradients: 0 = left
+                     unwritten, else written as 0 */
 } fft_delta_desc;
 
 /*
@@ -553,7 +555,8 @@ typedef struct fft_delta_desc {
  *                  `tokens` rows (ascending, from 0 to tokens; empty
  *                  sequences are fine).  Offsets that descend or leave the
  *                  rows are cut to the nearest that do not; rows of no
- *                  sequence are left unwritten.
+ *                  sequence (before the first one's or after the last
+ *                  one's) are left as they are, or cleared (clear_rows).
  *   initial_state  float [batch][vheads][dk][dv]; NULL: zero.
  *   final_state    the same, written; may be NULL; may be initial_state.
  *   o              [batch][tokens][vheads][dv], or [tokens][vheads][dv] with

@@ -1,9 +1,10 @@
 """What the tensor helpers of the sequence-model operators do around the
-kernels.
+kernels: streams, rows that belong to no sequence.
 """
 import pytest
 
 torch = pytest.importorskip("torch")
+import delta_reference as ref  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +34,19 @@ def test_strided_vectors_on_a_stream(fg):
         assert all(torch.equal(p, q) for p, q in zip(got, want))
         assert all(torch.equal(p, q) for p, q in zip(back, grads))
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("offsets", [[10, 70, 70, 150], [0, 130], [200], [0, 0, 0]])
+def test_rows_of_no_sequence_are_zero(fg, kind, offsets):
+    args = [t[0].cuda() for t in ref.inputs(16, 1, 200, 1, 2, 40, 64, kind)]
+    do = torch.randn(200, 2, 64, device="cuda").to(kind)
+    at = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    for _ in range(2):
+        # memory that the allocator gives out again is full of these
+        junk = [torch.full((n,), float("nan"), device="cuda") for n in (200 * 2, 200 * 2, 200 * 40, 200 * 128, 200 * 64, 200 * 20)]
+        del junk
+        rows = [fg.delta_rule(*args, offsets=at)[0], *fg.delta_rule_backward(do, *args, offsets=at)[:5]]
+        for t in rows:
+            assert not t[:offsets[0]].any() and not t[offsets[-1]:].any()
+            assert t.isfinite().all()
