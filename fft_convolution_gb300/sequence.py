@@ -3,7 +3,9 @@
 ``include/fft_gb300.h``): they check and marshal torch tensors, allocate
 outputs and workspaces, and call the library.  Every call is asynchronous on
 ``stream`` (default: torch's current stream); what a call allocates belongs
-to that stream.
+to that stream.  Results carry no autograd graph: forward and backward calls
+are the two halves of a torch.autograd.Function (examples/sequence_block.py).
+Tensors that a call overwrites count as changed in place.
 """
 from __future__ import annotations
 
@@ -61,6 +63,11 @@ def _device(first, *others):
     return device
 
 
+# Tells autograd of tensors that the library has written: a backward pass that
+# needs what was there before raises then instead of using what is there now.
+_changed = torch.autograd.graph.increment_version
+
+
 def _workspace(nbytes: int, device):
     return torch.empty(max(16, nbytes), dtype=torch.uint8, device=device)
 
@@ -112,6 +119,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
         wcode = code if w is None and b is None else _elem(w if w is not None else b, "weight")
         x2 = _rows(x)
         rows = x2.shape[0]
+        given = out
         if out is None:
             out = torch.empty(x.shape, dtype=x.dtype, device=device)
         elif out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous():
@@ -124,6 +132,8 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
                                  eps, code, wcode, handle)
     if rc:
         _check(rc, "fft_layer_norm")
+    if given is not None:
+        _changed(given)
     return out, mean, rstd
 
 
@@ -224,6 +234,7 @@ def clip_grad_norm(grads, max_norm: float, out=None, eps: float = 1e-6, stream=N
                                        _address(numels), _address(codes), max_norm, eps,
                                        norm.data_ptr(), ws.data_ptr(), nbytes, handle),
                "fft_clip_grad_norm")
+    _changed(grads if out is None else out)
     return norm
 
 
@@ -294,6 +305,7 @@ def delta_rule(q, k, v, g, beta, scale=None, initial_state=None, offsets=None, o
             offsets = offsets.to(torch.int32).contiguous()
         shape = (batch,) + sizes
         initial_state = _states(initial_state, shape, "initial_state")
+        given = out
         if out is None:
             out = torch.empty(v.shape, dtype=v.dtype, device=device)
         elif out.shape != v.shape or out.dtype != v.dtype or not out.is_contiguous():
@@ -305,6 +317,8 @@ def delta_rule(q, k, v, g, beta, scale=None, initial_state=None, offsets=None, o
                                    g.data_ptr(), beta.data_ptr(), _ptr(offsets),
                                    _ptr(initial_state), out.data_ptr(), final.data_ptr(),
                                    ws.data_ptr(), nbytes, handle), "fft_delta_rule")
+    if given is not None:
+        _changed(given)
     return out, final
 
 
@@ -357,6 +371,7 @@ def delta_rule_step(q, k, v, g, beta, state, slots=None, scale=None, out=None, s
         if slots is not None and (slots.dtype != torch.int32 or slots.shape != (q.shape[0],)
                                   or not slots.is_contiguous()):
             raise ValueError("slots must be contiguous int32 [batch]")
+        given = out
         if out is None:
             out = torch.empty(v.shape, dtype=v.dtype, device=device)
         elif out.shape != v.shape or out.dtype != v.dtype or not out.is_contiguous():
@@ -365,4 +380,5 @@ def delta_rule_step(q, k, v, g, beta, state, slots=None, scale=None, out=None, s
                                         g.data_ptr(), beta.data_ptr(), state.data_ptr(), _ptr(slots),
                                         state.shape[0], out.data_ptr(), handle),
                "fft_delta_rule_step")
+    _changed(state if given is None else [state, given])
     return out

@@ -1,5 +1,5 @@
 """What the tensor helpers of the sequence-model operators do around the
-kernels: streams, rows that belong to no sequence.
+kernels: streams, rows that belong to no sequence, tensors changed in place.
 """
 import pytest
 
@@ -50,3 +50,26 @@ def test_rows_of_no_sequence_are_zero(fg, kind, offsets):
         for t in rows:
             assert not t[:offsets[0]].any() and not t[offsets[-1]:].any()
             assert t.isfinite().all()
+
+
+def raises_for_a_change(make, change):
+    """Whether autograd notices that `change` overwrites what a product keeps for its gradient."""
+    a = make().requires_grad_()
+    kept = a * 1.0
+    y = (kept * kept).sum()
+    change(kept.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+
+
+def test_autograd_notices_tensors_changed_in_place(fg):
+    ones = lambda *shape: lambda: torch.ones(*shape, device="cuda")  # noqa: E731
+    other = torch.ones(8, device="cuda")
+    raises_for_a_change(ones(8), lambda t: fg.clip_grad_norm([t], 0.5))
+    raises_for_a_change(ones(8), lambda t: fg.clip_grad_norm([other], 0.5, out=[t]))
+    raises_for_a_change(ones(4, 8), lambda t: fg.layer_norm(torch.ones(4, 8, device="cuda"), out=t))
+    args = [t.cuda() for t in ref.inputs(17, 2, 3, 1, 2, 16, 24)]
+    raises_for_a_change(ones(2, 2, 16, 24), lambda t: fg.delta_rule_step(*args, t))
+    pool = torch.zeros(2, 2, 16, 24, device="cuda")
+    raises_for_a_change(ones(2, 3, 2, 24), lambda t: fg.delta_rule_step(*args, pool, out=t))
+    raises_for_a_change(ones(2, 3, 2, 24), lambda t: fg.delta_rule(*args, out=t))
