@@ -237,10 +237,10 @@ clip_scale_kernel(const __grid_constant__ ClipTable<N> tab, const double *partia
   for (int k = threadIdx.x; k < parts; k += kClipThreads) s += partial[k];
   const double n = sqrt(block_sum(s));
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
-  // NaN stays NaN (a comparison with it is false), and an infinite norm
-  // scales by 0.
+  // A norm that is NaN makes the factor NaN, an infinite one 0 (whatever the
+  // bound); a quotient 0 / 0 clips nothing.
   const double f = max_norm / (n + eps);
-  const double c = f > 1.0 ? 1.0 : f;
+  const double c = isinf(n) ? 0.0 : f < 1.0 || isnan(n) ? f : 1.0;
   const float cf = (float)c;
   const long long items = tab.first[tab.count];
   for (long long item = items - 1 - blockIdx.x; item >= 0; item -= gridDim.x) {

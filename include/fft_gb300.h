@@ -510,7 +510,8 @@ int fft_layer_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t
  *   workspace  fft_grad_norm_workspace_bytes(count) bytes.
  * Squares are summed in fp32 by groups of at most 64 and those sums in
  * fp64; squares that overflow or vanish in fp32 are taken in fp64.  An infinite
- * norm scales by 0, a NaN makes every output NaN.
+ * norm scales by 0 (also with an infinite max_norm), a NaN makes every output
+ * NaN; zeros stay zeros where max_norm and eps are 0 too.
  */
 size_t fft_grad_norm_workspace_bytes(int64_t count);
 int fft_grad_norm(int64_t count, const void *const *in, const int64_t *numel, const int *dtype,
