@@ -758,14 +758,17 @@ cudaError_t layer_norm_t(const LayerNormArgs &a, cudaStream_t st) {
     if (a.dim <= kNormRegMax) {
       const bool vec = norm_vec<T>(a.x, a.ldx, a.dim) && norm_vec<T>(a.y, a.ldy, a.dim);
       // Few long rows do not fill the multiprocessors with a warp each.
-      if (vec && a.dim <= 16 * 32 * Vec16<T>::N &&
-          (a.dim <= 512 || a.rows >= 8ll * sm_count()))
+      if (vec && a.dim <= 16 * 32 * Vec16<T>::N && a.rows >= 8ll * sm_count())
         return layer_norm_warp<T>(a, st);
       const int grid = (int)norm_grid(a.rows, a.dim);
       return norm_dispatch<T>(a.dim, vec, [&](auto tpr, auto ept, auto v) {
-        layer_norm_kernel<T, tpr.value, ept.value, v.value>
-            <<<grid, NormBlock<tpr.value>::THREADS, 0, st>>>(a);
-        return cudaGetLastError();
+        if constexpr (tpr.value == 32 && v.value) {
+          return layer_norm_warp<T>(a, st);
+        } else {
+          layer_norm_kernel<T, tpr.value, ept.value, v.value>
+              <<<grid, NormBlock<tpr.value>::THREADS, 0, st>>>(a);
+          return cudaGetLastError();
+        }
       });
     }
   }
