@@ -715,7 +715,8 @@ layer_norm_sum_kernel(const A *partial, int parts, int dim, void *dw, void *db, 
 // row's reduction (16 per thread, 256 threads: 90 us for 16384 x 4096 bf16
 // forwards).  The gradients of that size take 83 us, 72% of the copy rate, and
 // the sum of the partial rows 7: 16-bit rows are bound by their arithmetic (twice
-// the elements per byte; fp32 rows reach 81%).
+// the elements per byte; fp32 rows reach 81%).  4096 bf16 rows of 8192 elements:
+// 41 us forwards and 63 backwards, by the looping kernels 120 and 264.
 constexpr int kNormRegMax = 8192;
 inline int norm_tpr(int dim) {
   return dim <= 512 ? 32 : dim <= 1024 ? 128 : dim <= 2048 ? 256 : dim <= 4096 ? 512 : 1024;
@@ -757,8 +758,11 @@ cudaError_t layer_norm_t(const LayerNormArgs &a, cudaStream_t st) {
   if constexpr (sizeof(T) < 8) {
     if (a.dim <= kNormRegMax) {
       const bool vec = norm_vec<T>(a.x, a.ldx, a.dim) && norm_vec<T>(a.y, a.ldy, a.dim);
-      // Few long rows do not fill the multiprocessors with a warp each.
-      if (vec && a.dim <= 16 * 32 * Vec16<T>::N && a.rows >= 8ll * sm_count())
+      // Few long rows do not fill the multiprocessors with a warp or two each (bf16,
+      // 152 SMs, us by warps and by blocks: 304 rows of 1024 2.9 and 2.4, of 2048 4.5
+      // and 3.7, of 4096 5.0 and 5.5; 608 rows 3.3 and 3.4, 4.7 and 5.4, 5.6 and 7.2;
+      // 1216 rows 4.0 and 5.3, 5.3 and 7.0, 7.7 and 10.3).
+      if (vec && a.dim <= 16 * 32 * Vec16<T>::N && a.rows >= 4ll * sm_count())
         return layer_norm_warp<T>(a, st);
       const int grid = (int)norm_grid(a.rows, a.dim);
       return norm_dispatch<T>(a.dim, vec, [&](auto tpr, auto ept, auto v) {
@@ -777,7 +781,10 @@ cudaError_t layer_norm_t(const LayerNormArgs &a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-constexpr int kLongParts = 64;  // row ranges of the looping kernel's dw
+// Row ranges of the looping kernel's dw: with 16, 64 and 256 of them the
+// gradients of 512 bf16 rows of 12288 elements take 53, 56 and 66 us, of 64 rows
+// 31, 32 and 30, of 4096 rows 373 each.
+constexpr int kLongParts = 64;
 
 template <typename T>
 cudaError_t layer_norm_grad_t(const LayerNormGradArgs &a, cudaStream_t st) {
