@@ -30,10 +30,13 @@
 // to begin with (the state, E, U, the inverse, M, fp32 inputs) enters as the
 // sum of two fp16 values, of which the products leading x leading, leading x
 // trailing and trailing x leading are taken.  22 significand bits count that
-// way, at two to three times the products: results in fp32 are as good as
-// fp32 arithmetic's (8192 tokens: the final state 2.3e-7 off, the gradients of
-// 16384 tokens 3e-7 to 8e-7; with pairs of bf16, which need no scaling, a test
-// of 256 tokens was 6e-6 off, with single bf16 values 2e-3).
+// way, at two to three times the products: results in fp32 are about as good
+// as fp32 arithmetic's (8192 tokens: the final state 2.3e-7 off, the gradients of
+// 16384 tokens 3e-7 to 8e-7, up to 1.9 times the error of elementary fp32
+// operations; with pairs of bf16, which need no scaling, a test of 256 tokens was
+// 6e-6 off, with single bf16 values 2e-3).  What one scale covers loses digits
+// where it is small: in a chunk whose first half leaves a state of 2^12 (2^16,
+// 2^20) that a decay then drops, results of size 1 are 4e-6 (6e-5, 9e-4) off.
 #pragma once
 
 #include "seq.h"
