@@ -35,8 +35,8 @@
 // 16384 tokens 3e-7 to 8e-7, up to 1.9 times the error of elementary fp32
 // operations; with pairs of bf16, which need no scaling, a test of 256 tokens was
 // 6e-6 off, with single bf16 values 2e-3).  What one scale covers loses digits
-// where it is small: in a chunk whose first half leaves a state of 2^12 (2^16,
-// 2^20) that a decay then drops, results of size 1 are 4e-6 (6e-5, 9e-4) off.
+// where it is small: in a chunk whose first half reads a state of 2^12 (2^16,
+// 2^20) that a decay then drops, results of size 1 are 4e-6 (6e-5, 5e-4) off.
 #pragma once
 
 #include "seq.h"

@@ -201,15 +201,15 @@ __device__ __forceinline__ void delta_back(const DeltaArgs &a, const DeltaGradAr
       const float2 most = agree.largest(state_max(), max16(0.0f, x));
       const float Gamma = chunk[0], inv_s = scale_inverse(ss), smax = most.x * inv_s;
       const float os = bound_scale(most.y);
-      const float by = chunk[1] * smax + chunk[2] * most.y;
-      const float bw = fmaxf(by * chunk[3] * chunk[4], chunk[5] * most.y);
-      const float yb = fmaxf(by, fmaxf(smax, most.y) * kApart);
+      const float bx = chunk[2] * most.y;
+      const float bw = fmaxf(fmaf(chunk[7], smax, chunk[4] * bx), chunk[5] * most.y);
+      const float yb = fmaxf(fmaf(chunk[1], smax, bx), fmaxf(smax, most.y) * kApart);
       const float ys = bound_scale(yb);
       const float ws =
           bound_scale(fmaxf(bw, fmaxf(yb * fmaxf(1.0f, chunk[4]), chunk[5]) * kApart));
       const float inv_y = scale_inverse(ys);
       const float bs = fmaf(Gamma, smax, 256.0f * bw), next_ss = bound_scale(bs);
-      bounds.enter(it, 0, live ? by * chunk[3] : 0.0f, lane);
+      bounds.enter(it, 0, live ? fmaf(chunk[6], smax, chunk[3] * bx) : 0.0f, lane);
       bounds.enter(it, 1, live ? bs : 0.0f, lane);
       bounds.enter(it, 2, live ? most.y : 0.0f, lane);
 #pragma unroll

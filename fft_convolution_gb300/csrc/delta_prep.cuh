@@ -36,15 +36,20 @@
 //
 // Of the chunk: 0: Gamma, then bounds from which the scans choose the scales
 // of what they compute without looking at it first.  With |S| the largest
-// value of the state in a column of v, and K's scaled rows below 2:
-//   forward  |Y| <= |V| + b1 |S|,  |U| <= b2 |Y|,  |W| <= b3 |Y|
-//            b1 = 2 DK max gamma 2^ek,  b2 = max beta r,
-//            b3 = max Gamma/gamma 2^ek beta r,  r = row sums of |inverse|,  b4 = max r
-//   BACK     |dU| <= b1 |dS| + b2 |dO|,  |F| <= b3 |dU|,  |gamma beta F 2^ek| <= b4 |F|,
+// value of the state in a column of v, K's scaled rows below 2, c = 2 DK, and of
+// the inverse's rows r the sums of absolute values and t the same sums weighted
+// with gamma 2^ek (BACK: Gamma/gamma 2^ek) of their columns:
+//   forward  |Y| <= |V| + b1 |S|,         b1 = max c gamma 2^ek
+//            |U| <= b2 |V| + b5 |S|,      b2 = max beta r,  b5 = max c beta t
+//            |W| <= b3 |V| + b6 |S|,      the same times Gamma/gamma 2^ek
+//            |E| <= b4 |V| + b7 |S|,      b4 = max r,  b7 = max c t
+//   BACK     |dU| <= b1 |dS| + b2 |dO|,   b1 = max c Gamma/gamma 2^ek,
+//                                         b2 = max scale (row sums of |M^T|)
+//            |F| <= b3 b2 |dO| + b6 |dS|, b3 = max r,  b6 = max c t
+//            |gamma beta F 2^ek| <= b4 b2 |dO| + b7 |dS|,  the same times gamma beta 2^ek
 //            |scale gamma dO 2^eq| <= b5 |dO|
-//            b1 = 2 DK max Gamma/gamma 2^ek,  b2 = max scale (row sums of |M^T|),
-//            b3 = max r,  b4 = max gamma beta 2^ek,  b5 = max scale gamma 2^eq
-// Rounding in fp32 would leave errors of 2^-24 of these same bounds.
+// t, not r times the largest weight: what a decay drops within the chunk must not
+// set the scale of what comes behind it.
 #pragma once
 
 #include "delta.cuh"
@@ -64,10 +69,11 @@ template <typename T, int DK> constexpr size_t prep_smem() {
 // not read), or its transpose (TRANS), to the leading and trailing tile, rows
 // scaled; the rows' inverse scales go to `inv`, the sums of their absolute
 // values to `sum`.  INV: of m = R the inverse, I - R beta, or (TRANS) the
-// transpose of I - beta R.
+// transpose of I - beta R; the sums weighted with `reach` to `far`.
 template <bool TRANS, bool INV>
-__device__ __forceinline__ void write_image(const float *m, const float *beta, char *dst,
-                                            float *inv, float *sum, int tid) {
+__device__ __forceinline__ void write_image(const float *m, const float *beta, const float *reach,
+                                            char *dst, float *inv, float *sum, float *far,
+                                            int tid) {
 #pragma unroll
   for (int i = tid; i < 64 * 8; i += kPrepThreads) {
     const int r = i >> 3, c = i & 7;
@@ -88,19 +94,29 @@ __device__ __forceinline__ void write_image(const float *m, const float *beta, c
       f[4] *= -y.x; f[5] *= -y.y; f[6] *= -y.z; f[7] *= -y.w;
     }
     const int d = r - c * 8;  // the diagonal's place among the eight
-    float t = 0.0f;
+    float t = 0.0f, w = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       if (TRANS ? k < d : k > d) f[k] = 0.0f;
       if (INV && k == d) f[k] = 1.0f;
       t += fabsf(f[k]);
     }
+    if constexpr (INV) {
+      const float4 x = *reinterpret_cast<const float4 *>(reach + c * 8);
+      const float4 y = *reinterpret_cast<const float4 *>(reach + c * 8 + 4);
+      w = fmaf(fabsf(f[0]), x.x, fmaf(fabsf(f[1]), x.y, fmaf(fabsf(f[2]), x.z, fabsf(f[3]) * x.w)));
+      w = fmaf(fabsf(f[4]), y.x, fmaf(fabsf(f[5]), y.y, fmaf(fabsf(f[6]), y.z, fmaf(fabsf(f[7]), y.w, w))));
+    }
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    for (int o = 4; o > 0; o >>= 1) {
+      t += __shfl_xor_sync(0xffffffffu, t, o);
+      if constexpr (INV) w += __shfl_xor_sync(0xffffffffu, w, o);
+    }
     const float s = row_scale(lane_max<8>(max8(f)));
     if (c == 0) {
       inv[r] = scale_inverse(s);
       sum[r] = t;
+      if constexpr (INV) far[r] = w;
     }
     uint4 hi, lo;
     split8(f, s, hi, lo);
@@ -255,8 +271,9 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
   __shared__ float2 G[64];
   __shared__ float4 Gk[64];  // G, the scale of K's row
   __shared__ __align__(16) float beta_s[64];
-  __shared__ float inv_kq[2 * 64], inv[4][64], sum[4][64];
-  __shared__ float most[2][9];
+  __shared__ float inv_kq[2 * 64], inv[4][64], sum[4][64], far[2][64];
+  __shared__ __align__(16) float reach[2][64];  // gamma 2^ek, Gamma/gamma 2^ek
+  __shared__ float most[2][14];
   constexpr int NT = Terms<T>::value;
   constexpr uint32_t kPlane = 2 * (DK / 64) * kTile;  // [K; Q], one term
 
@@ -324,6 +341,10 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
       const int i = tid & 63;
       const float2 gi = G[i];
       const float fi = inv_kq[tid];
+      if (tid < 64) {
+        reach[0][i] = decay_between(gi, make_float2(0.0f, 0.0f)) * fi;
+        if constexpr (GRAD) reach[1][i] = decay_between(G[63], gi) * fi;
+      }
       float *row = (tid >= 64 ? X : L) + i * kPitch;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -345,8 +366,9 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
       }
       __syncthreads();
       char *imageb = back + (ci * a.vheads + hv) * (long long)kImageBytes;
-      write_image<false, false>(X, beta_s, image + 2 * kTile, inv[1], sum[1], tid);
-      if constexpr (GRAD) write_image<true, false>(X, beta_s, imageb + 2 * kTile, inv[3], sum[3], tid);
+      write_image<false, false>(X, beta_s, nullptr, image + 2 * kTile, inv[1], sum[1], nullptr, tid);
+      if constexpr (GRAD)
+        write_image<true, false>(X, beta_s, nullptr, imageb + 2 * kTile, inv[3], sum[3], nullptr, tid);
       __syncthreads();
       // Diagonal blocks of R: column `col` of block `warp`, R_m = A_m - sum_p
       // A_mp beta_p R_p; both halves of the warp do the same columns.
@@ -374,8 +396,9 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
       __syncthreads();
       join_blocks<16>(L, X, beta_s, tid);
       join_blocks<32>(L, X, beta_s, tid);
-      write_image<false, true>(X, beta_s, image, inv[0], sum[0], tid);
-      if constexpr (GRAD) write_image<true, true>(X, beta_s, imageb, inv[2], sum[2], tid);
+      write_image<false, true>(X, beta_s, reach[0], image, inv[0], sum[0], far[0], tid);
+      if constexpr (GRAD)
+        write_image<true, true>(X, beta_s, reach[1], imageb, inv[2], sum[2], far[1], tid);
       __syncthreads();
       if (tid < 64) {
         float *gates = reinterpret_cast<float *>(image + 4 * kTile) + tid;
@@ -384,11 +407,15 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
         const float dec = decay_between(G[63], G[tid]), bt = beta_s[tid];
         const float ga[kGates] = {-gam * ek, dec * bt * ek * et, bt * et, a.scale * gam * eq,
                                   a.scale * em, et, ek, eq};
-        const float ba = fabsf(bt) * sum[0][tid], sc = fabsf(a.scale);
-        float b[9];
+        const float ab = fabsf(bt), sc = fabsf(a.scale), t = 2.0f * DK * far[0][tid];
+        float b[14];
         b[0] = 2.0f * DK * gam * ek;
-        b[1] = ba;
-        b[2] = ba * dec * ek;
+        b[1] = ab * sum[0][tid];
+        b[2] = b[1] * (dec * ek);
+        b[3] = sum[0][tid];
+        b[4] = ab * t;
+        b[5] = b[4] * (dec * ek);
+        b[6] = t;
 #pragma unroll
         for (int k = 0; k < kGates; ++k) gates[k * 64] = ga[k];
         if (tid == 63) gates[kChunkAt - 63] = gam;
@@ -399,24 +426,26 @@ delta_prep_kernel(const DeltaArgs a, const DeltaPlan plan, char *kq, char *image
 #pragma unroll
           for (int k = 0; k < kGates; ++k) gates[k * 64] = gb[k];
           if (tid == 63) gates[kChunkAt - 63] = gam;
-          b[3] = 2.0f * DK * dec * ek;
-          b[4] = sc * sum[3][tid];
-          b[5] = sum[2][tid];
-          b[6] = gam * fabsf(bt) * ek;
-          b[7] = sc * gam * eq;
-          b[8] = sum[0][tid];
+          const float gbk = gam * ab * ek, tb = 2.0f * DK * far[1][tid];
+          b[7] = 2.0f * DK * dec * ek;
+          b[8] = sc * sum[3][tid];
+          b[9] = sum[2][tid];
+          b[10] = gbk * sum[2][tid];
+          b[11] = sc * gam * eq;
+          b[12] = tb;
+          b[13] = gbk * tb;
         }
+        // (of values that are not negative the bits are in order)
 #pragma unroll
-        for (int k = 0; k < (GRAD ? 9 : 3); ++k) {
-          b[k] = lane_max<32>(b[k]);
-          if (lane == 0) most[warp][k] = b[k];
+        for (int k = 0; k < (GRAD ? 14 : 7); ++k) {
+          const unsigned m = __reduce_max_sync(0xffffffffu, __float_as_uint(b[k]));
+          if (lane == 0) most[warp][k] = __uint_as_float(m);
         }
       }
       __syncthreads();
-      if (tid < (GRAD ? 9 : 3))
-        reinterpret_cast<float *>((tid < 3 || tid == 8 ? image : imageb) + 4 * kTile)
-            [kChunkAt + (tid < 3 ? 1 + tid : tid == 8 ? 4 : tid - 2)] =
-                fmaxf(most[0][tid], most[1][tid]);
+      if (tid < (GRAD ? 14 : 7))
+        reinterpret_cast<float *>((tid < 7 ? image : imageb) + 4 * kTile)
+            [kChunkAt + 1 + (tid < 7 ? tid : tid - 7)] = fmaxf(most[0][tid], most[1][tid]);
     }
     tc_fence_before();
   }

@@ -644,15 +644,16 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs &a, const DeltaPlan &
       const float2 most = agree.largest(state_max(), vmax);
       const float *chunk = gates_of(it) + kChunkAt;
       const float Gamma = chunk[0], inv_s = scale_inverse(ss), smax = most.x * inv_s;
-      const float by = most.y + chunk[1] * smax, bw = by * chunk[3];
-      const float yb = fmaxf(by, smax * kApart), least = yb * kApart;
+      const float bw = fmaf(chunk[6], smax, chunk[3] * most.y);
+      const float yb = fmaxf(fmaf(chunk[1], smax, most.y), smax * kApart), least = yb * kApart;
       const float ys = bound_scale(yb);
-      const float us = bound_scale(fmaxf(by * chunk[2], least * fmaxf(1.0f, chunk[2])));
+      const float us = bound_scale(
+          fmaxf(fmaf(chunk[5], smax, chunk[2] * most.y), least * fmaxf(1.0f, chunk[2])));
       const float wsc = bound_scale(fmaxf(bw, least * fmaxf(1.0f, chunk[3])));
       const float inv_y = scale_inverse(ys);
       const float bs = fmaf(Gamma, smax, 128.0f * bw), next_ss = bound_scale(bs);
       if constexpr (SAVE) {
-        bounds.enter(it, 0, live ? yb * chunk[4] : 0.0f, lane);
+        bounds.enter(it, 0, live ? fmaxf(fmaf(chunk[7], smax, chunk[4] * most.y), least) : 0.0f, lane);
         bounds.enter(it, 1, live ? bs : 0.0f, lane);
       }
 #pragma unroll

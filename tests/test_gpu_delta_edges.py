@@ -210,3 +210,21 @@ def test_gradients_of_sizes_far_apart(fg, how):
         args[0][:] *= 2.0 ** 40
         args[4][:] = 0.0
     check_gradients(fg, args, do, state, dfinal)
+
+
+# One scale per column of v holds a chunk, from a bound on what its tokens see: 2^7 to 2^8 times the
+# largest value of the state here (2 DK, keys of 1/4).  Scaled to 2^14, fp16 pairs end at 2^-25: 2^-31
+# of that value for each of the operands that one after the other carry a result of size 1 (Y, U, W),
+# whose rounding adds up over the row sums of the inverse (below 3): 2^-28.
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("larger", [0, 8, 12, 16])
+def test_what_a_dropped_state_leaves_in_its_chunk(fg, kind, larger):
+    q, k, v, g, beta = ref.inputs(81, 1, 100, 1, 2, 64, 64, TYPES[kind])
+    g[0, 32, :] = -float("inf")
+    state = 2.0 ** larger * normal(82, 1, 2, 64, 64)
+    o, s = fg.delta_rule(*cuda((q, k, v, g, beta)), initial_state=state.cuda())
+    o64, s64 = ref.forward(*(t[0] for t in (q, k, v, g, beta)), state=state[0])
+    bound = FP + 2.0 ** (larger - 28)
+    assert rel(s[0], s64) <= bound
+    for part in (slice(0, 32), slice(32, 64), slice(64, 100)):
+        assert rel(o[0, part], o64[part]) <= HALF_ULP[o.dtype] + bound, part
