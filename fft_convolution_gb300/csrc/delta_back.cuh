@@ -328,7 +328,7 @@ __device__ __forceinline__ void delta_back(const DeltaArgs &a, const DeltaGradAr
 // Both scans of the gradients in one launch: neither needs anything of the
 // other, and each has one block per sequence, head and 128 columns of v, so
 // apart they left most of the SMs idle (4 sequences of 4096 tokens, 16 heads of
-// 128 x 128, 64 blocks each: 246 + 295 us; together 348, with HBM 57% busy by
+// 128 x 128, 64 blocks each: 246 + 295 us; together 354, with HBM 57% busy by
 // what they leave).  Even blocks go forwards, odd ones backwards.
 template <typename T, int DK, bool STAGED>
 __global__ void __launch_bounds__(kScanThreads, 1)

@@ -31,7 +31,7 @@
 //
 // Each chunk and head reads 208 KB (128 x 128 heads of 16 bits) and its 16 warps
 // then work 13000 clocks on 64 x 64 and 128 x 64 accumulators, a fifth of them
-// waiting; HBM would need 9000.  16384 tokens of 16 heads: 250 us, 4.4 TB/s (as
+// waiting; HBM would need 9000.  16384 tokens of 16 heads: 258 us, 4.4 TB/s (as
 // a block per chunk that loaded and split fp32 rows itself 675).  Of its 96
 // registers per thread 16-bit types spill 44 bytes, 240 with more than 128 columns
 // of v (fp32 16 and 208).

@@ -15,10 +15,10 @@
 // series of A would cancel catastrophically for keys that repeat.
 //
 // Shared memory's latency bounds it: five blocks of four warps per SM (registers
-// and shared memory) issue 38% of the time (51% without the second image).  8192
-// tokens with 16 key and 32 value heads of 128 x 128 take 105 us, 16384 tokens of
-// 16 heads with the images for both directions, which spill 118 bytes per thread
-// in bf16, 202 (2.7 TB/s).
+// and shared memory) issue 39% of the time (49% without the second image).  8192
+// tokens with 16 key and 32 value heads of 128 x 128 take 110 us, 16384 tokens of
+// 16 heads with the images for both directions, which spill 124 bytes per thread
+// in bf16, 205 (2.6 TB/s).
 //
 // Everything is written in exactly the layout of the scans' shared memory,
 // so they fetch a chunk with two bulk copies, whatever the inputs' type,

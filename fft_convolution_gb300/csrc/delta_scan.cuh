@@ -24,10 +24,10 @@
 // The chain bounds it: a chunk takes 4900 clocks, of which the tensor cores work
 // about 1400; the rest are four trips from them through registers and back, with 65%
 // of the issue slots used.  8192 tokens of 32 heads of 128 x 128 (32 blocks,
-// 128 chunks each) take 331 us; HBM is idle meanwhile.  16-bit rows on 16-byte
+// 128 chunks each) take 333 us; HBM is idle meanwhile.  16-bit rows on 16-byte
 // boundaries (STAGED) leave the 96 registers of a thread enough for that.  Others,
 // all of fp32 among them, spill up to 94 bytes; where both scans of the gradients
-// share a kernel (delta_back.cuh) heads of 128 spill 58, not staged 126 to 250.
+// share a kernel (delta_back.cuh) heads of 128 spill 4, not staged 126 to 250.
 //
 // Roles: 16 warps of arithmetic (two per scheduler left its issue slots 60%
 // empty), one thread that issues the products, a warp that fetches the chunks'
