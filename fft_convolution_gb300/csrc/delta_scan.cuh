@@ -11,23 +11,25 @@
 // the state's columns: the state itself stays in their registers in fp32,
 // and what they hand to the tensor cores (S, Y, U, W) is scaled by a power of
 // two and split into two fp16 values.  Only P -> Y -> E -> U -> S is a chain;
-// N, U M^T, the output (their sum, in fp32: each has its own scale, and one of
-// them may be far below the other) and all loads run beside it.  So the scales do not come
-// from the values (finding the largest of a column takes the four threads a
-// barrier at each step of the chain) but from bounds on them: from the largest
-// values of V and of the state, which are found beside the chain, and the
-// chunk's bounds.  The scale brings the bound to 2^14; values down to 2^-16
-// of the bound keep all their digits.  A bound counts as kApart of what it is
-// computed from at least: the quotient of two scales stays finite then (a chunk
-// that writes nothing has a bound of 0 on U and W, however large the state).
+// N, U M^T, the output and all loads run beside it.  (Both products of the
+// output keep their own scales and meet in fp32: one may be far below the
+// other.)  So the scales do not come from the values (finding the largest of a
+// column takes the four threads a barrier at each step of the chain) but from
+// bounds on them: from the largest values of V and of the state, which are found
+// beside the chain, and the chunk's bounds.  The scale brings the bound to 2^14;
+// values down to 2^-16 of the bound keep all their digits.  A bound counts as
+// kApart of what it is computed from at least: the quotient of two scales stays
+// finite then (a chunk that writes nothing has a bound of 0 on U and W, however
+// large the state).
 //
 // The chain bounds it: a chunk takes 4900 clocks, of which the tensor cores work
-// about 1400; the rest are four trips from them through registers and back, with 65%
-// of the issue slots used.  8192 tokens of 32 heads of 128 x 128 (32 blocks,
+// about 1400; the rest are four trips from them through registers and back, with
+// 65% of the issue slots used.  8192 tokens of 32 heads of 128 x 128 (32 blocks,
 // 128 chunks each) take 333 us; HBM is idle meanwhile.  16-bit rows on 16-byte
-// boundaries (STAGED) leave the 96 registers of a thread enough for that.  Others,
-// all of fp32 among them, spill up to 94 bytes; where both scans of the gradients
-// share a kernel (delta_back.cuh) heads of 128 spill 4, not staged 126 to 250.
+// boundaries (STAGED) leave the 96 registers of a thread enough for that.
+// Others, all of fp32 among them, spill up to 94 bytes; where both scans of the
+// gradients share a kernel (delta_back.cuh) heads of 128 spill 4, not staged 126
+// to 250.
 //
 // Roles: 16 warps of arithmetic (two per scheduler left its issue slots 60%
 // empty), one thread that issues the products, a warp that fetches the chunks'
