@@ -65,6 +65,14 @@ class DeltaDesc(ctypes.Structure):
                 + [("scale", ctypes.c_double), ("dtype", ctypes.c_int), ("clear_rows", ctypes.c_int)])
 
 
+class RecurrenceDesc(ctypes.Structure):
+    """fft_recurrence_desc: sizes, strides (sequence, token; in elements),
+    types and treatment of padding of a call of the gated linear recurrence."""
+    _fields_ = ([(n, ctypes.c_int64) for n in ("batch", "tokens", "channels")]
+                + [(n + "_stride", ctypes.c_int64 * 2) for n in ("x", "g", "beta")]
+                + [(n, ctypes.c_int) for n in ("dtype", "gtype", "clear_rows")])
+
+
 SIGNATURES = {
     "fft_plan_create": (_VP, [_I64, _I64, _INT, _INT, _INT]),
     "fft_plan_create_nd": (_VP, [_INT, _VP, _I64, _INT, _INT]),
@@ -96,6 +104,19 @@ SIGNATURES = {
     "fft_delta_rule_backward_workspace_bytes": (_SZ, [_VP, _INT]),
     "fft_delta_rule_backward": (_INT, [_VP] * 17 + [_SZ, _VP]),
     "fft_delta_rule_step": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _VP]),
+    "fft_embedding": (_INT, [_VP, _INT, _VP, _I64, _VP, _I64, _I64, _I64, _I64, _DBL, _INT, _VP]),
+    "fft_embedding_workspace_bytes": (_SZ, [_I64, _I64, _INT]),
+    "fft_embedding_backward": (_INT, [_VP, _I64, _VP, _INT, _VP, _I64, _I64, _I64, _DBL, _INT, _INT,
+                                      _INT, _VP, _SZ, _VP]),
+    "fft_linear_recurrence": (_INT, [_VP] * 9),
+    "fft_linear_recurrence_backward": (_INT, [_VP] * 14),
+    "fft_linear_recurrence_step": (_INT, [_VP] * 6 + [_I64, _VP, _VP]),
+    "fft_linear_cross_entropy_workspace_bytes": (_SZ, [_VP, _I64, _VP, _I64, _I64, _I64, _I64, _INT,
+                                                       _INT]),
+    "fft_linear_cross_entropy": (_INT, [_VP, _I64, _VP, _I64, _VP, _INT, _VP, _VP, _I64, _I64, _I64,
+                                        _INT, _VP, _SZ, _VP]),
+    "fft_linear_cross_entropy_backward": (_INT, [_VP, _VP, _I64, _VP, _I64, _VP, _INT, _VP, _VP, _VP,
+                                                 _I64, _I64, _I64, _INT, _VP, _SZ, _VP]),
     "fft_debug_radix2_pass": (_INT, [_VP, _VP, _I64, _I64, _INT, _VP]),
     "fft_device_status": (_INT, [_VP]),
     "fft_debug_wait_timeout": (_INT, [_I64, _VP]),
@@ -291,6 +312,66 @@ def fft_delta_rule_step(desc: DeltaDesc, q: int, k: int, v: int, g: int, beta: i
                         slots: int, pool: int, o: int, stream: int) -> int:
     return _lib.fft_delta_rule_step(ctypes.byref(desc), q, k, v, g, beta, state, slots, pool, o,
                                     stream)
+
+
+def fft_embedding(ids: int, id_bytes: int, table: int, ldt: int, y: int, ldy: int, tokens: int,
+                  rows: int, dim: int, scale: float, dtype: int, stream: int) -> int:
+    return _lib.fft_embedding(ids, id_bytes, table, ldt, y, ldy, tokens, rows, dim, scale, dtype,
+                              stream)
+
+
+def fft_embedding_workspace_bytes(tokens: int, dim: int, dtype: int) -> int:
+    return int(_lib.fft_embedding_workspace_bytes(tokens, dim, dtype))
+
+
+def fft_embedding_backward(dy: int, lddy: int, ids: int, id_bytes: int, dtable: int, tokens: int,
+                           rows: int, dim: int, scale: float, add: int, dtype: int, ttype: int,
+                           workspace: int, workspace_bytes: int, stream: int) -> int:
+    return _lib.fft_embedding_backward(dy, lddy, ids, id_bytes, dtable, tokens, rows, dim, scale, add,
+                                       dtype, ttype, workspace, workspace_bytes, stream)
+
+
+def fft_linear_recurrence(desc: RecurrenceDesc, x: int, g: int, beta: int, offsets: int,
+                          initial_state: int, y: int, final_state: int, stream: int) -> int:
+    return _lib.fft_linear_recurrence(ctypes.byref(desc), x, g, beta, offsets, initial_state, y,
+                                      final_state, stream)
+
+
+def fft_linear_recurrence_backward(desc: RecurrenceDesc, dy: int, x: int, g: int, beta: int, y: int,
+                                   offsets: int, initial_state: int, dfinal_state: int, dx: int,
+                                   dg: int, dbeta: int, dinitial_state: int, stream: int) -> int:
+    return _lib.fft_linear_recurrence_backward(ctypes.byref(desc), dy, x, g, beta, y, offsets,
+                                               initial_state, dfinal_state, dx, dg, dbeta,
+                                               dinitial_state, stream)
+
+
+def fft_linear_recurrence_step(desc: RecurrenceDesc, x: int, g: int, beta: int, state: int, slots: int,
+                               pool: int, y: int, stream: int) -> int:
+    return _lib.fft_linear_recurrence_step(ctypes.byref(desc), x, g, beta, state, slots, pool, y,
+                                           stream)
+
+
+def fft_linear_cross_entropy_workspace_bytes(x: int, ldx: int, w: int, ldw: int, tokens: int,
+                                             vocabulary: int, dim: int, dtype: int,
+                                             backward: int) -> int:
+    return int(_lib.fft_linear_cross_entropy_workspace_bytes(x, ldx, w, ldw, tokens, vocabulary, dim,
+                                                             dtype, backward))
+
+
+def fft_linear_cross_entropy(x: int, ldx: int, w: int, ldw: int, targets: int, target_bytes: int,
+                             loss: int, lse: int, tokens: int, vocabulary: int, dim: int, dtype: int,
+                             workspace: int, workspace_bytes: int, stream: int) -> int:
+    return _lib.fft_linear_cross_entropy(x, ldx, w, ldw, targets, target_bytes, loss, lse, tokens,
+                                         vocabulary, dim, dtype, workspace, workspace_bytes, stream)
+
+
+def fft_linear_cross_entropy_backward(dloss: int, x: int, ldx: int, w: int, ldw: int, targets: int,
+                                      target_bytes: int, lse: int, dx: int, dw: int, tokens: int,
+                                      vocabulary: int, dim: int, dtype: int, workspace: int,
+                                      workspace_bytes: int, stream: int) -> int:
+    return _lib.fft_linear_cross_entropy_backward(dloss, x, ldx, w, ldw, targets, target_bytes, lse,
+                                                  dx, dw, tokens, vocabulary, dim, dtype, workspace,
+                                                  workspace_bytes, stream)
 
 
 def fft_debug_radix2_pass(in_ptr: int, out_ptr: int, n: int, half: int, dtype: int,
@@ -582,7 +663,9 @@ def fftn(x, ndim: int, direction: int = FFT_FORWARD, out=None, stream=None):
 # ---- operators of sequence models (tensor helpers in sequence.py) ---------------
 
 _SEQUENCE = ("layer_norm", "layer_norm_backward", "grad_norm", "clip_grad_norm", "delta_rule",
-             "delta_rule_backward", "delta_rule_step")
+             "delta_rule_backward", "delta_rule_step", "embedding", "embedding_backward",
+             "linear_recurrence", "linear_recurrence_backward", "linear_recurrence_step",
+             "linear_cross_entropy", "linear_cross_entropy_backward")
 
 
 def __getattr__(name):

@@ -1,0 +1,472 @@
+// embed.cu -- embedding of tokens and its gradient.
+//
+//   y_n = scale T[id_n]             (0 where id_n names no row)
+//   dT[v] = scale sum of dy_n over the n with id_n = v   (+ dT[v] before)
+//
+// The gradient adds in one order whatever the timing: the tokens are sorted by
+// row, equal rows in the order of the tokens (embed_sort_kernel), cut into
+// pieces of 32 whatever the runs of equal rows are -- text has a few rows with
+// a tenth of all tokens -- and summed piece by piece (embed_sum_kernel); runs
+// that cross pieces leave one partial row per piece, which embed_join_kernel
+// adds in the order of the pieces.
+#include "cluster.cuh"
+#include "seq.h"
+
+namespace fftgb {
+
+namespace {
+
+// ---- lookup --------------------------------------------------------------------
+
+__device__ __forceinline__ long long token_id(const void *ids, int id_bytes, long long n) {
+  return id_bytes == 8 ? static_cast<const long long *>(ids)[n]
+                       : (long long)static_cast<const int *>(ids)[n];
+}
+
+// blockDim.x threads along a row, blockDim.y rows.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) embed_kernel(const EmbedArgs a) {
+  using A = typename Acc<T>::type;
+  constexpr int E = VEC ? 16 / (int)sizeof(T) : 1;
+  const A scale = (A)a.scale;
+  const int units = a.dim / E;
+  for (long long n = (long long)blockIdx.x * blockDim.y + threadIdx.y; n < a.tokens;
+       n += (long long)gridDim.x * blockDim.y) {
+    const long long id = token_id(a.ids, a.id_bytes, n);
+    const bool there = id >= 0 && id < a.rows;
+    const T *src = static_cast<const T *>(a.table) + (there ? id : 0) * a.ldt;
+    T *dst = static_cast<T *>(a.y) + n * a.ldy;
+#pragma unroll 4
+    for (int c = threadIdx.x; c < units; c += blockDim.x) {
+      if constexpr (VEC) {
+        A f[E];
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (there) {
+          unpack<T>(__ldg(reinterpret_cast<const uint4 *>(src) + c), f);
+#pragma unroll
+          for (int i = 0; i < E; ++i) f[i] *= scale;
+          w = pack<T>(f);
+        }
+        reinterpret_cast<uint4 *>(dst)[c] = w;
+      } else {
+        dst[c] = there ? from_acc<T>(to_acc(src[c]) * scale) : from_acc<T>((A)0);
+      }
+    }
+  }
+}
+
+// ---- tokens in the order of their rows -----------------------------------------------
+
+constexpr int kSortBlocks = 8, kSortThreads = 1024, kSortBits = 9, kDigits = 1 << kSortBits;
+
+struct SortShared {
+  unsigned count[kSortThreads / 32][kDigits];  // of a tile, by warp; then where each warp's go
+  unsigned base[kDigits];                      // where the next of a digit goes
+  unsigned hist[kDigits];                      // of this block's tokens
+  unsigned sums[kSortThreads / 32];
+};
+
+// A stable radix sort of (row, token) by one cluster: each block has an eighth
+// of the tokens, digits of at most 9 bits, the arrays between the passes in
+// global memory (the L2 holds them).  Tokens of no row sort behind all others.
+// The clusters beside it meanwhile write the zeros of the rows that no token
+// names: 2 passes over 16384 tokens hide behind 268 MB of them.
+__global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThreads)
+embed_sort_kernel(const EmbedSortArgs a) {
+  extern __shared__ __align__(16) char smem[];
+  SortShared &s = *reinterpret_cast<SortShared *>(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (blockIdx.x >= kSortBlocks) {
+    const long long threads = (long long)(gridDim.x - kSortBlocks) * kSortThreads;
+    const long long at = (long long)(blockIdx.x - kSortBlocks) * kSortThreads + tid;
+    char *p = static_cast<char *>(a.fill);
+    // the table's gradient starts on a boundary of its elements: 2 bytes at least
+    long long head = (16 - ((uintptr_t)p & 15)) & 15;
+    if (head > a.fill_bytes) head = a.fill_bytes;
+    const long long words = (a.fill_bytes - head) >> 4, done = head + (words << 4);
+    for (long long i = 2 * at; i < head; i += 2 * threads) *reinterpret_cast<uint16_t *>(p + i) = 0;
+    for (long long i = at; i < words; i += threads)
+      reinterpret_cast<uint4 *>(p + head)[i] = make_uint4(0, 0, 0, 0);
+    for (long long i = done + 2 * at; i < a.fill_bytes; i += 2 * threads)
+      *reinterpret_cast<uint16_t *>(p + i) = 0;
+    return;
+  }
+  const unsigned rank = block_rank();
+  const long long share = (a.tokens + kSortBlocks - 1) / kSortBlocks;
+  const long long begin = min(share * rank, a.tokens), end = min(begin + share, a.tokens);
+  const unsigned mask = (1u << a.bits) - 1;
+  for (int d = tid; d < kDigits * (kSortThreads / 32); d += kSortThreads) (&s.count[0][0])[d] = 0;
+
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const unsigned *key = a.key[pass & 1], *pos = a.pos[pass & 1];
+    unsigned *key2 = a.key[(pass & 1) ^ 1], *pos2 = a.pos[(pass & 1) ^ 1];
+    const int shift = pass * a.bits;
+    auto key_of = [&](long long i) {
+      if (pass > 0) return __ldcg(key + i);
+      const long long id = token_id(a.ids, a.id_bytes, i);
+      return id >= 0 && id < a.rows ? (unsigned)id : (unsigned)a.rows;
+    };
+    for (int d = tid; d < kDigits; d += kSortThreads) s.hist[d] = 0;
+    __syncthreads();
+    // whole warps: equal digits of a warp are added at once
+    for (long long i0 = begin; i0 < end; i0 += kSortThreads) {
+      const long long i = i0 + tid;
+      const unsigned d = i < end ? (key_of(i) >> shift) & mask : ~0u;
+      const unsigned same = __match_any_sync(0xffffffffu, d);
+      if (i < end && (same & ((1u << lane) - 1)) == 0) atomicAdd(&s.hist[d], (unsigned)__popc(same));
+    }
+    cluster_sync();
+    // where this block's first token of each digit goes: behind all smaller
+    // digits and the same digit of the blocks before
+    unsigned total = 0, before = 0;
+    if (tid < kDigits) {
+      const uint32_t mine = (uint32_t)__cvta_generic_to_shared(&s.hist[tid]);
+#pragma unroll
+      for (unsigned r = 0; r < kSortBlocks; ++r) {
+        const unsigned n = peer_load(peer(mine, r));
+        total += n;
+        if (r < rank) before += n;
+      }
+    }
+    unsigned incl = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) s.sums[warp] = incl;
+    __syncthreads();
+    if (tid < kDigits) {
+      unsigned lower = 0;
+      for (int w = 0; w < warp; ++w) lower += s.sums[w];
+      s.base[tid] = lower + incl - total + before;
+    }
+    __syncthreads();
+    for (long long i0 = begin; i0 < end; i0 += kSortThreads) {
+      const long long i = i0 + tid;
+      const bool on = i < end;
+      const unsigned k = on ? key_of(i) : 0, p = on ? (pass > 0 ? __ldcg(pos + i) : (unsigned)i) : 0;
+      const unsigned d = on ? (k >> shift) & mask : ~0u;
+      const unsigned same = __match_any_sync(0xffffffffu, d);
+      const int ahead = __popc(same & ((1u << lane) - 1));
+      if (on && ahead == 0) s.count[warp][d] = (unsigned)__popc(same);
+      __syncthreads();
+      if (tid < kDigits) {
+        unsigned run = s.base[tid];
+#pragma unroll 8
+        for (int w = 0; w < kSortThreads / 32; ++w) {
+          const unsigned n = s.count[w][tid];
+          s.count[w][tid] = run;
+          run += n;
+        }
+        s.base[tid] = run;
+      }
+      __syncthreads();
+      if (on) {
+        const unsigned to = s.count[warp][d] + (unsigned)ahead;
+        key2[to] = k;
+        pos2[to] = p;
+      }
+      __syncthreads();
+      for (int e = tid; e < kDigits * (kSortThreads / 32); e += kSortThreads) (&s.count[0][0])[e] = 0;
+      __syncthreads();
+    }
+    __threadfence();
+    cluster_sync();  // the next pass reads what every block has written; counters are free
+  }
+}
+
+// ---- sums ------------------------------------------------------------------------
+
+constexpr int kPiece = 32;  // tokens: a lane each for their rows and places
+
+// The columns of a warp: `E` per lane, whole 16 bytes or 32 apart.
+template <typename T, bool VEC> struct Columns {
+  using A = typename Acc<T>::type;
+  static constexpr int E = VEC ? 16 / (int)sizeof(T) : 4;
+  static constexpr int kWide = 32 * E;
+  static __device__ __forceinline__ int at(int chunk, int lane, int i) {
+    return chunk * kWide + (VEC ? lane * E + i : lane + 32 * i);
+  }
+  static __device__ __forceinline__ void load(const T *row, int chunk, int lane, int dim, A (&f)[E]) {
+    if constexpr (VEC) {
+      const int c = at(chunk, lane, 0);
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (c < dim) w = __ldg(reinterpret_cast<const uint4 *>(row + c));
+      unpack<T>(w, f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int c = at(chunk, lane, i);
+        f[i] = c < dim ? to_acc(row[c]) : (A)0;
+      }
+    }
+  }
+};
+
+// Writes a row of the table's gradient, of type TO (T or float).
+template <typename T, typename TO, bool VEC, int E>
+__device__ __forceinline__ void put_row(const EmbedSumArgs &a, unsigned row, int chunk, int lane,
+                                        const typename Acc<T>::type (&f)[E]) {
+  using A = typename Acc<T>::type;
+  using C = Columns<T, VEC>;
+  TO *dst = static_cast<TO *>(a.dtable) + (long long)row * a.dim;
+  const A scale = (A)a.scale;
+  if constexpr (VEC) {
+    const int c = C::at(chunk, lane, 0);
+    if (c >= a.dim) return;
+    constexpr int P = 16 / (int)sizeof(TO);
+#pragma unroll
+    for (int j = 0; j < E / P; ++j) {
+      A v[P];
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[i] = f[j * P + i] * scale;
+      uint4 *p = reinterpret_cast<uint4 *>(dst + c) + j;
+      if (a.add) {
+        A old[P];
+        unpack<TO>(*p, old);
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] += old[i];
+      }
+      *p = pack<TO>(v);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int c = C::at(chunk, lane, i);
+      if (c < a.dim) {
+        const A v = f[i] * scale;
+        dst[c] = from_acc<TO>(a.add ? v + (A)to_acc(dst[c]) : v);
+      }
+    }
+  }
+}
+
+// One warp per piece of the sorted tokens and chunk of columns.
+template <typename T, typename TO, bool VEC>
+__global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedSumArgs a) {
+  using A = typename Acc<T>::type;
+  using C = Columns<T, VEC>;
+  constexpr int E = C::E, U = 8;
+  const int lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int chunks = (a.dim + C::kWide - 1) / C::kWide;
+  const long long piece = item / chunks;
+  const int chunk = (int)(item - piece * chunks);
+  const long long first = piece * kPiece;
+  if (first >= a.tokens) return;
+  const int count = (int)min((long long)kPiece, a.tokens - first);
+  const unsigned none = (unsigned)a.rows;
+  const unsigned key = lane < count ? a.key[first + lane] : none;
+  const unsigned pos = lane < count ? a.pos[first + lane] : 0;
+  const unsigned prev = first > 0 ? a.key[first - 1] : none;
+  const unsigned next = first + count < a.tokens ? a.key[first + count] : none;
+  const T *dy = static_cast<const T *>(a.dy);
+  A *partial = static_cast<A *>(a.partial) + piece * 2 * a.ldp;
+  A acc[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) acc[i] = 0;
+  unsigned cur = __shfl_sync(0xffffffffu, key, 0);
+  if (cur == none) return;  // sorted: nothing but padding from here on
+  bool open = cur == prev;  // the run comes from the piece before
+  auto flush = [&](bool goes_on) {
+    if (!open && !goes_on) {
+      put_row<T, TO, VEC, E>(a, cur, chunk, lane, acc);
+    } else {
+      A *to = partial + (open ? 0 : a.ldp);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int c = C::at(chunk, lane, i);
+        if (c < a.dim) to[c] = acc[i];
+      }
+    }
+  };
+  for (int j0 = 0; j0 < count; j0 += U) {
+    A f[U][E];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = min(j0 + u, kPiece - 1);
+      const unsigned k = __shfl_sync(0xffffffffu, key, j), p = __shfl_sync(0xffffffffu, pos, j);
+      const int dim = k == none || j0 + u >= count ? 0 : a.dim;
+      C::load(dy + (long long)p * a.lddy, chunk, lane, dim, f[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const unsigned k = j0 + u < count ? __shfl_sync(0xffffffffu, key, j0 + u) : cur;
+      if (k != cur) {
+        flush(false);
+        if (k == none) return;
+        cur = k;
+        open = false;
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = 0;
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) acc[i] += f[u][i];
+    }
+  }
+  flush(cur == next);
+}
+
+// The runs that go on behind a piece: its own part, then the heads of the
+// pieces behind it.
+template <typename T, typename TO, bool VEC>
+__global__ void __launch_bounds__(128) embed_join_kernel(const EmbedSumArgs a) {
+  using A = typename Acc<T>::type;
+  using C = Columns<T, VEC>;
+  constexpr int E = C::E, U = 8;
+  const int lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int chunks = (a.dim + C::kWide - 1) / C::kWide;
+  const long long piece = item / chunks;
+  const int chunk = (int)(item - piece * chunks);
+  const long long behind = (piece + 1) * kPiece;
+  if (behind >= a.tokens) return;
+  const unsigned row = a.key[behind - 1];
+  if (row == (unsigned)a.rows || a.key[behind] != row) return;
+  const long long first = piece * kPiece;
+  if (first > 0 && a.key[first] == row && a.key[first - 1] == row) return;  // began further ahead
+  long long lo = behind, hi = a.tokens;  // the last token of the row is before hi
+  while (hi - lo > 1) {
+    const long long mid = lo + (hi - lo) / 2;
+    if (a.key[mid] == row) lo = mid;
+    else hi = mid;
+  }
+  const long long last = lo / kPiece;
+  const A *partial = static_cast<const A *>(a.partial);
+  A acc[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int c = C::at(chunk, lane, i);
+    acc[i] = c < a.dim ? partial[(piece * 2 + 1) * a.ldp + c] : (A)0;
+  }
+  for (long long q = piece + 1; q <= last; q += U) {
+    A f[U][E];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int c = C::at(chunk, lane, i);
+        f[u][i] = q + u <= last && c < a.dim ? partial[(q + u) * 2 * a.ldp + c] : (A)0;
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < E; ++i) acc[i] += f[u][i];
+  }
+  put_row<T, TO, VEC, E>(a, row, chunk, lane, acc);
+}
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+template <typename T> cudaError_t lookup_t(const EmbedArgs &a, cudaStream_t st) {
+  const bool vec = (a.dim * sizeof(T)) % 16 == 0 && (a.ldt * sizeof(T)) % 16 == 0 &&
+                   (a.ldy * sizeof(T)) % 16 == 0 && aligned16(a.table) && aligned16(a.y);
+  const int units = vec ? a.dim / (16 / (int)sizeof(T)) : a.dim;
+  int tx = 8;  // four units of a row per thread, 8 .. 256 threads per row
+  while (tx < 256 && tx * 4 < units) tx *= 2;
+  const int ty = 256 / tx;
+  const long long most = (long long)sm_count() * 32, need = (a.tokens + ty - 1) / ty;
+  if (most <= 0) return cudaErrorInvalidDevice;
+  const dim3 block(tx, ty);
+  const unsigned grid = (unsigned)(need < most ? need : most);
+  if (vec) embed_kernel<T, true><<<grid, block, 0, st>>>(a);
+  else embed_kernel<T, false><<<grid, block, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, typename TO, bool VEC>
+cudaError_t sums_t(const EmbedSumArgs &a, cudaStream_t st) {
+  const long long chunks = (a.dim + Columns<T, VEC>::kWide - 1) / Columns<T, VEC>::kWide;
+  const long long pieces = (a.tokens + kPiece - 1) / kPiece;
+  const long long blocks = (pieces * chunks + 3) / 4;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  embed_sum_kernel<T, TO, VEC><<<(unsigned)blocks, 128, 0, st>>>(a);
+  if (pieces > 1) embed_join_kernel<T, TO, VEC><<<(unsigned)blocks, 128, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, typename TO> cudaError_t sums_to(const EmbedSumArgs &a, cudaStream_t st) {
+  const bool vec = (a.dim * sizeof(T)) % 16 == 0 && (a.lddy * sizeof(T)) % 16 == 0 &&
+                   (a.dim * sizeof(TO)) % 16 == 0 && aligned16(a.dy) && aligned16(a.dtable);
+  return vec ? sums_t<T, TO, true>(a, st) : sums_t<T, TO, false>(a, st);
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+size_t list_bytes(long long tokens) { return round256((size_t)tokens * 4); }
+
+}  // namespace
+
+size_t embed_workspace_bytes(long long tokens, int dim, int dtype) {
+  if (tokens == 0) return 0;
+  const size_t pieces = (size_t)(tokens + kPiece - 1) / kPiece;
+  return 4 * list_bytes(tokens) + pieces * 2 * (size_t)dim * (dtype == FFT_ELEM_F64 ? 8 : 4);
+}
+
+cudaError_t launch_embed(int dtype, const EmbedArgs &a, cudaStream_t st) {
+  switch (dtype) {
+    case FFT_ELEM_F32: return lookup_t<float>(a, st);
+    case FFT_ELEM_F64: return lookup_t<double>(a, st);
+    case FFT_ELEM_BF16: return lookup_t<__nv_bfloat16>(a, st);
+    default: return lookup_t<__half>(a, st);
+  }
+}
+
+cudaError_t launch_embed_grad(int dtype, int ttype, const EmbedGradArgs &g, void *workspace,
+                              cudaStream_t st) {
+  const size_t table_bytes = (size_t)g.rows * (size_t)g.dim * elem_bytes(ttype);
+  if (g.tokens == 0)
+    return g.add ? cudaSuccess : cudaMemsetAsync(g.dtable, 0, table_bytes, st);
+  char *ws = static_cast<char *>(workspace);
+  const size_t list = list_bytes(g.tokens);
+  EmbedSortArgs s{};
+  s.ids = g.ids;
+  s.id_bytes = g.id_bytes;
+  s.tokens = g.tokens;
+  s.rows = g.rows;
+  for (int i = 0; i < 2; ++i) {
+    s.key[i] = reinterpret_cast<unsigned *>(ws + 2 * i * list);
+    s.pos[i] = reinterpret_cast<unsigned *>(ws + (2 * i + 1) * list);
+  }
+  int bits = 0;  // of the largest key, which is `rows`
+  while (bits < 32 && ((unsigned long long)g.rows >> bits) != 0) ++bits;
+  s.passes = (bits + kSortBits - 1) / kSortBits;
+  s.bits = (bits + s.passes - 1) / s.passes;
+  s.fill = g.add ? nullptr : g.dtable;
+  s.fill_bytes = g.add ? 0 : (long long)table_bytes;
+  // one cluster fills 4 MB before another is worth its launch
+  long long fillers = (s.fill_bytes + (4ll << 20) - 1) >> 22;
+  const long long most = 2 * (sm_count() / kSortBlocks);
+  if (fillers > most) fillers = most;
+  static DeviceOnce once;
+  cudaError_t e = smem_limit_once((const void *)embed_sort_kernel, sizeof(SortShared), once);
+  if (e != cudaSuccess) return e;
+  embed_sort_kernel<<<(unsigned)(kSortBlocks * (1 + fillers)), kSortThreads, sizeof(SortShared),
+                      st>>>(s);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  EmbedSumArgs a{};
+  a.dy = g.dy;
+  a.lddy = g.lddy;
+  a.key = s.key[s.passes & 1];
+  a.pos = s.pos[s.passes & 1];
+  a.tokens = g.tokens;
+  a.rows = g.rows;
+  a.dim = g.dim;
+  a.ldp = g.dim;
+  a.partial = ws + 4 * list;
+  a.dtable = g.dtable;
+  a.scale = g.scale;
+  a.add = g.add;
+  switch (dtype) {
+    case FFT_ELEM_F32: return sums_to<float, float>(a, st);
+    case FFT_ELEM_F64: return sums_to<double, double>(a, st);
+    case FFT_ELEM_BF16:
+      return ttype == FFT_ELEM_F32 ? sums_to<__nv_bfloat16, float>(a, st)
+                                   : sums_to<__nv_bfloat16, __nv_bfloat16>(a, st);
+    default:
+      return ttype == FFT_ELEM_F32 ? sums_to<__half, float>(a, st) : sums_to<__half, __half>(a, st);
+  }
+}
+
+}  // namespace fftgb

@@ -1,0 +1,264 @@
+// pair_gemm.cuh -- matrix products of 16-bit operands on pairs of
+// multiprocessors (tcgen05, cta_group::2), as a frame that the kernels of the
+// cross entropy fill with their own order of tiles and their own use of a
+// finished tile.
+//
+// A cluster of two blocks works on one tile of 256 x 256: each block stages
+// 128 rows of A and 128 of B per 64 summed indexes (32 KB; six stages), and
+// gets the tile's 128 upper or lower rows as fp32 in its tensor memory, where
+// two tiles fit: one is summed while the other is read out.  The pair is what
+// lets the tensor cores run: a block alone would have to load twice the bytes
+// of B per product (96 bytes per clock and SM at the full rate, which the L2
+// does not deliver to all SMs at once; so it is 64).
+//
+// Warp 0 issues the loads (TMA, 128-byte swizzle), warp 1 of the even block
+// the products, warps 4 to 11 read the tiles out: 64 KB of values per tile
+// and block, half the columns to each four warps.
+#pragma once
+
+#include <cuda.h>
+
+#include "cluster.cuh"
+#include "seq.h"
+#include "tcgen05.cuh"
+
+namespace fftgb {
+
+constexpr int kPairTile = 256, kPairK = 64, kPairStages = 6;
+constexpr int kPairThreads = 384, kOutWarps = 8;
+constexpr uint32_t kStageHalf = 128 * 128;  // bytes of A (of B) per stage and block
+constexpr size_t kPairSmem = 1024 + (size_t)kPairStages * 2 * kStageHalf;
+
+// ---- instructions for a pair of blocks -------------------------------------------------
+
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t *slot) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                   smem_u32(slot))
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_free(uint32_t base) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(base) : "memory");
+}
+// A box of a tensor of three axes into this block's shared memory, counted by
+// the barrier at the cluster address `bar`.
+__device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x,
+                                          int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// D (TMEM of both blocks) (+)= A (shared, half the rows each) B (shared, half the columns each).
+__device__ __forceinline__ void pair_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                         bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "n"(kDescHigh)
+      : "memory");
+}
+// One arrival at the barrier of both blocks when the products so far have completed.
+__device__ __forceinline__ void pair_commit(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+// Whether the phase has completed, other blocks' writes before it seen.
+__device__ __forceinline__ bool poll_cluster(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *failed,
+                                             int *status) {
+  if (poll_cluster(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t it = 0; it < (1u << 24); ++it) {
+    if (poll_cluster(bar, parity)) return true;
+    if (*failed || clock64() - t0 > 8000000000ll) break;  // about 4 s
+  }
+  *failed = 1;
+  atomicExch(status, 1);  // kDeviceErrorTimeout
+  return false;
+}
+
+// ---- a tile's work ---------------------------------------------------------------------
+
+// One tile of A B^T summed over blocks k0 .. k1 - 1 of 64 indexes, for every
+// pair of parts.  K-major operands have their rows along `row`; MN-major
+// ones have the summed index along their rows, from row kbase on.
+struct PairTile {
+  int a_row, b_row;    // first row of the tile in A and B
+  int k0, k1;          // blocks of summed indexes
+  int a_base, b_base;  // row of summed index 0 in an MN-major operand
+};
+// A problem's operands.
+struct PairOperands {
+  CUtensorMap a, b;
+  int a_mn, b_mn;
+  uint32_t idesc;
+  // Products of parts: an fp32 operand is the sum of three bf16 parts, of
+  // which the six largest products are taken, the smallest first.
+  int parts;
+};
+__device__ __forceinline__ int part_pairs(int parts) { return parts == 1 ? 1 : 6; }
+__device__ __forceinline__ void part_pair(int parts, int q, int &pa, int &pb) {
+  // (2,0) (0,2) (1,1) (1,0) (0,1) (0,0)
+  pa = parts == 1 ? 0 : (0x001102 >> (4 * q)) & 15;
+  pb = parts == 1 ? 0 : (0x010120 >> (4 * q)) & 15;
+}
+
+struct PairShared {
+  uint64_t full[kPairStages], empty[kPairStages], ready[2], taken[2], done;
+  uint32_t tmem;
+  int failed;
+};
+
+// Runs the tiles pair, pair + pairs, ... < tiles.  of(t, &which) gives a tile
+// and which of the problems `ops` it belongs to; out(t, address of this
+// warp's lanes in TMEM) uses one, in warps 4 .. 11: warp w has lanes
+// 32 (w % 4) .. and columns 128 ((w - 4) / 4) .. of the tile's half.
+template <class Of, class Out>
+__device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int *status, Of of,
+                                         Out out) {
+  extern __shared__ char smem_raw[];
+  __shared__ PairShared sh;
+  const uint32_t stage0 = (smem_u32(smem_raw) + 1023) & ~1023u;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const uint32_t rank = block_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  volatile int *failed = &sh.failed;
+  if (tid == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      bar_init(&sh.full[s], 1);
+      bar_init(&sh.empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&sh.ready[i], 1);
+      bar_init(&sh.taken[i], 2 * kOutWarps);
+    }
+    bar_init(&sh.done, 1);
+    sh.failed = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) pair_tmem_alloc(&sh.tmem);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tm = sh.tmem;
+
+  if (warp == 0) {
+    if (elect_one()) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < tiles; t += pairs) {
+        int which = 0;
+        const PairTile w = of(t, which);
+        const PairOperands &p = ops[which];
+        const int a_row = w.a_row + (int)rank * 128, b_row = w.b_row + (int)rank * 128;
+        const int nq = part_pairs(p.parts);
+        for (int q = 0; ok && q < nq; ++q) {
+          int pa, pb;
+          part_pair(p.parts, q, pa, pb);
+          for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
+            const uint32_t s = it % kPairStages, round = it / kPairStages;
+            if (round > 0 && !wait_cluster(&sh.empty[s], (round - 1) & 1, failed, status)) {
+              ok = false;
+              break;
+            }
+            if (rank == 0) bar_arrive_tx(&sh.full[s], 4 * kStageHalf);
+            const uint32_t bar = peer(smem_u32(&sh.full[s]), 0);
+            const uint32_t sa = stage0 + s * 2 * kStageHalf, sb = sa + kStageHalf;
+            const int k = kb * kPairK;
+            if (p.a_mn) {
+              pair_load(sa, &p.a, bar, a_row, w.a_base + k, pa);
+              pair_load(sa + kStageHalf / 2, &p.a, bar, a_row + 64, w.a_base + k, pa);
+            } else {
+              pair_load(sa, &p.a, bar, k, a_row, pa);
+            }
+            if (p.b_mn) {
+              pair_load(sb, &p.b, bar, b_row, w.b_base + k, pb);
+              pair_load(sb + kStageHalf / 2, &p.b, bar, b_row + 64, w.b_base + k, pb);
+            } else {
+              pair_load(sb, &p.b, bar, k, b_row, pb);
+            }
+          }
+        }
+      }
+      if (*failed && rank == 0)  // given up: no copy may land after the blocks have gone
+        for (uint32_t i = it > kPairStages ? it - kPairStages : 0; i < it; ++i)
+          bar_wait(&sh.full[i % kPairStages], (i / kPairStages) & 1);
+    }
+  } else if (warp == 1 && rank == 0) {
+    if (elect_one()) {
+      uint32_t it = 0;
+      bool ok = true;
+      int n = 0;
+      for (int t = pair; ok && t < tiles; t += pairs, ++n) {
+        int which = 0;
+        const PairTile w = of(t, which);
+        const PairOperands &p = ops[which];
+        const int acc = n & 1;
+        if (n > 1 && !wait_cluster(&sh.taken[acc], ((n >> 1) - 1) & 1, failed, status)) break;
+        tc_fence_after();
+        const int blocks = (w.k1 - w.k0) * part_pairs(p.parts);
+        // 16 summed indexes: 32 bytes of a K-major row, 16 rows of an MN-major tile
+        const uint32_t step_a = p.a_mn ? 2048 : 32, step_b = p.b_mn ? 2048 : 32;
+        for (int kb = 0; kb < blocks; ++kb, ++it) {
+          const uint32_t s = it % kPairStages;
+          if (!wait_cluster(&sh.full[s], (it / kPairStages) & 1, failed, status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = stage0 + s * 2 * kStageHalf, sb = sa + kStageHalf;
+#pragma unroll
+          for (uint32_t k = 0; k < kPairK / 16; ++k)
+            pair_mma(tm + acc * kPairTile, tile_desc(sa + k * step_a, kStageHalf / 2),
+                     tile_desc(sb + k * step_b, kStageHalf / 2), p.idesc, kb > 0 || k > 0);
+          pair_commit(&sh.empty[s]);
+        }
+        if (ok) pair_commit(&sh.ready[acc]);
+      }
+      if (*failed) {  // no product may write tensor memory that has been given back
+        pair_commit(&sh.done);
+        bar_wait(&sh.done, 0);
+      }
+    }
+  } else if (warp >= 4) {
+    int n = 0;
+    const uint32_t base = tm + ((uint32_t)(warp & 3) << 21) + (uint32_t)((warp - 4) >> 2) * 128;
+    for (int t = pair; t < tiles; t += pairs, ++n) {
+      const int acc = n & 1;
+      if (!wait_cluster(&sh.ready[acc], (n >> 1) & 1, failed, status)) break;
+      __syncwarp();
+      tc_fence_after();
+      out(t, base + acc * kPairTile);
+      tc_fence_before();
+      __syncwarp();
+      if ((tid & 31) == 0) arrive_at(peer(smem_u32(&sh.taken[acc]), 0));
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 2) pair_tmem_free(tm);
+}
+
+}  // namespace fftgb

@@ -105,6 +105,101 @@ DeltaClear delta_clear(const DeltaArgs &a, const DeltaGradArgs *g, size_t elem);
 cudaError_t launch_delta_plan(const int *offsets, long long batch, long long tokens, int *row0,
                               int *chunk0, const DeltaClear &clear, cudaStream_t st);
 
+// ---- embedding of tokens (embed.cu) ----------------------------------------------
+
+struct EmbedArgs {
+  const void *ids;
+  int id_bytes;  // 4 or 8
+  const void *table;
+  void *y;
+  long long tokens, rows, ldt, ldy;
+  int dim;
+  double scale;
+};
+struct EmbedGradArgs {
+  const void *dy, *ids;
+  int id_bytes;
+  void *dtable;  // rows x dim
+  long long tokens, rows, lddy;
+  int dim;
+  double scale;
+  bool add;  // to what dtable holds
+};
+// The tokens sorted by row, and bytes to clear meanwhile.
+struct EmbedSortArgs {
+  const void *ids;
+  int id_bytes;
+  long long tokens, rows;
+  int passes, bits;
+  unsigned *key[2], *pos[2];  // row (tokens of no row: `rows`) and token; pass p reads [p & 1]
+  void *fill;
+  long long fill_bytes;
+};
+struct EmbedSumArgs {
+  const void *dy;
+  const unsigned *key, *pos;
+  void *dtable, *partial;  // partial: [piece][head, tail][ldp] accumulators
+  long long tokens, rows, lddy, ldp;
+  int dim;
+  double scale;
+  bool add;
+};
+size_t embed_workspace_bytes(long long tokens, int dim, int dtype);
+cudaError_t launch_embed(int dtype, const EmbedArgs &a, cudaStream_t st);
+cudaError_t launch_embed_grad(int dtype, int ttype, const EmbedGradArgs &a, void *workspace,
+                              cudaStream_t st);
+
+// ---- the gated linear recurrence (recur_*.cu) ---------------------------------------
+
+// Strides in elements: sequence (unused for packed rows) and token.
+struct RecurStride {
+  long long seq, tok;
+};
+struct RecurArgs {
+  const void *x, *g, *beta;  // beta may be null (1)
+  RecurStride sx, sg, sb;
+  const int *offsets;      // packed rows: batch + 1 first rows; else null
+  const float *state_in;   // may be null (zero)
+  float *state_out;        // may be null
+  void *y;                 // contiguous [sequence][token][channel]; the gradient reads it
+  long long batch, tokens;
+  int channels;
+  bool clear;  // packed rows of no sequence: results of 0
+  int blocks;  // of a cluster, which share a sequence's tokens
+  // Single tokens: the sequence's row of a pool of `pool` states (null: row = sequence).
+  const int *slots;
+  long long pool;
+  // The gradients' own arrays, contiguous like y.
+  const void *dy;
+  const float *dfinal;  // may be null (zero)
+  void *dx, *dg, *dbeta;
+  float *dinitial;  // may be null
+};
+// g and beta of type float where gfloat, else of type T.
+template <typename T> cudaError_t launch_recur(const RecurArgs &a, bool gfloat, cudaStream_t st);
+template <typename T>
+cudaError_t launch_recur_grad(const RecurArgs &a, bool gfloat, cudaStream_t st);
+template <typename T>
+cudaError_t launch_recur_step(const RecurArgs &a, bool gfloat, cudaStream_t st);
+
+// ---- cross entropy of a linear layer (xent.cu) --------------------------------------
+
+struct XentArgs {
+  const void *x, *w;  // tokens x dim, vocabulary x dim
+  long long ldx, ldw;
+  const void *targets;
+  int target_bytes;  // 4 or 8
+  long long tokens, vocabulary;
+  int dim;
+  float *loss, *lse;  // the gradients read lse
+  // The gradients' own arrays.
+  const float *dloss;
+  void *dx, *dw;  // contiguous; each may be null
+};
+size_t xent_workspace_bytes(int dtype, const XentArgs &a, bool grad);
+cudaError_t launch_xent(int dtype, const XentArgs &a, void *workspace, cudaStream_t st);
+cudaError_t launch_xent_grad(int dtype, const XentArgs &a, void *workspace, cudaStream_t st);
+
 // ---- element conversions -----------------------------------------------------
 
 #ifdef __CUDACC__

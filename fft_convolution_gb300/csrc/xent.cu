@@ -1,0 +1,714 @@
+// xent.cu -- the cross entropy of a linear layer over a vocabulary, without
+// its logits ever lying in memory:
+//
+//   l_nv = x_n . w_v,  lse_n = log sum_v e^{l_nv},  loss_n = lse_n - l_{n,t_n},
+//   G_nv = c_n (e^{l_nv - lse_n} - [v = t_n]),  dx = G W,  dW = G^T x
+//
+// (c: the gradient of the loss; a token whose target is no word has no loss
+// and no gradient).  The products are tiles of 256 tokens x 256 words on pairs of
+// multiprocessors (pair_gemm.cuh).  Forward, a tile leaves each row's maximum
+// and sum of exponentials, which a second kernel joins.  Backward, the logits are
+// computed again from lse, piece by piece of the vocabulary: a piece's G (at
+// most 256 MB, in the operands' type) is written, then both products with it run
+// in one launch, dW's rows of the piece in full and dx in fp32 on top of the
+// pieces before.  A product of few tiles is cut along its sum into slices, which the
+// last kernel adds in order.
+//
+// fp32 operands are laid out once per call as three bf16 parts each (24
+// significand bits, any exponent), of whose nine products the six largest are
+// taken: those left out are below 2^-24 of the factors' sizes.
+#include <math.h>
+
+#include "pair_gemm.cuh"
+
+namespace fftgb {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr size_t kPieceBytes = (size_t)256 << 20;  // of G
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ long long target_of(const void *t, int bytes, long long n) {
+  return bytes == 8 ? static_cast<const long long *>(t)[n]
+                    : (long long)static_cast<const int *>(t)[n];
+}
+
+// ---- operands ---------------------------------------------------------------------
+
+// Which rows count: those of tokens with a target and a weight (null: all).
+struct LiveRows {
+  const void *targets;
+  int target_bytes;
+  long long vocabulary;
+  const float *dloss;
+};
+// Rows of ld elements as `PARTS` arrays of rows of ldo, whole 16 bytes; rows
+// that do not count are 0.
+template <typename T, typename O, int PARTS>
+__global__ void __launch_bounds__(256) xent_lay_kernel(const T *in, long long ld, long long rows,
+                                                       int dim, O *out, int ldo, LiveRows live) {
+  const int tx = threadIdx.x;
+  for (long long r = (long long)blockIdx.x * blockDim.y + threadIdx.y; r < rows;
+       r += (long long)gridDim.x * blockDim.y) {
+    int wide = dim;
+    if (live.targets) {
+      const long long t = target_of(live.targets, live.target_bytes, r);
+      if (t < 0 || t >= live.vocabulary || live.dloss[r] == 0.0f) wide = 0;
+    }
+    for (int c = tx; c < ldo; c += blockDim.x) {
+      if constexpr (PARTS == 1) {
+        out[r * ldo + c] = c < wide ? in[r * ld + c] : from_acc<O>(0.0f);
+      } else {
+        float v = c < wide ? in[r * ld + c] : 0.0f;
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+          const O h = from_acc<O>(v);
+          out[((long long)p * rows + r) * ldo + c] = h;
+          v = isfinite(to_acc(h)) ? v - to_acc(h) : 0.0f;
+        }
+      }
+    }
+  }
+}
+
+// ---- forward ----------------------------------------------------------------------
+
+struct XentTiles {
+  long long tokens, vocabulary;
+  int m, n;  // tiles of tokens and of words
+  const void *targets;
+  int target_bytes;
+  // forward: per 128 words and token, largest logit and sum (both in powers of 2)
+  float2 *partial;
+  float *at_target;
+  // gradient: a piece of the words from v0 on
+  long long v0;
+  const float *lse, *dloss;
+  const float *unit;  // what G is scaled by (null: 1)
+  void *g;            // [parts][tokens][ldg]
+  long long ldg;
+};
+
+// The 32 columns of a warp's lanes from `addr` on.
+__device__ __forceinline__ void read32(uint32_t addr, float (&f)[32]) {
+  uint32_t r[32];
+  __syncwarp();
+  tmem_ld(addr, r);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
+}
+
+// Tiles of all token blocks before the next words: x stays in the L2, W is read once.
+__device__ __forceinline__ PairTile word_tile(const XentTiles &p, int t, long long v0, int k) {
+  PairTile w{};
+  w.a_row = (t % p.m) * kPairTile;
+  w.b_row = (int)v0 + (t / p.m) * kPairTile;
+  w.k0 = 0;
+  w.k1 = k;
+  return w;
+}
+
+__global__ void __launch_bounds__(kPairThreads, 1)
+xent_sums_kernel(const __grid_constant__ PairOperands ops, const XentTiles p, int kblocks,
+                 int *status) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = (int)block_rank(), half = (warp - 4) >> 2;
+  auto of = [&](int t, int &) { return word_tile(p, t, 0, kblocks); };
+  auto out = [&](int t, uint32_t tm) {
+    const PairTile w = word_tile(p, t, 0, kblocks);
+    const long long n = w.a_row + rank * 128 + (warp & 3) * 32 + lane;
+    const long long v0 = w.b_row + half * 128;
+    if (v0 >= p.vocabulary) return;
+    const int count = (int)min((long long)128, p.vocabulary - v0);
+    const long long target = n < p.tokens ? target_of(p.targets, p.target_bytes, n) - v0 : -1;
+    const bool mine = target >= 0 && target < count;
+    float top = -INFINITY;
+    for (int c = 0; c < count; c += 32) {
+      float f[32];
+      read32(tm + c, f);
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (c + i < count) top = fmaxf(top, f[i]);
+    }
+    // all of them -infinity (or NaN): in units of 1
+    top = top == -INFINITY ? top : top * kLog2e;
+    const float unit = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+    for (int c = 0; c < count; c += 32) {
+      float f[32];
+      read32(tm + c, f);
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (c + i < count) sum += exp2_approx(fmaf(f[i], kLog2e, -unit));
+      if (__any_sync(0xffffffffu, mine && target >= c && target < c + 32)) {
+        float at = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (target == c + i) at = f[i];
+        if (mine && target >= c && target < c + 32) p.at_target[n] = at;
+      }
+    }
+    if (n < p.tokens) p.partial[(v0 >> 7) * p.tokens + n] = make_float2(sum == 0.0f ? top : unit, sum);
+  };
+  pair_run(&ops, p.m * p.n, status, of, out);
+}
+
+// lse and loss from the parts of a token: a warp per 32 tokens and every eighth part.
+__global__ void __launch_bounds__(256) xent_join_kernel(const XentTiles p, float *loss, float *lse) {
+  __shared__ float2 parts[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long n = (long long)blockIdx.x * 32 + lane;
+  const int count = (int)((p.vocabulary + 127) >> 7);
+  float2 s = make_float2(-INFINITY, 0.0f);
+  // (m, s) + (m', s'): the sums in units of the larger power
+  auto join = [](float2 a, float2 b) {
+    const float m = fmaxf(a.x, b.x);
+    const float sa = a.x == m ? a.y : a.y * exp2f(a.x - m), sb = b.x == m ? b.y : b.y * exp2f(b.x - m);
+    return make_float2(m, sa + sb);
+  };
+  if (n < p.tokens)
+    for (int i = warp; i < count; i += 8) s = join(s, p.partial[(long long)i * p.tokens + n]);
+  parts[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || n >= p.tokens) return;
+#pragma unroll
+  for (int w = 1; w < 8; ++w) s = join(s, parts[w][lane]);
+  const float total = (s.x + log2f(s.y)) * kLn2;
+  const long long target = target_of(p.targets, p.target_bytes, n);
+  lse[n] = total;
+  loss[n] = target >= 0 && target < p.vocabulary ? total - p.at_target[n] : 0.0f;
+}
+
+// ---- gradients ----------------------------------------------------------------------
+
+// For half operands: the power of two that brings the largest |c_n| to 2^14 ..
+// 2^15, so that G = c (p - 1) uses the type's range, and its inverse.
+__global__ void __launch_bounds__(1024) xent_unit_kernel(const XentTiles p, float *unit) {
+  __shared__ float most[32];
+  float m = 0.0f;
+  for (long long n = threadIdx.x; n < p.tokens; n += 1024) {
+    const long long t = target_of(p.targets, p.target_bytes, n);
+    if (t >= 0 && t < p.vocabulary) m = fmaxf(m, fabsf(p.dloss[n]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < 32; ++w) m = fmaxf(m, most[w]);
+  int e = 0;
+  float u = 1.0f;
+  if (m > 0.0f && isfinite(m)) {
+    frexpf(m, &e);  // m < 2^e
+    u = ldexpf(1.0f, min(max(15 - e, -100), 100));
+  }
+  unit[0] = u;
+  unit[1] = 1.0f / u;
+}
+
+// 32 values as PARTS arrays, the rows of 16 bytes on their boundaries.
+template <typename O, int PARTS>
+__device__ __forceinline__ void put32(O *row, long long part, float (&f)[32]) {
+#pragma unroll
+  for (int q = 0; q < PARTS; ++q) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = f[8 * j + i];
+      reinterpret_cast<uint4 *>(row + q * part)[j] = pack<O>(v);
+      if constexpr (PARTS > 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[8 * j + i] -= to_acc(from_acc<O>(v[i]));
+      }
+    }
+  }
+}
+
+// G of a piece of the vocabulary; columns behind the last word are 0.
+template <typename O, int PARTS>
+__global__ void __launch_bounds__(kPairThreads, 1)
+xent_grad_kernel(const __grid_constant__ PairOperands ops, const XentTiles p, int kblocks,
+                 int *status) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = (int)block_rank(), half = (warp - 4) >> 2;
+  auto of = [&](int t, int &) { return word_tile(p, t, p.v0, kblocks); };
+  auto out = [&](int t, uint32_t tm) {
+    const PairTile w = word_tile(p, t, p.v0, kblocks);
+    const long long n = w.a_row + rank * 128 + (warp & 3) * 32 + lane;
+    const long long v = w.b_row + half * 128;
+    float c = 0.0f, lse = 0.0f;
+    long long target = -1;
+    if (n < p.tokens) {
+      target = target_of(p.targets, p.target_bytes, n);
+      if (target >= 0 && target < p.vocabulary) {
+        c = p.dloss[n] * (p.unit ? p.unit[0] : 1.0f);
+        lse = p.lse[n];
+      }
+    }
+    const bool live = c != 0.0f;  // NaN is live
+    O *row = static_cast<O *>(p.g) + n * p.ldg + (v - p.v0);
+    const int at = target >= v && target < v + 128 ? (int)(target - v) : -1;
+    const int count = (int)max(0ll, min((long long)128, p.vocabulary - v));
+#pragma unroll 1
+    for (int j = 0; j < 128; j += 32) {
+      float f[32];
+      read32(tm + j, f);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float q = exp2_approx((f[i] - lse) * kLog2e) - (at == j + i ? 1.0f : 0.0f);
+        f[i] = live && j + i < count ? q * c : 0.0f;
+      }
+      if (n < p.tokens) put32<O, PARTS>(row + j, p.tokens * p.ldg, f);
+    }
+  };
+  pair_run(&ops, p.m * p.n, status, of, out);
+}
+
+// dx += G W over a piece and dW = G^T x of its rows, in one launch: the
+// longer sums of dx first, so that the short ones fill the ends.
+struct XentProducts {
+  PairOperands ops[2];
+  long long tokens, vocabulary, v0;
+  int dim;
+  int m, n, slices, k;   // dx: tiles of tokens and of columns, cuts of the sum, its blocks
+  int wm, wk;            // dW: tiles of words, blocks of tokens
+  float *sums;           // [slices][tokens][dim]
+  int first;             // the piece: nothing to add to
+  void *dw;
+  const float *unit;
+};
+
+template <typename T>
+__device__ __forceinline__ void put_columns(T *row, int c, int dim, bool vec, const float (&f)[32]) {
+  constexpr int P = 16 / (int)sizeof(T);
+  if (vec) {
+#pragma unroll
+    for (int j = 0; j < 32 / P; ++j) {
+      if (c + j * P < dim) {
+        float v[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = f[j * P + i];
+        reinterpret_cast<uint4 *>(row + c)[j] = pack<T>(v);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (c + i < dim) row[c + i] = from_acc<T>(f[i]);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kPairThreads, 1)
+xent_products_kernel(const __grid_constant__ XentProducts p, int *status) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = (int)block_rank(), half = (warp - 4) >> 2;
+  const int mn = p.m * p.n, dx_tiles = mn * p.slices, dw_tiles = p.wm * p.n;
+  auto of = [&](int t, int &which) {
+    PairTile w{};
+    if (t < dx_tiles) {
+      which = 0;
+      const int slice = t / mn, u = t - slice * mn;
+      w.a_row = u / p.n * kPairTile;
+      w.b_row = u % p.n * kPairTile;
+      w.b_base = (int)p.v0;
+      w.k0 = (int)((long long)p.k * slice / p.slices);
+      w.k1 = (int)((long long)p.k * (slice + 1) / p.slices);
+    } else {
+      which = 1;
+      const int u = t - dx_tiles;
+      w.a_row = u / p.n * kPairTile;
+      w.b_row = u % p.n * kPairTile;
+      w.k1 = p.wk;
+    }
+    return w;
+  };
+  auto out = [&](int t, uint32_t tm) {
+    int which = 0;
+    const PairTile w = of(t, which);
+    const long long r = w.a_row + rank * 128 + (warp & 3) * 32 + lane;
+    const int c0 = w.b_row + half * 128;
+    const float back = p.unit ? p.unit[1] : 1.0f;
+#pragma unroll 1
+    for (int j = 0; j < 128 && c0 + j < p.dim; j += 32) {
+      float f[32];
+      read32(tm + j, f);
+      const int c = c0 + j;
+      if (which == 0) {
+        if (w.k0 == w.k1) {  // an empty cut of a short piece: nothing was summed
+#pragma unroll
+          for (int i = 0; i < 32; ++i) f[i] = 0.0f;
+        }
+        float *row = p.sums + ((long long)(t / mn) * p.tokens + r) * p.dim;
+        const bool vec = p.dim % 4 == 0, live = r < p.tokens;
+        if (live && !p.first) {
+          if (vec) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              if (c + i < p.dim) {
+                const float4 o = *reinterpret_cast<const float4 *>(row + c + i);
+                f[i] += o.x;
+                f[i + 1] += o.y;
+                f[i + 2] += o.z;
+                f[i + 3] += o.w;
+              }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c + i < p.dim) f[i] += row[c + i];
+          }
+        }
+        if (live) put_columns<float>(row, c, p.dim, vec, f);
+      } else {
+        const long long v = p.v0 + r;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] *= back;
+        const bool vec = p.dim % (16 / (int)sizeof(T)) == 0 && ((uintptr_t)p.dw & 15) == 0;
+        if (v < p.vocabulary) put_columns<T>(static_cast<T *>(p.dw) + v * p.dim, c, p.dim, vec, f);
+      }
+    }
+  };
+  pair_run(p.ops, dx_tiles + dw_tiles, status, of, out);
+}
+
+// dx: the slices added and rounded once.
+template <typename T>
+__global__ void __launch_bounds__(256) xent_dx_kernel(const float *sums, long long count, int slices,
+                                                      const float *unit, T *dx, bool vec) {
+  const float back = unit ? unit[1] : 1.0f;
+  const long long step = (long long)gridDim.x * 256, first = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (vec) {
+    for (long long i = first; i < count / 4; i += step) {
+      float4 s = reinterpret_cast<const float4 *>(sums)[i];
+      for (int k = 1; k < slices; ++k) {
+        const float4 o = *reinterpret_cast<const float4 *>(sums + k * count + 4 * i);
+        s.x += o.x;
+        s.y += o.y;
+        s.z += o.z;
+        s.w += o.w;
+      }
+      T *d = dx + 4 * i;
+      if constexpr (sizeof(T) == 2) {
+        const T v[4] = {from_acc<T>(s.x * back), from_acc<T>(s.y * back), from_acc<T>(s.z * back),
+                        from_acc<T>(s.w * back)};
+        uint2 u;
+        memcpy(&u, v, 8);
+        *reinterpret_cast<uint2 *>(d) = u;
+      } else {
+        *reinterpret_cast<float4 *>(d) = make_float4(s.x * back, s.y * back, s.z * back, s.w * back);
+      }
+    }
+    return;
+  }
+  for (long long i = first; i < count; i += step) {
+    float s = sums[i];
+    for (int k = 1; k < slices; ++k) s += sums[k * count + i];
+    dx[i] = from_acc<T>(s * back);
+  }
+}
+
+// ---- host -----------------------------------------------------------------------------
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_fn() {
+  static EncodeFn fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return static_cast<EncodeFn>(nullptr);
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// [parts][rows][cols] at a row stride of ld elements, boxes of 64 columns and
+// `box` rows; what lies outside reads as 0.
+bool make_map(CUtensorMap *map, bool half, const void *p, long long rows, long long cols,
+              long long ld, int parts, int box) {
+  EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * (cuuint64_t)rows};
+  const cuuint32_t shape[3] = {64, (cuuint32_t)box, 1}, ones[3] = {1, 1, 1};
+  return fn(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+            const_cast<void *>(p), dims, strides, shape, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+uint32_t idesc_of(bool half, bool a_mn, bool b_mn) {
+  return mma_desc(kPairTile, kPairTile, a_mn, b_mn) | (half ? 0u : (1u << 7) | (1u << 10));
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+long long up(long long n, long long d) { return (n + d - 1) / d; }
+
+// An operand as the loads can take it: the caller's array, or laid out in the workspace.
+struct Operand {
+  bool own;
+  long long ld;
+  size_t bytes;  // in the workspace
+};
+Operand operand(int dtype, const void *p, long long ld, long long rows, int dim, bool copy) {
+  Operand o{};
+  const int parts = dtype == FFT_ELEM_F32 ? 3 : 1;
+  o.own = copy || parts > 1 || ((uintptr_t)p & 15) != 0 || (ld * 2) % 16 != 0;
+  o.ld = o.own ? up(dim, 8) * 8 : ld;
+  o.bytes = o.own ? round256((size_t)parts * rows * o.ld * 2) : 0;
+  return o;
+}
+
+struct Layout {
+  Operand x, w;
+  int parts;
+  size_t partial, at_target;         // forward
+  long long piece;                   // words
+  int pieces, slices;
+  size_t unit, g, sums;              // backward
+  size_t bytes;
+  Layout(int dtype, const XentArgs &a, bool grad) {
+    parts = dtype == FFT_ELEM_F32 ? 3 : 1;
+    // gradients: x without the rows that do not count, whatever they hold (66 MB
+    // moved before 4 * 10^12 operations of the largest case)
+    x = operand(dtype, a.x, a.ldx, a.tokens, a.dim, grad);
+    w = operand(dtype, a.w, a.ldw, a.vocabulary, a.dim, false);
+    bytes = x.bytes + w.bytes;
+    partial = at_target = unit = g = sums = 0;
+    piece = 0;
+    pieces = slices = 0;
+    auto take = [&](size_t n) {
+      const size_t at = bytes;
+      bytes += round256(n);
+      return at;
+    };
+    if (!grad) {
+      partial = take((size_t)up(a.vocabulary, 128) * a.tokens * 8);
+      at_target = take((size_t)a.tokens * 4);
+      return;
+    }
+    const long long words = up(a.vocabulary, kPairTile);
+    long long fit = (long long)(kPieceBytes / ((size_t)a.tokens * 2 * parts * kPairTile));
+    // 1024 words at least: dx is read and written once per piece
+    if (fit < 4) fit = 4;
+    pieces = (int)up(words, fit);
+    piece = up(words, pieces) * kPairTile;
+    // dx's sums are cut so that its tiles fill the pairs, into cuts of 16 blocks at least
+    const long long tiles = up(a.tokens, kPairTile) * up(a.dim, kPairTile);
+    const long long pairs = sm_count() > 1 ? sm_count() / 2 : 1;
+    slices = 1;
+    while (slices < 32 && tiles * slices * 2 <= pairs && piece / kPairK / (slices * 2) >= 16)
+      slices *= 2;
+    unit = take(8);
+    g = take((size_t)parts * a.tokens * piece * 2);
+    sums = take((size_t)slices * a.tokens * a.dim * 4);
+  }
+};
+
+template <typename T>
+cudaError_t lay(const void *in, long long ld, long long rows, int dim, const Operand &o, void *out,
+                const LiveRows &live, cudaStream_t st) {
+  const dim3 block(64, 4);
+  const long long need = (rows + 3) / 4, most = (long long)sm_count() * 16;
+  const unsigned grid = (unsigned)(need < most ? need : most);
+  if constexpr (sizeof(T) == 4)
+    xent_lay_kernel<float, __nv_bfloat16, 3><<<grid, block, 0, st>>>(
+        static_cast<const float *>(in), ld, rows, dim, static_cast<__nv_bfloat16 *>(out), (int)o.ld,
+        live);
+  else
+    xent_lay_kernel<T, T, 1><<<grid, block, 0, st>>>(static_cast<const T *>(in), ld, rows, dim,
+                                                     static_cast<T *>(out), (int)o.ld, live);
+  return cudaGetLastError();
+}
+
+template <typename K, typename... Args>
+cudaError_t pair_launch(K *kern, DeviceOnce &once, long long tiles, cudaStream_t st,
+                        const Args &...args) {
+  cudaError_t e = smem_limit_once((const void *)kern, kPairSmem, once);
+  if (e != cudaSuccess) return e;
+  const long long pairs = sm_count() / 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// The type of the products' operands.
+template <typename T> struct Part { using type = T; };
+template <> struct Part<float> { using type = __nv_bfloat16; };
+
+// Lays out what has to be; xp, wp: the operands.
+template <typename T>
+cudaError_t lay_both(const XentArgs &a, const Layout &l, char *ws, bool grad, const void *&xp,
+                     const void *&wp, cudaStream_t st) {
+  const LiveRows all{}, live{a.targets, a.target_bytes, a.vocabulary, a.dloss};
+  xp = l.x.own ? ws : a.x;
+  wp = l.w.own ? ws + l.x.bytes : a.w;
+  cudaError_t e = cudaSuccess;
+  if (l.x.own) e = lay<T>(a.x, a.ldx, a.tokens, a.dim, l.x, ws, grad ? live : all, st);
+  if (e == cudaSuccess && l.w.own)
+    e = lay<T>(a.w, a.ldw, a.vocabulary, a.dim, l.w, ws + l.x.bytes, all, st);
+  return e;
+}
+
+XentTiles tiles_of(const XentArgs &a) {
+  XentTiles t{};
+  t.tokens = a.tokens;
+  t.vocabulary = a.vocabulary;
+  t.m = (int)up(a.tokens, kPairTile);
+  t.targets = a.targets;
+  t.target_bytes = a.target_bytes;
+  t.lse = a.lse;
+  t.dloss = a.dloss;
+  return t;
+}
+
+template <typename T>
+cudaError_t xent_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st) {
+  constexpr bool half = std::is_same<T, __half>::value;
+  int *status = device_status_word();
+  if (!status) return cudaErrorInvalidDevice;
+  const Layout l(dtype, a, false);
+  const void *xp, *wp;
+  cudaError_t e = lay_both<T>(a, l, ws, false, xp, wp, st);
+  if (e != cudaSuccess) return e;
+  PairOperands ops{};
+  if (!make_map(&ops.a, half, xp, a.tokens, a.dim, l.x.ld, l.parts, 128) ||
+      !make_map(&ops.b, half, wp, a.vocabulary, a.dim, l.w.ld, l.parts, 128))
+    return cudaErrorInvalidValue;
+  ops.idesc = idesc_of(half, false, false);
+  ops.parts = l.parts;
+  XentTiles t = tiles_of(a);
+  t.n = (int)up(a.vocabulary, kPairTile);
+  t.partial = reinterpret_cast<float2 *>(ws + l.partial);
+  t.at_target = reinterpret_cast<float *>(ws + l.at_target);
+  static DeviceOnce once;
+  e = pair_launch(xent_sums_kernel, once, (long long)t.m * t.n, st, ops, t, (int)up(a.dim, kPairK),
+                  status);
+  if (e != cudaSuccess) return e;
+  xent_join_kernel<<<(unsigned)up(a.tokens, 32), 256, 0, st>>>(t, a.loss, a.lse);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t xent_grad_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st) {
+  using O = typename Part<T>::type;
+  constexpr bool half = std::is_same<T, __half>::value;
+  constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+  int *status = device_status_word();
+  if (!status) return cudaErrorInvalidDevice;
+  const Layout l(dtype, a, true);
+  const void *xp, *wp;
+  cudaError_t e = lay_both<T>(a, l, ws, true, xp, wp, st);
+  if (e != cudaSuccess) return e;
+  XentTiles t = tiles_of(a);
+  float *unit = nullptr;
+  if (half) {
+    unit = reinterpret_cast<float *>(ws + l.unit);
+    xent_unit_kernel<<<1, 1024, 0, st>>>(t, unit);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  t.unit = unit;
+  t.g = ws + l.g;
+  t.ldg = l.piece;
+  PairOperands ops{};
+  XentProducts p{};
+  if (!make_map(&ops.a, half, xp, a.tokens, a.dim, l.x.ld, l.parts, 128) ||
+      !make_map(&ops.b, half, wp, a.vocabulary, a.dim, l.w.ld, l.parts, 128) ||
+      !make_map(&p.ops[0].a, half, t.g, a.tokens, l.piece, l.piece, l.parts, 128) ||
+      !make_map(&p.ops[0].b, half, wp, a.vocabulary, a.dim, l.w.ld, l.parts, 64) ||
+      !make_map(&p.ops[1].a, half, t.g, a.tokens, l.piece, l.piece, l.parts, 64) ||
+      !make_map(&p.ops[1].b, half, xp, a.tokens, a.dim, l.x.ld, l.parts, 64))
+    return cudaErrorInvalidValue;
+  ops.idesc = idesc_of(half, false, false);
+  p.ops[0].b_mn = p.ops[1].a_mn = p.ops[1].b_mn = 1;
+  p.ops[0].idesc = idesc_of(half, false, true);
+  p.ops[1].idesc = idesc_of(half, true, true);
+  ops.parts = p.ops[0].parts = p.ops[1].parts = l.parts;
+  p.tokens = a.tokens;
+  p.vocabulary = a.vocabulary;
+  p.dim = a.dim;
+  p.m = t.m;
+  p.n = (int)up(a.dim, kPairTile);
+  p.slices = a.dx ? l.slices : 0;
+  p.wk = (int)up(a.tokens, kPairK);
+  p.sums = reinterpret_cast<float *>(ws + l.sums);
+  p.dw = a.dw;
+  p.unit = unit;
+  const int kblocks = (int)up(a.dim, kPairK);
+  static DeviceOnce once_g, once_p;
+  for (int i = 0; i < l.pieces; ++i) {
+    t.v0 = p.v0 = i * l.piece;
+    if (t.v0 >= a.vocabulary) break;
+    const long long words = a.vocabulary - t.v0 < l.piece ? a.vocabulary - t.v0 : l.piece;
+    t.n = (int)up(words, kPairTile);
+    e = pair_launch(xent_grad_kernel<O, kParts>, once_g, (long long)t.m * t.n, st, ops, t, kblocks,
+                    status);
+    if (e != cudaSuccess) return e;
+    p.first = i == 0;
+    p.k = (int)up(words, kPairK);
+    p.wm = a.dw ? t.n : 0;
+    e = pair_launch(xent_products_kernel<T>, once_p,
+                    (long long)p.m * p.n * p.slices + (long long)p.wm * p.n, st, p, status);
+    if (e != cudaSuccess) return e;
+  }
+  if (!a.dx) return cudaSuccess;
+  const long long count = a.tokens * a.dim;
+  const bool vec = a.dim % 4 == 0 && ((uintptr_t)a.dx & (4 * sizeof(T) - 1)) == 0;
+  const long long need = up(vec ? count / 4 : count, 256), most = (long long)sm_count() * 16;
+  xent_dx_kernel<T><<<(unsigned)(need < most ? need : most), 256, 0, st>>>(
+      p.sums, count, p.slices, unit, static_cast<T *>(a.dx), vec);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t xent_workspace_bytes(int dtype, const XentArgs &a, bool grad) {
+  return a.tokens == 0 ? 0 : Layout(dtype, a, grad).bytes;
+}
+
+cudaError_t launch_xent(int dtype, const XentArgs &a, void *workspace, cudaStream_t st) {
+  char *ws = static_cast<char *>(workspace);
+  switch (dtype) {
+    case FFT_ELEM_F32: return xent_t<float>(dtype, a, ws, st);
+    case FFT_ELEM_BF16: return xent_t<__nv_bfloat16>(dtype, a, ws, st);
+    default: return xent_t<__half>(dtype, a, ws, st);
+  }
+}
+
+cudaError_t launch_xent_grad(int dtype, const XentArgs &a, void *workspace, cudaStream_t st) {
+  char *ws = static_cast<char *>(workspace);
+  if (a.tokens == 0)
+    return a.dw ? cudaMemsetAsync(a.dw, 0, (size_t)a.vocabulary * a.dim * elem_bytes(dtype), st)
+                : cudaSuccess;
+  switch (dtype) {
+    case FFT_ELEM_F32: return xent_grad_t<float>(dtype, a, ws, st);
+    case FFT_ELEM_BF16: return xent_grad_t<__nv_bfloat16>(dtype, a, ws, st);
+    default: return xent_grad_t<__half>(dtype, a, ws, st);
+  }
+}
+
+}  // namespace fftgb

@@ -22,6 +22,8 @@ _ELEM = {torch.float32: FFT_ELEM_F32, torch.float64: FFT_ELEM_F64,
 _NULL = contextlib.nullcontext()
 # fft_delta_desc: sizes, five strides of three, scale, type, whether to clear rows.
 _DESC = struct.Struct("=6q15qd2i")
+# fft_recurrence_desc: sizes, three strides of two, types, whether to clear rows, padding.
+_RECUR = struct.Struct("=3q6q3i4x")
 
 
 def _elem(t, what: str) -> int:
@@ -382,3 +384,253 @@ def delta_rule_step(q, k, v, g, beta, state, slots=None, scale=None, out=None, s
                "fft_delta_rule_step")
     _changed(state if given is None else [state, given])
     return out
+
+
+# ---- embedding of tokens ---------------------------------------------------------------
+
+def _indices(t, what: str):
+    """Contiguous indices and their size in bytes."""
+    if t.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{what}: int32 or int64, got {t.dtype}")
+    return t.contiguous(), t.element_size()
+
+
+def embedding(ids, table, scale: float = 1.0, out=None, stream=None):
+    """Rows of table [rows, dim] times `scale` (see fft_embedding), in ids'
+    shape with an axis of dim behind it.  ids: int32 or int64; one outside
+    0 .. rows - 1 is padding and gives zeros."""
+    if table.dim() != 2 or table.shape[0] == 0 or table.shape[1] == 0:
+        raise ValueError("table must be [rows, dim]")
+    device = _device(table, ids, out)
+    code = _elem(table, "table")
+    rows, dim = table.shape
+    context, handle = _on(stream, device)
+    with context:
+        ids2, size = _indices(ids, "ids")
+        t2 = _rows(table)
+        shape = (*ids.shape, dim)
+        given = out
+        if out is None:
+            out = torch.empty(shape, dtype=table.dtype, device=device)
+        elif out.shape != shape or out.dtype != table.dtype or not out.is_contiguous():
+            raise ValueError("out must be contiguous, of ids' shape and dim, and of the table's type")
+        rc = _lib.fft_embedding(ids2.data_ptr(), size, t2.data_ptr(), max(dim, t2.stride(0)),
+                                out.data_ptr(), dim, ids.numel(), rows, dim, scale, code, handle)
+    if rc:
+        _check(rc, "fft_embedding")
+    if given is not None:
+        _changed(given)
+    return out
+
+
+def embedding_backward(dy, ids, rows: int, scale: float = 1.0, add_to=None, dtype=None, stream=None):
+    """The gradient [rows, dim] of embedding's table (see
+    fft_embedding_backward) from dy [*ids.shape, dim]: a new tensor of type
+    `dtype` (dy's, or float32 with 16-bit dy), or `add_to` (contiguous, of one
+    of those types), to which it is added in place."""
+    if dy.dim() != ids.dim() + 1 or dy.shape[:-1] != ids.shape or dy.shape[-1] == 0:
+        raise ValueError("dy must be [*ids.shape, dim]")
+    device = _device(dy, ids, add_to)
+    code = _elem(dy, "dy")
+    dim = dy.shape[-1]
+    context, handle = _on(stream, device)
+    with context:
+        ids2, size = _indices(ids, "ids")
+        dy2 = _rows(dy)
+        if add_to is None:
+            dtable = torch.empty(rows, dim, dtype=dtype or dy.dtype, device=device)
+        elif add_to.shape != (rows, dim) or not add_to.is_contiguous():
+            raise ValueError("add_to must be contiguous [rows, dim]")
+        elif dtype is not None and dtype != add_to.dtype:
+            raise TypeError("dtype is add_to's")
+        else:
+            dtable = add_to
+        nbytes = _lib.fft_embedding_workspace_bytes(ids.numel(), dim, code)
+        ws = _workspace(nbytes, device)
+        _check(_lib.fft_embedding_backward(
+            dy2.data_ptr(), max(dim, dy2.stride(0)), ids2.data_ptr(), size, dtable.data_ptr(),
+            ids.numel(), rows, dim, scale, add_to is not None, code, _elem(dtable, "dtable"),
+            ws.data_ptr(), nbytes, handle), "fft_embedding_backward")
+    if add_to is not None:
+        _changed(add_to)
+    return dtable
+
+
+# ---- the gated linear recurrence -----------------------------------------------------------
+
+def _recur_inputs(x, g, beta, batch, packed: bool, clear: bool = False):
+    """Checks the inputs; returns them (channels contiguous), fft_recurrence_desc and the device."""
+    shape, lead = x.shape, 1 if packed else 2
+    if len(shape) != lead + 1 or g.shape != shape or (beta is not None and beta.shape != shape):
+        raise ValueError("x, g, beta: [batch, tokens, channels] (packed rows: without the batch axis)")
+    if shape[-1] == 0:
+        raise ValueError("at least one channel")
+    kind = x.dtype
+    if g.dtype not in (kind, torch.float32) or (beta is not None and beta.dtype != g.dtype):
+        raise TypeError("g and beta need one type: x's or float32")
+    device = _device(x, g, beta)
+    x, g = _dense(x), _dense(g)
+    beta = None if beta is None else _dense(beta)
+    first = (0,) if packed else ()
+    sx, sg = first + x.stride()[:lead], first + g.stride()[:lead]
+    sb = (0, 0) if beta is None else first + beta.stride()[:lead]
+    desc = _RECUR.pack(batch, shape[lead - 1], shape[-1], *sx, *sg, *sb, _elem(x, "x"), _elem(g, "g"),
+                       clear)
+    return x, g, beta, desc, device
+
+
+def linear_recurrence(x, g, beta=None, initial_state=None, offsets=None, out=None, stream=None):
+    """(y, final state) of h <- e^g h + beta x over whole sequences, by channel
+    (see fft_linear_recurrence); y holds every h.  x: [batch, tokens,
+    channels]; g (log decay) and beta (None: 1) like it, of its type or float32.
+    With offsets (int32 [sequences + 1] on the device) the rows of all
+    sequences are packed and the arrays have no batch axis; rows of no sequence
+    are 0 in y (in `out`, if it is given, as they were).  States: float32
+    [sequences, channels]."""
+    batch, packed = _packing(x, offsets)
+    context, handle = _on(stream, _device(x))
+    with context:
+        x, g, beta, desc, device = _recur_inputs(x, g, beta, batch, packed, packed and out is None)
+        _device(x, initial_state, offsets, out)
+        if packed:
+            offsets = offsets.to(torch.int32).contiguous()
+        shape = (batch, x.shape[-1])
+        initial_state = _states(initial_state, shape, "initial_state")
+        given = out
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=device)
+        elif out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous():
+            raise ValueError("out must be contiguous and like x")
+        final = torch.empty(shape, dtype=torch.float32, device=device)
+        _check(_lib.fft_linear_recurrence(desc, x.data_ptr(), g.data_ptr(), _ptr(beta), _ptr(offsets),
+                                          _ptr(initial_state), out.data_ptr(), final.data_ptr(),
+                                          handle), "fft_linear_recurrence")
+    if given is not None:
+        _changed(given)
+    return out, final
+
+
+def linear_recurrence_backward(dy, x, g, y, beta=None, initial_state=None, offsets=None,
+                               dfinal_state=None, stream=None):
+    """(dx, dg, dbeta, dinitial_state) of linear_recurrence, from the gradient
+    of y (like y) and of the final state (None: zero), and the forward call's
+    y; the other arguments as in it (see fft_linear_recurrence_backward).
+    dbeta is None without beta.  Packed rows of no sequence have gradients of 0."""
+    batch, packed = _packing(x, offsets)
+    context, handle = _on(stream, _device(x))
+    with context:
+        x, g, beta, desc, device = _recur_inputs(x, g, beta, batch, packed, packed)
+        _device(x, dy, y, initial_state, dfinal_state, offsets)
+        for t, name in ((dy, "dy"), (y, "y")):
+            if t.shape != x.shape or t.dtype != x.dtype:
+                raise ValueError(f"{name} must be like x")
+        dy, y = dy.contiguous(), y.contiguous()
+        if packed:
+            offsets = offsets.to(torch.int32).contiguous()
+        shape = (batch, x.shape[-1])
+        initial_state = _states(initial_state, shape, "initial_state")
+        dfinal_state = _states(dfinal_state, shape, "dfinal_state")
+        dx = torch.empty(x.shape, dtype=x.dtype, device=device)
+        dg = torch.empty(x.shape, dtype=g.dtype, device=device)
+        dbeta = None if beta is None else torch.empty(x.shape, dtype=g.dtype, device=device)
+        dinitial = torch.empty(shape, dtype=torch.float32, device=device)
+        _check(_lib.fft_linear_recurrence_backward(
+            desc, dy.data_ptr(), x.data_ptr(), g.data_ptr(), _ptr(beta), y.data_ptr(), _ptr(offsets),
+            _ptr(initial_state), _ptr(dfinal_state), dx.data_ptr(), dg.data_ptr(), _ptr(dbeta),
+            dinitial.data_ptr(), handle), "fft_linear_recurrence_backward")
+    return dx, dg, dbeta, dinitial
+
+
+def linear_recurrence_step(x, g, state, beta=None, slots=None, out=None, stream=None):
+    """One or a few tokens per sequence of the gated linear recurrence (see
+    fft_linear_recurrence_step): returns y [batch, tokens, channels] and updates
+    `state` (float32 [pool, channels], contiguous) in place.  slots: int32
+    [batch], the state of each sequence (negative: idle, y is 0); by default
+    sequence i has state i."""
+    context, handle = _on(stream, _device(x))
+    with context:
+        x, g, beta, desc, device = _recur_inputs(x, g, beta, x.shape[0], False)
+        _device(x, state, slots, out)
+        if state.dtype != torch.float32 or not state.is_contiguous() or state.dim() != 2 or \
+                state.shape[1] != x.shape[-1]:
+            raise ValueError("state must be contiguous float32 [pool, channels]")
+        if slots is not None and (slots.dtype != torch.int32 or slots.shape != (x.shape[0],)
+                                  or not slots.is_contiguous()):
+            raise ValueError("slots must be contiguous int32 [batch]")
+        given = out
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=device)
+        elif out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous():
+            raise ValueError("out must be contiguous and like x")
+        _check(_lib.fft_linear_recurrence_step(desc, x.data_ptr(), g.data_ptr(), _ptr(beta),
+                                               state.data_ptr(), _ptr(slots), state.shape[0],
+                                               out.data_ptr(), handle), "fft_linear_recurrence_step")
+    _changed(state if given is None else [state, given])
+    return out
+
+
+# ---- cross entropy of a linear layer ----------------------------------------------------------
+
+def _xent_inputs(x, weight, targets):
+    if weight.dim() != 2 or weight.shape[0] == 0 or weight.shape[1] == 0:
+        raise ValueError("weight must be [vocabulary, dim]")
+    if x.dim() < 1 or x.shape[-1] != weight.shape[1] or x.shape[:-1] != targets.shape:
+        raise ValueError("x must be [*targets.shape, dim]")
+    if x.dtype != weight.dtype:
+        raise TypeError("x and weight need one type")
+    targets, size = _indices(targets, "targets")
+    return _rows(x), _rows(weight), targets, size
+
+
+def linear_cross_entropy(x, weight, targets, stream=None):
+    """(loss, lse) of the logits x @ weight.T, which are never stored (see
+    fft_linear_cross_entropy): per token the cross entropy with its target and
+    the logarithm of the sum of exponentials, float32 in targets' shape.  x:
+    [*targets.shape, dim]; weight: [vocabulary, dim] of its type (float32,
+    bfloat16 or float16); targets: int32 or int64.  A target outside
+    0 .. vocabulary - 1 (such as -100) is none: its loss is 0."""
+    device = _device(x, weight, targets)
+    code = _elem(x, "x")
+    context, handle = _on(stream, device)
+    with context:
+        x2, w2, t2, size = _xent_inputs(x, weight, targets)
+        (rows, dim), vocabulary = x2.shape, w2.shape[0]
+        ldx, ldw = max(dim, x2.stride(0)), max(dim, w2.stride(0))
+        loss = torch.empty(targets.shape, dtype=torch.float32, device=device)
+        lse = torch.empty(targets.shape, dtype=torch.float32, device=device)
+        nbytes = _lib.fft_linear_cross_entropy_workspace_bytes(
+            x2.data_ptr(), ldx, w2.data_ptr(), ldw, rows, vocabulary, dim, code, 0)
+        ws = _workspace(nbytes, device)
+        _check(_lib.fft_linear_cross_entropy(
+            x2.data_ptr(), ldx, w2.data_ptr(), ldw, t2.data_ptr(), size, loss.data_ptr(),
+            lse.data_ptr(), rows, vocabulary, dim, code, ws.data_ptr(), nbytes, handle),
+            "fft_linear_cross_entropy")
+    return loss, lse
+
+
+def linear_cross_entropy_backward(dloss, x, weight, targets, lse, dx: bool = True,
+                                  dweight: bool = True, stream=None):
+    """(dx, dweight) of linear_cross_entropy from the gradient of its losses
+    (float32, in targets' shape; expanded ones are fine) and its lse (see
+    fft_linear_cross_entropy_backward); None where dx=False or dweight=False."""
+    device = _device(x, weight, targets, dloss, lse)
+    code = _elem(x, "x")
+    context, handle = _on(stream, device)
+    with context:
+        x2, w2, t2, size = _xent_inputs(x, weight, targets)
+        for t, name in ((dloss, "dloss"), (lse, "lse")):
+            if t.dtype != torch.float32 or t.shape != targets.shape:
+                raise ValueError(f"{name} must be float32 in targets' shape")
+        dloss, lse = dloss.contiguous(), lse.contiguous()
+        (rows, dim), vocabulary = x2.shape, w2.shape[0]
+        ldx, ldw = max(dim, x2.stride(0)), max(dim, w2.stride(0))
+        gx = torch.empty(x.shape, dtype=x.dtype, device=device) if dx else None
+        gw = torch.empty(weight.shape, dtype=x.dtype, device=device) if dweight else None
+        nbytes = _lib.fft_linear_cross_entropy_workspace_bytes(
+            x2.data_ptr(), ldx, w2.data_ptr(), ldw, rows, vocabulary, dim, code, 1)
+        ws = _workspace(nbytes, device)
+        _check(_lib.fft_linear_cross_entropy_backward(
+            dloss.data_ptr(), x2.data_ptr(), ldx, w2.data_ptr(), ldw, t2.data_ptr(), size,
+            lse.data_ptr(), _ptr(gx), _ptr(gw), rows, vocabulary, dim, code, ws.data_ptr(), nbytes,
+            handle), "fft_linear_cross_entropy_backward")
+    return gx, gw

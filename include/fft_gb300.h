@@ -621,6 +621,143 @@ int fft_delta_rule_step(const fft_delta_desc *desc, const void *q, const void *k
                         const float *g, const float *beta, float *state, const int32_t *slots,
                         int64_t pool, void *o, void *stream);
 
+/*
+ * fft_embedding -- y_n = scale * table[ids_n], rows of zeros where ids_n is not
+ * in 0 .. rows - 1 (padding).
+ *   ids        `tokens` integers of id_bytes = 4 or 8 bytes, on the device.
+ *   table      rows x dim elements of type dtype; row r starts at element
+ *              r * ldt, ldt >= dim.
+ *   y          tokens x dim elements of type dtype, row stride ldy >= dim;
+ *              rounded once.
+ *   tokens     0 .. 2^31 - 64 (0: nothing is done); rows 1 .. 2^31 - 1;
+ *              dim 1 .. 2^30.
+ */
+int fft_embedding(const void *ids, int id_bytes, const void *table, int64_t ldt, void *y,
+                  int64_t ldy, int64_t tokens, int64_t rows, int64_t dim, double scale, int dtype,
+                  void *stream);
+
+/*
+ * fft_embedding_backward -- the table's gradient: dtable[v] = scale * sum of dy_n
+ * over the n with ids_n = v, in the order of the tokens by groups of 32 whatever
+ * the timing, in float (double with FFT_ELEM_F64), rounded once.
+ *   dy         tokens x dim of type dtype, row stride lddy >= dim.
+ *   dtable     rows x dim of type ttype (dtype, or FFT_ELEM_F32 with 16-bit dy),
+ *              contiguous.  add = 0: every row is written, 0 where no token
+ *              names it.  add != 0: the sums are added to what is there, and
+ *              rows that no token names are left alone.
+ *   workspace  fft_embedding_workspace_bytes(tokens, dim, dtype) bytes.
+ */
+size_t fft_embedding_workspace_bytes(int64_t tokens, int64_t dim, int dtype);
+int fft_embedding_backward(const void *dy, int64_t lddy, const void *ids, int id_bytes,
+                           void *dtable, int64_t tokens, int64_t rows, int64_t dim, double scale,
+                           int add, int dtype, int ttype, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/*
+ * The gated linear recurrence.  Per sequence and channel, with a state h in
+ * float,
+ *   h <- e^{g_t} h + beta_t x_t,   y_t = h
+ * (beta = NULL: 1).  g is the logarithm of the decay (0: none; -infinity:
+ * the state is dropped; above 0 the state grows).
+ */
+typedef struct fft_recurrence_desc {
+  int64_t batch;    /* sequences, 0 .. 2^24 */
+  int64_t tokens;   /* of every sequence; packed: rows of all of them; 0 .. 2^31 - 1 */
+  int64_t channels; /* 1 .. 2^30 */
+  /* Strides in elements: of a sequence (not used for packed rows) and of a
+   * token.  Channels are contiguous. */
+  int64_t x_stride[2], g_stride[2], beta_stride[2];
+  int dtype;      /* of x and y: FFT_ELEM_F32, _BF16 or _F16 */
+  int gtype;      /* of g and beta: dtype or FFT_ELEM_F32 */
+  int clear_rows; /* packed rows of no sequence, in y or the gradients: 0 = left
+                     unwritten, else written as 0 */
+} fft_recurrence_desc;
+
+/*
+ * fft_linear_recurrence -- whole sequences.
+ *   offsets        as in fft_delta_rule: NULL, or int32 [batch + 1] on the
+ *                  device with the first rows of packed sequences.
+ *   initial_state  float [batch][channels]; NULL: zero.
+ *   final_state    the same, written; may be NULL; may be initial_state.
+ *   y              [batch][tokens][channels], or [tokens][channels] with
+ *                  offsets; contiguous.
+ * Tokens are combined in an order that depends on the sizes alone.  A value that
+ * is not finite spoils the later outputs of its sequence and channel.
+ */
+int fft_linear_recurrence(const fft_recurrence_desc *desc, const void *x, const void *g,
+                          const void *beta, const int32_t *offsets, const float *initial_state,
+                          void *y, float *final_state, void *stream);
+
+/*
+ * fft_linear_recurrence_backward -- the gradients, from dy (contiguous, like
+ * y), the forward call's y and (NULL: zero) the gradient of the final state.
+ *   dx             like y, contiguous; dg, dbeta the same of type gtype.
+ *                  dbeta and x are not used where beta is NULL.
+ *   dfinal_state, dinitial_state  float [batch][channels]; dinitial_state may
+ *                  be NULL, and may be dfinal_state.
+ * dg takes the states as y holds them, rounded to its type.  No output overlaps
+ * an input or another output except as said.
+ */
+int fft_linear_recurrence_backward(const fft_recurrence_desc *desc, const void *dy, const void *x,
+                                   const void *g, const void *beta, const void *y,
+                                   const int32_t *offsets, const float *initial_state,
+                                   const float *dfinal_state, void *dx, void *dg, void *dbeta,
+                                   float *dinitial_state, void *stream);
+
+/*
+ * fft_linear_recurrence_step -- a few tokens per sequence (decoding): the
+ * states are updated in place.
+ *   state  float [pool][channels].
+ *   slots  as in fft_delta_rule_step: int32 [batch] on the device, distinct; a
+ *          sequence whose slot is outside 0 .. pool - 1 is idle: its y is 0.
+ *          NULL: sequence i has state i (pool >= batch).
+ *   y      [batch][tokens][channels], contiguous.
+ */
+int fft_linear_recurrence_step(const fft_recurrence_desc *desc, const void *x, const void *g,
+                               const void *beta, float *state, const int32_t *slots, int64_t pool,
+                               void *y, void *stream);
+
+/*
+ * fft_linear_cross_entropy -- the cross entropy of the logits x w^T, which are
+ * never stored: lse_n = log sum_v e^{x_n . w_v}, loss_n = lse_n - x_n . w_{t_n}.
+ *   x          tokens x dim elements of type dtype (FFT_ELEM_F32, _BF16 or
+ *              _F16), row stride ldx >= dim.
+ *   w          vocabulary x dim of the same type, row stride ldw >= dim.
+ *   targets    `tokens` integers of target_bytes = 4 or 8 bytes, on the device; a
+ *              target outside 0 .. vocabulary - 1 is none: the loss is 0.
+ *   loss, lse  float, `tokens` each.
+ *   tokens     0 .. 2^24; vocabulary 1 .. 2^24; dim 1 .. 2^20.
+ *   workspace  fft_linear_cross_entropy_workspace_bytes(..., backward = 0) bytes:
+ *              8 per token and 128 words, and copies of float operands and of
+ *              those whose rows do not lie on 16-byte boundaries.
+ * Products of 16-bit operands are exact and added in float; float operands keep
+ * 24 significand bits as three bfloat16 values each.
+ *
+ * fft_linear_cross_entropy_backward -- its gradients, from the gradient dloss of
+ * the losses (float) and the forward call's lse:
+ *   G_nv = dloss_n (e^{x_n . w_v - lse_n} - [v = t_n]),  dx = G w,  dw = G^T x.
+ *   dx, dw     tokens x dim and vocabulary x dim of type dtype, contiguous; each
+ *              may be NULL.  Sums are float, rounded once.
+ *   workspace  fft_linear_cross_entropy_workspace_bytes(..., backward = 1) bytes:
+ *              G of up to 256 MB at a time (of 1024 words at least), a copy of x and a float dx
+ *              (up to 32 of a small one).
+ * G takes part in the products in the operands' type (float: as they).  Tokens
+ * without a target, or with a dloss of 0, take no part: what their rows of x
+ * hold does not matter.
+ */
+size_t fft_linear_cross_entropy_workspace_bytes(const void *x, int64_t ldx, const void *w,
+                                                int64_t ldw, int64_t tokens, int64_t vocabulary,
+                                                int64_t dim, int dtype, int backward);
+int fft_linear_cross_entropy(const void *x, int64_t ldx, const void *w, int64_t ldw,
+                             const void *targets, int target_bytes, float *loss, float *lse,
+                             int64_t tokens, int64_t vocabulary, int64_t dim, int dtype,
+                             void *workspace, size_t workspace_bytes, void *stream);
+int fft_linear_cross_entropy_backward(const float *dloss, const void *x, int64_t ldx, const void *w,
+                                      int64_t ldw, const void *targets, int target_bytes,
+                                      const float *lse, void *dx, void *dw, int64_t tokens,
+                                      int64_t vocabulary, int64_t dim, int dtype, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
 /* Last status recorded on this host thread by a call that returns a
  * pointer (fft_plan_create). */
 int fft_last_status(void);
