@@ -4,6 +4,8 @@
 
 #include <stdint.h>
 
+#include "tcgen05.cuh"
+
 namespace fftgb {
 
 __device__ __forceinline__ uint32_t block_rank() {
@@ -34,10 +36,41 @@ __device__ __forceinline__ uint32_t peer_load(uint32_t addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void peer_store(uint32_t addr, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y),
-               "f"(v.z), "f"(v.w)
-               : "memory");
+// Writes 16 bytes into another block's shared memory and counts them at its
+// barrier: no fence, so stores to global memory under way hold nothing up.
+__device__ __forceinline__ void peer_send(uint32_t addr, float4 v, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, "
+      "[%5];" ::"r"(addr),
+      "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+      : "memory");
+}
+
+// Whether the phase has completed, other blocks' writes before it seen.
+__device__ __forceinline__ bool poll_cluster(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// A wait for it that ends after some seconds, or when `failed` (shared memory) says
+// that another of the block's has; `status`: the device status word.
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *failed,
+                                             int *status) {
+  if (poll_cluster(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t it = 0; it < (1u << 24); ++it) {
+    if (poll_cluster(bar, parity)) return true;
+    if (*failed || clock64() - t0 > 8000000000ll) break;  // about 4 s
+  }
+  *failed = 1;
+  atomicExch(status, 1);  // kDeviceErrorTimeout
+  return false;
 }
 
 }  // namespace fftgb

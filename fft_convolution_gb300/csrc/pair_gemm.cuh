@@ -72,31 +72,6 @@ __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
-// Whether the phase has completed, other blocks' writes before it seen.
-__device__ __forceinline__ bool poll_cluster(uint64_t *bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.b32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *failed,
-                                             int *status) {
-  if (poll_cluster(bar, parity)) return true;
-  const long long t0 = clock64();
-  for (uint32_t it = 0; it < (1u << 24); ++it) {
-    if (poll_cluster(bar, parity)) return true;
-    if (*failed || clock64() - t0 > 8000000000ll) break;  // about 4 s
-  }
-  *failed = 1;
-  atomicExch(status, 1);  // kDeviceErrorTimeout
-  return false;
-}
-
 // ---- a tile's work ---------------------------------------------------------------------
 
 // One tile of A B^T summed over blocks k0 .. k1 - 1 of 64 indexes, for every

@@ -2,64 +2,62 @@
 //
 //   h_t = a_t h_{t-1} + b_t x_t,  a_t = e^{g_t},  y_t = h_t,
 //
-// its gradients and single tokens.  With d_t the gradient of h_t and e_t that
+// its gradients and single tokens.  With d_t the gradient of h_t and m_t that
 // of h_{t-1} through token t, from the end
 //
-//   d_t = dy_t + e_{t+1},  e_t = a_t d_t,
-//   dx_t = b_t d_t,  db_t = x_t d_t,  dg_t = e_t h_{t-1},  dh_0 = e_1.
+//   d_t = dy_t + m_{t+1},  m_t = a_t d_t,
+//   dx_t = b_t d_t,  db_t = x_t d_t,  dg_t = m_t h_{t-1},  dh_0 = m_1.
 //
-// Both are bound by HBM if enough loads are under way.  A block of 8 warps has
-// 128 channels, four per lane, and a warp 4 tokens of them at a time: its loads
-// for the next step are issued before it waits for anything.  Tokens
-// combine as maps h -> A h + H: each warp's into shared memory, each block's into
-// the shared memory of the other blocks of a cluster, which has one sequence and
-// walks it in steps of 32 tokens per block.  The state behind a step follows from the blocks'
-// maps, which every block combines for itself, so a step has one barrier.
-// Outputs are computed by the recurrence as it stands from the state in front of
-// the warp's tokens: the maps only carry it there.
+// HBM is the bound, if enough loads are under way and little else is done: a
+// block has 128 channels, four per lane of its 8 warps, and takes its tokens in
+// tiles that the TMA brings two ahead.  A warp has K tokens of a tile.  Tokens
+// combine as maps h -> A h + H: a warp's into shared memory, a block's (composed
+// by all its warps, a few channels each) into the shared memory of the other
+// blocks of its cluster, which share the sequence and walk it together, a tile
+// each per step.  The maps carry the state to the front of each warp's tokens;
+// outputs follow from there by the recurrence as it stands.
 #pragma once
+
+#include <cuda.h>
+
+#include <stddef.h>
 
 #include "cluster.cuh"
 #include "seq.h"
+#include "tcgen05.cuh"
 
 namespace fftgb {
 namespace {
 
-constexpr int kRecurWarps = 8, kRecurTok = 4, kRecurWide = 128, kRecurBlocks = 8;
+constexpr int kRecurWarps = 8, kRecurThreads = 256, kRecurWide = 128, kRecurBlocks = 8;
 
-// Four channels of a lane as they are loaded: adjacent ones (VEC), or 32 apart.
-template <typename T> struct Raw4 {
-  T v[4];
-};
-template <typename T> struct alignas(4 * sizeof(T)) Vec4 {
+// Four channels of a lane: adjacent ones (VEC: what the TMA brings as rows of 128
+// channels), or 32 apart, which the lane's own copies put there.
+template <typename T> struct alignas(4 * sizeof(T)) Four {
   T v[4];
 };
 template <typename T, bool VEC> struct Lane4 {
   static __device__ __forceinline__ int at(int c0, int lane, int i) {
     return VEC ? c0 + 4 * lane + i : c0 + lane + 32 * i;
   }
-  static __device__ __forceinline__ void load(Raw4<T> &r, const T *row, bool on, int c0, int lane,
-                                              int channels) {
-    if constexpr (VEC) {
-      const int c = at(c0, lane, 0);
-      Vec4<T> w{};
-      if (on && c < channels) {
-        if constexpr (sizeof(T) == 2) {
-          const uint2 u = __ldg(reinterpret_cast<const uint2 *>(row + c));
-          w = *reinterpret_cast<const Vec4<T> *>(&u);
-        } else {
-          const uint4 u = __ldg(reinterpret_cast<const uint4 *>(row + c));
-          w = *reinterpret_cast<const Vec4<T> *>(&u);
-        }
-      }
+  // Copies them from a row to *dst: by asynchronous copies as far as there are
+  // any of the elements' size.  Channels behind the last are left as they are.
+  static __device__ __forceinline__ void fetch(Four<T> *dst, const T *row, int c0, int lane,
+                                               int channels) {
+    const uint32_t d = smem_u32(dst);
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r.v[i] = w.v[i];
+      for (int i = 0; i < 4; ++i)
+        if (at(c0, lane, i) < channels)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d + 4 * i),
+                       "l"(row + at(c0, lane, i))
+                       : "memory");
     } else {
+      Four<T> w;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = at(c0, lane, i);
-        r.v[i] = on && c < channels ? __ldg(row + c) : from_acc<T>(0.0f);
-      }
+      for (int i = 0; i < 4; ++i)
+        w.v[i] = at(c0, lane, i) < channels ? __ldg(row + at(c0, lane, i)) : from_acc<T>(0.0f);
+      *dst = w;
     }
   }
   static __device__ __forceinline__ void store(T *row, int c0, int lane, int channels,
@@ -67,7 +65,7 @@ template <typename T, bool VEC> struct Lane4 {
     if constexpr (VEC) {
       const int c = at(c0, lane, 0);
       if (c >= channels) return;
-      Vec4<T> w;
+      Four<T> w;
 #pragma unroll
       for (int i = 0; i < 4; ++i) w.v[i] = from_acc<T>(f[i]);
       if constexpr (sizeof(T) == 2)
@@ -82,7 +80,77 @@ template <typename T, bool VEC> struct Lane4 {
       }
     }
   }
+  // Straight from global memory.
+  static __device__ __forceinline__ void load(float (&f)[4], const T *row, bool on, int c0, int lane,
+                                              int channels) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = at(c0, lane, i);
+      f[i] = on && c < channels ? to_acc(row[c]) : 0.0f;
+    }
+  }
 };
+// Four channels as two pairs, which most instructions take at once.
+struct Pairs {
+  float2 p[2];
+};
+__device__ __forceinline__ Pairs widen(const Four<float> &v) {
+  return Pairs{{make_float2(v.v[0], v.v[1]), make_float2(v.v[2], v.v[3])}};
+}
+__device__ __forceinline__ Pairs widen(const Four<__half> &v) {
+  const uint2 u = *reinterpret_cast<const uint2 *>(&v);
+  return Pairs{{__half22float2(*reinterpret_cast<const __half2 *>(&u.x)),
+                __half22float2(*reinterpret_cast<const __half2 *>(&u.y))}};
+}
+__device__ __forceinline__ Pairs widen(const Four<__nv_bfloat16> &v) {
+  const uint2 u = *reinterpret_cast<const uint2 *>(&v);
+  return Pairs{{make_float2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u)),
+                make_float2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u))}};
+}
+__device__ __forceinline__ Pairs operator*(const Pairs &a, const Pairs &b) {
+  return Pairs{{mul2(a.p[0], b.p[0]), mul2(a.p[1], b.p[1])}};
+}
+__device__ __forceinline__ Pairs fma4(const Pairs &a, const Pairs &b, const Pairs &c) {
+  return Pairs{{fma2(a.p[0], b.p[0], c.p[0]), fma2(a.p[1], b.p[1], c.p[1])}};
+}
+__device__ __forceinline__ Pairs splat(float v) { return Pairs{{both(v), both(v)}}; }
+// e^g as 2^(g log2 e): both off by about 2^-23, the rounding of the product by
+// |g| 2^-24 more, and no rounding of its own as expf has (eight instructions).
+__device__ __forceinline__ Pairs decay(const Pairs &g) {
+  Pairs t = g * splat(1.4426950408889634f);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t.p[i].x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t.p[i].y));
+  }
+  return t;
+}
+__device__ __forceinline__ void unpair(const Pairs &a, float (&f)[4]) {
+  f[0] = a.p[0].x;
+  f[1] = a.p[0].y;
+  f[2] = a.p[1].x;
+  f[3] = a.p[1].y;
+}
+__device__ __forceinline__ Pairs pair_up(const float (&f)[4]) {
+  return Pairs{{make_float2(f[0], f[1]), make_float2(f[2], f[3])}};
+}
+__device__ __forceinline__ Pairs pair_up(float4 v) {
+  return Pairs{{make_float2(v.x, v.y), make_float2(v.z, v.w)}};
+}
+__device__ __forceinline__ float4 quad(const Pairs &a) {
+  return make_float4(a.p[0].x, a.p[0].y, a.p[1].x, a.p[1].y);
+}
+// A product of decays above float's range (g > 0) ends at its largest value,
+// which leaves a state of 0 alone where infinity would not.
+__device__ __forceinline__ Pairs bounded(Pairs a) {
+  constexpr float most = 3.402823466e38f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    a.p[i].x = a.p[i].x > most ? most : a.p[i].x;
+    a.p[i].y = a.p[i].y > most ? most : a.p[i].y;
+  }
+  return a;
+}
 
 // A state of four channels, whose array needs no more than its elements' alignment
 // (adjacent loads of a lane share their sectors).
@@ -105,65 +173,110 @@ __device__ __forceinline__ void store_state(float *row, int c0, int lane, int ch
   }
 }
 
-// A state behind a map.  A product of decays may be infinite where g > 0: it
-// changes no state of 0.
-__device__ __forceinline__ void apply(float4 A, float4 H, float (&s)[4]) {
-  s[0] = s[0] == 0.0f ? H.x : fmaf(A.x, s[0], H.x);
-  s[1] = s[1] == 0.0f ? H.y : fmaf(A.y, s[1], H.y);
-  s[2] = s[2] == 0.0f ? H.z : fmaf(A.z, s[2], H.z);
-  s[3] = s[3] == 0.0f ? H.w : fmaf(A.w, s[3], H.w);
+struct RecurShared {
+  // maps h -> a h + h0 of the warps, of the cluster's blocks by step parity, and the
+  // states in front of the warps' tokens: of four channels each
+  float4 warp_a[kRecurWarps][32], warp_h[kRecurWarps][32];
+  float4 block_a[2][kRecurBlocks][32], block_h[2][kRecurBlocks][32];
+  float4 state[kRecurWarps][32];
+  uint64_t full[4];  // the stages' tiles have come
+  uint64_t sent[2];  // the blocks' maps have come
+  // A wait has run out: for a tile, for maps.  All threads look at each behind a
+  // barrier that everyone who may set it has passed, so they leave together.
+  int failed[2];
+};
+constexpr size_t kRecurShared = (sizeof(RecurShared) + 127) / 128 * 128;
+// Behind it the stages: of each input a tile of tokens x 128 channels.
+
+__device__ __forceinline__ void exchange_begin(RecurShared &sh, int blocks) {
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 4; ++i) bar_init(&sh.full[i], 1);
+    bar_init(&sh.sent[0], 1);
+    bar_init(&sh.sent[1], 1);
+    sh.failed[0] = sh.failed[1] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  if (blocks > 1) cluster_sync();  // every block's shared memory is there
 }
 
-struct RecurShared {
-  float4 warp_a[2][kRecurWarps][32], warp_h[2][kRecurWarps][32];      // by step parity
-  float4 block_a[2][kRecurBlocks][32], block_h[2][kRecurBlocks][32];  // of every block of the cluster
+// A lane's share of an exchange: channels 4 quad .. of the tile, for the block
+// (then the warp) `to`.  Eight lanes have the same channels: their loads are one.
+struct Share {
+  int quad, to;
 };
-
-// Hands this warp's map round; afterwards s is the state in front of the warp's tokens
-// and `carry` the one behind the whole step.
-__device__ __forceinline__ void exchange(RecurShared &sh, int parity, int rank, int blocks,
-                                         const float (&A)[4], const float (&H)[4],
-                                         float (&carry)[4], float (&s)[4]) {
+__device__ __forceinline__ Share my_share() {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  sh.warp_a[parity][warp][lane] = make_float4(A[0], A[1], A[2], A[3]);
-  sh.warp_h[parity][warp][lane] = make_float4(H[0], H[1], H[2], H[3]);
+  return Share{4 * warp + (lane & 3), lane >> 2};
+}
+
+// Step n, all of a block's warps: hands the warp's map A h + H round, after
+// which s is the state in front of the warp's tokens, and `carry` (of the lane's share)
+// the one behind the step.  `between` runs when every warp has come here.
+// False: a wait has run out.
+// A block map's buffer is written again two steps later: by a block that has the
+// maps of the step between, which are sent when all warps have read the older ones.
+template <class Between>
+__device__ __forceinline__ bool exchange(RecurShared &sh, uint32_t n, int rank, int blocks,
+                                         const Pairs &A, const Pairs &H, Pairs &carry, Pairs &s,
+                                         int *status, Between between) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, parity = n & 1;
+  const Share my = my_share();
+  sh.warp_a[warp][lane] = quad(bounded(A));
+  sh.warp_h[warp][lane] = quad(H);
   __syncthreads();
-  if (blocks > 1) {
-    if (warp < blocks) {  // warp w tells block w
-      float4 a = sh.warp_a[parity][0][lane];
-      const float4 h = sh.warp_h[parity][0][lane];
-      float t[4] = {h.x, h.y, h.z, h.w};
+  if (*(volatile int *)&sh.failed[0]) return false;
+  between();
+  Pairs a[kRecurWarps], h[kRecurWarps];
 #pragma unroll
-      for (int w = 1; w < kRecurWarps; ++w) {
-        const float4 b = sh.warp_a[parity][w][lane];
-        apply(b, sh.warp_h[parity][w][lane], t);
-        a = make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
-      }
-      peer_store(peer((uint32_t)__cvta_generic_to_shared(&sh.block_a[parity][rank][lane]), warp), a);
-      peer_store(peer((uint32_t)__cvta_generic_to_shared(&sh.block_h[parity][rank][lane]), warp),
-                 make_float4(t[0], t[1], t[2], t[3]));
-    }
-    cluster_sync();
-    for (int r = 0; r < blocks; ++r) {
-      if (r == rank) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = carry[i];
-      }
-      apply(sh.block_a[parity][r][lane], sh.block_h[parity][r][lane], carry);
-    }
-#pragma unroll
-    for (int w = 0; w < kRecurWarps - 1; ++w)
-      if (w < warp) apply(sh.warp_a[parity][w][lane], sh.warp_h[parity][w][lane], s);
-  } else {
-#pragma unroll
-    for (int w = 0; w < kRecurWarps; ++w) {
-      if (w == warp) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = carry[i];
-      }
-      apply(sh.warp_a[parity][w][lane], sh.warp_h[parity][w][lane], carry);
-    }
+  for (int w = 0; w < kRecurWarps; ++w) {
+    a[w] = pair_up(sh.warp_a[w][my.quad]);
+    h[w] = pair_up(sh.warp_h[w][my.quad]);
   }
+  if (blocks > 1) {
+    if (threadIdx.x == 0) bar_arrive_tx(&sh.sent[parity], (uint32_t)blocks * 1024);
+    Pairs all_a = a[0], all_h = h[0];
+#pragma unroll
+    for (int w = 1; w < kRecurWarps; ++w) {
+      all_h = fma4(a[w], all_h, h[w]);
+      all_a = all_a * a[w];
+    }
+    if (my.to < blocks) {
+      const uint32_t bar = peer(smem_u32(&sh.sent[parity]), my.to);
+      peer_send(peer(smem_u32(&sh.block_a[parity][rank][my.quad]), my.to), quad(bounded(all_a)), bar);
+      peer_send(peer(smem_u32(&sh.block_h[parity][rank][my.quad]), my.to), quad(all_h), bar);
+    }
+    wait_cluster(&sh.sent[parity], (n >> 1) & 1, &sh.failed[1], status);
+    s = carry;
+#pragma unroll
+    for (int r = 0; r < kRecurBlocks; ++r)
+      if (r < blocks) {
+        if (r == rank) s = carry;
+        carry = fma4(pair_up(sh.block_a[parity][r][my.quad]), carry,
+                     pair_up(sh.block_h[parity][r][my.quad]));
+      }
+  } else {
+    s = carry;
+#pragma unroll
+    for (int w = 0; w < kRecurWarps; ++w) carry = fma4(a[w], carry, h[w]);
+  }
+#pragma unroll
+  for (int w = 0; w < kRecurWarps - 1; ++w)
+    if (w < my.to) s = fma4(a[w], s, h[w]);
+  sh.state[my.to][my.quad] = quad(s);
+  __syncthreads();
+  s = pair_up(sh.state[warp][lane]);
+  return *(volatile int *)&sh.failed[1] == 0;
+}
+
+// A tile of `rows` tokens of 128 channels, counted by the barrier.
+__device__ __forceinline__ void tile_load(void *dst, const CUtensorMap *map, int c, int t, int seq,
+                                          uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c), "r"(t), "r"(seq)
+      : "memory");
 }
 
 // The rows of a sequence: offsets that descend or leave the rows are raised
@@ -216,14 +329,45 @@ __device__ __forceinline__ void clear_rows(void *p, const RecurArgs &a, const Ro
       Lane4<T, VEC>::store(out + t * a.channels, c0, lane, a.channels, zero);
 }
 
+// The inputs' tensor maps, where the TMA loads them (VEC): x, g, beta, dy, y.
+struct RecurMaps {
+  CUtensorMap x, g, b, d, y;
+};
+// Tokens of a warp per step, where a lane's loads of one take `bytes`: two stages
+// of tiles fill shared memory, one block per SM.  A step costs about 1500 clocks
+// beside its tokens, so many small ones lose (prompt of 32768 tokens, 4096
+// channels in bf16: 173 us with 16 tokens, 252 with 8, 301 with 4).
+constexpr int kRecurStages = 2;
+constexpr int recur_tokens(int bytes) { return bytes <= 24 ? 16 : bytes <= 48 ? 8 : 4; }
+
 // T: x and y; G: g and beta.
+template <typename T, typename G, bool GATED> struct RecurForward {
+  static constexpr int K = recur_tokens(4 * (int)(sizeof(T) + sizeof(G) * (GATED ? 2 : 1)));
+  static constexpr int kTokens = kRecurWarps * K, S = kRecurStages;
+  struct Stage {
+    alignas(128) Four<T> x[kTokens][32];
+    alignas(128) Four<G> g[kTokens][32];
+    alignas(128) Four<G> b[GATED ? kTokens : 1][GATED ? 32 : 1];
+  };
+  static_assert(sizeof(Stage) % 128 == 0 && offsetof(Stage, g) % 128 == 0 && offsetof(Stage, b) % 128 == 0, "TMA");
+  static constexpr uint32_t kBytes = kTokens * 128 * (sizeof(T) + sizeof(G) * (GATED ? 2 : 1));
+  static constexpr size_t kSmem = 128 + kRecurShared + S * sizeof(Stage);
+};
 template <typename T, typename G, bool VEC, bool GATED>
-__global__ void __launch_bounds__(kRecurWarps * 32, 2) recur_kernel(const RecurArgs a) {
-  constexpr int K = kRecurTok;
+__global__ void __launch_bounds__(kRecurThreads)
+recur_kernel(const RecurArgs a, const __grid_constant__ RecurMaps maps, int *status) {
+  using P = RecurForward<T, G, GATED>;
+  constexpr int K = P::K, S = P::S;
   using LT = Lane4<T, VEC>;
   using LG = Lane4<G, VEC>;
-  __shared__ RecurShared sh;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  extern __shared__ char smem_raw[];
+  char *smem = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
+  RecurShared &sh = *reinterpret_cast<RecurShared *>(smem);
+  auto stage = [&](uint32_t n) -> typename P::Stage & {
+    return *reinterpret_cast<typename P::Stage *>(smem + kRecurShared +
+                                                  (n % S) * sizeof(typename P::Stage));
+  };
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = a.blocks > 1 ? (int)block_rank() : 0, C = a.channels;
   const long long unit = blockIdx.x / a.blocks;
   const int groups = (C + kRecurWide - 1) / kRecurWide;
@@ -236,60 +380,125 @@ __global__ void __launch_bounds__(kRecurWarps * 32, 2) recur_kernel(const RecurA
   const G *g = static_cast<const G *>(a.g) + sq * a.sg.seq + from * a.sg.tok;
   const G *b = GATED ? static_cast<const G *>(a.beta) + sq * a.sb.seq + from * a.sb.tok : nullptr;
   T *y = static_cast<T *>(a.y) + r.begin * C;
-  float carry[4];
-  load_state<VEC>(carry, a.state_in ? a.state_in + seq * C : nullptr, c0, lane, C);
-  if (a.blocks > 1) cluster_sync();  // every block's shared memory is there
+  const int step = a.blocks * P::kTokens;
+  exchange_begin(sh, a.blocks);
 
-  Raw4<T> rx[K];
-  Raw4<G> rg[K], rb[K];
-  auto fetch = [&](long long t0) {
+  // The tile of step n, from its first token on: the TMA for the whole block
+  // (thread 0), or this lane's part of it.
+  auto fetch = [&](uint32_t n) {
+    const long long t0 = (long long)n * step + rank * P::kTokens;
+    typename P::Stage &st = stage(n);
+    if constexpr (VEC) {
+      if (tid != 0 || t0 >= r.len) return;
+      const int t = (int)(from + t0);
+      bar_arrive_tx(&sh.full[n % S], P::kBytes);
+      tile_load(&st.x, &maps.x, c0, t, (int)sq, &sh.full[n % S]);
+      tile_load(&st.g, &maps.g, c0, t, (int)sq, &sh.full[n % S]);
+      if constexpr (GATED) tile_load(&st.b, &maps.b, c0, t, (int)sq, &sh.full[n % S]);
+    } else {
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-      const long long t = t0 + j;
-      const bool on = t < r.len;
-      LT::load(rx[j], x + t * a.sx.tok, on, c0, lane, C);
-      LG::load(rg[j], g + t * a.sg.tok, on, c0, lane, C);
-      if constexpr (GATED) LG::load(rb[j], b + t * a.sb.tok, on, c0, lane, C);
+      for (int j = 0; j < K; ++j) {
+        const long long t = t0 + warp * K + j;
+        if (t < r.len) {
+          LT::fetch(&st.x[warp * K + j][lane], x + t * a.sx.tok, c0, lane, C);
+          LG::fetch(&st.g[warp * K + j][lane], g + t * a.sg.tok, c0, lane, C);
+          if constexpr (GATED) LG::fetch(&st.b[warp * K + j][lane], b + t * a.sb.tok, c0, lane, C);
+        }
+      }
+      copy_group();
     }
   };
-  const int step = a.blocks * kRecurWarps * K;
-  long long t0 = (long long)(rank * kRecurWarps + warp) * K;
-  fetch(t0);
-  int parity = 0;
-  for (long long at = 0; at < r.len; at += step, t0 += step, parity ^= 1) {
-    float e[K][4], u[K][4], A[4] = {1, 1, 1, 1}, H[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < K; ++j)  // behind the end g = x = 0: h stays
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        e[j][i] = expf(to_acc(rg[j].v[i]));
-        u[j][i] = to_acc(rx[j].v[i]);
-        if constexpr (GATED) u[j][i] *= to_acc(rb[j].v[i]);
-        A[i] *= e[j][i];
-        H[i] = fmaf(e[j][i], H[i], u[j][i]);
-      }
-    fetch(t0 + step);
-    float s[4];
-    exchange(sh, parity, rank, a.blocks, A, H, carry, s);
+  for (uint32_t n = 0; n < S; ++n) fetch(n);
+  float state[4];
+  const Share my = my_share();
+  load_state<VEC>(state, a.state_in ? a.state_in + seq * C : nullptr, c0, my.quad, C);
+  Pairs carry = pair_up(state);
+  uint32_t n = 0;
+  for (long long at = 0; at < r.len; at += step, ++n) {
+    const long long t0 = at + rank * P::kTokens + warp * K;
+    const int count = (int)max(0ll, min((long long)K, r.len - t0));
+    Pairs e[K], u[K], A = splat(1.0f), H = splat(0.0f), h;
+    if constexpr (VEC) {
+      if (at + rank * P::kTokens < r.len)
+        wait_cluster(&sh.full[n % S], (n / S) & 1, &sh.failed[0], status);
+    } else {
+      copy_wait<S - 1>();
+    }
+    const typename P::Stage &st = stage(n);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = fmaf(e[j][i], s[i], u[j][i]);
-      if (t0 + j < r.len) LT::store(y + (t0 + j) * C, c0, lane, C, s);
+      if (j < count) {
+        e[j] = decay(widen(st.g[warp * K + j][lane]));
+        u[j] = widen(st.x[warp * K + j][lane]);
+        if constexpr (GATED) u[j] = u[j] * widen(st.b[warp * K + j][lane]);
+        A = A * e[j];
+        H = fma4(e[j], H, u[j]);
+      }
     }
+    if constexpr (!VEC) fetch(n + S);
+    if (!exchange(sh, n, rank, a.blocks, A, H, carry, h, status, [&] {
+          if constexpr (VEC) fetch(n + S);  // every warp has read the tile
+        }))
+      break;
+    T *py = y + t0 * C;
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (j < count) {
+        h = fma4(e[j], h, u[j]);
+        float o[4];
+        unpair(h, o);
+        LT::store(py, c0, lane, C, o);
+        py += C;
+      }
   }
-  if (a.state_out && rank == 0 && warp == 0)
-    store_state<VEC>(a.state_out + seq * C, c0, lane, C, carry);
+  if (a.state_out && rank == 0 && my.to == 0) {
+    unpair(carry, state);
+    store_state<VEC>(a.state_out + seq * C, c0, my.quad, C, state);
+  }
+  if (VEC && tid == 0 && (sh.failed[0] | sh.failed[1]))  // given up: no copy may land after the block has gone
+    for (uint32_t i = n; i < n + S; ++i)
+      if ((long long)i * step + rank * P::kTokens < r.len) bar_wait(&sh.full[i % S], (i / S) & 1);
+  __syncwarp();
+  if (a.blocks > 1) cluster_sync();  // nor a map come to one that has
 }
 
-// The same from the end: token len - 1 - t is the t-th.
+// The same from the end: tile n has the tokens behind those of tile n + 1, and a
+// warp's j-th token is the j-th from its end.
+template <typename T, typename G, bool GATED> struct RecurBackward {
+  // more than 8 would not leave registers for both factors of a token
+  static constexpr int kMost =
+      recur_tokens(4 * (int)(sizeof(T) * (GATED ? 3 : 2) + sizeof(G) * (GATED ? 2 : 1)));
+  static constexpr int K = kMost < 8 ? kMost : 8;
+  static constexpr int kTokens = kRecurWarps * K, S = kRecurStages;
+  struct Stage {
+    alignas(128) Four<T> d[kTokens][32];
+    alignas(128) Four<T> y[kTokens][32];
+    alignas(128) Four<G> g[kTokens][32];
+    alignas(128) Four<T> x[GATED ? kTokens : 1][GATED ? 32 : 1];
+    alignas(128) Four<G> b[GATED ? kTokens : 1][GATED ? 32 : 1];
+  };
+  static_assert(sizeof(Stage) % 128 == 0 && offsetof(Stage, y) % 128 == 0 && offsetof(Stage, g) % 128 == 0 &&
+                    offsetof(Stage, x) % 128 == 0 && offsetof(Stage, b) % 128 == 0,
+                "TMA");
+  static constexpr uint32_t kBytes =
+      kTokens * 128 * (sizeof(T) * (GATED ? 3 : 2) + sizeof(G) * (GATED ? 2 : 1));
+  static constexpr size_t kSmem = 128 + kRecurShared + S * sizeof(Stage);
+};
 template <typename T, typename G, bool VEC, bool GATED>
-__global__ void __launch_bounds__(kRecurWarps * 32, 2) recur_grad_kernel(const RecurArgs a) {
-  constexpr int K = kRecurTok;
+__global__ void __launch_bounds__(kRecurThreads)
+recur_grad_kernel(const RecurArgs a, const __grid_constant__ RecurMaps maps, int *status) {
+  using P = RecurBackward<T, G, GATED>;
+  constexpr int K = P::K, S = P::S;
   using LT = Lane4<T, VEC>;
   using LG = Lane4<G, VEC>;
-  __shared__ RecurShared sh;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  extern __shared__ char smem_raw[];
+  char *smem = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
+  RecurShared &sh = *reinterpret_cast<RecurShared *>(smem);
+  auto stage = [&](uint32_t n) -> typename P::Stage & {
+    return *reinterpret_cast<typename P::Stage *>(smem + kRecurShared +
+                                                  (n % S) * sizeof(typename P::Stage));
+  };
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = a.blocks > 1 ? (int)block_rank() : 0, C = a.channels;
   const long long unit = blockIdx.x / a.blocks;
   const int groups = (C + kRecurWide - 1) / kRecurWide;
@@ -310,77 +519,112 @@ __global__ void __launch_bounds__(kRecurWarps * 32, 2) recur_grad_kernel(const R
   T *dx = static_cast<T *>(a.dx) + r.begin * C;
   G *dg = static_cast<G *>(a.dg) + r.begin * C;
   G *db = GATED ? static_cast<G *>(a.dbeta) + r.begin * C : nullptr;
-  float carry[4];
-  load_state<VEC>(carry, a.dfinal ? a.dfinal + seq * C : nullptr, c0, lane, C);
-  if (a.blocks > 1) cluster_sync();
+  const int step = a.blocks * P::kTokens;
+  exchange_begin(sh, a.blocks);
 
-  Raw4<T> rd[K], ry[K], rx[K];
-  Raw4<G> rg[K], rb[K];
-  auto fetch = [&](long long t0) {
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-      const long long t = r.len - 1 - t0 - j;
-      const bool on = t >= 0;
-      LT::load(rd[j], dy + t * C, on, c0, lane, C);
-      LG::load(rg[j], g + t * a.sg.tok, on, c0, lane, C);
-      LT::load(ry[j], y + (t - 1) * C, t > 0, c0, lane, C);
+  auto fetch = [&](uint32_t n) {
+    const long long last = r.len - 1 - ((long long)n * step + rank * P::kTokens);  // its last token
+    typename P::Stage &st = stage(n);
+    if constexpr (VEC) {
+      if (tid != 0 || last < 0) return;
+      const int t = (int)(from + last) - (P::kTokens - 1);
+      uint64_t *bar = &sh.full[n % S];
+      bar_arrive_tx(bar, P::kBytes);
+      tile_load(&st.d, &maps.d, c0, t, (int)sq, bar);
+      tile_load(&st.g, &maps.g, c0, t, (int)sq, bar);
+      tile_load(&st.y, &maps.y, c0, t - 1, (int)sq, bar);
       if constexpr (GATED) {
-        LT::load(rx[j], x + t * a.sx.tok, on, c0, lane, C);
-        LG::load(rb[j], b + t * a.sb.tok, on, c0, lane, C);
+        tile_load(&st.x, &maps.x, c0, t, (int)sq, bar);
+        tile_load(&st.b, &maps.b, c0, t, (int)sq, bar);
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        const long long t = last - warp * K - j;
+        const int row = P::kTokens - 1 - warp * K - j;
+        if (t >= 0) {
+          LT::fetch(&st.d[row][lane], dy + t * C, c0, lane, C);
+          LG::fetch(&st.g[row][lane], g + t * a.sg.tok, c0, lane, C);
+          if (t > 0) LT::fetch(&st.y[row][lane], y + (t - 1) * C, c0, lane, C);
+          if constexpr (GATED) {
+            LT::fetch(&st.x[row][lane], x + t * a.sx.tok, c0, lane, C);
+            LG::fetch(&st.b[row][lane], b + t * a.sb.tok, c0, lane, C);
+          }
+        }
+      }
+      copy_group();
     }
   };
-  const int step = a.blocks * kRecurWarps * K;
-  long long t0 = (long long)(rank * kRecurWarps + warp) * K;
-  int parity = 0;
-  fetch(t0);
-  for (long long at = 0; at < r.len; at += step, t0 += step, parity ^= 1) {
-    float e[K][4], d[K][4], A[4] = {1, 1, 1, 1}, H[4] = {0, 0, 0, 0};
-    Raw4<T> ky[K], kx[K];
-    Raw4<G> kb[K];
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-      ky[j] = ry[j];
-      if constexpr (GATED) kx[j] = rx[j], kb[j] = rb[j];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        e[j][i] = expf(to_acc(rg[j].v[i]));
-        d[j][i] = to_acc(rd[j].v[i]);
-        A[i] *= e[j][i];
-        H[i] = e[j][i] * (H[i] + d[j][i]);
-      }
+  for (uint32_t n = 0; n < S; ++n) fetch(n);
+  float state[4];
+  const Share my = my_share();
+  load_state<VEC>(state, a.dfinal ? a.dfinal + seq * C : nullptr, c0, my.quad, C);
+  Pairs carry = pair_up(state);
+  uint32_t n = 0;
+  for (long long at = 0; at < r.len; at += step, ++n) {
+    const long long t0 = r.len - 1 - at - rank * P::kTokens - warp * K;
+    const int count = (int)max(0ll, min((long long)K, t0 + 1));
+    const int row = P::kTokens - 1 - warp * K;
+    Pairs e[K], d[K], A = splat(1.0f), H = splat(0.0f), m;
+    if constexpr (VEC) {
+      if (at + rank * P::kTokens < r.len)
+        wait_cluster(&sh.full[n % S], (n / S) & 1, &sh.failed[0], status);
+    } else {
+      copy_wait<S - 1>();
     }
-    fetch(t0 + step);
-    float s[4];
-    exchange(sh, parity, rank, a.blocks, A, H, carry, s);
+    const typename P::Stage &st = stage(n);
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-      const long long t = r.len - 1 - t0 - j;
-      float before[4], o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) before[i] = to_acc(ky[j].v[i]);
-      if (t == 0) load_state<VEC>(before, a.state_in ? a.state_in + seq * C : nullptr, c0, lane, C);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        d[j][i] += s[i];
-        s[i] = e[j][i] * d[j][i];
+    for (int j = 0; j < K; ++j)
+      if (j < count) {
+        e[j] = decay(widen(st.g[row - j][lane]));
+        d[j] = widen(st.d[row - j][lane]);
+        A = A * e[j];
+        H = fma4(e[j], H, e[j] * d[j]);
       }
-      if (t < 0) continue;
+    if (!exchange(sh, n, rank, a.blocks, A, H, carry, m, status, [&] {
+          // every warp is done with the tile before this one
+          if (VEC && n > 0) fetch(n - 1 + S);
+        }))
+      break;
+    T *px = dx + t0 * C;
+    G *pg = dg + t0 * C, *pb = GATED ? db + t0 * C : nullptr;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = s[i] * before[i];
-      LG::store(dg + t * C, c0, lane, C, o);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = GATED ? to_acc(kb[j].v[i]) * d[j][i] : d[j][i];
-      LT::store(dx + t * C, c0, lane, C, o);
-      if constexpr (GATED) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = to_acc(kx[j].v[i]) * d[j][i];
-        LG::store(db + t * C, c0, lane, C, o);
+    for (int j = 0; j < K; ++j)
+      if (j < count) {
+        const Pairs now = Pairs{{make_float2(m.p[0].x + d[j].p[0].x, m.p[0].y + d[j].p[0].y),
+                                 make_float2(m.p[1].x + d[j].p[1].x, m.p[1].y + d[j].p[1].y)}};
+        m = e[j] * now;
+        Pairs before = widen(st.y[row - j][lane]);
+        if (j == t0) {
+          load_state<VEC>(state, a.state_in ? a.state_in + seq * C : nullptr, c0, lane, C);
+          before = pair_up(state);
+        }
+        float o[4];
+        unpair(m * before, o);
+        LG::store(pg, c0, lane, C, o);
+        Pairs out = now;
+        if constexpr (GATED) {
+          unpair(now * widen(st.x[row - j][lane]), o);
+          LG::store(pb, c0, lane, C, o);
+          out = now * widen(st.b[row - j][lane]);
+        }
+        unpair(out, o);
+        LT::store(px, c0, lane, C, o);
+        px -= C;
+        pg -= C;
+        if constexpr (GATED) pb -= C;
       }
-    }
+    if constexpr (!VEC) fetch(n + S);
   }
-  if (a.dinitial && rank == 0 && warp == 0)
-    store_state<VEC>(a.dinitial + seq * C, c0, lane, C, carry);
+  if (a.dinitial && rank == 0 && my.to == 0) {
+    unpair(carry, state);
+    store_state<VEC>(a.dinitial + seq * C, c0, my.quad, C, state);
+  }
+  if (VEC && tid == 0 && (sh.failed[0] | sh.failed[1]))
+    for (uint32_t i = n; i < n + S; ++i)
+      if ((long long)i * step + rank * P::kTokens < r.len) bar_wait(&sh.full[i % S], (i / S) & 1);
+  __syncwarp();
+  if (a.blocks > 1) cluster_sync();
 }
 
 // Single tokens: a thread has four channels of a sequence.
@@ -404,16 +648,14 @@ __global__ void __launch_bounds__(128) recur_step_kernel(const RecurArgs a) {
   float h[4];
   load_state<VEC>(h, state, c0, lane, C);
   for (long long t = 0; t < a.tokens; ++t) {
-    Raw4<T> rx;
-    Raw4<G> rg, rb;
-    LT::load(rx, x + t * a.sx.tok, live, c0, lane, C);
-    LG::load(rg, g + t * a.sg.tok, live, c0, lane, C);
-    if constexpr (GATED) LG::load(rb, b + t * a.sb.tok, live, c0, lane, C);
+    float fx[4], fg[4], fb[4];
+    LT::load(fx, x + t * a.sx.tok, live, c0, lane, C);
+    LG::load(fg, g + t * a.sg.tok, live, c0, lane, C);
+    if constexpr (GATED) LG::load(fb, b + t * a.sb.tok, live, c0, lane, C);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float u = to_acc(rx.v[i]);
-      if constexpr (GATED) u *= to_acc(rb.v[i]);
-      h[i] = fmaf(expf(to_acc(rg.v[i])), h[i], u);
+      if constexpr (GATED) fx[i] *= fb[i];
+      h[i] = fmaf(expf(fg[i]), h[i], fx[i]);
     }
     LT::store(y + t * C, c0, lane, C, h);
   }
@@ -422,31 +664,69 @@ __global__ void __launch_bounds__(128) recur_step_kernel(const RecurArgs a) {
 
 // ---- launches ----------------------------------------------------------------------
 
-// Rows of four channels that can be moved at once.
-template <typename E> bool vec_rows4(const void *p, const RecurStride &s) {
-  return ((uintptr_t)p & (4 * sizeof(E) - 1)) == 0 && s.seq % 4 == 0 && s.tok % 4 == 0;
-}
-template <typename T, typename G> bool vec_recur(const RecurArgs &a) {
-  const RecurStride own{0, 0};
-  return a.channels % 4 == 0 && vec_rows4<T>(a.x, a.sx) && vec_rows4<G>(a.g, a.sg) &&
-         vec_rows4<G>(a.beta, a.sb) && vec_rows4<T>(a.y, own) && vec_rows4<T>(a.dy, own) &&
-         vec_rows4<T>(a.dx, own) && vec_rows4<G>(a.dg, own) && vec_rows4<G>(a.dbeta, own);
+using RecurEncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline RecurEncodeFn recur_encode() {
+  static RecurEncodeFn fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return static_cast<RecurEncodeFn>(nullptr);
+    return reinterpret_cast<RecurEncodeFn>(p);
+  }();
+  return fn;
 }
 
-template <typename F> cudaError_t launch_clusters(F *kern, RecurArgs a, cudaStream_t st) {
+// The map of an array [sequence][token][channel] (packed: [1][row][channel])
+// in tiles of `tokens` x 128 channels; false where the TMA cannot take its rows.
+template <typename E>
+bool recur_map(CUtensorMap *map, const void *p, const RecurStride &s, const RecurArgs &a, int tokens) {
+  const long long seqs = a.offsets ? 1 : a.batch, bytes = (long long)sizeof(E);
+  const long long tok = a.tokens > 1 ? s.tok * bytes : 16;
+  const long long seq = seqs > 1 ? s.seq * bytes : tok;
+  RecurEncodeFn fn = recur_encode();
+  if (!fn || ((uintptr_t)p & 15) != 0 || a.channels % 4 != 0 || tok <= 0 || seq <= 0 || tok % 16 != 0 ||
+      seq % 16 != 0 || tok >= (1ll << 40) || seq >= (1ll << 40) || a.tokens == 0)
+    return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)a.channels, (cuuint64_t)a.tokens, (cuuint64_t)seqs};
+  const cuuint64_t strides[2] = {(cuuint64_t)tok, (cuuint64_t)seq};
+  const cuuint32_t box[3] = {kRecurWide, (cuuint32_t)tokens, 1}, ones[3] = {1, 1, 1};
+  const CUtensorMapDataType type = sizeof(E) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                                  : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+  return fn(map, type, 3, const_cast<void *>(p), dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Outputs in stores of four elements.
+template <typename E> bool quads(const void *p) { return ((uintptr_t)p & (4 * sizeof(E) - 1)) == 0; }
+
+template <typename F>
+cudaError_t launch_clusters(F *kern, RecurArgs a, const RecurMaps &maps, int tokens, size_t smem,
+                            DeviceOnce &once, std::atomic<int> (&resident)[64], cudaStream_t st) {
+  int *status = device_status_word();
+  if (!status) return cudaErrorInvalidDevice;
+  cudaError_t e = smem_limit_once((const void *)kern, smem, once);
+  if (e != cudaSuccess) return e;
   const long long groups = (a.channels + kRecurWide - 1) / kRecurWide, units = a.batch * groups;
-  const long long room = 2ll * sm_count();  // two blocks per SM
+  const long long room =
+      (long long)sm_count() * blocks_per_sm_once((const void *)kern, kRecurThreads, smem, resident);
   if (room <= 0) return cudaErrorInvalidDevice;
   // Sequences share a GPU of many SMs: more blocks along one while there is
   // room for them and it has tokens for them.
   const long long mean = a.offsets ? (a.tokens + a.batch - 1) / a.batch : a.tokens;
   a.blocks = 1;
   while (a.blocks < kRecurBlocks && units * a.blocks * 2 <= room &&
-         mean > (long long)a.blocks * kRecurWarps * kRecurTok)
+         mean > (long long)a.blocks * tokens)
     a.blocks *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(units * a.blocks));
-  cfg.blockDim = dim3(kRecurWarps * 32);
+  cfg.blockDim = dim3(kRecurThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -455,24 +735,50 @@ template <typename F> cudaError_t launch_clusters(F *kern, RecurArgs a, cudaStre
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = a.blocks > 1 ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, (const RecurArgs)a);
+  e = cudaLaunchKernelEx(&cfg, kern, (const RecurArgs)a, maps, status);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T, typename G, bool VEC, bool GATED>
+cudaError_t recur_whole(bool grad, const RecurArgs &a, const RecurMaps &maps, cudaStream_t st) {
+  static DeviceOnce once[2];
+  static std::atomic<int> resident[2][64];
+  using F = RecurForward<T, G, GATED>;
+  using B = RecurBackward<T, G, GATED>;
+  return grad ? launch_clusters(&recur_grad_kernel<T, G, VEC, GATED>, a, maps, B::kTokens, B::kSmem,
+                                once[1], resident[1], st)
+              : launch_clusters(&recur_kernel<T, G, VEC, GATED>, a, maps, F::kTokens, F::kSmem,
+                                once[0], resident[0], st);
+}
+template <typename T, typename G, bool GATED>
 cudaError_t recur_kind(int what, const RecurArgs &a, cudaStream_t st) {
-  if (what == 0) return launch_clusters(&recur_kernel<T, G, VEC, GATED>, a, st);
-  if (what == 1) return launch_clusters(&recur_grad_kernel<T, G, VEC, GATED>, a, st);
-  const long long units = a.batch * ((a.channels + kRecurWide - 1) / kRecurWide);
-  recur_step_kernel<T, G, VEC, GATED><<<(unsigned)((units + 3) / 4), 128, 0, st>>>(a);
-  return cudaGetLastError();
+  if (what == 2) {
+    const auto fits = [&](const void *p, const RecurStride &s, size_t e) {
+      return ((uintptr_t)p & (4 * e - 1)) == 0 && s.seq % 4 == 0 && s.tok % 4 == 0;
+    };
+    const bool vec = a.channels % 4 == 0 && quads<T>(a.y) && fits(a.x, a.sx, sizeof(T)) &&
+                     fits(a.g, a.sg, sizeof(G)) && fits(a.beta, a.sb, sizeof(G));
+    const long long units = a.batch * ((a.channels + kRecurWide - 1) / kRecurWide);
+    const unsigned grid = (unsigned)((units + 3) / 4);
+    if (vec) recur_step_kernel<T, G, true, GATED><<<grid, 128, 0, st>>>(a);
+    else recur_step_kernel<T, G, false, GATED><<<grid, 128, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  RecurMaps maps{};
+  const RecurStride own{a.tokens * a.channels, a.channels};
+  const bool grad = what == 1;
+  const int tokens = grad ? RecurBackward<T, G, GATED>::kTokens : RecurForward<T, G, GATED>::kTokens;
+  bool vec = quads<T>(a.y) && recur_map<G>(&maps.g, a.g, a.sg, a, tokens);
+  if (GATED) vec = vec && recur_map<G>(&maps.b, a.beta, a.sb, a, tokens);
+  if (GATED || !grad) vec = vec && recur_map<T>(&maps.x, a.x, a.sx, a, tokens);
+  if (grad)
+    vec = vec && quads<T>(a.dx) && quads<G>(a.dg) && quads<G>(a.dbeta) &&
+          recur_map<T>(&maps.d, a.dy, own, a, tokens) && recur_map<T>(&maps.y, a.y, own, a, tokens);
+  return vec ? recur_whole<T, G, true, GATED>(grad, a, maps, st)
+             : recur_whole<T, G, false, GATED>(grad, a, maps, st);
 }
 template <typename T, typename G> cudaError_t recur_t(int what, const RecurArgs &a, cudaStream_t st) {
-  if (vec_recur<T, G>(a))
-    return a.beta ? recur_kind<T, G, true, true>(what, a, st)
-                  : recur_kind<T, G, true, false>(what, a, st);
-  return a.beta ? recur_kind<T, G, false, true>(what, a, st)
-                : recur_kind<T, G, false, false>(what, a, st);
+  return a.beta ? recur_kind<T, G, true>(what, a, st) : recur_kind<T, G, false>(what, a, st);
 }
 template <typename T> cudaError_t recur_of(int what, const RecurArgs &a, bool gfloat, cudaStream_t st) {
   if constexpr (sizeof(T) == 2)
