@@ -5,7 +5,7 @@
 //
 // The gradient adds in one order whatever the timing: the tokens are sorted by
 // row, equal rows in the order of the tokens (embed_sort_kernel), cut into
-// pieces of 32 whatever the runs of equal rows are -- text has a few rows with
+// pieces of 16 whatever the runs of equal rows are -- text has a few rows with
 // a tenth of all tokens -- and summed piece by piece (embed_sum_kernel); runs
 // that cross pieces leave one partial row per piece, which embed_join_kernel
 // adds in the order of the pieces.
@@ -85,8 +85,9 @@ embed_sort_kernel(const EmbedSortArgs a) {
     if (head > a.fill_bytes) head = a.fill_bytes;
     const long long words = (a.fill_bytes - head) >> 4, done = head + (words << 4);
     for (long long i = 2 * at; i < head; i += 2 * threads) *reinterpret_cast<uint16_t *>(p + i) = 0;
+#pragma unroll 4
     for (long long i = at; i < words; i += threads)
-      reinterpret_cast<uint4 *>(p + head)[i] = make_uint4(0, 0, 0, 0);
+      __stcs(reinterpret_cast<uint4 *>(p + head) + i, make_uint4(0, 0, 0, 0));
     for (long long i = done + 2 * at; i < a.fill_bytes; i += 2 * threads)
       *reinterpret_cast<uint16_t *>(p + i) = 0;
     return;
@@ -178,76 +179,114 @@ embed_sort_kernel(const EmbedSortArgs a) {
 
 // ---- sums ------------------------------------------------------------------------
 
-constexpr int kPiece = 32;  // tokens: a lane each for their rows and places
+constexpr int kPiece = 16;  // tokens, whose rows are all loaded at once
 
 // The columns of a warp: `E` per lane, whole 16 bytes or 32 apart.
 template <typename T, bool VEC> struct Columns {
   using A = typename Acc<T>::type;
   static constexpr int E = VEC ? 16 / (int)sizeof(T) : 4;
   static constexpr int kWide = 32 * E;
+  // A lane's part of a row as it lies there.
+  struct alignas(VEC ? 16 : sizeof(T)) Raw {
+    T v[E];
+  };
   static __device__ __forceinline__ int at(int chunk, int lane, int i) {
     return chunk * kWide + (VEC ? lane * E + i : lane + 32 * i);
   }
-  static __device__ __forceinline__ void load(const T *row, int chunk, int lane, int dim, A (&f)[E]) {
+  static __device__ __forceinline__ Raw load(const T *row, int chunk, int lane, int dim) {
+    Raw r;
     if constexpr (VEC) {
       const int c = at(chunk, lane, 0);
       uint4 w = make_uint4(0, 0, 0, 0);
-      if (c < dim) w = __ldg(reinterpret_cast<const uint4 *>(row + c));
-      unpack<T>(w, f);
+      if (c < dim) w = *reinterpret_cast<const uint4 *>(row + c);
+      *reinterpret_cast<uint4 *>(&r) = w;
     } else {
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         const int c = at(chunk, lane, i);
-        f[i] = c < dim ? to_acc(row[c]) : (A)0;
+        r.v[i] = c < dim ? row[c] : from_acc<T>((A)0);
+      }
+    }
+    return r;
+  }
+  static __device__ __forceinline__ void widen(const Raw &r, A (&f)[E]) {
+    if constexpr (VEC) {
+      unpack<T>(*reinterpret_cast<const uint4 *>(&r), f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) f[i] = to_acc(r.v[i]);
+    }
+  }
+};
+
+// A lane's part of a row of the table's gradient, of type TO (T or float):
+// E columns as Columns<T, VEC> has them.
+template <typename T, typename TO, bool VEC> struct Row {
+  using A = typename Acc<T>::type;
+  using C = Columns<T, VEC>;
+  static constexpr int E = C::E;
+  struct alignas(VEC ? 16 : sizeof(TO)) Raw {
+    TO v[E];
+  };
+  static __device__ __forceinline__ TO *place(const EmbedSumArgs &a, unsigned row) {
+    return static_cast<TO *>(a.dtable) + (long long)row * a.dim;
+  }
+  static __device__ __forceinline__ Raw load(const EmbedSumArgs &a, unsigned row, int chunk, int lane) {
+    const TO *src = place(a, row);
+    Raw r;
+#pragma unroll
+    for (int i = 0; i < E; ++i) r.v[i] = from_acc<TO>((A)0);
+    if constexpr (VEC) {
+      const int c = C::at(chunk, lane, 0);
+      if (c < a.dim) {
+#pragma unroll
+        for (int j = 0; j < E * (int)sizeof(TO) / 16; ++j)
+          reinterpret_cast<uint4 *>(&r)[j] = reinterpret_cast<const uint4 *>(src + c)[j];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int c = C::at(chunk, lane, i);
+        if (c < a.dim) r.v[i] = src[c];
+      }
+    }
+    return r;
+  }
+  // scale f (+ old)
+  static __device__ __forceinline__ void store(const EmbedSumArgs &a, unsigned row, int chunk, int lane,
+                                               const A (&f)[E], const Raw *old) {
+    const A scale = (A)a.scale;
+    TO *dst = place(a, row);
+    Raw r;
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      r.v[i] = from_acc<TO>(old ? f[i] * scale + (A)to_acc(old->v[i]) : f[i] * scale);
+    if constexpr (VEC) {
+      const int c = C::at(chunk, lane, 0);
+      if (c < a.dim) {
+#pragma unroll
+        for (int j = 0; j < E * (int)sizeof(TO) / 16; ++j)
+          reinterpret_cast<uint4 *>(dst + c)[j] = reinterpret_cast<const uint4 *>(&r)[j];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int c = C::at(chunk, lane, i);
+        if (c < a.dim) dst[c] = r.v[i];
       }
     }
   }
 };
 
-// Writes a row of the table's gradient, of type TO (T or float).
-template <typename T, typename TO, bool VEC, int E>
-__device__ __forceinline__ void put_row(const EmbedSumArgs &a, unsigned row, int chunk, int lane,
-                                        const typename Acc<T>::type (&f)[E]) {
-  using A = typename Acc<T>::type;
-  using C = Columns<T, VEC>;
-  TO *dst = static_cast<TO *>(a.dtable) + (long long)row * a.dim;
-  const A scale = (A)a.scale;
-  if constexpr (VEC) {
-    const int c = C::at(chunk, lane, 0);
-    if (c >= a.dim) return;
-    constexpr int P = 16 / (int)sizeof(TO);
-#pragma unroll
-    for (int j = 0; j < E / P; ++j) {
-      A v[P];
-#pragma unroll
-      for (int i = 0; i < P; ++i) v[i] = f[j * P + i] * scale;
-      uint4 *p = reinterpret_cast<uint4 *>(dst + c) + j;
-      if (a.add) {
-        A old[P];
-        unpack<TO>(*p, old);
-#pragma unroll
-        for (int i = 0; i < P; ++i) v[i] += old[i];
-      }
-      *p = pack<TO>(v);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int c = C::at(chunk, lane, i);
-      if (c < a.dim) {
-        const A v = f[i] * scale;
-        dst[c] = from_acc<TO>(a.add ? v + (A)to_acc(dst[c]) : v);
-      }
-    }
-  }
-}
-
-// One warp per piece of the sorted tokens and chunk of columns.
-template <typename T, typename TO, bool VEC>
+// One warp per piece of the sorted tokens and chunk of columns.  ADD: rows that
+// end in the piece are loaded ahead too (half the piece at a time, for the
+// registers): one after the other their latency was three quarters of the time.
+template <typename T, typename TO, bool VEC, bool ADD>
 __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedSumArgs a) {
   using A = typename Acc<T>::type;
   using C = Columns<T, VEC>;
-  constexpr int E = C::E, U = 8;
+  using R = Row<T, TO, VEC>;
+  constexpr int E = C::E, U = ADD ? kPiece / 2 : kPiece;
   const int lane = threadIdx.x & 31;
   const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int chunks = (a.dim + C::kWide - 1) / C::kWide;
@@ -257,10 +296,12 @@ __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedSumArgs a) {
   if (first >= a.tokens) return;
   const int count = (int)min((long long)kPiece, a.tokens - first);
   const unsigned none = (unsigned)a.rows;
-  const unsigned key = lane < count ? a.key[first + lane] : none;
-  const unsigned pos = lane < count ? a.pos[first + lane] : 0;
-  const unsigned prev = first > 0 ? a.key[first - 1] : none;
-  const unsigned next = first + count < a.tokens ? a.key[first + count] : none;
+  // lanes 0 .. 15: the piece's tokens; 16: the one behind it, 17: the one before it
+  const long long where = lane < 17 ? first + lane : first - 1;
+  const bool here = lane < 18 && where >= 0 && where < a.tokens;
+  const unsigned key = here ? a.key[where] : none;
+  const unsigned pos = here && lane < count ? a.pos[where] : 0;
+  const unsigned prev = __shfl_sync(0xffffffffu, key, 17);
   const T *dy = static_cast<const T *>(a.dy);
   A *partial = static_cast<A *>(a.partial) + piece * 2 * a.ldp;
   A acc[E];
@@ -269,43 +310,47 @@ __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedSumArgs a) {
   unsigned cur = __shfl_sync(0xffffffffu, key, 0);
   if (cur == none) return;  // sorted: nothing but padding from here on
   bool open = cur == prev;  // the run comes from the piece before
-  auto flush = [&](bool goes_on) {
-    if (!open && !goes_on) {
-      put_row<T, TO, VEC, E>(a, cur, chunk, lane, acc);
-    } else {
-      A *to = partial + (open ? 0 : a.ldp);
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int c = C::at(chunk, lane, i);
-        if (c < a.dim) to[c] = acc[i];
-      }
-    }
-  };
-  for (int j0 = 0; j0 < count; j0 += U) {
-    A f[U][E];
+  for (int j0 = 0; j0 < kPiece; j0 += U) {
+    typename C::Raw f[U];
+    typename R::Raw old[ADD ? U : 1];
+    // the lanes hold `none` behind the last token
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = min(j0 + u, kPiece - 1);
-      const unsigned k = __shfl_sync(0xffffffffu, key, j), p = __shfl_sync(0xffffffffu, pos, j);
-      const int dim = k == none || j0 + u >= count ? 0 : a.dim;
-      C::load(dy + (long long)p * a.lddy, chunk, lane, dim, f[u]);
+      const unsigned k = __shfl_sync(0xffffffffu, key, j0 + u);
+      const unsigned p = __shfl_sync(0xffffffffu, pos, j0 + u);
+      const bool live = k != none && j0 + u < count;
+      f[u] = C::load(dy + (long long)p * a.lddy, chunk, lane, live ? a.dim : 0);
+      if constexpr (ADD)
+        if (live && k != __shfl_sync(0xffffffffu, key, j0 + u + 1))
+          old[u] = R::load(a, k, chunk, lane);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const unsigned k = j0 + u < count ? __shfl_sync(0xffffffffu, key, j0 + u) : cur;
-      if (k != cur) {
-        flush(false);
-        if (k == none) return;
-        cur = k;
-        open = false;
+      const unsigned k = __shfl_sync(0xffffffffu, key, j0 + u);
+      if (k == none || j0 + u >= count) return;  // runs have been written where they end
+      A v[E];
+      C::widen(f[u], v);
 #pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = 0;
+      for (int i = 0; i < E; ++i) acc[i] += v[i];
+      const unsigned next = __shfl_sync(0xffffffffu, key, j0 + u + 1);
+      const bool ends = next != k;
+      if (!ends && j0 + u + 1 < kPiece) continue;
+      if (ends && !open) {
+        R::store(a, k, chunk, lane, acc, ADD ? &old[ADD ? u : 0] : nullptr);
+      } else {
+        A *to = partial + (open ? 0 : a.ldp);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const int c = C::at(chunk, lane, i);
+          if (c < a.dim) to[c] = acc[i];
+        }
       }
+      open = false;
 #pragma unroll
-      for (int i = 0; i < E; ++i) acc[i] += f[u][i];
+      for (int i = 0; i < E; ++i) acc[i] = 0;
     }
   }
-  flush(cur == next);
 }
 
 // The runs that go on behind a piece: its own part, then the heads of the
@@ -314,27 +359,31 @@ template <typename T, typename TO, bool VEC>
 __global__ void __launch_bounds__(128) embed_join_kernel(const EmbedSumArgs a) {
   using A = typename Acc<T>::type;
   using C = Columns<T, VEC>;
+  using R = Row<T, TO, VEC>;
   constexpr int E = C::E, U = 8;
   const int lane = threadIdx.x & 31;
   const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int chunks = (a.dim + C::kWide - 1) / C::kWide;
   const long long piece = item / chunks;
   const int chunk = (int)(item - piece * chunks);
-  const long long behind = (piece + 1) * kPiece;
+  const long long first = piece * kPiece, behind = first + kPiece;
   if (behind >= a.tokens) return;
-  const unsigned row = a.key[behind - 1];
-  if (row == (unsigned)a.rows || a.key[behind] != row) return;
-  const long long first = piece * kPiece;
-  if (first > 0 && a.key[first] == row && a.key[first - 1] == row) return;  // began further ahead
-  long long lo = behind, hi = a.tokens;  // the last token of the row is before hi
-  while (hi - lo > 1) {
-    const long long mid = lo + (hi - lo) / 2;
-    if (a.key[mid] == row) lo = mid;
-    else hi = mid;
+  const unsigned row = a.key[behind - 1], next = a.key[behind];
+  const unsigned front = a.key[first], prev = first > 0 ? a.key[first - 1] : (unsigned)a.rows;
+  if (row == (unsigned)a.rows || next != row) return;
+  if (front == row && prev == row) return;  // began further ahead
+  long long last = piece + 1;  // the piece where the run ends: it goes on where the next begins with it
+  for (;;) {
+    const long long at = (last + 1 + lane) * kPiece;
+    const unsigned on = __ballot_sync(0xffffffffu, at < a.tokens && a.key[at] == row);
+    const int more = __ffs(~on) - 1;
+    last += more < 0 ? 32 : more;
+    if (more >= 0) break;
   }
-  const long long last = lo / kPiece;
   const A *partial = static_cast<const A *>(a.partial);
   A acc[E];
+  typename R::Raw old;
+  if (a.add) old = R::load(a, row, chunk, lane);
 #pragma unroll
   for (int i = 0; i < E; ++i) {
     const int c = C::at(chunk, lane, i);
@@ -354,7 +403,7 @@ __global__ void __launch_bounds__(128) embed_join_kernel(const EmbedSumArgs a) {
 #pragma unroll
       for (int i = 0; i < E; ++i) acc[i] += f[u][i];
   }
-  put_row<T, TO, VEC, E>(a, row, chunk, lane, acc);
+  R::store(a, row, chunk, lane, acc, a.add ? &old : nullptr);
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -381,7 +430,8 @@ cudaError_t sums_t(const EmbedSumArgs &a, cudaStream_t st) {
   const long long pieces = (a.tokens + kPiece - 1) / kPiece;
   const long long blocks = (pieces * chunks + 3) / 4;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  embed_sum_kernel<T, TO, VEC><<<(unsigned)blocks, 128, 0, st>>>(a);
+  if (a.add) embed_sum_kernel<T, TO, VEC, true><<<(unsigned)blocks, 128, 0, st>>>(a);
+  else embed_sum_kernel<T, TO, VEC, false><<<(unsigned)blocks, 128, 0, st>>>(a);
   if (pieces > 1) embed_join_kernel<T, TO, VEC><<<(unsigned)blocks, 128, 0, st>>>(a);
   return cudaGetLastError();
 }

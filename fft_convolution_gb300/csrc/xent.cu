@@ -49,11 +49,11 @@ struct LiveRows {
   const float *dloss;
 };
 // Rows of ld elements as `PARTS` arrays of rows of ldo, whole 16 bytes; rows
-// that do not count are 0.
+// that do not count are 0.  A thread makes eight elements at a time.
 template <typename T, typename O, int PARTS>
 __global__ void __launch_bounds__(256) xent_lay_kernel(const T *in, long long ld, long long rows,
-                                                       int dim, O *out, int ldo, LiveRows live) {
-  const int tx = threadIdx.x;
+                                                       int dim, O *out, int ldo, bool vec,
+                                                       LiveRows live) {
   for (long long r = (long long)blockIdx.x * blockDim.y + threadIdx.y; r < rows;
        r += (long long)gridDim.x * blockDim.y) {
     int wide = dim;
@@ -61,16 +61,31 @@ __global__ void __launch_bounds__(256) xent_lay_kernel(const T *in, long long ld
       const long long t = target_of(live.targets, live.target_bytes, r);
       if (t < 0 || t >= live.vocabulary || live.dloss[r] == 0.0f) wide = 0;
     }
-    for (int c = tx; c < ldo; c += blockDim.x) {
+#pragma unroll 4
+    for (int c = 8 * threadIdx.x; c < ldo; c += 8 * blockDim.x) {
+      const T *src = in + r * ld + c;
+      O *dst = out + r * ldo + c;
       if constexpr (PARTS == 1) {
-        out[r * ldo + c] = c < wide ? in[r * ld + c] : from_acc<O>(0.0f);
+        alignas(16) T v[8];
+        if (vec && c + 8 <= wide) {
+          *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(src);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = c + i < wide ? src[i] : from_acc<T>(0.0f);
+        }
+        *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(v);
       } else {
-        float v = c < wide ? in[r * ld + c] : 0.0f;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < wide ? src[i] : 0.0f;
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
-          const O h = from_acc<O>(v);
-          out[((long long)p * rows + r) * ldo + c] = h;
-          v = isfinite(to_acc(h)) ? v - to_acc(h) : 0.0f;
+          *reinterpret_cast<uint4 *>(dst + (long long)p * rows * ldo) = pack<O>(v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float h = to_acc(from_acc<O>(v[i]));
+            v[i] = isfinite(h) ? v[i] - h : 0.0f;
+          }
         }
       }
     }
@@ -160,26 +175,46 @@ xent_sums_kernel(const __grid_constant__ PairOperands ops, const XentTiles p, in
   pair_run(&ops, p.m * p.n, status, of, out);
 }
 
-// lse and loss from the parts of a token: a warp per 32 tokens and every eighth part.
-__global__ void __launch_bounds__(256) xent_join_kernel(const XentTiles p, float *loss, float *lse) {
-  __shared__ float2 parts[8][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long n = (long long)blockIdx.x * 32 + lane;
+// (m, s) + (m', s'): the sums in units of the larger power of two.
+__device__ __forceinline__ float2 join_sums(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  const float sa = a.x == m ? a.y : a.y * exp2f(a.x - m), sb = b.x == m ? b.y : b.y * exp2f(b.x - m);
+  return make_float2(m, sa + sb);
+}
+// lse and loss from the parts of a token: blocks of 8 tokens, a thread for every
+// 128th part of one (with 32 tokens and every eighth part, 48 tokens of 512 parts took
+// 16 us).
+constexpr int kJoinTokens = 8, kJoinParts = 128;
+__global__ void __launch_bounds__(kJoinTokens * kJoinParts)
+xent_join_kernel(const XentTiles p, float *loss, float *lse) {
+  __shared__ float2 parts[kJoinTokens * kJoinParts / 32][kJoinTokens];
+  const int at = threadIdx.x % kJoinTokens, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long n = (long long)blockIdx.x * kJoinTokens + at;
   const int count = (int)((p.vocabulary + 127) >> 7);
   float2 s = make_float2(-INFINITY, 0.0f);
-  // (m, s) + (m', s'): the sums in units of the larger power
-  auto join = [](float2 a, float2 b) {
-    const float m = fmaxf(a.x, b.x);
-    const float sa = a.x == m ? a.y : a.y * exp2f(a.x - m), sb = b.x == m ? b.y : b.y * exp2f(b.x - m);
-    return make_float2(m, sa + sb);
-  };
-  if (n < p.tokens)
-    for (int i = warp; i < count; i += 8) s = join(s, p.partial[(long long)i * p.tokens + n]);
-  parts[warp][lane] = s;
-  __syncthreads();
-  if (warp != 0 || n >= p.tokens) return;
+  if (n < p.tokens) {
+#pragma unroll 4
+    for (int i = threadIdx.x / kJoinTokens; i < count; i += kJoinParts)
+      s = join_sums(s, p.partial[(long long)i * p.tokens + n]);
+  }
 #pragma unroll
-  for (int w = 1; w < 8; ++w) s = join(s, parts[w][lane]);
+  for (int o = kJoinTokens; o < 32; o *= 2) {
+    const float2 b = make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o));
+    s = (lane & o) == 0 ? join_sums(s, b) : join_sums(b, s);
+  }
+  if (lane < kJoinTokens) parts[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0) return;
+  // 32 warps' parts of 8 tokens: four lanes a token, then one
+  s = parts[lane / kJoinTokens * 8][at];
+#pragma unroll
+  for (int w = 1; w < 8; ++w) s = join_sums(s, parts[lane / kJoinTokens * 8 + w][at]);
+#pragma unroll
+  for (int o = kJoinTokens; o < 32; o *= 2) {
+    const float2 b = make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o));
+    s = (lane & o) == 0 ? join_sums(s, b) : join_sums(b, s);
+  }
+  if (lane >= kJoinTokens || n >= p.tokens) return;
   const float total = (s.x + log2f(s.y)) * kLn2;
   const long long target = target_of(p.targets, p.target_bytes, n);
   lse[n] = total;
@@ -520,16 +555,18 @@ struct Layout {
 template <typename T>
 cudaError_t lay(const void *in, long long ld, long long rows, int dim, const Operand &o, void *out,
                 const LiveRows &live, cudaStream_t st) {
-  const dim3 block(64, 4);
-  const long long need = (rows + 3) / 4, most = (long long)sm_count() * 16;
+  const int tx = o.ld >= 512 ? 64 : 16;
+  const dim3 block(tx, 256 / tx);
+  const bool vec = ((uintptr_t)in & 15) == 0 && ld % 8 == 0;
+  const long long need = up(rows, 256 / tx), most = (long long)sm_count() * 16;
   const unsigned grid = (unsigned)(need < most ? need : most);
   if constexpr (sizeof(T) == 4)
     xent_lay_kernel<float, __nv_bfloat16, 3><<<grid, block, 0, st>>>(
         static_cast<const float *>(in), ld, rows, dim, static_cast<__nv_bfloat16 *>(out), (int)o.ld,
-        live);
+        false, live);
   else
     xent_lay_kernel<T, T, 1><<<grid, block, 0, st>>>(static_cast<const T *>(in), ld, rows, dim,
-                                                     static_cast<T *>(out), (int)o.ld, live);
+                                                     static_cast<T *>(out), (int)o.ld, vec, live);
   return cudaGetLastError();
 }
 
@@ -608,7 +645,8 @@ cudaError_t xent_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st) {
   e = pair_launch(xent_sums_kernel, once, (long long)t.m * t.n, st, ops, t, (int)up(a.dim, kPairK),
                   status);
   if (e != cudaSuccess) return e;
-  xent_join_kernel<<<(unsigned)up(a.tokens, 32), 256, 0, st>>>(t, a.loss, a.lse);
+  xent_join_kernel<<<(unsigned)up(a.tokens, kJoinTokens), kJoinTokens * kJoinParts, 0, st>>>(t, a.loss,
+                                                                                       a.lse);
   return cudaGetLastError();
 }
 
