@@ -97,6 +97,7 @@ embed_sort_kernel(const EmbedSortArgs a) {
   const long long begin = min(share * rank, a.tokens), end = min(begin + share, a.tokens);
   const unsigned mask = (1u << a.bits) - 1;
   for (int d = tid; d < kDigits * (kSortThreads / 32); d += kSortThreads) (&s.count[0][0])[d] = 0;
+  const int digits = 1 << a.bits;
 
   for (int pass = 0; pass < a.passes; ++pass) {
     const unsigned *key = a.key[pass & 1], *pos = a.pos[pass & 1];
@@ -110,9 +111,10 @@ embed_sort_kernel(const EmbedSortArgs a) {
     for (int d = tid; d < kDigits; d += kSortThreads) s.hist[d] = 0;
     __syncthreads();
     // whole warps: equal digits of a warp are added at once
+    const unsigned first = begin + tid < end ? key_of(begin + tid) : 0;
     for (long long i0 = begin; i0 < end; i0 += kSortThreads) {
       const long long i = i0 + tid;
-      const unsigned d = i < end ? (key_of(i) >> shift) & mask : ~0u;
+      const unsigned d = i < end ? ((i0 == begin ? first : key_of(i)) >> shift) & mask : ~0u;
       const unsigned same = __match_any_sync(0xffffffffu, d);
       if (i < end && (same & ((1u << lane) - 1)) == 0) atomicAdd(&s.hist[d], (unsigned)__popc(same));
     }
@@ -146,19 +148,21 @@ embed_sort_kernel(const EmbedSortArgs a) {
     for (long long i0 = begin; i0 < end; i0 += kSortThreads) {
       const long long i = i0 + tid;
       const bool on = i < end;
-      const unsigned k = on ? key_of(i) : 0, p = on ? (pass > 0 ? __ldcg(pos + i) : (unsigned)i) : 0;
+      const unsigned k = i0 == begin ? first : on ? key_of(i) : 0;
+      const unsigned p = on ? (pass > 0 ? __ldcg(pos + i) : (unsigned)i) : 0;
       const unsigned d = on ? (k >> shift) & mask : ~0u;
       const unsigned same = __match_any_sync(0xffffffffu, d);
       const int ahead = __popc(same & ((1u << lane) - 1));
       if (on && ahead == 0) s.count[warp][d] = (unsigned)__popc(same);
       __syncthreads();
-      if (tid < kDigits) {
-        unsigned run = s.base[tid];
-#pragma unroll 8
+      if (tid < digits) {
+        unsigned n[kSortThreads / 32], run = s.base[tid];
+#pragma unroll
+        for (int w = 0; w < kSortThreads / 32; ++w) n[w] = s.count[w][tid];
+#pragma unroll
         for (int w = 0; w < kSortThreads / 32; ++w) {
-          const unsigned n = s.count[w][tid];
-          s.count[w][tid] = run;
-          run += n;
+          if (n[w] != 0) s.count[w][tid] = run;
+          run += n[w];
         }
         s.base[tid] = run;
       }
@@ -168,9 +172,8 @@ embed_sort_kernel(const EmbedSortArgs a) {
         key2[to] = k;
         pos2[to] = p;
       }
-      __syncthreads();
-      for (int e = tid; e < kDigits * (kSortThreads / 32); e += kSortThreads) (&s.count[0][0])[e] = 0;
-      __syncthreads();
+      __syncwarp();
+      if (on && ahead == 0) s.count[warp][d] = 0;  // the next tile's counters, of this warp alone
     }
     __threadfence();
     cluster_sync();  // the next pass reads what every block has written; counters are free
@@ -354,18 +357,19 @@ __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedSumArgs a) {
 }
 
 // The runs that go on behind a piece: its own part, then the heads of the
-// pieces behind it.
+// pieces behind it, a quarter of them to each warp of the block (the most frequent
+// row of a text crosses dozens; one warp for all of them took 17 us for 16384 tokens).
 template <typename T, typename TO, bool VEC>
 __global__ void __launch_bounds__(128) embed_join_kernel(const EmbedSumArgs a) {
   using A = typename Acc<T>::type;
   using C = Columns<T, VEC>;
   using R = Row<T, TO, VEC>;
   constexpr int E = C::E, U = 8;
-  const int lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  __shared__ A parts[3][E][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunks = (a.dim + C::kWide - 1) / C::kWide;
-  const long long piece = item / chunks;
-  const int chunk = (int)(item - piece * chunks);
+  const long long piece = blockIdx.x / chunks;
+  const int chunk = (int)(blockIdx.x - piece * chunks);
   const long long first = piece * kPiece, behind = first + kPiece;
   if (behind >= a.tokens) return;
   const unsigned row = a.key[behind - 1], next = a.key[behind];
@@ -383,26 +387,38 @@ __global__ void __launch_bounds__(128) embed_join_kernel(const EmbedSumArgs a) {
   const A *partial = static_cast<const A *>(a.partial);
   A acc[E];
   typename R::Raw old;
-  if (a.add) old = R::load(a, row, chunk, lane);
+  if (a.add && warp == 0) old = R::load(a, row, chunk, lane);
+  // part 0 is the piece's own tail
+  const long long count = last - piece + 1, share = (count + 3) / 4;
+  const long long from = share * warp, to = min(from + share, count);
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int c = C::at(chunk, lane, i);
-    acc[i] = c < a.dim ? partial[(piece * 2 + 1) * a.ldp + c] : (A)0;
-  }
-  for (long long q = piece + 1; q <= last; q += U) {
+  for (int i = 0; i < E; ++i) acc[i] = 0;
+  for (long long q = from; q < to; q += U) {
     A f[U][E];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      const A *p = partial + ((piece + q + u) * 2 + (q + u == 0 ? 1 : 0)) * a.ldp;
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         const int c = C::at(chunk, lane, i);
-        f[u][i] = q + u <= last && c < a.dim ? partial[(q + u) * 2 * a.ldp + c] : (A)0;
+        f[u][i] = q + u < to && c < a.dim ? p[c] : (A)0;
       }
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int i = 0; i < E; ++i) acc[i] += f[u][i];
   }
+  if (warp > 0) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) parts[warp - 1][i][lane] = acc[i];
+  }
+  __syncthreads();
+  if (warp > 0) return;
+#pragma unroll
+  for (int w = 0; w < 3; ++w)
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[i] += parts[w][i][lane];
   R::store(a, row, chunk, lane, acc, a.add ? &old : nullptr);
 }
 
@@ -429,10 +445,10 @@ cudaError_t sums_t(const EmbedSumArgs &a, cudaStream_t st) {
   const long long chunks = (a.dim + Columns<T, VEC>::kWide - 1) / Columns<T, VEC>::kWide;
   const long long pieces = (a.tokens + kPiece - 1) / kPiece;
   const long long blocks = (pieces * chunks + 3) / 4;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if (pieces * chunks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   if (a.add) embed_sum_kernel<T, TO, VEC, true><<<(unsigned)blocks, 128, 0, st>>>(a);
   else embed_sum_kernel<T, TO, VEC, false><<<(unsigned)blocks, 128, 0, st>>>(a);
-  if (pieces > 1) embed_join_kernel<T, TO, VEC><<<(unsigned)blocks, 128, 0, st>>>(a);
+  if (pieces > 1) embed_join_kernel<T, TO, VEC><<<(unsigned)(pieces * chunks), 128, 0, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -3,10 +3,11 @@
 // cross entropy fill with their own order of tiles and their own use of a
 // finished tile.
 //
-// A cluster of two blocks works on one tile of 256 x 256: each block stages
-// 128 rows of A and 128 of B per 64 summed indexes (32 KB; six stages), and
-// gets the tile's 128 upper or lower rows as fp32 in its tensor memory, where
-// two tiles fit: one is summed while the other is read out.  The pair is what
+// A cluster of two blocks works on one tile of 256 x 256 (or fewer columns, where
+// that fills the GPU better): each block stages 128 rows of A and half of B's
+// per 64 summed indexes (32 KB; six stages), and gets the tile's 128 upper or lower
+// rows as fp32 in its tensor memory, where two tiles fit: one is summed while the
+// other is read out.  The pair is what
 // lets the tensor cores run: a block alone would have to load twice the bytes
 // of B per product (96 bytes per clock and SM at the full rate, which the L2
 // does not deliver to all SMs at once; so it is 64).
@@ -86,6 +87,8 @@ struct PairTile {
 struct PairOperands {
   CUtensorMap a, b;
   int a_mn, b_mn;
+  int width;  // columns of a tile: a multiple of 64 up to 256
+  uint32_t b_bytes;  // of B per block and stage, as the boxes of its map bring them
   uint32_t idesc;
   // Products of parts: an fp32 operand is the sum of three bf16 parts, of
   // which the six largest products are taken, the smallest first.
@@ -106,8 +109,8 @@ struct PairShared {
 
 // Runs the tiles pair, pair + pairs, ... < tiles.  of(t, &which) gives a tile
 // and which of the problems `ops` it belongs to; out(t, address of this
-// warp's lanes in TMEM) uses one, in warps 4 .. 11: warp w has lanes
-// 32 (w % 4) .. and columns 128 ((w - 4) / 4) .. of the tile's half.
+// warp's lanes in TMEM, at the tile's first column) uses one, in warps 4 .. 11: warp w has lanes
+// 32 (w % 4) .. and the first (w < 8) or last half of the tile's columns.
 template <class Of, class Out>
 __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int *status, Of of,
                                          Out out) {
@@ -146,7 +149,7 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
         int which = 0;
         const PairTile w = of(t, which);
         const PairOperands &p = ops[which];
-        const int a_row = w.a_row + (int)rank * 128, b_row = w.b_row + (int)rank * 128;
+        const int a_row = w.a_row + (int)rank * 128, b_row = w.b_row + (int)rank * (p.width / 2);
         const int nq = part_pairs(p.parts);
         for (int q = 0; ok && q < nq; ++q) {
           int pa, pb;
@@ -157,7 +160,7 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
               ok = false;
               break;
             }
-            if (rank == 0) bar_arrive_tx(&sh.full[s], 4 * kStageHalf);
+            if (rank == 0) bar_arrive_tx(&sh.full[s], 2 * (kStageHalf + p.b_bytes));
             const uint32_t bar = peer(smem_u32(&sh.full[s]), 0);
             const uint32_t sa = stage0 + s * 2 * kStageHalf, sb = sa + kStageHalf;
             const int k = kb * kPairK;
@@ -169,7 +172,8 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
             }
             if (p.b_mn) {
               pair_load(sb, &p.b, bar, b_row, w.b_base + k, pb);
-              pair_load(sb + kStageHalf / 2, &p.b, bar, b_row + 64, w.b_base + k, pb);
+              if (p.width > 128)
+                pair_load(sb + kStageHalf / 2, &p.b, bar, b_row + 64, w.b_base + k, pb);
             } else {
               pair_load(sb, &p.b, bar, k, b_row, pb);
             }
@@ -218,7 +222,7 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
     }
   } else if (warp >= 4) {
     int n = 0;
-    const uint32_t base = tm + ((uint32_t)(warp & 3) << 21) + (uint32_t)((warp - 4) >> 2) * 128;
+    const uint32_t base = tm + ((uint32_t)(warp & 3) << 21);
     for (int t = pair; t < tiles; t += pairs, ++n) {
       const int acc = n & 1;
       if (!wait_cluster(&sh.ready[acc], (n >> 1) & 1, failed, status)) break;

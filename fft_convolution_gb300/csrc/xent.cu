@@ -99,7 +99,8 @@ struct XentTiles {
   int m, n;  // tiles of tokens and of words
   const void *targets;
   int target_bytes;
-  // forward: per 128 words and token, largest logit and sum (both in powers of 2)
+  int width;  // words of a tile
+  // forward: per half a tile's words and token, largest logit and sum (both in powers of 2)
   float2 *partial;
   float *at_target;
   // gradient: a piece of the words from v0 on
@@ -124,7 +125,7 @@ __device__ __forceinline__ void read32(uint32_t addr, float (&f)[32]) {
 __device__ __forceinline__ PairTile word_tile(const XentTiles &p, int t, long long v0, int k) {
   PairTile w{};
   w.a_row = (t % p.m) * kPairTile;
-  w.b_row = (int)v0 + (t / p.m) * kPairTile;
+  w.b_row = (int)v0 + (t / p.m) * p.width;
   w.k0 = 0;
   w.k1 = k;
   return w;
@@ -139,9 +140,11 @@ xent_sums_kernel(const __grid_constant__ PairOperands ops, const XentTiles p, in
   auto out = [&](int t, uint32_t tm) {
     const PairTile w = word_tile(p, t, 0, kblocks);
     const long long n = w.a_row + rank * 128 + (warp & 3) * 32 + lane;
-    const long long v0 = w.b_row + half * 128;
+    const int wide = p.width / 2;
+    const long long v0 = w.b_row + half * wide;
+    tm += half * wide;
     if (v0 >= p.vocabulary) return;
-    const int count = (int)min((long long)128, p.vocabulary - v0);
+    const int count = (int)min((long long)wide, p.vocabulary - v0);
     const long long target = n < p.tokens ? target_of(p.targets, p.target_bytes, n) - v0 : -1;
     const bool mine = target >= 0 && target < count;
     float top = -INFINITY;
@@ -170,7 +173,7 @@ xent_sums_kernel(const __grid_constant__ PairOperands ops, const XentTiles p, in
         if (mine && target >= c && target < c + 32) p.at_target[n] = at;
       }
     }
-    if (n < p.tokens) p.partial[(v0 >> 7) * p.tokens + n] = make_float2(sum == 0.0f ? top : unit, sum);
+    if (n < p.tokens) p.partial[(2ll * (t / p.m) + half) * p.tokens + n] = make_float2(sum == 0.0f ? top : unit, sum);
   };
   pair_run(&ops, p.m * p.n, status, of, out);
 }
@@ -190,7 +193,7 @@ xent_join_kernel(const XentTiles p, float *loss, float *lse) {
   __shared__ float2 parts[kJoinTokens * kJoinParts / 32][kJoinTokens];
   const int at = threadIdx.x % kJoinTokens, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long n = (long long)blockIdx.x * kJoinTokens + at;
-  const int count = (int)((p.vocabulary + 127) >> 7);
+  const int count = (int)((p.vocabulary + p.width / 2 - 1) / (p.width / 2));
   float2 s = make_float2(-INFINITY, 0.0f);
   if (n < p.tokens) {
 #pragma unroll 4
@@ -278,7 +281,9 @@ xent_grad_kernel(const __grid_constant__ PairOperands ops, const XentTiles p, in
   auto out = [&](int t, uint32_t tm) {
     const PairTile w = word_tile(p, t, p.v0, kblocks);
     const long long n = w.a_row + rank * 128 + (warp & 3) * 32 + lane;
-    const long long v = w.b_row + half * 128;
+    const int wide = p.width / 2;
+    const long long v = w.b_row + half * wide;
+    tm += half * wide;
     float c = 0.0f, lse = 0.0f;
     long long target = -1;
     if (n < p.tokens) {
@@ -290,10 +295,10 @@ xent_grad_kernel(const __grid_constant__ PairOperands ops, const XentTiles p, in
     }
     const bool live = c != 0.0f;  // NaN is live
     O *row = static_cast<O *>(p.g) + n * p.ldg + (v - p.v0);
-    const int at = target >= v && target < v + 128 ? (int)(target - v) : -1;
-    const int count = (int)max(0ll, min((long long)128, p.vocabulary - v));
+    const int at = target >= v && target < v + wide ? (int)(target - v) : -1;
+    const int count = (int)max(0ll, min((long long)wide, p.vocabulary - v));
 #pragma unroll 1
-    for (int j = 0; j < 128; j += 32) {
+    for (int j = 0; j < wide; j += 32) {
       float f[32];
       read32(tm + j, f);
 #pragma unroll
@@ -311,8 +316,10 @@ xent_grad_kernel(const __grid_constant__ PairOperands ops, const XentTiles p, in
 // longer sums of dx first, so that the short ones fill the ends.
 struct XentProducts {
   PairOperands ops[2];
-  long long tokens, vocabulary, v0;
+  long long tokens, v0;
+  long long words;       // of the piece
   int dim;
+  int width;             // columns of a tile
   int m, n, slices, k;   // dx: tiles of tokens and of columns, cuts of the sum, its blocks
   int wm, wk;            // dW: tiles of words, blocks of tokens
   float *sums;           // [slices][tokens][dim]
@@ -353,7 +360,7 @@ xent_products_kernel(const __grid_constant__ XentProducts p, int *status) {
       which = 0;
       const int slice = t / mn, u = t - slice * mn;
       w.a_row = u / p.n * kPairTile;
-      w.b_row = u % p.n * kPairTile;
+      w.b_row = u % p.n * p.width;
       w.b_base = (int)p.v0;
       w.k0 = (int)((long long)p.k * slice / p.slices);
       w.k1 = (int)((long long)p.k * (slice + 1) / p.slices);
@@ -361,7 +368,7 @@ xent_products_kernel(const __grid_constant__ XentProducts p, int *status) {
       which = 1;
       const int u = t - dx_tiles;
       w.a_row = u / p.n * kPairTile;
-      w.b_row = u % p.n * kPairTile;
+      w.b_row = u % p.n * p.width;
       w.k1 = p.wk;
     }
     return w;
@@ -370,10 +377,11 @@ xent_products_kernel(const __grid_constant__ XentProducts p, int *status) {
     int which = 0;
     const PairTile w = of(t, which);
     const long long r = w.a_row + rank * 128 + (warp & 3) * 32 + lane;
-    const int c0 = w.b_row + half * 128;
+    const int wide = p.width / 2, c0 = w.b_row + half * wide;
+    tm += half * wide;
     const float back = p.unit ? p.unit[1] : 1.0f;
 #pragma unroll 1
-    for (int j = 0; j < 128 && c0 + j < p.dim; j += 32) {
+    for (int j = 0; j < wide && c0 + j < p.dim; j += 32) {
       float f[32];
       read32(tm + j, f);
       const int c = c0 + j;
@@ -407,7 +415,7 @@ xent_products_kernel(const __grid_constant__ XentProducts p, int *status) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) f[i] *= back;
         const bool vec = p.dim % (16 / (int)sizeof(T)) == 0 && ((uintptr_t)p.dw & 15) == 0;
-        if (v < p.vocabulary) put_columns<T>(static_cast<T *>(p.dw) + v * p.dim, c, p.dim, vec, f);
+        if (r < p.words) put_columns<T>(static_cast<T *>(p.dw) + v * p.dim, c, p.dim, vec, f);
       }
     }
   };
@@ -484,8 +492,8 @@ bool make_map(CUtensorMap *map, bool half, const void *p, long long rows, long l
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-uint32_t idesc_of(bool half, bool a_mn, bool b_mn) {
-  return mma_desc(kPairTile, kPairTile, a_mn, b_mn) | (half ? 0u : (1u << 7) | (1u << 10));
+uint32_t idesc_of(bool half, int width, bool a_mn, bool b_mn) {
+  return mma_desc(kPairTile, width, a_mn, b_mn) | (half ? 0u : (1u << 7) | (1u << 10));
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -506,10 +514,27 @@ Operand operand(int dtype, const void *p, long long ld, long long rows, int dim,
   return o;
 }
 
+// Words per tile: the width that takes the pairs the least time, in rounds of all of
+// them, where a tile costs as much as 32 columns beside its own (its first loads; at
+// many rounds that leaves 256).  777 tokens of 10007 words: 63 -> WIDTH_ODD us for G.
+int tile_width(long long words, long long m) {
+  const long long pairs = sm_count() > 1 ? sm_count() / 2 : 1;
+  long long best = 0, least = 0;
+  for (int width = kPairTile; width >= 64; width -= 64) {
+    const long long cost = up(m * up(words, width), pairs) * (width + 32);
+    if (best == 0 || cost < least) {
+      best = width;
+      least = cost;
+    }
+  }
+  return (int)best;
+}
+
 struct Layout {
   Operand x, w;
   int parts;
   size_t partial, at_target;         // forward
+  int width, wide;                   // words and columns of dx and dw per tile
   long long piece;                   // words
   int pieces, slices;
   size_t unit, g, sums;              // backward
@@ -521,6 +546,9 @@ struct Layout {
     x = operand(dtype, a.x, a.ldx, a.tokens, a.dim, grad);
     w = operand(dtype, a.w, a.ldw, a.vocabulary, a.dim, false);
     bytes = x.bytes + w.bytes;
+    width = tile_width(a.vocabulary, up(a.tokens, kPairTile));
+    // columns: as few tiles as there are of 256, of even size
+    wide = (int)up(up(a.dim, up(a.dim, kPairTile)), 64) * 64;
     partial = at_target = unit = g = sums = 0;
     piece = 0;
     pieces = slices = 0;
@@ -530,18 +558,18 @@ struct Layout {
       return at;
     };
     if (!grad) {
-      partial = take((size_t)up(a.vocabulary, 128) * a.tokens * 8);
+      partial = take(2 * (size_t)up(a.vocabulary, width) * a.tokens * 8);
       at_target = take((size_t)a.tokens * 4);
       return;
     }
-    const long long words = up(a.vocabulary, kPairTile);
-    long long fit = (long long)(kPieceBytes / ((size_t)a.tokens * 2 * parts * kPairTile));
+    const long long words = up(a.vocabulary, width);
+    long long fit = (long long)(kPieceBytes / ((size_t)a.tokens * 2 * parts * width));
     // 1024 words at least: dx is read and written once per piece
-    if (fit < 4) fit = 4;
+    if (fit * width < 1024) fit = up(1024, width);
     pieces = (int)up(words, fit);
-    piece = up(words, pieces) * kPairTile;
+    piece = up(words, pieces) * width;
     // dx's sums are cut so that its tiles fill the pairs, into cuts of 16 blocks at least
-    const long long tiles = up(a.tokens, kPairTile) * up(a.dim, kPairTile);
+    const long long tiles = up(a.tokens, kPairTile) * up(a.dim, wide);
     const long long pairs = sm_count() > 1 ? sm_count() / 2 : 1;
     slices = 1;
     while (slices < 32 && tiles * slices * 2 <= pairs && piece / kPairK / (slices * 2) >= 16)
@@ -633,12 +661,15 @@ cudaError_t xent_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   PairOperands ops{};
   if (!make_map(&ops.a, half, xp, a.tokens, a.dim, l.x.ld, l.parts, 128) ||
-      !make_map(&ops.b, half, wp, a.vocabulary, a.dim, l.w.ld, l.parts, 128))
+      !make_map(&ops.b, half, wp, a.vocabulary, a.dim, l.w.ld, l.parts, l.width / 2))
     return cudaErrorInvalidValue;
-  ops.idesc = idesc_of(half, false, false);
+  ops.width = l.width;
+  ops.b_bytes = (uint32_t)l.width / 2 * 128;
+  ops.idesc = idesc_of(half, l.width, false, false);
   ops.parts = l.parts;
   XentTiles t = tiles_of(a);
-  t.n = (int)up(a.vocabulary, kPairTile);
+  t.width = l.width;
+  t.n = (int)up(a.vocabulary, l.width);
   t.partial = reinterpret_cast<float2 *>(ws + l.partial);
   t.at_target = reinterpret_cast<float *>(ws + l.at_target);
   static DeviceOnce once;
@@ -662,6 +693,7 @@ cudaError_t xent_grad_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st)
   cudaError_t e = lay_both<T>(a, l, ws, true, xp, wp, st);
   if (e != cudaSuccess) return e;
   XentTiles t = tiles_of(a);
+  t.width = l.width;
   float *unit = nullptr;
   if (half) {
     unit = reinterpret_cast<float *>(ws + l.unit);
@@ -675,22 +707,25 @@ cudaError_t xent_grad_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st)
   PairOperands ops{};
   XentProducts p{};
   if (!make_map(&ops.a, half, xp, a.tokens, a.dim, l.x.ld, l.parts, 128) ||
-      !make_map(&ops.b, half, wp, a.vocabulary, a.dim, l.w.ld, l.parts, 128) ||
+      !make_map(&ops.b, half, wp, a.vocabulary, a.dim, l.w.ld, l.parts, l.width / 2) ||
       !make_map(&p.ops[0].a, half, t.g, a.tokens, l.piece, l.piece, l.parts, 128) ||
       !make_map(&p.ops[0].b, half, wp, a.vocabulary, a.dim, l.w.ld, l.parts, 64) ||
       !make_map(&p.ops[1].a, half, t.g, a.tokens, l.piece, l.piece, l.parts, 64) ||
       !make_map(&p.ops[1].b, half, xp, a.tokens, a.dim, l.x.ld, l.parts, 64))
     return cudaErrorInvalidValue;
-  ops.idesc = idesc_of(half, false, false);
+  ops.width = l.width;
+  ops.b_bytes = (uint32_t)l.width / 2 * 128;
+  p.width = p.ops[0].width = p.ops[1].width = l.wide;
+  p.ops[0].b_bytes = p.ops[1].b_bytes = (uint32_t)up(l.wide / 2, 64) * 64 * 128;
+  ops.idesc = idesc_of(half, l.width, false, false);
   p.ops[0].b_mn = p.ops[1].a_mn = p.ops[1].b_mn = 1;
-  p.ops[0].idesc = idesc_of(half, false, true);
-  p.ops[1].idesc = idesc_of(half, true, true);
+  p.ops[0].idesc = idesc_of(half, l.wide, false, true);
+  p.ops[1].idesc = idesc_of(half, l.wide, true, true);
   ops.parts = p.ops[0].parts = p.ops[1].parts = l.parts;
   p.tokens = a.tokens;
-  p.vocabulary = a.vocabulary;
   p.dim = a.dim;
   p.m = t.m;
-  p.n = (int)up(a.dim, kPairTile);
+  p.n = (int)up(a.dim, l.wide);
   p.slices = a.dx ? l.slices : 0;
   p.wk = (int)up(a.tokens, kPairK);
   p.sums = reinterpret_cast<float *>(ws + l.sums);
@@ -702,13 +737,14 @@ cudaError_t xent_grad_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st)
     t.v0 = p.v0 = i * l.piece;
     if (t.v0 >= a.vocabulary) break;
     const long long words = a.vocabulary - t.v0 < l.piece ? a.vocabulary - t.v0 : l.piece;
-    t.n = (int)up(words, kPairTile);
+    t.n = (int)up(words, l.width);
     e = pair_launch(xent_grad_kernel<O, kParts>, once_g, (long long)t.m * t.n, st, ops, t, kblocks,
                     status);
     if (e != cudaSuccess) return e;
     p.first = i == 0;
+    p.words = words;
     p.k = (int)up(words, kPairK);
-    p.wm = a.dw ? t.n : 0;
+    p.wm = a.dw ? (int)up(words, kPairTile) : 0;
     e = pair_launch(xent_products_kernel<T>, once_p,
                     (long long)p.m * p.n * p.slices + (long long)p.wm * p.n, st, p, status);
     if (e != cudaSuccess) return e;
