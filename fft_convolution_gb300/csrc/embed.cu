@@ -93,6 +93,7 @@ embed_sort_kernel(const EmbedSortArgs a) {
     return;
   }
   const unsigned rank = block_rank();
+  if (blockIdx.x == 0 && tid == 0) *a.crossing = 0;
   const long long share = (a.tokens + kSortBlocks - 1) / kSortBlocks;
   const long long begin = min(share * rank, a.tokens), end = min(begin + share, a.tokens);
   const unsigned mask = (1u << a.bits) - 1;
@@ -339,6 +340,9 @@ __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedSumArgs a) {
       const unsigned next = __shfl_sync(0xffffffffu, key, j0 + u + 1);
       const bool ends = next != k;
       if (!ends && j0 + u + 1 < kPiece) continue;
+      // a run that begins here and goes on: one more for the joins, in any order
+      if (!ends && !open && chunk == 0 && lane == 0)
+        a.list[atomicAdd(a.crossing, 1u)] = (unsigned)piece;
       if (ends && !open) {
         R::store(a, k, chunk, lane, acc, ADD ? &old[ADD ? u : 0] : nullptr);
       } else {
@@ -356,9 +360,10 @@ __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedSumArgs a) {
   }
 }
 
-// The runs that go on behind a piece: its own part, then the heads of the
-// pieces behind it, a quarter of them to each warp of the block (the most frequent
-// row of a text crosses dozens; one warp for all of them took 17 us for 16384 tokens).
+// The runs that go on behind the piece where they begin, from the list: its own part,
+// then the heads of the pieces behind it, a quarter of them to each warp of the
+// block (the most frequent row of a text crosses dozens; one warp for all of them, and
+// blocks for every piece, took 17 us for 16384 tokens).
 template <typename T, typename TO, bool VEC>
 __global__ void __launch_bounds__(128) embed_join_kernel(const EmbedSumArgs a) {
   using A = typename Acc<T>::type;
@@ -368,58 +373,58 @@ __global__ void __launch_bounds__(128) embed_join_kernel(const EmbedSumArgs a) {
   __shared__ A parts[3][E][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunks = (a.dim + C::kWide - 1) / C::kWide;
-  const long long piece = blockIdx.x / chunks;
-  const int chunk = (int)(blockIdx.x - piece * chunks);
-  const long long first = piece * kPiece, behind = first + kPiece;
-  if (behind >= a.tokens) return;
-  const unsigned row = a.key[behind - 1], next = a.key[behind];
-  const unsigned front = a.key[first], prev = first > 0 ? a.key[first - 1] : (unsigned)a.rows;
-  if (row == (unsigned)a.rows || next != row) return;
-  if (front == row && prev == row) return;  // began further ahead
-  long long last = piece + 1;  // the piece where the run ends: it goes on where the next begins with it
-  for (;;) {
-    const long long at = (last + 1 + lane) * kPiece;
-    const unsigned on = __ballot_sync(0xffffffffu, at < a.tokens && a.key[at] == row);
-    const int more = __ffs(~on) - 1;
-    last += more < 0 ? 32 : more;
-    if (more >= 0) break;
-  }
-  const A *partial = static_cast<const A *>(a.partial);
-  A acc[E];
-  typename R::Raw old;
-  if (a.add && warp == 0) old = R::load(a, row, chunk, lane);
-  // part 0 is the piece's own tail
-  const long long count = last - piece + 1, share = (count + 3) / 4;
-  const long long from = share * warp, to = min(from + share, count);
-#pragma unroll
-  for (int i = 0; i < E; ++i) acc[i] = 0;
-  for (long long q = from; q < to; q += U) {
-    A f[U][E];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const A *p = partial + ((piece + q + u) * 2 + (q + u == 0 ? 1 : 0)) * a.ldp;
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int c = C::at(chunk, lane, i);
-        f[u][i] = q + u < to && c < a.dim ? p[c] : (A)0;
-      }
+  const long long items = (long long)*a.crossing * chunks;
+  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    const long long piece = a.list[item / chunks];
+    const int chunk = (int)(item % chunks);
+    const unsigned row = a.key[(piece + 1) * kPiece - 1];
+    long long last = piece + 1;  // the piece where the run ends: it goes on where the next begins with it
+    for (;;) {
+      const long long at = (last + 1 + lane) * kPiece;
+      const unsigned on = __ballot_sync(0xffffffffu, at < a.tokens && a.key[at] == row);
+      const int more = __ffs(~on) - 1;
+      last += more < 0 ? 32 : more;
+      if (more >= 0) break;
     }
+    const A *partial = static_cast<const A *>(a.partial);
+    A acc[E];
+    typename R::Raw old;
+    if (a.add && warp == 0) old = R::load(a, row, chunk, lane);
+    // part 0 is the piece's own tail
+    const long long count = last - piece + 1, share = (count + 3) / 4;
+    const long long from = share * warp, to = min(from + share, count);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int i = 0; i < E; ++i) acc[i] = 0;
+    for (long long q = from; q < to; q += U) {
+      A f[U][E];
 #pragma unroll
-      for (int i = 0; i < E; ++i) acc[i] += f[u][i];
+      for (int u = 0; u < U; ++u) {
+        const A *p = partial + ((piece + q + u) * 2 + (q + u == 0 ? 1 : 0)) * a.ldp;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const int c = C::at(chunk, lane, i);
+          f[u][i] = q + u < to && c < a.dim ? p[c] : (A)0;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] += f[u][i];
+    }
+    if (warp > 0) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) parts[warp - 1][i][lane] = acc[i];
+    }
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int w = 0; w < 3; ++w)
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] += parts[w][i][lane];
+      R::store(a, row, chunk, lane, acc, a.add ? &old : nullptr);
+    }
+    __syncthreads();
   }
-  if (warp > 0) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) parts[warp - 1][i][lane] = acc[i];
-  }
-  __syncthreads();
-  if (warp > 0) return;
-#pragma unroll
-  for (int w = 0; w < 3; ++w)
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] += parts[w][i][lane];
-  R::store(a, row, chunk, lane, acc, a.add ? &old : nullptr);
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -445,10 +450,12 @@ cudaError_t sums_t(const EmbedSumArgs &a, cudaStream_t st) {
   const long long chunks = (a.dim + Columns<T, VEC>::kWide - 1) / Columns<T, VEC>::kWide;
   const long long pieces = (a.tokens + kPiece - 1) / kPiece;
   const long long blocks = (pieces * chunks + 3) / 4;
-  if (pieces * chunks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   if (a.add) embed_sum_kernel<T, TO, VEC, true><<<(unsigned)blocks, 128, 0, st>>>(a);
   else embed_sum_kernel<T, TO, VEC, false><<<(unsigned)blocks, 128, 0, st>>>(a);
-  if (pieces > 1) embed_join_kernel<T, TO, VEC><<<(unsigned)(pieces * chunks), 128, 0, st>>>(a);
+  if (pieces == 1) return cudaGetLastError();
+  const long long most = 8ll * sm_count(), items = pieces * chunks;
+  embed_join_kernel<T, TO, VEC><<<(unsigned)(items < most ? items : most), 128, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -466,7 +473,7 @@ size_t list_bytes(long long tokens) { return round256((size_t)tokens * 4); }
 size_t embed_workspace_bytes(long long tokens, int dim, int dtype) {
   if (tokens == 0) return 0;
   const size_t pieces = (size_t)(tokens + kPiece - 1) / kPiece;
-  return 4 * list_bytes(tokens) + pieces * 2 * (size_t)dim * (dtype == FFT_ELEM_F64 ? 8 : 4);
+  return 4 * list_bytes(tokens) + 256 + list_bytes((long long)pieces) + pieces * 2 * (size_t)dim * (dtype == FFT_ELEM_F64 ? 8 : 4);
 }
 
 cudaError_t launch_embed(int dtype, const EmbedArgs &a, cudaStream_t st) {
@@ -494,6 +501,7 @@ cudaError_t launch_embed_grad(int dtype, int ttype, const EmbedGradArgs &g, void
     s.key[i] = reinterpret_cast<unsigned *>(ws + 2 * i * list);
     s.pos[i] = reinterpret_cast<unsigned *>(ws + (2 * i + 1) * list);
   }
+  s.crossing = reinterpret_cast<unsigned *>(ws + 4 * list);
   int bits = 0;  // of the largest key, which is `rows`
   while (bits < 32 && ((unsigned long long)g.rows >> bits) != 0) ++bits;
   s.passes = (bits + kSortBits - 1) / kSortBits;
@@ -520,7 +528,9 @@ cudaError_t launch_embed_grad(int dtype, int ttype, const EmbedGradArgs &g, void
   a.rows = g.rows;
   a.dim = g.dim;
   a.ldp = g.dim;
-  a.partial = ws + 4 * list;
+  a.crossing = s.crossing;
+  a.list = reinterpret_cast<unsigned *>(ws + 4 * list + 256);
+  a.partial = ws + 4 * list + 256 + list_bytes((g.tokens + kPiece - 1) / kPiece);
   a.dtable = g.dtable;
   a.scale = g.scale;
   a.add = g.add;

@@ -134,11 +134,13 @@ struct EmbedSortArgs {
   unsigned *key[2], *pos[2];  // row (tokens of no row: `rows`) and token; pass p reads [p & 1]
   void *fill;
   long long fill_bytes;
+  unsigned *crossing;  // set to 0
 };
 struct EmbedSumArgs {
   const void *dy;
   const unsigned *key, *pos;
-  void *dtable, *partial;  // partial: [piece][head, tail][ldp] accumulators
+  unsigned *crossing, *list;  // how many runs go on behind their first piece, and those pieces
+  void *dtable, *partial;     // partial: [piece][head, tail][ldp] accumulators
   long long tokens, rows, lddy, ldp;
   int dim;
   double scale;
