@@ -69,8 +69,8 @@ struct SortShared {
 // A stable radix sort of (row, token) by one cluster: each block has an eighth
 // of the tokens, digits of at most 9 bits, the arrays between the passes in
 // global memory (the L2 holds them).  Tokens of no row sort behind all others.
-// The clusters beside it meanwhile write the zeros of the rows that no token
-// names: 2 passes over 16384 tokens hide behind 268 MB of them.
+// The clusters beside it meanwhile write zeros to the whole of a new gradient: 2
+// passes over 16384 tokens hide behind 268 MB of them.
 __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThreads)
 embed_sort_kernel(const EmbedSortArgs a) {
   extern __shared__ __align__(16) char smem[];
@@ -85,9 +85,8 @@ embed_sort_kernel(const EmbedSortArgs a) {
     if (head > a.fill_bytes) head = a.fill_bytes;
     const long long words = (a.fill_bytes - head) >> 4, done = head + (words << 4);
     for (long long i = 2 * at; i < head; i += 2 * threads) *reinterpret_cast<uint16_t *>(p + i) = 0;
-#pragma unroll 4
     for (long long i = at; i < words; i += threads)
-      __stcs(reinterpret_cast<uint4 *>(p + head) + i, make_uint4(0, 0, 0, 0));
+      reinterpret_cast<uint4 *>(p + head)[i] = make_uint4(0, 0, 0, 0);
     for (long long i = done + 2 * at; i < a.fill_bytes; i += 2 * threads)
       *reinterpret_cast<uint16_t *>(p + i) = 0;
     return;

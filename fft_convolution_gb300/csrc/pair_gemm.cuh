@@ -6,15 +6,19 @@
 // A cluster of two blocks works on one tile of 256 x 256 (or fewer columns, where
 // that fills the GPU better): each block stages 128 rows of A and half of B's
 // per 64 summed indexes (32 KB; six stages), and gets the tile's 128 upper or lower
-// rows as fp32 in its tensor memory, where two tiles fit: one is summed while the
-// other is read out.  The pair is what
+// rows as fp32.
+//
+// The tensor cores cut the sum off at every addition (toward zero): 4096 positive
+// terms come out 1.1e-5 too small, 16384 7e-5.  So tensor memory only ever holds the
+// sum over kSumBlocks blocks; what reads the tiles out adds these in registers,
+// rounded to nearest, 128 columns of a row per lane.  Two such sums fit: one is
+// made while the other is read.  The pair is what
 // lets the tensor cores run: a block alone would have to load twice the bytes
 // of B per product (96 bytes per clock and SM at the full rate, which the L2
 // does not deliver to all SMs at once; so it is 64).
 //
 // Warp 0 issues the loads (TMA, 128-byte swizzle), warp 1 of the even block
-// the products, warps 4 to 11 read the tiles out: 64 KB of values per tile
-// and block, half the columns to each four warps.
+// the products, warps 4 to 11 read the sums out, half the columns to each four.
 #pragma once
 
 #include <cuda.h>
@@ -27,8 +31,16 @@ namespace fftgb {
 
 constexpr int kPairTile = 256, kPairK = 64, kPairStages = 6;
 constexpr int kPairThreads = 384, kOutWarps = 8;
+constexpr int kSumBlocks = 8;  // sums of 512 terms: 7e-7 too small at most, 1% of the time
 constexpr uint32_t kStageHalf = 128 * 128;  // bytes of A (of B) per stage and block
-constexpr size_t kPairSmem = 1024 + (size_t)kPairStages * 2 * kStageHalf;
+// the stages, and behind them 32 x 33 floats for each of the warps that read tiles out
+constexpr size_t kPairStageBytes = (size_t)kPairStages * 2 * kStageHalf;
+constexpr size_t kPairSpare = kOutWarps * 32 * 33 * sizeof(float);
+constexpr size_t kPairSmem = 1024 + kPairStageBytes + kPairSpare;
+extern __shared__ char pair_smem[];
+__device__ __forceinline__ float *pair_spare() {
+  return reinterpret_cast<float *>(pair_smem + ((1024 - (smem_u32(pair_smem) & 1023)) & 1023) + kPairStageBytes);
+}
 
 // ---- instructions for a pair of blocks -------------------------------------------------
 
@@ -69,10 +81,45 @@ __device__ __forceinline__ void pair_commit(uint64_t *bar) {
       "h"((uint16_t)3)
       : "memory");
 }
+// What these barriers order lies in tensor memory and behind the asynchronous proxy, so
+// arrivals and waits have block scope: with cluster scope each would wait for the
+// stores to global memory under way.
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+__device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t parity, volatile int *failed,
+                                          int *status) {
+  if (bar_poll(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t it = 0; it < (1u << 24); ++it) {
+    if (bar_poll(bar, parity)) return true;
+    if (*failed || clock64() - t0 > 8000000000ll) break;  // about 4 s
+  }
+  *failed = 1;
+  atomicExch(status, 1);  // kDeviceErrorTimeout
+  return false;
+}
+// Registers: 384 threads are launched with 168 each (64 512); the loads and products
+// keep 56, the warps that add sums up have 224.  56 * 128 + 224 * 256 = 64 512.
+constexpr int kPairRegs = 168;
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+}
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 224;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void add32(float (&sums)[N], int j, const uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float2 v = add2(make_float2(sums[j + i], sums[j + i + 1]),
+                          make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])));
+    sums[j + i] = v.x;
+    sums[j + i + 1] = v.y;
+  }
+}
+
 // ---- a tile's work ---------------------------------------------------------------------
 
 // One tile of A B^T summed over blocks k0 .. k1 - 1 of 64 indexes, for every
@@ -107,16 +154,15 @@ struct PairShared {
   int failed;
 };
 
-// Runs the tiles pair, pair + pairs, ... < tiles.  of(t, &which) gives a tile
-// and which of the problems `ops` it belongs to; out(t, address of this
-// warp's lanes in TMEM, at the tile's first column) uses one, in warps 4 .. 11: warp w has lanes
-// 32 (w % 4) .. and the first (w < 8) or last half of the tile's columns.
+// Runs the tiles pair, pair + pairs, ... < tiles.  of(t, which) gives a tile
+// and which of the problems `ops` it belongs to; out(t, sums) uses one, in warps 4 ..
+// 11: a lane of warp w has the tile's row 128 rank + 32 (w % 4) + lane and, in
+// `sums`, the first (w < 8) or last half of its columns.
 template <class Of, class Out>
 __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int *status, Of of,
                                          Out out) {
-  extern __shared__ char smem_raw[];
   __shared__ PairShared sh;
-  const uint32_t stage0 = (smem_u32(smem_raw) + 1023) & ~1023u;
+  const uint32_t stage0 = (smem_u32(pair_smem) + 1023) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5;
   const uint32_t rank = block_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -141,97 +187,129 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
   tc_fence_after();
   const uint32_t tm = sh.tmem;
 
-  if (warp == 0) {
-    if (elect_one()) {
-      uint32_t it = 0;
-      bool ok = true;
-      for (int t = pair; ok && t < tiles; t += pairs) {
-        int which = 0;
-        const PairTile w = of(t, which);
-        const PairOperands &p = ops[which];
-        const int a_row = w.a_row + (int)rank * 128, b_row = w.b_row + (int)rank * (p.width / 2);
-        const int nq = part_pairs(p.parts);
-        for (int q = 0; ok && q < nq; ++q) {
-          int pa, pb;
-          part_pair(p.parts, q, pa, pb);
-          for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
-            const uint32_t s = it % kPairStages, round = it / kPairStages;
-            if (round > 0 && !wait_cluster(&sh.empty[s], (round - 1) & 1, failed, status)) {
+  if (warp < 4) {
+    fewer_registers();
+    if (warp == 0) {
+      if (elect_one()) {
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = pair; ok && t < tiles; t += pairs) {
+          int which = 0;
+          const PairTile w = of(t, which);
+          const PairOperands &p = ops[which];
+          const int a_row = w.a_row + (int)rank * 128, b_row = w.b_row + (int)rank * (p.width / 2);
+          const int nq = part_pairs(p.parts);
+          for (int q = 0; ok && q < nq; ++q) {
+            int pa, pb;
+            part_pair(p.parts, q, pa, pb);
+            for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
+              const uint32_t s = it % kPairStages, round = it / kPairStages;
+              if (round > 0 && !wait_pair(&sh.empty[s], (round - 1) & 1, failed, status)) {
+                ok = false;
+                break;
+              }
+              if (rank == 0) bar_arrive_tx(&sh.full[s], 2 * (kStageHalf + p.b_bytes));
+              const uint32_t bar = peer(smem_u32(&sh.full[s]), 0);
+              const uint32_t sa = stage0 + s * 2 * kStageHalf, sb = sa + kStageHalf;
+              const int k = kb * kPairK;
+              if (p.a_mn) {
+                pair_load(sa, &p.a, bar, a_row, w.a_base + k, pa);
+                pair_load(sa + kStageHalf / 2, &p.a, bar, a_row + 64, w.a_base + k, pa);
+              } else {
+                pair_load(sa, &p.a, bar, k, a_row, pa);
+              }
+              if (p.b_mn) {
+                pair_load(sb, &p.b, bar, b_row, w.b_base + k, pb);
+                if (p.width > 128)
+                  pair_load(sb + kStageHalf / 2, &p.b, bar, b_row + 64, w.b_base + k, pb);
+              } else {
+                pair_load(sb, &p.b, bar, k, b_row, pb);
+              }
+            }
+          }
+        }
+        if (*failed && rank == 0)  // given up: no copy may land after the blocks have gone
+          for (uint32_t i = it > kPairStages ? it - kPairStages : 0; i < it; ++i)
+            bar_wait(&sh.full[i % kPairStages], (i / kPairStages) & 1);
+      }
+    } else if (warp == 1 && rank == 0) {
+      if (elect_one()) {
+        uint32_t it = 0;
+        bool ok = true;
+        uint32_t n = 0;
+        for (int t = pair; ok && t < tiles; t += pairs) {
+          int which = 0;
+          const PairTile w = of(t, which);
+          const PairOperands &p = ops[which];
+          const int blocks = (w.k1 - w.k0) * part_pairs(p.parts);
+          // 16 summed indexes: 32 bytes of a K-major row, 16 rows of an MN-major tile
+          const uint32_t step_a = p.a_mn ? 2048 : 32, step_b = p.b_mn ? 2048 : 32;
+          for (int b0 = 0; ok && b0 < blocks; b0 += kSumBlocks, ++n) {
+            const int acc = n & 1, count = min(kSumBlocks, blocks - b0);
+            if (n > 1 && !wait_pair(&sh.taken[acc], ((n >> 1) - 1) & 1, failed, status)) {
               ok = false;
               break;
             }
-            if (rank == 0) bar_arrive_tx(&sh.full[s], 2 * (kStageHalf + p.b_bytes));
-            const uint32_t bar = peer(smem_u32(&sh.full[s]), 0);
-            const uint32_t sa = stage0 + s * 2 * kStageHalf, sb = sa + kStageHalf;
-            const int k = kb * kPairK;
-            if (p.a_mn) {
-              pair_load(sa, &p.a, bar, a_row, w.a_base + k, pa);
-              pair_load(sa + kStageHalf / 2, &p.a, bar, a_row + 64, w.a_base + k, pa);
-            } else {
-              pair_load(sa, &p.a, bar, k, a_row, pa);
+            tc_fence_after();
+            for (int kb = 0; kb < count; ++kb, ++it) {
+              const uint32_t s = it % kPairStages;
+              if (!wait_pair(&sh.full[s], (it / kPairStages) & 1, failed, status)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t sa = stage0 + s * 2 * kStageHalf, sb = sa + kStageHalf;
+  #pragma unroll
+              for (uint32_t k = 0; k < kPairK / 16; ++k)
+                pair_mma(tm + acc * kPairTile, tile_desc(sa + k * step_a, kStageHalf / 2),
+                         tile_desc(sb + k * step_b, kStageHalf / 2), p.idesc, kb > 0 || k > 0);
+              pair_commit(&sh.empty[s]);
             }
-            if (p.b_mn) {
-              pair_load(sb, &p.b, bar, b_row, w.b_base + k, pb);
-              if (p.width > 128)
-                pair_load(sb + kStageHalf / 2, &p.b, bar, b_row + 64, w.b_base + k, pb);
-            } else {
-              pair_load(sb, &p.b, bar, k, b_row, pb);
-            }
+            if (ok) pair_commit(&sh.ready[acc]);
           }
         }
-      }
-      if (*failed && rank == 0)  // given up: no copy may land after the blocks have gone
-        for (uint32_t i = it > kPairStages ? it - kPairStages : 0; i < it; ++i)
-          bar_wait(&sh.full[i % kPairStages], (i / kPairStages) & 1);
-    }
-  } else if (warp == 1 && rank == 0) {
-    if (elect_one()) {
-      uint32_t it = 0;
-      bool ok = true;
-      int n = 0;
-      for (int t = pair; ok && t < tiles; t += pairs, ++n) {
-        int which = 0;
-        const PairTile w = of(t, which);
-        const PairOperands &p = ops[which];
-        const int acc = n & 1;
-        if (n > 1 && !wait_cluster(&sh.taken[acc], ((n >> 1) - 1) & 1, failed, status)) break;
-        tc_fence_after();
-        const int blocks = (w.k1 - w.k0) * part_pairs(p.parts);
-        // 16 summed indexes: 32 bytes of a K-major row, 16 rows of an MN-major tile
-        const uint32_t step_a = p.a_mn ? 2048 : 32, step_b = p.b_mn ? 2048 : 32;
-        for (int kb = 0; kb < blocks; ++kb, ++it) {
-          const uint32_t s = it % kPairStages;
-          if (!wait_cluster(&sh.full[s], (it / kPairStages) & 1, failed, status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = stage0 + s * 2 * kStageHalf, sb = sa + kStageHalf;
-#pragma unroll
-          for (uint32_t k = 0; k < kPairK / 16; ++k)
-            pair_mma(tm + acc * kPairTile, tile_desc(sa + k * step_a, kStageHalf / 2),
-                     tile_desc(sb + k * step_b, kStageHalf / 2), p.idesc, kb > 0 || k > 0);
-          pair_commit(&sh.empty[s]);
+        if (*failed) {  // no product may write tensor memory that has been given back
+          pair_commit(&sh.done);
+          bar_wait(&sh.done, 0);
         }
-        if (ok) pair_commit(&sh.ready[acc]);
-      }
-      if (*failed) {  // no product may write tensor memory that has been given back
-        pair_commit(&sh.done);
-        bar_wait(&sh.done, 0);
       }
     }
-  } else if (warp >= 4) {
-    int n = 0;
+  } else {
+    more_registers();
+    uint32_t n = 0;
     const uint32_t base = tm + ((uint32_t)(warp & 3) << 21);
-    for (int t = pair; t < tiles; t += pairs, ++n) {
-      const int acc = n & 1;
-      if (!wait_cluster(&sh.ready[acc], (n >> 1) & 1, failed, status)) break;
-      __syncwarp();
-      tc_fence_after();
-      out(t, base + acc * kPairTile);
-      tc_fence_before();
-      __syncwarp();
-      if ((tid & 31) == 0) arrive_at(peer(smem_u32(&sh.taken[acc]), 0));
+    bool ok = true;
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      int which = 0;
+      const PairTile w = of(t, which);
+      const int wide = ops[which].width / 2;
+      const int blocks = (w.k1 - w.k0) * part_pairs(ops[which].parts);
+      float sums[kPairTile / 2];
+#pragma unroll
+      for (int i = 0; i < kPairTile / 2; ++i) sums[i] = 0.0f;
+      for (int b0 = 0; b0 < blocks; b0 += kSumBlocks, ++n) {
+        const int acc = n & 1;
+        ok = wait_pair(&sh.ready[acc], (n >> 1) & 1, failed, status);
+        if (!ok) break;
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t at = base + acc * kPairTile + (uint32_t)((warp - 4) >> 2) * wide;
+        uint32_t r[2][32];
+        tmem_ld(at, r[0]);
+        if (wide > 32) tmem_ld(at + 32, r[1]);
+        tmem_wait_ld();
+        add32(sums, 0, r[0]);
+        if (wide > 64) tmem_ld(at + 64, r[0]);
+        if (wide > 32) add32(sums, 32, r[1]);
+        if (wide > 96) tmem_ld(at + 96, r[1]);
+        tmem_wait_ld();
+        if (wide > 64) add32(sums, 64, r[0]);
+        if (wide > 96) add32(sums, 96, r[1]);
+        tc_fence_before();
+        __syncwarp();
+        if ((tid & 31) == 0) arrive_at(peer(smem_u32(&sh.taken[acc]), 0));
+      }
+      if (ok) out(t, sums);
     }
   }
   __syncwarp();

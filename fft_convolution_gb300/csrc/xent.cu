@@ -111,15 +111,7 @@ struct XentTiles {
   long long ldg;
 };
 
-// The 32 columns of a warp's lanes from `addr` on.
-__device__ __forceinline__ void read32(uint32_t addr, float (&f)[32]) {
-  uint32_t r[32];
-  __syncwarp();
-  tmem_ld(addr, r);
-  tmem_wait_ld();
-#pragma unroll
-  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
-}
+constexpr int kHalf = kPairTile / 2;  // columns of a lane, at most
 
 // Tiles of all token blocks before the next words: x stays in the L2, W is read once.
 __device__ __forceinline__ PairTile word_tile(const XentTiles &p, int t, long long v0, int k) {
@@ -137,43 +129,33 @@ xent_sums_kernel(const __grid_constant__ PairOperands ops, const XentTiles p, in
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = (int)block_rank(), half = (warp - 4) >> 2;
   auto of = [&](int t, int &) { return word_tile(p, t, 0, kblocks); };
-  auto out = [&](int t, uint32_t tm) {
+  auto out = [&](int t, float (&f)[kHalf]) {
     const PairTile w = word_tile(p, t, 0, kblocks);
     const long long n = w.a_row + rank * 128 + (warp & 3) * 32 + lane;
     const int wide = p.width / 2;
     const long long v0 = w.b_row + half * wide;
-    tm += half * wide;
-    if (v0 >= p.vocabulary) return;
+    if (v0 >= p.vocabulary || n >= p.tokens) return;
     const int count = (int)min((long long)wide, p.vocabulary - v0);
-    const long long target = n < p.tokens ? target_of(p.targets, p.target_bytes, n) - v0 : -1;
+    const long long target = target_of(p.targets, p.target_bytes, n) - v0;
     const bool mine = target >= 0 && target < count;
-    float top = -INFINITY;
-    for (int c = 0; c < count; c += 32) {
-      float f[32];
-      read32(tm + c, f);
+    float top = -INFINITY, at = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (c + i < count) top = fmaxf(top, f[i]);
+    for (int i = 0; i < kHalf; ++i)
+      if (i < count) top = fmaxf(top, f[i]);
+    if (mine) {
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i)
+        if (target == i) at = f[i];
+      p.at_target[n] = at;
     }
     // all of them -infinity (or NaN): in units of 1
     top = top == -INFINITY ? top : top * kLog2e;
     const float unit = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f;
-    for (int c = 0; c < count; c += 32) {
-      float f[32];
-      read32(tm + c, f);
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (c + i < count) sum += exp2_approx(fmaf(f[i], kLog2e, -unit));
-      if (__any_sync(0xffffffffu, mine && target >= c && target < c + 32)) {
-        float at = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (target == c + i) at = f[i];
-        if (mine && target >= c && target < c + 32) p.at_target[n] = at;
-      }
-    }
-    if (n < p.tokens) p.partial[(2ll * (t / p.m) + half) * p.tokens + n] = make_float2(sum == 0.0f ? top : unit, sum);
+    for (int i = 0; i < kHalf; ++i)
+      if (i < count) sum += exp2_approx(fmaf(f[i], kLog2e, -unit));
+    p.partial[(2ll * (t / p.m) + half) * p.tokens + n] = make_float2(sum == 0.0f ? top : unit, sum);
   };
   pair_run(&ops, p.m * p.n, status, of, out);
 }
@@ -278,36 +260,33 @@ xent_grad_kernel(const __grid_constant__ PairOperands ops, const XentTiles p, in
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = (int)block_rank(), half = (warp - 4) >> 2;
   auto of = [&](int t, int &) { return word_tile(p, t, p.v0, kblocks); };
-  auto out = [&](int t, uint32_t tm) {
+  auto out = [&](int t, float (&f)[kHalf]) {
     const PairTile w = word_tile(p, t, p.v0, kblocks);
     const long long n = w.a_row + rank * 128 + (warp & 3) * 32 + lane;
+    if (n >= p.tokens) return;
     const int wide = p.width / 2;
     const long long v = w.b_row + half * wide;
-    tm += half * wide;
+    const long long target = target_of(p.targets, p.target_bytes, n);
     float c = 0.0f, lse = 0.0f;
-    long long target = -1;
-    if (n < p.tokens) {
-      target = target_of(p.targets, p.target_bytes, n);
-      if (target >= 0 && target < p.vocabulary) {
-        c = p.dloss[n] * (p.unit ? p.unit[0] : 1.0f);
-        lse = p.lse[n];
-      }
+    if (target >= 0 && target < p.vocabulary) {
+      c = p.dloss[n] * (p.unit ? p.unit[0] : 1.0f);
+      lse = p.lse[n];
     }
     const bool live = c != 0.0f;  // NaN is live
     O *row = static_cast<O *>(p.g) + n * p.ldg + (v - p.v0);
     const int at = target >= v && target < v + wide ? (int)(target - v) : -1;
-    const int count = (int)max(0ll, min((long long)wide, p.vocabulary - v));
-#pragma unroll 1
-    for (int j = 0; j < wide; j += 32) {
-      float f[32];
-      read32(tm + j, f);
+    const int count = live ? (int)max(0ll, min((long long)wide, p.vocabulary - v)) : 0;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float q = exp2_approx((f[i] - lse) * kLog2e) - (at == j + i ? 1.0f : 0.0f);
-        f[i] = live && j + i < count ? q * c : 0.0f;
+    for (int j = 0; j < kHalf; j += 32)
+      if (j < wide) {
+        float q[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          q[i] = exp2_approx((f[j + i] - lse) * kLog2e) - (at == j + i ? 1.0f : 0.0f);
+          q[i] = j + i < count ? q[i] * c : 0.0f;
+        }
+        put32<O, PARTS>(row + j, p.tokens * p.ldg, q);
       }
-      if (n < p.tokens) put32<O, PARTS>(row + j, p.tokens * p.ldg, f);
-    }
   };
   pair_run(&ops, p.m * p.n, status, of, out);
 }
@@ -328,30 +307,55 @@ struct XentProducts {
   const float *unit;
 };
 
+// 32 columns from c on of a warp's 32 rows (a lane has one) into an array of rows of
+// dim elements, + what is there.  Rows on 16-byte boundaries: each lane its own;
+// others: a row at a time, through shared memory (each lane writing its row by
+// elements took half the time of 777 tokens, 333 wide).
 template <typename T>
-__device__ __forceinline__ void put_columns(T *row, int c, int dim, bool vec, const float (&f)[32]) {
+__device__ __forceinline__ void put_rows(T *out, long long row0, long long rows, int c, int dim, bool vec,
+                                         bool add, float (&f)[32], float *turn) {
   constexpr int P = 16 / (int)sizeof(T);
+  const int lane = threadIdx.x & 31;
   if (vec) {
+    if (row0 + lane >= rows) return;
+    T *row = out + (row0 + lane) * dim + c;
 #pragma unroll
     for (int j = 0; j < 32 / P; ++j) {
       if (c + j * P < dim) {
         float v[P];
 #pragma unroll
         for (int i = 0; i < P; ++i) v[i] = f[j * P + i];
-        reinterpret_cast<uint4 *>(row + c)[j] = pack<T>(v);
+        if (add) {
+          float o[P];
+          unpack<T>(reinterpret_cast<const uint4 *>(row)[j], o);
+#pragma unroll
+          for (int i = 0; i < P; ++i) v[i] += o[i];
+        }
+        reinterpret_cast<uint4 *>(row)[j] = pack<T>(v);
       }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (c + i < dim) row[c + i] = from_acc<T>(f[i]);
+    return;
   }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) turn[lane * 33 + i] = f[i];
+  __syncwarp();
+  const int count = (int)max(0ll, min(32ll, rows - row0));
+  if (c + lane < dim) {
+    T *col = out + row0 * dim + c + lane;
+#pragma unroll 8
+    for (int r = 0; r < count; ++r) {
+      float v = turn[r * 33 + lane];
+      if (add) v += to_acc(col[(long long)r * dim]);
+      col[(long long)r * dim] = from_acc<T>(v);
+    }
+  }
+  __syncwarp();
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kPairThreads, 1)
 xent_products_kernel(const __grid_constant__ XentProducts p, int *status) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5;
   const int rank = (int)block_rank(), half = (warp - 4) >> 2;
   const int mn = p.m * p.n, dx_tiles = mn * p.slices, dw_tiles = p.wm * p.n;
   auto of = [&](int t, int &which) {
@@ -373,51 +377,28 @@ xent_products_kernel(const __grid_constant__ XentProducts p, int *status) {
     }
     return w;
   };
-  auto out = [&](int t, uint32_t tm) {
+  auto out = [&](int t, float (&f)[kHalf]) {
     int which = 0;
     const PairTile w = of(t, which);
-    const long long r = w.a_row + rank * 128 + (warp & 3) * 32 + lane;
+    const long long r0 = w.a_row + rank * 128 + (warp & 3) * 32;  // the warp's first row
     const int wide = p.width / 2, c0 = w.b_row + half * wide;
-    tm += half * wide;
-    const float back = p.unit ? p.unit[1] : 1.0f;
-#pragma unroll 1
-    for (int j = 0; j < wide && c0 + j < p.dim; j += 32) {
-      float f[32];
-      read32(tm + j, f);
-      const int c = c0 + j;
-      if (which == 0) {
-        if (w.k0 == w.k1) {  // an empty cut of a short piece: nothing was summed
+    const float back = which == 1 && p.unit ? p.unit[1] : 1.0f;
+    float *turn = pair_spare() + (warp - 4) * (32 * 33);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) f[i] = 0.0f;
+    for (int j = 0; j < kHalf; j += 32)
+      if (j < wide && c0 + j < p.dim) {
+        float q[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) q[i] = f[j + i] * back;
+        const int c = c0 + j;
+        if (which == 0) {
+          put_rows<float>(p.sums + (long long)(t / mn) * p.tokens * p.dim, r0, p.tokens, c, p.dim,
+                          p.dim % 4 == 0, !p.first, q, turn);
+        } else {
+          const bool vec = p.dim % (16 / (int)sizeof(T)) == 0 && ((uintptr_t)p.dw & 15) == 0;
+          put_rows<T>(static_cast<T *>(p.dw) + p.v0 * p.dim, r0, p.words, c, p.dim, vec, false, q, turn);
         }
-        float *row = p.sums + ((long long)(t / mn) * p.tokens + r) * p.dim;
-        const bool vec = p.dim % 4 == 0, live = r < p.tokens;
-        if (live && !p.first) {
-          if (vec) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              if (c + i < p.dim) {
-                const float4 o = *reinterpret_cast<const float4 *>(row + c + i);
-                f[i] += o.x;
-                f[i + 1] += o.y;
-                f[i + 2] += o.z;
-                f[i + 3] += o.w;
-              }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c + i < p.dim) f[i] += row[c + i];
-          }
-        }
-        if (live) put_columns<float>(row, c, p.dim, vec, f);
-      } else {
-        const long long v = p.v0 + r;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) f[i] *= back;
-        const bool vec = p.dim % (16 / (int)sizeof(T)) == 0 && ((uintptr_t)p.dw & 15) == 0;
-        if (r < p.words) put_columns<T>(static_cast<T *>(p.dw) + v * p.dim, c, p.dim, vec, f);
       }
-    }
   };
   pair_run(p.ops, dx_tiles + dw_tiles, status, of, out);
 }
@@ -603,6 +584,15 @@ cudaError_t pair_launch(K *kern, DeviceOnce &once, long long tiles, cudaStream_t
                         const Args &...args) {
   cudaError_t e = smem_limit_once((const void *)kern, kPairSmem, once);
   if (e != cudaSuccess) return e;
+  // the split of registers counts on what a block is launched with
+  static std::atomic<int> regs;
+  if (regs.load(std::memory_order_acquire) == 0) {
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, (const void *)kern);
+    if (e != cudaSuccess) return e;
+    regs.store(at.numRegs, std::memory_order_release);
+  }
+  if (regs.load(std::memory_order_acquire) < kPairRegs) return cudaErrorLaunchOutOfResources;
   const long long pairs = sm_count() / 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
