@@ -108,8 +108,9 @@ SIGNATURES = {
     "fft_embedding_workspace_bytes": (_SZ, [_I64, _I64, _INT]),
     "fft_embedding_backward": (_INT, [_VP, _I64, _VP, _INT, _VP, _I64, _I64, _I64, _DBL, _INT, _INT,
                                       _INT, _VP, _SZ, _VP]),
-    "fft_linear_recurrence": (_INT, [_VP] * 9),
-    "fft_linear_recurrence_backward": (_INT, [_VP] * 14),
+    "fft_linear_recurrence_workspace_bytes": (_SZ, [_VP, _INT]),
+    "fft_linear_recurrence": (_INT, [_VP] * 9 + [_SZ, _VP]),
+    "fft_linear_recurrence_backward": (_INT, [_VP] * 14 + [_SZ, _VP]),
     "fft_linear_recurrence_step": (_INT, [_VP] * 6 + [_I64, _VP, _VP]),
     "fft_linear_cross_entropy_workspace_bytes": (_SZ, [_VP, _I64, _VP, _I64, _I64, _I64, _I64, _INT,
                                                        _INT]),
@@ -331,18 +332,24 @@ def fft_embedding_backward(dy: int, lddy: int, ids: int, id_bytes: int, dtable: 
                                        dtype, ttype, workspace, workspace_bytes, stream)
 
 
+def fft_linear_recurrence_workspace_bytes(desc: RecurrenceDesc, packed: int) -> int:
+    return int(_lib.fft_linear_recurrence_workspace_bytes(ctypes.byref(desc), packed))
+
+
 def fft_linear_recurrence(desc: RecurrenceDesc, x: int, g: int, beta: int, offsets: int,
-                          initial_state: int, y: int, final_state: int, stream: int) -> int:
+                          initial_state: int, y: int, final_state: int, workspace: int,
+                          workspace_bytes: int, stream: int) -> int:
     return _lib.fft_linear_recurrence(ctypes.byref(desc), x, g, beta, offsets, initial_state, y,
-                                      final_state, stream)
+                                      final_state, workspace, workspace_bytes, stream)
 
 
 def fft_linear_recurrence_backward(desc: RecurrenceDesc, dy: int, x: int, g: int, beta: int, y: int,
                                    offsets: int, initial_state: int, dfinal_state: int, dx: int,
-                                   dg: int, dbeta: int, dinitial_state: int, stream: int) -> int:
+                                   dg: int, dbeta: int, dinitial_state: int, workspace: int,
+                                   workspace_bytes: int, stream: int) -> int:
     return _lib.fft_linear_recurrence_backward(ctypes.byref(desc), dy, x, g, beta, y, offsets,
                                                initial_state, dfinal_state, dx, dg, dbeta,
-                                               dinitial_state, stream)
+                                               dinitial_state, workspace, workspace_bytes, stream)
 
 
 def fft_linear_recurrence_step(desc: RecurrenceDesc, x: int, g: int, beta: int, state: int, slots: int,

@@ -29,9 +29,8 @@ int embed_sizes(int64_t tokens, int64_t rows, int64_t dim, int dtype) {
 
 RecurStride stride(const int64_t s[2]) { return RecurStride{s[0], s[1]}; }
 
-// Sizes, types and inputs of a call of the recurrence.
-int recur_check(const fft_recurrence_desc *d, const void *x, const void *g, const void *beta,
-                bool x_used, RecurArgs *a) {
+// Sizes and types of a call of the recurrence.
+int recur_sizes(const fft_recurrence_desc *d, RecurArgs *a) {
   if (!d || d->batch < 0 || d->tokens < 0 || d->channels <= 0 || !elem_type(d->dtype) ||
       !elem_type(d->gtype))
     return FFT_ERR_INVALID_ARG;
@@ -43,13 +42,7 @@ int recur_check(const fft_recurrence_desc *d, const void *x, const void *g, cons
       (d->batch > 0 && (d->channels + 127) / 128 > kMaxInt / 8 / d->batch) ||
       (d->tokens > 0 && d->batch > kMaxElems / d->tokens / d->channels))
     return FFT_ERR_UNSUPPORTED;
-  if (d->batch > 0 && d->tokens > 0 && ((x_used && !x) || !g)) return FFT_ERR_INVALID_ARG;
-  if (off_element(x, d->dtype) || off_element(g, d->gtype) || off_element(beta, d->gtype))
-    return FFT_ERR_MISALIGNED;
   *a = RecurArgs{};
-  a->x = x;
-  a->g = g;
-  a->beta = beta;
   a->sx = stride(d->x_stride);
   a->sg = stride(d->g_stride);
   a->sb = stride(d->beta_stride);
@@ -57,6 +50,30 @@ int recur_check(const fft_recurrence_desc *d, const void *x, const void *g, cons
   a->tokens = d->tokens;
   a->channels = (int)d->channels;
   a->clear = d->clear_rows != 0;
+  return FFT_OK;
+}
+
+// Those and the inputs.
+int recur_check(const fft_recurrence_desc *d, const void *x, const void *g, const void *beta,
+                bool x_used, RecurArgs *a) {
+  const int rc = recur_sizes(d, a);
+  if (rc != FFT_OK) return rc;
+  if (d->batch > 0 && d->tokens > 0 && ((x_used && !x) || !g)) return FFT_ERR_INVALID_ARG;
+  if (off_element(x, d->dtype) || off_element(g, d->gtype) || off_element(beta, d->gtype))
+    return FFT_ERR_MISALIGNED;
+  a->x = x;
+  a->g = g;
+  a->beta = beta;
+  return FFT_OK;
+}
+
+// Where the first rows of many packed sequences are put.
+int recur_workspace(RecurArgs *a, void *workspace, size_t workspace_bytes) {
+  const size_t need = a->batch > 0 ? recur_workspace_bytes(a->batch, a->offsets != nullptr) : 0;
+  if (need == 0) return FFT_OK;
+  if (!workspace || workspace_bytes < need) return FFT_ERR_INVALID_ARG;
+  if (misaligned(workspace)) return FFT_ERR_MISALIGNED;
+  a->rows = static_cast<int *>(workspace);
   return FFT_OK;
 }
 
@@ -134,11 +151,18 @@ int fft_embedding_backward(const void *dy, int64_t lddy, const void *ids, int id
   return finish(launch_embed_grad(dtype, ttype, a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
+size_t fft_linear_recurrence_workspace_bytes(const fft_recurrence_desc *desc, int packed) {
+  RecurArgs a;
+  if (!desc || recur_sizes(desc, &a) != FFT_OK || a.batch == 0) return 0;
+  return recur_workspace_bytes(a.batch, packed != 0);
+}
+
 int fft_linear_recurrence(const fft_recurrence_desc *desc, const void *x, const void *g,
                           const void *beta, const int32_t *offsets, const float *initial_state,
-                          void *y, float *final_state, void *stream) {
+                          void *y, float *final_state, void *workspace, size_t workspace_bytes,
+                          void *stream) {
   RecurArgs a;
-  const int rc = recur_check(desc, x, g, beta, true, &a);
+  int rc = recur_check(desc, x, g, beta, true, &a);
   if (rc != FFT_OK) return rc;
   a.clear = a.clear && offsets && a.tokens > 0;
   if (a.batch == 0 && !a.clear) return FFT_OK;
@@ -150,6 +174,8 @@ int fft_linear_recurrence(const fft_recurrence_desc *desc, const void *x, const 
   a.state_in = initial_state;
   a.state_out = final_state;
   a.y = y;
+  rc = recur_workspace(&a, workspace, workspace_bytes);
+  if (rc != FFT_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a.batch == 0) return finish(clear_all(a, y, desc->dtype, st));
   const bool gf = desc->gtype == FFT_ELEM_F32;
@@ -164,9 +190,10 @@ int fft_linear_recurrence_backward(const fft_recurrence_desc *desc, const void *
                                    const void *g, const void *beta, const void *y,
                                    const int32_t *offsets, const float *initial_state,
                                    const float *dfinal_state, void *dx, void *dg, void *dbeta,
-                                   float *dinitial_state, void *stream) {
+                                   float *dinitial_state, void *workspace,
+                                   size_t workspace_bytes, void *stream) {
   RecurArgs a;
-  const int rc = recur_check(desc, x, g, beta, beta != nullptr, &a);
+  int rc = recur_check(desc, x, g, beta, beta != nullptr, &a);
   if (rc != FFT_OK) return rc;
   a.clear = a.clear && offsets && a.tokens > 0;
   if (a.batch == 0 && !a.clear) return FFT_OK;
@@ -187,6 +214,8 @@ int fft_linear_recurrence_backward(const fft_recurrence_desc *desc, const void *
   a.dg = dg;
   a.dbeta = beta ? dbeta : nullptr;
   a.dinitial = dinitial_state;
+  rc = recur_workspace(&a, workspace, workspace_bytes);
+  if (rc != FFT_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a.batch == 0) {
     cudaError_t e = clear_all(a, dx, desc->dtype, st);

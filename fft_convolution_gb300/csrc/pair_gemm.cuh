@@ -5,7 +5,7 @@
 //
 // A cluster of two blocks works on one tile of 256 x 256 (or fewer columns, where
 // that fills the GPU better): each block stages 128 rows of A and half of B's
-// per 64 summed indexes (32 KB; six stages), and gets the tile's 128 upper or lower
+// per 64 summed indexes (32 KB; six stages, more of narrower tiles), and gets the tile's 128 upper or lower
 // rows as fp32.
 //
 // The tensor cores cut the sum off at every addition (toward zero): 4096 positive
@@ -29,12 +29,12 @@
 
 namespace fftgb {
 
-constexpr int kPairTile = 256, kPairK = 64, kPairStages = 6;
+constexpr int kPairTile = 256, kPairK = 64, kPairStages = 10;  // stages at most
 constexpr int kPairThreads = 384, kOutWarps = 8;
 constexpr int kSumBlocks = 8;  // sums of 512 terms: 7e-7 too small at most, 1% of the time
 constexpr uint32_t kStageHalf = 128 * 128;  // bytes of A (of B) per stage and block
 // the stages, and behind them 32 x 33 floats for each of the warps that read tiles out
-constexpr size_t kPairStageBytes = (size_t)kPairStages * 2 * kStageHalf;
+constexpr uint32_t kPairStageBytes = 6 * 2 * kStageHalf;
 constexpr size_t kPairSpare = kOutWarps * 32 * 33 * sizeof(float);
 constexpr size_t kPairSmem = 1024 + kPairStageBytes + kPairSpare;
 extern __shared__ char pair_smem[];
@@ -163,6 +163,9 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
                                          Out out) {
   __shared__ PairShared sh;
   const uint32_t stage0 = (smem_u32(pair_smem) + 1023) & ~1023u;
+  // all problems of a launch have one width
+  const uint32_t stage_bytes = kStageHalf + ops[0].b_bytes;
+  const uint32_t stages = min((uint32_t)kPairStages, kPairStageBytes / stage_bytes);
   const int tid = threadIdx.x, warp = tid >> 5;
   const uint32_t rank = block_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -191,7 +194,7 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
     fewer_registers();
     if (warp == 0) {
       if (elect_one()) {
-        uint32_t it = 0;
+        uint32_t s = 0, round = 0;  // the stage, and how often the ring has gone round
         bool ok = true;
         for (int t = pair; ok && t < tiles; t += pairs) {
           int which = 0;
@@ -202,15 +205,14 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
           for (int q = 0; ok && q < nq; ++q) {
             int pa, pb;
             part_pair(p.parts, q, pa, pb);
-            for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
-              const uint32_t s = it % kPairStages, round = it / kPairStages;
+            for (int kb = w.k0; kb < w.k1; ++kb) {
               if (round > 0 && !wait_pair(&sh.empty[s], (round - 1) & 1, failed, status)) {
                 ok = false;
                 break;
               }
               if (rank == 0) bar_arrive_tx(&sh.full[s], 2 * (kStageHalf + p.b_bytes));
               const uint32_t bar = peer(smem_u32(&sh.full[s]), 0);
-              const uint32_t sa = stage0 + s * 2 * kStageHalf, sb = sa + kStageHalf;
+              const uint32_t sa = stage0 + s * stage_bytes, sb = sa + kStageHalf;
               const int k = kb * kPairK;
               if (p.a_mn) {
                 pair_load(sa, &p.a, bar, a_row, w.a_base + k, pa);
@@ -225,18 +227,19 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
               } else {
                 pair_load(sb, &p.b, bar, k, b_row, pb);
               }
+              if (++s == stages) s = 0, ++round;
             }
           }
         }
         if (*failed && rank == 0)  // given up: no copy may land after the blocks have gone
-          for (uint32_t i = it > kPairStages ? it - kPairStages : 0; i < it; ++i)
-            bar_wait(&sh.full[i % kPairStages], (i / kPairStages) & 1);
+          for (uint32_t i = 0; i < stages; ++i)
+            if (i < s) bar_wait(&sh.full[i], round & 1);
+            else if (round > 0) bar_wait(&sh.full[i], (round - 1) & 1);
       }
     } else if (warp == 1 && rank == 0) {
       if (elect_one()) {
-        uint32_t it = 0;
+        uint32_t s = 0, round = 0, n = 0;
         bool ok = true;
-        uint32_t n = 0;
         for (int t = pair; ok && t < tiles; t += pairs) {
           int which = 0;
           const PairTile w = of(t, which);
@@ -251,19 +254,19 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
               break;
             }
             tc_fence_after();
-            for (int kb = 0; kb < count; ++kb, ++it) {
-              const uint32_t s = it % kPairStages;
-              if (!wait_pair(&sh.full[s], (it / kPairStages) & 1, failed, status)) {
+            for (int kb = 0; kb < count; ++kb) {
+              if (!wait_pair(&sh.full[s], round & 1, failed, status)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
-              const uint32_t sa = stage0 + s * 2 * kStageHalf, sb = sa + kStageHalf;
-  #pragma unroll
+              const uint32_t sa = stage0 + s * stage_bytes, sb = sa + kStageHalf;
+#pragma unroll
               for (uint32_t k = 0; k < kPairK / 16; ++k)
                 pair_mma(tm + acc * kPairTile, tile_desc(sa + k * step_a, kStageHalf / 2),
                          tile_desc(sb + k * step_b, kStageHalf / 2), p.idesc, kb > 0 || k > 0);
               pair_commit(&sh.empty[s]);
+              if (++s == stages) s = 0, ++round;
             }
             if (ok) pair_commit(&sh.ready[acc]);
           }

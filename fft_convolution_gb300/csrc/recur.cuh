@@ -292,6 +292,11 @@ __device__ __forceinline__ Rows find_rows(const RecurArgs &a, long long seq) {
     r.len = a.tokens;
     return r;
   }
+  if (a.rows) {
+    r.begin = a.rows[seq];
+    r.len = a.rows[seq + 1] - r.begin;
+    return r;
+  }
   if (threadIdx.x < 2) found[threadIdx.x] = 0;
   __syncthreads();
   int m[2] = {0, 0};
@@ -716,6 +721,10 @@ cudaError_t launch_clusters(F *kern, RecurArgs a, const RecurMaps &maps, int tok
   const long long room =
       (long long)sm_count() * blocks_per_sm_once((const void *)kern, kRecurThreads, smem, resident);
   if (room <= 0) return cudaErrorInvalidDevice;
+  if (a.rows) {  // a block would read all offsets before its own
+    e = launch_delta_plan(a.offsets, a.batch, a.tokens, a.rows, a.rows + a.batch + 1, DeltaClear{}, st);
+    if (e != cudaSuccess) return e;
+  }
   // Sequences share a GPU of many SMs: more blocks along one while there is
   // room for them and it has tokens for them.
   const long long mean = a.offsets ? (a.tokens + a.batch - 1) / a.batch : a.tokens;

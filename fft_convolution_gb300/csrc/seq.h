@@ -168,6 +168,8 @@ struct RecurArgs {
   int channels;
   bool clear;  // packed rows of no sequence: results of 0
   int blocks;  // of a cluster, which share a sequence's tokens
+  int *rows;   // packed, many sequences: 2 (batch + 1) entries, the first half of which
+               // become the sequences' first rows; else null
   // Single tokens: the sequence's row of a pool of `pool` states (null: row = sequence).
   const int *slots;
   long long pool;
@@ -177,6 +179,7 @@ struct RecurArgs {
   void *dx, *dg, *dbeta;
   float *dinitial;  // may be null
 };
+size_t recur_workspace_bytes(long long batch, bool packed);
 // g and beta of type float where gfloat, else of type T.
 template <typename T> cudaError_t launch_recur(const RecurArgs &a, bool gfloat, cudaStream_t st);
 template <typename T>

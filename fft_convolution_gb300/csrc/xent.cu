@@ -99,7 +99,8 @@ struct XentTiles {
   int m, n;  // tiles of tokens and of words
   const void *targets;
   int target_bytes;
-  int width;  // words of a tile
+  int width;  // words of a tile (few tokens: tokens)
+  int part;   // words of a part
   // forward: per half a tile's words and token, largest logit and sum (both in powers of 2)
   float2 *partial;
   float *at_target;
@@ -112,6 +113,8 @@ struct XentTiles {
 };
 
 constexpr int kHalf = kPairTile / 2;  // columns of a lane, at most
+
+constexpr int kFewTokens = 128;  // up to here words are the rows of a tile
 
 // Tiles of all token blocks before the next words: x stays in the L2, W is read once.
 __device__ __forceinline__ PairTile word_tile(const XentTiles &p, int t, long long v0, int k) {
@@ -160,6 +163,51 @@ xent_sums_kernel(const __grid_constant__ PairOperands ops, const XentTiles p, in
   pair_run(&ops, p.m * p.n, status, of, out);
 }
 
+// The same for few tokens: tiles of 256 words x up to 128 tokens, so that a stage holds
+// little but words (W is all there is to read: 48 tokens, 65536 words, 4096 wide 105
+// -> FEWTIME us).  A lane's row is a word: 32 x 32 logits at a time turn in shared memory, after
+// which a lane has one token's.  Parts are of 32 words.
+__global__ void __launch_bounds__(kPairThreads, 1)
+xent_few_kernel(const __grid_constant__ PairOperands ops, const XentTiles p, int kblocks, int *status) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = (int)block_rank(), half = (warp - 4) >> 2;
+  auto of = [&](int t, int &) {
+    PairTile w{};
+    w.a_row = t * kPairTile;
+    w.k1 = kblocks;
+    return w;
+  };
+  auto out = [&](int t, float (&f)[kHalf]) {
+    const long long v0 = (long long)t * kPairTile + rank * 128 + (warp & 3) * 32;
+    if (v0 >= p.vocabulary) return;
+    const int count = (int)min(32ll, p.vocabulary - v0);
+    float *turn = pair_spare() + (warp - 4) * (32 * 33);
+    const int wide = p.width / 2;
+#pragma unroll
+    for (int j = 0; j < kHalf; j += 32)
+      if (j < wide && half * wide + j < p.tokens) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) turn[i * 33 + lane] = f[j + i];
+        __syncwarp();
+        const long long n = half * wide + j + lane;
+        if (n < p.tokens) {
+          const float *l = turn + lane * 33;
+          const long long target = target_of(p.targets, p.target_bytes, n) - v0;
+          if (target >= 0 && target < count) p.at_target[n] = l[target];
+          float top = -INFINITY, sum = 0.0f;
+          for (int i = 0; i < count; ++i) top = fmaxf(top, l[i]);
+          // all of them -infinity (or NaN): in units of 1
+          top = top == -INFINITY ? top : top * kLog2e;
+          const float unit = top == -INFINITY ? 0.0f : top;
+          for (int i = 0; i < count; ++i) sum += exp2_approx(fmaf(l[i], kLog2e, -unit));
+          p.partial[(v0 >> 5) * p.tokens + n] = make_float2(sum == 0.0f ? top : unit, sum);
+        }
+        __syncwarp();
+      }
+  };
+  pair_run(&ops, p.n, status, of, out);
+}
+
 // (m, s) + (m', s'): the sums in units of the larger power of two.
 __device__ __forceinline__ float2 join_sums(float2 a, float2 b) {
   const float m = fmaxf(a.x, b.x);
@@ -175,7 +223,7 @@ xent_join_kernel(const XentTiles p, float *loss, float *lse) {
   __shared__ float2 parts[kJoinTokens * kJoinParts / 32][kJoinTokens];
   const int at = threadIdx.x % kJoinTokens, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long n = (long long)blockIdx.x * kJoinTokens + at;
-  const int count = (int)((p.vocabulary + p.width / 2 - 1) / (p.width / 2));
+  const int count = (int)((p.vocabulary + p.part - 1) / p.part);
   float2 s = make_float2(-INFINITY, 0.0f);
   if (n < p.tokens) {
 #pragma unroll 4
@@ -515,6 +563,8 @@ struct Layout {
   Operand x, w;
   int parts;
   size_t partial, at_target;         // forward
+  bool few;
+  int part;                          // words of a part of lse
   int width, wide;                   // words and columns of dx and dw per tile
   long long piece;                   // words
   int pieces, slices;
@@ -527,7 +577,9 @@ struct Layout {
     x = operand(dtype, a.x, a.ldx, a.tokens, a.dim, grad);
     w = operand(dtype, a.w, a.ldw, a.vocabulary, a.dim, false);
     bytes = x.bytes + w.bytes;
-    width = tile_width(a.vocabulary, up(a.tokens, kPairTile));
+    few = !grad && a.tokens <= kFewTokens;
+    width = few ? (int)up(a.tokens, 64) * 64 : tile_width(a.vocabulary, up(a.tokens, kPairTile));
+    part = few ? 32 : width / 2;
     // columns: as few tiles as there are of 256, of even size
     wide = (int)up(up(a.dim, up(a.dim, kPairTile)), 64) * 64;
     partial = at_target = unit = g = sums = 0;
@@ -539,7 +591,7 @@ struct Layout {
       return at;
     };
     if (!grad) {
-      partial = take(2 * (size_t)up(a.vocabulary, width) * a.tokens * 8);
+      partial = take((size_t)up(a.vocabulary, part) * a.tokens * 8);
       at_target = take((size_t)a.tokens * 4);
       return;
     }
@@ -579,16 +631,16 @@ cudaError_t lay(const void *in, long long ld, long long rows, int dim, const Ope
   return cudaGetLastError();
 }
 
-template <typename K, typename... Args>
-cudaError_t pair_launch(K *kern, DeviceOnce &once, long long tiles, cudaStream_t st,
-                        const Args &...args) {
-  cudaError_t e = smem_limit_once((const void *)kern, kPairSmem, once);
+template <auto Kern, typename... Args>
+cudaError_t pair_launch(long long tiles, cudaStream_t st, const Args &...args) {
+  static DeviceOnce once;
+  cudaError_t e = smem_limit_once((const void *)Kern, kPairSmem, once);
   if (e != cudaSuccess) return e;
   // the split of registers counts on what a block is launched with
   static std::atomic<int> regs;
   if (regs.load(std::memory_order_acquire) == 0) {
     cudaFuncAttributes at;
-    e = cudaFuncGetAttributes(&at, (const void *)kern);
+    e = cudaFuncGetAttributes(&at, (const void *)Kern);
     if (e != cudaSuccess) return e;
     regs.store(at.numRegs, std::memory_order_release);
   }
@@ -606,7 +658,7 @@ cudaError_t pair_launch(K *kern, DeviceOnce &once, long long tiles, cudaStream_t
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, args...);
+  e = cudaLaunchKernelEx(&cfg, Kern, args...);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -650,8 +702,10 @@ cudaError_t xent_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st) {
   cudaError_t e = lay_both<T>(a, l, ws, false, xp, wp, st);
   if (e != cudaSuccess) return e;
   PairOperands ops{};
-  if (!make_map(&ops.a, half, xp, a.tokens, a.dim, l.x.ld, l.parts, 128) ||
-      !make_map(&ops.b, half, wp, a.vocabulary, a.dim, l.w.ld, l.parts, l.width / 2))
+  if (!make_map(l.few ? &ops.b : &ops.a, half, xp, a.tokens, a.dim, l.x.ld, l.parts,
+                l.few ? l.width / 2 : 128) ||
+      !make_map(l.few ? &ops.a : &ops.b, half, wp, a.vocabulary, a.dim, l.w.ld, l.parts,
+                l.few ? 128 : l.width / 2))
     return cudaErrorInvalidValue;
   ops.width = l.width;
   ops.b_bytes = (uint32_t)l.width / 2 * 128;
@@ -659,12 +713,13 @@ cudaError_t xent_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st) {
   ops.parts = l.parts;
   XentTiles t = tiles_of(a);
   t.width = l.width;
-  t.n = (int)up(a.vocabulary, l.width);
+  t.part = l.part;
+  t.n = (int)up(a.vocabulary, l.few ? kPairTile : l.width);
   t.partial = reinterpret_cast<float2 *>(ws + l.partial);
   t.at_target = reinterpret_cast<float *>(ws + l.at_target);
-  static DeviceOnce once;
-  e = pair_launch(xent_sums_kernel, once, (long long)t.m * t.n, st, ops, t, (int)up(a.dim, kPairK),
-                  status);
+  const int kblocks = (int)up(a.dim, kPairK);
+  e = l.few ? pair_launch<xent_few_kernel>(t.n, st, ops, t, kblocks, status)
+            : pair_launch<xent_sums_kernel>((long long)t.m * t.n, st, ops, t, kblocks, status);
   if (e != cudaSuccess) return e;
   xent_join_kernel<<<(unsigned)up(a.tokens, kJoinTokens), kJoinTokens * kJoinParts, 0, st>>>(t, a.loss,
                                                                                        a.lse);
@@ -722,21 +777,19 @@ cudaError_t xent_grad_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st)
   p.dw = a.dw;
   p.unit = unit;
   const int kblocks = (int)up(a.dim, kPairK);
-  static DeviceOnce once_g, once_p;
   for (int i = 0; i < l.pieces; ++i) {
     t.v0 = p.v0 = i * l.piece;
     if (t.v0 >= a.vocabulary) break;
     const long long words = a.vocabulary - t.v0 < l.piece ? a.vocabulary - t.v0 : l.piece;
     t.n = (int)up(words, l.width);
-    e = pair_launch(xent_grad_kernel<O, kParts>, once_g, (long long)t.m * t.n, st, ops, t, kblocks,
-                    status);
+    e = pair_launch<xent_grad_kernel<O, kParts>>((long long)t.m * t.n, st, ops, t, kblocks, status);
     if (e != cudaSuccess) return e;
     p.first = i == 0;
     p.words = words;
     p.k = (int)up(words, kPairK);
     p.wm = a.dw ? (int)up(words, kPairTile) : 0;
-    e = pair_launch(xent_products_kernel<T>, once_p,
-                    (long long)p.m * p.n * p.slices + (long long)p.wm * p.n, st, p, status);
+    e = pair_launch<xent_products_kernel<T>>(
+        (long long)p.m * p.n * p.slices + (long long)p.wm * p.n, st, p, status);
     if (e != cudaSuccess) return e;
   }
   if (!a.dx) return cudaSuccess;

@@ -479,6 +479,11 @@ def _recur_inputs(x, g, beta, batch, packed: bool, clear: bool = False):
     return x, g, beta, desc, device
 
 
+def _recur_workspace(desc, packed: bool, device):
+    nbytes = _lib.fft_linear_recurrence_workspace_bytes(desc, packed) if packed else 0
+    return (_workspace(nbytes, device) if nbytes else None), nbytes
+
+
 def linear_recurrence(x, g, beta=None, initial_state=None, offsets=None, out=None, stream=None):
     """(y, final state) of h <- e^g h + beta x over whole sequences, by channel
     (see fft_linear_recurrence); y holds every h.  x: [batch, tokens,
@@ -502,9 +507,10 @@ def linear_recurrence(x, g, beta=None, initial_state=None, offsets=None, out=Non
         elif out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous():
             raise ValueError("out must be contiguous and like x")
         final = torch.empty(shape, dtype=torch.float32, device=device)
+        ws, nbytes = _recur_workspace(desc, packed, device)
         _check(_lib.fft_linear_recurrence(desc, x.data_ptr(), g.data_ptr(), _ptr(beta), _ptr(offsets),
                                           _ptr(initial_state), out.data_ptr(), final.data_ptr(),
-                                          handle), "fft_linear_recurrence")
+                                          _ptr(ws), nbytes, handle), "fft_linear_recurrence")
     if given is not None:
         _changed(given)
     return out, final
@@ -534,10 +540,11 @@ def linear_recurrence_backward(dy, x, g, y, beta=None, initial_state=None, offse
         dg = torch.empty(x.shape, dtype=g.dtype, device=device)
         dbeta = None if beta is None else torch.empty(x.shape, dtype=g.dtype, device=device)
         dinitial = torch.empty(shape, dtype=torch.float32, device=device)
+        ws, nbytes = _recur_workspace(desc, packed, device)
         _check(_lib.fft_linear_recurrence_backward(
             desc, dy.data_ptr(), x.data_ptr(), g.data_ptr(), _ptr(beta), y.data_ptr(), _ptr(offsets),
             _ptr(initial_state), _ptr(dfinal_state), dx.data_ptr(), dg.data_ptr(), _ptr(dbeta),
-            dinitial.data_ptr(), handle), "fft_linear_recurrence_backward")
+            dinitial.data_ptr(), _ptr(ws), nbytes, handle), "fft_linear_recurrence_backward")
     return dx, dg, dbeta, dinitial
 
 

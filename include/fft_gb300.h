@@ -681,12 +681,17 @@ typedef struct fft_recurrence_desc {
  *   final_state    the same, written; may be NULL; may be initial_state.
  *   y              [batch][tokens][channels], or [tokens][channels] with
  *                  offsets; contiguous.
+ *   workspace      fft_linear_recurrence_workspace_bytes(desc, offsets != NULL) bytes
+ *                  (0, and none needed, except for many packed sequences).
  * Tokens are combined in an order that depends on the sizes alone.  A value that
- * is not finite spoils the later outputs of its sequence and channel.
+ * is not finite spoils the later outputs of its sequence and channel.  Where
+ * g > 0, products of decays end at float's largest value.
  */
+size_t fft_linear_recurrence_workspace_bytes(const fft_recurrence_desc *desc, int packed);
 int fft_linear_recurrence(const fft_recurrence_desc *desc, const void *x, const void *g,
                           const void *beta, const int32_t *offsets, const float *initial_state,
-                          void *y, float *final_state, void *stream);
+                          void *y, float *final_state, void *workspace, size_t workspace_bytes,
+                          void *stream);
 
 /*
  * fft_linear_recurrence_backward -- the gradients, from dy (contiguous, like
@@ -695,6 +700,7 @@ int fft_linear_recurrence(const fft_recurrence_desc *desc, const void *x, const 
  *                  dbeta and x are not used where beta is NULL.
  *   dfinal_state, dinitial_state  float [batch][channels]; dinitial_state may
  *                  be NULL, and may be dfinal_state.
+ *   workspace      as in fft_linear_recurrence.
  * dg takes the states as y holds them, rounded to its type.  No output overlaps
  * an input or another output except as said.
  */
@@ -702,7 +708,8 @@ int fft_linear_recurrence_backward(const fft_recurrence_desc *desc, const void *
                                    const void *g, const void *beta, const void *y,
                                    const int32_t *offsets, const float *initial_state,
                                    const float *dfinal_state, void *dx, void *dg, void *dbeta,
-                                   float *dinitial_state, void *stream);
+                                   float *dinitial_state, void *workspace,
+                                   size_t workspace_bytes, void *stream);
 
 /*
  * fft_linear_recurrence_step -- a few tokens per sequence (decoding): the

@@ -166,6 +166,32 @@ def test_packed(fg, channels, offsets, kind, gkind, gated):
         assert t is None or (not t[~used].any() and t.isfinite().all())
 
 
+@pytest.mark.parametrize("sequences", [1024, 1025, 3000])
+def test_many_packed_sequences(fg, sequences):
+    rng = np.random.default_rng(sequences)
+    lengths = rng.integers(0, 4, sequences)
+    ends = np.concatenate([[3], 3 + np.cumsum(lengths)])
+    tokens = int(ends[-1]) + 2
+    x, g, beta, _, dy, _ = inputs(12, (tokens, 36), torch.bfloat16, torch.float32, True)
+    h0 = torch.randn(sequences, 36, device="cuda")
+    at = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    y, final = fg.linear_recurrence(x, g, beta, initial_state=h0, offsets=at)
+    dx, dg, db, d0 = fg.linear_recurrence_backward(dy, x, g, y, beta=beta, initial_state=h0, offsets=at)
+    for t in (y, dx, dg, db):
+        assert not t[:3].any() and not t[-2:].any()
+    for i in rng.choice(sequences, 60, replace=False):
+        a, b = int(ends[i]), int(ends[i + 1])
+        (want, s, n), end = forward64(x[a:b], g[a:b], beta[a:b], h0[i])
+        within(final[i], end[0], U * (16 * end[1] + 6 * end[2]))
+        rows, last = backward64(dy[a:b], x[a:b], g[a:b], y[a:b], beta[a:b], h0[i], None)
+        within(d0[i], last[0], last[1])
+        if b > a:
+            within(y[a:b], want, U * (16 * s + 6 * n))
+            within(dx[a:b], rows[0], rows[1] + 4 * U * rows[0].abs())
+            within(dg[a:b], rows[2], rows[3])
+            within(db[a:b], rows[4], rows[5] + 4 * U * rows[4].abs())
+
+
 def test_clusters_agree_with_parts(fg):
     # one long sequence (blocks of a cluster share its tokens) against its pieces with carried states
     x, g, beta, h0, _, _ = inputs(3, (1, 4000, 96), torch.float32, torch.float32, True, 1)

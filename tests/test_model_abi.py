@@ -62,12 +62,13 @@ def desc(fg, **change):
     return d
 
 
-def forward(fg, d, x=P, g=P, beta=P, offsets=None, s0=None, y=P, s1=P):
-    return fg.fft_linear_recurrence(d, x, g, beta, offsets, s0, y, s1, None)
+def forward(fg, d, x=P, g=P, beta=P, offsets=None, s0=None, y=P, s1=P, ws=None, nbytes=0):
+    return fg.fft_linear_recurrence(d, x, g, beta, offsets, s0, y, s1, ws, nbytes, None)
 
 
-def backward(fg, d, dy=P, x=P, g=P, beta=P, y=P, offsets=None, s0=None, d1=None, dx=P, dg=P, db=P, d0=P):
-    return fg.fft_linear_recurrence_backward(d, dy, x, g, beta, y, offsets, s0, d1, dx, dg, db, d0, None)
+def backward(fg, d, dy=P, x=P, g=P, beta=P, y=P, offsets=None, s0=None, d1=None, dx=P, dg=P, db=P, d0=P, ws=None,
+             nbytes=0):
+    return fg.fft_linear_recurrence_backward(d, dy, x, g, beta, y, offsets, s0, d1, dx, dg, db, d0, ws, nbytes, None)
 
 
 def step(fg, d, x=P, g=P, beta=P, state=P, slots=None, pool=2, y=P):
@@ -113,7 +114,19 @@ def test_recurrence_step_refuses(fg):
     assert step(fg, d, state=None) == fg.FFT_ERR_INVALID_ARG
     assert step(fg, d, slots=P + 2) == fg.FFT_ERR_MISALIGNED
     assert step(fg, d, state=P + 2) == fg.FFT_ERR_MISALIGNED
-    assert fg._lib.fft_linear_recurrence(None, P, P, P, None, None, P, P, None) == fg.FFT_ERR_INVALID_ARG
+    assert fg._lib.fft_linear_recurrence(None, P, P, P, None, None, P, P, None, 0, None) == fg.FFT_ERR_INVALID_ARG
+
+
+def test_recurrence_workspaces(fg):
+    few, many = desc(fg, batch=1024), desc(fg, batch=1025)
+    size = fg.fft_linear_recurrence_workspace_bytes
+    assert size(few, 1) == 0 and size(many, 0) == 0 and size(desc(fg, channels=0), 1) == 0
+    need = size(many, 1)
+    assert need >= 1026 * 4
+    for call in (forward, backward):
+        assert call(fg, many, offsets=P, ws=P, nbytes=need - 1) == fg.FFT_ERR_INVALID_ARG
+        assert call(fg, many, offsets=P, nbytes=need) == fg.FFT_ERR_INVALID_ARG
+        assert call(fg, many, offsets=P, ws=P + 8, nbytes=need) == fg.FFT_ERR_MISALIGNED
 
 
 def test_recurrence_of_nothing(fg):
