@@ -341,13 +341,18 @@ struct RecurMaps {
 // Tokens of a warp per step, where a lane's loads of one take `bytes`: two stages
 // of tiles fill shared memory, one block per SM.  A step costs about 1500 clocks
 // beside its tokens, so many small ones lose (prompt of 32768 tokens, 4096
-// channels in bf16: 173 us with 16 tokens, 252 with 8, 301 with 4).
-constexpr int kRecurStages = 2;
-constexpr int recur_tokens(int bytes) { return bytes <= 24 ? 16 : bytes <= 48 ? 8 : 4; }
+// channels in bf16: 170 us with 16 tokens, 252 with 8, 301 with 4).  SHORT sequences
+// are all start and end: small tiles, two blocks per SM (4096 sequences of 16 tokens,
+// 1024 channels: 743 -> 273 us, 512 of 64 107 -> 63, 256 of 128 65 -> 57, but 64 of
+// 1024 92 -> 104).
+constexpr int kRecurStages = 2, kRecurShort = 192;
+constexpr int recur_tokens(int bytes, bool is_short) {
+  return is_short ? (bytes <= 40 ? 4 : 2) : bytes <= 24 ? 16 : bytes <= 48 ? 8 : 4;
+}
 
 // T: x and y; G: g and beta.
-template <typename T, typename G, bool GATED> struct RecurForward {
-  static constexpr int K = recur_tokens(4 * (int)(sizeof(T) + sizeof(G) * (GATED ? 2 : 1)));
+template <typename T, typename G, bool GATED, bool SHORT> struct RecurForward {
+  static constexpr int K = recur_tokens(4 * (int)(sizeof(T) + sizeof(G) * (GATED ? 2 : 1)), SHORT);
   static constexpr int kTokens = kRecurWarps * K, S = kRecurStages;
   struct Stage {
     alignas(128) Four<T> x[kTokens][32];
@@ -358,10 +363,10 @@ template <typename T, typename G, bool GATED> struct RecurForward {
   static constexpr uint32_t kBytes = kTokens * 128 * (sizeof(T) + sizeof(G) * (GATED ? 2 : 1));
   static constexpr size_t kSmem = 128 + kRecurShared + S * sizeof(Stage);
 };
-template <typename T, typename G, bool VEC, bool GATED>
-__global__ void __launch_bounds__(kRecurThreads)
+template <typename T, typename G, bool VEC, bool GATED, bool SHORT>
+__global__ void __launch_bounds__(kRecurThreads, SHORT ? 2 : 1)
 recur_kernel(const RecurArgs a, const __grid_constant__ RecurMaps maps, int *status) {
-  using P = RecurForward<T, G, GATED>;
+  using P = RecurForward<T, G, GATED, SHORT>;
   constexpr int K = P::K, S = P::S;
   using LT = Lane4<T, VEC>;
   using LG = Lane4<G, VEC>;
@@ -469,10 +474,10 @@ recur_kernel(const RecurArgs a, const __grid_constant__ RecurMaps maps, int *sta
 
 // The same from the end: tile n has the tokens behind those of tile n + 1, and a
 // warp's j-th token is the j-th from its end.
-template <typename T, typename G, bool GATED> struct RecurBackward {
+template <typename T, typename G, bool GATED, bool SHORT> struct RecurBackward {
   // more than 8 would not leave registers for both factors of a token
   static constexpr int kMost =
-      recur_tokens(4 * (int)(sizeof(T) * (GATED ? 3 : 2) + sizeof(G) * (GATED ? 2 : 1)));
+      recur_tokens(4 * (int)(sizeof(T) * (GATED ? 3 : 2) + sizeof(G) * (GATED ? 2 : 1)), SHORT);
   static constexpr int K = kMost < 8 ? kMost : 8;
   static constexpr int kTokens = kRecurWarps * K, S = kRecurStages;
   struct Stage {
@@ -489,10 +494,10 @@ template <typename T, typename G, bool GATED> struct RecurBackward {
       kTokens * 128 * (sizeof(T) * (GATED ? 3 : 2) + sizeof(G) * (GATED ? 2 : 1));
   static constexpr size_t kSmem = 128 + kRecurShared + S * sizeof(Stage);
 };
-template <typename T, typename G, bool VEC, bool GATED>
-__global__ void __launch_bounds__(kRecurThreads)
+template <typename T, typename G, bool VEC, bool GATED, bool SHORT>
+__global__ void __launch_bounds__(kRecurThreads, SHORT ? 2 : 1)
 recur_grad_kernel(const RecurArgs a, const __grid_constant__ RecurMaps maps, int *status) {
-  using P = RecurBackward<T, G, GATED>;
+  using P = RecurBackward<T, G, GATED, SHORT>;
   constexpr int K = P::K, S = P::S;
   using LT = Lane4<T, VEC>;
   using LG = Lane4<G, VEC>;
@@ -748,16 +753,28 @@ cudaError_t launch_clusters(F *kern, RecurArgs a, const RecurMaps &maps, int tok
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <typename T, typename G, bool VEC, bool GATED>
-cudaError_t recur_whole(bool grad, const RecurArgs &a, const RecurMaps &maps, cudaStream_t st) {
-  static DeviceOnce once[2];
-  static std::atomic<int> resident[2][64];
-  using F = RecurForward<T, G, GATED>;
-  using B = RecurBackward<T, G, GATED>;
-  return grad ? launch_clusters(&recur_grad_kernel<T, G, VEC, GATED>, a, maps, B::kTokens, B::kSmem,
-                                once[1], resident[1], st)
-              : launch_clusters(&recur_kernel<T, G, VEC, GATED>, a, maps, F::kTokens, F::kSmem,
-                                once[0], resident[0], st);
+template <typename T, typename G, bool GATED, bool SHORT>
+cudaError_t recur_whole(bool grad, const RecurArgs &a, cudaStream_t st) {
+  using F = RecurForward<T, G, GATED, SHORT>;
+  using B = RecurBackward<T, G, GATED, SHORT>;
+  RecurMaps maps{};
+  const RecurStride own{a.tokens * a.channels, a.channels};
+  const int tokens = grad ? B::kTokens : F::kTokens;
+  const size_t smem = grad ? B::kSmem : F::kSmem;
+  bool vec = quads<T>(a.y) && recur_map<G>(&maps.g, a.g, a.sg, a, tokens);
+  if (GATED) vec = vec && recur_map<G>(&maps.b, a.beta, a.sb, a, tokens);
+  if (GATED || !grad) vec = vec && recur_map<T>(&maps.x, a.x, a.sx, a, tokens);
+  if (grad)
+    vec = vec && quads<T>(a.dx) && quads<G>(a.dg) && quads<G>(a.dbeta) &&
+          recur_map<T>(&maps.d, a.dy, own, a, tokens) && recur_map<T>(&maps.y, a.y, own, a, tokens);
+  static DeviceOnce once[4];
+  static std::atomic<int> resident[4][64];
+  auto kern = grad ? (vec ? &recur_grad_kernel<T, G, true, GATED, SHORT>
+                          : &recur_grad_kernel<T, G, false, GATED, SHORT>)
+                   : (vec ? &recur_kernel<T, G, true, GATED, SHORT>
+                          : &recur_kernel<T, G, false, GATED, SHORT>);
+  const int which = (grad ? 2 : 0) + (vec ? 1 : 0);
+  return launch_clusters(kern, a, maps, tokens, smem, once[which], resident[which], st);
 }
 template <typename T, typename G, bool GATED>
 cudaError_t recur_kind(int what, const RecurArgs &a, cudaStream_t st) {
@@ -773,18 +790,9 @@ cudaError_t recur_kind(int what, const RecurArgs &a, cudaStream_t st) {
     else recur_step_kernel<T, G, false, GATED><<<grid, 128, 0, st>>>(a);
     return cudaGetLastError();
   }
-  RecurMaps maps{};
-  const RecurStride own{a.tokens * a.channels, a.channels};
-  const bool grad = what == 1;
-  const int tokens = grad ? RecurBackward<T, G, GATED>::kTokens : RecurForward<T, G, GATED>::kTokens;
-  bool vec = quads<T>(a.y) && recur_map<G>(&maps.g, a.g, a.sg, a, tokens);
-  if (GATED) vec = vec && recur_map<G>(&maps.b, a.beta, a.sb, a, tokens);
-  if (GATED || !grad) vec = vec && recur_map<T>(&maps.x, a.x, a.sx, a, tokens);
-  if (grad)
-    vec = vec && quads<T>(a.dx) && quads<G>(a.dg) && quads<G>(a.dbeta) &&
-          recur_map<T>(&maps.d, a.dy, own, a, tokens) && recur_map<T>(&maps.y, a.y, own, a, tokens);
-  return vec ? recur_whole<T, G, true, GATED>(grad, a, maps, st)
-             : recur_whole<T, G, false, GATED>(grad, a, maps, st);
+  const long long mean = a.offsets ? a.tokens / a.batch : a.tokens;
+  return mean <= kRecurShort ? recur_whole<T, G, GATED, true>(what == 1, a, st)
+                             : recur_whole<T, G, GATED, false>(what == 1, a, st);
 }
 template <typename T, typename G> cudaError_t recur_t(int what, const RecurArgs &a, cudaStream_t st) {
   return a.beta ? recur_kind<T, G, true>(what, a, st) : recur_kind<T, G, false>(what, a, st);

@@ -166,6 +166,19 @@ def test_packed(fg, channels, offsets, kind, gkind, gated):
         assert t is None or (not t[~used].any() and t.isfinite().all())
 
 
+@pytest.mark.parametrize("kind,gkind,gated", KINDS)
+@pytest.mark.parametrize("channels", [136, 45])
+def test_long_packed(fg, channels, kind, gkind, gated):
+    # sequences of different lengths of several steps, and rows of none on both sides
+    offsets = [5, 700, 701, 701, 1990]
+    x, g, beta, _, dy, _ = inputs(13, (2000, channels), TYPES[kind], TYPES[gkind], gated)
+    at = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    h0 = torch.randn(4, channels, device="cuda")
+    check(fg, (x, g, beta, h0, dy, None), bounds_of(4, offsets, 2000), at)
+    y, _ = fg.linear_recurrence(x, g, beta, offsets=at)
+    assert not y[:5].any() and not y[1990:].any()
+
+
 @pytest.mark.parametrize("sequences", [1024, 1025, 3000])
 def test_many_packed_sequences(fg, sequences):
     rng = np.random.default_rng(sequences)
