@@ -48,26 +48,37 @@ struct LiveRows {
   long long vocabulary;
   const float *dloss;
 };
-// Rows of ld elements as `PARTS` arrays of rows of ldo, whole 16 bytes; rows
-// that do not count are 0.  A thread makes eight elements at a time.
+// One operand: rows of ld elements, `vec`: on boundaries of 16 bytes.
+template <typename T, typename O> struct LayRows {
+  const T *in;
+  long long ld, rows;
+  O *out;
+  int ldo;
+  bool vec;
+};
+// Rows as `PARTS` arrays of rows of ldo elements, whole 16 bytes; those of x that do not
+// count are 0.  x and W in one launch (either may have no rows); a thread makes
+// eight elements at a time.
 template <typename T, typename O, int PARTS>
-__global__ void __launch_bounds__(256) xent_lay_kernel(const T *in, long long ld, long long rows,
-                                                       int dim, O *out, int ldo, bool vec,
-                                                       LiveRows live) {
-  for (long long r = (long long)blockIdx.x * blockDim.y + threadIdx.y; r < rows;
-       r += (long long)gridDim.x * blockDim.y) {
+__global__ void __launch_bounds__(256) xent_lay_kernel(const LayRows<T, O> x, const LayRows<T, O> w,
+                                                       int dim, LiveRows live) {
+  for (long long at = (long long)blockIdx.x * blockDim.y + threadIdx.y; at < x.rows + w.rows;
+       at += (long long)gridDim.x * blockDim.y) {
+    const bool mine = at < x.rows;
+    const LayRows<T, O> &o = mine ? x : w;
+    const long long r = mine ? at : at - x.rows;
     int wide = dim;
-    if (live.targets) {
+    if (mine && live.targets) {
       const long long t = target_of(live.targets, live.target_bytes, r);
       if (t < 0 || t >= live.vocabulary || live.dloss[r] == 0.0f) wide = 0;
     }
 #pragma unroll 4
-    for (int c = 8 * threadIdx.x; c < ldo; c += 8 * blockDim.x) {
-      const T *src = in + r * ld + c;
-      O *dst = out + r * ldo + c;
+    for (int c = 8 * threadIdx.x; c < o.ldo; c += 8 * blockDim.x) {
+      const T *src = o.in + r * o.ld + c;
+      O *dst = o.out + r * o.ldo + c;
       if constexpr (PARTS == 1) {
         alignas(16) T v[8];
-        if (vec && c + 8 <= wide) {
+        if (o.vec && c + 8 <= wide) {
           *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(src);
         } else {
 #pragma unroll
@@ -80,7 +91,7 @@ __global__ void __launch_bounds__(256) xent_lay_kernel(const T *in, long long ld
         for (int i = 0; i < 8; ++i) v[i] = c + i < wide ? src[i] : 0.0f;
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
-          *reinterpret_cast<uint4 *>(dst + (long long)p * rows * ldo) = pack<O>(v);
+          *reinterpret_cast<uint4 *>(dst + (long long)p * o.rows * o.ldo) = pack<O>(v);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float h = to_acc(from_acc<O>(v[i]));
@@ -165,7 +176,7 @@ xent_sums_kernel(const __grid_constant__ PairOperands ops, const XentTiles p, in
 
 // The same for few tokens: tiles of 256 words x up to 128 tokens, so that a stage holds
 // little but words (W is all there is to read: 48 tokens, 65536 words, 4096 wide 105
-// -> FEWTIME us).  A lane's row is a word: 32 x 32 logits at a time turn in shared memory, after
+// -> 98 us).  A lane's row is a word: 32 x 32 logits at a time turn in shared memory, after
 // which a lane has one token's.  Parts are of 32 words.
 __global__ void __launch_bounds__(kPairThreads, 1)
 xent_few_kernel(const __grid_constant__ PairOperands ops, const XentTiles p, int kblocks, int *status) {
@@ -545,7 +556,7 @@ Operand operand(int dtype, const void *p, long long ld, long long rows, int dim,
 
 // Words per tile: the width that takes the pairs the least time, in rounds of all of
 // them, where a tile costs as much as 32 columns beside its own (its first loads; at
-// many rounds that leaves 256).  777 tokens of 10007 words: 63 -> WIDTH_ODD us for G.
+// many rounds that leaves 256).  777 tokens of 10007 words: 63 -> 52 us for G in fp32.
 int tile_width(long long words, long long m) {
   const long long pairs = sm_count() > 1 ? sm_count() / 2 : 1;
   long long best = 0, least = 0;
@@ -613,24 +624,6 @@ struct Layout {
   }
 };
 
-template <typename T>
-cudaError_t lay(const void *in, long long ld, long long rows, int dim, const Operand &o, void *out,
-                const LiveRows &live, cudaStream_t st) {
-  const int tx = o.ld >= 512 ? 64 : 16;
-  const dim3 block(tx, 256 / tx);
-  const bool vec = ((uintptr_t)in & 15) == 0 && ld % 8 == 0;
-  const long long need = up(rows, 256 / tx), most = (long long)sm_count() * 16;
-  const unsigned grid = (unsigned)(need < most ? need : most);
-  if constexpr (sizeof(T) == 4)
-    xent_lay_kernel<float, __nv_bfloat16, 3><<<grid, block, 0, st>>>(
-        static_cast<const float *>(in), ld, rows, dim, static_cast<__nv_bfloat16 *>(out), (int)o.ld,
-        false, live);
-  else
-    xent_lay_kernel<T, T, 1><<<grid, block, 0, st>>>(static_cast<const T *>(in), ld, rows, dim,
-                                                     static_cast<T *>(out), (int)o.ld, vec, live);
-  return cudaGetLastError();
-}
-
 template <auto Kern, typename... Args>
 cudaError_t pair_launch(long long tiles, cudaStream_t st, const Args &...args) {
   static DeviceOnce once;
@@ -670,14 +663,23 @@ template <> struct Part<float> { using type = __nv_bfloat16; };
 template <typename T>
 cudaError_t lay_both(const XentArgs &a, const Layout &l, char *ws, bool grad, const void *&xp,
                      const void *&wp, cudaStream_t st) {
-  const LiveRows all{}, live{a.targets, a.target_bytes, a.vocabulary, a.dloss};
+  using O = typename Part<T>::type;
   xp = l.x.own ? ws : a.x;
   wp = l.w.own ? ws + l.x.bytes : a.w;
-  cudaError_t e = cudaSuccess;
-  if (l.x.own) e = lay<T>(a.x, a.ldx, a.tokens, a.dim, l.x, ws, grad ? live : all, st);
-  if (e == cudaSuccess && l.w.own)
-    e = lay<T>(a.w, a.ldw, a.vocabulary, a.dim, l.w, ws + l.x.bytes, all, st);
-  return e;
+  if (!l.x.own && !l.w.own) return cudaSuccess;
+  const LiveRows all{}, live{a.targets, a.target_bytes, a.vocabulary, a.dloss};
+  auto rows = [](const void *in, long long ld, long long n, const Operand &o, char *out) {
+    return LayRows<T, O>{static_cast<const T *>(in), ld, o.own ? n : 0, reinterpret_cast<O *>(out),
+                         (int)o.ld, ((uintptr_t)in & 15) == 0 && ld % 8 == 0};
+  };
+  const LayRows<T, O> x = rows(a.x, a.ldx, a.tokens, l.x, ws);
+  const LayRows<T, O> w = rows(a.w, a.ldw, a.vocabulary, l.w, ws + l.x.bytes);
+  const int tx = a.dim >= 512 ? 64 : 16;
+  const long long need = up(x.rows + w.rows, 256 / tx), most = (long long)sm_count() * 16;
+  xent_lay_kernel<T, O, sizeof(T) == 4 ? 3 : 1>
+      <<<(unsigned)(need < most ? need : most), dim3(tx, 256 / tx), 0, st>>>(x, w, a.dim,
+                                                                             grad ? live : all);
+  return cudaGetLastError();
 }
 
 XentTiles tiles_of(const XentArgs &a) {
