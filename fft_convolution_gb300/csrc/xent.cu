@@ -380,7 +380,7 @@ struct XentProducts {
 };
 
 // 32 columns from c on of a warp's 32 rows (a lane has one) into an array of rows of
-// dim elements, + what is there.  Rows on 16-byte boundaries: each lane its own;
+// dim elements, + what is there.  Rows on 32-byte boundaries: each lane its own;
 // others: a row at a time, through shared memory (each lane writing its row by
 // elements took half the time of 777 tokens, 333 wide).
 template <typename T>
@@ -392,18 +392,23 @@ __device__ __forceinline__ void put_rows(T *out, long long row0, long long rows,
     if (row0 + lane >= rows) return;
     T *row = out + (row0 + lane) * dim + c;
 #pragma unroll
-    for (int j = 0; j < 32 / P; ++j) {
-      if (c + j * P < dim) {
-        float v[P];
+    for (int j = 0; j < 32; j += 2 * P) {
+      if (c + j < dim) {
+        uint4 w[2];
 #pragma unroll
-        for (int i = 0; i < P; ++i) v[i] = f[j * P + i];
-        if (add) {
-          float o[P];
-          unpack<T>(reinterpret_cast<const uint4 *>(row)[j], o);
+        for (int h = 0; h < 2; ++h) {
+          float v[P];
 #pragma unroll
-          for (int i = 0; i < P; ++i) v[i] += o[i];
+          for (int i = 0; i < P; ++i) v[i] = f[j + h * P + i];
+          if (add) {
+            float o[P];
+            unpack<T>(*reinterpret_cast<const uint4 *>(row + j + h * P), o);
+#pragma unroll
+            for (int i = 0; i < P; ++i) v[i] += o[i];
+          }
+          w[h] = pack<T>(v);
         }
-        reinterpret_cast<uint4 *>(row)[j] = pack<T>(v);
+        store32(row + j, w[0], w[1]);
       }
     }
     return;
@@ -465,9 +470,9 @@ xent_products_kernel(const __grid_constant__ XentProducts p, int *status) {
         const int c = c0 + j;
         if (which == 0) {
           put_rows<float>(p.sums + (long long)(t / mn) * p.tokens * p.dim, r0, p.tokens, c, p.dim,
-                          p.dim % 4 == 0, !p.first, q, turn);
+                          p.dim % 8 == 0, !p.first, q, turn);
         } else {
-          const bool vec = p.dim % (16 / (int)sizeof(T)) == 0 && ((uintptr_t)p.dw & 15) == 0;
+          const bool vec = p.dim * (int)sizeof(T) % 32 == 0 && ((uintptr_t)p.dw & 31) == 0;
           put_rows<T>(static_cast<T *>(p.dw) + p.v0 * p.dim, r0, p.words, c, p.dim, vec, false, q, turn);
         }
       }
