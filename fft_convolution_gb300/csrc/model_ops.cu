@@ -138,6 +138,8 @@ int fft_embedding_backward(const void *dy, int64_t lddy, const void *ids, int id
     return FFT_ERR_INVALID_ARG;
   if (ttype != dtype && (ttype != FFT_ELEM_F32 || dtype == FFT_ELEM_F64))
     return FFT_ERR_UNSUPPORTED;
+  // a block per four pieces of 16 tokens x 128 columns
+  if ((tokens + 15) / 16 > 4 * kMaxInt / ((dim + 63) / 64)) return FFT_ERR_UNSUPPORTED;
   if (off_element(dtable, ttype)) return FFT_ERR_MISALIGNED;
   if (tokens > 0) {
     if (!dy || !ids || lddy < dim || !workspace ||

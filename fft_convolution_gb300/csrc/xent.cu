@@ -542,7 +542,8 @@ bool make_map(CUtensorMap *map, bool half, const void *p, long long rows, long l
   EncodeFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
-  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * (cuuint64_t)rows};
+  // one part has no stride between parts, whatever its size
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * (cuuint64_t)(parts > 1 ? rows : 1)};
   const cuuint32_t shape[3] = {64, (cuuint32_t)box, 1}, ones[3] = {1, 1, 1};
   return fn(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
             const_cast<void *>(p), dims, strides, shape, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -451,8 +451,8 @@ int fft_debug_set_option(int option, int64_t value);
  * allocated or synchronised, every call can be captured into a CUDA graph.
  * Array pointers are aligned to their elements (else FFT_ERR_MISALIGNED);
  * 16-byte aligned rows run faster.  Results do not depend on timing (sums are
- * added in a fixed order; the only atomic operations take a maximum): the same
- * call on the same inputs gives the same bits.
+ * added in a fixed order; atomic operations take a maximum or hand out work): the
+ * same call on the same inputs gives the same bits.
  */
 
 /* Element types of their arrays. */
@@ -631,6 +631,7 @@ int fft_delta_rule_step(const fft_delta_desc *desc, const void *q, const void *k
  *              rounded once.
  *   tokens     0 .. 2^31 - 64 (0: nothing is done); rows 1 .. 2^31 - 1;
  *              dim 1 .. 2^30.
+ * y does not overlap table or ids.
  */
 int fft_embedding(const void *ids, int id_bytes, const void *table, int64_t ldt, void *y,
                   int64_t ldy, int64_t tokens, int64_t rows, int64_t dim, double scale, int dtype,
@@ -645,7 +646,9 @@ int fft_embedding(const void *ids, int id_bytes, const void *table, int64_t ldt,
  *              contiguous.  add = 0: every row is written, 0 where no token
  *              names it.  add != 0: the sums are added to what is there, and
  *              rows that no token names are left alone.
- *   workspace  fft_embedding_workspace_bytes(tokens, dim, dtype) bytes.
+ *   workspace  fft_embedding_workspace_bytes(tokens, dim, dtype) bytes: 16.25 per
+ *              token, and two accumulators per column and 16 tokens.
+ * dtable does not overlap dy or ids.
  */
 size_t fft_embedding_workspace_bytes(int64_t tokens, int64_t dim, int dtype);
 int fft_embedding_backward(const void *dy, int64_t lddy, const void *ids, int id_bytes,
@@ -737,8 +740,10 @@ int fft_linear_recurrence_step(const fft_recurrence_desc *desc, const void *x, c
  *   workspace  fft_linear_cross_entropy_workspace_bytes(..., backward = 0) bytes:
  *              8 per token and 128 words, and copies of float operands and of
  *              those whose rows do not lie on 16-byte boundaries.
- * Products of 16-bit operands are exact and added in float; float operands keep
- * 24 significand bits as three bfloat16 values each.
+ * Products of 16-bit operands are exact; float operands keep 24 significand bits as
+ * three bfloat16 values each.  Sums are float: 512 terms at a time on the tensor
+ * cores, whose additions are cut off (7e-7 too small where all terms have one sign),
+ * these sums rounded to nearest.  Outputs overlap no inputs.
  *
  * fft_linear_cross_entropy_backward -- its gradients, from the gradient dloss of
  * the losses (float) and the forward call's lse:

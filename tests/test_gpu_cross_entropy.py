@@ -220,6 +220,37 @@ def test_gradient_against_differences(fg):
     assert abs(got - want) <= 1e-5 * float((dx * vx).abs().sum() + (dw * vw).abs().sum())
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_long_sums_of_one_sign(fg, kind):
+    # An addition of 16 terms on the tensor cores may cut off 2^-23 of the sum so far: 32 of them in 512
+    # terms (float: six products of parts, of which only one is not small), then sums rounded to nearest.
+    bound = lambda terms: 40 * 2.0 ** -23 + (terms / 512 + 8) * 2.0 ** -24  # noqa: E731
+    x = torch.rand(70, 16384, device="cuda").to(TYPES[kind])
+    w = (torch.rand(1, 16384, device="cuda") / 16384).to(TYPES[kind])
+    lse = fg.linear_cross_entropy(x, w, torch.zeros(70, dtype=torch.int64, device="cuda"))[1]
+    want = (x.double() @ w.double().t())[:, 0]
+    assert ((lse.double() / want - 1).abs() <= bound(16384)).all()
+    # dw over tokens: two words of equal weight, all targets the first
+    x = torch.rand(20000, 40, device="cuda").to(TYPES[kind])
+    w, targets = torch.zeros(2, 40, device="cuda").to(TYPES[kind]), torch.zeros(20000, dtype=torch.int64, device="cuda")
+    dloss = torch.full((20000,), 2.0 ** -10, device="cuda")
+    dw = fg.linear_cross_entropy_backward(dloss, x, w, targets, fg.linear_cross_entropy(x, w, targets)[1])[1]
+    want = 2.0 ** -11 * x.double().sum(0)
+    step = torch.finfo(TYPES[kind]).eps / 2 if kind != "f32" else 0
+    assert ((dw[1].double() / want - 1).abs() <= bound(20000) + 2.0 ** -20 + step).all()
+    # dx over words: equal logits of 0, the target's weights 0, the others positive
+    w = torch.rand(30000, 40, device="cuda").to(TYPES[kind])
+    w[0] = 0
+    x = torch.zeros(9, 40, device="cuda").to(TYPES[kind])
+    targets = torch.zeros(9, dtype=torch.int64, device="cuda")
+    lse = fg.linear_cross_entropy(x, w, targets)[1]
+    dx = fg.linear_cross_entropy_backward(torch.ones(9, device="cuda"), x, w, targets, lse)[0]
+    p = torch.exp(-lse.double())[:, None]
+    if kind == "bf16":  # one rounding of every p alike
+        p = p.to(TYPES[kind]).double()
+    assert ((dx.double() / (p * w.double().sum(0)) - 1).abs() <= bound(30000) + 2.0 ** -20 + step).all()
+
+
 def test_nothing_and_refusals(fg):
     x, w, targets, dloss = inputs(10, 10, 20, 16, "f32")
     loss, lse = fg.linear_cross_entropy(x[:0], w, targets[:0])

@@ -38,7 +38,7 @@ def grad(fg, dy=P, lddy=8, ids=P, id_bytes=8, dtable=P, tokens=2, rows=5, dim=8,
 @pytest.mark.parametrize("change,status", SIZES + [
     (dict(dy=None), 1), (dict(ids=None), 1), (dict(dtable=None), 1), (dict(ws=None), 1), (dict(lddy=7), 1), (dict(ttype=9), 1),
     (dict(nbytes=100), 1), (dict(dtype=0, ttype=2), 3), (dict(dtype=2, ttype=3), 3), (dict(dtype=1, ttype=0), 3),
-    (dict(lddy=2 ** 62), 3), (dict(dtable=P + 2), 6), (dict(ws=P + 8), 6), (dict(dy=P + 2), 6), (dict(ids=P + 4), 6)])
+    (dict(lddy=2 ** 62), 3), (dict(tokens=2 ** 30, dim=2 ** 15, lddy=2 ** 15), 3), (dict(dtable=P + 2), 6), (dict(ws=P + 8), 6), (dict(dy=P + 2), 6), (dict(ids=P + 4), 6)])
 def test_embedding_backward_refuses(fg, change, status):
     assert grad(fg, **change) == status
 
