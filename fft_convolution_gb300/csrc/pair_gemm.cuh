@@ -4,18 +4,20 @@
 // finished tile.
 //
 // A cluster of two blocks works on one tile of 256 x 256 (or fewer columns, where
-// that fills the GPU better): each block stages 128 rows of A and half of B's
-// per 64 summed indexes (32 KB; six stages, more of narrower tiles), and gets the tile's 128 upper or lower
-// rows as fp32.
+// that fills the GPU better): each block stages 128 rows of A and half of B's per
+// 64 summed indexes (32 KB; six stages, more of narrower tiles), and gets the
+// tile's upper or lower 128 rows.  The pair is what lets the tensor cores run: a
+// block alone would have to load twice the bytes of B per product, 96 bytes per
+// clock and SM at the full rate, which the L2 does not deliver to all SMs at once;
+// so it is 64.  Measured: 2.2 * 10^12 operations of 8192 x 65536 x 2048 in 1.01 ms
+// (2.18 PFLOP/s) alone; 1.61 in a training step under the power cap, where cuBLAS
+// sustains 1.70.
 //
 // The tensor cores cut the sum off at every addition (toward zero): 4096 positive
 // terms come out 1.1e-5 too small, 16384 7e-5.  So tensor memory only ever holds the
 // sum over kSumBlocks blocks; what reads the tiles out adds these in registers,
-// rounded to nearest, 128 columns of a row per lane.  Two such sums fit: one is
-// made while the other is read.  The pair is what
-// lets the tensor cores run: a block alone would have to load twice the bytes
-// of B per product (96 bytes per clock and SM at the full rate, which the L2
-// does not deliver to all SMs at once; so it is 64).
+// rounded to nearest, up to 128 columns of a row per lane.  Two such sums fit: one is
+// made while the other is read.
 //
 // Warp 0 issues the loads (TMA, 128-byte swizzle), warp 1 of the even block
 // the products, warps 4 to 11 read the sums out, half the columns to each four.
@@ -31,7 +33,9 @@ namespace fftgb {
 
 constexpr int kPairTile = 256, kPairK = 64, kPairStages = 10;  // stages at most
 constexpr int kPairThreads = 384, kOutWarps = 8;
-constexpr int kSumBlocks = 8;  // sums of 512 terms: 7e-7 too small at most, 1% of the time
+// Sums of 512 terms: 7e-7 too small at most, for 1 to 2% of the time (8192 tokens with
+// gradients: 5.52 ms with 1024 terms, 5.57 with 512, 5.83 with 256).
+constexpr int kSumBlocks = 8;
 constexpr uint32_t kStageHalf = 128 * 128;  // bytes of A (of B) per stage and block
 // the stages, and behind them 32 x 33 floats for each of the warps that read tiles out
 constexpr uint32_t kPairStageBytes = 6 * 2 * kStageHalf;
@@ -231,10 +235,13 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
             }
           }
         }
-        if (*failed && rank == 0)  // given up: no copy may land after the blocks have gone
-          for (uint32_t i = 0; i < stages; ++i)
-            if (i < s) bar_wait(&sh.full[i], round & 1);
-            else if (round > 0) bar_wait(&sh.full[i], (round - 1) & 1);
+        // no copy, and no arrival of a completed product, may land after a block has gone
+        for (uint32_t i = 0; i < stages; ++i) {
+          if (i >= s && round == 0) break;
+          const uint32_t last = (i < s ? round : round - 1) & 1;
+          if (ok) wait_pair(&sh.empty[i], last, failed, status);
+          else if (rank == 0) bar_wait(&sh.full[i], last);
+        }
       }
     } else if (warp == 1 && rank == 0) {
       if (elect_one()) {
