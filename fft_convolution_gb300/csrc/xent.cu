@@ -91,12 +91,15 @@ __global__ void __launch_bounds__(256) xent_lay_kernel(const LayRows<T, O> x, co
         for (int i = 0; i < 8; ++i) v[i] = c + i < wide ? src[i] : 0.0f;
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
-          *reinterpret_cast<uint4 *>(dst + (long long)p * o.rows * o.ldo) = pack<O>(v);
+          float h[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float h = to_acc(from_acc<O>(v[i]));
-            v[i] = isfinite(h) ? v[i] - h : 0.0f;
+            h[i] = to_acc(from_acc<O>(v[i]));
+            // float's largest values round to infinity: cut off instead
+            if (isinf(h[i]) && isfinite(v[i])) h[i] = __uint_as_float(__float_as_uint(v[i]) & 0xffff0000u);
+            v[i] = isfinite(h[i]) ? v[i] - h[i] : 0.0f;
           }
+          *reinterpret_cast<uint4 *>(dst + (long long)p * o.rows * o.ldo) = pack<O>(h);
         }
       }
     }

@@ -741,7 +741,8 @@ int fft_linear_recurrence_step(const fft_recurrence_desc *desc, const void *x, c
  *              8 per token and 128 words, and copies of float operands and of
  *              those whose rows do not lie on 16-byte boundaries.
  * Products of 16-bit operands are exact; float operands keep 24 significand bits as
- * three bfloat16 values each.  Sums are float: 512 terms at a time on the tensor
+ * three bfloat16 values each (an infinite element gives NaN; finite ones of any size
+ * do not).  Sums are float: 512 terms at a time on the tensor
  * cores, whose additions are cut off (7e-7 too small where all terms have one sign),
  * these sums rounded to nearest.  Outputs overlap no inputs.
  *

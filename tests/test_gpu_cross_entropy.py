@@ -188,6 +188,31 @@ def test_words_that_cannot_be(fg):
 
 
 @pytest.mark.parametrize("kind", list(TYPES))
+def test_words_masked_by_the_lowest_value(fg, kind):
+    # logits at the end of the type's range, alone in their tiles and between others
+    x, w, targets, dloss = inputs(16, 60, 700, 64, kind, padded=False)
+    x[:, 0] = 1.0
+    w[:, 0] = 0.0
+    targets %= 130
+    loss, lse = fg.linear_cross_entropy(x, w[:130].contiguous(), targets)
+    grads = fg.linear_cross_entropy_backward(dloss, x, w[:130].contiguous(), targets, lse)
+    w[130:] = 0
+    w[130:, 0] = torch.finfo(TYPES[kind]).min
+    order = torch.randperm(700, device="cuda")
+    back = torch.argsort(order)
+    for words, t in ((w, targets), (w[order], back[targets])):
+        l2, s2 = fg.linear_cross_entropy(x, words, t)
+        # the sums of another order of words
+        assert ((l2 - loss).abs() <= 1e-5 * (1 + loss.abs())).all() and ((s2 - lse).abs() <= 1e-5 * (1 + lse.abs())).all()
+        dx, dw = fg.linear_cross_entropy_backward(dloss, x, words, t, s2)
+        step = torch.finfo(TYPES[kind]).eps
+        assert ((dx.double() - grads[0].double()).abs() <= 2 * step * grads[0].double().abs().max() + 1e-7).all()
+        dw = dw[back] if t is not targets else dw
+        assert not dw[130:].any()
+        assert ((dw[:130].double() - grads[1].double()).abs() <= 2 * step * grads[1].double().abs().max() + 1e-7).all()
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
 def test_large_logits(fg, kind):
     x, w, targets, dloss = inputs(7, 40, 300, 64, kind)
     check(fg, (x * 30).to(x.dtype), w, targets, dloss)
