@@ -76,6 +76,7 @@ embed_sort_kernel(const EmbedSortArgs a) {
   extern __shared__ __align__(16) char smem[];
   SortShared &s = *reinterpret_cast<SortShared *>(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  let_next();
   if (blockIdx.x >= kSortBlocks) {
     const long long threads = (long long)(gridDim.x - kSortBlocks) * kSortThreads;
     const long long at = (long long)(blockIdx.x - kSortBlocks) * kSortThreads + tid;
@@ -290,6 +291,8 @@ __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedSumArgs a) {
   using C = Columns<T, VEC>;
   using R = Row<T, TO, VEC>;
   constexpr int E = C::E, U = ADD ? kPiece / 2 : kPiece;
+  let_next();
+  after_previous();
   const int lane = threadIdx.x & 31;
   const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int chunks = (a.dim + C::kWide - 1) / C::kWide;
@@ -370,6 +373,7 @@ __global__ void __launch_bounds__(128) embed_join_kernel(const EmbedSumArgs a) {
   using R = Row<T, TO, VEC>;
   constexpr int E = C::E, U = 4;  // 8: 118 registers, 2 us more
   __shared__ A parts[3][E][32];
+  after_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunks = (a.dim + C::kWide - 1) / C::kWide;
   const long long items = (long long)*a.crossing * chunks;
@@ -450,12 +454,13 @@ cudaError_t sums_t(const EmbedSumArgs &a, cudaStream_t st) {
   const long long pieces = (a.tokens + kPiece - 1) / kPiece;
   const long long blocks = (pieces * chunks + 3) / 4;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  if (a.add) embed_sum_kernel<T, TO, VEC, true><<<(unsigned)blocks, 128, 0, st>>>(a);
-  else embed_sum_kernel<T, TO, VEC, false><<<(unsigned)blocks, 128, 0, st>>>(a);
-  if (pieces == 1) return cudaGetLastError();
+  const cudaError_t e =
+      launch_kernel(true, a.add ? embed_sum_kernel<T, TO, VEC, true> : embed_sum_kernel<T, TO, VEC, false>,
+                    (unsigned)blocks, dim3(128), 0, 1, st, a);
+  if (e != cudaSuccess || pieces == 1) return e;
   const long long most = 8ll * sm_count(), items = pieces * chunks;
-  embed_join_kernel<T, TO, VEC><<<(unsigned)(items < most ? items : most), 128, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_kernel(true, embed_join_kernel<T, TO, VEC>, (unsigned)(items < most ? items : most),
+                       dim3(128), 0, 1, st, a);
 }
 
 template <typename T, typename TO> cudaError_t sums_to(const EmbedSumArgs &a, cudaStream_t st) {

@@ -187,11 +187,13 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
     sh.failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  let_next();
   if (warp == 2) pair_tmem_alloc(&sh.tmem);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
   tc_fence_after();
+  after_previous();
   const uint32_t tm = sh.tmem;
 
   if (warp < 4) {

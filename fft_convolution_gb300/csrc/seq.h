@@ -205,6 +205,48 @@ size_t xent_workspace_bytes(int dtype, const XentArgs &a, bool grad);
 cudaError_t launch_xent(int dtype, const XentArgs &a, void *workspace, cudaStream_t st);
 cudaError_t launch_xent_grad(int dtype, const XentArgs &a, void *workspace, cudaStream_t st);
 
+// ---- chains of kernels -----------------------------------------------------------
+
+// Launches a kernel of a call.  With `chained` it follows another kernel of the
+// same call, and its blocks may start before that one has finished (programmatic
+// dependent launch): such kernels begin with after_previous(), and the one before
+// lets them start with let_next().  `cluster` blocks form a cluster (1: none).
+template <typename... P, typename... A>
+cudaError_t launch_kernel(bool chained, void (*kern)(P...), unsigned grid, dim3 block, size_t smem,
+                          unsigned cluster, cudaStream_t st, const A &...args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  unsigned n = 0;
+  if (chained) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = cluster;
+    at[n].val.clusterDim.y = 1;
+    at[n++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = n;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+#ifdef __CUDACC__
+// Every kernel before this one in the call has finished, its writes are seen.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// The next kernel's blocks may start once all of this one's have come here.
+__device__ __forceinline__ void let_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+#endif
+
 // ---- element conversions -----------------------------------------------------
 
 #ifdef __CUDACC__

@@ -62,6 +62,7 @@ template <typename T, typename O> struct LayRows {
 template <typename T, typename O, int PARTS>
 __global__ void __launch_bounds__(256) xent_lay_kernel(const LayRows<T, O> x, const LayRows<T, O> w,
                                                        int dim, LiveRows live) {
+  let_next();
   for (long long at = (long long)blockIdx.x * blockDim.y + threadIdx.y; at < x.rows + w.rows;
        at += (long long)gridDim.x * blockDim.y) {
     const bool mine = at < x.rows;
@@ -235,6 +236,7 @@ constexpr int kJoinTokens = 8, kJoinParts = 128;
 __global__ void __launch_bounds__(kJoinTokens * kJoinParts)
 xent_join_kernel(const XentTiles p, float *loss, float *lse) {
   __shared__ float2 parts[kJoinTokens * kJoinParts / 32][kJoinTokens];
+  after_previous();
   const int at = threadIdx.x % kJoinTokens, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long n = (long long)blockIdx.x * kJoinTokens + at;
   const int count = (int)((p.vocabulary + p.part - 1) / p.part);
@@ -274,6 +276,8 @@ xent_join_kernel(const XentTiles p, float *loss, float *lse) {
 // 2^15, so that G = c (p - 1) uses the type's range, and its inverse.
 __global__ void __launch_bounds__(1024) xent_unit_kernel(const XentTiles p, float *unit) {
   __shared__ float most[32];
+  let_next();
+  after_previous();
   float m = 0.0f;
   for (long long n = threadIdx.x; n < p.tokens; n += 1024) {
     const long long t = target_of(p.targets, p.target_bytes, n);
@@ -487,6 +491,7 @@ xent_products_kernel(const __grid_constant__ XentProducts p, int *status) {
 template <typename T>
 __global__ void __launch_bounds__(256) xent_dx_kernel(const float *sums, long long count, int slices,
                                                       const float *unit, T *dx, bool vec) {
+  after_previous();
   const float back = unit ? unit[1] : 1.0f;
   const long long step = (long long)gridDim.x * 256, first = (long long)blockIdx.x * 256 + threadIdx.x;
   if (vec) {
@@ -647,7 +652,7 @@ struct Layout {
 };
 
 template <auto Kern, typename... Args>
-cudaError_t pair_launch(long long tiles, cudaStream_t st, const Args &...args) {
+cudaError_t pair_launch(bool chained, long long tiles, cudaStream_t st, const Args &...args) {
   static DeviceOnce once;
   cudaError_t e = smem_limit_once((const void *)Kern, kPairSmem, once);
   if (e != cudaSuccess) return e;
@@ -661,20 +666,8 @@ cudaError_t pair_launch(long long tiles, cudaStream_t st, const Args &...args) {
   }
   if (regs.load(std::memory_order_acquire) < kPairRegs) return cudaErrorLaunchOutOfResources;
   const long long pairs = sm_count() / 2;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
-  cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = kPairSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, Kern, args...);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_kernel(chained, Kern, (unsigned)(2 * (tiles < pairs ? tiles : pairs)),
+                       dim3(kPairThreads), kPairSmem, 2, st, args...);
 }
 
 // The type of the products' operands.
@@ -698,10 +691,9 @@ cudaError_t lay_both(const XentArgs &a, const Layout &l, char *ws, bool grad, co
   const LayRows<T, O> w = rows(a.w, a.ldw, a.vocabulary, l.w, ws + l.x.bytes);
   const int tx = a.dim >= 512 ? 64 : 16;
   const long long need = up(x.rows + w.rows, 256 / tx), most = (long long)sm_count() * 16;
-  xent_lay_kernel<T, O, sizeof(T) == 4 ? 3 : 1>
-      <<<(unsigned)(need < most ? need : most), dim3(tx, 256 / tx), 0, st>>>(x, w, a.dim,
-                                                                             grad ? live : all);
-  return cudaGetLastError();
+  return launch_kernel(false, xent_lay_kernel<T, O, sizeof(T) == 4 ? 3 : 1>,
+                       (unsigned)(need < most ? need : most), dim3(tx, 256 / tx), 0, 1, st, x, w, a.dim,
+                       grad ? live : all);
 }
 
 XentTiles tiles_of(const XentArgs &a) {
@@ -742,12 +734,12 @@ cudaError_t xent_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st) {
   t.partial = reinterpret_cast<float2 *>(ws + l.partial);
   t.at_target = reinterpret_cast<float *>(ws + l.at_target);
   const int kblocks = (int)up(a.dim, kPairK);
-  e = l.few ? pair_launch<xent_few_kernel>(t.n, st, ops, t, kblocks, status)
-            : pair_launch<xent_sums_kernel>((long long)t.m * t.n, st, ops, t, kblocks, status);
+  const bool laid = l.x.own || l.w.own;
+  e = l.few ? pair_launch<xent_few_kernel>(laid, t.n, st, ops, t, kblocks, status)
+            : pair_launch<xent_sums_kernel>(laid, (long long)t.m * t.n, st, ops, t, kblocks, status);
   if (e != cudaSuccess) return e;
-  xent_join_kernel<<<(unsigned)up(a.tokens, kJoinTokens), kJoinTokens * kJoinParts, 0, st>>>(t, a.loss,
-                                                                                       a.lse);
-  return cudaGetLastError();
+  return launch_kernel(true, xent_join_kernel, (unsigned)up(a.tokens, kJoinTokens),
+                       dim3(kJoinTokens * kJoinParts), 0, 1, st, t, a.loss, a.lse);
 }
 
 template <typename T>
@@ -766,8 +758,7 @@ cudaError_t xent_grad_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st)
   float *unit = nullptr;
   if (half) {
     unit = reinterpret_cast<float *>(ws + l.unit);
-    xent_unit_kernel<<<1, 1024, 0, st>>>(t, unit);
-    e = cudaGetLastError();
+    e = launch_kernel(true, xent_unit_kernel, 1, dim3(1024), 0, 1, st, t, unit);
     if (e != cudaSuccess) return e;
   }
   t.unit = unit;
@@ -806,23 +797,23 @@ cudaError_t xent_grad_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st)
     if (t.v0 >= a.vocabulary) break;
     const long long words = a.vocabulary - t.v0 < l.piece ? a.vocabulary - t.v0 : l.piece;
     t.n = (int)up(words, l.width);
-    e = pair_launch<xent_grad_kernel<O, kParts>>((long long)t.m * t.n, st, ops, t, kblocks, status);
+    e = pair_launch<xent_grad_kernel<O, kParts>>(true, (long long)t.m * t.n, st, ops, t, kblocks, status);
     if (e != cudaSuccess) return e;
     p.first = i == 0;
     p.words = words;
     p.k = (int)up(words, kPairK);
     p.wm = a.dw ? (int)up(words, kPairTile) : 0;
     e = pair_launch<xent_products_kernel<T>>(
-        (long long)p.m * p.n * p.slices + (long long)p.wm * p.n, st, p, status);
+        true, (long long)p.m * p.n * p.slices + (long long)p.wm * p.n, st, p, status);
     if (e != cudaSuccess) return e;
   }
   if (!a.dx) return cudaSuccess;
   const long long count = a.tokens * a.dim;
   const bool vec = a.dim % 4 == 0 && ((uintptr_t)a.dx & (4 * sizeof(T) - 1)) == 0;
   const long long need = up(vec ? count / 4 : count, 256), most = (long long)sm_count() * 16;
-  xent_dx_kernel<T><<<(unsigned)(need < most ? need : most), 256, 0, st>>>(
-      p.sums, count, p.slices, unit, static_cast<T *>(a.dx), vec);
-  return cudaGetLastError();
+  return launch_kernel(true, xent_dx_kernel<T>, (unsigned)(need < most ? need : most), dim3(256), 0, 1,
+                       st, (const float *)p.sums, count, p.slices, (const float *)unit,
+                       static_cast<T *>(a.dx), vec);
 }
 
 }  // namespace
