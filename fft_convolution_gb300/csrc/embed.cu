@@ -183,7 +183,7 @@ embed_sort_kernel(const EmbedSortArgs a) {
 
 // ---- sums ------------------------------------------------------------------------
 
-constexpr int kPiece = 16;  // tokens, whose rows are all loaded at once
+constexpr int kBatch = 16;  // tokens, whose rows are all loaded at once; a piece is one or more
 
 // The columns of a warp: `E` per lane, whole 16 bytes or 32 apart.
 template <typename T, bool VEC> struct Columns {
@@ -285,12 +285,12 @@ template <typename T, typename TO, bool VEC> struct Row {
 // One warp per piece of the sorted tokens and chunk of columns.  ADD: rows that
 // end in the piece are loaded ahead too (half the piece at a time, for the
 // registers): one after the other their latency was three quarters of the time.
-template <typename T, typename TO, bool VEC, bool ADD>
+template <typename T, typename TO, bool VEC, bool ADD, bool MANY>
 __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedSumArgs a) {
   using A = typename Acc<T>::type;
   using C = Columns<T, VEC>;
   using R = Row<T, TO, VEC>;
-  constexpr int E = C::E, U = ADD ? kPiece / 2 : kPiece;
+  constexpr int E = C::E, U = ADD ? kBatch / 2 : kBatch;
   let_next();
   after_previous();
   const int lane = threadIdx.x & 31;
@@ -298,15 +298,18 @@ __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedSumArgs a) {
   const int chunks = (a.dim + C::kWide - 1) / C::kWide;
   const long long piece = item / chunks;
   const int chunk = (int)(item - piece * chunks);
-  const long long first = piece * kPiece;
+  const long long first = piece * (MANY ? a.piece : kBatch);
   if (first >= a.tokens) return;
-  const int count = (int)min((long long)kPiece, a.tokens - first);
   const unsigned none = (unsigned)a.rows;
-  // lanes 0 .. 15: the piece's tokens; 16: the one behind it, 17: the one before it
-  const long long where = lane < 17 ? first + lane : first - 1;
-  const bool here = lane < 18 && where >= 0 && where < a.tokens;
-  const unsigned key = here ? a.key[where] : none;
-  const unsigned pos = here && lane < count ? a.pos[where] : 0;
+  // lanes 0 .. 15: a batch's tokens; 16: the one behind it, 17: the one before it
+  auto lane_key = [&](long long at) {
+    const long long where = lane < 17 ? at + lane : at - 1;
+    return lane < 18 && where >= 0 && where < a.tokens ? a.key[where] : none;
+  };
+  auto lane_pos = [&](long long at) {
+    return lane < kBatch && at + lane < a.tokens ? a.pos[at + lane] : 0u;
+  };
+  unsigned key = lane_key(first), pos = lane_pos(first);
   const unsigned prev = __shfl_sync(0xffffffffu, key, 17);
   const T *dy = static_cast<const T *>(a.dy);
   A *partial = static_cast<A *>(a.partial) + piece * 2 * a.ldp;
@@ -316,63 +319,73 @@ __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedSumArgs a) {
   unsigned cur = __shfl_sync(0xffffffffu, key, 0);
   if (cur == none) return;  // sorted: nothing but padding from here on
   bool open = cur == prev;  // the run comes from the piece before
+  // MANY: a piece of several batches (the loop and the next batch's tokens on their way
+  // cost one of a single batch 2 of 22 us)
+  for (int b0 = 0; b0 < (MANY ? a.piece : kBatch); b0 += kBatch) {
+    const long long ahead = first + b0 + kBatch;
+    const bool more = MANY && b0 + kBatch < a.piece;
+    const unsigned next_key = more ? lane_key(ahead) : none, next_pos = more ? lane_pos(ahead) : 0;
 #pragma unroll
-  for (int j0 = 0; j0 < kPiece; j0 += U) {
-    typename C::Raw f[U];
-    typename R::Raw old[ADD ? U : 1];
-    // the lanes hold `none` behind the last token
+    for (int j0 = 0; j0 < kBatch; j0 += U) {
+      typename C::Raw f[U];
+      typename R::Raw old[ADD ? U : 1];
+      // the lanes hold `none` behind the last token
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const unsigned k = __shfl_sync(0xffffffffu, key, j0 + u);
-      const unsigned p = __shfl_sync(0xffffffffu, pos, j0 + u);
-      const bool live = k != none && j0 + u < count;
-      f[u] = C::load(dy + (long long)p * a.lddy, chunk, lane, live ? a.dim : 0);
-      if constexpr (ADD)
-        if (live && k != __shfl_sync(0xffffffffu, key, j0 + u + 1))
-          old[u] = R::load(a, k, chunk, lane);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const unsigned k = __shfl_sync(0xffffffffu, key, j0 + u);
-      if (k == none || j0 + u >= count) return;  // runs have been written where they end
-      A v[E];
-      C::widen(f[u], v);
-#pragma unroll
-      for (int i = 0; i < E; ++i) acc[i] += v[i];
-      const unsigned next = __shfl_sync(0xffffffffu, key, j0 + u + 1);
-      const bool ends = next != k;
-      if (!ends && j0 + u + 1 < kPiece) continue;
-      // a run that begins here and goes on: one more for the joins, in any order
-      if (!ends && !open && chunk == 0 && lane == 0)
-        a.list[atomicAdd(a.crossing, 1u)] = (unsigned)piece;
-      if (ends && !open) {
-        R::store(a, k, chunk, lane, acc, ADD ? &old[ADD ? u : 0] : nullptr);
-      } else {
-        A *to = partial + (open ? 0 : a.ldp);
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const int c = C::at(chunk, lane, i);
-          if (c < a.dim) to[c] = acc[i];
-        }
+      for (int u = 0; u < U; ++u) {
+        const unsigned k = __shfl_sync(0xffffffffu, key, j0 + u);
+        const unsigned p = __shfl_sync(0xffffffffu, pos, j0 + u);
+        const bool live = k != none;
+        f[u] = C::load(dy + (long long)p * a.lddy, chunk, lane, live ? a.dim : 0);
+        if constexpr (ADD)
+          if (live && k != __shfl_sync(0xffffffffu, key, j0 + u + 1))
+            old[u] = R::load(a, k, chunk, lane);
       }
-      open = false;
 #pragma unroll
-      for (int i = 0; i < E; ++i) acc[i] = 0;
+      for (int u = 0; u < U; ++u) {
+        const unsigned k = __shfl_sync(0xffffffffu, key, j0 + u);
+        if (k == none) return;  // runs have been written where they end
+        A v[E];
+        C::widen(f[u], v);
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] += v[i];
+        const unsigned next = __shfl_sync(0xffffffffu, key, j0 + u + 1);
+        const bool ends = next != k;
+        if (!ends && (more || j0 + u + 1 < kBatch)) continue;
+        // a run that begins here and goes on: one more for the joins, in any order
+        if (!ends && !open && chunk == 0 && lane == 0)
+          a.list[atomicAdd(a.crossing, 1u)] = (unsigned)piece;
+        if (ends && !open) {
+          R::store(a, k, chunk, lane, acc, ADD ? &old[ADD ? u : 0] : nullptr);
+        } else {
+          A *to = partial + (open ? 0 : a.ldp);
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            const int c = C::at(chunk, lane, i);
+            if (c < a.dim) to[c] = acc[i];
+          }
+        }
+        open = false;
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = 0;
+      }
     }
+    key = next_key;
+    pos = next_pos;
   }
 }
 
 // The runs that go on behind the piece where they begin, from the list: its own part,
-// then the heads of the pieces behind it, a quarter of them to each warp of the
+// then the heads of the pieces behind it, an equal share to each warp of the
 // block (the most frequent row of a text crosses dozens; one warp for all of them, and
 // blocks for every piece, took 17 us for 16384 tokens).
+constexpr int kJoinWarps = 4;
 template <typename T, typename TO, bool VEC>
-__global__ void __launch_bounds__(128) embed_join_kernel(const EmbedSumArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const EmbedSumArgs a) {
   using A = typename Acc<T>::type;
   using C = Columns<T, VEC>;
   using R = Row<T, TO, VEC>;
   constexpr int E = C::E, U = 4;  // 8: 118 registers, 2 us more
-  __shared__ A parts[3][E][32];
+  __shared__ A parts[kJoinWarps - 1][E][32];
   after_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunks = (a.dim + C::kWide - 1) / C::kWide;
@@ -380,10 +393,10 @@ __global__ void __launch_bounds__(128) embed_join_kernel(const EmbedSumArgs a) {
   for (long long item = blockIdx.x; item < items; item += gridDim.x) {
     const long long piece = a.list[item / chunks];
     const int chunk = (int)(item % chunks);
-    const unsigned row = a.key[(piece + 1) * kPiece - 1];
+    const unsigned row = a.key[(piece + 1) * a.piece - 1];
     long long last = piece + 1;  // the piece where the run ends: it goes on where the next begins with it
     for (;;) {
-      const long long at = (last + 1 + lane) * kPiece;
+      const long long at = (last + 1 + lane) * a.piece;
       const unsigned on = __ballot_sync(0xffffffffu, at < a.tokens && a.key[at] == row);
       const int more = __ffs(~on) - 1;
       last += more < 0 ? 32 : more;
@@ -394,7 +407,7 @@ __global__ void __launch_bounds__(128) embed_join_kernel(const EmbedSumArgs a) {
     typename R::Raw old;
     if (a.add && warp == 0) old = R::load(a, row, chunk, lane);
     // part 0 is the piece's own tail
-    const long long count = last - piece + 1, share = (count + 3) / 4;
+    const long long count = last - piece + 1, share = (count + kJoinWarps - 1) / kJoinWarps;
     const long long from = share * warp, to = min(from + share, count);
 #pragma unroll
     for (int i = 0; i < E; ++i) acc[i] = 0;
@@ -421,7 +434,7 @@ __global__ void __launch_bounds__(128) embed_join_kernel(const EmbedSumArgs a) {
     __syncthreads();
     if (warp == 0) {
 #pragma unroll
-      for (int w = 0; w < 3; ++w)
+      for (int w = 0; w < kJoinWarps - 1; ++w)
 #pragma unroll
         for (int i = 0; i < E; ++i) acc[i] += parts[w][i][lane];
       R::store(a, row, chunk, lane, acc, a.add ? &old : nullptr);
@@ -451,16 +464,20 @@ template <typename T> cudaError_t lookup_t(const EmbedArgs &a, cudaStream_t st) 
 template <typename T, typename TO, bool VEC>
 cudaError_t sums_t(const EmbedSumArgs &a, cudaStream_t st) {
   const long long chunks = (a.dim + Columns<T, VEC>::kWide - 1) / Columns<T, VEC>::kWide;
-  const long long pieces = (a.tokens + kPiece - 1) / kPiece;
+  const long long pieces = (a.tokens + a.piece - 1) / a.piece;
   const long long blocks = (pieces * chunks + 3) / 4;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const cudaError_t e =
-      launch_kernel(true, a.add ? embed_sum_kernel<T, TO, VEC, true> : embed_sum_kernel<T, TO, VEC, false>,
+      launch_kernel(true,
+                    a.piece > kBatch ? (a.add ? embed_sum_kernel<T, TO, VEC, true, true>
+                                              : embed_sum_kernel<T, TO, VEC, false, true>)
+                                     : (a.add ? embed_sum_kernel<T, TO, VEC, true, false>
+                                              : embed_sum_kernel<T, TO, VEC, false, false>),
                     (unsigned)blocks, dim3(128), 0, 1, st, a);
   if (e != cudaSuccess || pieces == 1) return e;
-  const long long most = 8ll * sm_count(), items = pieces * chunks;
+  const long long most = 8ll * sm_count() * 4 / kJoinWarps, items = pieces * chunks;
   return launch_kernel(true, embed_join_kernel<T, TO, VEC>, (unsigned)(items < most ? items : most),
-                       dim3(128), 0, 1, st, a);
+                       dim3(32 * kJoinWarps), 0, 1, st, a);
 }
 
 template <typename T, typename TO> cudaError_t sums_to(const EmbedSumArgs &a, cudaStream_t st) {
@@ -474,9 +491,17 @@ size_t list_bytes(long long tokens) { return round256((size_t)tokens * 4); }
 
 }  // namespace
 
+// Tokens of a piece: many of them make long runs, whose parts one block adds (10^6
+// tokens of 64 columns: 271 -> 11 us for the joins, 88 -> 104 for the sums).
+int piece_tokens(long long tokens) {
+  const long long batches = tokens / 32768;
+  return kBatch * (int)(batches < 1 ? 1 : batches > 32 ? 32 : batches);
+}
+
 size_t embed_workspace_bytes(long long tokens, int dim, int dtype) {
   if (tokens == 0) return 0;
-  const size_t pieces = (size_t)(tokens + kPiece - 1) / kPiece;
+  const int piece = piece_tokens(tokens);
+  const size_t pieces = (size_t)(tokens + piece - 1) / piece;
   return 4 * list_bytes(tokens) + 256 + list_bytes((long long)pieces) + pieces * 2 * (size_t)dim * (dtype == FFT_ELEM_F64 ? 8 : 4);
 }
 
@@ -533,9 +558,10 @@ cudaError_t launch_embed_grad(int dtype, int ttype, const EmbedGradArgs &g, void
   a.rows = g.rows;
   a.dim = g.dim;
   a.ldp = g.dim;
+  a.piece = piece_tokens(g.tokens);
   a.crossing = s.crossing;
   a.list = reinterpret_cast<unsigned *>(ws + 4 * list + 256);
-  a.partial = ws + 4 * list + 256 + list_bytes((g.tokens + kPiece - 1) / kPiece);
+  a.partial = ws + 4 * list + 256 + list_bytes((g.tokens + a.piece - 1) / a.piece);
   a.dtable = g.dtable;
   a.scale = g.scale;
   a.add = g.add;

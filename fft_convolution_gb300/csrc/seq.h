@@ -143,6 +143,7 @@ struct EmbedSumArgs {
   void *dtable, *partial;     // partial: [piece][head, tail][ldp] accumulators
   long long tokens, rows, lddy, ldp;
   int dim;
+  int piece;  // tokens of a piece
   double scale;
   bool add;
 };

@@ -26,7 +26,10 @@ namespace fftgb {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr size_t kPieceBytes = (size_t)256 << 20;  // of G
+#ifndef PIECE_MB
+#define PIECE_MB 256
+#endif
+constexpr size_t kPieceBytes = (size_t)PIECE_MB << 20;  // of G
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -156,23 +159,39 @@ xent_sums_kernel(const __grid_constant__ PairOperands ops, const XentTiles p, in
     const int count = (int)min((long long)wide, p.vocabulary - v0);
     const long long target = target_of(p.targets, p.target_bytes, n) - v0;
     const bool mine = target >= 0 && target < count;
-    float top = -INFINITY, at = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kHalf; ++i)
-      if (i < count) top = fmaxf(top, f[i]);
     if (mine) {
+      float at = 0.0f;
 #pragma unroll
       for (int i = 0; i < kHalf; ++i)
         if (target == i) at = f[i];
       p.at_target[n] = at;
     }
+    if (count < wide) {  // the last words: what is behind them does not count
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i)
+        if (i >= count) f[i] = -INFINITY;
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kHalf; j += 32)
+      if (j < wide) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) top = fmaxf(top, f[j + i]);
+      }
     // all of them -infinity (or NaN): in units of 1
     top = top == -INFINITY ? top : top * kLog2e;
     const float unit = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f;
+    float2 sums = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < kHalf; ++i)
-      if (i < count) sum += exp2_approx(fmaf(f[i], kLog2e, -unit));
+    for (int j = 0; j < kHalf; j += 32)
+      if (j < wide) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float2 e = fma2(make_float2(f[j + i], f[j + i + 1]), both(kLog2e), both(-unit));
+          sums = add2(sums, make_float2(exp2_approx(e.x), exp2_approx(e.y)));
+        }
+      }
+    const float sum = sums.x + sums.y;
     p.partial[(2ll * (t / p.m) + half) * p.tokens + n] = make_float2(sum == 0.0f ? top : unit, sum);
   };
   pair_run(&ops, p.m * p.n, status, of, out);
@@ -229,41 +248,31 @@ __device__ __forceinline__ float2 join_sums(float2 a, float2 b) {
   const float sa = a.x == m ? a.y : a.y * exp2f(a.x - m), sb = b.x == m ? b.y : b.y * exp2f(b.x - m);
   return make_float2(m, sa + sb);
 }
-// lse and loss from the parts of a token: blocks of 8 tokens, a thread for every
-// 128th part of one (with 32 tokens and every eighth part, 48 tokens of 512 parts took
-// 16 us).
-constexpr int kJoinTokens = 8, kJoinParts = 128;
-__global__ void __launch_bounds__(kJoinTokens * kJoinParts)
-xent_join_kernel(const XentTiles p, float *loss, float *lse) {
-  __shared__ float2 parts[kJoinTokens * kJoinParts / 32][kJoinTokens];
+// lse and loss from the parts of a token: blocks of T tokens, the parts of each taken
+// by blockDim.x / T threads (with 32 tokens and every eighth part, 48 tokens of 512 parts
+// took 16 us; with 8 tokens and every 128th, 65536 tokens of 8 parts 100).
+template <int T>
+__global__ void __launch_bounds__(1024) xent_join_kernel(const XentTiles p, float *loss, float *lse) {
+  __shared__ float2 parts[1024];
   after_previous();
-  const int at = threadIdx.x % kJoinTokens, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long n = (long long)blockIdx.x * kJoinTokens + at;
+  const int at = threadIdx.x % T, slice = threadIdx.x / T, slices = blockDim.x / T;
+  const long long n = (long long)blockIdx.x * T + at;
   const int count = (int)((p.vocabulary + p.part - 1) / p.part);
   float2 s = make_float2(-INFINITY, 0.0f);
   if (n < p.tokens) {
 #pragma unroll 4
-    for (int i = threadIdx.x / kJoinTokens; i < count; i += kJoinParts)
+    for (int i = slice; i < count; i += slices)
       s = join_sums(s, p.partial[(long long)i * p.tokens + n]);
   }
-#pragma unroll
-  for (int o = kJoinTokens; o < 32; o *= 2) {
-    const float2 b = make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o));
-    s = (lane & o) == 0 ? join_sums(s, b) : join_sums(b, s);
+  parts[threadIdx.x] = s;
+  for (int half = slices / 2; half > 0; half /= 2) {
+    __syncthreads();
+    if (slice < half) {
+      s = join_sums(s, parts[threadIdx.x + half * T]);
+      parts[threadIdx.x] = s;
+    }
   }
-  if (lane < kJoinTokens) parts[warp][lane] = s;
-  __syncthreads();
-  if (warp != 0) return;
-  // 32 warps' parts of 8 tokens: four lanes a token, then one
-  s = parts[lane / kJoinTokens * 8][at];
-#pragma unroll
-  for (int w = 1; w < 8; ++w) s = join_sums(s, parts[lane / kJoinTokens * 8 + w][at]);
-#pragma unroll
-  for (int o = kJoinTokens; o < 32; o *= 2) {
-    const float2 b = make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o));
-    s = (lane & o) == 0 ? join_sums(s, b) : join_sums(b, s);
-  }
-  if (lane >= kJoinTokens || n >= p.tokens) return;
+  if (slice > 0 || n >= p.tokens) return;
   const float total = (s.x + log2f(s.y)) * kLn2;
   const long long target = target_of(p.targets, p.target_bytes, n);
   lse[n] = total;
@@ -342,29 +351,49 @@ xent_grad_kernel(const __grid_constant__ PairOperands ops, const XentTiles p, in
   auto out = [&](int t, float (&f)[kHalf]) {
     const PairTile w = word_tile(p, t, p.v0, kblocks);
     const long long n = w.a_row + rank * 128 + (warp & 3) * 32 + lane;
-    if (n >= p.tokens) return;
     const int wide = p.width / 2;
     const long long v = w.b_row + half * wide;
-    const long long target = target_of(p.targets, p.target_bytes, n);
-    float c = 0.0f, lse = 0.0f;
-    if (target >= 0 && target < p.vocabulary) {
-      c = p.dloss[n] * (p.unit ? p.unit[0] : 1.0f);
-      lse = p.lse[n];
+    // a token that takes no part: e^{0 - infinity} * 0 (its x has been laid out as 0)
+    float c = 0.0f, lse = INFINITY;
+    int at = -1;
+    if (n < p.tokens) {
+      const long long target = target_of(p.targets, p.target_bytes, n);
+      if (target >= 0 && target < p.vocabulary && p.dloss[n] != 0.0f) {
+        c = p.dloss[n] * (p.unit ? p.unit[0] : 1.0f);
+        lse = p.lse[n];
+        if (target >= v && target < v + wide) at = (int)(target - v);
+      }
     }
-    const bool live = c != 0.0f;  // NaN is live
     O *row = static_cast<O *>(p.g) + n * p.ldg + (v - p.v0);
-    const int at = target >= v && target < v + wide ? (int)(target - v) : -1;
-    const int count = live ? (int)max(0ll, min((long long)wide, p.vocabulary - v)) : 0;
+    const int count = (int)max(0ll, min((long long)wide, p.vocabulary - v));
 #pragma unroll
     for (int j = 0; j < kHalf; j += 32)
       if (j < wide) {
         float q[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          q[i] = exp2_approx((f[j + i] - lse) * kLog2e) - (at == j + i ? 1.0f : 0.0f);
-          q[i] = j + i < count ? q[i] * c : 0.0f;
+        for (int i = 0; i < 32; i += 2) {
+          // l - lse is exact where it counts, near 0: a product with log2 e before it would round lse
+          const float2 l = add2(make_float2(f[j + i], f[j + i + 1]), both(-lse));
+          const float2 e = mul2(l, both(kLog2e));
+          q[i] = exp2_approx(e.x);
+          q[i + 1] = exp2_approx(e.y);
         }
-        put32<O, PARTS>(row + j, p.tokens * p.ldg, q);
+        if (__any_sync(0xffffffffu, at >= j && at < j + 32)) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) q[i] -= at == j + i ? 1.0f : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float2 g = mul2(make_float2(q[i], q[i + 1]), both(c));
+          q[i] = g.x;
+          q[i + 1] = g.y;
+        }
+        if (count < wide) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (j + i >= count) q[i] = 0.0f;
+        }
+        if (n < p.tokens) put32<O, PARTS>(row + j, p.tokens * p.ldg, q);
       }
   };
   pair_run(&ops, p.m * p.n, status, of, out);
@@ -386,8 +415,15 @@ struct XentProducts {
   const float *unit;
 };
 
+// Adds to four floats where they lie: a reduction in the L2, once per element and launch,
+// that nobody waits for (to load, add and store them held the products back).
+__device__ __forceinline__ void add16(float *p, const float (&v)[4]) {
+  asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3])
+               : "memory");
+}
 // 32 columns from c on of a warp's 32 rows (a lane has one) into an array of rows of
-// dim elements, + what is there.  Rows on 32-byte boundaries: each lane its own;
+// dim elements, + what is there (floats only).  Rows on 32-byte boundaries: each lane its own;
 // others: a row at a time, through shared memory (each lane writing its row by
 // elements took half the time of 777 tokens, 333 wide).
 template <typename T>
@@ -407,15 +443,14 @@ __device__ __forceinline__ void put_rows(T *out, long long row0, long long rows,
           float v[P];
 #pragma unroll
           for (int i = 0; i < P; ++i) v[i] = f[j + h * P + i];
-          if (add) {
-            float o[P];
-            unpack<T>(*reinterpret_cast<const uint4 *>(row + j + h * P), o);
-#pragma unroll
-            for (int i = 0; i < P; ++i) v[i] += o[i];
-          }
+          if constexpr (sizeof(T) == 4)
+            if (add) {
+              add16(row + j + h * P, v);
+              continue;
+            }
           w[h] = pack<T>(v);
         }
-        store32(row + j, w[0], w[1]);
+        if (!add) store32(row + j, w[0], w[1]);
       }
     }
     return;
@@ -428,8 +463,12 @@ __device__ __forceinline__ void put_rows(T *out, long long row0, long long rows,
     T *col = out + row0 * dim + c + lane;
 #pragma unroll 8
     for (int r = 0; r < count; ++r) {
-      float v = turn[r * 33 + lane];
-      if (add) v += to_acc(col[(long long)r * dim]);
+      const float v = turn[r * 33 + lane];
+      if constexpr (sizeof(T) == 4)
+        if (add) {
+          atomicAdd(col + (long long)r * dim, v);
+          continue;
+        }
       col[(long long)r * dim] = from_acc<T>(v);
     }
   }
@@ -738,8 +777,14 @@ cudaError_t xent_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st) {
   e = l.few ? pair_launch<xent_few_kernel>(laid, t.n, st, ops, t, kblocks, status)
             : pair_launch<xent_sums_kernel>(laid, (long long)t.m * t.n, st, ops, t, kblocks, status);
   if (e != cudaSuccess) return e;
-  return launch_kernel(true, xent_join_kernel, (unsigned)up(a.tokens, kJoinTokens),
-                       dim3(kJoinTokens * kJoinParts), 0, 1, st, t, a.loss, a.lse);
+  const long long parts = up(a.vocabulary, l.part);
+  if (a.tokens <= 8ll * sm_count() && parts > 32)
+    return launch_kernel(true, xent_join_kernel<8>, (unsigned)up(a.tokens, 8), dim3(1024), 0, 1, st, t,
+                         a.loss, a.lse);
+  int threads = 32;  // 4 parts a thread, 1 to 8 threads a token
+  while (threads < 256 && threads / 32 * 4 < parts) threads *= 2;
+  return launch_kernel(true, xent_join_kernel<32>, (unsigned)up(a.tokens, 32), dim3(threads), 0, 1, st,
+                       t, a.loss, a.lse);
 }
 
 template <typename T>

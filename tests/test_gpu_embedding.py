@@ -97,7 +97,7 @@ def test_lookup_shapes_strides_and_out(fg):
 
 
 CASES = [(1, 1, 1), (2, 1, 3), (31, 4, 8), (32, 4, 8), (33, 4, 8), (64, 2, 40), (65, 1, 5), (100, 511, 24), (1000, 512, 17),
-         (1025, 513, 64), (3000, 3, 300), (5003, 30011, 33), (9000, 70000, 16), (40000, 20, 24), (20000, 300000, 8)]
+         (1025, 513, 64), (3000, 3, 300), (5003, 30011, 33), (9000, 70000, 16), (40000, 20, 24), (20000, 300000, 8), (70001, 500, 24), (300000, 4000, 8)]
 
 
 @pytest.mark.parametrize("kind,tkind", [("f32", "f32"), ("f64", "f64"), ("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"),
