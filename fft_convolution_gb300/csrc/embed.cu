@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(256) embed_kernel(const EmbedArgs a) {
 
 // ---- tokens in the order of their rows -----------------------------------------------
 
-constexpr int kSortBlocks = 8, kSortThreads = 1024, kSortBits = 9, kDigits = 1 << kSortBits;
+constexpr int kSortMost = 16, kSortThreads = 1024, kSortBits = 9, kDigits = 1 << kSortBits;
 
 struct SortShared {
   unsigned count[kSortThreads / 32][kDigits];  // of a tile, by warp; then where each warp's go
@@ -66,20 +66,19 @@ struct SortShared {
   unsigned sums[kSortThreads / 32];
 };
 
-// A stable radix sort of (row, token) by one cluster: each block has an eighth
-// of the tokens, digits of at most 9 bits, the arrays between the passes in
+// A stable radix sort of (row, token) by one cluster of a.blocks: each block has
+// its share of the tokens, digits of at most 9 bits, the arrays between the passes in
 // global memory (the L2 holds them).  Tokens of no row sort behind all others.
 // The clusters beside it meanwhile write zeros to the whole of a new gradient: 2
 // passes over 16384 tokens hide behind 268 MB of them.
-__global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThreads)
-embed_sort_kernel(const EmbedSortArgs a) {
+__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedSortArgs a) {
   extern __shared__ __align__(16) char smem[];
   SortShared &s = *reinterpret_cast<SortShared *>(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   let_next();
-  if (blockIdx.x >= kSortBlocks) {
-    const long long threads = (long long)(gridDim.x - kSortBlocks) * kSortThreads;
-    const long long at = (long long)(blockIdx.x - kSortBlocks) * kSortThreads + tid;
+  if (blockIdx.x >= a.blocks) {
+    const long long threads = (long long)(gridDim.x - a.blocks) * kSortThreads;
+    const long long at = (long long)(blockIdx.x - a.blocks) * kSortThreads + tid;
     char *p = static_cast<char *>(a.fill);
     // the table's gradient starts on a boundary of its elements: 2 bytes at least
     long long head = (16 - ((uintptr_t)p & 15)) & 15;
@@ -94,7 +93,7 @@ embed_sort_kernel(const EmbedSortArgs a) {
   }
   const unsigned rank = block_rank();
   if (blockIdx.x == 0 && tid == 0) *a.crossing = 0;
-  const long long share = (a.tokens + kSortBlocks - 1) / kSortBlocks;
+  const long long share = (a.tokens + a.blocks - 1) / a.blocks;
   const long long begin = min(share * rank, a.tokens), end = min(begin + share, a.tokens);
   const unsigned mask = (1u << a.bits) - 1;
   for (int d = tid; d < kDigits * (kSortThreads / 32); d += kSortThreads) (&s.count[0][0])[d] = 0;
@@ -126,11 +125,12 @@ embed_sort_kernel(const EmbedSortArgs a) {
     if (tid < kDigits) {
       const uint32_t mine = (uint32_t)__cvta_generic_to_shared(&s.hist[tid]);
 #pragma unroll
-      for (unsigned r = 0; r < kSortBlocks; ++r) {
-        const unsigned n = peer_load(peer(mine, r));
-        total += n;
-        if (r < rank) before += n;
-      }
+      for (unsigned r = 0; r < kSortMost; ++r)
+        if (r < a.blocks) {
+          const unsigned n = peer_load(peer(mine, r));
+          total += n;
+          if (r < rank) before += n;
+        }
     }
     unsigned incl = total;
 #pragma unroll
@@ -443,6 +443,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const Embed
   }
 }
 
+// Lets a kernel's clusters have 16 blocks, once per device and context.
+cudaError_t wide_cluster_once(const void *kern, DeviceOnce &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  const unsigned long long id = context_id();
+  if (id != 0 && done.ctx[dev].load(std::memory_order_acquire) == id) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done.ctx[dev].store(context_id(), std::memory_order_release);
+  return e;
+}
+
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 template <typename T> cudaError_t lookup_t(const EmbedArgs &a, cudaStream_t st) {
@@ -530,6 +543,10 @@ cudaError_t launch_embed_grad(int dtype, int ttype, const EmbedGradArgs &g, void
     s.key[i] = reinterpret_cast<unsigned *>(ws + 2 * i * list);
     s.pos[i] = reinterpret_cast<unsigned *>(ws + (2 * i + 1) * list);
   }
+  // 16 blocks where the sort takes longer than the zeros beside it (65536 tokens of 1024
+  // columns 130 -> 106 us, 10^6 of 64 955 -> 546, but 16384 of 2048 82 -> 87 and 30000 of
+  // 4096 224 -> 240).
+  s.blocks = g.tokens > 32768 ? kSortMost : 8;
   s.crossing = reinterpret_cast<unsigned *>(ws + 4 * list);
   int bits = 0;  // of the largest key, which is `rows`
   while (bits < 32 && ((unsigned long long)g.rows >> bits) != 0) ++bits;
@@ -540,14 +557,14 @@ cudaError_t launch_embed_grad(int dtype, int ttype, const EmbedGradArgs &g, void
   // A cluster for each MB, up to four blocks per SM: 268 MB of zeros and 16384 tokens
   // take 104 us with one per SM, 88 with two, 83.5 with four, 83 with sixteen.
   long long fillers = (s.fill_bytes + (1ll << 20) - 1) >> 20;
-  const long long most = 4 * (sm_count() / kSortBlocks);
+  const long long most = 4 * (sm_count() / (int)s.blocks);
   if (fillers > most) fillers = most;
-  static DeviceOnce once;
+  static DeviceOnce once, wide_once;
   cudaError_t e = smem_limit_once((const void *)embed_sort_kernel, sizeof(SortShared), once);
+  if (e == cudaSuccess && s.blocks > 8) e = wide_cluster_once((const void *)embed_sort_kernel, wide_once);
   if (e != cudaSuccess) return e;
-  embed_sort_kernel<<<(unsigned)(kSortBlocks * (1 + fillers)), kSortThreads, sizeof(SortShared),
-                      st>>>(s);
-  e = cudaGetLastError();
+  e = launch_kernel(false, embed_sort_kernel, (unsigned)(s.blocks * (1 + fillers)), dim3(kSortThreads),
+                    sizeof(SortShared), s.blocks, st, s);
   if (e != cudaSuccess) return e;
   EmbedSumArgs a{};
   a.dy = g.dy;

@@ -135,6 +135,7 @@ struct EmbedSortArgs {
   void *fill;
   long long fill_bytes;
   unsigned *crossing;  // set to 0
+  unsigned blocks;     // of a cluster
 };
 struct EmbedSumArgs {
   const void *dy;
