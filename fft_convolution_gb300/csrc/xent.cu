@@ -26,10 +26,7 @@ namespace fftgb {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-#ifndef PIECE_MB
-#define PIECE_MB 256
-#endif
-constexpr size_t kPieceBytes = (size_t)PIECE_MB << 20;  // of G
+constexpr size_t kPieceBytes = (size_t)256 << 20;  // of G
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -400,7 +397,7 @@ xent_grad_kernel(const __grid_constant__ PairOperands ops, const XentTiles p, in
 }
 
 // dx += G W over a piece and dW = G^T x of its rows, in one launch: the
-// longer sums of dx first, so that the short ones fill the ends.
+// longer sums first, so that the short ones fill the ends.
 struct XentProducts {
   PairOperands ops[2];
   long long tokens, v0;
@@ -408,7 +405,9 @@ struct XentProducts {
   int dim;
   int width;             // columns of a tile
   int m, n, slices, k;   // dx: tiles of tokens and of columns, cuts of the sum, its blocks
-  int wm, wk;            // dW: tiles of words, blocks of tokens
+  int wm, wk, wslices;   // dW: tiles of words, blocks of tokens, cuts of their sum
+  int words_first;       // dW's tiles before dx's
+  float *wsums;          // [wslices][words][dim]; one cut: not used
   float *sums;           // [slices][tokens][dim]
   int first;             // the piece: nothing to add to
   void *dw;
@@ -480,32 +479,37 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 xent_products_kernel(const __grid_constant__ XentProducts p, int *status) {
   const int warp = threadIdx.x >> 5;
   const int rank = (int)block_rank(), half = (warp - 4) >> 2;
-  const int mn = p.m * p.n, dx_tiles = mn * p.slices, dw_tiles = p.wm * p.n;
+  const int mn = p.m * p.n, dx_tiles = mn * p.slices;
+  const int wmn = p.wm * p.n, dw_tiles = wmn * p.wslices;
+  // which of the products (0: dx), which cut, and the tile there
+  auto place = [&](int t, int &which, int &slice) {
+    int u = p.words_first ? (t < dw_tiles ? t + dx_tiles : t - dw_tiles) : t;
+    which = u < dx_tiles ? 0 : 1;
+    if (which) u -= dx_tiles;
+    slice = u / (which ? wmn : mn);
+    return u - slice * (which ? wmn : mn);
+  };
   auto of = [&](int t, int &which) {
     PairTile w{};
-    if (t < dx_tiles) {
-      which = 0;
-      const int slice = t / mn, u = t - slice * mn;
-      w.a_row = u / p.n * kPairTile;
-      w.b_row = u % p.n * p.width;
-      w.b_base = (int)p.v0;
-      w.k0 = (int)((long long)p.k * slice / p.slices);
-      w.k1 = (int)((long long)p.k * (slice + 1) / p.slices);
-    } else {
-      which = 1;
-      const int u = t - dx_tiles;
-      w.a_row = u / p.n * kPairTile;
-      w.b_row = u % p.n * p.width;
-      w.k1 = p.wk;
-    }
+    int slice;
+    const int u = place(t, which, slice);
+    const long long k = which ? p.wk : p.k;
+    const int slices = which ? p.wslices : p.slices;
+    w.a_row = u / p.n * kPairTile;
+    w.b_row = u % p.n * p.width;
+    w.b_base = which ? 0 : (int)p.v0;
+    w.k0 = (int)(k * slice / slices);
+    w.k1 = (int)(k * (slice + 1) / slices);
     return w;
   };
   auto out = [&](int t, float (&f)[kHalf]) {
-    int which = 0;
+    int which, slice;
+    place(t, which, slice);
     const PairTile w = of(t, which);
     const long long r0 = w.a_row + rank * 128 + (warp & 3) * 32;  // the warp's first row
     const int wide = p.width / 2, c0 = w.b_row + half * wide;
-    const float back = which == 1 && p.unit ? p.unit[1] : 1.0f;
+    const bool last = which == 1 && p.wslices == 1;  // the result, not a part of it
+    const float back = last && p.unit ? p.unit[1] : 1.0f;
     float *turn = pair_spare() + (warp - 4) * (32 * 33);
 #pragma unroll
     for (int j = 0; j < kHalf; j += 32)
@@ -514,9 +518,10 @@ xent_products_kernel(const __grid_constant__ XentProducts p, int *status) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) q[i] = f[j + i] * back;
         const int c = c0 + j;
-        if (which == 0) {
-          put_rows<float>(p.sums + (long long)(t / mn) * p.tokens * p.dim, r0, p.tokens, c, p.dim,
-                          p.dim % 8 == 0, !p.first, q, turn);
+        if (!last) {
+          const long long rows = which ? p.words : p.tokens;
+          put_rows<float>((which ? p.wsums : p.sums) + slice * rows * p.dim, r0, rows, c, p.dim,
+                          p.dim % 8 == 0, which == 0 && !p.first, q, turn);
         } else {
           const bool vec = p.dim * (int)sizeof(T) % 32 == 0 && ((uintptr_t)p.dw & 31) == 0;
           put_rows<T>(static_cast<T *>(p.dw) + p.v0 * p.dim, r0, p.words, c, p.dim, vec, false, q, turn);
@@ -526,9 +531,9 @@ xent_products_kernel(const __grid_constant__ XentProducts p, int *status) {
   pair_run(p.ops, dx_tiles + dw_tiles, status, of, out);
 }
 
-// dx: the slices added and rounded once.
+// dx (dW of few words): the slices added and rounded once.
 template <typename T>
-__global__ void __launch_bounds__(256) xent_dx_kernel(const float *sums, long long count, int slices,
+__global__ void __launch_bounds__(256) xent_slices_kernel(const float *sums, long long count, int slices,
                                                       const float *unit, T *dx, bool vec) {
   after_previous();
   const float back = unit ? unit[1] : 1.0f;
@@ -645,7 +650,8 @@ struct Layout {
   int width, wide;                   // words and columns of dx and dw per tile
   long long piece;                   // words
   int pieces, slices;
-  size_t unit, g, sums;              // backward
+  int wslices;
+  size_t unit, g, sums, wsums;       // backward
   size_t bytes;
   Layout(int dtype, const XentArgs &a, bool grad) {
     parts = dtype == FFT_ELEM_F32 ? 3 : 1;
@@ -659,9 +665,9 @@ struct Layout {
     part = few ? 32 : width / 2;
     // columns: as few tiles as there are of 256, of even size
     wide = (int)up(up(a.dim, up(a.dim, kPairTile)), 64) * 64;
-    partial = at_target = unit = g = sums = 0;
+    partial = at_target = unit = g = sums = wsums = 0;
     piece = 0;
-    pieces = slices = 0;
+    pieces = slices = wslices = 0;
     auto take = [&](size_t n) {
       const size_t at = bytes;
       bytes += round256(n);
@@ -684,9 +690,15 @@ struct Layout {
     slices = 1;
     while (slices < 32 && tiles * slices * 2 <= pairs && piece / kPairK / (slices * 2) >= 16)
       slices *= 2;
+    // and so are dW's, of few words and many tokens
+    const long long wtiles = up(piece, kPairTile) * up(a.dim, wide);
+    wslices = 1;
+    while (wslices < 32 && wtiles * wslices * 2 <= pairs && up(a.tokens, kPairK) / (wslices * 2) >= 16)
+      wslices *= 2;
     unit = take(8);
     g = take((size_t)parts * a.tokens * piece * 2);
     sums = take((size_t)slices * a.tokens * a.dim * 4);
+    if (wslices > 1) wsums = take((size_t)wslices * piece * a.dim * 4);
   }
 };
 
@@ -733,6 +745,15 @@ cudaError_t lay_both(const XentArgs &a, const Layout &l, char *ws, bool grad, co
   return launch_kernel(false, xent_lay_kernel<T, O, sizeof(T) == 4 ? 3 : 1>,
                        (unsigned)(need < most ? need : most), dim3(tx, 256 / tx), 0, 1, st, x, w, a.dim,
                        grad ? live : all);
+}
+
+template <typename T>
+cudaError_t add_slices(const float *sums, long long count, int slices, const float *unit, T *out,
+                       cudaStream_t st) {
+  const bool vec = count % 4 == 0 && ((uintptr_t)out & (4 * sizeof(T) - 1)) == 0;
+  const long long need = up(vec ? count / 4 : count, 256), most = (long long)sm_count() * 16;
+  return launch_kernel(true, xent_slices_kernel<T>, (unsigned)(need < most ? need : most), dim3(256), 0,
+                       1, st, sums, count, slices, unit, out, vec);
 }
 
 XentTiles tiles_of(const XentArgs &a) {
@@ -833,7 +854,9 @@ cudaError_t xent_grad_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st)
   p.n = (int)up(a.dim, l.wide);
   p.slices = a.dx ? l.slices : 0;
   p.wk = (int)up(a.tokens, kPairK);
+  p.wslices = l.wslices;
   p.sums = reinterpret_cast<float *>(ws + l.sums);
+  p.wsums = reinterpret_cast<float *>(ws + l.wsums);
   p.dw = a.dw;
   p.unit = unit;
   const int kblocks = (int)up(a.dim, kPairK);
@@ -848,17 +871,15 @@ cudaError_t xent_grad_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st)
     p.words = words;
     p.k = (int)up(words, kPairK);
     p.wm = a.dw ? (int)up(words, kPairTile) : 0;
+    p.words_first = p.wk / p.wslices > p.k / (p.slices > 0 ? p.slices : 1);
     e = pair_launch<xent_products_kernel<T>>(
-        true, (long long)p.m * p.n * p.slices + (long long)p.wm * p.n, st, p, status);
+        true, (long long)p.m * p.n * p.slices + (long long)p.wm * p.n * p.wslices, st, p, status);
+    if (e == cudaSuccess && a.dw && p.wslices > 1)
+      e = add_slices(p.wsums, words * a.dim, p.wslices, unit, static_cast<T *>(a.dw) + t.v0 * a.dim, st);
     if (e != cudaSuccess) return e;
   }
   if (!a.dx) return cudaSuccess;
-  const long long count = a.tokens * a.dim;
-  const bool vec = a.dim % 4 == 0 && ((uintptr_t)a.dx & (4 * sizeof(T) - 1)) == 0;
-  const long long need = up(vec ? count / 4 : count, 256), most = (long long)sm_count() * 16;
-  return launch_kernel(true, xent_dx_kernel<T>, (unsigned)(need < most ? need : most), dim3(256), 0, 1,
-                       st, (const float *)p.sums, count, p.slices, (const float *)unit,
-                       static_cast<T *>(a.dx), vec);
+  return add_slices(p.sums, a.tokens * a.dim, p.slices, unit, static_cast<T *>(a.dx), st);
 }
 
 }  // namespace

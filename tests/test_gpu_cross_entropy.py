@@ -110,6 +110,12 @@ def test_pieces_of_the_vocabulary(fg, kind, tokens, vocabulary, dim):
     check(fg, *inputs(2, tokens, vocabulary, dim, kind))
 
 
+@pytest.mark.parametrize("kind,tokens,vocabulary,dim", [("f16", 30000, 300, 72), ("bf16", 40000, 257, 33),
+                                                        ("f32", 20000, 90, 100), ("bf16", 9000, 256, 520)])
+def test_few_words_for_many_tokens(fg, kind, tokens, vocabulary, dim):
+    check(fg, *inputs(17, tokens, vocabulary, dim, kind))
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_operands_off_their_boundaries(fg, kind):
     x, w, targets, dloss = inputs(3, 90, 400, 64, kind)
