@@ -5,10 +5,16 @@
 //
 // The gradient adds in one order whatever the timing: the tokens are sorted by
 // row, equal rows in the order of the tokens (embed_sort_kernel), cut into
-// pieces of 16 whatever the runs of equal rows are -- text has a few rows with
-// a tenth of all tokens -- and summed piece by piece (embed_sum_kernel); runs
-// that cross pieces leave one partial row per piece, which embed_join_kernel
-// adds in the order of the pieces.
+// pieces of 16 (more of many tokens) whatever the runs of equal rows are -- text
+// has a few rows with a tenth of all tokens -- and summed piece by piece
+// (embed_sum_kernel); runs that cross pieces leave one partial row per piece, which
+// embed_join_kernel adds in the order of the pieces.
+//
+// Measured: 16384 tokens of 2048 bf16 columns, looked up in 20.5 us (67 MB written,
+// 25 read of 6200 rows; 2 to 8 rows per thread or more blocks change nothing); their
+// gradient over 65536 rows 82 us: 268 MB of zeros with the sort beside them 48, the
+// sums 22 (67 MB read and rows written, 5 TB/s), the joins 11, a chain of six dependent
+// loads.  HBM bounds the first two.
 #include "cluster.cuh"
 #include "seq.h"
 
@@ -283,8 +289,9 @@ template <typename T, typename TO, bool VEC> struct Row {
 };
 
 // One warp per piece of the sorted tokens and chunk of columns.  ADD: rows that
-// end in the piece are loaded ahead too (half the piece at a time, for the
-// registers): one after the other their latency was three quarters of the time.
+// end in the piece are loaded ahead too (half a batch at a time, for the
+// registers): one after the other their latency was three quarters of the time
+// (5003 tokens of 1001 fp32 columns: 78 -> 9 us).
 template <typename T, typename TO, bool VEC, bool ADD, bool MANY>
 __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedSumArgs a) {
   using A = typename Acc<T>::type;

@@ -16,6 +16,9 @@
 // blocks of its cluster, which share the sequence and walk it together, a tile
 // each per step.  The maps carry the state to the front of each warp's tokens;
 // outputs follow from there by the recurrence as it stands.
+//
+// Measured (bf16): 32768 tokens of 4096 channels 170 us, 8 x 4096 tokens of 2048
+// channels backwards 175: 6.3 and 6.1 TB/s, 92% and 90% of a copy's rate.
 #pragma once
 
 #include <cuda.h>
@@ -25,6 +28,7 @@
 #include "cluster.cuh"
 #include "seq.h"
 #include "tcgen05.cuh"
+#include "tensor_map.h"
 
 namespace fftgb {
 namespace {
@@ -674,23 +678,6 @@ __global__ void __launch_bounds__(128) recur_step_kernel(const RecurArgs a) {
 
 // ---- launches ----------------------------------------------------------------------
 
-using RecurEncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-inline RecurEncodeFn recur_encode() {
-  static RecurEncodeFn fn = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return static_cast<RecurEncodeFn>(nullptr);
-    return reinterpret_cast<RecurEncodeFn>(p);
-  }();
-  return fn;
-}
-
 // The map of an array [sequence][token][channel] (packed: [1][row][channel])
 // in tiles of `tokens` x 128 channels; false where the TMA cannot take its rows.
 template <typename E>
@@ -698,7 +685,7 @@ bool recur_map(CUtensorMap *map, const void *p, const RecurStride &s, const Recu
   const long long seqs = a.offsets ? 1 : a.batch, bytes = (long long)sizeof(E);
   const long long tok = a.tokens > 1 ? s.tok * bytes : 16;
   const long long seq = seqs > 1 ? s.seq * bytes : tok;
-  RecurEncodeFn fn = recur_encode();
+  const TensorMapEncodeFn fn = tensor_map_encode();
   if (!fn || ((uintptr_t)p & 15) != 0 || a.channels % 4 != 0 || tok <= 0 || seq <= 0 || tok % 16 != 0 ||
       seq % 16 != 0 || tok >= (1ll << 40) || seq >= (1ll << 40) || a.tokens == 0)
     return false;

@@ -752,8 +752,8 @@ int fft_linear_recurrence_step(const fft_recurrence_desc *desc, const void *x, c
  *   dx, dw     tokens x dim and vocabulary x dim of type dtype, contiguous; each
  *              may be NULL.  Sums are float, rounded once.
  *   workspace  fft_linear_cross_entropy_workspace_bytes(..., backward = 1) bytes:
- *              G of up to 256 MB at a time (of 1024 words at least), a copy of x and a float dx
- *              (up to 32 of a small one).
+ *              G of up to 256 MB at a time (of 1024 words at least), a copy of x, and
+ *              float sums of dx (of dw for few words; up to 32 of small ones).
  * G takes part in the products in the operands' type (float: as they).  Tokens
  * without a target, or with a dloss of 0, take no part: what their rows of x
  * hold does not matter.
