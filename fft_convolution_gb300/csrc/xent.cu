@@ -793,8 +793,8 @@ cudaError_t xent_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st) {
   if (a.tokens <= 8ll * sm_count() && parts > 32)
     return launch_kernel(true, xent_join_kernel<8>, (unsigned)up(a.tokens, 8), dim3(1024), 0, 1, st, t,
                          a.loss, a.lse);
-  int threads = 32;  // 4 parts a thread, 1 to 8 threads a token
-  while (threads < 256 && threads / 32 * 4 < parts) threads *= 2;
+  int threads = 32;  // 4 parts a thread, 1 to 32 threads a token
+  while (threads < 1024 && threads / 32 * 4 < parts) threads *= 2;
   return launch_kernel(true, xent_join_kernel<32>, (unsigned)up(a.tokens, 32), dim3(threads), 0, 1, st,
                        t, a.loss, a.lse);
 }
