@@ -6,7 +6,9 @@ operands are exact, their sum of dim terms in float loses at most 2^-23 of the
 sizes summed per addition; float operands lose 2^-24 of each product more by the
 parts left out: e_l = (dim + 8) 2^-23 |x| . |w|.  lse and loss are off by the largest
 of their token's e_l, 2^-24 of the logits' largest size and 2^-21 (exponentials
-of 2^-22, summed) more.  G is off by (2 e_l + 2^-21 + 2^-22 |l - lse|) of
+of 2^-22, summed) more; and 4 * 2^-24 of lse, which is up to log V above the logits'
+size: the logarithm, its sum with the power of two, their product with ln 2 and that
+constant round by 2^-24 of it each.  G is off by (2 e_l + 2^-21 + 2^-22 |l - lse|) of
 e^{l - lse} c, is then rounded to the operands' type (float: three parts, 2^-24), and
 the two products add the sizes |G| |w| with 2^-23 per addition of rounding, before the
 results are rounded once.  In half, G has a power of two that brings the largest c to
@@ -56,7 +58,7 @@ def check(fg, x, w, targets, dloss, forward_only=False):
     want = torch.logsumexp(logits, 1)
     there = (targets >= 0) & (targets < w.shape[0])
     at = torch.where(there, targets, 0)[:, None]
-    tol = el.amax(1) + 2.0 ** -23 * logits.abs().amax(1) + 2.0 ** -21
+    tol = el.amax(1) + 2.0 ** -23 * logits.abs().amax(1) + 2.0 ** -21 + 2.0 ** -22 * want.abs()
     assert ((lse.double() - want).abs() <= tol).all()
     want_loss = torch.where(there, want - logits.gather(1, at)[:, 0], 0)
     assert ((loss.double() - want_loss).abs() <= 2 * tol).all()
