@@ -600,6 +600,9 @@ uint32_t idesc_of(bool half, int width, bool a_mn, bool b_mn) {
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 long long up(long long n, long long d) { return (n + d - 1) / d; }
+char *first_boundary(void *workspace) {
+  return reinterpret_cast<char *>(((uintptr_t)workspace + 255) & ~(uintptr_t)255);
+}
 
 // An operand as the loads can take it: the caller's array, or laid out in the workspace.
 struct Operand {
@@ -632,6 +635,8 @@ int tile_width(long long words, long long m) {
   return (int)best;
 }
 
+// Where everything lies, from the workspace's first 256-byte boundary on: G and the float
+// sums are stored 32 bytes at a time, and a caller's workspace is on 16.
 struct Layout {
   Operand x, w;
   int parts;
@@ -877,11 +882,11 @@ cudaError_t xent_grad_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st)
 }  // namespace
 
 size_t xent_workspace_bytes(int dtype, const XentArgs &a, bool grad) {
-  return a.tokens == 0 ? 0 : Layout(dtype, a, grad).bytes;
+  return a.tokens == 0 ? 0 : Layout(dtype, a, grad).bytes + 240;
 }
 
 cudaError_t launch_xent(int dtype, const XentArgs &a, void *workspace, cudaStream_t st) {
-  char *ws = static_cast<char *>(workspace);
+  char *ws = first_boundary(workspace);
   switch (dtype) {
     case FFT_ELEM_F32: return xent_t<float>(dtype, a, ws, st);
     case FFT_ELEM_BF16: return xent_t<__nv_bfloat16>(dtype, a, ws, st);
@@ -890,7 +895,7 @@ cudaError_t launch_xent(int dtype, const XentArgs &a, void *workspace, cudaStrea
 }
 
 cudaError_t launch_xent_grad(int dtype, const XentArgs &a, void *workspace, cudaStream_t st) {
-  char *ws = static_cast<char *>(workspace);
+  char *ws = first_boundary(workspace);
   if (a.tokens == 0)
     return a.dw ? cudaMemsetAsync(a.dw, 0, (size_t)a.vocabulary * a.dim * elem_bytes(dtype), st)
                 : cudaSuccess;
