@@ -144,14 +144,18 @@ __device__ __forceinline__ Pairs pair_up(float4 v) {
 __device__ __forceinline__ float4 quad(const Pairs &a) {
   return make_float4(a.p[0].x, a.p[0].y, a.p[1].x, a.p[1].y);
 }
-// A product of decays above float's range (g > 0) ends at its largest value,
-// which leaves a state of 0 alone where infinity would not.
+// A product of decays (all of them finite and none below 0), taken without bounds, as maps
+// hand it on. Above float's range (g > 0) it ends at the largest value, which leaves a
+// state of 0 alone where infinity would not. Infinity stays infinity under every factor
+// but 0, which makes it NaN for good: then the product has a factor of 0 and is 0. (A g
+// that is NaN or infinite shows in the map's other half.) A bound at every factor would
+// take 178.7 us instead of 171.7 for 32768 tokens of 4096 channels.
 __device__ __forceinline__ Pairs bounded(Pairs a) {
   constexpr float most = 3.402823466e38f;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    a.p[i].x = a.p[i].x > most ? most : a.p[i].x;
-    a.p[i].y = a.p[i].y > most ? most : a.p[i].y;
+    a.p[i].x = fminf(fmaxf(a.p[i].x, 0.0f), most);  // fmaxf(NaN, 0) is 0
+    a.p[i].y = fminf(fmaxf(a.p[i].y, 0.0f), most);
   }
   return a;
 }
