@@ -29,8 +29,8 @@ int embed_sizes(int64_t tokens, int64_t rows, int64_t dim, int dtype) {
 
 RecurStride stride(const int64_t s[2]) { return RecurStride{s[0], s[1]}; }
 
-// Sizes and types of a call of the recurrence.
-int recur_sizes(const fft_recurrence_desc *d, RecurArgs *a) {
+// Sizes and types of a call of the recurrence. Packed: `tokens` are those of all sequences.
+int recur_sizes(const fft_recurrence_desc *d, bool packed, RecurArgs *a) {
   if (!d || d->batch < 0 || d->tokens < 0 || d->channels <= 0 || !elem_type(d->dtype) ||
       !elem_type(d->gtype))
     return FFT_ERR_INVALID_ARG;
@@ -40,7 +40,7 @@ int recur_sizes(const fft_recurrence_desc *d, RecurArgs *a) {
   if (d->dtype == FFT_ELEM_F64 || (d->gtype != d->dtype && d->gtype != FFT_ELEM_F32) ||
       d->tokens > kMaxInt || d->channels > kMaxDim || d->batch > ((int64_t)1 << 24) ||
       (d->batch > 0 && (d->channels + 127) / 128 > kMaxInt / 8 / d->batch) ||
-      (d->tokens > 0 && d->batch > kMaxElems / d->tokens / d->channels))
+      (d->tokens > 0 && (packed ? 1 : d->batch) > kMaxElems / d->tokens / d->channels))
     return FFT_ERR_UNSUPPORTED;
   *a = RecurArgs{};
   a->sx = stride(d->x_stride);
@@ -55,8 +55,8 @@ int recur_sizes(const fft_recurrence_desc *d, RecurArgs *a) {
 
 // Those and the inputs.
 int recur_check(const fft_recurrence_desc *d, const void *x, const void *g, const void *beta,
-                bool x_used, RecurArgs *a) {
-  const int rc = recur_sizes(d, a);
+                bool x_used, bool packed, RecurArgs *a) {
+  const int rc = recur_sizes(d, packed, a);
   if (rc != FFT_OK) return rc;
   if (d->batch > 0 && d->tokens > 0 && ((x_used && !x) || !g)) return FFT_ERR_INVALID_ARG;
   if (off_element(x, d->dtype) || off_element(g, d->gtype) || off_element(beta, d->gtype))
@@ -155,7 +155,7 @@ int fft_embedding_backward(const void *dy, int64_t lddy, const void *ids, int id
 
 size_t fft_linear_recurrence_workspace_bytes(const fft_recurrence_desc *desc, int packed) {
   RecurArgs a;
-  if (!desc || recur_sizes(desc, &a) != FFT_OK || a.batch == 0) return 0;
+  if (!desc || recur_sizes(desc, packed != 0, &a) != FFT_OK || a.batch == 0) return 0;
   return recur_workspace_bytes(a.batch, packed != 0);
 }
 
@@ -164,7 +164,7 @@ int fft_linear_recurrence(const fft_recurrence_desc *desc, const void *x, const 
                           void *y, float *final_state, void *workspace, size_t workspace_bytes,
                           void *stream) {
   RecurArgs a;
-  int rc = recur_check(desc, x, g, beta, true, &a);
+  int rc = recur_check(desc, x, g, beta, true, offsets != nullptr, &a);
   if (rc != FFT_OK) return rc;
   a.clear = a.clear && offsets && a.tokens > 0;
   if (a.batch == 0 && !a.clear) return FFT_OK;
@@ -195,7 +195,7 @@ int fft_linear_recurrence_backward(const fft_recurrence_desc *desc, const void *
                                    float *dinitial_state, void *workspace,
                                    size_t workspace_bytes, void *stream) {
   RecurArgs a;
-  int rc = recur_check(desc, x, g, beta, beta != nullptr, &a);
+  int rc = recur_check(desc, x, g, beta, beta != nullptr, offsets != nullptr, &a);
   if (rc != FFT_OK) return rc;
   a.clear = a.clear && offsets && a.tokens > 0;
   if (a.batch == 0 && !a.clear) return FFT_OK;
@@ -237,7 +237,7 @@ int fft_linear_recurrence_step(const fft_recurrence_desc *desc, const void *x, c
                                const void *beta, float *state, const int32_t *slots, int64_t pool,
                                void *y, void *stream) {
   RecurArgs a;
-  const int rc = recur_check(desc, x, g, beta, true, &a);
+  const int rc = recur_check(desc, x, g, beta, true, false, &a);
   if (rc != FFT_OK) return rc;
   if (pool < 0 || (!slots && pool < desc->batch)) return FFT_ERR_INVALID_ARG;
   if (a.batch == 0 || a.tokens == 0) return FFT_OK;
