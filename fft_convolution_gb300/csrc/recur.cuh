@@ -196,7 +196,7 @@ struct RecurShared {
 constexpr size_t kRecurShared = (sizeof(RecurShared) + 127) / 128 * 128;
 // Behind it the stages: of each input a tile of tokens x 128 channels.
 
-__device__ __forceinline__ void exchange_begin(RecurShared &sh, int blocks) {
+__device__ __forceinline__ void exchange_begin(RecurShared &sh) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) bar_init(&sh.full[i], 1);
     bar_init(&sh.sent[0], 1);
@@ -205,7 +205,13 @@ __device__ __forceinline__ void exchange_begin(RecurShared &sh, int blocks) {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
-  if (blocks > 1) cluster_sync();  // every block's shared memory is there
+}
+
+// Every block's shared memory is there, and what it reads of the first state has been read:
+// the last state, which one of them writes, may lie in the same place.
+__device__ __forceinline__ void exchange_ready(int blocks) {
+  __syncwarp();
+  if (blocks > 1) cluster_sync();
 }
 
 // A lane's share of an exchange: channels 4 quad .. of the tile, for the block
@@ -399,7 +405,7 @@ recur_kernel(const RecurArgs a, const __grid_constant__ RecurMaps maps, int *sta
   const G *b = GATED ? static_cast<const G *>(a.beta) + sq * a.sb.seq + from * a.sb.tok : nullptr;
   T *y = static_cast<T *>(a.y) + r.begin * C;
   const int step = a.blocks * P::kTokens;
-  exchange_begin(sh, a.blocks);
+  exchange_begin(sh);
 
   // The tile of step n, from its first token on: the TMA for the whole block
   // (thread 0), or this lane's part of it.
@@ -431,6 +437,7 @@ recur_kernel(const RecurArgs a, const __grid_constant__ RecurMaps maps, int *sta
   const Share my = my_share();
   load_state<VEC>(state, a.state_in ? a.state_in + seq * C : nullptr, c0, my.quad, C);
   Pairs carry = pair_up(state);
+  exchange_ready(a.blocks);
   uint32_t n = 0;
   for (long long at = 0; at < r.len; at += step, ++n) {
     const long long t0 = at + rank * P::kTokens + warp * K;
@@ -538,7 +545,7 @@ recur_grad_kernel(const RecurArgs a, const __grid_constant__ RecurMaps maps, int
   G *dg = static_cast<G *>(a.dg) + r.begin * C;
   G *db = GATED ? static_cast<G *>(a.dbeta) + r.begin * C : nullptr;
   const int step = a.blocks * P::kTokens;
-  exchange_begin(sh, a.blocks);
+  exchange_begin(sh);
 
   auto fetch = [&](uint32_t n) {
     const long long last = r.len - 1 - ((long long)n * step + rank * P::kTokens);  // its last token
@@ -578,6 +585,7 @@ recur_grad_kernel(const RecurArgs a, const __grid_constant__ RecurMaps maps, int
   const Share my = my_share();
   load_state<VEC>(state, a.dfinal ? a.dfinal + seq * C : nullptr, c0, my.quad, C);
   Pairs carry = pair_up(state);
+  exchange_ready(a.blocks);
   uint32_t n = 0;
   for (long long at = 0; at < r.len; at += step, ++n) {
     const long long t0 = r.len - 1 - at - rank * P::kTokens - warp * K;
