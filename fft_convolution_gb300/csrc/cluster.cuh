@@ -58,19 +58,32 @@ __device__ __forceinline__ bool poll_cluster(uint64_t *bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-// A wait for it that ends after some seconds, or when `failed` (shared memory) says
+// A wait for it that ends after `limit` clocks, or when `failed` (shared memory) says
 // that another of the block's has; `status`: the device status word.
 __device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *failed,
-                                             int *status) {
+                                             int *status, long long limit) {
   if (poll_cluster(bar, parity)) return true;
   const long long t0 = clock64();
+#pragma unroll 1
   for (uint32_t it = 0; it < (1u << 24); ++it) {
     if (poll_cluster(bar, parity)) return true;
-    if (*failed || clock64() - t0 > 8000000000ll) break;  // about 4 s
+    if (*failed || clock64() - t0 > limit) break;
   }
   *failed = 1;
   atomicExch(status, 1);  // kDeviceErrorTimeout
   return false;
+}
+
+// How a block that has given up leaves: its own copies, which take microseconds, are waited for,
+// some milliseconds at most (a barrier that has been given up may never complete).
+__device__ __forceinline__ void let_land(uint64_t *bar, uint32_t parity) {
+#pragma unroll 1
+  for (int it = 0; it < 4096 && !bar_poll(bar, parity); ++it) __nanosleep(2048);
+}
+// And what other blocks have sent it, which it does not count any more, gets about 60 us.
+__device__ __forceinline__ void linger() {
+#pragma unroll 1
+  for (int it = 0; it < 64; ++it) __nanosleep(1024);
 }
 
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {

@@ -216,6 +216,7 @@ int fft_debug_set_option(int option, int64_t value) {
     case FFT_OPT_PASS_SHFL: ok = value <= 1; break;
     case FFT_OPT_CLUSTER_LOG_MIN: ok = value >= 11 && value <= 13; break;
     case FFT_OPT_COL_RADIX_LOG: ok = value <= 3; break;
+    case FFT_OPT_STARVED_WAIT: ok = value >= 1 && value <= 4; break;
     default: ok = false;
   }
   return ok && set_option(option, value) ? FFT_OK : FFT_ERR_INVALID_ARG;

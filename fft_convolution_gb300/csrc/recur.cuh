@@ -33,7 +33,7 @@
 namespace fftgb {
 namespace {
 
-constexpr int kRecurWarps = 8, kRecurThreads = 256, kRecurWide = 128, kRecurBlocks = 8;
+constexpr int kRecurWarps = 8, kRecurThreads = 256, kRecurWide = 128, kRecurBlocks = 8, kRecurStages = 2;
 
 // Four channels of a lane: adjacent ones (VEC: what the TMA brings as rows of 128
 // channels), or 32 apart, which the lane's own copies put there.
@@ -187,7 +187,7 @@ struct RecurShared {
   float4 warp_a[kRecurWarps][32], warp_h[kRecurWarps][32];
   float4 block_a[2][kRecurBlocks][32], block_h[2][kRecurBlocks][32];
   float4 state[kRecurWarps][32];
-  uint64_t full[4];  // the stages' tiles have come
+  uint64_t full[kRecurStages];  // the stages' tiles have come
   uint64_t sent[2];  // the blocks' maps have come
   // A wait has run out: for a tile, for maps.  All threads look at each behind a
   // barrier that everyone who may set it has passed, so they leave together.
@@ -196,11 +196,11 @@ struct RecurShared {
 constexpr size_t kRecurShared = (sizeof(RecurShared) + 127) / 128 * 128;
 // Behind it the stages: of each input a tile of tokens x 128 channels.
 
-__device__ __forceinline__ void exchange_begin(RecurShared &sh) {
+__device__ __forceinline__ void exchange_begin(RecurShared &sh, const Waits &waits) {
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 4; ++i) bar_init(&sh.full[i], 1);
-    bar_init(&sh.sent[0], 1);
-    bar_init(&sh.sent[1], 1);
+    const int starved = blockIdx.x == 0 ? waits.starved : 0;  // one arrival more than will come
+    for (int i = 0; i < kRecurStages; ++i) bar_init(&sh.full[i], starved == 1 + i ? 2 : 1);
+    for (int i = 0; i < 2; ++i) bar_init(&sh.sent[i], starved == 3 + i ? 2 : 1);
     sh.failed[0] = sh.failed[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -212,6 +212,15 @@ __device__ __forceinline__ void exchange_begin(RecurShared &sh) {
 __device__ __forceinline__ void exchange_ready(int blocks) {
   __syncwarp();
   if (blocks > 1) cluster_sync();
+}
+
+// No block leaves before the others have sent their last map, and none that has given up before
+// those have come.
+__device__ __forceinline__ void exchange_end(const RecurShared &sh, int blocks) {
+  __syncwarp();
+  if (blocks == 1) return;
+  cluster_sync();
+  if (sh.failed[0] | sh.failed[1]) linger();
 }
 
 // A lane's share of an exchange: channels 4 quad .. of the tile, for the block
@@ -233,7 +242,7 @@ __device__ __forceinline__ Share my_share() {
 template <class Between>
 __device__ __forceinline__ bool exchange(RecurShared &sh, uint32_t n, int rank, int blocks,
                                          const Pairs &A, const Pairs &H, Pairs &carry, Pairs &s,
-                                         int *status, Between between) {
+                                         int *status, long long limit, Between between) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, parity = n & 1;
   const Share my = my_share();
   sh.warp_a[warp][lane] = quad(bounded(A));
@@ -260,7 +269,7 @@ __device__ __forceinline__ bool exchange(RecurShared &sh, uint32_t n, int rank, 
       peer_send(peer(smem_u32(&sh.block_a[parity][rank][my.quad]), my.to), quad(bounded(all_a)), bar);
       peer_send(peer(smem_u32(&sh.block_h[parity][rank][my.quad]), my.to), quad(all_h), bar);
     }
-    wait_cluster(&sh.sent[parity], (n >> 1) & 1, &sh.failed[1], status);
+    wait_cluster(&sh.sent[parity], (n >> 1) & 1, &sh.failed[1], status, limit);
     s = carry;
 #pragma unroll
     for (int r = 0; r < kRecurBlocks; ++r)
@@ -359,7 +368,7 @@ struct RecurMaps {
 // are all start and end: small tiles, two blocks per SM (4096 sequences of 16 tokens,
 // 1024 channels: 743 -> 273 us, 512 of 64 107 -> 63, 256 of 128 65 -> 57, but 64 of
 // 1024 92 -> 104).
-constexpr int kRecurStages = 2, kRecurShort = 192;
+constexpr int kRecurShort = 192;
 constexpr int recur_tokens(int bytes, bool is_short) {
   return is_short ? (bytes <= 40 ? 4 : 2) : bytes <= 24 ? 16 : bytes <= 48 ? 8 : 4;
 }
@@ -405,7 +414,7 @@ recur_kernel(const RecurArgs a, const __grid_constant__ RecurMaps maps, int *sta
   const G *b = GATED ? static_cast<const G *>(a.beta) + sq * a.sb.seq + from * a.sb.tok : nullptr;
   T *y = static_cast<T *>(a.y) + r.begin * C;
   const int step = a.blocks * P::kTokens;
-  exchange_begin(sh);
+  exchange_begin(sh, a.waits);
 
   // The tile of step n, from its first token on: the TMA for the whole block
   // (thread 0), or this lane's part of it.
@@ -445,7 +454,7 @@ recur_kernel(const RecurArgs a, const __grid_constant__ RecurMaps maps, int *sta
     Pairs e[K], u[K], A = splat(1.0f), H = splat(0.0f), h;
     if constexpr (VEC) {
       if (at + rank * P::kTokens < r.len)
-        wait_cluster(&sh.full[n % S], (n / S) & 1, &sh.failed[0], status);
+        wait_cluster(&sh.full[n % S], (n / S) & 1, &sh.failed[0], status, a.waits.limit);
     } else {
       copy_wait<S - 1>();
     }
@@ -461,7 +470,7 @@ recur_kernel(const RecurArgs a, const __grid_constant__ RecurMaps maps, int *sta
       }
     }
     if constexpr (!VEC) fetch(n + S);
-    if (!exchange(sh, n, rank, a.blocks, A, H, carry, h, status, [&] {
+    if (!exchange(sh, n, rank, a.blocks, A, H, carry, h, status, a.waits.limit, [&] {
           if constexpr (VEC) fetch(n + S);  // every warp has read the tile
         }))
       break;
@@ -480,11 +489,19 @@ recur_kernel(const RecurArgs a, const __grid_constant__ RecurMaps maps, int *sta
     unpair(carry, state);
     store_state<VEC>(a.state_out + seq * C, c0, my.quad, C, state);
   }
-  if (VEC && tid == 0 && (sh.failed[0] | sh.failed[1]))  // given up: no copy may land after the block has gone
-    for (uint32_t i = n; i < n + S; ++i)
-      if ((long long)i * step + rank * P::kTokens < r.len) bar_wait(&sh.full[i % S], (i / S) & 1);
-  __syncwarp();
-  if (a.blocks > 1) cluster_sync();  // nor a map come to one that has
+  // Given up: no copy may land after the block has gone. Tiles n .. n + S - 1 have been asked
+  // for, and the one behind them where the step came as far as the blocks' maps.
+  if (sh.failed[0] | sh.failed[1]) {
+    if constexpr (VEC) {
+      const uint32_t end = n + S + (sh.failed[1] ? 1 : 0);
+#pragma unroll 1
+      for (uint32_t i = n; tid == 0 && i < end; ++i)
+        if ((long long)i * step + rank * P::kTokens < r.len) let_land(&sh.full[i % S], (i / S) & 1);
+    } else {
+      copy_wait_all();
+    }
+  }
+  exchange_end(sh, a.blocks);
 }
 
 // The same from the end: tile n has the tokens behind those of tile n + 1, and a
@@ -545,7 +562,7 @@ recur_grad_kernel(const RecurArgs a, const __grid_constant__ RecurMaps maps, int
   G *dg = static_cast<G *>(a.dg) + r.begin * C;
   G *db = GATED ? static_cast<G *>(a.dbeta) + r.begin * C : nullptr;
   const int step = a.blocks * P::kTokens;
-  exchange_begin(sh);
+  exchange_begin(sh, a.waits);
 
   auto fetch = [&](uint32_t n) {
     const long long last = r.len - 1 - ((long long)n * step + rank * P::kTokens);  // its last token
@@ -594,7 +611,7 @@ recur_grad_kernel(const RecurArgs a, const __grid_constant__ RecurMaps maps, int
     Pairs e[K], d[K], A = splat(1.0f), H = splat(0.0f), m;
     if constexpr (VEC) {
       if (at + rank * P::kTokens < r.len)
-        wait_cluster(&sh.full[n % S], (n / S) & 1, &sh.failed[0], status);
+        wait_cluster(&sh.full[n % S], (n / S) & 1, &sh.failed[0], status, a.waits.limit);
     } else {
       copy_wait<S - 1>();
     }
@@ -607,7 +624,7 @@ recur_grad_kernel(const RecurArgs a, const __grid_constant__ RecurMaps maps, int
         A = A * e[j];
         H = fma4(e[j], H, e[j] * d[j]);
       }
-    if (!exchange(sh, n, rank, a.blocks, A, H, carry, m, status, [&] {
+    if (!exchange(sh, n, rank, a.blocks, A, H, carry, m, status, a.waits.limit, [&] {
           // every warp is done with the tile before this one
           if (VEC && n > 0) fetch(n - 1 + S);
         }))
@@ -646,11 +663,18 @@ recur_grad_kernel(const RecurArgs a, const __grid_constant__ RecurMaps maps, int
     unpair(carry, state);
     store_state<VEC>(a.dinitial + seq * C, c0, my.quad, C, state);
   }
-  if (VEC && tid == 0 && (sh.failed[0] | sh.failed[1]))
-    for (uint32_t i = n; i < n + S; ++i)
-      if ((long long)i * step + rank * P::kTokens < r.len) bar_wait(&sh.full[i % S], (i / S) & 1);
-  __syncwarp();
-  if (a.blocks > 1) cluster_sync();
+  // Given up, as forward: tile n - 1 + S has been asked for in step n, as far as that came.
+  if (sh.failed[0] | sh.failed[1]) {
+    if constexpr (VEC) {
+      const uint32_t end = n + S - (sh.failed[0] && n > 0 ? 1 : 0);
+#pragma unroll 1
+      for (uint32_t i = n; tid == 0 && i < end; ++i)
+        if ((long long)i * step + rank * P::kTokens < r.len) let_land(&sh.full[i % S], (i / S) & 1);
+    } else {
+      copy_wait_all();
+    }
+  }
+  exchange_end(sh, a.blocks);
 }
 
 // Single tokens: a thread has four channels of a sequence.
@@ -732,6 +756,7 @@ cudaError_t launch_clusters(F *kern, RecurArgs a, const RecurMaps &maps, int tok
   // Sequences share a GPU of many SMs: more blocks along one while there is
   // room for them and it has tokens for them.
   const long long mean = a.offsets ? (a.tokens + a.batch - 1) / a.batch : a.tokens;
+  a.waits = waits_now();
   a.blocks = 1;
   while (a.blocks < kRecurBlocks && units * a.blocks * 2 <= room &&
          mean > (long long)a.blocks * tokens)

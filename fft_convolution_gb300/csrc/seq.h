@@ -155,6 +155,17 @@ cudaError_t launch_embed_grad(int dtype, int ttype, const EmbedGradArgs &a, void
 
 // ---- the gated linear recurrence (recur_*.cu) ---------------------------------------
 
+// How long waits inside kernels may take, in clocks, and (FFT_OPT_STARVED_WAIT) which barrier
+// of the first block never completes: 0, none.
+struct Waits {
+  long long limit;
+  int starved;
+};
+inline Waits waits_now() {
+  const long long starved = option(FFT_OPT_STARVED_WAIT);
+  return starved > 0 ? Waits{1ll << 21, (int)starved} : Waits{8000000000ll, 0};  // about 4 s
+}
+
 // Strides in elements: sequence (unused for packed rows) and token.
 struct RecurStride {
   long long seq, tok;
@@ -172,6 +183,7 @@ struct RecurArgs {
   int blocks;  // of a cluster, which share a sequence's tokens
   int *rows;   // packed, many sequences: 2 (batch + 1) entries, the first half of which
                // become the sequences' first rows; else null
+  Waits waits;
   // Single tokens: the sequence's row of a pool of `pool` states (null: row = sequence).
   const int *slots;
   long long pool;

@@ -40,3 +40,10 @@ def test_packed_rows_have_a_limit(fg):
     d = recurrence(fg, 1025, 2 ** 31 - 1, 2 ** 16)
     assert fg.fft_linear_recurrence_workspace_bytes(d, 1) == 0
     assert fg.fft_linear_recurrence(d, P, P, P, P, None, P, P, P, 1 << 40, None) == fg.FFT_ERR_UNSUPPORTED
+
+
+def test_starved_waits_are_named(fg):
+    for barrier in (0, 5):
+        assert fg.fft_debug_set_option(fg.FFT_OPT_STARVED_WAIT, barrier) == fg.FFT_ERR_INVALID_ARG
+    for value in (1, 4, -1):
+        assert fg.fft_debug_set_option(fg.FFT_OPT_STARVED_WAIT, value) == fg.FFT_OK
