@@ -92,12 +92,13 @@ __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t parity, volatile int *failed,
-                                          int *status) {
+                                          int *status, long long limit) {
   if (bar_poll(bar, parity)) return true;
   const long long t0 = clock64();
+#pragma unroll 1
   for (uint32_t it = 0; it < (1u << 24); ++it) {
     if (bar_poll(bar, parity)) return true;
-    if (*failed || clock64() - t0 > 8000000000ll) break;  // about 4 s
+    if (*failed || clock64() - t0 > limit) break;
   }
   *failed = 1;
   atomicExch(status, 1);  // kDeviceErrorTimeout
@@ -144,6 +145,7 @@ struct PairOperands {
   // Products of parts: an fp32 operand is the sum of three bf16 parts, of
   // which the six largest products are taken, the smallest first.
   int parts;
+  Waits waits;  // of a launch: its first problem's
 };
 __device__ __forceinline__ int part_pairs(int parts) { return parts == 1 ? 1 : 6; }
 __device__ __forceinline__ void part_pair(int parts, int q, int &pa, int &pb) {
@@ -174,14 +176,16 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
   const uint32_t rank = block_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   volatile int *failed = &sh.failed;
+  const long long limit = ops[0].waits.limit;
   if (tid == 0) {
+    const int starved = blockIdx.x == 0 ? ops[0].waits.starved : 0;  // one arrival more than will come
     for (int s = 0; s < kPairStages; ++s) {
-      bar_init(&sh.full[s], 1);
-      bar_init(&sh.empty[s], 1);
+      bar_init(&sh.full[s], starved == 1 && s == 0 ? 2 : 1);
+      bar_init(&sh.empty[s], starved == 2 && s == 0 ? 2 : 1);
     }
     for (int i = 0; i < 2; ++i) {
-      bar_init(&sh.ready[i], 1);
-      bar_init(&sh.taken[i], 2 * kOutWarps);
+      bar_init(&sh.ready[i], starved == 3 && i == 0 ? 2 : 1);
+      bar_init(&sh.taken[i], 2 * kOutWarps + (starved == 4 && i == 0 ? 1 : 0));
     }
     bar_init(&sh.done, 1);
     sh.failed = 0;
@@ -212,7 +216,7 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
             int pa, pb;
             part_pair(p.parts, q, pa, pb);
             for (int kb = w.k0; kb < w.k1; ++kb) {
-              if (round > 0 && !wait_pair(&sh.empty[s], (round - 1) & 1, failed, status)) {
+              if (round > 0 && !wait_pair(&sh.empty[s], (round - 1) & 1, failed, status, limit)) {
                 ok = false;
                 break;
               }
@@ -241,8 +245,8 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
         for (uint32_t i = 0; i < stages; ++i) {
           if (i >= s && round == 0) break;
           const uint32_t last = (i < s ? round : round - 1) & 1;
-          if (ok) wait_pair(&sh.empty[i], last, failed, status);
-          else if (rank == 0) bar_wait(&sh.full[i], last);
+          if (ok) wait_pair(&sh.empty[i], last, failed, status, limit);
+          else if (rank == 0) let_land(&sh.full[i], last);
         }
       }
     } else if (warp == 1 && rank == 0) {
@@ -258,13 +262,13 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
           const uint32_t step_a = p.a_mn ? 2048 : 32, step_b = p.b_mn ? 2048 : 32;
           for (int b0 = 0; ok && b0 < blocks; b0 += kSumBlocks, ++n) {
             const int acc = n & 1, count = min(kSumBlocks, blocks - b0);
-            if (n > 1 && !wait_pair(&sh.taken[acc], ((n >> 1) - 1) & 1, failed, status)) {
+            if (n > 1 && !wait_pair(&sh.taken[acc], ((n >> 1) - 1) & 1, failed, status, limit)) {
               ok = false;
               break;
             }
             tc_fence_after();
             for (int kb = 0; kb < count; ++kb) {
-              if (!wait_pair(&sh.full[s], round & 1, failed, status)) {
+              if (!wait_pair(&sh.full[s], round & 1, failed, status, limit)) {
                 ok = false;
                 break;
               }
@@ -282,7 +286,7 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
         }
         if (*failed) {  // no product may write tensor memory that has been given back
           pair_commit(&sh.done);
-          bar_wait(&sh.done, 0);
+          let_land(&sh.done, 0);
         }
       }
     }
@@ -301,7 +305,8 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
       for (int i = 0; i < kPairTile / 2; ++i) sums[i] = 0.0f;
       for (int b0 = 0; b0 < blocks; b0 += kSumBlocks, ++n) {
         const int acc = n & 1;
-        ok = wait_pair(&sh.ready[acc], (n >> 1) & 1, failed, status);
+        // a warp reads on or leaves as one: lanes may see the end of a wait differently
+        ok = __all_sync(0xffffffffu, wait_pair(&sh.ready[acc], (n >> 1) & 1, failed, status, limit));
         if (!ok) break;
         __syncwarp();
         tc_fence_after();
@@ -326,7 +331,13 @@ __device__ __forceinline__ void pair_run(const PairOperands *ops, int tiles, int
   }
   __syncwarp();
   __syncthreads();
+  // Given up: what this block has on its way to the other (its loads count there, its products'
+  // ends too), and what the other has on its way here, lands before either goes.
+  if (*failed) linger();
+  __syncwarp();
   cluster_sync();
+  if (*failed) linger();
+  __syncwarp();
   if (warp == 2) pair_tmem_free(tm);
 }
 

@@ -783,6 +783,7 @@ cudaError_t xent_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st) {
   ops.b_bytes = (uint32_t)l.width / 2 * 128;
   ops.idesc = idesc_of(half, l.width, false, false);
   ops.parts = l.parts;
+  ops.waits = waits_now();
   XentTiles t = tiles_of(a);
   t.width = l.width;
   t.part = l.part;
@@ -844,6 +845,7 @@ cudaError_t xent_grad_t(int dtype, const XentArgs &a, char *ws, cudaStream_t st)
   p.ops[0].idesc = idesc_of(half, l.wide, false, true);
   p.ops[1].idesc = idesc_of(half, l.wide, true, true);
   ops.parts = p.ops[0].parts = p.ops[1].parts = l.parts;
+  ops.waits = p.ops[0].waits = waits_now();
   p.tokens = a.tokens;
   p.dim = a.dim;
   p.m = t.m;

@@ -440,12 +440,15 @@ int fft_debug_cluster_timeout(void *data, int64_t polls, void *stream);
                                      column to one warp and exchange by warp shuffles (tiles
                                      loaded and stored with the TMA's 64-byte swizzle);
                                      0 = shared-memory exchanges */
-#define FFT_OPT_STARVED_WAIT 10   /* launch: test hook of the linear recurrence's waits.  The
-                                     first block gets one barrier that never completes (1, 2:
-                                     a tile of the first, second stage; 3, 4: the blocks' maps
-                                     of even, odd steps) and no wait lasts longer than 2^21
-                                     clocks: the call's results are undefined, and
-                                     fft_device_status says FFT_ERR_DEVICE_TIMEOUT */
+#define FFT_OPT_STARVED_WAIT 10   /* launch: test hook of the waits of the linear recurrence
+                                     and the cross entropy of a linear layer.  The first block
+                                     gets one barrier that never completes (recurrence: 1, 2 a
+                                     tile of the first, second stage, 3, 4 the blocks' maps of
+                                     even, odd steps; cross entropy: 1 operands, 2 their stage
+                                     free again, 3 sums made, 4 sums read) and no wait lasts
+                                     longer than 2^21 clocks: the call's results are undefined,
+                                     and fft_device_status says FFT_ERR_DEVICE_TIMEOUT if the
+                                     barrier was waited for */
 int fft_debug_set_option(int option, int64_t value);
 
 /* ---- Operators of sequence models --------------------------------------------

@@ -1,8 +1,9 @@
-"""The waits inside the linear recurrence's kernels run out: a barrier of the first
-block expects one arrival more than will come (FFT_OPT_STARVED_WAIT).  The call
-ends, the device status word says so, and the next call on the context is right.
-Nothing is read or written out of place meanwhile: copies and maps that are on
-their way land before their block leaves."""
+"""The waits inside the kernels of the linear recurrence and the cross entropy of a
+linear layer run out: a barrier of the first block expects one arrival more than
+will come (FFT_OPT_STARVED_WAIT).  The call ends, the device status word says so,
+and the next call on the context is right.  Nothing is read or written out of
+place meanwhile: copies, maps and products that are on their way land before
+their block leaves."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -43,4 +44,27 @@ def test_recurrence(fg, opt, batch, tokens, channels, kind, gated, barrier):
         opt("STARVED_WAIT", -1)
         assert fg.fft_device_status(stream) == fg.FFT_OK
         assert all(a is None and b is None or torch.equal(a, b) for a, b in zip(run(), want))
+    assert fg.fft_device_status(stream) == fg.FFT_OK
+
+
+# tiles of tokens x words, of words x few tokens; one tile for a pair of blocks and many; three parts of fp32 operands
+@pytest.mark.parametrize("barrier", [1, 2, 3, 4])
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("tokens,vocabulary,dim", [(300, 2100, 1600), (40, 3000, 1600), (3000, 20000, 136)])
+def test_cross_entropy(fg, opt, tokens, vocabulary, dim, kind, barrier):
+    x, w = torch.randn(tokens, dim, device="cuda").to(TYPES[kind]), 0.1 * torch.randn(vocabulary, dim, device="cuda")
+    w, targets = w.to(TYPES[kind]), torch.randint(-1, vocabulary, (tokens,), device="cuda")
+    dloss = torch.rand(tokens, device="cuda")
+    run = lambda: (lambda loss, lse: (loss, lse, *fg.linear_cross_entropy_backward(dloss, x, w, targets, lse)))(  # noqa: E731
+        *fg.linear_cross_entropy(x, w, targets))
+    want, stream = run(), torch.cuda.current_stream().cuda_stream
+    assert fg.fft_device_status(stream) == fg.FFT_OK
+    for call in (lambda: fg.linear_cross_entropy(x, w, targets),
+                 lambda: fg.linear_cross_entropy_backward(dloss, x, w, targets, want[1])):
+        opt("STARVED_WAIT", barrier)
+        call()
+        assert fg.fft_device_status(stream) == fg.FFT_ERR_DEVICE_TIMEOUT
+        opt("STARVED_WAIT", -1)
+        assert fg.fft_device_status(stream) == fg.FFT_OK
+        assert all(torch.equal(a, b) for a, b in zip(run(), want))
     assert fg.fft_device_status(stream) == fg.FFT_OK
