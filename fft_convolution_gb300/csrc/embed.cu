@@ -11,10 +11,11 @@
 // embed_join_kernel adds in the order of the pieces.
 //
 // Measured: 16384 tokens of 2048 bf16 columns, looked up in 20.5 us (67 MB written,
-// 25 read of 6200 rows; 2 to 8 rows per thread or more blocks change nothing); their
-// gradient over 65536 rows 82 us: 268 MB of zeros with the sort beside them 48, the
-// sums 22 (67 MB read and rows written, 5 TB/s), the joins 11, a chain of six dependent
-// loads.  HBM bounds the first two.
+// 25 read of 6200 rows; 2 to 8 rows per thread or more blocks change nothing: it waits
+// for the rows, at 27% of HBM's rate, and most of what it writes is still in the L2 when
+// it ends); their gradient over 65536 rows 83 us: 268 MB of zeros with the sort beside
+// them 48, which HBM bounds, the sums 22 (67 MB read and rows written), the joins 11, a
+// chain of six dependent loads.
 #include "cluster.cuh"
 #include "seq.h"
 
@@ -550,9 +551,11 @@ cudaError_t launch_embed_grad(int dtype, int ttype, const EmbedGradArgs &g, void
     s.key[i] = reinterpret_cast<unsigned *>(ws + 2 * i * list);
     s.pos[i] = reinterpret_cast<unsigned *>(ws + (2 * i + 1) * list);
   }
-  // 16 blocks where the sort takes longer than the zeros beside it (65536 tokens of 1024
-  // columns 130 -> 106 us, 10^6 of 64 955 -> 546, but 16384 of 2048 82 -> 87 and 30000 of
-  // 4096 224 -> 240).
+  // 16 blocks from 32768 tokens on, whatever is beside the sort. Above: 65536 tokens of 1024
+  // columns 130 -> 105 us (added to a table 159 -> 133), 36000 added 104 -> 91, 10^6 of 64
+  // columns 955 -> 546. Below, where zeros hide the sort, they hold these back: 16384 of 2048
+  // 90 -> 91, 30000 of 4096 over 65536 rows 183 -> 192. Without many zeros 8 blocks lose there
+  // too: 30000 of 1024 added 77 -> 89, of 256 over 2000 rows 44 -> 52; 5003 added are even.
   s.blocks = g.tokens > 32768 ? kSortMost : 8;
   s.crossing = reinterpret_cast<unsigned *>(ws + 4 * list);
   int bits = 0;  // of the largest key, which is `rows`

@@ -17,8 +17,9 @@
 // each per step.  The maps carry the state to the front of each warp's tokens;
 // outputs follow from there by the recurrence as it stands.
 //
-// Measured (bf16): 32768 tokens of 4096 channels 170 us, 8 x 4096 tokens of 2048
-// channels backwards 175: 6.3 and 6.1 TB/s, 92% and 90% of a copy's rate.
+// Measured (bf16): 32768 tokens of 4096 channels 173 us, 8 x 4096 tokens of 2048
+// channels backwards 176: 6.2 and 6.1 TB/s, 91% and 90% of a copy's rate.  In float
+// 314 and 313, a copy's rate.
 #pragma once
 
 #include <cuda.h>
@@ -118,8 +119,8 @@ __device__ __forceinline__ Pairs fma4(const Pairs &a, const Pairs &b, const Pair
   return Pairs{{fma2(a.p[0], b.p[0], c.p[0]), fma2(a.p[1], b.p[1], c.p[1])}};
 }
 __device__ __forceinline__ Pairs splat(float v) { return Pairs{{both(v), both(v)}}; }
-// e^g as 2^(g log2 e): both off by about 2^-23, the rounding of the product by
-// |g| 2^-24 more, and no rounding of its own as expf has (eight instructions).
+// e^g as 2^(g log2 e): off by about 2^-23, and by |g| 2^-24 more through the product's
+// rounding.
 __device__ __forceinline__ Pairs decay(const Pairs &g) {
   Pairs t = g * splat(1.4426950408889634f);
 #pragma unroll
@@ -367,7 +368,9 @@ struct RecurMaps {
 // channels in bf16: 170 us with 16 tokens, 252 with 8, 301 with 4).  SHORT sequences
 // are all start and end: small tiles, two blocks per SM (4096 sequences of 16 tokens,
 // 1024 channels: 743 -> 273 us, 512 of 64 107 -> 63, 256 of 128 65 -> 57, but 64 of
-// 1024 92 -> 104).
+// 1024 92 -> 104). Of packed sequences it is the mean length that decides, as the host
+// does not know the offsets: one long among many short ones loses (16000 tokens and 500
+// times 16, 1024 channels: 537 us in small tiles, 281 in large ones).
 constexpr int kRecurShort = 192;
 constexpr int recur_tokens(int bytes, bool is_short) {
   return is_short ? (bytes <= 40 ? 4 : 2) : bytes <= 24 ? 16 : bytes <= 48 ? 8 : 4;

@@ -17,7 +17,9 @@
 // Measured (bf16): 8192 tokens, 65536 words, 2048 wide: 1.01 ms for the sums, which is
 // 2.18 PFLOP/s, 0.31 for a piece's G and 0.61 to 0.66 for its products, alone; 5.4 ms
 // for the loss and its gradients (1.63 PFLOP/s of 8 N V D operations), bound by the
-// power cap.  Small widths (64) are bound by the exponentials, 16 per clock and SM.
+// power cap.  At small widths (64) the reading warps are the bound, two per scheduler:
+// 44% of the issue slots, their own instructions' latencies the largest stall; the
+// exponentials fill 32% of their units, the products 16% of the tensor cores.
 //
 // fp32 operands are laid out once per call as three bf16 parts each (24
 // significand bits, any exponent), of whose nine products the six largest are

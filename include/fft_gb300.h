@@ -460,8 +460,9 @@ int fft_debug_set_option(int option, int64_t value);
  * allocated or synchronised, every call can be captured into a CUDA graph.
  * Array pointers are aligned to their elements (else FFT_ERR_MISALIGNED);
  * 16-byte aligned rows run faster.  Results do not depend on timing (sums are
- * added in a fixed order; atomic operations take a maximum or hand out work): the
- * same call on the same inputs gives the same bits.
+ * added in a fixed order; atomic operations take a maximum, hand out work, or
+ * add to an element that nothing else in the same launch adds to): the same call
+ * on the same inputs gives the same bits.
  */
 
 /* Element types of their arrays. */
@@ -636,8 +637,9 @@ int fft_delta_rule_step(const fft_delta_desc *desc, const void *q, const void *k
  *   ids        `tokens` integers of id_bytes = 4 or 8 bytes, on the device.
  *   table      rows x dim elements of type dtype; row r starts at element
  *              r * ldt, ldt >= dim.
- *   y          tokens x dim elements of type dtype, row stride ldy >= dim;
- *              rounded once.
+ *   y          tokens x dim elements of type dtype, row stride ldy >= dim.
+ *              scale and the product are rounded to float (double with
+ *              FFT_ELEM_F64), then the product to the type.
  *   tokens     0 .. 2^31 - 64 (0: nothing is done); rows 1 .. 2^31 - 1;
  *              dim 1 .. 2^30.
  * y does not overlap table or ids.
@@ -648,15 +650,17 @@ int fft_embedding(const void *ids, int id_bytes, const void *table, int64_t ldt,
 
 /*
  * fft_embedding_backward -- the table's gradient: dtable[v] = scale * sum of dy_n
- * over the n with ids_n = v, in the order of the tokens by groups of 32 whatever
- * the timing, in float (double with FFT_ELEM_F64), rounded once.
+ * over the n with ids_n = v, in float (double with FFT_ELEM_F64), rounded once.
+ * The order of a sum depends on `tokens` and the ids alone: the tokens, sorted by
+ * row, are cut into pieces of 16 (of up to 512 where there are many), each added in
+ * order; the pieces of a row that goes on over several are added as four shares.
  *   dy         tokens x dim of type dtype, row stride lddy >= dim.
  *   dtable     rows x dim of type ttype (dtype, or FFT_ELEM_F32 with 16-bit dy),
  *              contiguous.  add = 0: every row is written, 0 where no token
  *              names it.  add != 0: the sums are added to what is there, and
  *              rows that no token names are left alone.
- *   workspace  fft_embedding_workspace_bytes(tokens, dim, dtype) bytes: 16.25 per
- *              token, and two accumulators per column and 16 tokens.
+ *   workspace  fft_embedding_workspace_bytes(tokens, dim, dtype) bytes: 16 per
+ *              token; 4 and two accumulators per column for each piece.
  * dtable does not overlap dy or ids.
  */
 size_t fft_embedding_workspace_bytes(int64_t tokens, int64_t dim, int dtype);
@@ -696,8 +700,14 @@ typedef struct fft_recurrence_desc {
  *   workspace      fft_linear_recurrence_workspace_bytes(desc, offsets != NULL) bytes
  *                  (0, and none needed, except for many packed sequences).
  * Tokens are combined in an order that depends on the sizes alone.  A value that
- * is not finite spoils the later outputs of its sequence and channel.  Where
- * g > 0, products of decays end at float's largest value.
+ * is not finite spoils the later outputs of its sequence and channel, and e^g
+ * above float's range (g > 88.7) is one; e^g below 2^-126 counts as 0.  Stretches
+ * of tokens are taken as maps h -> A h + H: A, a product of decays, ends at float's
+ * largest value (g > 0) and at its smallest; H is the stretch's state from 0, and
+ * may overflow where it would cancel against A h.  A state of 0 stays 0 however
+ * much it could grow, and a decay of 0 drops any finite one.
+ * Packed rows times channels, or batch * tokens * channels, are 2^46 at most, and
+ * batch times groups of 128 channels below 2^28.
  */
 size_t fft_linear_recurrence_workspace_bytes(const fft_recurrence_desc *desc, int packed);
 int fft_linear_recurrence(const fft_recurrence_desc *desc, const void *x, const void *g,
@@ -747,8 +757,9 @@ int fft_linear_recurrence_step(const fft_recurrence_desc *desc, const void *x, c
  *   loss, lse  float, `tokens` each.
  *   tokens     0 .. 2^24; vocabulary 1 .. 2^24; dim 1 .. 2^20.
  *   workspace  fft_linear_cross_entropy_workspace_bytes(..., backward = 0) bytes:
- *              8 per token and 128 words, and copies of float operands and of
- *              those whose rows do not lie on 16-byte boundaries.
+ *              8 per token and part of the words (32 of them up to 128 tokens,
+ *              else 32 to 128), and copies of float operands and of those whose
+ *              rows do not lie on 16-byte boundaries.
  * Products of 16-bit operands are exact; float operands keep 24 significand bits as
  * three bfloat16 values each (an infinite element gives NaN; finite ones of any size
  * do not).  Sums are float: 512 terms at a time on the tensor
